@@ -1,0 +1,275 @@
+"""The 4-bit key/value cache (q4_kv_* of include/q4.h): argument marshalling.
+
+A `KVCache` is the pool of pages, a `Batch` says which sequences a call works
+on and where their new tokens are.  Both are thin handles over device tensors
+that the caller owns and may update in place (lens, table) between calls:
+
+    cache = kv.alloc_cache(q4.INT4_SYM, 64, pages=512, page=64, heads=8, dim=128, device="cuda:0")
+    step = kv.Batch(table, lens)                    # one new token a sequence
+    kv.append(cache, step, k, v)                    # k, v [seqs, heads, dim]
+    out = kv.attention(cache, step, q, mass=mass)   # q [seqs, q_heads, dim]
+    lens, mass, kept = kv.evict(cache, step, mass, fresh_table, budget=1024, recent=128)
+
+Prompts and drafts pass `starts`, the packed rows' offsets: sequence b's new
+tokens are rows starts[b] .. starts[b+1] - 1 of k, v and q.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+from . import q4
+from .q4 import _act_code, _check, _stream_ptr, _torch, lib
+
+_vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+
+
+class _CacheArgs(ctypes.Structure):
+    _fields_ = [("k_codes", _vp), ("k_scales", _vp), ("k_zeros", _vp), ("v_codes", _vp),
+                ("v_scales", _vp), ("v_zeros", _vp), ("pages", _i64), ("page", _i32), ("heads", _i32),
+                ("dim", _i32), ("g", _i32), ("format", _i32), ("reserved", _i32)]
+
+
+class _BatchArgs(ctypes.Structure):
+    _fields_ = [("table", _vp), ("lens", _vp), ("starts", _vp), ("tokens", _i64),
+                ("table_width", _i32), ("seqs", _i32), ("max_new", _i32), ("max_len", _i32)]
+
+
+def _tensor(t, name, dtype, shape=None, device=None):
+    """t as a contiguous CUDA tensor of this dtype and shape, or an error."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    return t
+
+
+class KVCache:
+    """Pages of 4-bit keys and values.
+
+    codes uint8 [pages, heads, page, dim/2]; scales [pages, heads, page,
+    dim/g], float16 (INT4) or float32 (NF4, FP4); zeros (INT4-asym) uint8
+    [pages, heads, page, ceil(dim/g / 2)], else None."""
+
+    def __init__(self, fmt, g, k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros):
+        torch = _torch()
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [pages, heads, page, dim/2]")
+        pages, heads, page, half = k_codes.shape
+        dim = 2 * half
+        if fmt not in (q4.NF4, q4.INT4_SYM, q4.INT4_ASYM, q4.FP4):
+            raise q4.Q4Error(q4.EUNSUPPORTED, "KVCache")
+        if g not in (32, 64, 128):
+            raise q4.Q4Error(q4.EUNSUPPORTED, "KVCache")
+        if dim % g:
+            raise q4.Q4Error(q4.EINVAL, "KVCache")
+        sdt = torch.float32 if fmt in (q4.NF4, q4.FP4) else torch.float16
+        dev, rows = k_codes.device, (pages, heads, page)
+        for w, codes, scales, zeros in (("k", k_codes, k_scales, k_zeros), ("v", v_codes, v_scales, v_zeros)):
+            _tensor(codes, w + "_codes", torch.uint8, (*rows, half), dev)
+            _tensor(scales, w + "_scales", sdt, (*rows, dim // g), dev)
+            if (fmt == q4.INT4_ASYM) != (zeros is not None):
+                raise ValueError(w + "_zeros belong to INT4-asym caches, and to them alone")
+            if zeros is not None:
+                _tensor(zeros, w + "_zeros", torch.uint8, (*rows, (dim // g + 1) // 2), dev)
+        self.fmt, self.g, self.pages, self.heads, self.page, self.dim = fmt, g, pages, heads, page, dim
+        self.k_codes, self.k_scales, self.k_zeros = k_codes, k_scales, k_zeros
+        self.v_codes, self.v_scales, self.v_zeros = v_codes, v_scales, v_zeros
+        self.device = dev
+        self._args = _CacheArgs(*(None if t is None else t.data_ptr() for t in
+                                  (k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros)),
+                                pages, page, heads, dim, g, fmt, 0)
+        self._ref = ctypes.addressof(self._args)
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in
+                   (self.k_codes, self.k_scales, self.k_zeros, self.v_codes, self.v_scales, self.v_zeros)
+                   if t is not None)
+
+
+def alloc_cache(fmt, g, pages, page, heads, dim, device) -> KVCache:
+    """A zeroed cache of `pages` pages."""
+    torch = _torch()
+    sdt = torch.float32 if fmt in (q4.NF4, q4.FP4) else torch.float16
+    if g not in (32, 64, 128):
+        raise q4.Q4Error(q4.EUNSUPPORTED, "alloc_cache")
+    if dim <= 0 or dim % g:
+        raise q4.Q4Error(q4.EINVAL, "alloc_cache")
+
+    def half():
+        z = lambda n, dt: torch.zeros((pages, heads, page, n), dtype=dt, device=device)  # noqa: E731
+        return (z(dim // 2, torch.uint8), z(dim // g, sdt),
+                z((dim // g + 1) // 2, torch.uint8) if fmt == q4.INT4_ASYM else None)
+
+    return KVCache(fmt, g, *half(), *half())
+
+
+class Batch:
+    """Sequences of a call: table int32 [seqs, width] of page numbers, lens
+    int32 [seqs] (new tokens counted), and for more or fewer than one new token
+    a sequence starts int32 [seqs + 1], the total `tokens` and the largest
+    number `max_new`.  max_len bounds lens (default: what the table can hold);
+    a tight bound spares work."""
+
+    def __init__(self, table, lens, starts=None, *, tokens=None, max_new=None, max_len=None):
+        torch = _torch()
+        if table.dim() != 2:
+            raise ValueError("table must be [seqs, width]")
+        seqs, width = table.shape
+        dev = table.device
+        _tensor(table, "table", torch.int32)
+        _tensor(lens, "lens", torch.int32, (seqs,), dev)
+        if starts is None:
+            if tokens not in (None, seqs) or max_new not in (None, 1):
+                raise ValueError("without starts, every sequence has one new token")
+            tokens, max_new = seqs, 1
+        else:
+            _tensor(starts, "starts", torch.int32, (seqs + 1,), dev)
+            if tokens is None or max_new is None:
+                raise ValueError("starts needs tokens and max_new")
+        self.table, self.lens, self.starts = table, lens, starts
+        self.seqs, self.width, self.tokens, self.max_new = seqs, width, tokens, max_new
+        self.max_len, self.device = max_len, dev
+        self._page = None
+
+    def _ref(self, cache):
+        """The C record for a cache (its page size bounds the lengths)."""
+        if self.device != cache.device:
+            raise ValueError(f"the batch is on {self.device}, the cache on {cache.device}")
+        if self._page != cache.page:
+            self._page = cache.page
+            room = self.width * cache.page
+            self._max_len = room if self.max_len is None else self.max_len
+            self._args = _BatchArgs(self.table.data_ptr(), self.lens.data_ptr(),
+                                    None if self.starts is None else self.starts.data_ptr(),
+                                    self.tokens, self.width, self.seqs, self.max_new, self._max_len)
+            self._addr = ctypes.addressof(self._args)
+        return self._addr
+
+
+def _rows(t, name, tokens, heads, dim, device):
+    """Checks of a packed [tokens, heads, dim] array (rows contiguous)."""
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {dim}], got {list(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    st = t.stride()
+    if st[2] != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    # (a stride over an axis of one says nothing)
+    return st[0] if tokens > 1 else 0, st[1] if heads > 1 else 0
+
+
+def append(cache, batch, k, v):
+    """Code the new tokens' keys and values [tokens, heads, dim] (fp16 or bf16,
+    rows contiguous, any multiple of 8 between them) into their pages
+    (q4_kv_append)."""
+    ref = batch._ref(cache)
+    ks = _rows(k, "k", batch.tokens, cache.heads, cache.dim, cache.device)
+    vs = _rows(v, "v", batch.tokens, cache.heads, cache.dim, cache.device)
+    if v.dtype != k.dtype:
+        raise TypeError("k and v must have one dtype")
+    st = lib().q4_kv_append(cache._ref, ref, _act_code(k.dtype), k.data_ptr(), *ks, v.data_ptr(), *vs,
+                            _stream_ptr(k))
+    _check(st, "q4_kv_append")
+
+
+def read(cache, batch, dtype, out=None):
+    """The new tokens' keys and values as the cache holds them, dequantized to
+    [tokens, heads, dim] (q4_kv_read).  Returns (k, v)."""
+    torch = _torch()
+    ref = batch._ref(cache)
+    code = _act_code(dtype)
+    shape = (batch.tokens, cache.heads, cache.dim)
+    if out is None:
+        out = tuple(torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
+    else:
+        for t in out:
+            _tensor(t, "out", dtype, shape, cache.device)
+    k, v = out
+    st = lib().q4_kv_read(cache._ref, ref, code, k.data_ptr(), v.data_ptr(), _stream_ptr(k))
+    _check(st, "q4_kv_read")
+    return k, v
+
+
+def workspace_bytes(cache, batch, q_heads, mass=False) -> int:
+    """Bytes of device workspace that attention needs (q4_kv_workspace_bytes)."""
+    return lib().q4_kv_workspace_bytes(cache._ref, batch._ref(cache), q_heads, int(mass))
+
+
+def attention(cache, batch, q, *, scale=None, window=0, mass=None, lse=None, out=None, workspace=None):
+    """Attention of the new tokens' queries [tokens, q_heads, dim] over the
+    cached tokens (q4_kv_attention).
+
+    scale defaults to dim ** -0.5.  window > 0 lets a token see only the last
+    `window` positions up to its own.  mass, float32 [seqs, heads, width >=
+    max_len], gets each cached token's softmax weights added in place.  lse,
+    float32 [tokens, q_heads], receives the log-sum-exp.  workspace: a uint8
+    tensor of at least workspace_bytes, else one is allocated."""
+    torch = _torch()
+    ref = batch._ref(cache)
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, q_heads, dim]")
+    heads = q.shape[1]
+    qs = _rows(q, "q", batch.tokens, heads, cache.dim, cache.device)
+    code = _act_code(q.dtype)
+    if out is None:
+        out = torch.empty((batch.tokens, heads, cache.dim), dtype=q.dtype, device=cache.device)
+    else:
+        _tensor(out, "out", q.dtype, (batch.tokens, heads, cache.dim), cache.device)
+    mass_p, width = None, 0
+    if mass is not None:
+        if mass.dim() != 3:
+            raise ValueError("mass must be [seqs, heads, width]")
+        width = mass.shape[2]
+        _tensor(mass, "mass", torch.float32, (batch.seqs, cache.heads, width), cache.device)
+        mass_p = mass.data_ptr()
+    lse_p = None
+    if lse is not None:
+        lse_p = _tensor(lse, "lse", torch.float32, (batch.tokens, heads), cache.device).data_ptr()
+    L = lib()
+    need = L.q4_kv_workspace_bytes(cache._ref, ref, heads, mass is not None)
+    work_p, have = None, 0
+    if workspace is not None:
+        _tensor(workspace, "workspace", torch.uint8, None, cache.device)
+        work_p, have = workspace.data_ptr(), workspace.numel()
+    elif need:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=cache.device)
+        work_p, have = workspace.data_ptr(), need
+    st = L.q4_kv_attention(cache._ref, ref, code, q.data_ptr(), *qs, heads,
+                           cache.dim ** -0.5 if scale is None else scale, window, out.data_ptr(), lse_p,
+                           mass_p, width, work_p, have, _stream_ptr(q))
+    _check(st, "q4_kv_attention")
+    return out
+
+
+def evict(cache, batch, mass, new_table, budget, recent, *, width=None):
+    """Keep `budget` tokens of every sequence and head that has more: the last
+    `recent` and the heaviest others by mass (q4_kv_evict).  They move to the
+    pages that new_table [seqs, new_width] names, free pages of this pool.
+    Returns (new_lens [seqs], new_mass [seqs, heads, width], kept [seqs, heads,
+    budget]); width defaults to what new_table can hold."""
+    torch = _torch()
+    ref = batch._ref(cache)
+    if mass.dim() != 3:
+        raise ValueError("mass must be [seqs, heads, width]")
+    _tensor(mass, "mass", torch.float32, (batch.seqs, cache.heads, mass.shape[2]), cache.device)
+    if new_table.dim() != 2:
+        raise ValueError("new_table must be [seqs, width]")
+    _tensor(new_table, "new_table", torch.int32, (batch.seqs, new_table.shape[1]), cache.device)
+    if budget <= 0:
+        raise q4.Q4Error(q4.EINVAL, "q4_kv_evict")
+    if width is None:
+        width = new_table.shape[1] * cache.page
+    new_lens = torch.empty((batch.seqs,), dtype=torch.int32, device=cache.device)
+    new_mass = torch.empty((batch.seqs, cache.heads, width), dtype=torch.float32, device=cache.device)
+    kept = torch.empty((batch.seqs, cache.heads, budget), dtype=torch.int32, device=cache.device)
+    st = lib().q4_kv_evict(cache._ref, ref, mass.data_ptr(), mass.shape[2], new_table.data_ptr(),
+                           new_table.shape[1], budget, recent, new_lens.data_ptr(), new_mass.data_ptr(),
+                           width, kept.data_ptr(), _stream_ptr(mass))
+    _check(st, "q4_kv_evict")
+    return new_lens, new_mass, kept

@@ -35,6 +35,13 @@ SIGNATURES = {
     "q4_gemv_chain": (_int, [_int, _int, _int, ctypes.c_void_p, _int, _vp, _vp]),
     "q4_gemv_chain_static": (_int, [_int, _int, _int, ctypes.c_void_p, _int, _vp]),
     "q4_status_str": (ctypes.c_char_p, [_int]),
+    # the key/value cache (bit_group_wise_amd.kv)
+    "q4_kv_append": (_int, [_vp, _vp, _int, _vp, _i64, _i64, _vp, _i64, _i64, _vp]),
+    "q4_kv_read": (_int, [_vp, _vp, _int, _vp, _vp, _vp]),
+    "q4_kv_workspace_bytes": (_sz, [_vp, _vp, _int, _int]),
+    "q4_kv_attention": (_int, [_vp, _vp, _int, _vp, _i64, _i64, _int, ctypes.c_float, _int, _vp, _vp,
+                               _vp, _i64, _vp, _sz, _vp]),
+    "q4_kv_evict": (_int, [_vp, _vp, _vp, _i64, _vp, _int, _int, _int, _vp, _vp, _i64, _vp, _vp]),
 }
 
 # q4_gemv_chain limits and the task record (layout of q4_gemv_task)

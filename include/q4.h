@@ -5,7 +5,9 @@
  * Four operations: quantize fp16 weights to packed 4-bit codes plus per-group
  * metadata, dequantize them back to fp16/bf16, and multiply activations by
  * the quantized weights without materialising them (y = x . W^T), as a decode
- * GEMV (1 <= M <= 16) and a prefill GEMM (any M).
+ * GEMV (1 <= M <= 16) and a prefill GEMM (any M).  Beside them, the key/value
+ * cache of a decoder in the same 4 bits: append, read back, attention over it
+ * and eviction from it (q4_kv_*).
  *
  * Definitions this library implements (web pages on 4-bit group-wise
  * quantization, cited by title and section):
@@ -253,6 +255,128 @@ q4_status q4_gemv_chain(q4_format f, int g, q4_dtype act_t, const q4_gemv_task *
  * must use q4_gemv_chain with their own sync buffers instead. */
 q4_status q4_gemv_chain_static(q4_format f, int g, q4_dtype act_t, const q4_gemv_task *tasks,
                                int ntasks, void *stream);
+
+/* ------------------------------------------------- the 4-bit key/value cache
+ * Attention layers keep the keys and values of earlier tokens; here they are
+ * held in the same 4 bits per value as the weights, and read by attention
+ * without being written out.  The cache is a pool of pages: a page holds
+ * `page` consecutive tokens of one sequence for every key/value head, and a
+ * table gives each sequence's pages in order, so sequences grow and leave
+ * without moving the others.
+ *
+ * Layout (row-major; `dim` values per row, a row being one token's key or
+ * value in one head):
+ *   k_codes, v_codes   uint8 [pages, heads, page, dim/2], low nibble first
+ *   k_scales, v_scales [pages, heads, page, dim/g]: float32 (NF4, FP4) or
+ *                      fp16 (INT4), as q4_quantize stores them for [N, dim]
+ *   k_zeros, v_zeros   INT4-asym: uint8 [pages, heads, page, ceil(dim/g / 2)],
+ *                      a row's zero-points two per byte, low nibble first (a
+ *                      row starts a byte); NULL for the other formats
+ * A group is g consecutive values of a row.  Coding and decoding follow the
+ * rules above with w a row of fp16 or bf16 values, except that an INT4 scale
+ * saturates at 65504 (bf16 rows can exceed fp16's range).  NF4_DQ is not
+ * offered: its second-level constants span 256 groups, which arrive at
+ * different times.
+ *
+ * Limits: dim 64, 128 or 256, g | dim; page 16, 32, 64, 128 or 256; up to
+ * Q4_KV_MAX_LEN tokens a sequence.  Alignment: codes 16 bytes, scales 16,
+ * zeros 4.  Memory past a sequence's length (the rest of its last page) and
+ * pages no table names may hold anything, NaN scales included. */
+#define Q4_KV_MAX_LEN 4194304
+typedef struct {
+    uint8_t *k_codes;
+    void *k_scales;
+    uint8_t *k_zeros;
+    uint8_t *v_codes;
+    void *v_scales;
+    uint8_t *v_zeros;
+    int64_t pages; /* in the pool */
+    int32_t page;  /* tokens per page */
+    int32_t heads; /* key/value heads */
+    int32_t dim;   /* values per row */
+    int32_t g;     /* group size */
+    int32_t format; /* q4_format */
+    int32_t reserved; /* 0 */
+} q4_kv_cache;
+
+/* A batch: `seqs` sequences, each with some new tokens at its end.  The new
+ * tokens' rows are packed: those of sequence b are rows starts[b] ..
+ * starts[b+1] - 1 of the packed arrays, its i-th new token at position
+ * lens[b] - (starts[b+1] - starts[b]) + i (starts NULL: one token each, row b).
+ * lens counts the new tokens.  Table, lens and starts are device arrays, read
+ * by the kernels; max_new and max_len are upper bounds the caller knows
+ * (they shape the launches; a sequence is taken to end at max_len if lens
+ * says more).  A new token whose position is negative sees no key (and is not
+ * stored); a table entry outside 0 .. pages - 1 is never followed: its tokens
+ * are not stored, read as zero, and take no part in attention. */
+typedef struct {
+    const int32_t *table;  /* [seqs, table_width] page numbers */
+    const int32_t *lens;   /* [seqs] */
+    const int32_t *starts; /* [seqs + 1], or NULL */
+    int64_t tokens;        /* rows of the packed arrays */
+    int32_t table_width;
+    int32_t seqs;
+    int32_t max_new;       /* most new tokens of a sequence */
+    int32_t max_len;       /* at least every lens[b]; <= table_width * page */
+} q4_kv_batch;
+
+/* Code the new tokens' keys and values into their pages.  k and v are
+ * [tokens, heads, dim] of in_t with the given distances between tokens and
+ * between heads in elements (multiples of 8; a row itself is contiguous). */
+q4_status q4_kv_append(const q4_kv_cache *cache, const q4_kv_batch *batch, q4_dtype in_t,
+                       const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                       const void *v, int64_t v_token_stride, int64_t v_head_stride, void *stream);
+
+/* The new tokens' keys and values as they stand in the cache, dequantized to
+ * contiguous [tokens, heads, dim] arrays of out_t: one binary32 product
+ * rounded once, as q4_dequantize. */
+q4_status q4_kv_read(const q4_kv_cache *cache, const q4_kv_batch *batch, q4_dtype out_t, void *k,
+                     void *v, void *stream);
+
+/* Attention of the new tokens over their sequences' cached tokens.
+ *   q    [tokens, q_heads, dim] of act_t, strides as in q4_kv_append;
+ *        q_heads = G heads with 1 <= G <= Q4_KV_MAX_GROUP, query head j
+ *        reading key/value head j / G
+ *   out  [tokens, q_heads, dim] of act_t, contiguous, 16-byte aligned
+ *   lse  float32 [tokens, q_heads] or NULL: log of the softmax denominator
+ *   mass float32 [seqs, heads, mass_width] or NULL, mass_width >= max_len:
+ *        mass[b, h, t] += the softmax weights that the rows of head h's
+ *        query heads put on token t, all new tokens together
+ * A token at position p sees the tokens t with t <= p and, for window > 0,
+ * t > p - window.  With x_t = scale * <q, K_t>: out = sum_t softmax(x)_t V_t.
+ * A row that sees nothing gives out = 0 and lse = -infinity.  scale > 0.
+ * Scores, softmax statistics and sums are binary32; the result does not
+ * depend on timing (no floating-point atomics).  |value| < 2^60 is assumed
+ * of what a table format's cache holds.
+ * workspace: device memory of q4_kv_workspace_bytes, 256-byte aligned, needed
+ * until the call's work has run; its contents before and after do not matter
+ * (calls that may overlap need their own). */
+#define Q4_KV_MAX_GROUP 64
+size_t q4_kv_workspace_bytes(const q4_kv_cache *cache, const q4_kv_batch *batch, int q_heads,
+                             int with_mass);
+q4_status q4_kv_attention(const q4_kv_cache *cache, const q4_kv_batch *batch, q4_dtype act_t,
+                          const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                          int q_heads, float scale, int window, void *out, float *lse,
+                          float *mass, int64_t mass_width, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* Eviction by accumulated attention weight.  Per sequence and head, the tokens
+ * that stay are: all of them if lens[b] <= budget; otherwise the last
+ * `recent` tokens and the budget - recent others of largest mass (equal
+ * masses: the earlier token; NaN counts below every number).  They move, in
+ * token order, to slots 0, 1, ... of the pages new_table names, with their
+ * mass; codes, scales and zero-points are copied as they are.
+ * batch: table, lens, seqs and max_len are used; starts, tokens and max_new
+ * are not.  new_table [seqs, new_table_width] names pages of the same pool,
+ * none of them in use by the sequences that are read.  0 <= recent <= budget.
+ *   new_lens int32 [seqs]: min(lens[b], budget)
+ *   new_mass float32 [seqs, heads, new_width], new_width >= budget: the kept
+ *            tokens' masses, then zeros; not overlapping mass
+ *   kept     int32 [seqs, heads, budget]: the kept tokens' positions, then -1 */
+q4_status q4_kv_evict(const q4_kv_cache *cache, const q4_kv_batch *batch, const float *mass,
+                      int64_t mass_width, const int32_t *new_table, int new_table_width,
+                      int budget, int recent, int32_t *new_lens, float *new_mass,
+                      int64_t new_width, int32_t *kept, void *stream);
 
 /* A static, human-readable name for a status code. */
 const char *q4_status_str(q4_status s);
