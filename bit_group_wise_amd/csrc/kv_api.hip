@@ -3,7 +3,6 @@
 // runs before the first HIP call.
 #include <hip/hip_runtime.h>
 
-#include <cmath>
 #include <cstdint>
 
 #include "kv_common.hpp"
@@ -157,7 +156,7 @@ q4_status q4_kv_attention(const q4_kv_cache *cache, const q4_kv_batch *batch, q4
         return st;
     if (!dtype_ok(act_t))
         return Q4_EUNSUPPORTED;
-    if (!(scale > 0.0f) || !std::isfinite(scale) || window < 0)
+    if (!(scale > 0.0f) || !(scale <= 0x1p60f) || window < 0)
         return Q4_EINVAL;
     if (mass && mass_width < batch->max_len)
         return Q4_EINVAL;

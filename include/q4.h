@@ -344,7 +344,7 @@ q4_status q4_kv_read(const q4_kv_cache *cache, const q4_kv_batch *batch, q4_dtyp
  *        query heads put on token t, all new tokens together
  * A token at position p sees the tokens t with t <= p and, for window > 0,
  * t > p - window.  With x_t = scale * <q, K_t>: out = sum_t softmax(x)_t V_t.
- * A row that sees nothing gives out = 0 and lse = -infinity.  scale > 0.
+ * A row that sees nothing gives out = 0 and lse = -infinity.  0 < scale <= 2^60.
  * Scores, softmax statistics and sums are binary32; the result does not
  * depend on timing (no floating-point atomics).  |value| < 2^60 is assumed
  * of what a table format's cache holds.
