@@ -79,7 +79,10 @@ q4_status check_q(const q4_kv_cache *c, const q4_kv_batch *b, int q_heads)
     if (q_heads <= 0 || q_heads % c->heads != 0)
         return Q4_EINVAL;
     if (q_heads / c->heads > Q4_KV_MAX_GROUP || q_heads > kMaxGridYZ ||
-        (int64_t)b->max_new * (q_heads / c->heads) > INT32_MAX)
+        (int64_t)b->max_new * (q_heads / c->heads) > INT32_MAX / 2)
+        return Q4_EUNSUPPORTED;
+    // the grids count 16-row tiles of all sequences and heads
+    if ((((int64_t)b->max_new * (q_heads / c->heads) >> 4) + 1) * b->seqs * c->heads > 1 << 30)
         return Q4_EUNSUPPORTED;
     return Q4_OK;
 }
@@ -132,13 +135,14 @@ q4_status q4_kv_read(const q4_kv_cache *cache, const q4_kv_batch *batch, q4_dtyp
                                        q4::kv_batch_args(*batch), out_t, k, v, (hipStream_t)stream));
 }
 
-size_t q4_kv_workspace_bytes(const q4_kv_cache *cache, const q4_kv_batch *batch, int q_heads, int with_mass)
+size_t q4_kv_workspace_bytes(const q4_kv_cache *cache, const q4_kv_batch *batch, int q_heads, int window,
+                             int with_mass)
 {
     if (check_cache(cache) != Q4_OK || check_batch(cache, batch, true) != Q4_OK ||
-        check_q(cache, batch, q_heads) != Q4_OK || empty(batch))
+        check_q(cache, batch, q_heads) != Q4_OK || window < 0 || empty(batch))
         return 0;
-    return q4::kv_attention_workspace(cache->format, q4::kv_cache_args(*cache), q4::kv_batch_args(*batch),
-                                      q_heads, with_mass != 0);
+    return q4::kv_attention_workspace(q4::kv_cache_args(*cache), q4::kv_batch_args(*batch), q_heads, window,
+                                      with_mass != 0);
 }
 
 q4_status q4_kv_attention(const q4_kv_cache *cache, const q4_kv_batch *batch, q4_dtype act_t,
@@ -166,7 +170,7 @@ q4_status q4_kv_attention(const q4_kv_cache *cache, const q4_kv_batch *batch, q4
         return Q4_EINVAL;
     const q4::KvCache c = q4::kv_cache_args(*cache);
     const q4::KvBatch b = q4::kv_batch_args(*batch);
-    const size_t need = q4::kv_attention_workspace(cache->format, c, b, q_heads, mass != nullptr);
+    const size_t need = q4::kv_attention_workspace(c, b, q_heads, window, mass != nullptr);
     if (need > workspace_bytes || (need && !workspace))
         return Q4_EINVAL;
     if (!aligned(q, 16) || !aligned(out, 16) || !strides_ok(q_token_stride, q_head_stride) ||

@@ -121,7 +121,7 @@ hipError_t launch_kv_append(int f, const KvCache &c, const KvBatch &b, int in_t,
                             hipStream_t s);
 hipError_t launch_kv_read(int f, const KvCache &c, const KvBatch &b, int out_t, void *k, void *v,
                           hipStream_t s);
-size_t kv_attention_workspace(int f, const KvCache &c, const KvBatch &b, int q_heads, bool mass);
+size_t kv_attention_workspace(const KvCache &c, const KvBatch &b, int q_heads, int window, bool mass);
 hipError_t launch_kv_attention(int f, const KvCache &c, const KvBatch &b, int act_t, const void *q,
                                int64_t qts, int64_t qhs, int q_heads, float scale, int window,
                                void *out, float *lse, float *mass, int64_t mass_width,

@@ -1,0 +1,473 @@
+// kv_prompt.hip -- attention over the 4-bit cache for many rows a head: prompts
+// and chunks of them (q4_kv_attention).
+//
+// Mathematics: as in kv_token.hip (one pass, running reference, scores in
+// powers of two, K as exact levels with one accumulator per scale group).
+// With many rows the unpacking is shared: a workgroup turns a tile of cached
+// tokens into matrix operands in LDS once, for all its rows.
+//
+//  * Keys lie there as exact fp16 levels less zero-points, their scales beside
+//    them in binary32; a score is sum_j s_j acc_j as before.
+//  * Values lie there as fp16(level * s_t 2^-E), one rounding of the cached
+//    value, where 2^E bounds the tile's scales: E is added to the tile's
+//    scores, which puts it into the weights, and taken off the row sums again.
+//    So neither weights (at most 2^15) nor values (at most 15, 1 for tables)
+//    leave fp16, whatever the cache's magnitude.
+//  * LDS holds operands as the lanes read them, 16 bytes a lane in a row, in
+//    two buffers: the next tile is fetched while one is worked on, one barrier
+//    a tile.  Rows of V operands are values d = 8 i + j of the dword i that a
+//    staging lane unpacked, so both its writes and a result's stores are
+//    contiguous.
+//
+// Bound: vector-ALU issue.  A score costs about ten issue slots (its groups'
+// scales, maximum, the exponent's fma, exp2 at a quarter rate, sum, rounding)
+// against 4 D / 1024 of matrix time; tiles are 64 tokens (dim 128) by 16 NT
+// rows a wave.
+#include "kv_attn.hpp"
+
+namespace q4 {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kBlock = 64 * kWaves;
+
+template <int D>
+constexpr int prompt_nt() { return D == 64 ? 4 : D == 128 ? 2 : 1; }
+template <int D>
+constexpr int prompt_rows() { return 16 * prompt_nt<D>() * kWaves; }
+// Tokens a tile: 256 staging items of 32 keys or 32 values each.
+template <int D>
+constexpr int prompt_tile() { return 8192 / D; }
+
+// Value d of an output operand's row rho in product n (the rows are the
+// nibbles j of dwords i, d = 8 i + j).
+template <int D>
+__device__ __forceinline__ int out_value(int n, int rho)
+{
+    if constexpr (D == 64)
+        return 8 * (rho >> 1) + 2 * n + (rho & 1);
+    else if constexpr (D == 128)
+        return 8 * rho + n;
+    else
+        return 8 * (rho + 16 * (n >> 3)) + (n & 7);
+}
+// And the operand and row of nibble j of dword i.
+template <int D>
+__device__ __forceinline__ int operand_slot(int i, int j)  // (n * 64 + rho)
+{
+    if constexpr (D == 64)
+        return (j >> 1) * 64 + 2 * i + (j & 1);
+    else if constexpr (D == 128)
+        return j * 64 + i;
+    else
+        return (j + 8 * (i >> 4)) * 64 + (i & 15);
+}
+
+// A staging lane's share of a tile as it is in memory.
+template <int FMT, int D, int GS>
+struct Fetch {
+    static constexpr int NG = D / GS, TT = prompt_tile<D>(), ND = D / 8;
+    static constexpr int TL = TT > 64 ? TT / 64 : 1;  // tokens a lane for the scales
+    u32x4 kc;
+    uint32_t kz;
+    uint32_t vw[4];
+    float vs[4];
+    uint32_t vz[4];
+    float top;      // largest V scale of the lane's tokens
+    float ks[2];    // K scales of the wave's (group, 64 tokens) shares
+    uint32_t ok;    // bit 0: K item, 1: V item, 2..: the lane's tokens
+
+    // K items: token u % TT, 32 values u / TT.  V items: dword u % ND of the
+    // four tokens of quad u / ND, whose tt moves fastest.
+    static __device__ __forceinline__ int k_token(int u) { return u % TT; }
+    static __device__ __forceinline__ int k_chunk(int u) { return u / TT; }
+    static __device__ __forceinline__ int v_dword(int u) { return u % ND; }
+    static __device__ __forceinline__ int v_quad(int u)
+    {
+        const int s = u / ND;  // tt | kg << 1 | tb << 3
+        return (s >> 3) * 8 + (s & 1) * 4 + ((s >> 1) & 3);
+    }
+
+    __device__ __forceinline__ int64_t row(const KvCache &c, const Pages &pg, int t, int end, bool &in) const
+    {
+        const int p = min(t, max(end - 1, 0)) >> c.page_shift;
+        const int id = __shfl(pg.mine, p - pg.first);
+        in = t < end && (unsigned)id < (unsigned)c.pages;
+        return in ? (((int64_t)id * c.heads + pg.h) << c.page_shift) + (t & ((1 << c.page_shift) - 1)) : 0;
+    }
+
+    __device__ __forceinline__ void load(const KvCache &c, Pages &pg, int t0, int end, int tid)
+    {
+        const int lane = tid & 63, wave = tid >> 6;
+        const int p0 = t0 >> c.page_shift, p1 = (min(t0 + TT, end) - 1) >> c.page_shift;
+        if (p0 < pg.first || p1 - pg.first >= 64)
+            pg.fetch(p0, lane);
+        bool in;
+        int64_t r = row(c, pg, t0 + k_token(tid), end, in);
+        ok = in;
+        const int ch = k_chunk(tid);
+        kc = *(const u32x4 *)(c.k.codes + r * (D / 2) + 16 * ch);
+        constexpr int ZB = (NG + 1) / 2;
+        if constexpr (FMT == Q4_INT4_ASYM) {
+            const int j = 32 * ch / GS;
+            kz = c.k.zeros[r * ZB + (j >> 1)] >> (4 * (j & 1)) & 15;
+        }
+        const int i = v_dword(tid), j = 8 * i / GS;
+        r = row(c, pg, t0 + 4 * v_quad(tid), end, in);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            // (the four tokens share a page; those past the end are not used)
+            vw[e] = *(const uint32_t *)(c.v.codes + (r + e) * (D / 2) + 4 * i);
+            vs[e] = kv_scale<FMT>(c.v, r + e, NG, j);
+            if constexpr (FMT == Q4_INT4_ASYM)
+                vz[e] = c.v.zeros[(r + e) * ZB + (j >> 1)] >> (4 * (j & 1)) & 15;
+            ok |= (uint32_t)(in && t0 + 4 * v_quad(tid) + e < end) << (8 + e);
+        }
+        top = 0.0f;
+#pragma unroll
+        for (int x = 0; x < TL; ++x) {
+            const int64_t q = row(c, pg, t0 + (64 * x + lane) % TT, end, in);
+            ok |= (uint32_t)in << (2 + x);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const float sv = kv_scale<FMT>(c.v, q, NG, g);
+                top = fmaxf(top, in ? sv : 0.0f);
+                // share (g, x) of the K scales goes to wave (g TL + x) % kWaves
+                if ((g * TL + x) % kWaves == wave)
+                    ks[(g * TL + x) / kWaves] = in ? kv_scale<FMT>(c.k, q, NG, g) : 0.0f;
+            }
+        }
+    }
+};
+
+template <int FMT, int D, int GS>
+struct Stage {
+    static constexpr int NG = D / GS, TT = prompt_tile<D>();
+    u32x4 k[TT * D / 8];        // [16 tokens][D / 32] operands of 64 lanes
+    u32x2 v[TT * D / 4];        // [32 tokens][D / 16] operands, halves of lanes
+    float ks[NG][TT];
+    uint32_t valid[TT / 32];
+    float e;
+};
+
+template <int FMT, int D, int GS>
+__device__ __forceinline__ void stage(Stage<FMT, D, GS> &st, const Fetch<FMT, D, GS> &f, int tid, const uint32_t *pairs)
+{
+    using F = Fetch<FMT, D, GS>;
+    constexpr int NG = D / GS, TT = F::TT, TL = F::TL;
+    const int lane = tid & 63, wave = tid >> 6;
+    // the exponent of the tile's largest V scale; every wave finds the same
+    float top = f.top;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        top = fmaxf(top, __shfl_xor(top, d));
+    const int e = min(max(__builtin_amdgcn_frexp_expf(fmaxf(top, 0x1p-40f)), -40), 100);
+    const float down = __builtin_amdgcn_ldexpf(1.0f, -e);
+    if (tid == 0)
+        st.e = (float)e;
+#pragma unroll
+    for (int x = 0; x < TL; ++x) {
+        const uint64_t in = __ballot((f.ok >> (2 + x)) & 1);
+        if (wave == 0 && lane < 2 && 2 * x + lane < TT / 32)
+            st.valid[2 * x + lane] = (uint32_t)(in >> (32 * lane));
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+            if ((g * TL + x) % kWaves == wave && lane < TT)
+                st.ks[g][64 * x + lane] = f.ks[(g * TL + x) / kWaves];
+    }
+    // keys
+    {
+        const int t = F::k_token(tid), ch = F::k_chunk(tid);
+        const KeyZero z = key_zero(FMT == Q4_INT4_ASYM ? f.kz : 8u);
+        u32x4 *to = st.k + ((t >> 4) * (D / 32) + ch) * 64 + (t & 15);
+#pragma unroll
+        for (int kg = 0; kg < 4; ++kg)
+            to[16 * kg] = key_operand<FMT>(f.kc[kg], z, pairs);
+    }
+    // values: four tokens' eight, scaled, then by value
+    {
+        const int i = F::v_dword(tid), qd = F::v_quad(tid);
+        uint32_t x[4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const float s = (f.ok >> (8 + t)) & 1 ? f.vs[t] * down : 0.0f;
+            const u32x4 a = key_operand<FMT>(f.vw[t], key_zero(FMT == Q4_INT4_ASYM ? f.vz[t] : 8u), pairs);
+            if constexpr (kv_int<FMT>()) {
+                const uint32_t h = f2h_bits(s), h2 = h | h << 16;
+                const uint32_t q = f2h_bits(s * 0.0625f), q2 = q | q << 16;
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    x[t][p] = std::bit_cast<uint32_t>(std::bit_cast<f16x2>(a[p]) * std::bit_cast<f16x2>(p & 1 ? q2 : h2));
+            } else {
+                const float u = s * key_unit<FMT>();
+#pragma unroll
+                for (int p = 0; p < 4; ++p)
+                    x[t][p] = pack_h2(h2f(a[p] & 0xffffu) * u, h2f(a[p] >> 16) * u);
+            }
+        }
+        // quad qd = 8 tb + 4 tt + kg: half tt of lane (kg, row)
+        u32x2 *to = st.v + (((qd >> 3) * (D / 16)) * 64 + 16 * (qd & 3)) * 2 + ((qd >> 2) & 1);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const uint32_t lo = 0x05040100u, hi = 0x07060302u;
+            // pair p holds values (p, p + 4) for INT4, (2p, 2p + 1) otherwise
+            const int j0 = kv_int<FMT>() ? p : 2 * p, j1 = kv_int<FMT>() ? p + 4 : 2 * p + 1;
+            to[2 * operand_slot<D>(i, j0)] = u32x2{__builtin_amdgcn_perm(x[1][p], x[0][p], lo),
+                                                   __builtin_amdgcn_perm(x[3][p], x[2][p], lo)};
+            to[2 * operand_slot<D>(i, j1)] = u32x2{__builtin_amdgcn_perm(x[1][p], x[0][p], hi),
+                                                   __builtin_amdgcn_perm(x[3][p], x[2][p], hi)};
+        }
+    }
+}
+
+template <int FMT, int D, int GS>
+__global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch b, Rows rows, Split sp,
+                                                              float *__restrict__ part,
+                                                              float2 *__restrict__ part_ml)
+{
+    constexpr int NG = D / GS, NT = prompt_nt<D>(), R = prompt_rows<D>(), TT = prompt_tile<D>(), NV = D / 16;
+    __shared__ Stage<FMT, D, GS> st[2];
+    __shared__ uint32_t pairs[FMT == Q4_NF4 ? 256 : 1];
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int i = lane & 15, kg = lane >> 4;
+    // heads fastest (a head's blocks share an XCD's L2 where heads fill all
+    // eight), the blocks with most to see first
+    int id = blockIdx.x;
+    const int h = id % c.heads;
+    id /= c.heads;
+    const int seq = id % b.seqs;
+    id /= b.seqs;
+    const int pt = id % sp.parts, blk = sp.tiles - 1 - id / sp.parts;
+    const KvSeq s = kv_seq(b, seq);
+    const int nrows = s.fresh * rows.group, base = s.len - s.fresh;
+    if (blk * R >= nrows)
+        return;
+    const int pos_min = base + blk * R / rows.group, pos_max = base + (min(blk * R + R, nrows) - 1) / rows.group;
+    int begin = rows.window > 0 ? max(0, pos_min - rows.window + 1) & ~15 : 0;
+    int end = pos_max + 1;
+    if (sp.parts > 1) {
+        const int p0 = range_begin(s, rows.window) + pt * sp.span;
+        begin = max(begin, p0);
+        end = min(end, p0 + sp.span);
+    }
+    if constexpr (FMT == Q4_NF4) {
+        pairs[tid] = nf4_pair(tid);
+        __syncthreads();
+    }
+
+    const int w0 = blk * R + wave * 16 * NT;  // the wave's first row
+    Queries<FMT, D, GS> q[NT];
+    int pos[NT], low[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int r = w0 + 16 * n + i;
+        const bool live = r < nrows;
+        const int tok = live ? r / rows.group : 0;
+        const int head = h * rows.group + (live ? r - tok * rows.group : 0);
+        q[n].load(rows.q + (int64_t)(s.first + tok) * rows.qts + (int64_t)head * rows.qhs, live, rows.act,
+                  rows.scale2, kg);
+        pos[n] = live ? base + tok : -1;
+        low[n] = rows.window > 0 ? pos[n] - rows.window : -1;
+    }
+    // tokens that all the wave's live rows see, and that any sees
+    const int last = min(w0 + 16 * NT, nrows) - 1;
+    const int all_to = base + w0 / rows.group, any_to = last < w0 ? -1 : base + last / rows.group;
+    const int all_from = rows.window > 0 ? any_to - rows.window + 1 : 0;
+    const int any_from = rows.window > 0 ? all_to - rows.window + 1 : 0;
+
+    f32x4 o[NV][NT];
+    float m[NT], l[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        m[n] = kNone;
+        l[n] = 0.0f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            o[v][n] = f32x4{0, 0, 0, 0};
+    }
+
+    Pages pg{b.table + (int64_t)seq * b.table_width, c.page_shift, c.heads, h, c.pages, 1 << 30, 0, -1};
+    pg.last = (end - 1) >> c.page_shift;
+    Fetch<FMT, D, GS> f;
+    if (begin < end)
+        f.load(c, pg, begin, end, tid);
+    int buf = 0;
+    for (int t0 = begin; t0 < end; t0 += TT, buf ^= 1) {
+        stage<FMT, D, GS>(st[buf], f, tid, pairs);
+        if (t0 + TT < end)
+            f.load(c, pg, t0 + TT, end, tid);
+        __syncthreads();
+        const Stage<FMT, D, GS> &S = st[buf];
+        const float e = S.e, inv_e = __builtin_amdgcn_ldexpf(1.0f, -(int)e);
+#pragma unroll 1
+        for (int tb = 0; tb < TT / 32; ++tb) {
+            const int t1 = t0 + 32 * tb;
+            if (t1 > any_to || t1 + 31 < any_from)
+                continue;
+            const uint32_t valid = __builtin_amdgcn_readfirstlane(S.valid[tb]);
+            float x[NT][8];
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                u32x4 ka[D / 32];
+                f32x4 ks[NG];
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k)
+                    ka[k] = S.k[((2 * tb + tt) * (D / 32) + k) * 64 + lane];
+#pragma unroll
+                for (int j = 0; j < NG; ++j)
+                    ks[j] = *(const f32x4 *)&S.ks[j][32 * tb + 16 * tt + 4 * kg];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    f32x4 y;
+#pragma unroll
+                    for (int j = 0; j < NG; ++j) {
+                        f32x4 a = {0, 0, 0, 0};
+#pragma unroll
+                        for (int k = 0; k < GS / 32; ++k)
+                            a = mfma<Q4_F16>(ka[j * (GS / 32) + k], q[n].op[j * (GS / 32) + k], a);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            y[r] = j == 0 ? a[r] * ks[j][r] : __builtin_fmaf(a[r], ks[j][r], y[r]);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        x[n][4 * tt + r] = y[r];
+                }
+            }
+            if (valid != ~0u || t1 + 31 > all_to || t1 < all_from) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int at = 16 * (k >> 2) + 4 * kg + (k & 3);
+                        const bool see = (valid >> at & 1) && t1 + at <= pos[n] && t1 + at > low[n];
+                        x[n][k] = see ? x[n][k] : -__builtin_inff();
+                    }
+            }
+            u32x4 w[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float top = x[n][0];
+#pragma unroll
+                for (int k = 1; k < 8; ++k)
+                    top = fmaxf(top, x[n][k]);
+                const float reach = __builtin_fmaf(top, q[n].factor, e);
+                if (__any(reach > m[n] + 15.0f)) {
+                    const float to = fmaxf(m[n], quad_max(reach) - 6.0f);
+                    const float g = __builtin_amdgcn_exp2f(m[n] - to);
+                    m[n] = to;
+                    l[n] *= g;
+#pragma unroll
+                    for (int v = 0; v < NV; ++v)
+                        o[v][n] *= g;
+                }
+                const float off = e - m[n];
+                float sum = 0.0f, p[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][k], q[n].factor, off));
+                    sum += p[k];
+                }
+                l[n] = __builtin_fmaf(sum, inv_e, l[n]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    w[n][k] = pack_h2(p[2 * k], p[2 * k + 1]);
+            }
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const u32x4 a = *(const u32x4 *)&S.v[((tb * NV + v) * 64 + lane) * 2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    o[v][n] = mfma<Q4_F16>(a, w[n], o[v][n]);
+            }
+        }
+    }
+
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const float ll = quad_sum(l[n]);
+        const int r0 = w0 + 16 * n + i;
+        if (r0 >= nrows)
+            continue;
+        const int tok = r0 / rows.group;
+        const int64_t to = (int64_t)(s.first + tok) * rows.q_heads + h * rows.group + r0 - tok * rows.group;
+        const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+        // a lane's rows 4 kg .. + 3 of all products are runs of 8 values
+        constexpr int RUNS = D / 32;
+#pragma unroll
+        for (int run = 0; run < RUNS; ++run) {
+            float v[8];
+            int d = 0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                int nv, r;
+                if constexpr (D == 64)
+                    nv = k >> 1, r = 2 * run + (k & 1);
+                else if constexpr (D == 128)
+                    nv = k, r = run;
+                else
+                    nv = k + 8 * (run >> 2), r = run & 3;
+                v[k] = o[nv][n][r];
+                if (k == 0)
+                    d = out_value<D>(nv, 4 * kg + r);
+            }
+            if (sp.parts == 1) {
+                u32x4 pk;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    pk[k] = rows.act == Q4_F16 ? pack_h2(v[2 * k] * inv, v[2 * k + 1] * inv)
+                                               : pack_bf2(v[2 * k] * inv, v[2 * k + 1] * inv);
+                *(u32x4 *)(rows.out + to * D + d) = pk;
+            } else {
+                float *p = part + (to * sp.parts + pt) * D + d;
+                *(f32x4 *)p = f32x4{v[0], v[1], v[2], v[3]};
+                *(f32x4 *)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+            }
+        }
+        if (kg == 0) {
+            if (sp.parts > 1) {
+                part_ml[to * sp.parts + pt] = float2{m[n], ll};
+            } else {
+                const float v = ll > 0.0f ? m[n] + __builtin_amdgcn_logf(ll) : -__builtin_inff();
+                if (rows.lse)
+                    rows.lse[to] = v * kLn2;
+                if (rows.stat)
+                    rows.stat[to] = v;
+            }
+        }
+    }
+}
+
+int rows_a_block(int dim) { return dim == 64 ? prompt_rows<64>() : dim == 128 ? prompt_rows<128>() : prompt_rows<256>(); }
+
+}  // namespace
+
+// Parts only where rows alone would leave compute units idle: as many as give
+// about two workgroups each, none shorter than 512 tokens.
+Split prompt_split(const KvCache &c, const KvBatch &b, int group, int window)
+{
+    Split sp;
+    const int rows = rows_a_block(c.dim);
+    sp.tiles = (int)(((int64_t)b.max_new * group + rows - 1) / rows);
+    const int64_t range = longest_range(b, window);
+    const int64_t wgs = (int64_t)b.seqs * c.heads * sp.tiles;
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((512 + wgs - 1) / wgs, range / 512));
+    sp.span = (int)std::max<int64_t>(((range + parts - 1) / parts + 127) / 128 * 128, 128);
+    sp.parts = (int)std::max<int64_t>((range + sp.span - 1) / sp.span, 1);
+    return sp;
+}
+
+hipError_t launch_kv_prompt(int f, const KvCache &c, const KvBatch &b, const Rows &rows, const Split &sp,
+                            float *part, float2 *part_ml, hipStream_t s)
+{
+    return kv_by_shape(f, c.dim, c.g, [&](auto fmt, auto dim, auto gs) {
+        const int64_t grid = (int64_t)sp.parts * sp.tiles * b.seqs * c.heads;
+        kv_prompt_kernel<decltype(fmt)::value, decltype(dim)::value, decltype(gs)::value>
+            <<<dim3((unsigned)grid), kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace q4

@@ -196,9 +196,9 @@ def read(cache, batch, dtype, out=None):
     return k, v
 
 
-def workspace_bytes(cache, batch, q_heads, mass=False) -> int:
+def workspace_bytes(cache, batch, q_heads, mass=False, window=0) -> int:
     """Bytes of device workspace that attention needs (q4_kv_workspace_bytes)."""
-    return lib().q4_kv_workspace_bytes(cache._ref, batch._ref(cache), q_heads, int(mass))
+    return lib().q4_kv_workspace_bytes(cache._ref, batch._ref(cache), q_heads, window, int(mass))
 
 
 def attention(cache, batch, q, *, scale=None, window=0, mass=None, lse=None, out=None, workspace=None):
@@ -232,7 +232,7 @@ def attention(cache, batch, q, *, scale=None, window=0, mass=None, lse=None, out
     if lse is not None:
         lse_p = _tensor(lse, "lse", torch.float32, (batch.tokens, heads), cache.device).data_ptr()
     L = lib()
-    need = L.q4_kv_workspace_bytes(cache._ref, ref, heads, mass is not None)
+    need = L.q4_kv_workspace_bytes(cache._ref, ref, heads, window, mass is not None)
     work_p, have = None, 0
     if workspace is not None:
         _tensor(workspace, "workspace", torch.uint8, None, cache.device)

@@ -38,7 +38,7 @@ SIGNATURES = {
     # the key/value cache (bit_group_wise_amd.kv)
     "q4_kv_append": (_int, [_vp, _vp, _int, _vp, _i64, _i64, _vp, _i64, _i64, _vp]),
     "q4_kv_read": (_int, [_vp, _vp, _int, _vp, _vp, _vp]),
-    "q4_kv_workspace_bytes": (_sz, [_vp, _vp, _int, _int]),
+    "q4_kv_workspace_bytes": (_sz, [_vp, _vp, _int, _int, _int]),
     "q4_kv_attention": (_int, [_vp, _vp, _int, _vp, _i64, _i64, _int, ctypes.c_float, _int, _vp, _vp,
                                _vp, _i64, _vp, _sz, _vp]),
     "q4_kv_evict": (_int, [_vp, _vp, _vp, _i64, _vp, _int, _int, _int, _vp, _vp, _i64, _vp, _vp]),

@@ -348,12 +348,13 @@ q4_status q4_kv_read(const q4_kv_cache *cache, const q4_kv_batch *batch, q4_dtyp
  * Scores, softmax statistics and sums are binary32; the result does not
  * depend on timing (no floating-point atomics).  |value| < 2^60 is assumed
  * of what a table format's cache holds.
- * workspace: device memory of q4_kv_workspace_bytes, 256-byte aligned, needed
+ * workspace: device memory of q4_kv_workspace_bytes (for the same window and
+ * with_mass = (mass != NULL)), 256-byte aligned, needed
  * until the call's work has run; its contents before and after do not matter
  * (calls that may overlap need their own). */
 #define Q4_KV_MAX_GROUP 64
 size_t q4_kv_workspace_bytes(const q4_kv_cache *cache, const q4_kv_batch *batch, int q_heads,
-                             int with_mass);
+                             int window, int with_mass);
 q4_status q4_kv_attention(const q4_kv_cache *cache, const q4_kv_batch *batch, q4_dtype act_t,
                           const void *q, int64_t q_token_stride, int64_t q_head_stride,
                           int q_heads, float scale, int window, void *out, float *lse,

@@ -184,7 +184,7 @@ def test_evict_rejected(kw, status):
 
 def test_workspace_bytes_of_bad_arguments():
     L = q4.lib()
-    size = lambda c, b, h, m: L.q4_kv_workspace_bytes(ctypes.addressof(c), ctypes.addressof(b), h, m)  # noqa: E731
+    size = lambda c, b, h, m: L.q4_kv_workspace_bytes(ctypes.addressof(c), ctypes.addressof(b), h, 0, m)  # noqa: E731
     assert size(cache(g=16), batch(), 4, 1) == 0
     assert size(cache(), batch(seqs=0), 4, 1) == 0
     assert size(cache(), batch(), 3, 1) == 0
