@@ -57,10 +57,11 @@ size_t kv_attention_workspace(const KvCache &c, const KvBatch &b, int q_heads, i
 {
     const Split sp = split_for(c, b, q_heads / c.heads, window);
     const size_t rows = (size_t)b.tokens * q_heads;
-    size_t n = mass ? round256(rows * 4) : 0;
+    size_t n = 0;
     if (sp.parts > 1)
-        n += round256(rows * sp.parts * sizeof(float2)) + round256(rows * sp.parts * c.dim * 4);
-    return n;
+        n = round256(rows * sp.parts * sizeof(float2)) + rows * sp.parts * c.dim * 4;
+    // (the parts are done with when the mass pass starts)
+    return mass ? round256(rows * 4) + std::max(n, kv_mass_workspace(c, b, q_heads / c.heads)) : n;
 }
 
 hipError_t launch_kv_attention(int f, const KvCache &c, const KvBatch &b, int act_t, const void *q,
@@ -96,7 +97,7 @@ hipError_t launch_kv_attention(int f, const KvCache &c, const KvBatch &b, int ac
         if (e != hipSuccess)
             return e;
     }
-    return mass ? launch_kv_mass(f, c, b, rows, mass, mass_width, s) : hipSuccess;
+    return mass ? launch_kv_mass(f, c, b, rows, mass, mass_width, w, s) : hipSuccess;
 }
 
 }  // namespace q4

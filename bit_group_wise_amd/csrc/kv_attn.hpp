@@ -229,7 +229,8 @@ hipError_t launch_kv_token(int f, const KvCache &c, const KvBatch &b, const Rows
                            float *part, float2 *part_ml, hipStream_t s);
 hipError_t launch_kv_prompt(int f, const KvCache &c, const KvBatch &b, const Rows &rows, const Split &sp,
                             float *part, float2 *part_ml, hipStream_t s);
+size_t kv_mass_workspace(const KvCache &c, const KvBatch &b, int group);
 hipError_t launch_kv_mass(int f, const KvCache &c, const KvBatch &b, const Rows &rows, float *mass,
-                          int64_t mass_width, hipStream_t s);
+                          int64_t mass_width, void *workspace, hipStream_t s);
 
 }  // namespace q4

@@ -1,10 +1,20 @@
 // kv_mass.hip -- the attention weight that each cached token draws, added to
 // its mass (q4_kv_attention with mass).
 //
-// A token's mass is a sum over rows of exp(x_t - lse): it needs every row's
-// final statistics, so it is a second pass over the keys.  A lane's scores
-// belong to one row and several tokens; sums run over rows in the lane and
-// then over the 16 columns of a tile, in a fixed order.
+// A token's mass is a sum over rows of 2^(x_t - stat): it needs every row's
+// final statistics, so it is a second pass over the keys.  Scores come as in
+// the attention kernels (16 tokens by 16 rows a product, exact levels, scales
+// in binary32), so they are the same numbers.  A lane adds up the weights of
+// its tokens over the rows it meets; the 16 columns meet once at the end, in a
+// fixed order.
+//
+//  * Few rows (at most 32 a head): the rows stay in registers and a wave walks
+//    over 64-token blocks of a span.  Bound as kv_token.hip.
+//  * Many rows: 64 tokens' keys stay in registers, unpacked once, and the rows
+//    pass by as operands that a first launch laid out (kv_rows_kernel), with
+//    their factors and statistics.  The four waves of a workgroup hold 256
+//    tokens and read the same rows, from the L1.  Bound by vector-ALU issue:
+//    a score costs its groups' scales, an fma, exp2 at a quarter rate, a sum.
 #include "kv_attn.hpp"
 
 namespace q4 {
@@ -12,83 +22,321 @@ namespace {
 
 constexpr int kWaves = 4;
 constexpr int kBlock = 64 * kWaves;
-constexpr int kStep = 32;  // tokens per wave
+constexpr int kBlk = 64;  // tokens of a wave at a time
 
-// mass[b, h, t] += sum over rows of 2^(x - stat), one wave per 32 tokens, the
-// rows 16 at a time.  A row that sees nothing has stat = -inf and is skipped.
+// 64 tokens' keys as operands, with the scales of the lane's rows.
 template <int FMT, int D, int GS>
-__global__ __launch_bounds__(kBlock) void kv_mass_kernel(KvCache c, KvBatch b, Rows rows,
-                                                         float *__restrict__ mass, int64_t mass_width)
+struct Keys {
+    static constexpr int NG = D / GS, ZB = (NG + 1) / 2;
+    u32x4 op[4][D / 32];
+    f32x4 s[4][NG];
+    uint32_t there;  // bit tt: the tile's page exists
+
+    __device__ __forceinline__ void load(const KvCache &c, Pages &pg, int t0, int end, int lane, const uint32_t *pairs)
+    {
+        const int i = lane & 15, kg = lane >> 4;
+        uint32_t w[4][D / 32], z[4];
+        there = 0;
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+            const int64_t row0 = pg.row(t0 + 16 * tt, end, lane);
+            there |= (row0 >= 0 ? 1u : 0u) << tt;
+            const int64_t row = row0 >= 0 ? row0 : 0;
+            const uint8_t *kc = c.k.codes + row * (D / 2);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+                w[tt][k] = *(const uint32_t *)(kc + (uint32_t)(i * (D / 2) + 16 * k + 4 * kg));
+#pragma unroll
+            for (int j = 0; j < NG; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    s[tt][j][r] = kv_scale<FMT>(c.k, row + 4 * kg + r, NG, j);
+            if constexpr (FMT == Q4_INT4_ASYM) {
+                const uint8_t *zp = c.k.zeros + row * ZB + (uint32_t)(i * ZB);
+                if constexpr (ZB == 1)
+                    z[tt] = *zp;
+                else if constexpr (ZB == 2)
+                    z[tt] = *(const uint16_t *)zp;
+                else
+                    z[tt] = *(const uint32_t *)zp;
+            }
+        }
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+                op[tt][k] = key_operand<FMT>(
+                    w[tt][k], key_zero(FMT == Q4_INT4_ASYM ? (z[tt] >> (4 * (k * 32 / GS))) & 15u : 8u), pairs);
+    }
+};
+
+// Scores of tile tt by the lane's column, in units of the column's factor.
+template <int FMT, int D, int GS>
+__device__ __forceinline__ f32x4 tile_scores(const Keys<FMT, D, GS> &k, int tt, const u32x4 *q)
+{
+    f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < D / GS; ++j) {
+        f32x4 a = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < GS / 32; ++e)
+            a = mfma<Q4_F16>(k.op[tt][j * (GS / 32) + e], q[j * (GS / 32) + e], a);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            x[r] = __builtin_fmaf(a[r], k.s[tt][j][r], x[r]);
+    }
+    return x;
+}
+
+// Sum over the 16 lanes of a column tile, every lane the same bits.
+template <int ROT>
+__device__ __forceinline__ float add_rotated(float v)
+{
+    return v + std::bit_cast<float>(__builtin_amdgcn_update_dpp(0, std::bit_cast<int>(v), 0x120 + ROT, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float sum16(float v)
+{
+    return add_rotated<1>(add_rotated<2>(add_rotated<4>(add_rotated<8>(v))));
+}
+
+// Adds a wave's 64 sums (lane's tokens 16 (e / 4) + 4 kg + e % 4) to the mass.
+__device__ __forceinline__ void add_mass(float (&sum)[16], float *mass, int t0, int len, uint32_t there, int lane)
+{
+    const int i = lane & 15, kg = lane >> 4;
+    float v = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float s = sum16(sum[e]);
+        v = i == e ? s : v;
+    }
+    const int at = t0 + 16 * (i >> 2) + 4 * kg + (i & 3);
+    if (at < len && (there >> (i >> 2) & 1))
+        mass[at] += v;
+}
+
+template <int FMT, int D, int GS, int NT>
+__global__ __launch_bounds__(kBlock) void kv_mass_few_kernel(KvCache c, KvBatch b, Rows rows, int span,
+                                                             float *__restrict__ mass, int64_t mass_width)
 {
     __shared__ uint32_t pairs[FMT == Q4_NF4 ? 256 : 1];
     const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int seq = blockIdx.z, h = blockIdx.y;
     const KvSeq s = kv_seq(b, seq);
+    const int nrows = s.fresh * rows.group;
+    const int begin = range_begin(s, rows.window) + (int)blockIdx.x * span, end = min(s.len, begin + span);
+    if (begin >= end || nrows == 0)
+        return;
     if constexpr (FMT == Q4_NF4) {
         pairs[tid] = nf4_pair(tid);
         __syncthreads();
     }
-    const int t0 = range_begin(s, rows.window) + ((int)blockIdx.x * kWaves + wave) * kStep;
-    if (t0 >= s.len)
-        return;
-    Pages pg{b.table + (int64_t)seq * b.table_width, c.page_shift, c.heads, h, c.pages, -1000,
-             (s.len - 1) >> c.page_shift, -1};
-    Tile<FMT, D, GS> t[2];
-    t[0].load(c, pg.row(t0, s.len, lane), lane);
-    t[1].load(c, pg.row(t0 + 16, s.len, lane), lane);
-    float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    const int nrows = s.fresh * rows.group;
-    for (int r0 = 0; r0 < nrows; r0 += 16) {
-        const int row = r0 + i;
+    Queries<FMT, D, GS> q[NT];
+    float st[NT];
+    int pos[NT], low[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int row = 16 * n + i;
         const bool live = row < nrows;
         const int tok = live ? row / rows.group : 0;
         const int head = h * rows.group + (live ? row - tok * rows.group : 0);
-        const int pos = live ? s.len - s.fresh + tok : -1;
-        const int low = rows.window > 0 ? pos - rows.window : -1;
-        Queries<FMT, D, GS> q;
-        q.load(rows.q + (int64_t)(s.first + tok) * rows.qts + (int64_t)head * rows.qhs, live, rows.act,
-               rows.scale2, kg);
-        const float st = live ? rows.stat[(int64_t)(s.first + tok) * rows.q_heads + head] : 0.0f;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const f32x4 a = scores<FMT, D, GS>(t[u], q, pairs);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int at = t0 + 16 * u + 4 * kg + r;
-                const bool see = t[u].there && at <= pos && at > low;
-                sum[4 * u + r] += see ? __builtin_amdgcn_exp2f(__builtin_fmaf(a[r], q.factor, -st)) : 0.0f;
-            }
-        }
+        q[n].load(rows.q + (int64_t)(s.first + tok) * rows.qts + (int64_t)head * rows.qhs, live, rows.act,
+                  rows.scale2, kg);
+        st[n] = live ? rows.stat[(int64_t)(s.first + tok) * rows.q_heads + head] : 0.0f;
+        pos[n] = live ? s.len - s.fresh + tok : -1;
+        low[n] = rows.window > 0 ? pos[n] - rows.window : -1;
     }
-    // over the 16 columns, in a fixed order
+    Pages pg{b.table + (int64_t)seq * b.table_width, c.page_shift, c.heads, h, c.pages, 1 << 30,
+             (s.len - 1) >> c.page_shift, -1};
+    for (int t0 = begin + wave * kBlk; t0 < end; t0 += kWaves * kBlk) {
+        Keys<FMT, D, GS> k;
+        k.load(c, pg, t0, end, lane, pairs);
+        float sum[16];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < 16; ++e)
+            sum[e] = 0.0f;
 #pragma unroll
-        for (int d = 1; d < 16; d <<= 1)
-            sum[e] += __shfl_xor(sum[e], d);
-    if (i < 8) {
-        float v = sum[0];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 1; e < 8; ++e)
-            v = i == e ? sum[e] : v;
-        const int at = t0 + 16 * (i >> 2) + 4 * kg + (i & 3);
-        if (at < s.len)
-            mass[((int64_t)seq * c.heads + h) * mass_width + at] += v;
+            for (int tt = 0; tt < 4; ++tt) {
+                const f32x4 x = tile_scores<FMT, D, GS>(k, tt, q[n].op);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int at = t0 + 16 * tt + 4 * kg + r;
+                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], q[n].factor, -st[n]));
+                    sum[4 * tt + r] += at <= pos[n] && at > low[n] ? p : 0.0f;
+                }
+            }
+        add_mass(sum, mass + ((int64_t)seq * c.heads + h) * mass_width, t0, end, k.there, lane);
     }
 }
 
+// Rows as operands: tile t of head h holds 16 rows of a sequence, the
+// sequence's first tile being floor(first * group / 16) + seq (so sequences
+// never share one).
+struct RowTiles {
+    u32x4 *op;     // [tiles][heads][D / 32][64]
+    float2 *fs;    // [tiles][heads][16]: factor, statistics
+};
+__device__ __forceinline__ int64_t first_tile(const KvSeq &s, int group, int seq)
+{
+    return ((int64_t)s.first * group >> 4) + seq;
+}
+
+template <int FMT, int D, int GS>
+__global__ __launch_bounds__(64) void kv_rows_kernel(KvCache c, KvBatch b, Rows rows, RowTiles to)
+{
+    const int seq = blockIdx.z, h = blockIdx.y, t = blockIdx.x, lane = threadIdx.x, i = lane & 15;
+    const KvSeq s = kv_seq(b, seq);
+    const int nrows = s.fresh * rows.group;
+    if (16 * t >= nrows)
+        return;
+    const int row = 16 * t + i;
+    const bool live = row < nrows;
+    const int tok = live ? row / rows.group : 0;
+    const int head = h * rows.group + (live ? row - tok * rows.group : 0);
+    Queries<FMT, D, GS> q;
+    q.load(rows.q + (int64_t)(s.first + tok) * rows.qts + (int64_t)head * rows.qhs, live, rows.act, rows.scale2,
+           lane >> 4);
+    const int64_t at = (first_tile(s, rows.group, seq) + t) * c.heads + h;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k)
+        to.op[(at * (D / 32) + k) * 64 + lane] = q.op[k];
+    if (lane < 16) {
+        // rows that see nothing, and none at all, weigh nothing anywhere
+        const float st = live ? rows.stat[(int64_t)(s.first + tok) * rows.q_heads + head] : -__builtin_inff();
+        to.fs[at * 16 + i] = float2{q.factor, st == -__builtin_inff() ? __builtin_inff() : st};
+    }
+}
+
+template <int FMT, int D, int GS>
+__global__ __launch_bounds__(kBlock) void kv_mass_many_kernel(KvCache c, KvBatch b, int group, int window, RowTiles from,
+                                                              float *__restrict__ mass, int64_t mass_width)
+{
+    __shared__ uint32_t pairs[FMT == Q4_NF4 ? 256 : 1];
+    const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, kg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int h = blockIdx.x, seq = blockIdx.z;
+    const KvSeq s = kv_seq(b, seq);
+    if constexpr (FMT == Q4_NF4) {
+        pairs[tid] = nf4_pair(tid);
+        __syncthreads();
+    }
+    const int t0 = range_begin(s, window) + ((int)blockIdx.y * kWaves + wave) * kBlk;
+    if (t0 >= s.len)
+        return;
+    Pages pg{b.table + (int64_t)seq * b.table_width, c.page_shift, c.heads, h, c.pages, 1 << 30,
+             (s.len - 1) >> c.page_shift, -1};
+    Keys<FMT, D, GS> k;
+    k.load(c, pg, t0, s.len, lane, pairs);
+    float sum[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        sum[e] = 0.0f;
+    // the row tiles that see any of the tokens: new tokens from t0 - base on,
+    // and with a window those less than `window` past the last
+    const int base = s.len - s.fresh, nrows = s.fresh * group;
+    int rt = max(t0 - base, 0) * group >> 4, rt_end = (nrows + 15) >> 4;
+    if (window > 0) {
+        const int64_t past = (int64_t)t0 + kBlk - 1 + window - base;  // first new token past every window
+        if (past * group < nrows)
+            rt_end = min(rt_end, (int)((max(past, (int64_t)0) * group + 15) >> 4));
+    }
+    const int64_t at0 = first_tile(s, group, seq);
+    const u32x4 *op = from.op + ((at0 + rt) * c.heads + h) * (D / 32) * 64 + lane;
+    const float2 *fs = from.fs + ((at0 + rt) * c.heads + h) * 16 + i;
+    const int64_t op_step = (int64_t)c.heads * (D / 32) * 64, fs_step = (int64_t)c.heads * 16;
+    u32x4 next[D / 32];
+    float2 nf;
+    if (rt < rt_end) {
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+            next[e] = op[64 * e];
+        nf = *fs;
+    }
+    for (; rt < rt_end; ++rt) {
+        u32x4 q[D / 32];
+        const float2 f = nf;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+            q[e] = next[e];
+        if (rt + 1 < rt_end) {
+            op += op_step;
+            fs += fs_step;
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e)
+                next[e] = op[64 * e];
+            nf = *fs;
+        }
+        const int first = base + 16 * rt / group, last = base + (16 * rt + 15) / group;
+        const bool whole = t0 + kBlk - 1 <= first && (window == 0 || t0 > last - window);
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt) {
+            const f32x4 x = tile_scores<FMT, D, GS>(k, tt, q);
+            if (whole) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    sum[4 * tt + r] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], f.x, -f.y));
+            } else {
+                const int pos = base + (16 * rt + i) / group, low = window > 0 ? pos - window : -1;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int at = t0 + 16 * tt + 4 * kg + r;
+                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], f.x, -f.y));
+                    sum[4 * tt + r] += at <= pos && at > low ? p : 0.0f;
+                }
+            }
+        }
+    }
+    add_mass(sum, mass + ((int64_t)seq * c.heads + h) * mass_width, t0, s.len, k.there, lane);
+}
+
+bool is_few(const KvBatch &b, int group) { return (int64_t)b.max_new * group <= 32; }
+
+int64_t row_tiles(const KvBatch &b, int group) { return (b.tokens * group >> 4) + b.seqs; }
+
+size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
+
 }  // namespace
 
+size_t kv_mass_workspace(const KvCache &c, const KvBatch &b, int group)
+{
+    if (is_few(b, group))
+        return 0;
+    const size_t n = (size_t)row_tiles(b, group) * c.heads;
+    return round256(n * 16 * sizeof(float2)) + n * c.dim * 32;
+}
+
 hipError_t launch_kv_mass(int f, const KvCache &c, const KvBatch &b, const Rows &rows, float *mass,
-                          int64_t mass_width, hipStream_t s)
+                          int64_t mass_width, void *workspace, hipStream_t s)
 {
     const int64_t range = longest_range(b, rows.window);
-    const int per = kWaves * kStep;
+    if (range == 0)
+        return hipSuccess;
     return kv_by_shape(f, c.dim, c.g, [&](auto fmt, auto dim, auto gs) {
-        kv_mass_kernel<decltype(fmt)::value, decltype(dim)::value, decltype(gs)::value>
-            <<<dim3((unsigned)((range + per - 1) / per), c.heads, b.seqs), kBlock, 0, s>>>(c, b, rows, mass,
-                                                                                           mass_width);
+        constexpr int F = decltype(fmt)::value, D = decltype(dim)::value, GS = decltype(gs)::value;
+        const int per = kWaves * kBlk;
+        if (is_few(b, rows.group)) {
+            // spans of whole rounds, about eight workgroups a compute unit
+            const int64_t wgs = (int64_t)b.seqs * c.heads;
+            const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((2048 + wgs - 1) / wgs, (range + per - 1) / per));
+            const int64_t span = ((range + parts - 1) / parts + per - 1) / per * per;
+            const dim3 grid((unsigned)((range + span - 1) / span), c.heads, b.seqs);
+            if ((int64_t)b.max_new * rows.group <= 16)
+                kv_mass_few_kernel<F, D, GS, 1><<<grid, kBlock, 0, s>>>(c, b, rows, (int)span, mass, mass_width);
+            else
+                kv_mass_few_kernel<F, D, GS, 2><<<grid, kBlock, 0, s>>>(c, b, rows, (int)span, mass, mass_width);
+            return hipGetLastError();
+        }
+        const size_t n = (size_t)row_tiles(b, rows.group) * c.heads;
+        const RowTiles t{(u32x4 *)((char *)workspace + round256(n * 16 * sizeof(float2))), (float2 *)workspace};
+        kv_rows_kernel<F, D, GS><<<dim3((unsigned)(((int64_t)b.max_new * rows.group + 15) / 16), c.heads, b.seqs), 64, 0, s>>>(
+            c, b, rows, t);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+        kv_mass_many_kernel<F, D, GS><<<dim3(c.heads, (unsigned)((range + per - 1) / per), b.seqs), kBlock, 0, s>>>(
+            c, b, rows.group, rows.window, t, mass, mass_width);
         return hipGetLastError();
     });
 }
