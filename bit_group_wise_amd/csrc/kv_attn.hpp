@@ -11,6 +11,15 @@ namespace q4 {
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1.0e30f;  // reference before any token
 
+// A wave-uniform value that is only known inside the branch that asks for it:
+// what is computed from it stays in there, where the optimizer would otherwise
+// compute the masks of the few tiles that need them for all.
+__device__ __forceinline__ int branch_only(int v)
+{
+    asm volatile("" : "+s"(v));
+    return v;
+}
+
 // Where a launch puts a row's result.
 struct Rows {
     const uint16_t *q;

@@ -210,7 +210,7 @@ __global__ __launch_bounds__(64) void kv_rows_kernel(KvCache c, KvBatch b, Rows 
 }
 
 template <int FMT, int D, int GS>
-__global__ __launch_bounds__(kBlock) void kv_mass_many_kernel(KvCache c, KvBatch b, int group, int window, RowTiles from,
+__global__ __launch_bounds__(kBlock, 2) void kv_mass_many_kernel(KvCache c, KvBatch b, int group, int window, RowTiles from,
                                                               float *__restrict__ mass, int64_t mass_width)
 {
     __shared__ uint32_t pairs[FMT == Q4_NF4 ? 256 : 1];
@@ -242,51 +242,52 @@ __global__ __launch_bounds__(kBlock) void kv_mass_many_kernel(KvCache c, KvBatch
         if (past * group < nrows)
             rt_end = min(rt_end, (int)((max(past, (int64_t)0) * group + 15) >> 4));
     }
+    // rows that see all the tokens: from the last one's on, and inside every window
+    const int from_row = max(t0 + kBlk - 1 - base, 0) * group;
+    const int64_t past = window > 0 ? ((int64_t)t0 + window - base) * group : INT32_MAX;
+    const int to_row = (int)min(max(past, (int64_t)0), (int64_t)INT32_MAX);
     const int64_t at0 = first_tile(s, group, seq);
     const u32x4 *op = from.op + ((at0 + rt) * c.heads + h) * (D / 32) * 64 + lane;
     const float2 *fs = from.fs + ((at0 + rt) * c.heads + h) * 16 + i;
     const int64_t op_step = (int64_t)c.heads * (D / 32) * 64, fs_step = (int64_t)c.heads * 16;
-    u32x4 next[D / 32];
-    float2 nf;
+    u32x4 q[D / 32];
+    float2 next;
     if (rt < rt_end) {
 #pragma unroll
         for (int e = 0; e < D / 32; ++e)
-            next[e] = op[64 * e];
-        nf = *fs;
+            q[e] = op[64 * e];
+        next = *fs;
     }
     for (; rt < rt_end; ++rt) {
-        u32x4 q[D / 32];
-        const float2 f = nf;
+        float x[16];
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e)
-            q[e] = next[e];
+        for (int tt = 0; tt < 4; ++tt) {
+            const f32x4 y = tile_scores<FMT, D, GS>(k, tt, q);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                x[4 * tt + r] = y[r];
+        }
+        // the next tile's rows come while this one's weights are formed
+        const float2 f = next;
         if (rt + 1 < rt_end) {
             op += op_step;
             fs += fs_step;
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e)
-                next[e] = op[64 * e];
-            nf = *fs;
         }
-        const int first = base + 16 * rt / group, last = base + (16 * rt + 15) / group;
-        const bool whole = t0 + kBlk - 1 <= first && (window == 0 || t0 > last - window);
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
-            const f32x4 x = tile_scores<FMT, D, GS>(k, tt, q);
-            if (whole) {
+        for (int e = 0; e < D / 32; ++e)
+            q[e] = op[64 * e];
+        next = *fs;
+        if (__builtin_expect(16 * rt < from_row || 16 * rt + 15 >= to_row, 0)) {
+            const int pos = branch_only(base) + (16 * rt + i) / group, low = window > 0 ? pos - window : -1;
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    sum[4 * tt + r] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], f.x, -f.y));
-            } else {
-                const int pos = base + (16 * rt + i) / group, low = window > 0 ? pos - window : -1;
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int at = t0 + 16 * tt + 4 * kg + r;
-                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], f.x, -f.y));
-                    sum[4 * tt + r] += at <= pos && at > low ? p : 0.0f;
-                }
+            for (int e = 0; e < 16; ++e) {
+                const int at = t0 + 16 * (e >> 2) + 4 * kg + (e & 3);
+                x[e] = at <= pos && at > low ? x[e] : -__builtin_inff();
             }
         }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            sum[e] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], f.x, -f.y));
     }
     add_mass(sum, mass + ((int64_t)seq * c.heads + h) * mass_width, t0, s.len, k.there, lane);
 }

@@ -46,6 +46,14 @@ __device__ __forceinline__ uint32_t nf4_pair(int byte)
     return pack_h2(a, b);
 }
 
+// Two binary32 numbers as an fp16 pair, each rounded to nearest even
+// (v_cvt_pk_f16_f32).
+__device__ __forceinline__ uint32_t pair_h2(float a, float b)
+{
+    const f16x2 v = {(_Float16)a, (_Float16)b};
+    return std::bit_cast<uint32_t>(v);
+}
+
 // Eight codes of one row (a dword) as the row operand of a product over d.
 // The order of the eight within the operand is that of q_pair_order: INT4
 // (0,4)(1,5)(2,6)(3,7) with the second and fourth pair sixteenfold, otherwise
@@ -72,9 +80,12 @@ template <int FMT>
 __device__ __forceinline__ u32x4 key_operand(uint32_t w, const KeyZero &z, const uint32_t *pairs)
 {
     if constexpr (kv_int<FMT>()) {
+        // (masks in vector registers, the offset in a scalar one: mask and OR
+        // are one v_and_or_b32)
+        const uint32_t m0 = opaque_word(kNib0), m1 = opaque_word(kNib1);
         const uint32_t one = opaque_sword(0x64006400u), h = w >> 8;
-        return u32x4{add_h2((w & kNib0) | one, z.even), add_h2((w & kNib1) | one, z.odd),
-                     add_h2((h & kNib0) | one, z.even), add_h2((h & kNib1) | one, z.odd)};
+        return u32x4{add_h2((w & m0) | one, z.even), add_h2((w & m1) | one, z.odd),
+                     add_h2((h & m0) | one, z.even), add_h2((h & m1) | one, z.odd)};
     } else if constexpr (FMT == Q4_NF4) {
         return u32x4{pairs[w & 255], pairs[(w >> 8) & 255], pairs[(w >> 16) & 255], pairs[w >> 24]};
     } else {
@@ -157,10 +168,10 @@ __device__ __forceinline__ u32x4 query_operand(const u32x4 &raw, int act, float 
         x[2 * i + 1] = (act == Q4_F16 ? h2f(raw[i] >> 16) : bf2f(raw[i] >> 16)) * f;
     }
     if constexpr (kv_int<FMT>())
-        return u32x4{pack_h2(x[0], x[4]), pack_h2(x[1] * 0.0625f, x[5] * 0.0625f), pack_h2(x[2], x[6]),
-                     pack_h2(x[3] * 0.0625f, x[7] * 0.0625f)};
+        return u32x4{pair_h2(x[0], x[4]), pair_h2(x[1] * 0.0625f, x[5] * 0.0625f), pair_h2(x[2], x[6]),
+                     pair_h2(x[3] * 0.0625f, x[7] * 0.0625f)};
     else
-        return u32x4{pack_h2(x[0], x[1]), pack_h2(x[2], x[3]), pack_h2(x[4], x[5]), pack_h2(x[6], x[7])};
+        return u32x4{pair_h2(x[0], x[1]), pair_h2(x[2], x[3]), pair_h2(x[4], x[5]), pair_h2(x[6], x[7])};
 }
 __device__ __forceinline__ float query_max(const u32x4 &raw, int act)
 {

@@ -9,10 +9,11 @@
 //  * Keys lie there as exact fp16 levels less zero-points, their scales beside
 //    them in binary32; a score is sum_j s_j acc_j as before.
 //  * Values lie there as fp16(level * s_t 2^-E), one rounding of the cached
-//    value, where 2^E bounds the tile's scales: E is added to the tile's
-//    scores, which puts it into the weights, and taken off the row sums again.
-//    So neither weights (at most 2^15) nor values (at most 15, 1 for tables)
-//    leave fp16, whatever the cache's magnitude.
+//    value, where 2^E bounds the scales of the tokens that one wave stages: E
+//    is added to those tokens' scores, which puts it into the weights, and
+//    taken off the row sums again.  So neither weights (at most 2^15) nor
+//    values (at most 15, 1 for tables) leave fp16, whatever the cache's
+//    magnitude.
 //  * LDS holds operands as the lanes read them, 16 bytes a lane in a row, in
 //    two buffers: the next tile is fetched while one is worked on, one barrier
 //    a tile.  Rows of V operands are values d = 8 i + j of the dword i that a
@@ -22,22 +23,23 @@
 // Bound: vector-ALU issue.  A score costs about ten issue slots (its groups'
 // scales, maximum, the exponent's fma, exp2 at a quarter rate, sum, rounding)
 // against 4 D / 1024 of matrix time; tiles are 64 tokens (dim 128) by 16 NT
-// rows a wave.
+// rows a wave, eight waves, so that a row pays little of the unpacking.
 #include "kv_attn.hpp"
 
 namespace q4 {
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 8;
 constexpr int kBlock = 64 * kWaves;
+constexpr int kStagers = 256;  // lanes that stage keys; as many stage values
 
 template <int D>
-constexpr int prompt_nt() { return D == 64 ? 4 : D == 128 ? 2 : 1; }
+constexpr int prompt_nt() { return D == 256 ? 1 : 2; }
 template <int D>
 constexpr int prompt_rows() { return 16 * prompt_nt<D>() * kWaves; }
-// Tokens a tile: 256 staging items of 32 keys or 32 values each.
+// Tokens a tile: one staging item of 32 keys or 32 values a lane.
 template <int D>
-constexpr int prompt_tile() { return 8192 / D; }
+constexpr int prompt_tile() { return 32 * kStagers / D; }
 
 // Value d of an output operand's row rho in product n (the rows are the
 // nibbles j of dwords i, d = 8 i + j).
@@ -63,78 +65,60 @@ __device__ __forceinline__ int operand_slot(int i, int j)  // (n * 64 + rho)
         return (j + 8 * (i >> 4)) * 64 + (i & 15);
 }
 
-// A staging lane's share of a tile as it is in memory.
+// A staging lane's share of a tile as it is in memory: 32 keys of a token (the
+// first four waves), or a dword of values of four tokens (the others).
 template <int FMT, int D, int GS>
 struct Fetch {
-    static constexpr int NG = D / GS, TT = prompt_tile<D>(), ND = D / 8;
-    static constexpr int TL = TT > 64 ? TT / 64 : 1;  // tokens a lane for the scales
-    u32x4 kc;
-    uint32_t kz;
-    uint32_t vw[4];
-    float vs[4];
-    uint32_t vz[4];
-    float top;      // largest V scale of the lane's tokens
-    float ks[2];    // K scales of the wave's (group, 64 tokens) shares
-    uint32_t ok;    // bit 0: K item, 1: V item, 2..: the lane's tokens
+    static constexpr int NG = D / GS, ZB = (NG + 1) / 2, TT = prompt_tile<D>(), ND = D / 8;
+    uint32_t w[4];
+    float s[4];   // keys: s[0], the scale of the token's group number `chunk`
+    uint32_t z[4];
+    uint32_t ok;  // keys: the token is there; values: bit e, token e is
 
-    // K items: token u % TT, 32 values u / TT.  V items: dword u % ND of the
-    // four tokens of quad u / ND, whose tt moves fastest.
+    // Keys: token u % TT, 32 values u / TT.  Values: dword u % ND of the four
+    // tokens of quad u / ND, whose place tt in a 32-token step moves fastest.
     static __device__ __forceinline__ int k_token(int u) { return u % TT; }
     static __device__ __forceinline__ int k_chunk(int u) { return u / TT; }
     static __device__ __forceinline__ int v_dword(int u) { return u % ND; }
     static __device__ __forceinline__ int v_quad(int u)
     {
-        const int s = u / ND;  // tt | kg << 1 | tb << 3
-        return (s >> 3) * 8 + (s & 1) * 4 + ((s >> 1) & 3);
+        const int p = u / ND;  // tt | kg << 1 | tb << 3
+        return (p >> 3) * 8 + (p & 1) * 4 + ((p >> 1) & 3);
     }
+    // The wave of value stagers that holds the tokens of step tb in lanes kg.
+    static __device__ __forceinline__ int v_wave(int tb, int kg) { return (8 * tb + 2 * kg) * ND / 64; }
 
-    __device__ __forceinline__ int64_t row(const KvCache &c, const Pages &pg, int t, int end, bool &in) const
+    __device__ __forceinline__ void load(const KvCache &c, Pages &pg, int t0, int end, int wave, int u)
     {
-        const int p = min(t, max(end - 1, 0)) >> c.page_shift;
-        const int id = __shfl(pg.mine, p - pg.first);
-        in = t < end && (unsigned)id < (unsigned)c.pages;
-        return in ? (((int64_t)id * c.heads + pg.h) << c.page_shift) + (t & ((1 << c.page_shift) - 1)) : 0;
-    }
-
-    __device__ __forceinline__ void load(const KvCache &c, Pages &pg, int t0, int end, int tid)
-    {
-        const int lane = tid & 63, wave = tid >> 6;
+        const int lane = u & 63;
         const int p0 = t0 >> c.page_shift, p1 = (min(t0 + TT, end) - 1) >> c.page_shift;
         if (p0 < pg.first || p1 - pg.first >= 64)
             pg.fetch(p0, lane);
-        bool in;
-        int64_t r = row(c, pg, t0 + k_token(tid), end, in);
-        ok = in;
-        const int ch = k_chunk(tid);
-        kc = *(const u32x4 *)(c.k.codes + r * (D / 2) + 16 * ch);
-        constexpr int ZB = (NG + 1) / 2;
-        if constexpr (FMT == Q4_INT4_ASYM) {
-            const int j = 32 * ch / GS;
-            kz = c.k.zeros[r * ZB + (j >> 1)] >> (4 * (j & 1)) & 15;
-        }
-        const int i = v_dword(tid), j = 8 * i / GS;
-        r = row(c, pg, t0 + 4 * v_quad(tid), end, in);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            // (the four tokens share a page; those past the end are not used)
-            vw[e] = *(const uint32_t *)(c.v.codes + (r + e) * (D / 2) + 4 * i);
-            vs[e] = kv_scale<FMT>(c.v, r + e, NG, j);
+        const int t = t0 + (wave < 4 ? k_token(u) : 4 * v_quad(u));
+        const int id = __shfl(pg.mine, (min(t, end - 1) >> c.page_shift) - pg.first);
+        const bool in = t < end && (unsigned)id < (unsigned)c.pages;
+        const int64_t r = in ? (((int64_t)id * c.heads + pg.h) << c.page_shift) + (t & ((1 << c.page_shift) - 1)) : 0;
+        if (wave < 4) {
+            const int ch = k_chunk(u);
+            ok = in;
+            const u32x4 v = *(const u32x4 *)(c.k.codes + r * (D / 2) + 16 * ch);
+            w[0] = v[0], w[1] = v[1], w[2] = v[2], w[3] = v[3];
+            if (ch < NG)
+                s[0] = kv_scale<FMT>(c.k, r, NG, ch);
             if constexpr (FMT == Q4_INT4_ASYM)
-                vz[e] = c.v.zeros[(r + e) * ZB + (j >> 1)] >> (4 * (j & 1)) & 15;
-            ok |= (uint32_t)(in && t0 + 4 * v_quad(tid) + e < end) << (8 + e);
-        }
-        top = 0.0f;
+                z[0] = c.k.zeros[r * ZB + (32 * ch / GS >> 1)];
+        } else {
+            // (the four tokens share a page; those past the end are not used)
+            const int i = v_dword(u), j = 8 * i / GS;
+            const uint8_t *vc = c.v.codes + r * (D / 2) + 4 * i;
+            ok = 0;
 #pragma unroll
-        for (int x = 0; x < TL; ++x) {
-            const int64_t q = row(c, pg, t0 + (64 * x + lane) % TT, end, in);
-            ok |= (uint32_t)in << (2 + x);
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                const float sv = kv_scale<FMT>(c.v, q, NG, g);
-                top = fmaxf(top, in ? sv : 0.0f);
-                // share (g, x) of the K scales goes to wave (g TL + x) % kWaves
-                if ((g * TL + x) % kWaves == wave)
-                    ks[(g * TL + x) / kWaves] = in ? kv_scale<FMT>(c.k, q, NG, g) : 0.0f;
+            for (int e = 0; e < 4; ++e) {
+                w[e] = *(const uint32_t *)(vc + e * (D / 2));
+                s[e] = kv_scale<FMT>(c.v, r + e, NG, j);
+                if constexpr (FMT == Q4_INT4_ASYM)
+                    z[e] = c.v.zeros[(r + e) * ZB + (j >> 1)];
+                ok |= (uint32_t)(in && t + e < end) << e;
             }
         }
     }
@@ -147,76 +131,75 @@ struct Stage {
     u32x2 v[TT * D / 4];        // [32 tokens][D / 16] operands, halves of lanes
     float ks[NG][TT];
     uint32_t valid[TT / 32];
-    float e;
+    float e[4];                 // by v_wave
 };
 
 template <int FMT, int D, int GS>
-__device__ __forceinline__ void stage(Stage<FMT, D, GS> &st, const Fetch<FMT, D, GS> &f, int tid, const uint32_t *pairs)
+__device__ __forceinline__ void stage(Stage<FMT, D, GS> &st, const Fetch<FMT, D, GS> &f, int wave, int u,
+                                      const uint32_t *pairs)
 {
     using F = Fetch<FMT, D, GS>;
-    constexpr int NG = D / GS, TT = F::TT, TL = F::TL;
-    const int lane = tid & 63, wave = tid >> 6;
-    // the exponent of the tile's largest V scale; every wave finds the same
-    float top = f.top;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        top = fmaxf(top, __shfl_xor(top, d));
-    const int e = min(max(__builtin_amdgcn_frexp_expf(fmaxf(top, 0x1p-40f)), -40), 100);
-    const float down = __builtin_amdgcn_ldexpf(1.0f, -e);
-    if (tid == 0)
-        st.e = (float)e;
-#pragma unroll
-    for (int x = 0; x < TL; ++x) {
-        const uint64_t in = __ballot((f.ok >> (2 + x)) & 1);
-        if (wave == 0 && lane < 2 && 2 * x + lane < TT / 32)
-            st.valid[2 * x + lane] = (uint32_t)(in >> (32 * lane));
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-            if ((g * TL + x) % kWaves == wave && lane < TT)
-                st.ks[g][64 * x + lane] = f.ks[(g * TL + x) / kWaves];
-    }
-    // keys
-    {
-        const int t = F::k_token(tid), ch = F::k_chunk(tid);
-        const KeyZero z = key_zero(FMT == Q4_INT4_ASYM ? f.kz : 8u);
+    constexpr int TT = F::TT;
+    const int lane = u & 63;
+    if (wave < 4) {
+        const int t = F::k_token(u), ch = F::k_chunk(u);
+        if (ch < F::NG)
+            st.ks[ch][t] = f.ok ? f.s[0] : 0.0f;
+        const uint64_t in = __ballot(f.ok);
+        const int word = 2 * wave + lane;
+        if (lane < 2 && word < TT / 32)
+            st.valid[word] = (uint32_t)(in >> (32 * lane));
+        const KeyZero z = key_zero(FMT == Q4_INT4_ASYM ? (f.z[0] >> (4 * (32 * ch / GS & 1))) & 15u : 8u);
         u32x4 *to = st.k + ((t >> 4) * (D / 32) + ch) * 64 + (t & 15);
 #pragma unroll
         for (int kg = 0; kg < 4; ++kg)
-            to[16 * kg] = key_operand<FMT>(f.kc[kg], z, pairs);
+            to[16 * kg] = key_operand<FMT>(f.w[kg], z, pairs);
+        return;
     }
-    // values: four tokens' eight, scaled, then by value
-    {
-        const int i = F::v_dword(tid), qd = F::v_quad(tid);
-        uint32_t x[4][4];
+    // values: four tokens' eight, scaled by 2^-E, then by value
+    float s[4], top = 0.0f;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const float s = (f.ok >> (8 + t)) & 1 ? f.vs[t] * down : 0.0f;
-            const u32x4 a = key_operand<FMT>(f.vw[t], key_zero(FMT == Q4_INT4_ASYM ? f.vz[t] : 8u), pairs);
-            if constexpr (kv_int<FMT>()) {
-                const uint32_t h = f2h_bits(s), h2 = h | h << 16;
-                const uint32_t q = f2h_bits(s * 0.0625f), q2 = q | q << 16;
+    for (int e = 0; e < 4; ++e) {
+        s[e] = f.ok >> e & 1 ? f.s[e] : 0.0f;
+        top = fmaxf(top, s[e]);
+    }
 #pragma unroll
-                for (int p = 0; p < 4; ++p)
-                    x[t][p] = std::bit_cast<uint32_t>(std::bit_cast<f16x2>(a[p]) * std::bit_cast<f16x2>(p & 1 ? q2 : h2));
-            } else {
-                const float u = s * key_unit<FMT>();
+    for (int d = 1; d < 64; d <<= 1)
+        top = fmaxf(top, __shfl_xor(top, d));
+    const int e2 = min(max(__builtin_amdgcn_frexp_expf(fmaxf(top, 0x1p-40f)), -40), 100);
+    const float down = __builtin_amdgcn_ldexpf(1.0f, -e2);
+    if (lane == 0)
+        st.e[wave - 4] = (float)e2;
+    const int i = F::v_dword(u), qd = F::v_quad(u), j = 8 * i / GS;
+    uint32_t x[4][4];
 #pragma unroll
-                for (int p = 0; p < 4; ++p)
-                    x[t][p] = pack_h2(h2f(a[p] & 0xffffu) * u, h2f(a[p] >> 16) * u);
-            }
+    for (int t = 0; t < 4; ++t) {
+        s[t] *= down;
+        const u32x4 a = key_operand<FMT>(
+            f.w[t], key_zero(FMT == Q4_INT4_ASYM ? (f.z[t] >> (4 * (j & 1))) & 15u : 8u), pairs);
+        if constexpr (kv_int<FMT>()) {
+            const uint32_t h = pair_h2(s[t], s[t]), q = pair_h2(s[t] * 0.0625f, s[t] * 0.0625f);
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                x[t][p] = std::bit_cast<uint32_t>(std::bit_cast<f16x2>(a[p]) * std::bit_cast<f16x2>(p & 1 ? q : h));
+        } else {
+            const float un = s[t] * key_unit<FMT>();
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                x[t][p] = pair_h2(h2f(a[p] & 0xffffu) * un, h2f(a[p] >> 16) * un);
         }
-        // quad qd = 8 tb + 4 tt + kg: half tt of lane (kg, row)
-        u32x2 *to = st.v + (((qd >> 3) * (D / 16)) * 64 + 16 * (qd & 3)) * 2 + ((qd >> 2) & 1);
+    }
+    // quad qd = 8 tb + 4 tt + kg: half tt of lane (kg, row)
+    u32x2 *to = st.v + (((qd >> 3) * (D / 16)) * 64 + 16 * (qd & 3)) * 2 + ((qd >> 2) & 1);
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const uint32_t lo = 0x05040100u, hi = 0x07060302u;
-            // pair p holds values (p, p + 4) for INT4, (2p, 2p + 1) otherwise
-            const int j0 = kv_int<FMT>() ? p : 2 * p, j1 = kv_int<FMT>() ? p + 4 : 2 * p + 1;
-            to[2 * operand_slot<D>(i, j0)] = u32x2{__builtin_amdgcn_perm(x[1][p], x[0][p], lo),
-                                                   __builtin_amdgcn_perm(x[3][p], x[2][p], lo)};
-            to[2 * operand_slot<D>(i, j1)] = u32x2{__builtin_amdgcn_perm(x[1][p], x[0][p], hi),
-                                                   __builtin_amdgcn_perm(x[3][p], x[2][p], hi)};
-        }
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t lo = 0x05040100u, hi = 0x07060302u;
+        // pair p holds values (p, p + 4) for INT4, (2p, 2p + 1) otherwise
+        const int j0 = kv_int<FMT>() ? p : 2 * p, j1 = kv_int<FMT>() ? p + 4 : 2 * p + 1;
+        to[2 * operand_slot<D>(i, j0)] = u32x2{__builtin_amdgcn_perm(x[1][p], x[0][p], lo),
+                                               __builtin_amdgcn_perm(x[3][p], x[2][p], lo)};
+        to[2 * operand_slot<D>(i, j1)] = u32x2{__builtin_amdgcn_perm(x[1][p], x[0][p], hi),
+                                               __builtin_amdgcn_perm(x[3][p], x[2][p], hi)};
     }
 }
 
@@ -226,6 +209,7 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
                                                               float2 *__restrict__ part_ml)
 {
     constexpr int NG = D / GS, NT = prompt_nt<D>(), R = prompt_rows<D>(), TT = prompt_tile<D>(), NV = D / 16;
+    constexpr int TB = TT >= 64 ? 2 : 1;  // 32-token steps worked on together
     __shared__ Stage<FMT, D, GS> st[2];
     __shared__ uint32_t pairs[FMT == Q4_NF4 ? 256 : 1];
 
@@ -253,7 +237,8 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
         end = min(end, p0 + sp.span);
     }
     if constexpr (FMT == Q4_NF4) {
-        pairs[tid] = nf4_pair(tid);
+        if (tid < 256)
+            pairs[tid] = nf4_pair(tid);
         __syncthreads();
     }
 
@@ -292,24 +277,30 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
     pg.last = (end - 1) >> c.page_shift;
     Fetch<FMT, D, GS> f;
     if (begin < end)
-        f.load(c, pg, begin, end, tid);
+        f.load(c, pg, begin, end, wave, tid & 255);
     int buf = 0;
     for (int t0 = begin; t0 < end; t0 += TT, buf ^= 1) {
-        stage<FMT, D, GS>(st[buf], f, tid, pairs);
+        stage<FMT, D, GS>(st[buf], f, wave, tid & 255, pairs);
         if (t0 + TT < end)
-            f.load(c, pg, t0 + TT, end, tid);
+            f.load(c, pg, t0 + TT, end, wave, tid & 255);
         __syncthreads();
         const Stage<FMT, D, GS> &S = st[buf];
-        const float e = S.e, inv_e = __builtin_amdgcn_ldexpf(1.0f, -(int)e);
 #pragma unroll 1
-        for (int tb = 0; tb < TT / 32; ++tb) {
+        for (int tb = 0; tb < TT / 32; tb += TB) {
             const int t1 = t0 + 32 * tb;
-            if (t1 > any_to || t1 + 31 < any_from)
+            if (t1 > any_to || t1 + 32 * TB - 1 < any_from)
                 continue;
-            const uint32_t valid = __builtin_amdgcn_readfirstlane(S.valid[tb]);
-            float x[NT][8];
+            uint32_t valid[TB];
+            float e[TB], x[NT][8 * TB];
+            bool whole = t1 + 32 * TB - 1 <= all_to && t1 >= all_from;
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
+            for (int u = 0; u < TB; ++u) {
+                valid[u] = __builtin_amdgcn_readfirstlane(S.valid[tb + u]);
+                e[u] = S.e[Fetch<FMT, D, GS>::v_wave(tb + u, kg)];
+                whole = whole && valid[u] == ~0u;
+            }
+#pragma unroll
+            for (int tt = 0; tt < 2 * TB; ++tt) {
                 u32x4 ka[D / 32];
                 f32x4 ks[NG];
 #pragma unroll
@@ -320,7 +311,6 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
                     ks[j] = *(const f32x4 *)&S.ks[j][32 * tb + 16 * tt + 4 * kg];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    f32x4 y;
 #pragma unroll
                     for (int j = 0; j < NG; ++j) {
                         f32x4 a = {0, 0, 0, 0};
@@ -329,33 +319,41 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
                             a = mfma<Q4_F16>(ka[j * (GS / 32) + k], q[n].op[j * (GS / 32) + k], a);
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            y[r] = j == 0 ? a[r] * ks[j][r] : __builtin_fmaf(a[r], ks[j][r], y[r]);
+                            x[n][4 * tt + r] = j == 0 ? a[r] * ks[j][r]
+                                                      : __builtin_fmaf(a[r], ks[j][r], x[n][4 * tt + r]);
                     }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        x[n][4 * tt + r] = y[r];
                 }
             }
-            if (valid != ~0u || t1 + 31 > all_to || t1 < all_from) {
+            if (__builtin_expect(!whole, 0)) {
+                const int ta = branch_only(t1);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
+                    for (int k = 0; k < 8 * TB; ++k) {
                         const int at = 16 * (k >> 2) + 4 * kg + (k & 3);
-                        const bool see = (valid >> at & 1) && t1 + at <= pos[n] && t1 + at > low[n];
+                        const bool see = (valid[k >> 3] >> (at & 31) & 1) && ta + at <= pos[n] && ta + at > low[n];
                         x[n][k] = see ? x[n][k] : -__builtin_inff();
                     }
             }
-            u32x4 w[NT];
+            float reach[NT];
+            bool move = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float top = x[n][0];
 #pragma unroll
-                for (int k = 1; k < 8; ++k)
-                    top = fmaxf(top, x[n][k]);
-                const float reach = __builtin_fmaf(top, q[n].factor, e);
-                if (__any(reach > m[n] + 15.0f)) {
-                    const float to = fmaxf(m[n], quad_max(reach) - 6.0f);
+                for (int u = 0; u < TB; ++u) {
+                    float top = x[n][8 * u];
+#pragma unroll
+                    for (int k = 1; k < 8; ++k)
+                        top = fmaxf(top, x[n][8 * u + k]);
+                    const float to = __builtin_fmaf(top, q[n].factor, e[u]);
+                    reach[n] = u ? fmaxf(reach[n], to) : to;
+                }
+                move = move || reach[n] > m[n] + 15.0f;
+            }
+            if (__builtin_expect(__any(move), 0)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float to = fmaxf(m[n], quad_max(reach[n]) - 6.0f);
                     const float g = __builtin_amdgcn_exp2f(m[n] - to);
                     m[n] = to;
                     l[n] *= g;
@@ -363,24 +361,32 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
                     for (int v = 0; v < NV; ++v)
                         o[v][n] *= g;
                 }
-                const float off = e - m[n];
-                float sum = 0.0f, p[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][k], q[n].factor, off));
-                    sum += p[k];
-                }
-                l[n] = __builtin_fmaf(sum, inv_e, l[n]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    w[n][k] = pack_h2(p[2 * k], p[2 * k + 1]);
             }
 #pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const u32x4 a = *(const u32x4 *)&S.v[((tb * NV + v) * 64 + lane) * 2];
+            for (int u = 0; u < TB; ++u) {
+                const float inv_e = __builtin_amdgcn_ldexpf(1.0f, -(int)e[u]);
+                u32x4 w[NT];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    o[v][n] = mfma<Q4_F16>(a, w[n], o[v][n]);
+                for (int n = 0; n < NT; ++n) {
+                    const float off = e[u] - m[n];
+                    float sum = 0.0f, p[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][8 * u + k], q[n].factor, off));
+                        sum += p[k];
+                    }
+                    l[n] = __builtin_fmaf(sum, inv_e, l[n]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        w[n][k] = pair_h2(p[2 * k], p[2 * k + 1]);
+                }
+#pragma unroll
+                for (int v = 0; v < NV; ++v) {
+                    const u32x4 a = *(const u32x4 *)&S.v[(((tb + u) * NV + v) * 64 + lane) * 2];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        o[v][n] = mfma<Q4_F16>(a, w[n], o[v][n]);
+                }
             }
         }
     }

@@ -118,9 +118,10 @@ __global__ __launch_bounds__(kBlock) void kv_token_kernel(KvCache c, KvBatch b, 
             }
         }
         if (!whole) {
+            const int ta = branch_only(t0);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int at = t0 + 16 * (e >> 2) + 4 * kg + (e & 3);
+                const int at = ta + 16 * (e >> 2) + 4 * kg + (e & 3);
                 const bool in = t[e >> 2].there && at < end;
                 x[e] = in && at <= pos && at > low ? x[e] : -__builtin_inff();
 #pragma unroll
@@ -161,7 +162,7 @@ __global__ __launch_bounds__(kBlock) void kv_token_kernel(KvCache c, KvBatch b, 
             u32x4 wp, va[NP];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                wp[e] = pack_h2(w[2 * e] * vs[j][2 * e], w[2 * e + 1] * vs[j][2 * e + 1]);
+                wp[e] = pair_h2(w[2 * e] * vs[j][2 * e], w[2 * e + 1] * vs[j][2 * e + 1]);
                 uint32_t p[NP];
                 const int u = e >> 1, r = 2 * (e & 1);
                 value_pairs<FMT, GS>(t[u].vw[r][j], t[u].vw[r + 1][j], sel, pairs, p);
