@@ -109,67 +109,50 @@ struct Queries {
     }
 };
 
-// Sixteen tokens' rows as they are in memory, a lane's share.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&to)[N], const void *from)
+{
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j) {
+            const u32x4 v = ((const u32x4 *)from)[j];
+            to[4 * j] = v[0], to[4 * j + 1] = v[1], to[4 * j + 2] = v[2], to[4 * j + 3] = v[3];
+        }
+    } else if constexpr (N == 2) {
+        const u32x2 v = *(const u32x2 *)from;
+        to[0] = v[0], to[1] = v[1];
+    } else {
+        to[0] = *(const uint32_t *)from;
+    }
+}
+
+// Sixteen tokens' keys as they are in memory, a lane's share: row i's dwords
+// 4 m + kg, the scales of rows 4 kg .. + 3, row i's zero-points.
 template <int FMT, int D, int GS>
-struct Tile {
-    static constexpr int NG = D / GS;                       // groups a row
-    static constexpr int SW = f32_absmax(FMT) ? NG : (NG + 1) / 2;  // scale words a row (rounded up)
-    static constexpr int ZB = (NG + 1) / 2;                 // zero-point bytes a row
-    uint32_t kw[D / 32];
-    uint32_t vw[4][NG];
-    uint32_t ks[4 * NG * (f32_absmax(FMT) ? 2 : 1) / 2];    // 4 tokens' scales, in order
-    uint32_t vs[4 * NG * (f32_absmax(FMT) ? 2 : 1) / 2];
-    uint32_t kz;                                            // row i's zero-points (ZB bytes)
-    uint32_t vz[FMT == Q4_INT4_ASYM ? ZB : 1];              // 4 tokens' bytes
-    bool there;                                             // the page exists
+struct KeyTile {
+    static constexpr int NG = D / GS, ZB = (NG + 1) / 2, SB = f32_absmax(FMT) ? 4 : 2;
+    uint32_t w[D / 32], s[NG * SB], z;
 
     __device__ __forceinline__ void load(const KvCache &c, int64_t row0, int lane)
     {
         const int i = lane & 15, kg = lane >> 4;
-        there = row0 >= 0;
-        const int64_t row = there ? row0 : 0;  // (page 0 is read and not used)
-        const uint8_t *kc = c.k.codes + row * (D / 2), *vc = c.v.codes + row * (D / 2);
+        const int64_t row = row0 >= 0 ? row0 : 0;  // (page 0 is read and not used)
+        const uint8_t *kc = c.k.codes + row * (D / 2);
 #pragma unroll
         for (int m = 0; m < D / 32; ++m)
-            kw[m] = *(const uint32_t *)(kc + (uint32_t)(i * (D / 2) + 16 * m + 4 * kg));
-        const uint32_t vo = 4 * kg * (D / 2) + 4 * value_dword<GS>(i);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int j = 0; j < NG; ++j)
-                vw[r][j] = *(const uint32_t *)(vc + vo + (uint32_t)(r * (D / 2) + j * (GS / 2)));
-        constexpr int SB = f32_absmax(FMT) ? 4 : 2;  // bytes a scale
-        load_words(ks, (const char *)c.k.scales + row * (NG * SB) + (uint32_t)(4 * kg * NG * SB));
-        load_words(vs, (const char *)c.v.scales + row * (NG * SB) + (uint32_t)(4 * kg * NG * SB));
+            w[m] = *(const uint32_t *)(kc + (uint32_t)(i * (D / 2) + 16 * m + 4 * kg));
+        load_words(s, (const char *)c.k.scales + row * (NG * SB) + (uint32_t)(4 * kg * NG * SB));
         if constexpr (FMT == Q4_INT4_ASYM) {
-            const uint8_t *z = c.k.zeros + row * ZB + (uint32_t)(i * ZB);
+            const uint8_t *zp = c.k.zeros + row * ZB + (uint32_t)(i * ZB);
             if constexpr (ZB == 1)
-                kz = *z;
+                z = *zp;
             else if constexpr (ZB == 2)
-                kz = *(const uint16_t *)z;
+                z = *(const uint16_t *)zp;
             else
-                kz = *(const uint32_t *)z;
-            load_words(vz, (const char *)c.v.zeros + row * ZB + (uint32_t)(4 * kg * ZB));
+                z = *(const uint32_t *)zp;
         }
     }
-    template <int N>
-    static __device__ __forceinline__ void load_words(uint32_t (&to)[N], const char *from)
-    {
-        if constexpr (N % 4 == 0) {
-#pragma unroll
-            for (int j = 0; j < N / 4; ++j) {
-                const u32x4 v = ((const u32x4 *)from)[j];
-                to[4 * j] = v[0], to[4 * j + 1] = v[1], to[4 * j + 2] = v[2], to[4 * j + 3] = v[3];
-            }
-        } else if constexpr (N == 2) {
-            const u32x2 v = *(const u32x2 *)from;
-            to[0] = v[0], to[1] = v[1];
-        } else {
-            to[0] = *(const uint32_t *)from;
-        }
-    }
-    // Scale and zero-point of the lane's token 4 kg + r, group j.
-    static __device__ __forceinline__ float scale(const uint32_t *s, int r, int j)
+    __device__ __forceinline__ float scale(int r, int j) const
     {
         const int e = r * NG + j;
         if constexpr (f32_absmax(FMT))
@@ -177,7 +160,75 @@ struct Tile {
         else
             return h2f((s[e >> 1] >> (16 * (e & 1))) & 0xffffu);
     }
-    static __device__ __forceinline__ uint32_t zero(const uint32_t *z, int r, int j)
+    __device__ __forceinline__ KeyZero zero(int j) const
+    {
+        return key_zero(FMT == Q4_INT4_ASYM ? (z >> (4 * j)) & 15u : 8u);
+    }
+};
+
+// Sixteen tokens' values, a lane's share of rows 4 kg .. + 3: one dword a
+// group, the scales, the zero-points.
+template <int FMT, int D, int GS>
+struct ValueTile {
+    static constexpr int NG = D / GS, ZB = (NG + 1) / 2, SB = f32_absmax(FMT) ? 4 : 2;
+    uint32_t w[4][NG], s[NG * SB], z[FMT == Q4_INT4_ASYM ? ZB : 1];
+
+    __device__ __forceinline__ void load(const KvCache &c, int64_t row0, int lane)
+    {
+        const int i = lane & 15, kg = lane >> 4;
+        const int64_t row = row0 >= 0 ? row0 : 0;
+        const uint8_t *vc = c.v.codes + row * (D / 2);
+        const uint32_t vo = 4 * kg * (D / 2) + 4 * value_dword<GS>(i);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int j = 0; j < NG; ++j)
+                w[r][j] = *(const uint32_t *)(vc + vo + (uint32_t)(r * (D / 2) + j * (GS / 2)));
+        load_words(s, (const char *)c.v.scales + row * (NG * SB) + (uint32_t)(4 * kg * NG * SB));
+        if constexpr (FMT == Q4_INT4_ASYM)
+            load_words(z, c.v.zeros + row * ZB + (uint32_t)(4 * kg * ZB));
+    }
+    __device__ __forceinline__ float scale(int r, int j) const
+    {
+        const int e = r * NG + j;
+        if constexpr (f32_absmax(FMT))
+            return std::bit_cast<float>(s[e]);
+        else
+            return h2f((s[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+    }
+    // The scales of rows at and past `n` become 0 (rows of the lane count from
+    // 4 kg).
+    __device__ __forceinline__ void keep(int n)
+    {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                const int e = r * NG + j;
+                if constexpr (f32_absmax(FMT))
+                    s[e] = r < n ? s[e] : 0u;
+                else
+                    s[e >> 1] = r < n ? s[e >> 1] : s[e >> 1] & (e & 1 ? 0x0000ffffu : 0xffff0000u);
+            }
+    }
+    // The largest scale (none is negative).
+    __device__ __forceinline__ float largest() const
+    {
+        if constexpr (f32_absmax(FMT)) {
+            float m = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4 * NG; ++e)
+                m = fmaxf(m, std::bit_cast<float>(s[e]));
+            return m;
+        } else {
+            f16x2 m = std::bit_cast<f16x2>(s[0]);
+#pragma unroll
+            for (int e = 1; e < 2 * NG; ++e)
+                m = __builtin_elementwise_max(m, std::bit_cast<f16x2>(s[e]));
+            return fmaxf((float)m[0], (float)m[1]);
+        }
+    }
+    __device__ __forceinline__ uint32_t zero(int r, int j) const
     {
         const int byte = r * ZB + (j >> 1);
         return (z[byte >> 2] >> (8 * (byte & 3) + 4 * (j & 1))) & 15u;
@@ -187,21 +238,20 @@ struct Tile {
 // Scores of 16 tokens (rows 4 kg + r of the tile) by the lane's column, in
 // units of the column's factor.
 template <int FMT, int D, int GS>
-__device__ __forceinline__ f32x4 scores(const Tile<FMT, D, GS> &t, const Queries<FMT, D, GS> &q,
+__device__ __forceinline__ f32x4 scores(const KeyTile<FMT, D, GS> &t, const Queries<FMT, D, GS> &q,
                                         const uint32_t *pairs)
 {
-    constexpr int NG = D / GS;
     f32x4 x = {0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < NG; ++j) {
-        const KeyZero z = key_zero(FMT == Q4_INT4_ASYM ? (t.kz >> (4 * j)) & 15u : 8u);
+    for (int j = 0; j < D / GS; ++j) {
+        const KeyZero z = t.zero(j);
         f32x4 a = {0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < GS / 32; ++k)
-            a = mfma<Q4_F16>(key_operand<FMT>(t.kw[j * (GS / 32) + k], z, pairs), q.op[j * (GS / 32) + k], a);
+            a = mfma<Q4_F16>(key_operand<FMT>(t.w[j * (GS / 32) + k], z, pairs), q.op[j * (GS / 32) + k], a);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            x[r] = __builtin_fmaf(a[r], t.scale(t.ks, r, j), x[r]);
+            x[r] = __builtin_fmaf(a[r], t.scale(r, j), x[r]);
     }
     return x;
 }

@@ -43,7 +43,7 @@ constexpr int kBlock = 64 * kWaves;
 constexpr int kStep = 32;  // tokens per wave and step
 
 template <int FMT, int D, int GS>
-__global__ __launch_bounds__(kBlock) void kv_token_kernel(KvCache c, KvBatch b, Rows rows, Split sp,
+__global__ __launch_bounds__(kBlock, (D == 256 ? 1 : GS == 32 && D == 128 ? 2 : 3)) void kv_token_kernel(KvCache c, KvBatch b, Rows rows, Split sp,
                                                           float *__restrict__ part,
                                                           float2 *__restrict__ part_ml)
 {
@@ -99,46 +99,55 @@ __global__ __launch_bounds__(kBlock) void kv_token_kernel(KvCache c, KvBatch b, 
     Pages pg{b.table + (int64_t)seq * b.table_width, c.page_shift, c.heads, h, c.pages, 0, 0, -1};
     pg.last = (s.len - 1) >> c.page_shift;
     pg.first = -1000;
-    Tile<FMT, D, GS> t[2];
-    for (int t0 = begin + wave * kStep; t0 < end; t0 += kWaves * kStep) {
-        t[0].load(c, pg.row(t0, end, lane), lane);
-        t[1].load(c, pg.row(t0 + 16, end, lane), lane);
-        const bool whole = t[0].there && t[1].there && t0 + kStep - 1 <= all_to && t0 >= all_from;
-        float x[8], vs[NG][8];
-        float top = -__builtin_inff(), big = 0.0f;
+    // The registers of a step's keys take the next step's as soon as the scores
+    // are formed, those of its values once they are summed: loads are always
+    // in flight, without a second set.
+    KeyTile<FMT, D, GS> kt[2];
+    ValueTile<FMT, D, GS> vt[2];
+    int t0 = begin + wave * kStep;
+    int64_t row0 = pg.row(t0, end, lane), row1 = pg.row(t0 + 16, end, lane);
+    if (t0 < end) {
+        kt[0].load(c, row0, lane);
+        kt[1].load(c, row1, lane);
+        vt[0].load(c, row0, lane);
+        vt[1].load(c, row1, lane);
+    }
+    while (t0 < end) {
+        const int tn = t0 + kWaves * kStep;
+        float x[8];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const f32x4 a = scores<FMT, D, GS>(t[u], q, pairs);
+            const f32x4 a = scores<FMT, D, GS>(kt[u], q, pairs);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
+            for (int r = 0; r < 4; ++r)
                 x[4 * u + r] = a[r];
-#pragma unroll
-                for (int j = 0; j < NG; ++j)
-                    vs[j][4 * u + r] = t[u].scale(t[u].vs, r, j);
-            }
         }
-        if (!whole) {
+        const int64_t next0 = pg.row(tn, end, lane), next1 = pg.row(tn + 16, end, lane);
+        if (tn < end) {
+            kt[0].load(c, next0, lane);
+            kt[1].load(c, next1, lane);
+        }
+        if (__builtin_expect(row0 < 0 || row1 < 0 || t0 + kStep - 1 > all_to || t0 < all_from, 0)) {
             const int ta = branch_only(t0);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int at = ta + 16 * (e >> 2) + 4 * kg + (e & 3);
-                const bool in = t[e >> 2].there && at < end;
-                x[e] = in && at <= pos && at > low ? x[e] : -__builtin_inff();
+            for (int u = 0; u < 2; ++u) {
+                const int n = (u ? row1 : row0) < 0 ? 0 : end - ta - 16 * u - 4 * kg;
+                vt[u].keep(n);
 #pragma unroll
-                for (int j = 0; j < NG; ++j)
-                    vs[j][e] = in ? vs[j][e] : 0.0f;
+                for (int r = 0; r < 4; ++r) {
+                    const int at = ta + 16 * u + 4 * kg + r;
+                    x[4 * u + r] = r < n && at <= pos && at > low ? x[4 * u + r] : -__builtin_inff();
+                }
             }
         }
+        float top = x[0];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 1; e < 8; ++e)
             top = fmaxf(top, x[e]);
-#pragma unroll
-            for (int j = 0; j < NG; ++j)
-                big = fmaxf(big, vs[j][e]);
-        }
         // (2^-40: rows of zeros do not pull the reference down)
-        const float reach = __builtin_fmaf(top, q.factor, __builtin_amdgcn_logf(fmaxf(big, 0x1p-40f)));
-        if (__any(reach > m + 15.0f)) {
+        const float big = fmaxf(fmaxf(vt[0].largest(), vt[1].largest()), 0x1p-40f);
+        const float reach = __builtin_fmaf(top, q.factor, __builtin_amdgcn_logf(big));
+        if (__builtin_expect(__any(reach > m + 15.0f), 0)) {
             const float to = fmaxf(m, quad_max(reach) - 6.0f);
             const float f = __builtin_amdgcn_exp2f(m - to);
             m = to;
@@ -162,10 +171,12 @@ __global__ __launch_bounds__(kBlock) void kv_token_kernel(KvCache c, KvBatch b, 
             u32x4 wp, va[NP];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                wp[e] = pair_h2(w[2 * e] * vs[j][2 * e], w[2 * e + 1] * vs[j][2 * e + 1]);
-                uint32_t p[NP];
                 const int u = e >> 1, r = 2 * (e & 1);
-                value_pairs<FMT, GS>(t[u].vw[r][j], t[u].vw[r + 1][j], sel, pairs, p);
+                // (fma with 0: the scale's conversion is part of v_fma_mix)
+                wp[e] = pair_h2(__builtin_fmaf(w[2 * e], vt[u].scale(r, j), 0.0f),
+                                __builtin_fmaf(w[2 * e + 1], vt[u].scale(r + 1, j), 0.0f));
+                uint32_t p[NP];
+                value_pairs<FMT, GS>(vt[u].w[r][j], vt[u].w[r + 1][j], sel, pairs, p);
 #pragma unroll
                 for (int n = 0; n < NP; ++n)
                     va[n][e] = p[n];
@@ -179,12 +190,19 @@ __global__ __launch_bounds__(kBlock) void kv_token_kernel(KvCache c, KvBatch b, 
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int u = e >> 1, r = 2 * (e & 1);
-                        z[e] = t[u].zero(t[u].vz, r, j) | t[u].zero(t[u].vz, r + 1, j) << 16;
+                        z[e] = vt[u].zero(r, j) | vt[u].zero(r + 1, j) << 16;
                     }
                 }
                 oz[j] = mfma<Q4_F16>(z, wp, oz[j]);
             }
         }
+        if (tn < end) {
+            vt[0].load(c, next0, lane);
+            vt[1].load(c, next1, lane);
+        }
+        t0 = tn;
+        row0 = next0;
+        row1 = next1;
     }
 
     // join the waves
