@@ -42,13 +42,13 @@ __global__ __launch_bounds__(D) void kv_join_kernel(KvBatch b, Rows rows, Split 
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Rows of a head that the token kernel takes (16 a workgroup, each reading the
-// whole range); more go to the prompt kernel.
-bool is_prompt(const KvBatch &b, int group) { return (int64_t)b.max_new * group > 32; }
+// A head's rows by scale groups fill the columns of the token kernel's tiles;
+// what does not fit goes to the prompt kernel.
+bool is_prompt(const KvCache &c, const KvBatch &b, int group) { return (int64_t)b.max_new * group > few_rows(c); }
 
 Split split_for(const KvCache &c, const KvBatch &b, int group, int window)
 {
-    return is_prompt(b, group) ? prompt_split(c, b, group, window) : token_split(c, b, group, window);
+    return is_prompt(c, b, group) ? prompt_split(c, b, group, window) : token_split(c, b, group, window);
 }
 
 }  // namespace
@@ -81,7 +81,7 @@ hipError_t launch_kv_attention(int f, const KvCache &c, const KvBatch &b, int ac
     }
     float2 *part_ml = (float2 *)w;
     float *part = (float *)(w + round256(n * sp.parts * sizeof(float2)));
-    hipError_t e = is_prompt(b, group) ? launch_kv_prompt(f, c, b, rows, sp, part, part_ml, s)
+    hipError_t e = is_prompt(c, b, group) ? launch_kv_prompt(f, c, b, rows, sp, part, part_ml, s)
                                        : launch_kv_token(f, c, b, rows, sp, part, part_ml, s);
     if (e != hipSuccess)
         return e;

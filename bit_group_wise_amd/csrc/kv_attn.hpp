@@ -79,6 +79,20 @@ __device__ __forceinline__ int range_begin(const KvSeq &s, int window)
     return window > 0 ? max(0, s.len - s.fresh - window + 1) & ~15 : 0;
 }
 
+// The power of two that puts a row's largest query just below 2^12, and the
+// factor from products with rows of levels to scores in powers of two.
+__device__ __forceinline__ float query_factor(float largest, float scale2, float unit, float &factor)
+{
+    // 2^e > the largest value >= 2^(e-1); both powers are normal numbers
+    int e = 0;
+    if (largest > 0.0f)
+        e = min(max(__builtin_amdgcn_frexp_expf(largest), -110), 128);
+    // (never 0, which would make a masked score's -inf a NaN; scores of such
+    // rows are 0 to any precision)
+    factor = fmaxf(__builtin_amdgcn_ldexpf(scale2, e - 12) * unit, 0x1p-120f);
+    return __builtin_amdgcn_ldexpf(1.0f, 12 - e);
+}
+
 // A column's queries as operands, and the factor from products to scores.
 template <int FMT, int D, int GS>
 struct Queries {
@@ -94,54 +108,89 @@ struct Queries {
             raw[k] = live ? *(const u32x4 *)(q + 32 * k + 8 * kg) : u32x4{0, 0, 0, 0};
             m = fmaxf(m, query_max(raw[k], act));
         }
-        m = quad_max(m);
-        // 2^e >= the largest value > 2^(e-1); both powers are normal numbers
-        int e = 0;
-        if (m > 0.0f)
-            e = min(max(__builtin_amdgcn_frexp_expf(m), -110), 128);
-        const float f = __builtin_amdgcn_ldexpf(1.0f, 12 - e);
-        // (never 0, which would make a masked score's -inf a NaN; scores of
-        // such rows are 0 to any precision)
-        factor = fmaxf(__builtin_amdgcn_ldexpf(scale2, e - 12) * key_unit<FMT>(), 0x1p-120f);
+        const float f = query_factor(quad_max(m), scale2, key_unit<FMT>(), factor);
 #pragma unroll
         for (int k = 0; k < D / 32; ++k)
             op[k] = query_operand<FMT>(raw[k], act, f);
     }
 };
 
-template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&to)[N], const void *from)
+// Columns of the few-row kernels.  A column is a row (a new token's query head)
+// and a scale group: col = row * NG + group.  Its queries are zero outside the
+// group, so a product over all of d leaves the group's share of the score, the
+// lane scales it, and the shares of a row meet in neighbouring lanes.  So a
+// head's rows fill the columns a tile has anyway, and the order of d within
+// the product is free: lane kg takes d = D/4 kg .. + D/4 - 1 of a key row, one
+// contiguous load.
+template <int NG>
+__device__ __forceinline__ float group_sum(float v)  // the same bits in all lanes of a row
 {
-    if constexpr (N % 4 == 0) {
-#pragma unroll
-        for (int j = 0; j < N / 4; ++j) {
-            const u32x4 v = ((const u32x4 *)from)[j];
-            to[4 * j] = v[0], to[4 * j + 1] = v[1], to[4 * j + 2] = v[2], to[4 * j + 3] = v[3];
-        }
-    } else if constexpr (N == 2) {
-        const u32x2 v = *(const u32x2 *)from;
-        to[0] = v[0], to[1] = v[1];
-    } else {
-        to[0] = *(const uint32_t *)from;
-    }
+    if constexpr (NG >= 2)
+        v += std::bit_cast<float>(__builtin_amdgcn_update_dpp(0, std::bit_cast<int>(v), 0xb1, 0xf, 0xf, true));
+    if constexpr (NG >= 4)
+        v += std::bit_cast<float>(__builtin_amdgcn_update_dpp(0, std::bit_cast<int>(v), 0x4e, 0xf, 0xf, true));
+    if constexpr (NG >= 8)  // (half mirror: the four lanes of a quad agree by now)
+        v += std::bit_cast<float>(__builtin_amdgcn_update_dpp(0, std::bit_cast<int>(v), 0x141, 0xf, 0xf, true));
+    return v;
+}
+template <int NG>
+__device__ __forceinline__ float group_max(float v)
+{
+    if constexpr (NG >= 2)
+        v = fmaxf(v, std::bit_cast<float>(__builtin_amdgcn_update_dpp(0, std::bit_cast<int>(v), 0xb1, 0xf, 0xf, true)));
+    if constexpr (NG >= 4)
+        v = fmaxf(v, std::bit_cast<float>(__builtin_amdgcn_update_dpp(0, std::bit_cast<int>(v), 0x4e, 0xf, 0xf, true)));
+    if constexpr (NG >= 8)
+        v = fmaxf(v, std::bit_cast<float>(__builtin_amdgcn_update_dpp(0, std::bit_cast<int>(v), 0x141, 0xf, 0xf, true)));
+    return v;
 }
 
-// Sixteen tokens' keys as they are in memory, a lane's share: row i's dwords
-// 4 m + kg, the scales of rows 4 kg .. + 3, row i's zero-points.
+// The scales of rows 4 kg .. + 3 from `row` in group j, as they are in memory.
+template <int FMT, int NG>
+__device__ __forceinline__ void load_scales(uint32_t (&s)[4], const void *scales, int64_t row, int kg, int j)
+{
+    if constexpr (f32_absmax(FMT)) {
+        const uint32_t *p = (const uint32_t *)scales + row * NG + (uint32_t)(4 * kg * NG + j);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            s[r] = p[r * NG];
+    } else {
+        const uint16_t *p = (const uint16_t *)scales + row * NG + (uint32_t)(4 * kg * NG + j);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            s[r] = p[r * NG];
+    }
+}
+template <int FMT>
+__device__ __forceinline__ float scale_of(uint32_t s)
+{
+    return f32_absmax(FMT) ? std::bit_cast<float>(s) : h2f(s);
+}
+
+// Sixteen tokens' keys as they are in memory, a lane's share: values D/4 kg ..
+// of row i, the scales of rows 4 kg .. + 3 in the lane's group, row i's
+// zero-points.
 template <int FMT, int D, int GS>
 struct KeyTile {
-    static constexpr int NG = D / GS, ZB = (NG + 1) / 2, SB = f32_absmax(FMT) ? 4 : 2;
-    uint32_t w[D / 32], s[NG * SB], z;
+    static constexpr int NG = D / GS, ZB = (NG + 1) / 2, NW = D / 32;
+    uint32_t w[NW], s[4], z;
 
     __device__ __forceinline__ void load(const KvCache &c, int64_t row0, int lane)
     {
         const int i = lane & 15, kg = lane >> 4;
         const int64_t row = row0 >= 0 ? row0 : 0;  // (page 0 is read and not used)
-        const uint8_t *kc = c.k.codes + row * (D / 2);
+        const uint8_t *p = c.k.codes + row * (D / 2) + (uint32_t)(i * (D / 2) + kg * (D / 8));
+        if constexpr (NW == 2) {
+            const u32x2 v = *(const u32x2 *)p;
+            w[0] = v[0], w[1] = v[1];
+        } else {
 #pragma unroll
-        for (int m = 0; m < D / 32; ++m)
-            w[m] = *(const uint32_t *)(kc + (uint32_t)(i * (D / 2) + 16 * m + 4 * kg));
-        load_words(s, (const char *)c.k.scales + row * (NG * SB) + (uint32_t)(4 * kg * NG * SB));
+            for (int m = 0; m < NW / 4; ++m) {
+                const u32x4 v = ((const u32x4 *)p)[m];
+                w[4 * m] = v[0], w[4 * m + 1] = v[1], w[4 * m + 2] = v[2], w[4 * m + 3] = v[3];
+            }
+        }
+        load_scales<FMT, NG>(s, c.k.scales, row, kg, i % NG);
         if constexpr (FMT == Q4_INT4_ASYM) {
             const uint8_t *zp = c.k.zeros + row * ZB + (uint32_t)(i * ZB);
             if constexpr (ZB == 1)
@@ -152,109 +201,83 @@ struct KeyTile {
                 z = *(const uint32_t *)zp;
         }
     }
-    __device__ __forceinline__ float scale(int r, int j) const
+    // Operand m of the row: values D/4 kg + 8 m .. + 7.
+    __device__ __forceinline__ u32x4 operand(int m, int kg, const uint32_t *pairs) const
     {
-        const int e = r * NG + j;
-        if constexpr (f32_absmax(FMT))
-            return std::bit_cast<float>(s[e]);
-        else
-            return h2f((s[e >> 1] >> (16 * (e & 1))) & 0xffffu);
-    }
-    __device__ __forceinline__ KeyZero zero(int j) const
-    {
-        return key_zero(FMT == Q4_INT4_ASYM ? (z >> (4 * j)) & 15u : 8u);
+        uint32_t zp = 8;
+        if constexpr (FMT == Q4_INT4_ASYM)
+            zp = (z >> (4 * (((D / 4) * kg + 8 * m) / GS))) & 15u;
+        return key_operand<FMT>(w[m], key_zero(zp), pairs);
     }
 };
 
-// Sixteen tokens' values, a lane's share of rows 4 kg .. + 3: one dword a
-// group, the scales, the zero-points.
-template <int FMT, int D, int GS>
-struct ValueTile {
-    static constexpr int NG = D / GS, ZB = (NG + 1) / 2, SB = f32_absmax(FMT) ? 4 : 2;
-    uint32_t w[4][NG], s[NG * SB], z[FMT == Q4_INT4_ASYM ? ZB : 1];
+// NT column tiles' queries as operands, and the factor from products to
+// scores.
+template <int FMT, int D, int GS, int NT>
+struct ColQueries {
+    static constexpr int NG = D / GS, NW = D / 32, ROWS = NT * 16 / NG;
+    u32x4 op[NT][NW];
+    float factor[NT];
+    int pos[NT], low[NT];  // the row sees low < t <= pos
 
-    __device__ __forceinline__ void load(const KvCache &c, int64_t row0, int lane)
+    // Row of the lane in column tile n, counted from the first.
+    static __device__ __forceinline__ int row(int n, int lane) { return (16 * n + (lane & 15)) / NG; }
+
+    __device__ __forceinline__ void load(const KvSeq &s, const Rows &rows, int h, int row0, int lane)
     {
-        const int i = lane & 15, kg = lane >> 4;
-        const int64_t row = row0 >= 0 ? row0 : 0;
-        const uint8_t *vc = c.v.codes + row * (D / 2);
-        const uint32_t vo = 4 * kg * (D / 2) + 4 * value_dword<GS>(i);
+        const int nrows = s.fresh * rows.group, kg = lane >> 4, g = lane % NG;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int j = 0; j < NG; ++j)
-                w[r][j] = *(const uint32_t *)(vc + vo + (uint32_t)(r * (D / 2) + j * (GS / 2)));
-        load_words(s, (const char *)c.v.scales + row * (NG * SB) + (uint32_t)(4 * kg * NG * SB));
-        if constexpr (FMT == Q4_INT4_ASYM)
-            load_words(z, c.v.zeros + row * ZB + (uint32_t)(4 * kg * ZB));
-    }
-    __device__ __forceinline__ float scale(int r, int j) const
-    {
-        const int e = r * NG + j;
-        if constexpr (f32_absmax(FMT))
-            return std::bit_cast<float>(s[e]);
-        else
-            return h2f((s[e >> 1] >> (16 * (e & 1))) & 0xffffu);
-    }
-    // The scales of rows at and past `n` become 0 (rows of the lane count from
-    // 4 kg).
-    __device__ __forceinline__ void keep(int n)
-    {
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                const int e = r * NG + j;
-                if constexpr (f32_absmax(FMT))
-                    s[e] = r < n ? s[e] : 0u;
-                else
-                    s[e >> 1] = r < n ? s[e >> 1] : s[e >> 1] & (e & 1 ? 0x0000ffffu : 0xffff0000u);
-            }
-    }
-    // The largest scale (none is negative).
-    __device__ __forceinline__ float largest() const
-    {
-        if constexpr (f32_absmax(FMT)) {
+        for (int n = 0; n < NT; ++n) {
+            const int r = row0 + row(n, lane);
+            const bool live = r < nrows;
+            const int tok = live ? r / rows.group : 0;
+            const int head = h * rows.group + (live ? r - tok * rows.group : 0);
+            const uint16_t *q = rows.q + (int64_t)(s.first + tok) * rows.qts + (int64_t)head * rows.qhs;
+            pos[n] = live ? s.len - s.fresh + tok : -1;
+            low[n] = rows.window > 0 ? pos[n] - rows.window : -1;
+            u32x4 raw[NW];
             float m = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 4 * NG; ++e)
-                m = fmaxf(m, std::bit_cast<float>(s[e]));
-            return m;
-        } else {
-            f16x2 m = std::bit_cast<f16x2>(s[0]);
+            for (int k = 0; k < NW; ++k) {
+                raw[k] = live ? *(const u32x4 *)(q + (D / 4) * kg + 8 * k) : u32x4{0, 0, 0, 0};
+                m = fmaxf(m, query_max(raw[k], rows.act));
+            }
+            const float f = query_factor(quad_max(m), rows.scale2, key_unit<FMT>(), factor[n]);
 #pragma unroll
-            for (int e = 1; e < 2 * NG; ++e)
-                m = __builtin_elementwise_max(m, std::bit_cast<f16x2>(s[e]));
-            return fmaxf((float)m[0], (float)m[1]);
+            for (int k = 0; k < NW; ++k) {
+                const bool mine = ((D / 4) * kg + 8 * k) / GS == g;
+                op[n][k] = query_operand<FMT>(mine ? raw[k] : u32x4{0, 0, 0, 0}, rows.act, f);
+            }
         }
-    }
-    __device__ __forceinline__ uint32_t zero(int r, int j) const
-    {
-        const int byte = r * ZB + (j >> 1);
-        return (z[byte >> 2] >> (8 * (byte & 3) + 4 * (j & 1))) & 15u;
     }
 };
 
-// Scores of 16 tokens (rows 4 kg + r of the tile) by the lane's column, in
-// units of the column's factor.
-template <int FMT, int D, int GS>
-__device__ __forceinline__ f32x4 scores(const KeyTile<FMT, D, GS> &t, const Queries<FMT, D, GS> &q,
-                                        const uint32_t *pairs)
+// Scores of 16 tokens (4 kg + r of the tile) by the lane's row, in units of
+// its factor.
+template <int FMT, int D, int GS, int NT>
+__device__ __forceinline__ void col_scores(const KeyTile<FMT, D, GS> &t, const ColQueries<FMT, D, GS, NT> &q, int kg,
+                                           const uint32_t *pairs, f32x4 (&x)[NT])
 {
-    f32x4 x = {0, 0, 0, 0};
+    f32x4 a[NT];
 #pragma unroll
-    for (int j = 0; j < D / GS; ++j) {
-        const KeyZero z = t.zero(j);
-        f32x4 a = {0, 0, 0, 0};
+    for (int n = 0; n < NT; ++n)
+        a[n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < GS / 32; ++k)
-            a = mfma<Q4_F16>(key_operand<FMT>(t.w[j * (GS / 32) + k], z, pairs), q.op[j * (GS / 32) + k], a);
+    for (int m = 0; m < D / 32; ++m) {
+        const u32x4 k = t.operand(m, kg, pairs);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            a[n] = mfma<Q4_F16>(k, q.op[n][m], a[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            x[r] = __builtin_fmaf(a[r], t.scale(r, j), x[r]);
-    }
-    return x;
+            x[n][r] = group_sum<D / GS>(__builtin_fmaf(a[n][r], scale_of<FMT>(t.s[r]), 0.0f));
 }
+
+// Rows that the few-row kernels take: four column tiles (dim 64) or two.
+inline int few_rows(const KvCache &c) { return (c.dim == 64 ? 64 : 32) / (c.dim / c.g); }
 
 template <class F>
 hipError_t kv_by_shape(int f, int dim, int g, F &&fn)

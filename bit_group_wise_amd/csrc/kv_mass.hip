@@ -8,7 +8,7 @@
 // its tokens over the rows it meets; the 16 columns meet once at the end, in a
 // fixed order.
 //
-//  * Few rows (at most 32 a head): the rows stay in registers and a wave walks
+//  * Few rows (as kv_token.hip takes): the rows stay in registers and a wave walks
 //    over 64-token blocks of a span.  Bound as kv_token.hip.
 //  * Many rows: 64 tokens' keys stay in registers, unpacked once, and the rows
 //    pass by as operands that a first launch laid out (kv_rows_kernel), with
@@ -118,6 +118,7 @@ template <int FMT, int D, int GS, int NT>
 __global__ __launch_bounds__(kBlock) void kv_mass_few_kernel(KvCache c, KvBatch b, Rows rows, int span,
                                                              float *__restrict__ mass, int64_t mass_width)
 {
+    constexpr int NG = D / GS;
     __shared__ uint32_t pairs[FMT == Q4_NF4 ? 256 : 1];
     const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -131,43 +132,58 @@ __global__ __launch_bounds__(kBlock) void kv_mass_few_kernel(KvCache c, KvBatch 
         pairs[tid] = nf4_pair(tid);
         __syncthreads();
     }
-    Queries<FMT, D, GS> q[NT];
+    ColQueries<FMT, D, GS, NT> q;
+    q.load(s, rows, h, 0, lane);
     float st[NT];
-    int pos[NT], low[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int row = 16 * n + i;
+        const int row = ColQueries<FMT, D, GS, NT>::row(n, lane);
         const bool live = row < nrows;
         const int tok = live ? row / rows.group : 0;
         const int head = h * rows.group + (live ? row - tok * rows.group : 0);
-        q[n].load(rows.q + (int64_t)(s.first + tok) * rows.qts + (int64_t)head * rows.qhs, live, rows.act,
-                  rows.scale2, kg);
-        st[n] = live ? rows.stat[(int64_t)(s.first + tok) * rows.q_heads + head] : 0.0f;
-        pos[n] = live ? s.len - s.fresh + tok : -1;
-        low[n] = rows.window > 0 ? pos[n] - rows.window : -1;
+        const float v = rows.stat[(int64_t)(s.first + tok) * rows.q_heads + head];
+        // a row counts once, in its first group's column; rows that see
+        // nothing weigh nothing anywhere
+        st[n] = live && i % NG == 0 && v != -__builtin_inff() ? v : __builtin_inff();
     }
+    const int all_to = s.len - s.fresh, all_from = rows.window > 0 ? s.len - rows.window : 0;
     Pages pg{b.table + (int64_t)seq * b.table_width, c.page_shift, c.heads, h, c.pages, 1 << 30,
              (s.len - 1) >> c.page_shift, -1};
     for (int t0 = begin + wave * kBlk; t0 < end; t0 += kWaves * kBlk) {
-        Keys<FMT, D, GS> k;
-        k.load(c, pg, t0, end, lane, pairs);
+        KeyTile<FMT, D, GS> k[4];
+        uint32_t there = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t row0 = pg.row(t0 + 16 * u, end, lane);
+            there |= (row0 >= 0 ? 1u : 0u) << u;
+            k[u].load(c, row0, lane);
+        }
         float sum[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e)
             sum[e] = 0.0f;
+        f32x4 x[4][NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int u = 0; u < 4; ++u)
+            col_scores<FMT, D, GS, NT>(k[u], q, kg, pairs, x[u]);
+        if (__builtin_expect(t0 + kBlk - 1 > all_to || t0 < all_from, 0)) {
+            const int ta = branch_only(t0);
 #pragma unroll
-            for (int tt = 0; tt < 4; ++tt) {
-                const f32x4 x = tile_scores<FMT, D, GS>(k, tt, q[n].op);
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int at = t0 + 16 * tt + 4 * kg + r;
-                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(x[r], q[n].factor, -st[n]));
-                    sum[4 * tt + r] += at <= pos[n] && at > low[n] ? p : 0.0f;
+                    const int at = ta + 16 * u + 4 * kg + r;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        x[u][n][r] = at <= q.pos[n] && at > q.low[n] ? x[u][n][r] : -__builtin_inff();
                 }
-            }
-        add_mass(sum, mass + ((int64_t)seq * c.heads + h) * mass_width, t0, end, k.there, lane);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                sum[e] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[e >> 2][n][e & 3], q.factor[n], -st[n]));
+        add_mass(sum, mass + ((int64_t)seq * c.heads + h) * mass_width, t0, end, there, lane);
     }
 }
 
@@ -292,7 +308,7 @@ __global__ __launch_bounds__(kBlock, 2) void kv_mass_many_kernel(KvCache c, KvBa
     add_mass(sum, mass + ((int64_t)seq * c.heads + h) * mass_width, t0, s.len, k.there, lane);
 }
 
-bool is_few(const KvBatch &b, int group) { return (int64_t)b.max_new * group <= 32; }
+bool is_few(const KvCache &c, const KvBatch &b, int group) { return (int64_t)b.max_new * group <= few_rows(c); }
 
 int64_t row_tiles(const KvBatch &b, int group) { return (b.tokens * group >> 4) + b.seqs; }
 
@@ -302,7 +318,7 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 size_t kv_mass_workspace(const KvCache &c, const KvBatch &b, int group)
 {
-    if (is_few(b, group))
+    if (is_few(c, b, group))
         return 0;
     const size_t n = (size_t)row_tiles(b, group) * c.heads;
     return round256(n * 16 * sizeof(float2)) + n * c.dim * 32;
@@ -317,16 +333,19 @@ hipError_t launch_kv_mass(int f, const KvCache &c, const KvBatch &b, const Rows 
     return kv_by_shape(f, c.dim, c.g, [&](auto fmt, auto dim, auto gs) {
         constexpr int F = decltype(fmt)::value, D = decltype(dim)::value, GS = decltype(gs)::value;
         const int per = kWaves * kBlk;
-        if (is_few(b, rows.group)) {
+        if (is_few(c, b, rows.group)) {
             // spans of whole rounds, about eight workgroups a compute unit
             const int64_t wgs = (int64_t)b.seqs * c.heads;
             const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((2048 + wgs - 1) / wgs, (range + per - 1) / per));
             const int64_t span = ((range + parts - 1) / parts + per - 1) / per * per;
             const dim3 grid((unsigned)((range + span - 1) / span), c.heads, b.seqs);
-            if ((int64_t)b.max_new * rows.group <= 16)
+            const int64_t cols = (int64_t)b.max_new * rows.group * (D / GS);
+            if (cols <= 16)
                 kv_mass_few_kernel<F, D, GS, 1><<<grid, kBlock, 0, s>>>(c, b, rows, (int)span, mass, mass_width);
-            else
+            else if (cols <= 32)
                 kv_mass_few_kernel<F, D, GS, 2><<<grid, kBlock, 0, s>>>(c, b, rows, (int)span, mass, mass_width);
+            else if constexpr (D == 64)
+                kv_mass_few_kernel<F, D, GS, 4><<<grid, kBlock, 0, s>>>(c, b, rows, (int)span, mass, mass_width);
             return hipGetLastError();
         }
         const size_t n = (size_t)row_tiles(b, rows.group) * c.heads;

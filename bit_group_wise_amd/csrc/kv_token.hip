@@ -6,33 +6,32 @@
 // into the row's factor), weights w_t = 2^(x_t - m), row sum l = sum w_t and
 // output sum w_t V_t / l; raising m scales both sums by 2^(m_old - m_new).
 //
-//  * Scores.  S = K Q^T on 16x16x32 products, 16 cached tokens by 16 rows (the
-//    new tokens' query heads of one key head).  K enters as levels (see
-//    kv_mfma.hpp) less zero-points, one accumulator per scale group, so x =
-//    sum_j s_j acc_j holds exact products.  q is fp16 exactly: a row is scaled
-//    by a power of two that puts its largest value just below 2^12 (values
-//    2^-22 below the largest would round).
-//  * Output.  O^T = V^T W^T, 16 values by 16 rows over 32 tokens.  S leaves
+//  * Scores.  S = K Q^T on 16x16x32 products, 16 cached tokens by 16 columns.
+//    K enters as levels (see kv_mfma.hpp) less zero-points, exactly; q is fp16
+//    exactly (a row is scaled by a power of two that puts its largest value
+//    just below 2^12; values 2^-22 below the largest would round).  Scales are
+//    applied in binary32: a column is a row and a scale group (see kv_attn.hpp).
+//  * Output.  O^T = V^T W^T, 16 values by 16 columns over 32 tokens.  S leaves
 //    each lane with eight tokens of one row; contracting the tokens in that
-//    order makes them the second product's column operand without moving.
-//    A V scale belongs to a token, so it goes into the weight: w_t s_tj, one
-//    set per group j, rounded to fp16 (11 bits against the output's 8 or 11:
-//    each weight is off by at most 2^-12 of itself, independently).  The
-//    zero-points' share, sum_t w_t s_tj z_tj, is one more product of the same
-//    rounded weights with the zero-points as rows, taken off at the end.
+//    order makes them the second product's column operand without moving.  A
+//    V scale belongs to a token and a group, so it goes into the weight of the
+//    group's column, w_t s_tj, rounded to fp16 (11 bits against the output's 8
+//    or 11: each weight is off by at most 2^-11 of itself, independently).  Of
+//    a column's result only its group's values are used.  The zero-points'
+//    share, sum_t w_t s_tj z_tj, is one more product of the same rounded
+//    weights with the zero-points as rows, taken off at the end.
 //  * Reference.  w_t s_tj must stay below 65504 and the largest should be well
 //    inside fp16's normal range whatever the values' size, so m tracks
 //    x_t + log2(s_t), not x_t: it moves only when a weight would pass 2^15 and
 //    is then set to put the largest at 2^6.
 //
-// Bound: HBM traffic of the packed rows in the limit, vector-ALU issue in
-// practice (unpacking about 1.5 instructions a code word's nibble pair, and
-// the softmax of a 16-column tile of which a head group may fill only some).
+// Bound: HBM traffic of the packed rows in the limit; in practice the rate at
+// which lanes receive their words (texture path) and vector-ALU issue.
 //
 // Split: a workgroup's four waves take 32-token steps of one range of one
 // sequence and head in turn and join their sums in LDS; where sequences and
 // heads alone would leave compute units idle the length is split over
-// workgroups and a second launch joins the parts (kv_token_split).
+// workgroups and a second launch joins the parts.
 #include "kv_attn.hpp"
 
 namespace q4 {
@@ -42,23 +41,72 @@ constexpr int kWaves = 4;
 constexpr int kBlock = 64 * kWaves;
 constexpr int kStep = 32;  // tokens per wave and step
 
+// Values of 16 tokens as they are in memory, a lane's share of rows 4 kg .. + 3:
+// the values (D/16) i .. of row part h, the scales in the column's group, the
+// zero-points of the values' groups.
 template <int FMT, int D, int GS>
-__global__ __launch_bounds__(kBlock, (D == 256 ? 1 : GS == 32 && D == 128 ? 2 : 3)) void kv_token_kernel(KvCache c, KvBatch b, Rows rows, Split sp,
-                                                          float *__restrict__ part,
-                                                          float2 *__restrict__ part_ml)
+struct ValueTile {
+    static constexpr int NG = D / GS, ZB = (NG + 1) / 2, W = D < 128 ? D : 128, HV = D / W;
+    uint32_t w[4][HV], s[4], z[FMT == Q4_INT4_ASYM ? ZB : 1];
+
+    __device__ __forceinline__ void load(const KvCache &c, int64_t row0, int lane)
+    {
+        const int i = lane & 15, kg = lane >> 4;
+        const int64_t row = row0 >= 0 ? row0 : 0;  // (page 0 is read and not used)
+        const uint8_t *p = c.v.codes + row * (D / 2) + (uint32_t)(4 * kg * (D / 2) + 4 * value_dword<W>(i));
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int h = 0; h < HV; ++h)
+                w[r][h] = *(const uint32_t *)(p + r * (D / 2) + h * (W / 2));
+        load_scales<FMT, NG>(s, c.v.scales, row, kg, i % NG);
+        if constexpr (FMT == Q4_INT4_ASYM) {
+            const uint32_t *zp = (const uint32_t *)(c.v.zeros + row * ZB + (uint32_t)(4 * kg * ZB));
+#pragma unroll
+            for (int k = 0; k < ZB; ++k)
+                z[k] = zp[k];
+        }
+    }
+    // The scales of the lane's rows from the n-th on become 0.
+    __device__ __forceinline__ void keep(int n)
+    {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            s[r] = r < n ? s[r] : 0u;
+    }
+    __device__ __forceinline__ float largest() const  // (no scale is negative)
+    {
+        return fmaxf(fmaxf(scale_of<FMT>(s[0]), scale_of<FMT>(s[1])), fmaxf(scale_of<FMT>(s[2]), scale_of<FMT>(s[3])));
+    }
+    // Zero-points of rows r and r + 1 in the group of the lane's values of
+    // part h, as the two halves of a word.
+    __device__ __forceinline__ uint32_t zero_pair(int r, int h, int i) const
+    {
+        const int sh = 4 * ((W * h + W / 16 * i) / GS);
+        const uint32_t a = z[r * ZB / 4] >> (8 * (r * ZB % 4)) >> sh;
+        const uint32_t b = z[(r + 1) * ZB / 4] >> (8 * ((r + 1) * ZB % 4)) >> sh;
+        return (a & 15u) | (b & 15u) << 16;
+    }
+};
+
+template <int FMT, int D, int GS, int NT>
+__global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_token_kernel(
+    KvCache c, KvBatch b, Rows rows, Split sp, float *__restrict__ part, float2 *__restrict__ part_ml)
 {
-    constexpr int NG = D / GS, NP = GS / 16;
-    __shared__ float os[kWaves][16][D + 4];
-    __shared__ float2 ml[kWaves][16];
+    constexpr int NG = D / GS, W = D < 128 ? D : 128, HV = D / W, NP = W / 16;
+    constexpr int NR = NT * 16 / NG;                         // rows
+    constexpr int HZ = FMT == Q4_INT4_ASYM ? HV : 1;         // zero-point products
+    __shared__ float os[kWaves][NR][D + 4];
+    __shared__ float2 ml[kWaves][NR];
     __shared__ uint32_t pairs[FMT == Q4_NF4 ? 256 : 1];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int i = lane & 15, kg = lane >> 4;
-    const int seq = blockIdx.z, h = blockIdx.y, ct = blockIdx.x / sp.parts, pt = blockIdx.x % sp.parts;
+    const int seq = blockIdx.z, h = blockIdx.y, pt = blockIdx.x;
     const KvSeq s = kv_seq(b, seq);
     const int nrows = s.fresh * rows.group;
-    if (ct * 16 >= nrows)
+    if (nrows == 0)
         return;
     const int begin = range_begin(s, rows.window) + pt * sp.span;
     const int end = min(s.len, begin + sp.span);
@@ -70,35 +118,30 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : GS == 32 && D == 128 ? 2 : 
         __syncthreads();
     }
 
-    // the lane's column: a new token's query head
-    const int r0 = ct * 16 + i;
-    const bool live = r0 < nrows;
-    const int tok = live ? r0 / rows.group : 0;
-    const int head = h * rows.group + (live ? r0 - tok * rows.group : 0);
-    Queries<FMT, D, GS> q;
-    q.load(rows.q + (int64_t)(s.first + tok) * rows.qts + (int64_t)head * rows.qhs, live, rows.act,
-           rows.scale2, kg);
-    const int pos = live ? s.len - s.fresh + tok : -1;  // sees low < t <= pos
-    const int low = rows.window > 0 ? pos - rows.window : -1;
-    // tokens that every live row sees need no mask
-    const int all_to = s.len - s.fresh + ct * 16 / rows.group;
-    const int all_from = rows.window > 0
-        ? s.len - s.fresh + (min(ct * 16 + 16, nrows) - 1) / rows.group - rows.window + 1 : 0;
+    ColQueries<FMT, D, GS, NT> q;
+    q.load(s, rows, h, 0, lane);
+    // tokens that every row sees need no mask
+    const int all_to = s.len - s.fresh, all_from = rows.window > 0 ? s.len - rows.window : 0;
 
-    const uint32_t sel = value_select<FMT, GS>(i);
-    f32x4 o[NG][NP], oz[NG];
+    const uint32_t sel = value_select<FMT, W>(i);
+    f32x4 o[NT][HV][NP], oz[NT][HZ];
+    float m[NT], l[NT];
 #pragma unroll
-    for (int j = 0; j < NG; ++j) {
-        oz[j] = f32x4{0, 0, 0, 0};
+    for (int n = 0; n < NT; ++n) {
+        m[n] = kNone;
+        l[n] = 0.0f;
 #pragma unroll
-        for (int n = 0; n < NP; ++n)
-            o[j][n] = f32x4{0, 0, 0, 0};
+        for (int v = 0; v < HZ; ++v)
+            oz[n][v] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int v = 0; v < HV; ++v)
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+                o[n][v][p] = f32x4{0, 0, 0, 0};
     }
-    float m = kNone, l = 0.0f;
 
-    Pages pg{b.table + (int64_t)seq * b.table_width, c.page_shift, c.heads, h, c.pages, 0, 0, -1};
-    pg.last = (s.len - 1) >> c.page_shift;
-    pg.first = -1000;
+    Pages pg{b.table + (int64_t)seq * b.table_width, c.page_shift, c.heads, h, c.pages, 1 << 30,
+             (s.len - 1) >> c.page_shift, -1};
     // The registers of a step's keys take the next step's as soon as the scores
     // are formed, those of its values once they are summed: loads are always
     // in flight, without a second set.
@@ -114,14 +157,10 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : GS == 32 && D == 128 ? 2 : 
     }
     while (t0 < end) {
         const int tn = t0 + kWaves * kStep;
-        float x[8];
+        f32x4 x[2][NT];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const f32x4 a = scores<FMT, D, GS>(kt[u], q, pairs);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                x[4 * u + r] = a[r];
-        }
+        for (int u = 0; u < 2; ++u)
+            col_scores<FMT, D, GS, NT>(kt[u], q, kg, pairs, x[u]);
         const int64_t next0 = pg.row(tn, end, lane), next1 = pg.row(tn + 16, end, lane);
         if (tn < end) {
             kt[0].load(c, next0, lane);
@@ -131,69 +170,91 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : GS == 32 && D == 128 ? 2 : 
             const int ta = branch_only(t0);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int n = (u ? row1 : row0) < 0 ? 0 : end - ta - 16 * u - 4 * kg;
-                vt[u].keep(n);
+                const int have = (u ? row1 : row0) < 0 ? 0 : end - ta - 16 * u - 4 * kg;
+                vt[u].keep(have);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int at = ta + 16 * u + 4 * kg + r;
-                    x[4 * u + r] = r < n && at <= pos && at > low ? x[4 * u + r] : -__builtin_inff();
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        x[u][n][r] = r < have && at <= q.pos[n] && at > q.low[n] ? x[u][n][r] : -__builtin_inff();
                 }
             }
         }
-        float top = x[0];
-#pragma unroll
-        for (int e = 1; e < 8; ++e)
-            top = fmaxf(top, x[e]);
         // (2^-40: rows of zeros do not pull the reference down)
-        const float big = fmaxf(fmaxf(vt[0].largest(), vt[1].largest()), 0x1p-40f);
-        const float reach = __builtin_fmaf(top, q.factor, __builtin_amdgcn_logf(big));
-        if (__builtin_expect(__any(reach > m + 15.0f), 0)) {
-            const float to = fmaxf(m, quad_max(reach) - 6.0f);
-            const float f = __builtin_amdgcn_exp2f(m - to);
-            m = to;
-            l *= f;
+        const float big = __builtin_amdgcn_logf(
+            fmaxf(group_max<NG>(fmaxf(vt[0].largest(), vt[1].largest())), 0x1p-40f));
+        float reach[NT];
+        bool move = false;
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                oz[j] *= f;
+        for (int n = 0; n < NT; ++n) {
+            float top = fmaxf(x[0][n][0], x[1][n][0]);
 #pragma unroll
-                for (int n = 0; n < NP; ++n)
-                    o[j][n] *= f;
+            for (int r = 1; r < 4; ++r)
+                top = fmaxf(top, fmaxf(x[0][n][r], x[1][n][r]));
+            reach[n] = __builtin_fmaf(top, q.factor[n], big);
+            move = move || reach[n] > m[n] + 15.0f;
+        }
+        if (__builtin_expect(__any(move), 0)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float to = fmaxf(m[n], quad_max(reach[n]) - 6.0f);
+                const float f = __builtin_amdgcn_exp2f(m[n] - to);
+                m[n] = to;
+                l[n] *= f;
+#pragma unroll
+                for (int v = 0; v < HZ; ++v)
+                    oz[n][v] *= f;
+#pragma unroll
+                for (int v = 0; v < HV; ++v)
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)
+                        o[n][v][p] *= f;
             }
         }
-        float w[8];
+        u32x4 wp[NT];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], q.factor, -m));
-            l += w[e];
-        }
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-            u32x4 wp, va[NP];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int u = e >> 1, r = 2 * (e & 1);
+                const float w0 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[u][n][r], q.factor[n], -m[n]));
+                const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[u][n][r + 1], q.factor[n], -m[n]));
+                l[n] += w0 + w1;
                 // (fma with 0: the scale's conversion is part of v_fma_mix)
-                wp[e] = pair_h2(__builtin_fmaf(w[2 * e], vt[u].scale(r, j), 0.0f),
-                                __builtin_fmaf(w[2 * e + 1], vt[u].scale(r + 1, j), 0.0f));
-                uint32_t p[NP];
-                value_pairs<FMT, GS>(vt[u].w[r][j], vt[u].w[r + 1][j], sel, pairs, p);
-#pragma unroll
-                for (int n = 0; n < NP; ++n)
-                    va[n][e] = p[n];
+                wp[n][e] = pair_h2(__builtin_fmaf(w0, scale_of<FMT>(vt[u].s[r]), 0.0f),
+                                   __builtin_fmaf(w1, scale_of<FMT>(vt[u].s[r + 1]), 0.0f));
             }
 #pragma unroll
-            for (int n = 0; n < NP; ++n)
-                o[j][n] = mfma<Q4_F16>(va[n], wp, o[j][n]);
-            if constexpr (kv_int<FMT>()) {
+        for (int v = 0; v < HV; ++v) {
+            u32x4 va[NP];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int u = e >> 1, r = 2 * (e & 1);
+                uint32_t p[NP];
+                value_pairs<FMT, W>(vt[u].w[r][v], vt[u].w[r + 1][v], sel, pairs, p);
+#pragma unroll
+                for (int k = 0; k < NP; ++k)
+                    va[k][e] = p[k];
+            }
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    o[n][v][k] = mfma<Q4_F16>(va[k], wp[n], o[n][v][k]);
+        }
+        if constexpr (kv_int<FMT>()) {
+#pragma unroll
+            for (int v = 0; v < HZ; ++v) {
                 u32x4 z = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
                 if constexpr (FMT == Q4_INT4_ASYM) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int u = e >> 1, r = 2 * (e & 1);
-                        z[e] = vt[u].zero(r, j) | vt[u].zero(r + 1, j) << 16;
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        z[e] = vt[e >> 1].zero_pair(2 * (e & 1), v, i);
                 }
-                oz[j] = mfma<Q4_F16>(z, wp, oz[j]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    oz[n][v] = mfma<Q4_F16>(z, wp[n], oz[n][v]);
             }
         }
         if (tn < end) {
@@ -206,38 +267,49 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : GS == 32 && D == 128 ? 2 : 
     }
 
     // join the waves
-    l = quad_sum(l);
-    if (kg == 0)
-        ml[wave][i] = float2{m, l};
 #pragma unroll
-    for (int j = 0; j < NG; ++j)
+    for (int n = 0; n < NT; ++n) {
+        const int r0 = ColQueries<FMT, D, GS, NT>::row(n, lane);
+        l[n] = quad_sum(l[n]);
+        if (kg == 0 && i % NG == 0)
+            ml[wave][r0] = float2{m[n], l[n]};
 #pragma unroll
-        for (int n = 0; n < NP; ++n)
+        for (int v = 0; v < HV; ++v) {
+            // values (W/16) (4 kg + r) + k of part v, of use in their group's column
+            if ((W * v + W / 4 * kg) / GS != i % NG)
+                continue;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float unit = value_unit<FMT>() * (kv_int<FMT>() && (n & 1) ? 0.0625f : 1.0f);
-                float v = o[j][n][r] * unit;
-                if constexpr (kv_int<FMT>())
-                    v -= oz[j][r] * value_unit<FMT>();
-                os[wave][i][j * GS + NP * (4 * kg + r) + n] = v;
-            }
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int k = 0; k < NP; k += 4) {
+                    f32x4 y;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float unit = value_unit<FMT>() * (kv_int<FMT>() && (e & 1) ? 0.0625f : 1.0f);
+                        y[e] = o[n][v][k + e][r] * unit;
+                        if constexpr (kv_int<FMT>())
+                            y[e] -= oz[n][HZ == 1 ? 0 : v][r] * value_unit<FMT>();
+                    }
+                    *(f32x4 *)&os[wave][r0][W * v + W / 16 * (4 * kg + r) + k] = y;
+                }
+        }
+    }
     __syncthreads();
-    for (int e = tid; e < 16 * D / 4; e += kBlock) {
-        const int col = e / (D / 4), d = 4 * (e % (D / 4));
-        const int row = ct * 16 + col;
+    for (int e = tid; e < NR * D / 4; e += kBlock) {
+        const int row = e / (D / 4), d = 4 * (e % (D / 4));
         if (row >= nrows)
-            continue;
+            break;
         float mm = kNone;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w)
-            mm = fmaxf(mm, ml[w][col].x);
+            mm = fmaxf(mm, ml[w][row].x);
         f32x4 sum = {0, 0, 0, 0};
         float ll = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            const float f = __builtin_amdgcn_exp2f(ml[w][col].x - mm);
-            ll += ml[w][col].y * f;
-            sum += *(const f32x4 *)&os[w][col][d] * f;
+            const float f = __builtin_amdgcn_exp2f(ml[w][row].x - mm);
+            ll += ml[w][row].y * f;
+            sum += *(const f32x4 *)&os[w][row][d] * f;
         }
         const int tk = row / rows.group;
         const int64_t to = (int64_t)(s.first + tk) * rows.q_heads + h * rows.group + row - tk * rows.group;
@@ -245,8 +317,8 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : GS == 32 && D == 128 ? 2 : 
             const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
             sum *= inv;
             u32x2 pk;
-            pk[0] = rows.act == Q4_F16 ? pack_h2(sum[0], sum[1]) : pack_bf2(sum[0], sum[1]);
-            pk[1] = rows.act == Q4_F16 ? pack_h2(sum[2], sum[3]) : pack_bf2(sum[2], sum[3]);
+            pk[0] = rows.act == Q4_F16 ? pair_h2(sum[0], sum[1]) : pack_bf2(sum[0], sum[1]);
+            pk[1] = rows.act == Q4_F16 ? pair_h2(sum[2], sum[3]) : pack_bf2(sum[2], sum[3]);
             *(u32x2 *)(rows.out + to * D + d) = pk;
             if (d == 0) {
                 const float v = ll > 0.0f ? mm + __builtin_amdgcn_logf(ll) : -__builtin_inff();
@@ -267,11 +339,11 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : GS == 32 && D == 128 ? 2 : 
 // Most parts that a length is split into: as many as give the 256 compute
 // units about four workgroups each, none shorter than 256 tokens; up to 512
 // tokens one (a single launch of at most four steps a wave).
-int most_parts(const KvCache &c, const KvBatch &b, int64_t tiles)
+int most_parts(const KvCache &c, const KvBatch &b)
 {
     if (b.max_len <= 512)
         return 1;
-    const int64_t wgs = b.seqs * c.heads * tiles;
+    const int64_t wgs = (int64_t)b.seqs * c.heads;
     return (int)std::min<int64_t>((1024 + wgs - 1) / wgs, (b.max_len + 255) / 256);
 }
 
@@ -280,9 +352,9 @@ int most_parts(const KvCache &c, const KvBatch &b, int64_t tiles)
 Split token_split(const KvCache &c, const KvBatch &b, int group, int window)
 {
     Split sp;
-    sp.tiles = (int)(((int64_t)b.max_new * group + 15) / 16);
+    sp.tiles = 1;
     const int64_t range = longest_range(b, window);
-    const int64_t parts = range <= 512 ? 1 : most_parts(c, b, sp.tiles);
+    const int64_t parts = range <= 512 ? 1 : most_parts(c, b);
     // whole rounds of the four waves' steps
     const int64_t span = std::max<int64_t>((range + parts - 1) / parts, parts > 1 ? 256 : 1);
     sp.span = (int)((span + kWaves * kStep - 1) / (kWaves * kStep) * (kWaves * kStep));
@@ -294,8 +366,15 @@ hipError_t launch_kv_token(int f, const KvCache &c, const KvBatch &b, const Rows
                            float *part, float2 *part_ml, hipStream_t s)
 {
     return kv_by_shape(f, c.dim, c.g, [&](auto fmt, auto dim, auto gs) {
-        kv_token_kernel<decltype(fmt)::value, decltype(dim)::value, decltype(gs)::value>
-            <<<dim3(sp.parts * sp.tiles, c.heads, b.seqs), kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+        constexpr int F = decltype(fmt)::value, D = decltype(dim)::value, GS = decltype(gs)::value;
+        const dim3 grid(sp.parts, c.heads, b.seqs);
+        const int64_t cols = (int64_t)b.max_new * rows.group * (D / GS);
+        if (cols <= 16)
+            kv_token_kernel<F, D, GS, 1><<<grid, kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+        else if (cols <= 32)
+            kv_token_kernel<F, D, GS, 2><<<grid, kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+        else if constexpr (D == 64)
+            kv_token_kernel<F, D, GS, 4><<<grid, kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
         return hipGetLastError();
     });
 }
