@@ -145,35 +145,136 @@ __device__ __forceinline__ float group_max(float v)
     return v;
 }
 
-// The scales of rows 4 kg .. + 3 from `row` in group j, as they are in memory.
-template <int FMT, int NG>
-__device__ __forceinline__ void load_scales(uint32_t (&s)[4], const void *scales, int64_t row, int kg, int j)
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&to)[N], const void *from)
 {
-    if constexpr (f32_absmax(FMT)) {
-        const uint32_t *p = (const uint32_t *)scales + row * NG + (uint32_t)(4 * kg * NG + j);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            s[r] = p[r * NG];
+    if constexpr (N == 4) {
+        const u32x4 v = *(const u32x4 *)from;
+        to[0] = v[0], to[1] = v[1], to[2] = v[2], to[3] = v[3];
+    } else if constexpr (N == 2) {
+        const u32x2 v = *(const u32x2 *)from;
+        to[0] = v[0], to[1] = v[1];
     } else {
-        const uint16_t *p = (const uint16_t *)scales + row * NG + (uint32_t)(4 * kg * NG + j);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            s[r] = p[r * NG];
+        to[0] = *(const uint32_t *)from;
     }
 }
-template <int FMT>
-__device__ __forceinline__ float scale_of(uint32_t s)
+
+// What a wave keeps in LDS of the tokens it works on.  Every lane needs scales
+// and values of four tokens that other lanes are next to in memory, and a
+// load costs the texture path about 16 cycles however little it fetches
+// (measured: 26-30 narrow loads a step kept it busy two thirds of the time).
+// So memory is read in few wide loads and handed round through LDS, each wave
+// in its own part (its LDS operations stay in order: no barrier).
+
+// Orders a wave's LDS accesses for the compiler (a wave's lanes read what its
+// other lanes wrote; the hardware keeps them in order by itself).
+__device__ __forceinline__ void wave_order()
 {
-    return f32_absmax(FMT) ? std::bit_cast<float>(s) : h2f(s);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
-// Sixteen tokens' keys as they are in memory, a lane's share: values D/4 kg ..
-// of row i, the scales of rows 4 kg .. + 3 in the lane's group, row i's
-// zero-points.
+// Scales and zero-points, a token a lane, all its groups (32 tokens' keys and
+// values, or 64 tokens' keys).
+template <int FMT, int NG, int LANES>
+struct Meta {
+    static constexpr int SB = f32_absmax(FMT) ? 4 : 2, ZB = (NG + 1) / 2, SW = (NG * SB + 3) / 4;
+    struct Lds {
+        __attribute__((aligned(16))) uint8_t s[NG][LANES * SB];
+        __attribute__((aligned(16))) uint8_t z[FMT == Q4_INT4_ASYM ? LANES * ZB : 16];
+    };
+    uint32_t s[SW], z;
+
+    __device__ __forceinline__ void load(const KvHalf &x, int64_t row)
+    {
+        const char *p = (const char *)x.scales + row * (NG * SB);
+        if constexpr (NG * SB == 2)
+            s[0] = *(const uint16_t *)p;
+        else if constexpr (SW == 1)
+            s[0] = *(const uint32_t *)p;
+        else if constexpr (SW == 2) {
+            const u32x2 v = *(const u32x2 *)p;
+            s[0] = v[0], s[1] = v[1];
+        } else {
+#pragma unroll
+            for (int k = 0; k < SW / 4; ++k) {
+                const u32x4 v = ((const u32x4 *)p)[k];
+                s[4 * k] = v[0], s[4 * k + 1] = v[1], s[4 * k + 2] = v[2], s[4 * k + 3] = v[3];
+            }
+        }
+        if constexpr (FMT == Q4_INT4_ASYM) {
+            const uint8_t *zp = x.zeros + row * ZB;
+            if constexpr (ZB == 1)
+                z = *zp;
+            else if constexpr (ZB == 2)
+                z = *(const uint16_t *)zp;
+            else
+                z = *(const uint32_t *)zp;
+        }
+    }
+    __device__ __forceinline__ void put(Lds &to, int lane) const
+    {
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            if constexpr (SB == 4)
+                ((uint32_t *)to.s[j])[lane] = s[j];
+            else
+                ((uint16_t *)to.s[j])[lane] = (uint16_t)(s[j >> 1] >> (16 * (j & 1)));
+        }
+        if constexpr (FMT == Q4_INT4_ASYM) {
+            if constexpr (ZB == 1)
+                to.z[lane] = (uint8_t)z;
+            else if constexpr (ZB == 2)
+                ((uint16_t *)to.z)[lane] = (uint16_t)z;
+            else
+                ((uint32_t *)to.z)[lane] = z;
+        }
+    }
+};
+// The scales of tokens t .. t + 3 in a group.
+template <int FMT>
+struct Scales4 {
+    uint32_t w[f32_absmax(FMT) ? 4 : 2];
+    __device__ __forceinline__ void get(const uint8_t *row, int t)
+    {
+        if constexpr (f32_absmax(FMT)) {
+            const u32x4 v = *(const u32x4 *)(row + 4 * t);
+            w[0] = v[0], w[1] = v[1], w[2] = v[2], w[3] = v[3];
+        } else {
+            const u32x2 v = *(const u32x2 *)(row + 2 * t);
+            w[0] = v[0], w[1] = v[1];
+        }
+    }
+    __device__ __forceinline__ float operator[](int r) const
+    {
+        if constexpr (f32_absmax(FMT))
+            return std::bit_cast<float>(w[r]);
+        else
+            return h2f((w[r >> 1] >> (16 * (r & 1))) & 0xffffu);
+    }
+    // Those from the n-th on become 0.
+    __device__ __forceinline__ void keep(int n)
+    {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if constexpr (f32_absmax(FMT))
+                w[r] = r < n ? w[r] : 0u;
+            else
+                w[r >> 1] = r < n ? w[r >> 1] : w[r >> 1] & (r & 1 ? 0x0000ffffu : 0xffff0000u);
+        }
+    }
+    __device__ __forceinline__ float largest() const  // (no scale is negative)
+    {
+        return fmaxf(fmaxf((*this)[0], (*this)[1]), fmaxf((*this)[2], (*this)[3]));
+    }
+};
+
+// The codes of 16 keys as they are in memory, a lane's share: values D/4 kg ..
+// of row i.
 template <int FMT, int D, int GS>
-struct KeyTile {
+struct KeyCodes {
     static constexpr int NG = D / GS, ZB = (NG + 1) / 2, NW = D / 32;
-    uint32_t w[NW], s[4], z;
+    uint32_t w[NW];
 
     __device__ __forceinline__ void load(const KvCache &c, int64_t row0, int lane)
     {
@@ -190,26 +291,25 @@ struct KeyTile {
                 w[4 * m] = v[0], w[4 * m + 1] = v[1], w[4 * m + 2] = v[2], w[4 * m + 3] = v[3];
             }
         }
-        load_scales<FMT, NG>(s, c.k.scales, row, kg, i % NG);
-        if constexpr (FMT == Q4_INT4_ASYM) {
-            const uint8_t *zp = c.k.zeros + row * ZB + (uint32_t)(i * ZB);
-            if constexpr (ZB == 1)
-                z = *zp;
-            else if constexpr (ZB == 2)
-                z = *(const uint16_t *)zp;
-            else
-                z = *(const uint32_t *)zp;
-        }
     }
-    // Operand m of the row: values D/4 kg + 8 m .. + 7.
-    __device__ __forceinline__ u32x4 operand(int m, int kg, const uint32_t *pairs) const
+    // Operand m of the row: values D/4 kg + 8 m .. + 7; z: the row's
+    // zero-points, shifted to the group of value D/4 kg.
+    __device__ __forceinline__ u32x4 operand(int m, uint32_t z, const uint32_t *pairs) const
     {
         uint32_t zp = 8;
         if constexpr (FMT == Q4_INT4_ASYM)
-            zp = (z >> (4 * (((D / 4) * kg + 8 * m) / GS))) & 15u;
+            zp = (z >> (4 * (8 * m / GS))) & 15u;
         return key_operand<FMT>(w[m], key_zero(zp), pairs);
     }
 };
+// Zero-points of the token `t` from LDS, for KeyCodes::operand.
+template <int D, int GS>
+__device__ __forceinline__ uint32_t key_zeros(const uint8_t *z, int t, int kg)
+{
+    constexpr int ZB = (D / GS + 1) / 2;
+    const uint32_t v = ZB == 1 ? z[t] : ZB == 2 ? ((const uint16_t *)z)[t] : ((const uint32_t *)z)[t];
+    return v >> (4 * (D / 4 * kg / GS));
+}
 
 // NT column tiles' queries as operands, and the factor from products to
 // scores.
@@ -255,8 +355,9 @@ struct ColQueries {
 // Scores of 16 tokens (4 kg + r of the tile) by the lane's row, in units of
 // its factor.
 template <int FMT, int D, int GS, int NT>
-__device__ __forceinline__ void col_scores(const KeyTile<FMT, D, GS> &t, const ColQueries<FMT, D, GS, NT> &q, int kg,
-                                           const uint32_t *pairs, f32x4 (&x)[NT])
+__device__ __forceinline__ void col_scores(const KeyCodes<FMT, D, GS> &t, uint32_t z, const Scales4<FMT> &s,
+                                           const ColQueries<FMT, D, GS, NT> &q, const uint32_t *pairs,
+                                           f32x4 (&x)[NT])
 {
     f32x4 a[NT];
 #pragma unroll
@@ -264,7 +365,7 @@ __device__ __forceinline__ void col_scores(const KeyTile<FMT, D, GS> &t, const C
         a[n] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int m = 0; m < D / 32; ++m) {
-        const u32x4 k = t.operand(m, kg, pairs);
+        const u32x4 k = t.operand(m, z, pairs);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             a[n] = mfma<Q4_F16>(k, q.op[n][m], a[n]);
@@ -272,8 +373,8 @@ __device__ __forceinline__ void col_scores(const KeyTile<FMT, D, GS> &t, const C
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            x[n][r] = group_sum<D / GS>(__builtin_fmaf(a[n][r], scale_of<FMT>(t.s[r]), 0.0f));
+        for (int r = 0; r < 4; ++r)  // (fma with 0: the conversion is part of v_fma_mix)
+            x[n][r] = group_sum<D / GS>(__builtin_fmaf(a[n][r], s[r], 0.0f));
 }
 
 // Rows that the few-row kernels take: four column tiles (dim 64) or two.

@@ -119,6 +119,8 @@ __global__ __launch_bounds__(kBlock) void kv_mass_few_kernel(KvCache c, KvBatch 
                                                              float *__restrict__ mass, int64_t mass_width)
 {
     constexpr int NG = D / GS;
+    using M = Meta<FMT, NG, 64>;
+    __shared__ typename M::Lds share[kWaves];
     __shared__ uint32_t pairs[FMT == Q4_NF4 ? 256 : 1];
     const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -149,23 +151,44 @@ __global__ __launch_bounds__(kBlock) void kv_mass_few_kernel(KvCache c, KvBatch 
     const int all_to = s.len - s.fresh, all_from = rows.window > 0 ? s.len - rows.window : 0;
     Pages pg{b.table + (int64_t)seq * b.table_width, c.page_shift, c.heads, h, c.pages, 1 << 30,
              (s.len - 1) >> c.page_shift, -1};
-    for (int t0 = begin + wave * kBlk; t0 < end; t0 += kWaves * kBlk) {
-        KeyTile<FMT, D, GS> k[4];
-        uint32_t there = 0;
+    KeyCodes<FMT, D, GS> k[4];
+    M meta;
+    uint32_t there = 0;
+    auto load_block = [&](int t0) {
+        int64_t mine = 0;
+        there = 0;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int64_t row0 = pg.row(t0 + 16 * u, end, lane);
             there |= (row0 >= 0 ? 1u : 0u) << u;
+            mine = kg == u ? max(row0, (int64_t)0) + i : mine;
             k[u].load(c, row0, lane);
         }
+        meta.load(c.k, mine);
+    };
+    int t0 = begin + wave * kBlk;
+    if (t0 < end)
+        load_block(t0);
+    for (; t0 < end; t0 += kWaves * kBlk) {
+        typename M::Lds &mt = share[wave];
+        const uint32_t here = there;
         float sum[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e)
             sum[e] = 0.0f;
+        wave_order();
+        meta.put(mt, lane);
+        wave_order();
         f32x4 x[4][NT];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            col_scores<FMT, D, GS, NT>(k[u], q, kg, pairs, x[u]);
+        for (int u = 0; u < 4; ++u) {
+            Scales4<FMT> ks;
+            ks.get(mt.s[i % NG], 16 * u + 4 * kg);
+            const uint32_t z = FMT == Q4_INT4_ASYM ? key_zeros<D, GS>(mt.z, 16 * u + i, kg) : 0u;
+            col_scores<FMT, D, GS, NT>(k[u], z, ks, q, pairs, x[u]);
+        }
+        if (t0 + kWaves * kBlk < end)
+            load_block(t0 + kWaves * kBlk);
         if (__builtin_expect(t0 + kBlk - 1 > all_to || t0 < all_from, 0)) {
             const int ta = branch_only(t0);
 #pragma unroll
@@ -183,7 +206,7 @@ __global__ __launch_bounds__(kBlock) void kv_mass_few_kernel(KvCache c, KvBatch 
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 sum[e] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[e >> 2][n][e & 3], q.factor[n], -st[n]));
-        add_mass(sum, mass + ((int64_t)seq * c.heads + h) * mass_width, t0, end, there, lane);
+        add_mass(sum, mass + ((int64_t)seq * c.heads + h) * mass_width, t0, end, here, lane);
     }
 }
 

@@ -41,53 +41,62 @@ constexpr int kWaves = 4;
 constexpr int kBlock = 64 * kWaves;
 constexpr int kStep = 32;  // tokens per wave and step
 
-// Values of 16 tokens as they are in memory, a lane's share of rows 4 kg .. + 3:
-// the values (D/16) i .. of row part h, the scales in the column's group, the
-// zero-points of the values' groups.
-template <int FMT, int D, int GS>
-struct ValueTile {
-    static constexpr int NG = D / GS, ZB = (NG + 1) / 2, W = D < 128 ? D : 128, HV = D / W;
-    uint32_t w[4][HV], s[4], z[FMT == Q4_INT4_ASYM ? ZB : 1];
+// The values of a step's 32 tokens: as they are in memory, 16 bytes a lane in a
+// row, and from LDS a lane's share of rows 4 kg .. + 3, the values (D/16) i ..
+// of row part h.
+template <int D>
+struct ValueCodes {
+    static constexpr int W = D < 128 ? D : 128, HV = D / W, RD = D / 8, NL = D / 64;  // 16-byte loads
+    static constexpr int STRIDE = 4 * RD + (D == 64 ? 8 : 16);  // words of four rows: no two lanes on a bank
+    struct Lds {
+        __attribute__((aligned(16))) uint32_t v[2][4 * STRIDE];
+    };
+    u32x4 w[NL];
 
-    __device__ __forceinline__ void load(const KvCache &c, int64_t row0, int lane)
+    // Place k of the lane: subtile u, row, 16-byte chunk.
+    static __device__ __forceinline__ void place(int k, int lane, int &u, int &row, int &chunk)
     {
-        const int i = lane & 15, kg = lane >> 4;
-        const int64_t row = row0 >= 0 ? row0 : 0;  // (page 0 is read and not used)
-        const uint8_t *p = c.v.codes + row * (D / 2) + (uint32_t)(4 * kg * (D / 2) + 4 * value_dword<W>(i));
+        const int e = 64 * k + lane, at = e % (16 * (D / 32));
+        u = e / (16 * (D / 32));
+        row = at / (D / 32);
+        chunk = at % (D / 32);
+    }
+    __device__ __forceinline__ void load(const KvCache &c, int64_t row0, int64_t row1, int lane)
+    {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int h = 0; h < HV; ++h)
-                w[r][h] = *(const uint32_t *)(p + r * (D / 2) + h * (W / 2));
-        load_scales<FMT, NG>(s, c.v.scales, row, kg, i % NG);
-        if constexpr (FMT == Q4_INT4_ASYM) {
-            const uint32_t *zp = (const uint32_t *)(c.v.zeros + row * ZB + (uint32_t)(4 * kg * ZB));
-#pragma unroll
-            for (int k = 0; k < ZB; ++k)
-                z[k] = zp[k];
+        for (int k = 0; k < NL; ++k) {
+            int u, row, chunk;
+            place(k, lane, u, row, chunk);
+            const int64_t r = max(u ? row1 : row0, (int64_t)0);  // (page 0 is read and not used)
+            w[k] = *(const u32x4 *)(c.v.codes + r * (D / 2) + (uint32_t)(row * (D / 2) + 16 * chunk));
         }
     }
-    // The scales of the lane's rows from the n-th on become 0.
-    __device__ __forceinline__ void keep(int n)
+    __device__ __forceinline__ void put(Lds &to, int lane) const
     {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            s[r] = r < n ? s[r] : 0u;
+        for (int k = 0; k < NL; ++k) {
+            int u, row, chunk;
+            place(k, lane, u, row, chunk);
+            *(u32x4 *)&to.v[u][(row >> 2) * STRIDE + (row & 3) * RD + 4 * chunk] = w[k];
+        }
     }
-    __device__ __forceinline__ float largest() const  // (no scale is negative)
+    static __device__ __forceinline__ uint32_t get(const Lds &from, int u, int r, int h, int i, int kg)
     {
-        return fmaxf(fmaxf(scale_of<FMT>(s[0]), scale_of<FMT>(s[1])), fmaxf(scale_of<FMT>(s[2]), scale_of<FMT>(s[3])));
-    }
-    // Zero-points of rows r and r + 1 in the group of the lane's values of
-    // part h, as the two halves of a word.
-    __device__ __forceinline__ uint32_t zero_pair(int r, int h, int i) const
-    {
-        const int sh = 4 * ((W * h + W / 16 * i) / GS);
-        const uint32_t a = z[r * ZB / 4] >> (8 * (r * ZB % 4)) >> sh;
-        const uint32_t b = z[(r + 1) * ZB / 4] >> (8 * ((r + 1) * ZB % 4)) >> sh;
-        return (a & 15u) | (b & 15u) << 16;
+        return from.v[u][kg * STRIDE + r * RD + h * (W / 8) + value_dword<W>(i)];
     }
 };
+
+// Zero-points of tokens t and t + 1 in the group of the lane's values of part
+// h, as the two halves of a word; z: those of four tokens from 4 kg.
+template <int D, int GS, int ZB>
+__device__ __forceinline__ uint32_t zero_pair(const uint32_t *z, int r, int h, int i)
+{
+    constexpr int W = D < 128 ? D : 128;
+    const int sh = 4 * ((W * h + W / 16 * i) / GS);
+    const uint32_t a = z[r * ZB / 4] >> (8 * (r * ZB % 4)) >> sh;
+    const uint32_t b = z[(r + 1) * ZB / 4] >> (8 * ((r + 1) * ZB % 4)) >> sh;
+    return (a & 15u) | (b & 15u) << 16;
+}
 
 template <int FMT, int D, int GS, int NT>
 __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_token_kernel(
@@ -96,7 +105,18 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
     constexpr int NG = D / GS, W = D < 128 ? D : 128, HV = D / W, NP = W / 16;
     constexpr int NR = NT * 16 / NG;                         // rows
     constexpr int HZ = FMT == Q4_INT4_ASYM ? HV : 1;         // zero-point products
-    __shared__ float os[kWaves][NR][D + 4];
+    constexpr int ZB = (NG + 1) / 2;
+    using Codes = ValueCodes<D>;
+    using M = Meta<FMT, NG, 64>;  // lanes 0..31: keys, 32..63: values
+    struct Work {
+        typename Codes::Lds v;
+        typename M::Lds m;
+    };
+    union Share {  // a wave's: the step's, and its sums in the end
+        Work work;
+        float os[NR][D + 4];
+    };
+    __shared__ Share share[kWaves];
     __shared__ float2 ml[kWaves][NR];
     __shared__ uint32_t pairs[FMT == Q4_NF4 ? 256 : 1];
 
@@ -142,36 +162,49 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
 
     Pages pg{b.table + (int64_t)seq * b.table_width, c.page_shift, c.heads, h, c.pages, 1 << 30,
              (s.len - 1) >> c.page_shift, -1};
-    // The registers of a step's keys take the next step's as soon as the scores
-    // are formed, those of its values once they are summed: loads are always
-    // in flight, without a second set.
-    KeyTile<FMT, D, GS> kt[2];
-    ValueTile<FMT, D, GS> vt[2];
+    // The registers of a step's codes take the next step's as soon as they are
+    // unpacked or in LDS: loads are in flight most of the time without a
+    // second set.
+    Work &wk = share[wave].work;
+    KeyCodes<FMT, D, GS> kt[2];
+    Codes vt;
+    M meta;
     int t0 = begin + wave * kStep;
     int64_t row0 = pg.row(t0, end, lane), row1 = pg.row(t0 + 16, end, lane);
-    if (t0 < end) {
-        kt[0].load(c, row0, lane);
-        kt[1].load(c, row1, lane);
-        vt[0].load(c, row0, lane);
-        vt[1].load(c, row1, lane);
-    }
+    auto load_step = [&](int64_t r0, int64_t r1) {
+        kt[0].load(c, r0, lane);
+        kt[1].load(c, r1, lane);
+        const int64_t r = max(lane & 16 ? r1 : r0, (int64_t)0) + (lane & 15);
+        meta.load(lane < 32 ? c.k : c.v, r);
+        vt.load(c, r0, r1, lane);
+    };
+    if (t0 < end)
+        load_step(row0, row1);
     while (t0 < end) {
         const int tn = t0 + kWaves * kStep;
+        wave_order();
+        meta.put(wk.m, lane);
+        vt.put(wk.v, lane);
+        wave_order();
         f32x4 x[2][NT];
+        Scales4<FMT> vs[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-            col_scores<FMT, D, GS, NT>(kt[u], q, kg, pairs, x[u]);
-        const int64_t next0 = pg.row(tn, end, lane), next1 = pg.row(tn + 16, end, lane);
-        if (tn < end) {
-            kt[0].load(c, next0, lane);
-            kt[1].load(c, next1, lane);
+        for (int u = 0; u < 2; ++u) {
+            Scales4<FMT> ks;
+            ks.get(wk.m.s[i % NG], 16 * u + 4 * kg);
+            vs[u].get(wk.m.s[i % NG], 32 + 16 * u + 4 * kg);
+            const uint32_t z = FMT == Q4_INT4_ASYM ? key_zeros<D, GS>(wk.m.z, 16 * u + i, kg) : 0u;
+            col_scores<FMT, D, GS, NT>(kt[u], z, ks, q, pairs, x[u]);
         }
+        const int64_t next0 = pg.row(tn, end, lane), next1 = pg.row(tn + 16, end, lane);
+        if (tn < end)
+            load_step(next0, next1);
         if (__builtin_expect(row0 < 0 || row1 < 0 || t0 + kStep - 1 > all_to || t0 < all_from, 0)) {
             const int ta = branch_only(t0);
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int have = (u ? row1 : row0) < 0 ? 0 : end - ta - 16 * u - 4 * kg;
-                vt[u].keep(have);
+                vs[u].keep(have);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int at = ta + 16 * u + 4 * kg + r;
@@ -183,7 +216,7 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
         }
         // (2^-40: rows of zeros do not pull the reference down)
         const float big = __builtin_amdgcn_logf(
-            fmaxf(group_max<NG>(fmaxf(vt[0].largest(), vt[1].largest())), 0x1p-40f));
+            fmaxf(group_max<NG>(fmaxf(vs[0].largest(), vs[1].largest())), 0x1p-40f));
         float reach[NT];
         bool move = false;
 #pragma unroll
@@ -222,8 +255,7 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
                 const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[u][n][r + 1], q.factor[n], -m[n]));
                 l[n] += w0 + w1;
                 // (fma with 0: the scale's conversion is part of v_fma_mix)
-                wp[n][e] = pair_h2(__builtin_fmaf(w0, scale_of<FMT>(vt[u].s[r]), 0.0f),
-                                   __builtin_fmaf(w1, scale_of<FMT>(vt[u].s[r + 1]), 0.0f));
+                wp[n][e] = pair_h2(__builtin_fmaf(w0, vs[u][r], 0.0f), __builtin_fmaf(w1, vs[u][r + 1], 0.0f));
             }
 #pragma unroll
         for (int v = 0; v < HV; ++v) {
@@ -232,7 +264,8 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
             for (int e = 0; e < 4; ++e) {
                 const int u = e >> 1, r = 2 * (e & 1);
                 uint32_t p[NP];
-                value_pairs<FMT, W>(vt[u].w[r][v], vt[u].w[r + 1][v], sel, pairs, p);
+                value_pairs<FMT, W>(Codes::get(wk.v, u, r, v, i, kg), Codes::get(wk.v, u, r + 1, v, i, kg), sel,
+                                    pairs, p);
 #pragma unroll
                 for (int k = 0; k < NP; ++k)
                     va[k][e] = p[k];
@@ -249,17 +282,17 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
                 u32x4 z = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
                 if constexpr (FMT == Q4_INT4_ASYM) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        z[e] = vt[e >> 1].zero_pair(2 * (e & 1), v, i);
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t zw[ZB];
+                        load_words(zw, wk.m.z + ZB * (32 + 16 * u + 4 * kg));
+                        z[2 * u] = zero_pair<D, GS, ZB>(zw, 0, v, i);
+                        z[2 * u + 1] = zero_pair<D, GS, ZB>(zw, 2, v, i);
+                    }
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     oz[n][v] = mfma<Q4_F16>(z, wp[n], oz[n][v]);
             }
-        }
-        if (tn < end) {
-            vt[0].load(c, next0, lane);
-            vt[1].load(c, next1, lane);
         }
         t0 = tn;
         row0 = next0;
@@ -267,6 +300,7 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
     }
 
     // join the waves
+    wave_order();
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int r0 = ColQueries<FMT, D, GS, NT>::row(n, lane);
@@ -290,7 +324,7 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
                         if constexpr (kv_int<FMT>())
                             y[e] -= oz[n][HZ == 1 ? 0 : v][r] * value_unit<FMT>();
                     }
-                    *(f32x4 *)&os[wave][r0][W * v + W / 16 * (4 * kg + r) + k] = y;
+                    *(f32x4 *)&share[wave].os[r0][W * v + W / 16 * (4 * kg + r) + k] = y;
                 }
         }
     }
@@ -309,7 +343,7 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
         for (int w = 0; w < kWaves; ++w) {
             const float f = __builtin_amdgcn_exp2f(ml[w][row].x - mm);
             ll += ml[w][row].y * f;
-            sum += *(const f32x4 *)&os[w][row][d] * f;
+            sum += *(const f32x4 *)&share[w].os[row][d] * f;
         }
         const int tk = row / rows.group;
         const int64_t to = (int64_t)(s.first + tk) * rows.q_heads + h * rows.group + row - tk * rows.group;
