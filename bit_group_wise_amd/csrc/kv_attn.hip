@@ -5,12 +5,20 @@
 namespace q4 {
 namespace {
 
-// Joins the parts of a row: one workgroup per new token and query head.
-template <int D>
-__global__ __launch_bounds__(D) void kv_join_kernel(KvBatch b, Rows rows, Split sp, const float *__restrict__ part,
-                                                    const float2 *__restrict__ part_ml)
+constexpr int kJoin = 256;
+
+// Joins the parts of a row (a new token's query head): D / 4 lanes a part,
+// TEAMS parts at a time.  Many parts are shared by a workgroup's teams; few
+// are summed by one team, the workgroup taking several rows.
+template <int D, bool MANY>
+__global__ __launch_bounds__(kJoin) void kv_join_kernel(KvBatch b, Rows rows, Split sp, const float *__restrict__ part,
+                                                        const float2 *__restrict__ part_ml)
 {
-    const int seq = blockIdx.z, head = blockIdx.y, tok = blockIdx.x, d = threadIdx.x;
+    constexpr int LANES = D / 4, TEAMS = MANY ? kJoin / LANES : 1, RPB = kJoin / (LANES * TEAMS);
+    __shared__ f32x4 sums[MANY ? TEAMS : 1][LANES];
+    __shared__ float ls[TEAMS];
+    const int seq = blockIdx.z, head = blockIdx.y, tok = blockIdx.x * RPB + threadIdx.x / (LANES * TEAMS);
+    const int team = threadIdx.x / LANES % TEAMS, d = threadIdx.x % LANES;
     const KvSeq s = kv_seq(b, seq);
     if (tok >= s.fresh)
         return;
@@ -20,17 +28,43 @@ __global__ __launch_bounds__(D) void kv_join_kernel(KvBatch b, Rows rows, Split 
     const int n = max(1, (seen + sp.span - 1) / sp.span);
     const float2 *ml = part_ml + to * sp.parts;
     float m = kNone;
-    for (int p = 0; p < n; ++p)
-        m = fmaxf(m, ml[p].x);
-    float sum = 0.0f, l = 0.0f;
-#pragma unroll 4
-    for (int p = 0; p < n; ++p) {
-        const float f = __builtin_amdgcn_exp2f(ml[p].x - m);
-        l += ml[p].y * f;
-        sum += part[(to * sp.parts + p) * D + d] * f;
+    if constexpr (MANY) {
+        for (int p = threadIdx.x & 63; p < n; p += 64)
+            m = fmaxf(m, ml[p].x);
+#pragma unroll
+        for (int e = 1; e < 64; e <<= 1)
+            m = fmaxf(m, __shfl_xor(m, e));
+    } else {
+        for (int p = 0; p < n; ++p)
+            m = fmaxf(m, ml[p].x);
     }
-    const float v = l > 0.0f ? sum / l : 0.0f;
-    rows.out[to * D + d] = (uint16_t)(rows.act == Q4_F16 ? f2h_bits(v) : f2bf_bits(v));
+    f32x4 sum = {0, 0, 0, 0};
+    float l = 0.0f;
+#pragma unroll 4
+    for (int p = team; p < n; p += TEAMS) {
+        const float2 e = ml[p];
+        const float f = __builtin_amdgcn_exp2f(e.x - m);
+        l += e.y * f;
+        sum += *(const f32x4 *)(part + (to * sp.parts + p) * D + 4 * d) * f;
+    }
+    if constexpr (MANY) {
+        sums[team][d] = sum;
+        if (d == 0)
+            ls[team] = l;
+        __syncthreads();
+        if (team)
+            return;
+#pragma unroll
+        for (int e = 1; e < TEAMS; ++e) {
+            sum += sums[e][d];
+            l += ls[e];
+        }
+    }
+    sum *= l > 0.0f ? 1.0f / l : 0.0f;
+    u32x2 pk;
+    pk[0] = rows.act == Q4_F16 ? pair_h2(sum[0], sum[1]) : pack_bf2(sum[0], sum[1]);
+    pk[1] = rows.act == Q4_F16 ? pair_h2(sum[2], sum[3]) : pack_bf2(sum[2], sum[3]);
+    *(u32x2 *)(rows.out + to * D + 4 * d) = pk;
     if (d == 0) {
         const float e = l > 0.0f ? m + __builtin_amdgcn_logf(l) : -__builtin_inff();
         if (rows.lse)
@@ -38,6 +72,17 @@ __global__ __launch_bounds__(D) void kv_join_kernel(KvBatch b, Rows rows, Split 
         if (rows.stat)
             rows.stat[to] = e;
     }
+}
+
+template <int D>
+void join(const KvBatch &b, const Rows &rows, const Split &sp, const float *part, const float2 *part_ml, hipStream_t s)
+{
+    constexpr int RPB = kJoin / (D / 4);
+    if (sp.parts > 4)
+        kv_join_kernel<D, true><<<dim3(b.max_new, rows.q_heads, b.seqs), kJoin, 0, s>>>(b, rows, sp, part, part_ml);
+    else
+        kv_join_kernel<D, false><<<dim3((b.max_new + RPB - 1) / RPB, rows.q_heads, b.seqs), kJoin, 0, s>>>(b, rows, sp, part,
+                                                                                                     part_ml);
 }
 
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -86,13 +131,12 @@ hipError_t launch_kv_attention(int f, const KvCache &c, const KvBatch &b, int ac
     if (e != hipSuccess)
         return e;
     if (sp.parts > 1) {
-        const dim3 grid(b.max_new, q_heads, b.seqs);
         if (c.dim == 64)
-            kv_join_kernel<64><<<grid, 64, 0, s>>>(b, rows, sp, part, part_ml);
+            join<64>(b, rows, sp, part, part_ml, s);
         else if (c.dim == 128)
-            kv_join_kernel<128><<<grid, 128, 0, s>>>(b, rows, sp, part, part_ml);
+            join<128>(b, rows, sp, part, part_ml, s);
         else
-            kv_join_kernel<256><<<grid, 256, 0, s>>>(b, rows, sp, part, part_ml);
+            join<256>(b, rows, sp, part, part_ml, s);
         e = hipGetLastError();
         if (e != hipSuccess)
             return e;

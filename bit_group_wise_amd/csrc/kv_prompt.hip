@@ -450,8 +450,8 @@ int rows_a_block(int dim) { return dim == 64 ? prompt_rows<64>() : dim == 128 ? 
 
 }  // namespace
 
-// Parts only where rows alone would leave compute units idle: as many as give
-// about two workgroups each, none shorter than 512 tokens.
+// Parts only where rows alone would leave compute units idle: as many as leave
+// one workgroup to each of the 256, none shorter than 512 tokens.
 Split prompt_split(const KvCache &c, const KvBatch &b, int group, int window)
 {
     Split sp;
@@ -459,7 +459,7 @@ Split prompt_split(const KvCache &c, const KvBatch &b, int group, int window)
     sp.tiles = (int)(((int64_t)b.max_new * group + rows - 1) / rows);
     const int64_t range = longest_range(b, window);
     const int64_t wgs = (int64_t)b.seqs * c.heads * sp.tiles;
-    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>((512 + wgs - 1) / wgs, range / 512));
+    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(256 / wgs, range / 512));
     sp.span = (int)std::max<int64_t>(((range + parts - 1) / parts + 127) / 128 * 128, 128);
     sp.parts = (int)std::max<int64_t>((range + sp.span - 1) / sp.span, 1);
     return sp;
