@@ -33,7 +33,7 @@ q4_status check_cache(const q4_kv_cache *c)
         return Q4_EINVAL;
     if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128 && c->page != 256)
         return Q4_EUNSUPPORTED;
-    if (c->pages > INT32_MAX || c->heads > kMaxGridYZ)
+    if (c->pages > INT32_MAX || 2 * (int64_t)c->heads > kMaxGridYZ)  // (a grid counts heads of keys and of values)
         return Q4_EUNSUPPORTED;
     if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales)
         return Q4_EINVAL;

@@ -9,10 +9,12 @@
 //
 // gfx950 mapping: a lane owns 8 consecutive values (16 bytes in, one dword of
 // codes out), so a row is dim / 8 lanes and a group g / 8 adjacent lanes
-// joined by cross-lane maxima.  Keys and values of a sequence go in one
-// launch: the grid's y counts sequences, x their (key | value, token, head,
-// chunk) in order, so that neighbouring lanes read neighbouring bytes.
+// joined by cross-lane maxima.  Keys and values go in one launch: the grid
+// counts sequences (z), heads of keys and of values (y) and stretches of new
+// tokens (x), so a workgroup's rows lie next to each other in the cache and
+// nothing but the page is looked up a lane.
 #include "kv_common.hpp"
+#include "q4_code.hpp"
 
 namespace q4 {
 namespace {
@@ -35,30 +37,22 @@ __constant__ NF4Bucket c_buckets[33] = {
 #undef B
 };
 
-template <int LPG>
-__device__ __forceinline__ float group_max(float v)
-{
-#pragma unroll
-    for (int d = 1; d < LPG; d <<= 1)
-        v = fmaxf(v, __shfl_xor(v, d));
-    return v;
-}
-
-// (key | value, token, head, chunk of 8 values) of item i of a sequence.
+// What a lane works on: 8 values of a new token's row.
 struct Item {
-    int half, tok, head, chunk;
+    int tok, chunk, pos;
     bool in;
+    int64_t row;  // in the pool, or -1
 };
-__device__ __forceinline__ Item item_of(int64_t i, int fresh, int heads, int chunk_shift)
+__device__ __forceinline__ Item item_of(const KvCache &c, const KvBatch &b, const KvSeq &s, int seq, int h,
+                                        int chunk_shift)
 {
     Item t;
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     t.chunk = (int)(i & ((1 << chunk_shift) - 1));
-    const int64_t row = i >> chunk_shift;
-    const int64_t tok = row / heads;
-    t.head = (int)(row - tok * heads);
-    t.in = tok < 2 * (int64_t)fresh;
-    t.half = tok >= fresh;
-    t.tok = (int)(t.half ? tok - fresh : tok);
+    t.in = (i >> chunk_shift) < s.fresh;
+    t.tok = (int)(i >> chunk_shift);
+    t.pos = s.len - s.fresh + t.tok;
+    t.row = t.in && t.pos >= 0 ? kv_row(c, b.table + (int64_t)seq * b.table_width, t.pos, h) : -1;
     return t;
 }
 
@@ -73,20 +67,16 @@ __global__ __launch_bounds__(kBlock) void kv_append_kernel(
             buckets[threadIdx.x] = c_buckets[threadIdx.x];
         __syncthreads();
     }
-    const int seq = blockIdx.y;
+    const int seq = blockIdx.z, half = blockIdx.y & 1, h = blockIdx.y >> 1;
     const KvSeq s = kv_seq(b, seq);
-    const Item t = item_of((int64_t)blockIdx.x * kBlock + threadIdx.x, s.fresh, c.heads, chunk_shift);
-    const int pos = s.len - s.fresh + t.tok;
-    // every lane of a group has the same token, so a group leaves as one
-    if (!t.in || pos < 0)
+    const Item t = item_of(c, b, s, seq, h, chunk_shift);
+    // every lane of a row has the same token, so a group leaves as one
+    if (t.row < 0)
         return;
-    const int64_t row = kv_row(c, b.table + (int64_t)seq * b.table_width, pos, t.head);
-    if (row < 0)
-        return;
-    const KvHalf &to = t.half ? c.v : c.k;
-    const int64_t src = (int64_t)(s.first + t.tok) * (t.half ? vts : kts) +
-                        (int64_t)t.head * (t.half ? vhs : khs) + 8 * t.chunk;
-    const u32x4 raw = *(const u32x4 *)((t.half ? v : k) + src);
+    const KvHalf &to = half ? c.v : c.k;
+    const uint16_t *from = half ? v + (int64_t)(s.first + t.tok) * vts + (int64_t)h * vhs
+                                : k + (int64_t)(s.first + t.tok) * kts + (int64_t)h * khs;
+    const u32x4 raw = __builtin_nontemporal_load((const u32x4 *)(from + 8 * t.chunk));
     float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -108,23 +98,30 @@ __global__ __launch_bounds__(kBlock) void kv_append_kernel(
             lo = fminf(lo, x[i]);
             hi = fmaxf(hi, x[i]);
         }
+        lo = group_min<LPG>(lo);
         hi = group_max<LPG>(hi);
-        lo = -group_max<LPG>(-lo);
-        const uint32_t sb = f2h_bits(fminf((hi - lo) / 15.0f, 65504.0f));
+        // (the constant reciprocal is checked for differences of fp16 values)
+        const float q = IN == Q4_F16 ? div_mk(hi - lo, 15.0f, kInv15) : (hi - lo) / 15.0f;
+        const uint32_t sb = f2h_bits(keep_f32(fminf(q, 65504.0f)));
         const float d = h2f(sb);
-        const float z = d > 0.0f ? fminf(fmaxf(rintf(-lo / d), 0.0f), 15.0f) : 0.0f;
+        int z = 0;
+        if (d != 0.0f) {
+            const float r = rcp_rn(d);
+            z = (int)fminf(fmaxf(__builtin_rintf(div_mk(-lo, d, r)), 0.0f), 15.0f);
+            const float lo_c = kRint - (float)z;
+            uint32_t q8[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float q = d > 0.0f ? fminf(fmaxf(rintf(x[i] / d) + z, 0.0f), 15.0f) : 0.0f;
-            word |= (uint32_t)q << (4 * i);
+            for (int i = 0; i < 8; ++i)
+                q8[i] = code_bits(div_mk(x[i], d, r), lo_c, lo_c + 15.0f);
+            word = pack8(q8, kRintBias - (uint32_t)z);
         }
         // the odd group's zero-point joins the even one's byte
-        const float z1 = __shfl_down(z, LPG);
+        const int z1 = __shfl_down(z, LPG);
         if (first) {
-            ((uint16_t *)to.scales)[row * groups + j] = (uint16_t)sb;
+            ((uint16_t *)to.scales)[t.row * groups + j] = (uint16_t)sb;
             if ((j & 1) == 0)
-                to.zeros[row * kv_zero_bytes(c.dim, c.g) + (j >> 1)] =
-                    (uint8_t)((uint32_t)z | (j + 1 < groups ? (uint32_t)z1 << 4 : 0u));
+                to.zeros[t.row * kv_zero_bytes(c.dim, c.g) + (j >> 1)] =
+                    (uint8_t)(z | (j + 1 < groups ? z1 << 4 : 0));
         }
     } else {
         float a = 0.0f;
@@ -133,80 +130,97 @@ __global__ __launch_bounds__(kBlock) void kv_append_kernel(
             a = fmaxf(a, fabsf(x[i]));
         a = group_max<LPG>(a);
         if constexpr (FMT == Q4_INT4_SYM) {
-            const uint32_t sb = f2h_bits(fminf(a / 7.0f, 65504.0f));
+            const uint32_t sb = f2h_bits(keep_f32(fminf(div_mk(a, 7.0f, kInv7), 65504.0f)));
             const float d = h2f(sb);
+            if (d != 0.0f) {
+                const float r = rcp_rn(d);
+                uint32_t q8[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float q = d > 0.0f ? fminf(fmaxf(rintf(x[i] / d), -8.0f), 7.0f) : 0.0f;
-                word |= (uint32_t)(int)(q + 8.0f) << (4 * i);
+                for (int i = 0; i < 8; ++i)
+                    q8[i] = code_bits(div_mk(x[i], d, r), kRint - 8.0f, kRint + 7.0f);
+                word = pack8(q8, kRintBias - 8u);
+            } else {
+                word = 0x88888888u;
             }
             if (first)
-                ((uint16_t *)to.scales)[row * groups + j] = (uint16_t)sb;
+                ((uint16_t *)to.scales)[t.row * groups + j] = (uint16_t)sb;
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float q = a > 0.0f ? x[i] / a : 0.0f;
-                uint32_t code;
-                if constexpr (FMT == Q4_NF4) {
-                    const NF4Bucket e = buckets[(int)((q + 1.0f) * 16.0f)];
-                    code = e.base + (q >= e.thr ? 1u : 0u);
-                } else {
-                    code = 0;
-#pragma unroll
-                    for (int m = 0; m < 7; ++m)
-                        code += fabsf(q) >= kFP4Thr[m] ? 1u : 0u;
-                    code |= q < 0.0f && code ? 8u : 0u;
-                }
-                word |= code << (4 * i);
-            }
             if (first)
-                ((float *)to.scales)[row * groups + j] = a;
+                ((float *)to.scales)[t.row * groups + j] = a;
+            if (IN == Q4_BF16 && !(a >= 0x1p-100f && a <= 0x1p100f) && a != 0.0f) {
+                // the reciprocal of so small or large a bf16 absmax is not a
+                // normal number: divide both by a power of two (values this
+                // takes out of range code as 0 either way)
+                const float k2 = a < 1.0f ? 0x1p100f : 0x1p-100f;
+                a *= k2;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[i] *= k2;
+            }
+            if constexpr (FMT == Q4_NF4)
+                word = a != 0.0f ? nf4_word(x, a, buckets) : 0x77777777u;
+            else
+                word = a != 0.0f ? fp4_word(x, a) : 0u;
         }
     }
-    *(uint32_t *)(to.codes + row * (c.dim >> 1) + 4 * t.chunk) = word;
+    *(uint32_t *)(to.codes + t.row * (c.dim >> 1) + 4 * t.chunk) = word;
 }
 
 template <int FMT, int OUT>
 __global__ __launch_bounds__(kBlock) void kv_read_kernel(KvCache c, KvBatch b, uint16_t *__restrict__ k,
                                                          uint16_t *__restrict__ v, int chunk_shift)
 {
-    __shared__ float tbl[16];
+    __shared__ float2 pairs[f32_absmax(FMT) ? 256 : 1];  // the two levels of a byte
     if constexpr (f32_absmax(FMT)) {
-        if (threadIdx.x < 16)
-            tbl[threadIdx.x] = FMT == Q4_NF4 ? c_nf4[threadIdx.x] : c_fp4[threadIdx.x];
+        const float *tbl = FMT == Q4_NF4 ? c_nf4 : c_fp4;
+        for (int i = threadIdx.x; i < 256; i += blockDim.x)
+            pairs[i] = float2{tbl[i & 15], tbl[i >> 4]};
         __syncthreads();
     }
-    const int seq = blockIdx.y;
+    const int seq = blockIdx.z, half = blockIdx.y & 1, h = blockIdx.y >> 1;
     const KvSeq s = kv_seq(b, seq);
-    const Item t = item_of((int64_t)blockIdx.x * kBlock + threadIdx.x, s.fresh, c.heads, chunk_shift);
+    const Item t = item_of(c, b, s, seq, h, chunk_shift);
     if (!t.in)
         return;
-    const int pos = s.len - s.fresh + t.tok;
-    const int64_t row =
-        pos < 0 ? -1 : kv_row(c, b.table + (int64_t)seq * b.table_width, pos, t.head);
     u32x4 o = {0, 0, 0, 0};
-    if (row >= 0) {
-        const KvHalf &from = t.half ? c.v : c.k;
-        const uint32_t w = *(const uint32_t *)(from.codes + row * (c.dim >> 1) + 4 * t.chunk);
+    if (t.row >= 0) {
+        const KvHalf &from = half ? c.v : c.k;
+        const uint32_t w = *(const uint32_t *)(from.codes + t.row * (c.dim >> 1) + 4 * t.chunk);
         const int groups = c.dim / c.g, j = 8 * t.chunk / c.g;
-        const float sc = kv_scale<FMT>(from, row, groups, j);
-        const float z = kv_zero<FMT>(from, row, groups, j);
+        const float sc = kv_scale<FMT>(from, t.row, groups, j);
+        const float z = kv_zero<FMT>(from, t.row, groups, j);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             // one binary32 product each, then one rounding
-            const float p0 = keep_f32((kv_level<FMT>(w >> (8 * i), tbl) - z) * sc);
-            const float p1 = keep_f32((kv_level<FMT>(w >> (8 * i + 4), tbl) - z) * sc);
-            o[i] = OUT == Q4_F16 ? pack_h2(p0, p1) : pack_bf2(p0, p1);
+            float l0, l1;
+            if constexpr (f32_absmax(FMT)) {
+                const float2 p = pairs[(w >> (8 * i)) & 255];
+                l0 = p.x, l1 = p.y;
+            } else {
+                l0 = (float)((w >> (8 * i)) & 15u) - z;
+                l1 = (float)((w >> (8 * i + 4)) & 15u) - z;
+            }
+            l0 = keep_f32(l0 * sc);
+            l1 = keep_f32(l1 * sc);
+            o[i] = OUT == Q4_F16 ? pack_h2(l0, l1) : pack_bf2(l0, l1);
         }
     }
-    *(u32x4 *)((t.half ? v : k) + ((int64_t)(s.first + t.tok) * c.heads + t.head) * c.dim +
-               8 * t.chunk) = o;
+    __builtin_nontemporal_store(
+        o, (u32x4 *)((half ? v : k) + ((int64_t)(s.first + t.tok) * c.heads + h) * c.dim + 8 * t.chunk));
 }
 
-dim3 item_grid(const KvCache &c, const KvBatch &b)
+struct Launch {
+    dim3 grid;
+    int block, shift;
+};
+Launch launch_of(const KvCache &c, const KvBatch &b)
 {
-    const int64_t items = 2 * (int64_t)b.max_new * c.heads * (c.dim / 8);
-    return dim3((unsigned)((items + kBlock - 1) / kBlock), (unsigned)b.seqs);
+    Launch l;
+    l.shift = __builtin_ctz(c.dim / 8);
+    const int64_t items = (int64_t)b.max_new << l.shift;
+    l.block = items <= 64 ? 64 : kBlock;  // (single tokens leave most of a large workgroup idle)
+    l.grid = dim3((unsigned)((items + l.block - 1) / l.block), (unsigned)(2 * c.heads), (unsigned)b.seqs);
+    return l;
 }
 
 }  // namespace
@@ -217,11 +231,10 @@ hipError_t launch_kv_append(int f, const KvCache &c, const KvBatch &b, int in_t,
 {
     return kv_by_format(f, [&](auto fmt) {
         constexpr int F = decltype(fmt)::value;
-        const int shift = __builtin_ctz(c.dim / 8);
+        const Launch l = launch_of(c, b);
         auto go = [&](auto in, auto lpg) {
-            kv_append_kernel<F, decltype(in)::value, decltype(lpg)::value>
-                <<<item_grid(c, b), kBlock, 0, s>>>(c, b, (const uint16_t *)k, kts, khs,
-                                                    (const uint16_t *)v, vts, vhs, shift);
+            kv_append_kernel<F, decltype(in)::value, decltype(lpg)::value><<<l.grid, l.block, 0, s>>>(
+                c, b, (const uint16_t *)k, kts, khs, (const uint16_t *)v, vts, vhs, l.shift);
             return hipGetLastError();
         };
         auto by_g = [&](auto in) {
@@ -236,11 +249,11 @@ hipError_t launch_kv_read(int f, const KvCache &c, const KvBatch &b, int out_t, 
 {
     return kv_by_format(f, [&](auto fmt) {
         constexpr int F = decltype(fmt)::value;
-        const int shift = __builtin_ctz(c.dim / 8);
+        const Launch l = launch_of(c, b);
         if (out_t == Q4_F16)
-            kv_read_kernel<F, Q4_F16><<<item_grid(c, b), kBlock, 0, s>>>(c, b, (uint16_t *)k, (uint16_t *)v, shift);
+            kv_read_kernel<F, Q4_F16><<<l.grid, l.block, 0, s>>>(c, b, (uint16_t *)k, (uint16_t *)v, l.shift);
         else
-            kv_read_kernel<F, Q4_BF16><<<item_grid(c, b), kBlock, 0, s>>>(c, b, (uint16_t *)k, (uint16_t *)v, shift);
+            kv_read_kernel<F, Q4_BF16><<<l.grid, l.block, 0, s>>>(c, b, (uint16_t *)k, (uint16_t *)v, l.shift);
         return hipGetLastError();
     });
 }

@@ -3,15 +3,18 @@
 //
 // Select: per (sequence, head) the budget - recent largest masses among the
 // tokens before the recent ones.  The masses map to integers of the same
-// order; the smallest one kept, T, is found digit by digit (8 bits a pass,
-// most significant first) by counting the keys that share the digits found so
-// far; the counts are integers, so their atomics' order does not matter.
-// Everything above T stays, and of the tokens equal to T the first ones, as
-// many as are missing.  A pass over the tokens in order with a running count
-// then lists the kept positions.
+// order; the smallest one kept, T, is the largest integer that at least that
+// many keys reach, found two bits at a time by counting the keys at or above
+// three candidates.  Everything above T stays, and of the tokens equal to T
+// the first ones, as many as are missing.  A workgroup's threads hold runs of
+// consecutive tokens, so two running counts over the threads give every kept
+// token's place.  Counting needs no atomics: a wave counts by ballot, and the
+// waves' counts meet in LDS.
 //
-// Move: one lane per 16 bytes of codes copies the kept rows to their new
-// pages; rows never move within their old pages, so no order is needed.
+// Move: rows go to other pages, so no order is needed: a lane copies 16 bytes
+// of a row's codes, and a row's lanes share its scales and zero-points.
+#include <algorithm>
+
 #include "kv_common.hpp"
 
 namespace q4 {
@@ -29,38 +32,37 @@ __device__ __forceinline__ uint32_t mass_key(float f)
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Inclusive sum over the workgroup's threads; every thread gets the total.
-__device__ __forceinline__ int block_scan(int v, int *wsum, int *total)
+// Exclusive sum over the workgroup's threads, in their order.
+__device__ __forceinline__ int block_before(int v, int *wsum)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int sum = v;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(v, d);
-        v += lane >= d ? o : 0;
+        const int o = __shfl_up(sum, d);
+        sum += lane >= d ? o : 0;
     }
-    __syncthreads();
     if (lane == 63)
-        wsum[wave] = v;
+        wsum[wave] = sum;
     __syncthreads();
-    int before = 0, all = 0;
-    for (int i = 0; i < kSel / 64; ++i) {
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < kSel / 64; ++i)
         before += i < wave ? wsum[i] : 0;
-        all += wsum[i];
-    }
-    *total = all;
-    return v + before;
+    return before + sum - v;
 }
 
-__global__ __launch_bounds__(kSel) void kv_select_kernel(KvCache c, KvBatch b,
-                                                         const float *__restrict__ mass, int64_t width,
-                                                         int budget, int recent, int32_t *__restrict__ new_lens,
-                                                         float *__restrict__ new_mass, int64_t new_width,
-                                                         int32_t *__restrict__ kept)
+// One workgroup per (head, sequence).  Thread `tid` has the tokens per * tid ..
+// + per - 1; HELD of them at most stay in registers as keys (HELD >= per), or,
+// with HELD = 0, they are read again on every pass.
+template <int HELD>
+__global__ __launch_bounds__(kSel) void kv_select_kernel(KvCache c, KvBatch b, const float *__restrict__ mass,
+                                                         int64_t width, int budget, int recent,
+                                                         int32_t *__restrict__ new_lens, float *__restrict__ new_mass,
+                                                         int64_t new_width, int32_t *__restrict__ kept, int per)
 {
-    __shared__ int hist[256], wsum[kSel / 64];
-    __shared__ uint32_t sh_key;
-    __shared__ int sh_need;
-    const int h = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x;
+    __shared__ int counts[2][3][kSel / 64], wsum[2][kSel / 64];
+    const int h = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int len = min(max(b.lens[seq], 0), b.max_len);
     const int64_t rowid = (int64_t)seq * c.heads + h;
     const float *m = mass + rowid * width;
@@ -69,69 +71,135 @@ __global__ __launch_bounds__(kSel) void kv_select_kernel(KvCache c, KvBatch b,
     const int n = min(len, budget);
     if (h == 0 && tid == 0)
         new_lens[seq] = n;
+    for (int64_t i = n + tid; i < new_width; i += kSel)
+        mo[i] = 0.0f;
     if (len <= budget) {
-        for (int64_t i = tid; i < new_width; i += kSel)
-            mo[i] = i < n ? m[i] : 0.0f;
+        for (int i = tid; i < n; i += kSel)
+            mo[i] = m[i];
         for (int i = tid; i < budget; i += kSel)
             ko[i] = i < n ? i : -1;
         return;
     }
     const int old = len - recent, want = budget - recent;  // want < old
+    const int t0 = per * tid;
+    // keys of the thread's tokens; 0, which no candidate is, past the old ones
+    uint32_t key[HELD ? HELD : 1];
+    if constexpr (HELD) {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+            key[i] = i < per && t0 + i < old ? mass_key(m[t0 + i]) : 0u;
+    }
     uint32_t T = 0;
-    int need = want;  // tokens equal to T (in the digits found) still to take
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kSel)
-            hist[i] = 0;
-        __syncthreads();
-        const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-        for (int t = tid; t < old; t += kSel) {
-            const uint32_t k = mass_key(m[t]);
-            if ((k & mask) == T)
-                atomicAdd(&hist[(k >> shift) & 255], 1);
+    int above = 0;  // keys above T
+    for (int shift = 30; shift >= 0; shift -= 2) {
+        int cnt[3] = {0, 0, 0};
+        auto count = [&](uint32_t k) {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                cnt[e] += __popcll(__ballot(k >= (T | (uint32_t)(e + 1) << shift)));
+        };
+        if constexpr (HELD) {
+#pragma unroll
+            for (int i = 0; i < HELD; ++i)
+                if (i < per)  // (uniform)
+                    count(key[i]);
+        } else {
+            // (in strides here: no order is needed to count)
+            for (int t = tid; t < per * kSel; t += kSel)
+                count(t < old ? mass_key(m[t]) : 0u);
         }
+        int(&to)[3][kSel / 64] = counts[(shift >> 1) & 1];
+        if (lane < 3)
+            to[lane][wave] = lane == 0 ? cnt[0] : lane == 1 ? cnt[1] : cnt[2];
         __syncthreads();
-        if (tid == 0) {
-            int left = need, d = 255;
-            while (d > 0 && hist[d] < left)
-                left -= hist[d--];
-            sh_key = T | (uint32_t)d << shift;
-            sh_need = left;
-        }
-        __syncthreads();
-        T = sh_key;
-        need = sh_need;
-        __syncthreads();
+        int sum[3] = {0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+#pragma unroll
+            for (int w = 0; w < kSel / 64; ++w)
+                sum[e] += to[e][w];
+        // sum[0] >= sum[1] >= sum[2]: the largest candidate that `want` reach
+        const int d = sum[2] >= want ? 3 : sum[1] >= want ? 2 : sum[0] >= want ? 1 : 0;
+        if (d < 3)
+            above = sum[d];
+        T |= (uint32_t)d << shift;
     }
-    int done = 0, ties = 0;  // kept, and tokens equal to T seen, before this stretch
-    for (int t0 = 0; t0 < len; t0 += kSel) {
-        const int t = t0 + tid;
-        const float f = t < len ? m[t] : 0.0f;
-        const uint32_t k = mass_key(f);
-        const bool tie = t < old && k == T;
-        int total;
-        const int rank = block_scan(tie, wsum, &total);
-        const bool stay = t < len && (t >= old || k > T || (tie && ties + rank <= need));
-        ties += total;
-        const int place = done + block_scan(stay, wsum, &total) - 1;
-        if (stay) {
-            ko[place] = t;
-            mo[place] = f;
+    // `above` was last set where a digit was not 3: the keys past the prefix
+    // T then had, which are those above T (later digits of 3 leave none between)
+    const int need = want - above;  // tokens equal to T to take
+    auto key_at = [&](int i) -> uint32_t {
+        if constexpr (HELD)
+            return key[i];
+        else
+            return t0 + i < old ? mass_key(m[t0 + i]) : 0u;
+    };
+    int ties = 0;
+    auto each = [&](auto &&fn) {
+        if constexpr (HELD) {
+#pragma unroll
+            for (int i = 0; i < HELD; ++i)
+                if (i < per)
+                    fn(i);
+        } else {
+            for (int i = 0; i < per; ++i)
+                fn(i);
         }
-        done += total;
-    }
-    for (int64_t i = n + tid; i < new_width; i += kSel)
-        mo[i] = 0.0f;
+    };
+    each([&](int i) { ties += t0 + i < old && key_at(i) == T; });
+    int tie = block_before(ties, wsum[0]);
+    auto stays = [&](int i) -> bool {  // in order of i, once
+        const int t = t0 + i;
+        if (t >= len)
+            return false;
+        if (t >= old)
+            return true;
+        const uint32_t k = key_at(i);
+        return k > T || (k == T && tie++ < need);
+    };
+    int stay = 0;
+    const int tie0 = tie;
+    each([&](int i) { stay += stays(i); });
+    int place = block_before(stay, wsum[1]);
+    tie = tie0;
+    each([&](int i) {
+        if (stays(i)) {
+            ko[place] = t0 + i;
+            mo[place] = m[t0 + i];
+            ++place;
+        }
+    });
 }
 
-__global__ __launch_bounds__(kMove) void kv_move_kernel(KvCache c, KvBatch b,
-                                                        const int32_t *__restrict__ new_table, int new_tw,
-                                                        int budget, const int32_t *__restrict__ kept,
-                                                        int row_scale_bytes, int row_zero_bytes, int chunk_shift)
+// N bytes, by the widest accesses that their alignment in an array of N-byte
+// rows allows.
+template <int N>
+__device__ __forceinline__ void copy_bytes(uint8_t *to, const uint8_t *from)
 {
+    if constexpr (N % 16 == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i)
+            ((u32x4 *)to)[i] = ((const u32x4 *)from)[i];
+    } else if constexpr (N == 8) {
+        *(u32x2 *)to = *(const u32x2 *)from;
+    } else if constexpr (N == 4) {
+        *(uint32_t *)to = *(const uint32_t *)from;
+    } else if constexpr (N == 2) {
+        *(uint16_t *)to = *(const uint16_t *)from;
+    } else if constexpr (N == 1) {
+        *to = *from;
+    }
+}
+
+// SB: bytes of scales a row, ZB: of zero-points.
+template <int D, int SB, int ZB>
+__global__ __launch_bounds__(kMove) void kv_move_kernel(KvCache c, KvBatch b, const int32_t *__restrict__ new_table,
+                                                        int new_tw, int budget, const int32_t *__restrict__ kept)
+{
+    constexpr int LANES = D / 32;  // 16 bytes of codes a lane
     const int h = blockIdx.y, seq = blockIdx.z;
     const int64_t item = (int64_t)blockIdx.x * kMove + threadIdx.x;
-    const int chunk = (int)(item & ((1 << chunk_shift) - 1));
-    const int64_t place = item >> chunk_shift;
+    const int chunk = (int)(item % LANES);
+    const int64_t place = item / LANES;
     if (place >= budget)
         return;
     const int t = kept[((int64_t)seq * c.heads + h) * budget + place];
@@ -141,21 +209,23 @@ __global__ __launch_bounds__(kMove) void kv_move_kernel(KvCache c, KvBatch b,
     const int64_t dst = kv_row(c, new_table + (int64_t)seq * new_tw, (int)place, h);
     if (src < 0 || dst < 0)
         return;
-    const int row_bytes = c.dim >> 1;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const KvHalf &x = i ? c.v : c.k;
-        *(u32x4 *)(x.codes + dst * row_bytes + 16 * chunk) =
-            *(const u32x4 *)(x.codes + src * row_bytes + 16 * chunk);
-        if (chunk == 0) {
-            const uint16_t *s = (const uint16_t *)((const char *)x.scales + src * row_scale_bytes);
-            uint16_t *d = (uint16_t *)((char *)x.scales + dst * row_scale_bytes);
-            for (int j = 0; j < row_scale_bytes / 2; ++j)
-                d[j] = s[j];
-            for (int j = 0; j < row_zero_bytes; ++j)
-                x.zeros[dst * row_zero_bytes + j] = x.zeros[src * row_zero_bytes + j];
-        }
+    copy_bytes<16>(c.k.codes + dst * (D / 2) + 16 * chunk, c.k.codes + src * (D / 2) + 16 * chunk);
+    copy_bytes<16>(c.v.codes + dst * (D / 2) + 16 * chunk, c.v.codes + src * (D / 2) + 16 * chunk);
+    if (chunk < 2) {
+        const KvHalf &x = chunk ? c.v : c.k;
+        copy_bytes<SB>((uint8_t *)x.scales + dst * SB, (const uint8_t *)x.scales + src * SB);
+        if constexpr (ZB > 0)
+            copy_bytes<ZB>(x.zeros + dst * ZB, x.zeros + src * ZB);
     }
+}
+
+template <int D, int SB, int ZB>
+void move(const KvCache &c, const KvBatch &b, const int32_t *new_table, int new_tw, int budget, const int32_t *kept,
+          hipStream_t s)
+{
+    const int64_t items = (int64_t)budget * (D / 32);
+    kv_move_kernel<D, SB, ZB><<<dim3((unsigned)((items + kMove - 1) / kMove), c.heads, b.seqs), kMove, 0, s>>>(
+        c, b, new_table, new_tw, budget, kept);
 }
 
 }  // namespace
@@ -165,18 +235,45 @@ hipError_t launch_kv_evict(int f, const KvCache &c, const KvBatch &b, const floa
                            int budget, int recent, int32_t *new_lens, float *new_mass,
                            int64_t new_width, int32_t *kept, hipStream_t s)
 {
-    kv_select_kernel<<<dim3(c.heads, b.seqs), kSel, 0, s>>>(c, b, mass, mass_width, budget, recent,
-                                                           new_lens, new_mass, new_width, kept);
+    const dim3 grid(c.heads, b.seqs);
+    const int per = std::max(1, (b.max_len + kSel - 1) / kSel);
+    auto select = [&](auto held) {
+        kv_select_kernel<decltype(held)::value><<<grid, kSel, 0, s>>>(c, b, mass, mass_width, budget, recent, new_lens,
+                                                                     new_mass, new_width, kept, per);
+    };
+    if (per <= 4)
+        select(KvInt<4>{});
+    else if (per <= 16)
+        select(KvInt<16>{});
+    else if (per <= 32)
+        select(KvInt<32>{});
+    else
+        select(KvInt<0>{});
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;
-    const int shift = __builtin_ctz(c.dim / 32);
-    const int64_t items = (int64_t)budget << shift;
-    const int groups = c.dim / c.g;
-    kv_move_kernel<<<dim3((unsigned)((items + kMove - 1) / kMove), c.heads, b.seqs), kMove, 0, s>>>(
-        c, b, new_table, new_table_width, budget, kept, groups * (f32_absmax(f) ? 4 : 2),
-        f == Q4_INT4_ASYM ? kv_zero_bytes(c.dim, c.g) : 0, shift);
-    return hipGetLastError();
+    const int sb = c.dim / c.g * (f32_absmax(f) ? 4 : 2), zb = f == Q4_INT4_ASYM ? kv_zero_bytes(c.dim, c.g) : 0;
+    // every pair of scale and zero-point bytes that a format, width and group give
+    auto go = [&](auto dim) -> hipError_t {
+        constexpr int D = decltype(dim)::value;
+        auto with = [&](auto s2, auto z2) {
+            move<D, decltype(s2)::value, decltype(z2)::value>(c, b, new_table, new_table_width, budget, kept, s);
+            return hipGetLastError();
+        };
+        switch (sb * 8 + zb) {
+        case 2 * 8: return with(KvInt<2>{}, KvInt<0>{});
+        case 2 * 8 + 1: return with(KvInt<2>{}, KvInt<1>{});
+        case 4 * 8: return with(KvInt<4>{}, KvInt<0>{});
+        case 4 * 8 + 1: return with(KvInt<4>{}, KvInt<1>{});
+        case 8 * 8: return with(KvInt<8>{}, KvInt<0>{});
+        case 8 * 8 + 2: return with(KvInt<8>{}, KvInt<2>{});
+        case 16 * 8: return with(KvInt<16>{}, KvInt<0>{});
+        case 16 * 8 + 4: return with(KvInt<16>{}, KvInt<4>{});
+        case 32 * 8: return with(KvInt<32>{}, KvInt<0>{});
+        }
+        return hipErrorInvalidValue;
+    };
+    return c.dim == 64 ? go(KvInt<64>{}) : c.dim == 128 ? go(KvInt<128>{}) : go(KvInt<256>{});
 }
 
 }  // namespace q4
