@@ -112,12 +112,15 @@ __global__ __launch_bounds__(kSel) void kv_select_kernel(KvCache c, KvBatch b, c
         if (lane < 3)
             to[lane][wave] = lane == 0 ? cnt[0] : lane == 1 ? cnt[1] : cnt[2];
         __syncthreads();
-        int sum[3] = {0, 0, 0};
-#pragma unroll
-        for (int e = 0; e < 3; ++e)
-#pragma unroll
-            for (int w = 0; w < kSel / 64; ++w)
-                sum[e] += to[e][w];
+        // 16 waves' counts of a candidate in 16 lanes, summed by rotations
+        static_assert(kSel / 64 == 16, "a row of lanes a candidate");
+        int all = lane < 48 ? to[lane >> 4][lane & 15] : 0;
+        all += __builtin_amdgcn_update_dpp(0, all, 0x128, 0xf, 0xf, true);
+        all += __builtin_amdgcn_update_dpp(0, all, 0x124, 0xf, 0xf, true);
+        all += __builtin_amdgcn_update_dpp(0, all, 0x122, 0xf, 0xf, true);
+        all += __builtin_amdgcn_update_dpp(0, all, 0x121, 0xf, 0xf, true);
+        const int sum[3] = {__builtin_amdgcn_readlane(all, 0), __builtin_amdgcn_readlane(all, 16),
+                            __builtin_amdgcn_readlane(all, 32)};
         // sum[0] >= sum[1] >= sum[2]: the largest candidate that `want` reach
         const int d = sum[2] >= want ? 3 : sum[1] >= want ? 2 : sum[0] >= want ? 1 : 0;
         if (d < 3)
