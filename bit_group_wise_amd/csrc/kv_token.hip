@@ -371,17 +371,19 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
 }
 
 // Most parts that a length is split into: as many as leave every workgroup
-// resident at once (three to each of the 256 compute units; dim 256 takes the
-// registers of one), none shorter than 256 tokens; up to 512 tokens one (a
+// resident at once (three to each of the 256 compute units, two where rows
+// fill more than one column tile; dim 256 takes the registers of one), none
+// shorter than 256 tokens; up to 512 tokens one (a
 // single launch of at most four steps a wave).  A second round of workgroups
 // costs more than it balances: 32 x 4096 tokens in 3, 4, 8 parts 27.3, 31.0,
 // 34.8 us; 512 sequences and heads of 2048 tokens in 1, 2, 4 parts 36.8, 40.1
 // (+ 4.6 to join), 44.3 (+ 4.4) us.
-int most_parts(const KvCache &c, const KvBatch &b)
+int most_parts(const KvCache &c, const KvBatch &b, int group)
 {
     if (b.max_len <= 512)
         return 1;
-    const int64_t wgs = (int64_t)b.seqs * c.heads, room = c.dim == 256 ? 256 : 768;
+    const int64_t wgs = (int64_t)b.seqs * c.heads, cols = (int64_t)b.max_new * group * (c.dim / c.g);
+    const int64_t room = c.dim == 256 ? 256 : cols <= 16 ? 768 : 512;
     return (int)std::max<int64_t>(1, std::min<int64_t>(room / wgs, (b.max_len + 255) / 256));
 }
 
@@ -392,7 +394,7 @@ Split token_split(const KvCache &c, const KvBatch &b, int group, int window)
     Split sp;
     sp.tiles = 1;
     const int64_t range = longest_range(b, window);
-    const int64_t parts = range <= 512 ? 1 : most_parts(c, b);
+    const int64_t parts = range <= 512 ? 1 : most_parts(c, b, group);
     // whole rounds of the four waves' steps
     const int64_t span = std::max<int64_t>((range + parts - 1) / parts, parts > 1 ? 256 : 1);
     sp.span = (int)((span + kWaves * kStep - 1) / (kWaves * kStep) * (kWaves * kStep));

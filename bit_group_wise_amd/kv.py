@@ -19,7 +19,7 @@ from __future__ import annotations
 import ctypes
 
 from . import q4
-from .q4 import _act_code, _check, _stream_ptr, _torch, lib
+from .q4 import _act_code, _check, _torch, lib
 
 _vp, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
 
@@ -33,6 +33,12 @@ class _CacheArgs(ctypes.Structure):
 class _BatchArgs(ctypes.Structure):
     _fields_ = [("table", _vp), ("lens", _vp), ("starts", _vp), ("tokens", _i64),
                 ("table_width", _i32), ("seqs", _i32), ("max_new", _i32), ("max_len", _i32)]
+
+
+def _stream(device) -> int:
+    """The current stream of a device as the raw handle (a decode step makes a
+    few calls of some microseconds each, of which a stream object is one)."""
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
 def _tensor(t, name, dtype, shape=None, device=None):
@@ -134,33 +140,40 @@ class Batch:
         self.table, self.lens, self.starts = table, lens, starts
         self.seqs, self.width, self.tokens, self.max_new = seqs, width, tokens, max_new
         self.max_len, self.device = max_len, dev
-        self._page = None
+        self._cache, self._sizes = None, {}
 
     def _ref(self, cache):
         """The C record for a cache (its page size bounds the lengths)."""
-        if self.device != cache.device:
-            raise ValueError(f"the batch is on {self.device}, the cache on {cache.device}")
-        if self._page != cache.page:
-            self._page = cache.page
-            room = self.width * cache.page
-            self._max_len = room if self.max_len is None else self.max_len
+        if self._cache is not cache:
+            if self.device != cache.device:
+                raise ValueError(f"the batch is on {self.device}, the cache on {cache.device}")
             self._args = _BatchArgs(self.table.data_ptr(), self.lens.data_ptr(),
                                     None if self.starts is None else self.starts.data_ptr(),
-                                    self.tokens, self.width, self.seqs, self.max_new, self._max_len)
+                                    self.tokens, self.width, self.seqs, self.max_new,
+                                    self.width * cache.page if self.max_len is None else self.max_len)
             self._addr = ctypes.addressof(self._args)
+            self._cache, self._sizes = cache, {}
         return self._addr
+
+    def _workspace(self, cache, q_heads, window, mass):
+        """q4_kv_workspace_bytes, asked once for each kind of call."""
+        ref, key = self._ref(cache), (q_heads, window, mass)
+        n = self._sizes.get(key)
+        if n is None:
+            n = self._sizes[key] = lib().q4_kv_workspace_bytes(cache._ref, ref, q_heads, window, int(mass))
+        return n
 
 
 def _rows(t, name, tokens, heads, dim, device):
-    """Checks of a packed [tokens, heads, dim] array (rows contiguous)."""
-    if t.dim() != 3 or t.shape[0] != tokens or t.shape[1] != heads or t.shape[2] != dim:
+    """Checks of a packed [tokens, heads, dim] array (rows contiguous); its
+    strides between tokens and heads (one over an axis of one says nothing)."""
+    if t.shape != (tokens, heads, dim):
         raise ValueError(f"{name} must be [{tokens}, {heads}, {dim}], got {list(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
     st = t.stride()
     if st[2] != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    # (a stride over an axis of one says nothing)
     return st[0] if tokens > 1 else 0, st[1] if heads > 1 else 0
 
 
@@ -174,7 +187,7 @@ def append(cache, batch, k, v):
     if v.dtype != k.dtype:
         raise TypeError("k and v must have one dtype")
     st = lib().q4_kv_append(cache._ref, ref, _act_code(k.dtype), k.data_ptr(), *ks, v.data_ptr(), *vs,
-                            _stream_ptr(k))
+                            _stream(cache.device))
     _check(st, "q4_kv_append")
 
 
@@ -186,19 +199,19 @@ def read(cache, batch, dtype, out=None):
     code = _act_code(dtype)
     shape = (batch.tokens, cache.heads, cache.dim)
     if out is None:
-        out = tuple(torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
+        out = torch.empty((2, *shape), dtype=dtype, device=cache.device).unbind(0)
     else:
         for t in out:
             _tensor(t, "out", dtype, shape, cache.device)
     k, v = out
-    st = lib().q4_kv_read(cache._ref, ref, code, k.data_ptr(), v.data_ptr(), _stream_ptr(k))
+    st = lib().q4_kv_read(cache._ref, ref, code, k.data_ptr(), v.data_ptr(), _stream(cache.device))
     _check(st, "q4_kv_read")
     return k, v
 
 
 def workspace_bytes(cache, batch, q_heads, mass=False, window=0) -> int:
     """Bytes of device workspace that attention needs (q4_kv_workspace_bytes)."""
-    return lib().q4_kv_workspace_bytes(cache._ref, batch._ref(cache), q_heads, window, int(mass))
+    return batch._workspace(cache, q_heads, window, bool(mass))
 
 
 def attention(cache, batch, q, *, scale=None, window=0, mass=None, lse=None, out=None, workspace=None):
@@ -231,8 +244,7 @@ def attention(cache, batch, q, *, scale=None, window=0, mass=None, lse=None, out
     lse_p = None
     if lse is not None:
         lse_p = _tensor(lse, "lse", torch.float32, (batch.tokens, heads), cache.device).data_ptr()
-    L = lib()
-    need = L.q4_kv_workspace_bytes(cache._ref, ref, heads, window, mass is not None)
+    need = batch._workspace(cache, heads, window, mass is not None)
     work_p, have = None, 0
     if workspace is not None:
         _tensor(workspace, "workspace", torch.uint8, None, cache.device)
@@ -240,9 +252,9 @@ def attention(cache, batch, q, *, scale=None, window=0, mass=None, lse=None, out
     elif need:
         workspace = torch.empty((need,), dtype=torch.uint8, device=cache.device)
         work_p, have = workspace.data_ptr(), need
-    st = L.q4_kv_attention(cache._ref, ref, code, q.data_ptr(), *qs, heads,
-                           cache.dim ** -0.5 if scale is None else scale, window, out.data_ptr(), lse_p,
-                           mass_p, width, work_p, have, _stream_ptr(q))
+    st = lib().q4_kv_attention(cache._ref, ref, code, q.data_ptr(), *qs, heads,
+                               cache.dim ** -0.5 if scale is None else scale, window, out.data_ptr(), lse_p,
+                               mass_p, width, work_p, have, _stream(cache.device))
     _check(st, "q4_kv_attention")
     return out
 
@@ -270,6 +282,6 @@ def evict(cache, batch, mass, new_table, budget, recent, *, width=None):
     kept = torch.empty((batch.seqs, cache.heads, budget), dtype=torch.int32, device=cache.device)
     st = lib().q4_kv_evict(cache._ref, ref, mass.data_ptr(), mass.shape[2], new_table.data_ptr(),
                            new_table.shape[1], budget, recent, new_lens.data_ptr(), new_mass.data_ptr(),
-                           width, kept.data_ptr(), _stream_ptr(mass))
+                           width, kept.data_ptr(), _stream(cache.device))
     _check(st, "q4_kv_evict")
     return new_lens, new_mass, kept

@@ -65,6 +65,8 @@ class Q4Error(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libq4.so (built in-tree by bit_group_wise_amd.build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
