@@ -65,6 +65,20 @@ __device__ __forceinline__ int operand_slot(int i, int j)  // (n * 64 + rho)
         return (j + 8 * (i >> 4)) * 64 + (i & 15);
 }
 
+// The largest of a wave's numbers, none negative (as integers they compare
+// alike): rotations within 16 lanes, then the four rows as scalars.
+__device__ __forceinline__ float wave_max(float v)
+{
+    int u = std::bit_cast<int>(v);
+    u = max(u, __builtin_amdgcn_update_dpp(0, u, 0x128, 0xf, 0xf, true));
+    u = max(u, __builtin_amdgcn_update_dpp(0, u, 0x124, 0xf, 0xf, true));
+    u = max(u, __builtin_amdgcn_update_dpp(0, u, 0x122, 0xf, 0xf, true));
+    u = max(u, __builtin_amdgcn_update_dpp(0, u, 0x121, 0xf, 0xf, true));
+    const int a = max(__builtin_amdgcn_readlane(u, 0), __builtin_amdgcn_readlane(u, 16));
+    const int b = max(__builtin_amdgcn_readlane(u, 32), __builtin_amdgcn_readlane(u, 48));
+    return std::bit_cast<float>(max(a, b));
+}
+
 // A staging lane's share of a tile as it is in memory: 32 keys of a token (the
 // first four waves), or a dword of values of four tokens (the others).
 template <int FMT, int D, int GS>
@@ -88,16 +102,24 @@ struct Fetch {
     // The wave of value stagers that holds the tokens of step tb in lanes kg.
     static __device__ __forceinline__ int v_wave(int tb, int kg) { return (8 * tb + 2 * kg) * ND / 64; }
 
-    __device__ __forceinline__ void load(const KvCache &c, Pages &pg, int t0, int end, int wave, int u)
+    int64_t r;    // the row of the tile to load next
+    bool in;      // which is there
+    int t;        // and its token
+
+    // Looks up where the tile from t0 lies.
+    __device__ __forceinline__ void locate(const KvCache &c, Pages &pg, int t0, int end, int wave, int u)
     {
         const int lane = u & 63;
         const int p0 = t0 >> c.page_shift, p1 = (min(t0 + TT, end) - 1) >> c.page_shift;
         if (p0 < pg.first || p1 - pg.first >= 64)
             pg.fetch(p0, lane);
-        const int t = t0 + (wave < 4 ? k_token(u) : 4 * v_quad(u));
+        t = t0 + (wave < 4 ? k_token(u) : 4 * v_quad(u));
         const int id = __shfl(pg.mine, (min(t, end - 1) >> c.page_shift) - pg.first);
-        const bool in = t < end && (unsigned)id < (unsigned)c.pages;
-        const int64_t r = in ? (((int64_t)id * c.heads + pg.h) << c.page_shift) + (t & ((1 << c.page_shift) - 1)) : 0;
+        in = t < end && (unsigned)id < (unsigned)c.pages;
+        r = in ? (((int64_t)id * c.heads + pg.h) << c.page_shift) + (t & ((1 << c.page_shift) - 1)) : 0;
+    }
+    __device__ __forceinline__ void load(const KvCache &c, int end, int wave, int u)
+    {
         if (wave < 4) {
             const int ch = k_chunk(u);
             ok = in;
@@ -163,9 +185,7 @@ __device__ __forceinline__ void stage(Stage<FMT, D, GS> &st, const Fetch<FMT, D,
         s[e] = f.ok >> e & 1 ? f.s[e] : 0.0f;
         top = fmaxf(top, s[e]);
     }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        top = fmaxf(top, __shfl_xor(top, d));
+    top = wave_max(top);
     const int e2 = min(max(__builtin_amdgcn_frexp_expf(fmaxf(top, 0x1p-40f)), -40), 100);
     const float down = __builtin_amdgcn_ldexpf(1.0f, -e2);
     if (lane == 0)
@@ -209,7 +229,7 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
                                                               float2 *__restrict__ part_ml)
 {
     constexpr int NG = D / GS, NT = prompt_nt<D>(), R = prompt_rows<D>(), TT = prompt_tile<D>(), NV = D / 16;
-    constexpr int TB = TT >= 64 ? 2 : 1;  // 32-token steps worked on together
+    constexpr int KT = D == 256 ? 1 : 2;  // 16-token halves of a step whose keys are fetched together
     __shared__ Stage<FMT, D, GS> st[2];
     __shared__ uint32_t pairs[FMT == Q4_NF4 ? 256 : 1];
 
@@ -276,78 +296,92 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
     Pages pg{b.table + (int64_t)seq * b.table_width, c.page_shift, c.heads, h, c.pages, 1 << 30, 0, -1};
     pg.last = (end - 1) >> c.page_shift;
     Fetch<FMT, D, GS> f;
-    if (begin < end)
-        f.load(c, pg, begin, end, wave, tid & 255);
+    if (begin < end) {
+        f.locate(c, pg, begin, end, wave, tid & 255);
+        f.load(c, end, wave, tid & 255);
+    }
     int buf = 0;
     for (int t0 = begin; t0 < end; t0 += TT, buf ^= 1) {
+        if (t0 + TT < end)
+            f.locate(c, pg, t0 + TT, end, wave, tid & 255);
         stage<FMT, D, GS>(st[buf], f, wave, tid & 255, pairs);
         if (t0 + TT < end)
-            f.load(c, pg, t0 + TT, end, wave, tid & 255);
+            f.load(c, end, wave, tid & 255);
         __syncthreads();
         const Stage<FMT, D, GS> &S = st[buf];
 #pragma unroll 1
-        for (int tb = 0; tb < TT / 32; tb += TB) {
+        for (int tb = 0; tb < TT / 32; ++tb) {
             const int t1 = t0 + 32 * tb;
-            if (t1 > any_to || t1 + 32 * TB - 1 < any_from)
+            if (t1 > any_to || t1 + 31 < any_from)
                 continue;
-            uint32_t valid[TB];
-            float e[TB], x[NT][8 * TB];
-            bool whole = t1 + 32 * TB - 1 <= all_to && t1 >= all_from;
+            const uint32_t valid = __builtin_amdgcn_readfirstlane(S.valid[tb]);
+            const float e = S.e[Fetch<FMT, D, GS>::v_wave(tb, kg)];
+            float x[NT][8];
+            // An LDS read takes about as long as ten products: operands are
+            // asked for well before their use, those of a step's keys (KT of
+            // its two halves) together, those of its values before the softmax
+            // (the scheduler would fetch them one by one to save registers).
 #pragma unroll
-            for (int u = 0; u < TB; ++u) {
-                valid[u] = __builtin_amdgcn_readfirstlane(S.valid[tb + u]);
-                e[u] = S.e[Fetch<FMT, D, GS>::v_wave(tb + u, kg)];
-                whole = whole && valid[u] == ~0u;
-            }
+            for (int t2 = 0; t2 < 2; t2 += KT) {
+                u32x4 ka[KT][D / 32];
+                f32x4 ks[KT][NG];
 #pragma unroll
-            for (int tt = 0; tt < 2 * TB; ++tt) {
-                u32x4 ka[D / 32];
-                f32x4 ks[NG];
+                for (int u = 0; u < KT; ++u) {
+                    const int tt = t2 + u;
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k)
-                    ka[k] = S.k[((2 * tb + tt) * (D / 32) + k) * 64 + lane];
+                    for (int k = 0; k < D / 32; ++k)
+                        ka[u][k] = S.k[((2 * tb + tt) * (D / 32) + k) * 64 + lane];
 #pragma unroll
-                for (int j = 0; j < NG; ++j)
-                    ks[j] = *(const f32x4 *)&S.ks[j][32 * tb + 16 * tt + 4 * kg];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-#pragma unroll
-                    for (int j = 0; j < NG; ++j) {
-                        f32x4 a = {0, 0, 0, 0};
-#pragma unroll
-                        for (int k = 0; k < GS / 32; ++k)
-                            a = mfma<Q4_F16>(ka[j * (GS / 32) + k], q[n].op[j * (GS / 32) + k], a);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            x[n][4 * tt + r] = j == 0 ? a[r] * ks[j][r]
-                                                      : __builtin_fmaf(a[r], ks[j][r], x[n][4 * tt + r]);
-                    }
+                    for (int j = 0; j < NG; ++j)
+                        ks[u][j] = *(const f32x4 *)&S.ks[j][32 * tb + 16 * tt + 4 * kg];
                 }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int u = 0; u < KT; ++u)
+#pragma unroll
+                    for (int j = 0; j < NG; ++j)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            f32x4 a = {0, 0, 0, 0};
+#pragma unroll
+                            for (int k = 0; k < GS / 32; ++k)
+                                a = mfma<Q4_F16>(ka[u][j * (GS / 32) + k], q[n].op[j * (GS / 32) + k], a);
+                            float *y = x[n] + 4 * (t2 + u);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                y[r] = j == 0 ? a[r] * ks[u][j][r] : __builtin_fmaf(a[r], ks[u][j][r], y[r]);
+                        }
             }
-            if (__builtin_expect(!whole, 0)) {
-                const int ta = branch_only(t1);
+            u32x4 va[8];
+            auto fetch_values = [&](int v0) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int v = 0; v < 8 && v < NV; ++v)
+                    va[v] = *(const u32x4 *)&S.v[((tb * NV + v0 + v) * 64 + lane) * 2];
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            fetch_values(0);
+            if (__builtin_expect(valid != ~0u || t1 + 31 > all_to || t1 < all_from, 0)) {
+                const int ta = branch_only(t1), k4 = 4 * (int)opaque_word(kg);
+                const uint32_t here = valid >> k4;
 #pragma unroll
-                    for (int k = 0; k < 8 * TB; ++k) {
-                        const int at = 16 * (k >> 2) + 4 * kg + (k & 3);
-                        const bool see = (valid[k >> 3] >> (at & 31) & 1) && ta + at <= pos[n] && ta + at > low[n];
+                for (int k = 0; k < 8; ++k) {
+                    const int at = 16 * (k >> 2) + (k & 3);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const bool see = (here >> at & 1) && ta + k4 + at <= pos[n] && ta + k4 + at > low[n];
                         x[n][k] = see ? x[n][k] : -__builtin_inff();
                     }
+                }
             }
             float reach[NT];
             bool move = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+                float top = x[n][0];
 #pragma unroll
-                for (int u = 0; u < TB; ++u) {
-                    float top = x[n][8 * u];
-#pragma unroll
-                    for (int k = 1; k < 8; ++k)
-                        top = fmaxf(top, x[n][8 * u + k]);
-                    const float to = __builtin_fmaf(top, q[n].factor, e[u]);
-                    reach[n] = u ? fmaxf(reach[n], to) : to;
-                }
+                for (int k = 1; k < 8; ++k)
+                    top = fmaxf(top, x[n][k]);
+                reach[n] = __builtin_fmaf(top, q[n].factor, e);
                 move = move || reach[n] > m[n] + 15.0f;
             }
             if (__builtin_expect(__any(move), 0)) {
@@ -362,31 +396,31 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
                         o[v][n] *= g;
                 }
             }
+            const float inv_e = __builtin_amdgcn_ldexpf(1.0f, -(int)e);
+            u32x4 w[NT];
 #pragma unroll
-            for (int u = 0; u < TB; ++u) {
-                const float inv_e = __builtin_amdgcn_ldexpf(1.0f, -(int)e[u]);
-                u32x4 w[NT];
+            for (int n = 0; n < NT; ++n) {
+                const float off = e - m[n];
+                float sum = 0.0f, p[8];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float off = e[u] - m[n];
-                    float sum = 0.0f, p[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][8 * u + k], q[n].factor, off));
-                        sum += p[k];
-                    }
-                    l[n] = __builtin_fmaf(sum, inv_e, l[n]);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        w[n][k] = pair_h2(p[2 * k], p[2 * k + 1]);
+                for (int k = 0; k < 8; ++k) {
+                    p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][k], q[n].factor, off));
+                    sum += p[k];
                 }
+                l[n] = __builtin_fmaf(sum, inv_e, l[n]);
 #pragma unroll
-                for (int v = 0; v < NV; ++v) {
-                    const u32x4 a = *(const u32x4 *)&S.v[(((tb + u) * NV + v) * 64 + lane) * 2];
+                for (int k = 0; k < 4; ++k)
+                    w[n][k] = pair_h2(p[2 * k], p[2 * k + 1]);
+            }
+#pragma unroll
+            for (int v0 = 0; v0 < NV; v0 += 8) {
+                if (v0)
+                    fetch_values(v0);
+#pragma unroll
+                for (int v = 0; v < 8 && v0 + v < NV; ++v)
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        o[v][n] = mfma<Q4_F16>(a, w[n], o[v][n]);
-                }
+                        o[v0 + v][n] = mfma<Q4_F16>(va[v], w[n], o[v0 + v][n]);
             }
         }
     }
