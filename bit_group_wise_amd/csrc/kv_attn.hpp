@@ -145,6 +145,19 @@ __device__ __forceinline__ float group_max(float v)
     return v;
 }
 
+// A scale as it is stored, and its value.  (A load's result is left alone until
+// it is used: whatever touches it earlier waits for it.)
+template <int FMT>
+__device__ __forceinline__ uint32_t scale_bits(const KvHalf &x, int64_t i)
+{
+    return f32_absmax(FMT) ? ((const uint32_t *)x.scales)[i] : ((const uint16_t *)x.scales)[i];
+}
+template <int FMT>
+__device__ __forceinline__ float scale_of(uint32_t s)
+{
+    return f32_absmax(FMT) ? std::bit_cast<float>(s) : h2f(s);
+}
+
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t (&to)[N], const void *from)
 {

@@ -84,10 +84,8 @@ __device__ __forceinline__ float wave_max(float v)
 template <int FMT, int D, int GS>
 struct Fetch {
     static constexpr int NG = D / GS, ZB = (NG + 1) / 2, TT = prompt_tile<D>(), ND = D / 8;
-    uint32_t w[4];
-    float s[4];   // keys: s[0], the scale of the token's group number `chunk`
-    uint32_t z[4];
-    uint32_t ok;  // keys: the token is there; values: bit e, token e is
+    uint32_t w[4], s[4], z[4];  // as stored
+    uint32_t ok;                // keys: the token is there; values: bit e, token e is
 
     // Keys: token u % TT, 32 values u / TT.  Values: dword u % ND of the four
     // tokens of quad u / ND, whose place tt in a 32-token step moves fastest.
@@ -110,7 +108,7 @@ struct Fetch {
     __device__ __forceinline__ void locate(const KvCache &c, Pages &pg, int t0, int end, int wave, int u)
     {
         const int lane = u & 63;
-        const int p0 = t0 >> c.page_shift, p1 = (min(t0 + TT, end) - 1) >> c.page_shift;
+        const int p0 = min(t0, end - 1) >> c.page_shift, p1 = (min(t0 + TT, end) - 1) >> c.page_shift;
         if (p0 < pg.first || p1 - pg.first >= 64)
             pg.fetch(p0, lane);
         t = t0 + (wave < 4 ? k_token(u) : 4 * v_quad(u));
@@ -118,31 +116,29 @@ struct Fetch {
         in = t < end && (unsigned)id < (unsigned)c.pages;
         r = in ? (((int64_t)id * c.heads + pg.h) << c.page_shift) + (t & ((1 << c.page_shift) - 1)) : 0;
     }
+    // One straight run of loads for both roles and every tile (past the end from
+    // row 0): where branches met after their loads, the merged registers would
+    // be copied, and so waited for, at once.
     __device__ __forceinline__ void load(const KvCache &c, int end, int wave, int u)
     {
-        if (wave < 4) {
-            const int ch = k_chunk(u);
-            ok = in;
-            const u32x4 v = *(const u32x4 *)(c.k.codes + r * (D / 2) + 16 * ch);
-            w[0] = v[0], w[1] = v[1], w[2] = v[2], w[3] = v[3];
-            if (ch < NG)
-                s[0] = kv_scale<FMT>(c.k, r, NG, ch);
-            if constexpr (FMT == Q4_INT4_ASYM)
-                z[0] = c.k.zeros[r * ZB + (32 * ch / GS >> 1)];
-        } else {
-            // (the four tokens share a page; those past the end are not used)
-            const int i = v_dword(u), j = 8 * i / GS;
-            const uint8_t *vc = c.v.codes + r * (D / 2) + 4 * i;
-            ok = 0;
+        const bool keys = wave < 4;
+        // keys: four dwords of a row, one scale; values: a dword and its scale
+        // of four rows (which share a page; those past the end are not used)
+        const int first = keys ? 4 * k_chunk(u) : v_dword(u);
+        const int j = keys ? min(k_chunk(u), NG - 1) : 8 * first / GS;
+        const int step = keys ? 4 : D / 2, rows = keys ? 0 : 1;
+        const KvHalf &x = keys ? c.k : c.v;
+        const uint8_t *p = x.codes + r * (D / 2) + 4 * first;
+        const int zj = 8 * first / GS;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                w[e] = *(const uint32_t *)(vc + e * (D / 2));
-                s[e] = kv_scale<FMT>(c.v, r + e, NG, j);
-                if constexpr (FMT == Q4_INT4_ASYM)
-                    z[e] = c.v.zeros[(r + e) * ZB + (j >> 1)];
-                ok |= (uint32_t)(in && t + e < end) << e;
-            }
+        for (int e = 0; e < 4; ++e) {
+            w[e] = *(const uint32_t *)(p + e * step);
+            s[e] = scale_bits<FMT>(x, (r + e * rows) * NG + j);
+            if constexpr (FMT == Q4_INT4_ASYM)
+                z[e] = x.zeros[(r + e * rows) * ZB + (zj >> 1)];
         }
+        const int left = in ? min(end - t, 4) : 0;
+        ok = (1u << left) - 1;
     }
 };
 
@@ -166,8 +162,8 @@ __device__ __forceinline__ void stage(Stage<FMT, D, GS> &st, const Fetch<FMT, D,
     if (wave < 4) {
         const int t = F::k_token(u), ch = F::k_chunk(u);
         if (ch < F::NG)
-            st.ks[ch][t] = f.ok ? f.s[0] : 0.0f;
-        const uint64_t in = __ballot(f.ok);
+            st.ks[ch][t] = f.ok & 1 ? scale_of<FMT>(f.s[0]) : 0.0f;
+        const uint64_t in = __ballot(f.ok & 1);
         const int word = 2 * wave + lane;
         if (lane < 2 && word < TT / 32)
             st.valid[word] = (uint32_t)(in >> (32 * lane));
@@ -182,7 +178,7 @@ __device__ __forceinline__ void stage(Stage<FMT, D, GS> &st, const Fetch<FMT, D,
     float s[4], top = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        s[e] = f.ok >> e & 1 ? f.s[e] : 0.0f;
+        s[e] = f.ok >> e & 1 ? scale_of<FMT>(f.s[e]) : 0.0f;
         top = fmaxf(top, s[e]);
     }
     top = wave_max(top);
@@ -302,11 +298,9 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
     }
     int buf = 0;
     for (int t0 = begin; t0 < end; t0 += TT, buf ^= 1) {
-        if (t0 + TT < end)
-            f.locate(c, pg, t0 + TT, end, wave, tid & 255);
+        f.locate(c, pg, t0 + TT, end, wave, tid & 255);
         stage<FMT, D, GS>(st[buf], f, wave, tid & 255, pairs);
-        if (t0 + TT < end)
-            f.load(c, end, wave, tid & 255);
+        f.load(c, end, wave, tid & 255);
         __syncthreads();
         const Stage<FMT, D, GS> &S = st[buf];
 #pragma unroll 1
