@@ -225,6 +225,7 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
                                                               float2 *__restrict__ part_ml)
 {
     constexpr int NG = D / GS, NT = prompt_nt<D>(), R = prompt_rows<D>(), TT = prompt_tile<D>(), NV = D / 16;
+    constexpr int TB = TT >= 64 ? 2 : 1;   // 32-token steps worked on together
     constexpr int KT = D == 256 ? 1 : 2;  // 16-token halves of a step whose keys are fetched together
     __shared__ Stage<FMT, D, GS> st[2];
     __shared__ uint32_t pairs[FMT == Q4_NF4 ? 256 : 1];
@@ -304,66 +305,75 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
         __syncthreads();
         const Stage<FMT, D, GS> &S = st[buf];
 #pragma unroll 1
-        for (int tb = 0; tb < TT / 32; ++tb) {
+        for (int tb = 0; tb < TT / 32; tb += TB) {
             const int t1 = t0 + 32 * tb;
-            if (t1 > any_to || t1 + 31 < any_from)
+            if (t1 > any_to || t1 + 32 * TB - 1 < any_from)
                 continue;
-            const uint32_t valid = __builtin_amdgcn_readfirstlane(S.valid[tb]);
-            const float e = S.e[Fetch<FMT, D, GS>::v_wave(tb, kg)];
-            float x[NT][8];
+            uint32_t valid[TB];
+            float e[TB], x[TB][NT][8];
+            bool whole = t1 + 32 * TB - 1 <= all_to && t1 >= all_from;
+#pragma unroll
+            for (int b2 = 0; b2 < TB; ++b2) {
+                valid[b2] = __builtin_amdgcn_readfirstlane(S.valid[tb + b2]);
+                e[b2] = S.e[Fetch<FMT, D, GS>::v_wave(tb + b2, kg)];
+                whole = whole && valid[b2] == ~0u;
+            }
             // An LDS read takes about as long as ten products: operands are
             // asked for well before their use, those of a step's keys (KT of
             // its two halves) together, those of its values before the softmax
             // (the scheduler would fetch them one by one to save registers).
 #pragma unroll
-            for (int t2 = 0; t2 < 2; t2 += KT) {
-                u32x4 ka[KT][D / 32];
-                f32x4 ks[KT][NG];
+            for (int b2 = 0; b2 < TB; ++b2)
 #pragma unroll
-                for (int u = 0; u < KT; ++u) {
-                    const int tt = t2 + u;
+                for (int t2 = 0; t2 < 2; t2 += KT) {
+                    u32x4 ka[KT][D / 32];
+                    f32x4 ks[KT][NG];
 #pragma unroll
-                    for (int k = 0; k < D / 32; ++k)
-                        ka[u][k] = S.k[((2 * tb + tt) * (D / 32) + k) * 64 + lane];
+                    for (int u = 0; u < KT; ++u) {
+                        const int tt = t2 + u;
 #pragma unroll
-                    for (int j = 0; j < NG; ++j)
-                        ks[u][j] = *(const f32x4 *)&S.ks[j][32 * tb + 16 * tt + 4 * kg];
+                        for (int k = 0; k < D / 32; ++k)
+                            ka[u][k] = S.k[((2 * (tb + b2) + tt) * (D / 32) + k) * 64 + lane];
+#pragma unroll
+                        for (int j = 0; j < NG; ++j)
+                            ks[u][j] = *(const f32x4 *)&S.ks[j][32 * (tb + b2) + 16 * tt + 4 * kg];
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int u = 0; u < KT; ++u)
+#pragma unroll
+                        for (int j = 0; j < NG; ++j)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                f32x4 a = {0, 0, 0, 0};
+#pragma unroll
+                                for (int k = 0; k < GS / 32; ++k)
+                                    a = mfma<Q4_F16>(ka[u][j * (GS / 32) + k], q[n].op[j * (GS / 32) + k], a);
+                                float *y = x[b2][n] + 4 * (t2 + u);
+#pragma unroll
+                                for (int r = 0; r < 4; ++r)
+                                    y[r] = j == 0 ? a[r] * ks[u][j][r] : __builtin_fmaf(a[r], ks[u][j][r], y[r]);
+                            }
                 }
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int u = 0; u < KT; ++u)
-#pragma unroll
-                    for (int j = 0; j < NG; ++j)
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            f32x4 a = {0, 0, 0, 0};
-#pragma unroll
-                            for (int k = 0; k < GS / 32; ++k)
-                                a = mfma<Q4_F16>(ka[u][j * (GS / 32) + k], q[n].op[j * (GS / 32) + k], a);
-                            float *y = x[n] + 4 * (t2 + u);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                y[r] = j == 0 ? a[r] * ks[u][j][r] : __builtin_fmaf(a[r], ks[u][j][r], y[r]);
-                        }
-            }
             u32x4 va[8];
-            auto fetch_values = [&](int v0) {
+            auto fetch_values = [&](int b2, int v0) {
 #pragma unroll
                 for (int v = 0; v < 8 && v < NV; ++v)
-                    va[v] = *(const u32x4 *)&S.v[((tb * NV + v0 + v) * 64 + lane) * 2];
+                    va[v] = *(const u32x4 *)&S.v[(((tb + b2) * NV + v0 + v) * 64 + lane) * 2];
                 __builtin_amdgcn_sched_barrier(0);
             };
-            fetch_values(0);
-            if (__builtin_expect(valid != ~0u || t1 + 31 > all_to || t1 < all_from, 0)) {
+            fetch_values(0, 0);
+            if (__builtin_expect(!whole, 0)) {
                 const int ta = branch_only(t1), k4 = 4 * (int)opaque_word(kg);
-                const uint32_t here = valid >> k4;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int at = 16 * (k >> 2) + (k & 3);
+                for (int b2 = 0; b2 < TB; ++b2) {
+                    const uint32_t here = valid[b2] >> k4;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const bool see = (here >> at & 1) && ta + k4 + at <= pos[n] && ta + k4 + at > low[n];
-                        x[n][k] = see ? x[n][k] : -__builtin_inff();
+                    for (int k = 0; k < 8; ++k) {
+                        const int at = 16 * (k >> 2) + (k & 3), t = ta + 32 * b2 + k4 + at;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            x[b2][n][k] = (here >> at & 1) && t <= pos[n] && t > low[n] ? x[b2][n][k] : -__builtin_inff();
                     }
                 }
             }
@@ -371,11 +381,15 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
             bool move = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float top = x[n][0];
 #pragma unroll
-                for (int k = 1; k < 8; ++k)
-                    top = fmaxf(top, x[n][k]);
-                reach[n] = __builtin_fmaf(top, q[n].factor, e);
+                for (int b2 = 0; b2 < TB; ++b2) {
+                    float top = x[b2][n][0];
+#pragma unroll
+                    for (int k = 1; k < 8; ++k)
+                        top = fmaxf(top, x[b2][n][k]);
+                    const float to = __builtin_fmaf(top, q[n].factor, e[b2]);
+                    reach[n] = b2 ? fmaxf(reach[n], to) : to;
+                }
                 move = move || reach[n] > m[n] + 15.0f;
             }
             if (__builtin_expect(__any(move), 0)) {
@@ -390,31 +404,38 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
                         o[v][n] *= g;
                 }
             }
-            const float inv_e = __builtin_amdgcn_ldexpf(1.0f, -(int)e);
-            u32x4 w[NT];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float off = e - m[n];
-                float sum = 0.0f, p[8];
+            for (int b2 = 0; b2 < TB; ++b2) {
+                const float inv_e = __builtin_amdgcn_ldexpf(1.0f, -(int)e[b2]);
+                u32x4 w[NT];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[n][k], q[n].factor, off));
-                    sum += p[k];
+                for (int n = 0; n < NT; ++n) {
+                    const float off = e[b2] - m[n];
+                    float sum = 0.0f, p[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b2][n][k], q[n].factor, off));
+                        sum += p[k];
+                    }
+                    l[n] = __builtin_fmaf(sum, inv_e, l[n]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        w[n][k] = pair_h2(p[2 * k], p[2 * k + 1]);
                 }
-                l[n] = __builtin_fmaf(sum, inv_e, l[n]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    w[n][k] = pair_h2(p[2 * k], p[2 * k + 1]);
-            }
+                for (int v0 = 0; v0 < NV; v0 += 8) {
+                    if (v0)
+                        fetch_values(b2, v0);
 #pragma unroll
-            for (int v0 = 0; v0 < NV; v0 += 8) {
-                if (v0)
-                    fetch_values(v0);
+                    for (int v = 0; v < 8 && v0 + v < NV; ++v)
 #pragma unroll
-                for (int v = 0; v < 8 && v0 + v < NV; ++v)
+                        for (int n = 0; n < NT; ++n)
+                            o[v0 + v][n] = mfma<Q4_F16>(va[v], w[n], o[v0 + v][n]);
+                }
+                if (b2 + 1 < TB)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        o[v0 + v][n] = mfma<Q4_F16>(va[v], w[n], o[v0 + v][n]);
+                    for (int v = 0; v < 8 && v < NV; ++v)
+                        va[v] = *(const u32x4 *)&S.v[(((tb + b2 + 1) * NV + v) * 64 + lane) * 2];
             }
         }
     }
