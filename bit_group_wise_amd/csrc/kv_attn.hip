@@ -106,7 +106,10 @@ size_t kv_attention_workspace(const KvCache &c, const KvBatch &b, int q_heads, i
     if (sp.parts > 1)
         n = round256(rows * sp.parts * sizeof(float2)) + rows * sp.parts * c.dim * 4;
     // (the parts are done with when the mass pass starts)
-    return mass ? round256(rows * 4) + std::max(n, kv_mass_workspace(c, b, q_heads / c.heads)) : n;
+    const int group = q_heads / c.heads;
+    return mass ? round256(rows * 4) + round256(kv_kept_bytes(c, b, group, window)) +
+                      std::max(n, kv_mass_workspace(c, b, group))
+                : n;
 }
 
 hipError_t launch_kv_attention(int f, const KvCache &c, const KvBatch &b, int act_t, const void *q,
@@ -119,10 +122,16 @@ hipError_t launch_kv_attention(int f, const KvCache &c, const KvBatch &b, int ac
     const size_t n = (size_t)b.tokens * q_heads;
     char *w = (char *)workspace;
     Rows rows{(const uint16_t *)q, qts, qhs, q_heads, group, act_t, window, scale * kLog2e,
-              (uint16_t *)out, lse, nullptr};
+              (uint16_t *)out, lse, nullptr, nullptr, 0, 0};
     if (mass) {
         rows.stat = (float *)w;
         w += round256(n * 4);
+        if (const size_t kept = kv_kept_bytes(c, b, group, window)) {
+            rows.kept = (float *)w;
+            rows.kept_range = longest_range(b, window);
+            rows.kept_rows = b.max_new * group;
+            w += round256(kept);
+        }
     }
     float2 *part_ml = (float2 *)w;
     float *part = (float *)(w + round256(n * sp.parts * sizeof(float2)));

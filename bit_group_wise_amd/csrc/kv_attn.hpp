@@ -29,6 +29,10 @@ struct Rows {
     uint16_t *out;
     float *lse;    // natural log, or null
     float *stat;   // base-2 log of the denominator for the mass pass, or null
+    float *kept;   // the scores themselves for it, or null: [seqs][heads]
+                   // [kept_range tokens from range_begin][kept_rows]
+    int64_t kept_range;
+    int kept_rows;
 };
 
 // How a launch divides a sequence's range of cached tokens and its rows.
@@ -426,6 +430,8 @@ hipError_t launch_kv_token(int f, const KvCache &c, const KvBatch &b, const Rows
 hipError_t launch_kv_prompt(int f, const KvCache &c, const KvBatch &b, const Rows &rows, const Split &sp,
                             float *part, float2 *part_ml, hipStream_t s);
 size_t kv_mass_workspace(const KvCache &c, const KvBatch &b, int group);
+// Bytes of scores that few rows keep for the mass pass; 0: it forms them anew.
+size_t kv_kept_bytes(const KvCache &c, const KvBatch &b, int group, int window);
 hipError_t launch_kv_mass(int f, const KvCache &c, const KvBatch &b, const Rows &rows, float *mass,
                           int64_t mass_width, void *workspace, hipStream_t s);
 

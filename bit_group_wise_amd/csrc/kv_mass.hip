@@ -8,7 +8,9 @@
 // its tokens over the rows it meets; the 16 columns meet once at the end, in a
 // fixed order.
 //
-//  * Few rows (as kv_token.hip takes): the rows stay in registers and a wave walks
+//  * Up to 8 rows: the attention kept the scores, in binary32; this pass only
+//    reads them (kv_mass_kept_kernel).
+//  * Few rows (as kv_token.hip takes), else: the rows stay in registers and a wave walks
 //    over 64-token blocks of a span.  Bound as kv_token.hip.
 //  * Many rows: 64 tokens' keys stay in registers, unpacked once, and the rows
 //    pass by as operands that a first launch laid out (kv_rows_kernel), with
@@ -23,6 +25,7 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kBlock = 64 * kWaves;
 constexpr int kBlk = 64;  // tokens of a wave at a time
+constexpr int kMaxKept = 8;  // rows whose scores are kept
 
 // 64 tokens' keys as operands, with the scales of the lane's rows.
 template <int FMT, int D, int GS>
@@ -210,6 +213,53 @@ __global__ __launch_bounds__(kBlock) void kv_mass_few_kernel(KvCache c, KvBatch 
     }
 }
 
+constexpr int kKeptTokens = 4 * kBlock;
+
+// The same from the scores that the attention kept: four tokens a thread.
+// W: rows read at a time (4 where their number is a multiple of four).
+template <int W>
+__global__ __launch_bounds__(kBlock) void kv_mass_kept_kernel(KvBatch b, Rows rows, int heads, float *__restrict__ mass,
+                                                              int64_t mass_width)
+{
+    __shared__ float st[kMaxKept];
+    const int seq = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
+    const KvSeq s = kv_seq(b, seq);
+    const int nrows = s.fresh * rows.group, begin = range_begin(s, rows.window);
+    const int n = s.len - begin, t0 = (int)blockIdx.x * kKeptTokens + tid;
+    if ((int)blockIdx.x * kKeptTokens >= n || nrows == 0)
+        return;
+    if (tid < nrows) {
+        const int tok = tid / rows.group;
+        const float v = rows.stat[(int64_t)(s.first + tok) * rows.q_heads + h * rows.group + tid - tok * rows.group];
+        st[tid] = v == -__builtin_inff() ? __builtin_inff() : v;  // rows that see nothing weigh nothing
+    }
+    __syncthreads();
+    const float *x = rows.kept + ((int64_t)seq * heads + h) * rows.kept_range * rows.kept_rows;
+    float *m = mass + ((int64_t)seq * heads + h) * mass_width + begin;
+    float sum[4] = {0, 0, 0, 0}, old[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int t = min(t0 + k * kBlock, n - 1);  // (past the end: read and not used)
+        old[k] = m[t];
+        for (int r = 0; r < nrows; r += W) {
+            float v[W];
+            if constexpr (W == 4) {
+                const f32x4 y = *(const f32x4 *)(x + (int64_t)t * rows.kept_rows + r);
+                v[0] = y[0], v[1] = y[1], v[2] = y[2], v[3] = y[3];
+            } else {
+                v[0] = x[(int64_t)t * rows.kept_rows + r];
+            }
+#pragma unroll
+            for (int e = 0; e < W; ++e)  // (rows past a sequence's own are not)
+                sum[k] += r + e < nrows ? __builtin_amdgcn_exp2f(v[e] - st[r + e]) : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (t0 + k * kBlock < n)
+            m[t0 + k * kBlock] = old[k] + sum[k];
+}
+
 // Rows as operands: tile t of head h holds 16 rows of a sequence, the
 // sequence's first tile being floor(first * group / 16) + seq (so sequences
 // never share one).
@@ -339,6 +389,16 @@ size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
 
+// Scores of up to 8 rows a head are kept between the passes where they take at
+// most 1 GiB: 4 bytes a row and token, written and read once, against half a
+// cached row to read and unpack again.
+size_t kv_kept_bytes(const KvCache &c, const KvBatch &b, int group, int window)
+{
+    const int64_t rows = (int64_t)b.max_new * group;
+    const double n = 4.0 * rows * b.seqs * c.heads * longest_range(b, window);
+    return rows <= kMaxKept && rows <= few_rows(c) && n <= 0x1p30 ? (size_t)n : 0;
+}
+
 size_t kv_mass_workspace(const KvCache &c, const KvBatch &b, int group)
 {
     if (is_few(c, b, group))
@@ -353,6 +413,14 @@ hipError_t launch_kv_mass(int f, const KvCache &c, const KvBatch &b, const Rows 
     const int64_t range = longest_range(b, rows.window);
     if (range == 0)
         return hipSuccess;
+    if (rows.kept) {
+        const dim3 grid((unsigned)((range + kKeptTokens - 1) / kKeptTokens), c.heads, b.seqs);
+        if (rows.kept_rows % 4 == 0)
+            kv_mass_kept_kernel<4><<<grid, kBlock, 0, s>>>(b, rows, c.heads, mass, mass_width);
+        else
+            kv_mass_kept_kernel<1><<<grid, kBlock, 0, s>>>(b, rows, c.heads, mass, mass_width);
+        return hipGetLastError();
+    }
     return kv_by_shape(f, c.dim, c.g, [&](auto fmt, auto dim, auto gs) {
         constexpr int F = decltype(fmt)::value, D = decltype(dim)::value, GS = decltype(gs)::value;
         const int per = kWaves * kBlk;

@@ -98,7 +98,7 @@ __device__ __forceinline__ uint32_t zero_pair(const uint32_t *z, int r, int h, i
     return (a & 15u) | (b & 15u) << 16;
 }
 
-template <int FMT, int D, int GS, int NT>
+template <int FMT, int D, int GS, int NT, bool KEEP>
 __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_token_kernel(
     KvCache c, KvBatch b, Rows rows, Split sp, float *__restrict__ part, float2 *__restrict__ part_ml)
 {
@@ -128,7 +128,8 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
     const int nrows = s.fresh * rows.group;
     if (nrows == 0)
         return;
-    const int begin = range_begin(s, rows.window) + pt * sp.span;
+    const int begin0 = range_begin(s, rows.window), begin = begin0 + pt * sp.span;
+    float *kept = KEEP ? rows.kept + ((int64_t)seq * c.heads + h) * rows.kept_range * rows.kept_rows : nullptr;
     const int end = min(s.len, begin + sp.span);
     if (begin >= s.len && pt > 0)
         return;
@@ -211,6 +212,23 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
                         x[u][n][r] = r < have && at <= q.pos[n] && at > q.low[n] ? x[u][n][r] : -__builtin_inff();
+                }
+            }
+        }
+        if constexpr (KEEP) {
+            // the scores, in powers of two, for the mass pass; a row's first
+            // column writes them
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int row = ColQueries<FMT, D, GS, NT>::row(n, lane);
+                if (i % NG == 0 && row < nrows) {
+                    float *to = kept + (int64_t)(t0 - begin0 + 4 * kg) * rows.kept_rows + row;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (t0 + 16 * u + 4 * kg + r < end)
+                                to[(16 * u + r) * rows.kept_rows] = x[u][n][r] * q.factor[n];
                 }
             }
         }
@@ -409,12 +427,19 @@ hipError_t launch_kv_token(int f, const KvCache &c, const KvBatch &b, const Rows
         constexpr int F = decltype(fmt)::value, D = decltype(dim)::value, GS = decltype(gs)::value;
         const dim3 grid(sp.parts, c.heads, b.seqs);
         const int64_t cols = (int64_t)b.max_new * rows.group * (D / GS);
+        auto go = [&](auto nt) {
+            constexpr int NT = decltype(nt)::value;
+            if (rows.kept)
+                kv_token_kernel<F, D, GS, NT, true><<<grid, kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+            else
+                kv_token_kernel<F, D, GS, NT, false><<<grid, kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+        };
         if (cols <= 16)
-            kv_token_kernel<F, D, GS, 1><<<grid, kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+            go(KvInt<1>{});
         else if (cols <= 32)
-            kv_token_kernel<F, D, GS, 2><<<grid, kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+            go(KvInt<2>{});
         else if constexpr (D == 64)
-            kv_token_kernel<F, D, GS, 4><<<grid, kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+            go(KvInt<4>{});
         return hipGetLastError();
     });
 }
