@@ -11,7 +11,7 @@
 //  * Values lie there as fp16(level * s_t 2^-E), one rounding of the cached
 //    value, where 2^E bounds the scales of the tokens that one wave stages: E
 //    is added to those tokens' scores, which puts it into the weights, and
-//    taken off the row sums again.  So neither weights (at most 2^15) nor
+//    taken off the row sums again.  So neither weights (at most 2^15.5) nor
 //    values (at most 15, 1 for tables) leave fp16, whatever the cache's
 //    magnitude.
 //  * LDS holds operands as the lanes read them, 16 bytes a lane in a row, in
@@ -390,12 +390,12 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
                     const float to = __builtin_fmaf(top, q[n].factor, e[b2]);
                     reach[n] = b2 ? fmaxf(reach[n], to) : to;
                 }
-                move = move || reach[n] > m[n] + 15.0f;
+                move = move || reach[n] > m[n] + 15.5f;
             }
             if (__builtin_expect(__any(move), 0)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float to = fmaxf(m[n], quad_max(reach[n]) - 6.0f);
+                    const float to = fmaxf(m[n], quad_max(reach[n]) - 13.5f);
                     const float g = __builtin_amdgcn_exp2f(m[n] - to);
                     m[n] = to;
                     l[n] *= g;

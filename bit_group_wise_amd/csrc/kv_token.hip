@@ -22,8 +22,11 @@
 //    weights with the zero-points as rows, taken off at the end.
 //  * Reference.  w_t s_tj must stay below 65504 and the largest should be well
 //    inside fp16's normal range whatever the values' size, so m tracks
-//    x_t + log2(s_t), not x_t: it moves only when a weight would pass 2^15 and
-//    is then set to put the largest at 2^6.
+//    x_t + log2(s_t), not x_t: it moves only when a weight would pass 2^15.5
+//    and is then set to put the largest at 2^13.5, so that a weight has fp16's
+//    full 11 bits down to 2^-27 of the largest (in long caches most of the sum
+//    is in weights far below it; with the largest at 2^6 the 131071-token case
+//    was 2.5 times as far from binary64).
 //
 // Bound: HBM traffic of the packed rows in the limit; in practice the rate at
 // which lanes receive their words (texture path) and vector-ALU issue.
@@ -244,12 +247,12 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
             for (int r = 1; r < 4; ++r)
                 top = fmaxf(top, fmaxf(x[0][n][r], x[1][n][r]));
             reach[n] = __builtin_fmaf(top, q.factor[n], big);
-            move = move || reach[n] > m[n] + 15.0f;
+            move = move || reach[n] > m[n] + 15.5f;
         }
         if (__builtin_expect(__any(move), 0)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const float to = fmaxf(m[n], quad_max(reach[n]) - 6.0f);
+                const float to = fmaxf(m[n], quad_max(reach[n]) - 13.5f);
                 const float f = __builtin_amdgcn_exp2f(m[n] - to);
                 m[n] = to;
                 l[n] *= f;
