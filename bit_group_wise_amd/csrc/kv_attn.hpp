@@ -40,6 +40,7 @@ struct Split {
     int span;   // tokens a part
     int parts;
     int tiles;  // row tiles a head
+    int rows;   // rows a tile (prompts)
 };
 
 // The page numbers of a range, 64 at a time in one register across the lanes.

@@ -21,6 +21,7 @@ namespace q4 {
 namespace {
 
 constexpr int kSel = 1024;
+constexpr int kSelFew = 256;
 constexpr int kMove = 256;
 
 // Masses as integers of the same order; NaN below everything.
@@ -33,6 +34,7 @@ __device__ __forceinline__ uint32_t mass_key(float f)
 }
 
 // Exclusive sum over the workgroup's threads, in their order.
+template <int WAVES>
 __device__ __forceinline__ int block_before(int v, int *wsum)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -47,7 +49,7 @@ __device__ __forceinline__ int block_before(int v, int *wsum)
     __syncthreads();
     int before = 0;
 #pragma unroll
-    for (int i = 0; i < kSel / 64; ++i)
+    for (int i = 0; i < WAVES; ++i)
         before += i < wave ? wsum[i] : 0;
     return before + sum - v;
 }
@@ -55,13 +57,14 @@ __device__ __forceinline__ int block_before(int v, int *wsum)
 // One workgroup per (head, sequence).  Thread `tid` has the tokens per * tid ..
 // + per - 1; HELD of them at most stay in registers as keys (HELD >= per), or,
 // with HELD = 0, they are read again on every pass.
-template <int HELD>
-__global__ __launch_bounds__(kSel) void kv_select_kernel(KvCache c, KvBatch b, const float *__restrict__ mass,
+template <int SEL, int HELD>
+__global__ __launch_bounds__(SEL) void kv_select_kernel(KvCache c, KvBatch b, const float *__restrict__ mass,
                                                          int64_t width, int budget, int recent,
                                                          int32_t *__restrict__ new_lens, float *__restrict__ new_mass,
                                                          int64_t new_width, int32_t *__restrict__ kept, int per)
 {
-    __shared__ int counts[2][3][kSel / 64], wsum[2][kSel / 64];
+    constexpr int WAVES = SEL / 64;
+    __shared__ int counts[2][3][16], wsum[2][WAVES];
     const int h = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int len = min(max(b.lens[seq], 0), b.max_len);
     const int64_t rowid = (int64_t)seq * c.heads + h;
@@ -71,12 +74,12 @@ __global__ __launch_bounds__(kSel) void kv_select_kernel(KvCache c, KvBatch b, c
     const int n = min(len, budget);
     if (h == 0 && tid == 0)
         new_lens[seq] = n;
-    for (int64_t i = n + tid; i < new_width; i += kSel)
+    for (int64_t i = n + tid; i < new_width; i += SEL)
         mo[i] = 0.0f;
     if (len <= budget) {
-        for (int i = tid; i < n; i += kSel)
+        for (int i = tid; i < n; i += SEL)
             mo[i] = m[i];
-        for (int i = tid; i < budget; i += kSel)
+        for (int i = tid; i < budget; i += SEL)
             ko[i] = i < n ? i : -1;
         return;
     }
@@ -105,16 +108,16 @@ __global__ __launch_bounds__(kSel) void kv_select_kernel(KvCache c, KvBatch b, c
                     count(key[i]);
         } else {
             // (in strides here: no order is needed to count)
-            for (int t = tid; t < per * kSel; t += kSel)
+            for (int t = tid; t < per * SEL; t += SEL)
                 count(t < old ? mass_key(m[t]) : 0u);
         }
-        int(&to)[3][kSel / 64] = counts[(shift >> 1) & 1];
+        int(&to)[3][16] = counts[(shift >> 1) & 1];
         if (lane < 3)
             to[lane][wave] = lane == 0 ? cnt[0] : lane == 1 ? cnt[1] : cnt[2];
         __syncthreads();
-        // 16 waves' counts of a candidate in 16 lanes, summed by rotations
-        static_assert(kSel / 64 == 16, "a row of lanes a candidate");
-        int all = lane < 48 ? to[lane >> 4][lane & 15] : 0;
+        // the waves' counts of a candidate in 16 lanes, summed by rotations
+        static_assert(WAVES <= 16, "a row of lanes a candidate");
+        int all = lane < 48 && (lane & 15) < WAVES ? to[lane >> 4][lane & 15] : 0;
         all += __builtin_amdgcn_update_dpp(0, all, 0x128, 0xf, 0xf, true);
         all += __builtin_amdgcn_update_dpp(0, all, 0x124, 0xf, 0xf, true);
         all += __builtin_amdgcn_update_dpp(0, all, 0x122, 0xf, 0xf, true);
@@ -149,7 +152,7 @@ __global__ __launch_bounds__(kSel) void kv_select_kernel(KvCache c, KvBatch b, c
         }
     };
     each([&](int i) { ties += t0 + i < old && key_at(i) == T; });
-    int tie = block_before(ties, wsum[0]);
+    int tie = block_before<WAVES>(ties, wsum[0]);
     auto stays = [&](int i) -> bool {  // in order of i, once
         const int t = t0 + i;
         if (t >= len)
@@ -162,7 +165,7 @@ __global__ __launch_bounds__(kSel) void kv_select_kernel(KvCache c, KvBatch b, c
     int stay = 0;
     const int tie0 = tie;
     each([&](int i) { stay += stays(i); });
-    int place = block_before(stay, wsum[1]);
+    int place = block_before<WAVES>(stay, wsum[1]);
     tie = tie0;
     each([&](int i) {
         if (stays(i)) {
@@ -239,19 +242,24 @@ hipError_t launch_kv_evict(int f, const KvCache &c, const KvBatch &b, const floa
                            int64_t new_width, int32_t *kept, hipStream_t s)
 {
     const dim3 grid(c.heads, b.seqs);
-    const int per = std::max(1, (b.max_len + kSel - 1) / kSel);
-    auto select = [&](auto held) {
-        kv_select_kernel<decltype(held)::value><<<grid, kSel, 0, s>>>(c, b, mass, mass_width, budget, recent, new_lens,
-                                                                     new_mass, new_width, kept, per);
+    // up to 4096 tokens in four waves (one to a SIMD: a pass over the candidates
+    // is a few hundred cycles of latency, which more waves only lengthen), else
+    // in sixteen
+    const int threads = b.max_len <= 16 * kSelFew ? kSelFew : kSel;
+    const int per = std::max(1, (b.max_len + threads - 1) / threads);
+    auto select = [&](auto sel, auto held) {
+        constexpr int SEL = decltype(sel)::value;
+        kv_select_kernel<SEL, decltype(held)::value><<<grid, SEL, 0, s>>>(c, b, mass, mass_width, budget, recent, new_lens,
+                                                                          new_mass, new_width, kept, per);
     };
-    if (per <= 4)
-        select(KvInt<4>{});
+    if (threads == kSelFew)
+        per <= 4 ? select(KvInt<kSelFew>{}, KvInt<4>{}) : select(KvInt<kSelFew>{}, KvInt<16>{});
     else if (per <= 16)
-        select(KvInt<16>{});
+        select(KvInt<kSel>{}, KvInt<16>{});
     else if (per <= 32)
-        select(KvInt<32>{});
+        select(KvInt<kSel>{}, KvInt<32>{});
     else
-        select(KvInt<0>{});
+        select(KvInt<kSel>{}, KvInt<0>{});
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess)
         return e;

@@ -27,21 +27,21 @@ constexpr int kBlock = 64 * kWaves;
 constexpr int kBlk = 64;  // tokens of a wave at a time
 constexpr int kMaxKept = 8;  // rows whose scores are kept
 
-// 64 tokens' keys as operands, with the scales of the lane's rows.
-template <int FMT, int D, int GS>
+// 16 TT tokens' keys as operands, with the scales of the lane's rows.
+template <int FMT, int D, int GS, int TT>
 struct Keys {
     static constexpr int NG = D / GS, ZB = (NG + 1) / 2;
-    u32x4 op[4][D / 32];
-    f32x4 s[4][NG];
+    u32x4 op[TT][D / 32];
+    f32x4 s[TT][NG];
     uint32_t there;  // bit tt: the tile's page exists
 
     __device__ __forceinline__ void load(const KvCache &c, Pages &pg, int t0, int end, int lane, const uint32_t *pairs)
     {
         const int i = lane & 15, kg = lane >> 4;
-        uint32_t w[4][D / 32], z[4];
+        uint32_t w[TT][D / 32], z[TT];
         there = 0;
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
+        for (int tt = 0; tt < TT; ++tt) {
             const int64_t row0 = pg.row(t0 + 16 * tt, end, lane);
             there |= (row0 >= 0 ? 1u : 0u) << tt;
             const int64_t row = row0 >= 0 ? row0 : 0;
@@ -65,7 +65,7 @@ struct Keys {
             }
         }
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
+        for (int tt = 0; tt < TT; ++tt)
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
                 op[tt][k] = key_operand<FMT>(
@@ -74,8 +74,8 @@ struct Keys {
 };
 
 // Scores of tile tt by the lane's column, in units of the column's factor.
-template <int FMT, int D, int GS>
-__device__ __forceinline__ f32x4 tile_scores(const Keys<FMT, D, GS> &k, int tt, const u32x4 *q)
+template <int FMT, int D, int GS, int TT>
+__device__ __forceinline__ f32x4 tile_scores(const Keys<FMT, D, GS, TT> &k, int tt, const u32x4 *q)
 {
     f32x4 x = {0, 0, 0, 0};
 #pragma unroll
@@ -102,18 +102,19 @@ __device__ __forceinline__ float sum16(float v)
     return add_rotated<1>(add_rotated<2>(add_rotated<4>(add_rotated<8>(v))));
 }
 
-// Adds a wave's 64 sums (lane's tokens 16 (e / 4) + 4 kg + e % 4) to the mass.
-__device__ __forceinline__ void add_mass(float (&sum)[16], float *mass, int t0, int len, uint32_t there, int lane)
+// Adds a wave's 4 N sums (lane's tokens 16 (e / 4) + 4 kg + e % 4) to the mass.
+template <int N>
+__device__ __forceinline__ void add_mass(float (&sum)[N], float *mass, int t0, int len, uint32_t there, int lane)
 {
     const int i = lane & 15, kg = lane >> 4;
     float v = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
+    for (int e = 0; e < N; ++e) {
         const float s = sum16(sum[e]);
         v = i == e ? s : v;
     }
     const int at = t0 + 16 * (i >> 2) + 4 * kg + (i & 3);
-    if (at < len && (there >> (i >> 2) & 1))
+    if (i < N && at < len && (there >> (i >> 2) & 1))
         mass[at] += v;
 }
 
@@ -298,41 +299,43 @@ __global__ __launch_bounds__(64) void kv_rows_kernel(KvCache c, KvBatch b, Rows 
     }
 }
 
-template <int FMT, int D, int GS>
+template <int FMT, int D, int GS, int TT>
 __global__ __launch_bounds__(kBlock, 2) void kv_mass_many_kernel(KvCache c, KvBatch b, int group, int window, RowTiles from,
                                                               float *__restrict__ mass, int64_t mass_width)
 {
     __shared__ uint32_t pairs[FMT == Q4_NF4 ? 256 : 1];
+    constexpr int BLK = 16 * TT;  // tokens of a wave
     const int tid = threadIdx.x, lane = tid & 63, i = lane & 15, kg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = blockIdx.x, seq = blockIdx.z;
     const KvSeq s = kv_seq(b, seq);
     if constexpr (FMT == Q4_NF4) {
-        pairs[tid] = nf4_pair(tid);
+        for (int e = tid; e < 256; e += blockDim.x)
+            pairs[e] = nf4_pair(e);
         __syncthreads();
     }
-    const int t0 = range_begin(s, window) + ((int)blockIdx.y * kWaves + wave) * kBlk;
+    const int t0 = range_begin(s, window) + ((int)blockIdx.y * (int)(blockDim.x >> 6) + wave) * BLK;
     if (t0 >= s.len)
         return;
     Pages pg{b.table + (int64_t)seq * b.table_width, c.page_shift, c.heads, h, c.pages, 1 << 30,
              (s.len - 1) >> c.page_shift, -1};
-    Keys<FMT, D, GS> k;
+    Keys<FMT, D, GS, TT> k;
     k.load(c, pg, t0, s.len, lane, pairs);
-    float sum[16];
+    float sum[4 * TT];
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
+    for (int e = 0; e < 4 * TT; ++e)
         sum[e] = 0.0f;
     // the row tiles that see any of the tokens: new tokens from t0 - base on,
     // and with a window those less than `window` past the last
     const int base = s.len - s.fresh, nrows = s.fresh * group;
     int rt = max(t0 - base, 0) * group >> 4, rt_end = (nrows + 15) >> 4;
     if (window > 0) {
-        const int64_t past = (int64_t)t0 + kBlk - 1 + window - base;  // first new token past every window
+        const int64_t past = (int64_t)t0 + BLK - 1 + window - base;  // first new token past every window
         if (past * group < nrows)
             rt_end = min(rt_end, (int)((max(past, (int64_t)0) * group + 15) >> 4));
     }
     // rows that see all the tokens: from the last one's on, and inside every window
-    const int from_row = max(t0 + kBlk - 1 - base, 0) * group;
+    const int from_row = max(t0 + BLK - 1 - base, 0) * group;
     const int64_t past = window > 0 ? ((int64_t)t0 + window - base) * group : INT32_MAX;
     const int to_row = (int)min(max(past, (int64_t)0), (int64_t)INT32_MAX);
     const int64_t at0 = first_tile(s, group, seq);
@@ -348,9 +351,9 @@ __global__ __launch_bounds__(kBlock, 2) void kv_mass_many_kernel(KvCache c, KvBa
         next = *fs;
     }
     for (; rt < rt_end; ++rt) {
-        float x[16];
+        float x[4 * TT];
 #pragma unroll
-        for (int tt = 0; tt < 4; ++tt) {
+        for (int tt = 0; tt < TT; ++tt) {
             const f32x4 y = tile_scores<FMT, D, GS>(k, tt, q);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -369,13 +372,13 @@ __global__ __launch_bounds__(kBlock, 2) void kv_mass_many_kernel(KvCache c, KvBa
         if (__builtin_expect(16 * rt < from_row || 16 * rt + 15 >= to_row, 0)) {
             const int pos = branch_only(base) + (16 * rt + i) / group, low = window > 0 ? pos - window : -1;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 4 * TT; ++e) {
                 const int at = t0 + 16 * (e >> 2) + 4 * kg + (e & 3);
                 x[e] = at <= pos && at > low ? x[e] : -__builtin_inff();
             }
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
+        for (int e = 0; e < 4 * TT; ++e)
             sum[e] += __builtin_amdgcn_exp2f(__builtin_fmaf(x[e], f.x, -f.y));
     }
     add_mass(sum, mass + ((int64_t)seq * c.heads + h) * mass_width, t0, s.len, k.there, lane);
@@ -447,7 +450,12 @@ hipError_t launch_kv_mass(int f, const KvCache &c, const KvBatch &b, const Rows 
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;
-        kv_mass_many_kernel<F, D, GS><<<dim3(c.heads, (unsigned)((range + per - 1) / per), b.seqs), kBlock, 0, s>>>(
+        // 64 tokens a wave (dim 256: 32, by registers); four waves share the
+        // rows they read, unless that leaves compute units without one
+        constexpr int TT = D == 256 ? 2 : 4;
+        const int64_t waves = (range + 16 * TT - 1) / (16 * TT);
+        const int w = waves * c.heads * b.seqs >= 2048 ? kWaves : 1;
+        kv_mass_many_kernel<F, D, GS, TT><<<dim3(c.heads, (unsigned)((waves + w - 1) / w), b.seqs), 64 * w, 0, s>>>(
             c, b, rows.group, rows.window, t, mass, mass_width);
         return hipGetLastError();
     });

@@ -13,7 +13,8 @@
 //    is added to those tokens' scores, which puts it into the weights, and
 //    taken off the row sums again.  So neither weights (at most 2^15.5) nor
 //    values (at most 15, 1 for tables) leave fp16, whatever the cache's
-//    magnitude.
+//    magnitude.  (The reference puts the largest weight at 2^11: it moves
+//    rarely, and weights down to 2^-25 of the largest keep all their bits.)
 //  * LDS holds operands as the lanes read them, 16 bytes a lane in a row, in
 //    two buffers: the next tile is fetched while one is worked on, one barrier
 //    a tile.  Rows of V operands are values d = 8 i + j of the dword i that a
@@ -33,10 +34,12 @@ constexpr int kWaves = 8;
 constexpr int kBlock = 64 * kWaves;
 constexpr int kStagers = 256;  // lanes that stage keys; as many stage values
 
+// 16-row column tiles a wave: two where rows are many (one for dim 256, whose
+// sums take the registers); one, with room for a second workgroup on the unit,
+// where they are few.
 template <int D>
-constexpr int prompt_nt() { return D == 256 ? 1 : 2; }
-template <int D>
-constexpr int prompt_rows() { return 16 * prompt_nt<D>() * kWaves; }
+constexpr int most_nt() { return D == 256 ? 1 : 2; }
+constexpr int block_rows(int nt) { return 16 * nt * kWaves; }
 // Tokens a tile: one staging item of 32 keys or 32 values a lane.
 template <int D>
 constexpr int prompt_tile() { return 32 * kStagers / D; }
@@ -219,14 +222,15 @@ __device__ __forceinline__ void stage(Stage<FMT, D, GS> &st, const Fetch<FMT, D,
     }
 }
 
-template <int FMT, int D, int GS>
-__global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch b, Rows rows, Split sp,
+template <int FMT, int D, int GS, int NT>
+__global__ __launch_bounds__(kBlock, (NT < most_nt<D>() ? 4 : 2)) void kv_prompt_kernel(KvCache c, KvBatch b, Rows rows, Split sp,
                                                               float *__restrict__ part,
                                                               float2 *__restrict__ part_ml)
 {
-    constexpr int NG = D / GS, NT = prompt_nt<D>(), R = prompt_rows<D>(), TT = prompt_tile<D>(), NV = D / 16;
-    constexpr int TB = TT >= 64 ? 2 : 1;   // 32-token steps worked on together
-    constexpr int KT = D == 256 ? 1 : 2;  // 16-token halves of a step whose keys are fetched together
+    constexpr int NG = D / GS, R = block_rows(NT), TT = prompt_tile<D>(), NV = D / 16;
+    constexpr int TB = TT >= 64 && NT == most_nt<D>() ? 2 : 1;   // 32-token steps worked on together
+    constexpr int VF = NV < 8 || NT < most_nt<D>() ? 4 : 8;  // value operands fetched together
+    constexpr int KT = D == 256 || NT < most_nt<D>() ? 1 : 2;  // 16-token halves of a step whose keys are fetched together
     __shared__ Stage<FMT, D, GS> st[2];
     __shared__ uint32_t pairs[FMT == Q4_NF4 ? 256 : 1];
 
@@ -355,10 +359,10 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
                                     y[r] = j == 0 ? a[r] * ks[u][j][r] : __builtin_fmaf(a[r], ks[u][j][r], y[r]);
                             }
                 }
-            u32x4 va[8];
+            u32x4 va[VF];
             auto fetch_values = [&](int b2, int v0) {
 #pragma unroll
-                for (int v = 0; v < 8 && v < NV; ++v)
+                for (int v = 0; v < VF; ++v)
                     va[v] = *(const u32x4 *)&S.v[(((tb + b2) * NV + v0 + v) * 64 + lane) * 2];
                 __builtin_amdgcn_sched_barrier(0);
             };
@@ -395,7 +399,7 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
             if (__builtin_expect(__any(move), 0)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float to = fmaxf(m[n], quad_max(reach[n]) - 13.5f);
+                    const float to = fmaxf(m[n], quad_max(reach[n]) - 11.0f);
                     const float g = __builtin_amdgcn_exp2f(m[n] - to);
                     m[n] = to;
                     l[n] *= g;
@@ -423,18 +427,18 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
                         w[n][k] = pair_h2(p[2 * k], p[2 * k + 1]);
                 }
 #pragma unroll
-                for (int v0 = 0; v0 < NV; v0 += 8) {
+                for (int v0 = 0; v0 < NV; v0 += VF) {
                     if (v0)
                         fetch_values(b2, v0);
 #pragma unroll
-                    for (int v = 0; v < 8 && v0 + v < NV; ++v)
+                    for (int v = 0; v < VF; ++v)
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
                             o[v0 + v][n] = mfma<Q4_F16>(va[v], w[n], o[v0 + v][n]);
                 }
                 if (b2 + 1 < TB)
 #pragma unroll
-                    for (int v = 0; v < 8 && v < NV; ++v)
+                    for (int v = 0; v < VF; ++v)
                         va[v] = *(const u32x4 *)&S.v[(((tb + b2 + 1) * NV + v) * 64 + lane) * 2];
             }
         }
@@ -495,23 +499,29 @@ __global__ __launch_bounds__(kBlock, 2) void kv_prompt_kernel(KvCache c, KvBatch
     }
 }
 
-int rows_a_block(int dim) { return dim == 64 ? prompt_rows<64>() : dim == 128 ? prompt_rows<128>() : prompt_rows<256>(); }
-
 }  // namespace
 
-// Parts only where rows alone would leave compute units idle: as many as leave
-// one workgroup to each of the 256, none shorter than 512 tokens.
+// Row tiles of 256 (dim 256: 128) rows fill the 256 compute units, one
+// workgroup each, or are split into as many parts as do, none shorter than 256
+// tokens.  Where even that leaves units idle or rows empty, tiles of 128 rows,
+// two workgroups a unit.
 Split prompt_split(const KvCache &c, const KvBatch &b, int group, int window)
 {
-    Split sp;
-    const int rows = rows_a_block(c.dim);
-    sp.tiles = (int)(((int64_t)b.max_new * group + rows - 1) / rows);
-    const int64_t range = longest_range(b, window);
-    const int64_t wgs = (int64_t)b.seqs * c.heads * sp.tiles;
-    const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(256 / wgs, range / 512));
-    sp.span = (int)std::max<int64_t>(((range + parts - 1) / parts + 127) / 128 * 128, 128);
-    sp.parts = (int)std::max<int64_t>((range + sp.span - 1) / sp.span, 1);
-    return sp;
+    const int64_t range = longest_range(b, window), rows = (int64_t)b.max_new * group;
+    auto with = [&](int nt, int64_t room) {
+        Split sp;
+        sp.rows = block_rows(nt);
+        sp.tiles = (int)((rows + sp.rows - 1) / sp.rows);
+        const int64_t wgs = (int64_t)b.seqs * c.heads * sp.tiles;
+        const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(room / wgs, range / 256));
+        sp.span = (int)std::max<int64_t>(((range + parts - 1) / parts + 127) / 128 * 128, 128);
+        sp.parts = (int)std::max<int64_t>((range + sp.span - 1) / sp.span, 1);
+        return sp;
+    };
+    if (c.dim == 256)
+        return with(1, 256);
+    const Split big = with(2, 256);
+    return rows <= 128 || (int64_t)b.seqs * c.heads * big.tiles * big.parts < 224 ? with(1, 512) : big;
 }
 
 hipError_t launch_kv_prompt(int f, const KvCache &c, const KvBatch &b, const Rows &rows, const Split &sp,
@@ -519,8 +529,11 @@ hipError_t launch_kv_prompt(int f, const KvCache &c, const KvBatch &b, const Row
 {
     return kv_by_shape(f, c.dim, c.g, [&](auto fmt, auto dim, auto gs) {
         const int64_t grid = (int64_t)sp.parts * sp.tiles * b.seqs * c.heads;
-        kv_prompt_kernel<decltype(fmt)::value, decltype(dim)::value, decltype(gs)::value>
-            <<<dim3((unsigned)grid), kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+        constexpr int F = decltype(fmt)::value, D = decltype(dim)::value, GS = decltype(gs)::value;
+        if (sp.rows == block_rows(most_nt<D>()))
+            kv_prompt_kernel<F, D, GS, most_nt<D>()><<<dim3((unsigned)grid), kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+        else
+            kv_prompt_kernel<F, D, GS, 1><<<dim3((unsigned)grid), kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
         return hipGetLastError();
     });
 }
