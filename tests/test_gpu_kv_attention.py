@@ -85,6 +85,23 @@ def test_token_groups_and_pages(group, page):
     check(pool, [1] * 5, q4.BF16, 3 * group, seed=group)
 
 
+@pytest.mark.parametrize("dim,g,rows", [(64, 64, 64), (64, 32, 32), (64, 64, 33), (128, 128, 32), (128, 128, 17), (128, 32, 8),
+                                        (128, 32, 5), (256, 128, 16), (256, 64, 8), (256, 32, 4), (256, 32, 3), (256, 32, 1)])
+@pytest.mark.parametrize("fmt", [q4.INT4_ASYM, q4.NF4])
+def test_token_rows(fmt, dim, g, rows):
+    """As many rows as fill one, two or four column tiles, by one token's heads and by several tokens'."""
+    pool = Pool(fmt, g, dim, 2, 32, [700, 45, 2], seed=rows)
+    check(pool, [1, 1, 1], q4.F16, 2 * rows, seed=rows)
+    check(pool, [rows, max(1, rows - 1), 1], q4.BF16, 2, seed=rows, window=100)
+
+
+def test_many_sequences():
+    """Sequences and heads enough to fill the card unsplit (of 6 and of 4 waves a workgroup), and beyond."""
+    for seqs, heads in ((100, 4), (128, 4), (150, 4), (210, 4)):
+        pool = Pool(q4.NF4, 64, 64, heads, 16, [530 + (7 * b) % 60 if b % 9 else b % 5 for b in range(seqs)], seed=seqs)
+        check(pool, [1] * seqs, q4.BF16, 2 * heads, seed=seqs)
+
+
 @pytest.mark.parametrize("length", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 257, 511, 1023, 1025, 5003])
 @pytest.mark.parametrize("fmt", [q4.INT4_ASYM, q4.NF4])
 def test_token_lengths(fmt, length):
