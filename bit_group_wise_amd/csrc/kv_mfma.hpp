@@ -8,12 +8,13 @@
 //
 // INT4 keys: OR-ing a nibble into 0x6400 makes the fp16 number 1024 + c (bits
 // 0-3) or 1024 + 16 c (bits 4-7); a packed add takes 1024 and the zero-point
-// off again, exactly.  INT4 values: a nibble left in place is an fp16
-// subnormal, c 2^-24 (bits 0-3) or c 2^-20 (bits 4-7), one mask a pair.  The
-// matrix cores take subnormals, but align their products by the exponent
-// field, so that of a sum only about 2^-14 of its largest term is kept
-// (measured on the scores of fp16 queries, which lost up to 1e-4): far below
-// the rounding of a 16-bit output, and too much for scores.  NF4: the
+// off again, exactly.  INT4 values do the same, a pair of tokens to a
+// word.  (A nibble left in place is an fp16 subnormal, c 2^-24 or c 2^-20, for
+// one mask a pair and no add.  But the matrix cores align subnormals' products
+// by the exponent field and lose their low bits beside larger terms: scores of
+// fp16 queries were off by up to 1e-4, and the output over 131071 tokens was
+// 4.2e-4 from binary64 where rounding the weights and the output gives 2.9e-4.)
+// NF4: the
 // table's three-decimal entries times 1000 are integers of at most 10 bits,
 // exact in fp16; a 256-entry LDS table gives the two levels of a byte.  FP4:
 // E2M1 elements, converted by v_cvt_scalef32_pk_f16_fp4.
@@ -34,7 +35,7 @@ constexpr float key_unit()
 template <int FMT>
 constexpr float value_unit()
 {
-    return FMT == Q4_NF4 ? 1.0f / 1000.0f : FMT == Q4_FP4 ? 1.0f / 6.0f : 16777216.0f;
+    return FMT == Q4_NF4 ? 1.0f / 1000.0f : FMT == Q4_FP4 ? 1.0f / 6.0f : 1.0f;
 }
 template <int FMT>
 constexpr bool kv_int() { return FMT == Q4_INT4_SYM || FMT == Q4_INT4_ASYM; }
@@ -68,6 +69,10 @@ __device__ __forceinline__ uint32_t fp4_pair(uint32_t w)
 struct KeyZero {
     uint32_t even, odd;
 };
+__device__ __forceinline__ KeyZero zero_of_pair(uint32_t z)  // a zero-point 0..15 in each half
+{
+    return KeyZero{0xe400e400u + z, 0xe400e400u + 16 * z};
+}
 __device__ __forceinline__ KeyZero key_zero(uint32_t z)  // z in 0..15
 {
     return KeyZero{0xe400e400u + z * 0x00010001u, 0xe400e400u + z * 0x00100010u};
@@ -114,26 +119,29 @@ __device__ __forceinline__ uint32_t value_select(int i)
     }
 }
 // Pairs (token a, token b) of the lane's g/16 values from the two tokens'
-// dwords; o[n] is the pair of product n (INT4: odd n sixteenfold).
+// dwords; o[n] is the pair of product n (INT4: odd n sixteenfold).  z: the two
+// tokens' zero-points.
 template <int FMT, int GS>
-__device__ __forceinline__ void value_pairs(uint32_t a, uint32_t b, uint32_t sel, const uint32_t *pairs,
-                                            uint32_t (&o)[GS / 16])
+__device__ __forceinline__ void value_pairs(uint32_t a, uint32_t b, uint32_t sel, const KeyZero &z,
+                                            const uint32_t *pairs, uint32_t (&o)[GS / 16])
 {
     if constexpr (kv_int<FMT>()) {
+        const uint32_t m0 = opaque_word(kNib0), m1 = opaque_word(kNib1);
+        const uint32_t one = opaque_sword(0x64006400u);
         const uint32_t x = __builtin_amdgcn_perm(b, a, sel);
-        o[0] = x & kNib0;
-        o[1] = x & kNib1;
+        o[0] = add_h2((x & m0) | one, z.even);
+        o[1] = add_h2((x & m1) | one, z.odd);
         if constexpr (GS >= 64) {
             const uint32_t y = x >> 8;
-            o[2] = y & kNib0;
-            o[3] = y & kNib1;
+            o[2] = add_h2((y & m0) | one, z.even);
+            o[3] = add_h2((y & m1) | one, z.odd);
         }
         if constexpr (GS == 128) {
             const uint32_t u = __builtin_amdgcn_perm(b, a, 0x07060302u), v = u >> 8;
-            o[4] = u & kNib0;
-            o[5] = u & kNib1;
-            o[6] = v & kNib0;
-            o[7] = v & kNib1;
+            o[4] = add_h2((u & m0) | one, z.even);
+            o[5] = add_h2((u & m1) | one, z.odd);
+            o[6] = add_h2((v & m0) | one, z.even);
+            o[7] = add_h2((v & m1) | one, z.odd);
         }
     } else {
         if constexpr (GS != 128) {

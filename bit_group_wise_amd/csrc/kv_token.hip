@@ -17,9 +17,7 @@
 //    V scale belongs to a token and a group, so it goes into the weight of the
 //    group's column, w_t s_tj, rounded to fp16 (11 bits against the output's 8
 //    or 11: each weight is off by at most 2^-11 of itself, independently).  Of
-//    a column's result only its group's values are used.  The zero-points'
-//    share, sum_t w_t s_tj z_tj, is one more product of the same rounded
-//    weights with the zero-points as rows, taken off at the end.
+//    a column's result only its group's values are used.
 //  * Reference.  w_t s_tj must stay below 65504 and the largest should be well
 //    inside fp16's normal range whatever the values' size, so m tracks
 //    x_t + log2(s_t), not x_t: it moves only when a weight would pass 2^15.5
@@ -107,7 +105,6 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
 {
     constexpr int NG = D / GS, W = D < 128 ? D : 128, HV = D / W, NP = W / 16;
     constexpr int NR = NT * 16 / NG;                         // rows
-    constexpr int HZ = FMT == Q4_INT4_ASYM ? HV : 1;         // zero-point products
     constexpr int ZB = (NG + 1) / 2;
     using Codes = ValueCodes<D>;
     using M = Meta<FMT, NG, 64>;  // lanes 0..31: keys, 32..63: values
@@ -148,15 +145,12 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
     const int all_to = s.len - s.fresh, all_from = rows.window > 0 ? s.len - rows.window : 0;
 
     const uint32_t sel = value_select<FMT, W>(i);
-    f32x4 o[NT][HV][NP], oz[NT][HZ];
+    f32x4 o[NT][HV][NP];
     float m[NT], l[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         m[n] = kNone;
         l[n] = 0.0f;
-#pragma unroll
-        for (int v = 0; v < HZ; ++v)
-            oz[n][v] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int v = 0; v < HV; ++v)
 #pragma unroll
@@ -257,9 +251,6 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
                 m[n] = to;
                 l[n] *= f;
 #pragma unroll
-                for (int v = 0; v < HZ; ++v)
-                    oz[n][v] *= f;
-#pragma unroll
                 for (int v = 0; v < HV; ++v)
 #pragma unroll
                     for (int p = 0; p < NP; ++p)
@@ -285,7 +276,13 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
             for (int e = 0; e < 4; ++e) {
                 const int u = e >> 1, r = 2 * (e & 1);
                 uint32_t p[NP];
-                value_pairs<FMT, W>(Codes::get(wk.v, u, r, v, i, kg), Codes::get(wk.v, u, r + 1, v, i, kg), sel,
+                KeyZero z = zero_of_pair(0x00080008u);
+                if constexpr (FMT == Q4_INT4_ASYM) {
+                    uint32_t zw[ZB];
+                    load_words(zw, wk.m.z + ZB * (32 + 16 * u + 4 * kg));
+                    z = zero_of_pair(zero_pair<D, GS, ZB>(zw, r, v, i));
+                }
+                value_pairs<FMT, W>(Codes::get(wk.v, u, r, v, i, kg), Codes::get(wk.v, u, r + 1, v, i, kg), sel, z,
                                     pairs, p);
 #pragma unroll
                 for (int k = 0; k < NP; ++k)
@@ -296,24 +293,6 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     o[n][v][k] = mfma<Q4_F16>(va[k], wp[n], o[n][v][k]);
-        }
-        if constexpr (kv_int<FMT>()) {
-#pragma unroll
-            for (int v = 0; v < HZ; ++v) {
-                u32x4 z = {0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u};
-                if constexpr (FMT == Q4_INT4_ASYM) {
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        uint32_t zw[ZB];
-                        load_words(zw, wk.m.z + ZB * (32 + 16 * u + 4 * kg));
-                        z[2 * u] = zero_pair<D, GS, ZB>(zw, 0, v, i);
-                        z[2 * u + 1] = zero_pair<D, GS, ZB>(zw, 2, v, i);
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    oz[n][v] = mfma<Q4_F16>(z, wp[n], oz[n][v]);
-            }
         }
         t0 = tn;
         row0 = next0;
@@ -342,8 +321,6 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
                     for (int e = 0; e < 4; ++e) {
                         const float unit = value_unit<FMT>() * (kv_int<FMT>() && (e & 1) ? 0.0625f : 1.0f);
                         y[e] = o[n][v][k + e][r] * unit;
-                        if constexpr (kv_int<FMT>())
-                            y[e] -= oz[n][HZ == 1 ? 0 : v][r] * value_unit<FMT>();
                     }
                     *(f32x4 *)&share[wave].os[r0][W * v + W / 16 * (4 * kg + r) + k] = y;
                 }
