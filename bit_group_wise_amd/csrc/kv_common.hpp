@@ -88,17 +88,6 @@ __device__ __forceinline__ float kv_zero(const KvHalf &x, int64_t row, int group
     else
         return FMT == Q4_INT4_SYM ? 8.0f : 0.0f;
 }
-// Level of a code before the zero-point is taken off: the code itself (INT4),
-// the table's entry (NF4, FP4; tbl holds the 16 entries).
-template <int FMT>
-__device__ __forceinline__ float kv_level(uint32_t code, const float *tbl)
-{
-    if constexpr (f32_absmax(FMT))
-        return tbl[code & 15];
-    else
-        return (float)(code & 15);
-}
-
 // Calls fn(integral_constant<FMT>) for the run-time format.
 template <int V>
 struct KvInt {

@@ -17,6 +17,7 @@ tokens are rows starts[b] .. starts[b+1] - 1 of k, v and q.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import q4
 from .q4 import _act_code, _check, _torch, lib
@@ -33,12 +34,6 @@ class _CacheArgs(ctypes.Structure):
 class _BatchArgs(ctypes.Structure):
     _fields_ = [("table", _vp), ("lens", _vp), ("starts", _vp), ("tokens", _i64),
                 ("table_width", _i32), ("seqs", _i32), ("max_new", _i32), ("max_len", _i32)]
-
-
-def _stream(device) -> int:
-    """The current stream of a device as the raw handle (a decode step makes a
-    few calls of some microseconds each, of which a stream object is one)."""
-    return _torch()._C._cuda_getCurrentRawStream(device.index)
 
 
 def _tensor(t, name, dtype, shape=None, device=None):
@@ -85,7 +80,10 @@ class KVCache:
         self.fmt, self.g, self.pages, self.heads, self.page, self.dim = fmt, g, pages, heads, page, dim
         self.k_codes, self.k_scales, self.k_zeros = k_codes, k_scales, k_zeros
         self.v_codes, self.v_scales, self.v_zeros = v_codes, v_scales, v_zeros
-        self.device = dev
+        self.device, self._index = dev, dev.index
+        # The current stream as the raw handle: a decode step makes a few calls
+        # of some microseconds each, of which a stream object is one.
+        self._stream = functools.partial(torch._C._cuda_getCurrentRawStream, dev.index)
         self._args = _CacheArgs(*(None if t is None else t.data_ptr() for t in
                                   (k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros)),
                                 pages, page, heads, dim, g, fmt, 0)
@@ -164,17 +162,17 @@ class Batch:
         return n
 
 
-def _rows(t, name, tokens, heads, dim, device):
+def _rows(t, name, tokens, heads, cache):
     """Checks of a packed [tokens, heads, dim] array (rows contiguous); its
     strides between tokens and heads (one over an axis of one says nothing)."""
-    if t.shape != (tokens, heads, dim):
-        raise ValueError(f"{name} must be [{tokens}, {heads}, {dim}], got {list(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-    st = t.stride()
-    if st[2] != 1:
+    if t.shape != (tokens, heads, cache.dim):
+        raise ValueError(f"{name} must be [{tokens}, {heads}, {cache.dim}], got {list(t.shape)}")
+    if t.get_device() != cache._index:  # (-1 on the host)
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    ts, hs, ds = t.stride()
+    if ds != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    return st[0] if tokens > 1 else 0, st[1] if heads > 1 else 0
+    return ts if tokens > 1 else 0, hs if heads > 1 else 0
 
 
 def append(cache, batch, k, v):
@@ -182,12 +180,12 @@ def append(cache, batch, k, v):
     rows contiguous, any multiple of 8 between them) into their pages
     (q4_kv_append)."""
     ref = batch._ref(cache)
-    ks = _rows(k, "k", batch.tokens, cache.heads, cache.dim, cache.device)
-    vs = _rows(v, "v", batch.tokens, cache.heads, cache.dim, cache.device)
+    ks = _rows(k, "k", batch.tokens, cache.heads, cache)
+    vs = _rows(v, "v", batch.tokens, cache.heads, cache)
     if v.dtype != k.dtype:
         raise TypeError("k and v must have one dtype")
     st = lib().q4_kv_append(cache._ref, ref, _act_code(k.dtype), k.data_ptr(), *ks, v.data_ptr(), *vs,
-                            _stream(cache.device))
+                            cache._stream())
     _check(st, "q4_kv_append")
 
 
@@ -199,12 +197,13 @@ def read(cache, batch, dtype, out=None):
     code = _act_code(dtype)
     shape = (batch.tokens, cache.heads, cache.dim)
     if out is None:
-        out = torch.empty((2, *shape), dtype=dtype, device=cache.device).unbind(0)
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
+        v = torch.empty_like(k)
     else:
         for t in out:
             _tensor(t, "out", dtype, shape, cache.device)
-    k, v = out
-    st = lib().q4_kv_read(cache._ref, ref, code, k.data_ptr(), v.data_ptr(), _stream(cache.device))
+        k, v = out
+    st = lib().q4_kv_read(cache._ref, ref, code, k.data_ptr(), v.data_ptr(), cache._stream())
     _check(st, "q4_kv_read")
     return k, v
 
@@ -228,10 +227,10 @@ def attention(cache, batch, q, *, scale=None, window=0, mass=None, lse=None, out
     if q.dim() != 3:
         raise ValueError("q must be [tokens, q_heads, dim]")
     heads = q.shape[1]
-    qs = _rows(q, "q", batch.tokens, heads, cache.dim, cache.device)
+    qs = _rows(q, "q", batch.tokens, heads, cache)
     code = _act_code(q.dtype)
     if out is None:
-        out = torch.empty((batch.tokens, heads, cache.dim), dtype=q.dtype, device=cache.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _tensor(out, "out", q.dtype, (batch.tokens, heads, cache.dim), cache.device)
     mass_p, width = None, 0
@@ -254,7 +253,7 @@ def attention(cache, batch, q, *, scale=None, window=0, mass=None, lse=None, out
         work_p, have = workspace.data_ptr(), need
     st = lib().q4_kv_attention(cache._ref, ref, code, q.data_ptr(), *qs, heads,
                                cache.dim ** -0.5 if scale is None else scale, window, out.data_ptr(), lse_p,
-                               mass_p, width, work_p, have, _stream(cache.device))
+                               mass_p, width, work_p, have, cache._stream())
     _check(st, "q4_kv_attention")
     return out
 
@@ -282,6 +281,6 @@ def evict(cache, batch, mass, new_table, budget, recent, *, width=None):
     kept = torch.empty((batch.seqs, cache.heads, budget), dtype=torch.int32, device=cache.device)
     st = lib().q4_kv_evict(cache._ref, ref, mass.data_ptr(), mass.shape[2], new_table.data_ptr(),
                            new_table.shape[1], budget, recent, new_lens.data_ptr(), new_mass.data_ptr(),
-                           width, kept.data_ptr(), _stream(cache.device))
+                           width, kept.data_ptr(), cache._stream())
     _check(st, "q4_kv_evict")
     return new_lens, new_mass, kept
