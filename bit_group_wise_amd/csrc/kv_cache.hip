@@ -20,6 +20,9 @@ namespace q4 {
 namespace {
 
 constexpr int kBlock = 256;
+// Rows a lane works on, and from how many pieces of 8 values on.
+constexpr int kRowsMany = 4;
+constexpr int64_t kManyItems = 1 << 20;
 
 __constant__ float c_nf4[16] = {kNF4[0], kNF4[1], kNF4[2],  kNF4[3],  kNF4[4],  kNF4[5],
                                 kNF4[6], kNF4[7], kNF4[8],  kNF4[9],  kNF4[10], kNF4[11],
@@ -37,46 +40,42 @@ __constant__ NF4Bucket c_buckets[33] = {
 #undef B
 };
 
-// What a lane works on: 8 values of a new token's row.
+// What a lane works on: 8 values of a new token's row, U rows at a time so
+// that their loads (page, then row) are in flight together.
 struct Item {
-    int tok, chunk, pos;
+    int tok, chunk;
     bool in;
     int64_t row;  // in the pool, or -1
 };
-__device__ __forceinline__ Item item_of(const KvCache &c, const KvBatch &b, const KvSeq &s, int seq, int h,
-                                        int chunk_shift)
+template <int U>
+__device__ __forceinline__ void items_of(Item (&t)[U], const KvCache &c, const KvBatch &b, const KvSeq &s, int seq,
+                                         int h, int chunk_shift)
 {
-    Item t;
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    t.chunk = (int)(i & ((1 << chunk_shift) - 1));
-    t.in = (i >> chunk_shift) < s.fresh;
-    t.tok = (int)(i >> chunk_shift);
-    t.pos = s.len - s.fresh + t.tok;
-    t.row = t.in && t.pos >= 0 ? kv_row(c, b.table + (int64_t)seq * b.table_width, t.pos, h) : -1;
-    return t;
+    const int32_t *table = b.table + (int64_t)seq * b.table_width;
+    int page[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t i = ((int64_t)blockIdx.x * U + u) * blockDim.x + threadIdx.x;
+        t[u].chunk = (int)(i & ((1 << chunk_shift) - 1));
+        t[u].tok = (int)(i >> chunk_shift);
+        const int pos = s.len - s.fresh + t[u].tok;
+        t[u].in = t[u].tok < s.fresh;
+        const bool there = t[u].in && pos >= 0;
+        page[u] = table[there ? pos >> c.page_shift : 0];
+        t[u].row = there ? pos & ((1 << c.page_shift) - 1) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        t[u].row = t[u].row >= 0 && (unsigned)page[u] < (unsigned)c.pages
+                       ? (((int64_t)page[u] * c.heads + h) << c.page_shift) + t[u].row
+                       : -1;
 }
 
+// Codes 8 values, `raw`, of row t and stores them.
 template <int FMT, int IN, int LPG>
-__global__ __launch_bounds__(kBlock) void kv_append_kernel(
-    KvCache c, KvBatch b, const uint16_t *__restrict__ k, int64_t kts, int64_t khs,
-    const uint16_t *__restrict__ v, int64_t vts, int64_t vhs, int chunk_shift)
+__device__ __forceinline__ void code_row(const KvCache &c, const KvHalf &to, const Item &t, const u32x4 &raw,
+                                         const NF4Bucket *buckets)
 {
-    __shared__ NF4Bucket buckets[FMT == Q4_NF4 ? 33 : 1];
-    if constexpr (FMT == Q4_NF4) {
-        if (threadIdx.x < 33)
-            buckets[threadIdx.x] = c_buckets[threadIdx.x];
-        __syncthreads();
-    }
-    const int seq = blockIdx.z, half = blockIdx.y & 1, h = blockIdx.y >> 1;
-    const KvSeq s = kv_seq(b, seq);
-    const Item t = item_of(c, b, s, seq, h, chunk_shift);
-    // every lane of a row has the same token, so a group leaves as one
-    if (t.row < 0)
-        return;
-    const KvHalf &to = half ? c.v : c.k;
-    const uint16_t *from = half ? v + (int64_t)(s.first + t.tok) * vts + (int64_t)h * vhs
-                                : k + (int64_t)(s.first + t.tok) * kts + (int64_t)h * khs;
-    const u32x4 raw = __builtin_nontemporal_load((const u32x4 *)(from + 8 * t.chunk));
     float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -117,7 +116,7 @@ __global__ __launch_bounds__(kBlock) void kv_append_kernel(
         }
         // the odd group's zero-point joins the even one's byte
         const int z1 = __shfl_down(z, LPG);
-        if (first) {
+        if (first && t.row >= 0) {
             ((uint16_t *)to.scales)[t.row * groups + j] = (uint16_t)sb;
             if ((j & 1) == 0)
                 to.zeros[t.row * kv_zero_bytes(c.dim, c.g) + (j >> 1)] =
@@ -142,10 +141,10 @@ __global__ __launch_bounds__(kBlock) void kv_append_kernel(
             } else {
                 word = 0x88888888u;
             }
-            if (first)
+            if (first && t.row >= 0)
                 ((uint16_t *)to.scales)[t.row * groups + j] = (uint16_t)sb;
         } else {
-            if (first)
+            if (first && t.row >= 0)
                 ((float *)to.scales)[t.row * groups + j] = a;
             if (IN == Q4_BF16 && !(a >= 0x1p-100f && a <= 0x1p100f) && a != 0.0f) {
                 // the reciprocal of so small or large a bf16 absmax is not a
@@ -163,10 +162,42 @@ __global__ __launch_bounds__(kBlock) void kv_append_kernel(
                 word = a != 0.0f ? fp4_word(x, a) : 0u;
         }
     }
-    *(uint32_t *)(to.codes + t.row * (c.dim >> 1) + 4 * t.chunk) = word;
+    if (t.row >= 0)
+        *(uint32_t *)(to.codes + t.row * (c.dim >> 1) + 4 * t.chunk) = word;
 }
 
-template <int FMT, int OUT>
+template <int FMT, int IN, int LPG, int U>
+__global__ __launch_bounds__(kBlock) void kv_append_kernel(
+    KvCache c, KvBatch b, const uint16_t *__restrict__ k, int64_t kts, int64_t khs,
+    const uint16_t *__restrict__ v, int64_t vts, int64_t vhs, int chunk_shift)
+{
+    __shared__ NF4Bucket buckets[FMT == Q4_NF4 ? 33 : 1];
+    if constexpr (FMT == Q4_NF4) {
+        if (threadIdx.x < 33)
+            buckets[threadIdx.x] = c_buckets[threadIdx.x];
+        __syncthreads();
+    }
+    const int seq = blockIdx.z, half = blockIdx.y & 1, h = blockIdx.y >> 1;
+    const KvSeq s = kv_seq(b, seq);
+    if (s.fresh == 0)
+        return;
+    const uint16_t *from = half ? v + (int64_t)h * vhs : k + (int64_t)h * khs;
+    const int64_t ts = half ? vts : kts;
+    // every lane of a row has the same token, so a group works as one; what
+    // has no place in the cache reads a row that is there and stores nothing
+    Item t[U];
+    items_of(t, c, b, s, seq, h, chunk_shift);
+    u32x4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        raw[u] = __builtin_nontemporal_load(
+            (const u32x4 *)(from + (s.first + min(t[u].tok, s.fresh - 1)) * ts + 8 * t[u].chunk));
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        code_row<FMT, IN, LPG>(c, half ? c.v : c.k, t[u], raw[u], buckets);
+}
+
+template <int FMT, int OUT, int U>
 __global__ __launch_bounds__(kBlock) void kv_read_kernel(KvCache c, KvBatch b, uint16_t *__restrict__ k,
                                                          uint16_t *__restrict__ v, int chunk_shift)
 {
@@ -179,39 +210,53 @@ __global__ __launch_bounds__(kBlock) void kv_read_kernel(KvCache c, KvBatch b, u
     }
     const int seq = blockIdx.z, half = blockIdx.y & 1, h = blockIdx.y >> 1;
     const KvSeq s = kv_seq(b, seq);
-    const Item t = item_of(c, b, s, seq, h, chunk_shift);
-    if (!t.in)
-        return;
-    u32x4 o = {0, 0, 0, 0};
-    if (t.row >= 0) {
-        const KvHalf &from = half ? c.v : c.k;
-        const uint32_t w = *(const uint32_t *)(from.codes + t.row * (c.dim >> 1) + 4 * t.chunk);
-        const int groups = c.dim / c.g, j = 8 * t.chunk / c.g;
-        const float sc = kv_scale<FMT>(from, t.row, groups, j);
-        const float z = kv_zero<FMT>(from, t.row, groups, j);
+    Item t[U];
+    items_of(t, c, b, s, seq, h, chunk_shift);
+    const KvHalf &from = half ? c.v : c.k;
+    const int groups = c.dim / c.g;
+    uint32_t w[U];
+    float sc[U], z[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t row = max(t[u].row, (int64_t)0);  // (page 0 is read and not used)
+        const int j = 8 * t[u].chunk / c.g;
+        w[u] = *(const uint32_t *)(from.codes + row * (c.dim >> 1) + 4 * t[u].chunk);
+        sc[u] = kv_scale<FMT>(from, row, groups, j);
+        z[u] = kv_zero<FMT>(from, row, groups, j);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        u32x4 o;
+        // one binary32 product each, then one rounding; INT4's is an fma,
+        // c s - z s with z s exact: the same single rounding of (c - z) s
+        const uint32_t lo = w[u] & 0x0f0f0f0fu, hi = (w[u] >> 4) & 0x0f0f0f0fu;
+        const float off = -z[u] * sc[u];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            // one binary32 product each, then one rounding
             float l0, l1;
             if constexpr (f32_absmax(FMT)) {
-                const float2 p = pairs[(w >> (8 * i)) & 255];
-                l0 = p.x, l1 = p.y;
+                const float2 p = pairs[(w[u] >> (8 * i)) & 255];
+                l0 = keep_f32(p.x * sc[u]);
+                l1 = keep_f32(p.y * sc[u]);
             } else {
-                l0 = (float)((w >> (8 * i)) & 15u) - z;
-                l1 = (float)((w >> (8 * i + 4)) & 15u) - z;
+                l0 = __builtin_fmaf((float)((lo >> (8 * i)) & 255u), sc[u], off);
+                l1 = __builtin_fmaf((float)((hi >> (8 * i)) & 255u), sc[u], off);
             }
-            l0 = keep_f32(l0 * sc);
-            l1 = keep_f32(l1 * sc);
             o[i] = OUT == Q4_F16 ? pack_h2(l0, l1) : pack_bf2(l0, l1);
         }
+        if (t[u].row < 0)
+            o = u32x4{0, 0, 0, 0};
+        if (t[u].in)
+            __builtin_nontemporal_store(o, (u32x4 *)((half ? v : k) +
+                                                     ((int64_t)(s.first + t[u].tok) * c.heads + h) * c.dim +
+                                                     8 * t[u].chunk));
     }
-    __builtin_nontemporal_store(
-        o, (u32x4 *)((half ? v : k) + ((int64_t)(s.first + t.tok) * c.heads + h) * c.dim + 8 * t.chunk));
 }
 
 struct Launch {
     dim3 grid;
     int block, shift;
+    bool many;  // kRowsMany rows a lane
 };
 Launch launch_of(const KvCache &c, const KvBatch &b)
 {
@@ -219,7 +264,9 @@ Launch launch_of(const KvCache &c, const KvBatch &b)
     l.shift = __builtin_ctz(c.dim / 8);
     const int64_t items = (int64_t)b.max_new << l.shift;
     l.block = items <= 64 ? 64 : kBlock;  // (single tokens leave most of a large workgroup idle)
-    l.grid = dim3((unsigned)((items + l.block - 1) / l.block), (unsigned)(2 * c.heads), (unsigned)b.seqs);
+    l.many = items * 2 * c.heads * b.seqs >= kManyItems;
+    const int64_t per = (int64_t)l.block * (l.many ? kRowsMany : 1);
+    l.grid = dim3((unsigned)((items + per - 1) / per), (unsigned)(2 * c.heads), (unsigned)b.seqs);
     return l;
 }
 
@@ -232,10 +279,14 @@ hipError_t launch_kv_append(int f, const KvCache &c, const KvBatch &b, int in_t,
     return kv_by_format(f, [&](auto fmt) {
         constexpr int F = decltype(fmt)::value;
         const Launch l = launch_of(c, b);
-        auto go = [&](auto in, auto lpg) {
-            kv_append_kernel<F, decltype(in)::value, decltype(lpg)::value><<<l.grid, l.block, 0, s>>>(
-                c, b, (const uint16_t *)k, kts, khs, (const uint16_t *)v, vts, vhs, l.shift);
+        auto launch = [&](auto in, auto lpg, auto rows) {
+            kv_append_kernel<F, decltype(in)::value, decltype(lpg)::value, decltype(rows)::value>
+                <<<l.grid, l.block, 0, s>>>(c, b, (const uint16_t *)k, kts, khs, (const uint16_t *)v, vts, vhs,
+                                            l.shift);
             return hipGetLastError();
+        };
+        auto go = [&](auto in, auto lpg) {
+            return l.many ? launch(in, lpg, KvInt<kRowsMany>{}) : launch(in, lpg, KvInt<1>{});
         };
         auto by_g = [&](auto in) {
             return c.g == 32 ? go(in, KvInt<4>{}) : c.g == 64 ? go(in, KvInt<8>{}) : go(in, KvInt<16>{});
@@ -250,11 +301,13 @@ hipError_t launch_kv_read(int f, const KvCache &c, const KvBatch &b, int out_t, 
     return kv_by_format(f, [&](auto fmt) {
         constexpr int F = decltype(fmt)::value;
         const Launch l = launch_of(c, b);
-        if (out_t == Q4_F16)
-            kv_read_kernel<F, Q4_F16><<<l.grid, l.block, 0, s>>>(c, b, (uint16_t *)k, (uint16_t *)v, l.shift);
-        else
-            kv_read_kernel<F, Q4_BF16><<<l.grid, l.block, 0, s>>>(c, b, (uint16_t *)k, (uint16_t *)v, l.shift);
-        return hipGetLastError();
+        auto launch = [&](auto out, auto rows) {
+            kv_read_kernel<F, decltype(out)::value, decltype(rows)::value>
+                <<<l.grid, l.block, 0, s>>>(c, b, (uint16_t *)k, (uint16_t *)v, l.shift);
+            return hipGetLastError();
+        };
+        auto go = [&](auto out) { return l.many ? launch(out, KvInt<kRowsMany>{}) : launch(out, KvInt<1>{}); };
+        return out_t == Q4_F16 ? go(KvInt<Q4_F16>{}) : go(KvInt<Q4_BF16>{});
     });
 }
 
