@@ -104,8 +104,7 @@ __global__ __launch_bounds__(SEL) void kv_select_kernel(KvCache c, KvBatch b, co
         if constexpr (HELD) {
 #pragma unroll
             for (int i = 0; i < HELD; ++i)
-                if (i < per)  // (uniform)
-                    count(key[i]);
+                count(key[i]);
         } else {
             // (in strides here: no order is needed to count)
             for (int t = tid; t < per * SEL; t += SEL)
@@ -129,6 +128,13 @@ __global__ __launch_bounds__(SEL) void kv_select_kernel(KvCache c, KvBatch b, co
         if (d < 3)
             above = sum[d];
         T |= (uint32_t)d << shift;
+        // exactly `want` reach T: no later bit matters (without ties this
+        // comes after about 24 of 32 bits)
+        if (d > 0 && sum[max(d, 1) - 1] == want) {
+            T -= 1;
+            above = want;
+            break;
+        }
     }
     // `above` was last set where a digit was not 3: the keys past the prefix
     // T then had, which are those above T (later digits of 3 leave none between)
@@ -162,6 +168,13 @@ __global__ __launch_bounds__(SEL) void kv_select_kernel(KvCache c, KvBatch b, co
         const uint32_t k = key_at(i);
         return k > T || (k == T && tie++ < need);
     };
+    // (the kept tokens' masses, asked for together before the places are known)
+    float val[HELD ? HELD : 1];
+    if constexpr (HELD) {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+            val[i] = i < per ? m[min(t0 + i, len - 1)] : 0.0f;
+    }
     int stay = 0;
     const int tie0 = tie;
     each([&](int i) { stay += stays(i); });
@@ -170,7 +183,7 @@ __global__ __launch_bounds__(SEL) void kv_select_kernel(KvCache c, KvBatch b, co
     each([&](int i) {
         if (stays(i)) {
             ko[place] = t0 + i;
-            mo[place] = m[t0 + i];
+            mo[place] = HELD ? val[HELD ? i : 0] : m[t0 + i];
             ++place;
         }
     });
@@ -253,7 +266,11 @@ hipError_t launch_kv_evict(int f, const KvCache &c, const KvBatch &b, const floa
                                                                           new_mass, new_width, kept, per);
     };
     if (threads == kSelFew)
-        per <= 4 ? select(KvInt<kSelFew>{}, KvInt<4>{}) : select(KvInt<kSelFew>{}, KvInt<16>{});
+        per <= 4   ? select(KvInt<kSelFew>{}, KvInt<4>{})
+        : per <= 8 ? select(KvInt<kSelFew>{}, KvInt<8>{})
+                   : select(KvInt<kSelFew>{}, KvInt<16>{});
+    else if (per <= 8)
+        select(KvInt<kSel>{}, KvInt<8>{});
     else if (per <= 16)
         select(KvInt<kSel>{}, KvInt<16>{});
     else if (per <= 32)
