@@ -11,8 +11,16 @@
 // token's place.  Counting needs no atomics: a wave counts by ballot, and the
 // waves' counts meet in LDS.
 //
+// Bound: latency.  A pass over the candidates is some 500 cycles of ballots, a
+// barrier and the exchange in LDS, whatever the length: 12 us for 1088 tokens
+// in four waves, 23 us for 16 x 8 rows of 8192 in sixteen.
+//
 // Move: rows go to other pages, so no order is needed: a lane copies 16 bytes
-// of a row's codes, and a row's lanes share its scales and zero-points.
+// of a row's codes, and a row's lanes share its scales and zero-points.  Bound:
+// HBM traffic.  Kept tokens lie among dropped ones and a row of codes is half a
+// 128-byte line (dim 128), so nearly every line is read: 16 x 4096 of 8192
+// tokens, 8 heads of 128, INT4-asym g32 36.6 us, 86 MB written and up to twice
+// that read, 7 TB/s.
 #include <algorithm>
 
 #include "kv_common.hpp"
@@ -23,6 +31,11 @@ namespace {
 constexpr int kSel = 1024;
 constexpr int kSelFew = 256;
 constexpr int kMove = 256;
+// Rows a lane moves, and from how many 16-byte pieces on (16 x 4096 kept tokens
+// of 8 heads of 128: 1, 2, 4 rows 39.5, 36.6, 38.1 us; fewer pieces leave units
+// without work).
+constexpr int kRowsMany = 2;
+constexpr int64_t kManyPieces = 1 << 19;
 
 // Masses as integers of the same order; NaN below everything.
 __device__ __forceinline__ uint32_t mass_key(float f)
@@ -189,52 +202,105 @@ __global__ __launch_bounds__(SEL) void kv_select_kernel(KvCache c, KvBatch b, co
     });
 }
 
-// N bytes, by the widest accesses that their alignment in an array of N-byte
-// rows allows.
+// N bytes of an array of N-byte rows, by the widest accesses that their
+// alignment allows.
 template <int N>
-__device__ __forceinline__ void copy_bytes(uint8_t *to, const uint8_t *from)
-{
-    if constexpr (N % 16 == 0) {
+struct Bytes {
+    uint32_t w[(N + 3) / 4];
+    __device__ __forceinline__ void load(const uint8_t *from)
+    {
+        if constexpr (N % 16 == 0) {
 #pragma unroll
-        for (int i = 0; i < N / 16; ++i)
-            ((u32x4 *)to)[i] = ((const u32x4 *)from)[i];
-    } else if constexpr (N == 8) {
-        *(u32x2 *)to = *(const u32x2 *)from;
-    } else if constexpr (N == 4) {
-        *(uint32_t *)to = *(const uint32_t *)from;
-    } else if constexpr (N == 2) {
-        *(uint16_t *)to = *(const uint16_t *)from;
-    } else if constexpr (N == 1) {
-        *to = *from;
+            for (int i = 0; i < N / 16; ++i) {
+                const u32x4 v = ((const u32x4 *)from)[i];
+                w[4 * i] = v[0], w[4 * i + 1] = v[1], w[4 * i + 2] = v[2], w[4 * i + 3] = v[3];
+            }
+        } else if constexpr (N == 8) {
+            const u32x2 v = *(const u32x2 *)from;
+            w[0] = v[0], w[1] = v[1];
+        } else if constexpr (N == 4) {
+            w[0] = *(const uint32_t *)from;
+        } else if constexpr (N == 2) {
+            w[0] = *(const uint16_t *)from;
+        } else {
+            static_assert(N == 1, "rows of 1, 2, 4, 8 or a multiple of 16 bytes");
+            w[0] = *from;
+        }
     }
-}
+    __device__ __forceinline__ void store(uint8_t *to) const
+    {
+        if constexpr (N % 16 == 0) {
+#pragma unroll
+            for (int i = 0; i < N / 16; ++i)
+                ((u32x4 *)to)[i] = u32x4{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
+        } else if constexpr (N == 8) {
+            *(u32x2 *)to = u32x2{w[0], w[1]};
+        } else if constexpr (N == 4) {
+            *(uint32_t *)to = w[0];
+        } else if constexpr (N == 2) {
+            *(uint16_t *)to = (uint16_t)w[0];
+        } else {
+            *to = (uint8_t)w[0];
+        }
+    }
+};
 
-// SB: bytes of scales a row, ZB: of zero-points.
-template <int D, int SB, int ZB>
+// SB: bytes of scales a row, ZB: of zero-points; U rows a lane, their loads
+// (token, pages, row) in flight together.  A place without a token or a page
+// reads row 0 of the pool and stores nothing.
+template <int D, int SB, int ZB, int U>
 __global__ __launch_bounds__(kMove) void kv_move_kernel(KvCache c, KvBatch b, const int32_t *__restrict__ new_table,
                                                         int new_tw, int budget, const int32_t *__restrict__ kept)
 {
     constexpr int LANES = D / 32;  // 16 bytes of codes a lane
     const int h = blockIdx.y, seq = blockIdx.z;
-    const int64_t item = (int64_t)blockIdx.x * kMove + threadIdx.x;
-    const int chunk = (int)(item % LANES);
-    const int64_t place = item / LANES;
-    if (place >= budget)
-        return;
-    const int t = kept[((int64_t)seq * c.heads + h) * budget + place];
-    if (t < 0)
-        return;
-    const int64_t src = kv_row(c, b.table + (int64_t)seq * b.table_width, t, h);
-    const int64_t dst = kv_row(c, new_table + (int64_t)seq * new_tw, (int)place, h);
-    if (src < 0 || dst < 0)
-        return;
-    copy_bytes<16>(c.k.codes + dst * (D / 2) + 16 * chunk, c.k.codes + src * (D / 2) + 16 * chunk);
-    copy_bytes<16>(c.v.codes + dst * (D / 2) + 16 * chunk, c.v.codes + src * (D / 2) + 16 * chunk);
-    if (chunk < 2) {
-        const KvHalf &x = chunk ? c.v : c.k;
-        copy_bytes<SB>((uint8_t *)x.scales + dst * SB, (const uint8_t *)x.scales + src * SB);
-        if constexpr (ZB > 0)
-            copy_bytes<ZB>(x.zeros + dst * ZB, x.zeros + src * ZB);
+    const int chunk = threadIdx.x % LANES;
+    const int64_t place0 = ((int64_t)blockIdx.x * U * kMove + threadIdx.x) / LANES;
+    const int32_t *from = kept + ((int64_t)seq * c.heads + h) * budget;
+    const int32_t *table = b.table + (int64_t)seq * b.table_width, *ntable = new_table + (int64_t)seq * new_tw;
+    int t[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t place = place0 + u * (kMove / LANES);
+        t[u] = from[min(place, (int64_t)budget - 1)];
+        if (place >= budget)
+            t[u] = -1;
+    }
+    int64_t src[U], dst[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int place = t[u] < 0 ? 0 : (int)(place0 + u * (kMove / LANES));
+        src[u] = kv_row(c, table, max(t[u], 0), h);
+        dst[u] = kv_row(c, ntable, place, h);
+        if (t[u] < 0 || src[u] < 0)
+            dst[u] = -1;
+        src[u] = max(src[u], (int64_t)0);
+    }
+    const KvHalf &x = chunk & 1 ? c.v : c.k;  // whose scales the lane moves
+    Bytes<16> k[U], v[U];
+    Bytes<SB> sc[U];
+    Bytes<ZB ? ZB : 1> z[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        k[u].load(c.k.codes + src[u] * (D / 2) + 16 * chunk);
+        v[u].load(c.v.codes + src[u] * (D / 2) + 16 * chunk);
+        if (chunk < 2) {
+            sc[u].load((const uint8_t *)x.scales + src[u] * SB);
+            if constexpr (ZB > 0)
+                z[u].load(x.zeros + src[u] * ZB);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (dst[u] < 0)
+            continue;
+        k[u].store(c.k.codes + dst[u] * (D / 2) + 16 * chunk);
+        v[u].store(c.v.codes + dst[u] * (D / 2) + 16 * chunk);
+        if (chunk < 2) {
+            sc[u].store((uint8_t *)x.scales + dst[u] * SB);
+            if constexpr (ZB > 0)
+                z[u].store(x.zeros + dst[u] * ZB);
+        }
     }
 }
 
@@ -243,8 +309,12 @@ void move(const KvCache &c, const KvBatch &b, const int32_t *new_table, int new_
           hipStream_t s)
 {
     const int64_t items = (int64_t)budget * (D / 32);
-    kv_move_kernel<D, SB, ZB><<<dim3((unsigned)((items + kMove - 1) / kMove), c.heads, b.seqs), kMove, 0, s>>>(
-        c, b, new_table, new_tw, budget, kept);
+    auto go = [&](auto rows) {
+        constexpr int U = decltype(rows)::value;
+        const unsigned wgs = (unsigned)((items + U * kMove - 1) / (U * kMove));
+        kv_move_kernel<D, SB, ZB, U><<<dim3(wgs, c.heads, b.seqs), kMove, 0, s>>>(c, b, new_table, new_tw, budget, kept);
+    };
+    items * c.heads * b.seqs >= kManyPieces ? go(KvInt<kRowsMany>{}) : go(KvInt<1>{});
 }
 
 }  // namespace

@@ -109,6 +109,36 @@ def test_append(fmt, dim, g, act):
         assert bool(same[~written].all())
 
 
+@pytest.mark.parametrize("fmt,dim,g", [(q4.INT4_SYM, 128, 128), (q4.INT4_ASYM, 64, 32), (q4.NF4, 256, 64), (q4.FP4, 128, 32)])
+def test_many_rows_are_as_few(fmt, dim, g):
+    """One call of many tokens stores and reads the bits that calls of few do, pages that are missing included."""
+    rng = np.random.default_rng(fmt)
+    heads, page, lens = 8, 16, [1024 * 256 // dim + 5, 700 * 256 // dim + 9]
+    many, table = fresh_cache(fmt, g, dim, heads, page, lens, seed=5)
+    few, _ = fresh_cache(fmt, g, dim, heads, page, lens, seed=5)
+    table[0, 3], table[1, 0] = -1, many.pages   # no such pages: nothing is stored, zeros are read
+    tab = torch.from_numpy(table.astype(np.int32)).to(DEV)
+    T = sum(lens)
+    k, v = (torch.from_numpy(rng.standard_normal((T, heads, dim)).astype(np.float32)).to(torch.bfloat16).to(DEV) for _ in range(2))
+
+    def batch(upto, new):
+        starts = torch.tensor([0, new[0], sum(new)], dtype=torch.int32, device=DEV)
+        return kv.Batch(tab, torch.tensor(upto, dtype=torch.int32, device=DEV), starts, tokens=sum(new), max_new=max(new))
+
+    kv.append(many, batch(lens, lens), k, v)
+    got = kv.read(many, batch(lens, lens), torch.bfloat16)
+    at, ends = [0, 0], [0, lens[0]]
+    while at != lens:
+        new = [min(200, n - a) for n, a in zip(lens, at)]
+        rows = torch.cat([torch.arange(e + a, e + a + n) for e, a, n in zip(ends, at, new)]).to(DEV)
+        at = [a + n for a, n in zip(at, new)]
+        kv.append(few, batch(at, new), k[rows], v[rows])
+        for x, y in zip(got, kv.read(few, batch(at, new), torch.bfloat16)):
+            assert torch.equal(x[rows].view(torch.int16), y.view(torch.int16))
+    for a, b in zip(snapshot(many), snapshot(few)):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_append_tokens_one_by_one(fmt):
     """A sequence grown token by token holds what one prompt of it holds."""
@@ -240,6 +270,15 @@ def test_evict(fmt, dim, g):
                                                 ([9000, 70], 2500, 17), ([33000], 16000, 1000)])
 def test_evict_sizes(lens, budget, recent):
     run_evict(q4.INT4_ASYM, 64, 32, 2, 64, lens, budget, recent, seed=budget)
+
+
+@pytest.mark.parametrize("fmt", [q4.INT4_ASYM, q4.NF4])
+def test_evict_many_rows(fmt):
+    run_evict(fmt, 256, 64, 8, 64, [5000, 4500], 4096, 64, seed=fmt)
+
+
+def test_evict_many_keys_a_thread():
+    run_evict(q4.FP4, 64, 64, 2, 128, [20000, 17000], 9000, 33, seed=2, masses=lambda rng, shape: rng.integers(0, 9000, shape).astype(np.float32))
 
 
 def _ties(rng, shape):
