@@ -10,13 +10,16 @@
 //
 //  * Up to 8 rows: the attention kept the scores, in binary32; this pass only
 //    reads them (kv_mass_kept_kernel).
-//  * Few rows (as kv_token.hip takes), else: the rows stay in registers and a wave walks
-//    over 64-token blocks of a span.  Bound as kv_token.hip.
+//  * Few rows (as kv_token.hip takes), else: the rows stay in registers and a
+//    wave walks over 64-token blocks of a span.  Bound as kv_token.hip.
 //  * Many rows: 64 tokens' keys stay in registers, unpacked once, and the rows
 //    pass by as operands that a first launch laid out (kv_rows_kernel), with
 //    their factors and statistics.  The four waves of a workgroup hold 256
 //    tokens and read the same rows, from the L1.  Bound by vector-ALU issue:
-//    a score costs its groups' scales, an fma, exp2 at a quarter rate, a sum.
+//    a score costs its groups' scales, an fma, exp2 at a quarter rate, a sum:
+//    at 8 issue slots with two groups, 220 us for the 1.05e9 visible scores of
+//    1024 new tokens after 31744 (8 heads of 4 rows, dim 128, g 64), which take
+//    294 to 314 us; 32 x 4096 tokens of kept scores take 6 us.
 #include "kv_attn.hpp"
 
 namespace q4 {

@@ -27,7 +27,15 @@
 //    was 2.5 times as far from binary64).
 //
 // Bound: HBM traffic of the packed rows in the limit; in practice the rate at
-// which lanes receive their words (texture path) and vector-ALU issue.
+// which lanes receive their words (the texture path takes some 16 cycles an
+// instruction, whatever its width, hence 16-byte loads of whole rows handed on
+// through LDS) and vector-ALU issue, each busy for half to two thirds of the
+// time.  Nothing is read twice.  One new token a sequence, dim 128:
+//   2 x 131071 tokens, 8 heads, 4 rows, INT4-asym g32   60 us + 5 to join, 4.3 TB/s
+//   32 x 4096, 8 heads, 4 rows, INT4-sym g64, scores kept   35 us + 4 to 6
+//   16 x 2048, 32 heads, 1 row, NF4 g64                 35 us, 3.4 TB/s (level
+//     lookups: LDS busy half the time, with conflicts; levels by v_perm 39 us)
+//   333 tokens, 8 heads                                  8 us, of which a launch 2.5
 //
 // Split: a workgroup's four waves take 32-token steps of one range of one
 // sequence and head in turn and join their sums in LDS; where sequences and

@@ -42,7 +42,7 @@ def _tensor(t, name, dtype, shape=None, device=None):
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
@@ -276,9 +276,9 @@ def evict(cache, batch, mass, new_table, budget, recent, *, width=None):
         raise q4.Q4Error(q4.EINVAL, "q4_kv_evict")
     if width is None:
         width = new_table.shape[1] * cache.page
-    new_lens = torch.empty((batch.seqs,), dtype=torch.int32, device=cache.device)
-    new_mass = torch.empty((batch.seqs, cache.heads, width), dtype=torch.float32, device=cache.device)
-    kept = torch.empty((batch.seqs, cache.heads, budget), dtype=torch.int32, device=cache.device)
+    new_lens = torch.empty_like(batch.lens)
+    new_mass = mass.new_empty((batch.seqs, cache.heads, width))
+    kept = new_lens.new_empty((batch.seqs, cache.heads, budget))
     st = lib().q4_kv_evict(cache._ref, ref, mass.data_ptr(), mass.shape[2], new_table.data_ptr(),
                            new_table.shape[1], budget, recent, new_lens.data_ptr(), new_mass.data_ptr(),
                            width, kept.data_ptr(), cache._stream())
