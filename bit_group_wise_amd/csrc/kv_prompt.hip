@@ -8,27 +8,31 @@
 //
 //  * Keys lie there as exact fp16 levels less zero-points, their scales beside
 //    them in binary32; a score is sum_j s_j acc_j as before.
-//  * Values lie there as fp16(level * s_t 2^-E), one rounding of the cached
-//    value, where 2^E bounds the scales of the tokens that one wave stages: E
-//    is added to those tokens' scores, which puts it into the weights, and
-//    taken off the row sums again.  So neither weights (at most 2^15.5) nor
-//    values (at most 15, 1 for tables) leave fp16, whatever the cache's
-//    magnitude.  (The reference puts the largest weight at 2^11: it moves
-//    rarely, and weights down to 2^-25 of the largest keep all their bits.)
+//  * Values lie there as fp16(level * s_tj 2^-E_t), one rounding of the cached
+//    value.  E_t puts a token's largest scale just below 2^12: it is added to
+//    the token's score, which puts it into the weight, and taken off the row
+//    sum again.  So a row meets a token's size only in what it sees of it (a
+//    size shared by several tokens would let one that a row does not see take
+//    the others' bits), and neither weights (at most 2^15.5) nor values (at
+//    most 61440) leave fp16: groups down to 2^-21 of their token's largest
+//    keep all their bits.  (The reference puts the largest weight at 2^11: it
+//    moves rarely, and weights down to 2^-25 of the largest are exact to fp16's
+//    11 bits.)
 //  * LDS holds operands as the lanes read them, 16 bytes a lane in a row, in
 //    two buffers: the next tile is fetched while one is worked on, one barrier
 //    a tile.  Rows of V operands are values d = 8 i + j of the dword i that a
 //    staging lane unpacked, so both its writes and a result's stores are
 //    contiguous.
 //
-// Bound: vector-ALU issue.  A score costs about ten issue slots (its groups'
-// scales, maximum, the exponent's fma, exp2 at a quarter rate, sum, rounding)
+// Bound: vector-ALU issue.  A score costs about eleven issue slots (its groups'
+// scales, the exponent's fma, maximum, reference, exp2 at a quarter rate, sum,
+// rounding; one size a wave's tokens would save one: 110 us where this takes 115)
 // against 4 D / 1024 of matrix time; tiles are 64 tokens (dim 128) by 16 NT
 // rows a wave, eight waves, so that a row pays little of the unpacking.  The
 // vector ALUs are busy 60 % of the time, the matrix cores 33 %; the rest is the
 // barrier a tile and the staging waves' wait for their loads.  dim 128, g 64:
-//   2 x 2048 new tokens, 32 heads, causal, INT4-sym       110 us, 610 TFLOP/s
-//   1024 after 31744, 8 heads of 4 rows, INT4-asym        640 us, 845 TFLOP/s
+//   2 x 2048 new tokens, 32 heads, causal, INT4-sym       115 us, 588 TFLOP/s
+//   1024 after 31744, 8 heads of 4 rows, INT4-asym        675 us, 800 TFLOP/s
 #include "kv_attn.hpp"
 
 namespace q4 {
@@ -72,18 +76,20 @@ __device__ __forceinline__ int operand_slot(int i, int j)  // (n * 64 + rho)
         return (j + 8 * (i >> 4)) * 64 + (i & 15);
 }
 
-// The largest of a wave's numbers, none negative (as integers they compare
-// alike): rotations within 16 lanes, then the four rows as scalars.
-__device__ __forceinline__ float wave_max(float v)
+// The largest scale of a token, its D / 8 staging lanes holding their group's
+// (those of a group alike; none is negative, so as integers they compare the
+// same): mirrored in 8 lanes, rotated by 8 in 16, and across 16.
+template <int D, int GS>
+__device__ __forceinline__ float token_max(float v)
 {
     int u = std::bit_cast<int>(v);
-    u = max(u, __builtin_amdgcn_update_dpp(0, u, 0x128, 0xf, 0xf, true));
-    u = max(u, __builtin_amdgcn_update_dpp(0, u, 0x124, 0xf, 0xf, true));
-    u = max(u, __builtin_amdgcn_update_dpp(0, u, 0x122, 0xf, 0xf, true));
-    u = max(u, __builtin_amdgcn_update_dpp(0, u, 0x121, 0xf, 0xf, true));
-    const int a = max(__builtin_amdgcn_readlane(u, 0), __builtin_amdgcn_readlane(u, 16));
-    const int b = max(__builtin_amdgcn_readlane(u, 32), __builtin_amdgcn_readlane(u, 48));
-    return std::bit_cast<float>(max(a, b));
+    if constexpr (GS == 32)
+        u = max(u, __builtin_amdgcn_update_dpp(0, u, 0x141, 0xf, 0xf, true));
+    if constexpr (GS <= 64 && D >= 128)
+        u = max(u, __builtin_amdgcn_update_dpp(0, u, 0x128, 0xf, 0xf, true));
+    if constexpr (D == 256)
+        u = max(u, __shfl_xor(u, 16));
+    return std::bit_cast<float>(u);
 }
 
 // A staging lane's share of a tile as it is in memory: 32 keys of a token (the
@@ -104,8 +110,6 @@ struct Fetch {
         const int p = u / ND;  // tt | kg << 1 | tb << 3
         return (p >> 3) * 8 + (p & 1) * 4 + ((p >> 1) & 3);
     }
-    // The wave of value stagers that holds the tokens of step tb in lanes kg.
-    static __device__ __forceinline__ int v_wave(int tb, int kg) { return (8 * tb + 2 * kg) * ND / 64; }
 
     int64_t r;    // the row of the tile to load next
     bool in;      // which is there
@@ -156,7 +160,7 @@ struct Stage {
     u32x2 v[TT * D / 4];        // [32 tokens][D / 16] operands, halves of lanes
     float ks[NG][TT];
     uint32_t valid[TT / 32];
-    float e[4];                 // by v_wave
+    float e[TT], down[TT];      // E_t, and 2^-E_t
 };
 
 template <int FMT, int D, int GS>
@@ -182,22 +186,26 @@ __device__ __forceinline__ void stage(Stage<FMT, D, GS> &st, const Fetch<FMT, D,
         return;
     }
     // values: four tokens' eight, scaled by 2^-E, then by value
-    float s[4], top = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        s[e] = f.ok >> e & 1 ? scale_of<FMT>(f.s[e]) : 0.0f;
-        top = fmaxf(top, s[e]);
-    }
-    top = wave_max(top);
-    const int e2 = min(max(__builtin_amdgcn_frexp_expf(fmaxf(top, 0x1p-40f)), -40), 100);
-    const float down = __builtin_amdgcn_ldexpf(1.0f, -e2);
-    if (lane == 0)
-        st.e[wave - 4] = (float)e2;
     const int i = F::v_dword(u), qd = F::v_quad(u), j = 8 * i / GS;
+    float s[4];
+    f32x4 e, down;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        s[t] = f.ok >> t & 1 ? scale_of<FMT>(f.s[t]) : 0.0f;
+        // (2^-40: a token of zeros has a weight in the row sum all the same,
+        // which must not vanish beside large ones)
+        const int e2 = min(max(__builtin_amdgcn_frexp_expf(fmaxf(token_max<D, GS>(s[t]), 0x1p-40f)), -40), 100) - 12;
+        e[t] = (float)e2;
+        down[t] = __builtin_amdgcn_ldexpf(1.0f, -e2);
+        s[t] *= down[t];
+    }
+    if (i == 0) {
+        *(f32x4 *)&st.e[4 * qd] = e;
+        *(f32x4 *)&st.down[4 * qd] = down;
+    }
     uint32_t x[4][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-        s[t] *= down;
         const u32x4 a = key_operand<FMT>(
             f.w[t], key_zero(FMT == Q4_INT4_ASYM ? (f.z[t] >> (4 * (j & 1))) & 15u : 8u), pairs);
         if constexpr (kv_int<FMT>()) {
@@ -318,12 +326,11 @@ __global__ __launch_bounds__(kBlock, (NT < most_nt<D>() ? 4 : 2)) void kv_prompt
             if (t1 > any_to || t1 + 32 * TB - 1 < any_from)
                 continue;
             uint32_t valid[TB];
-            float e[TB], x[TB][NT][8];
+            float x[TB][NT][8];
             bool whole = t1 + 32 * TB - 1 <= all_to && t1 >= all_from;
 #pragma unroll
             for (int b2 = 0; b2 < TB; ++b2) {
                 valid[b2] = __builtin_amdgcn_readfirstlane(S.valid[tb + b2]);
-                e[b2] = S.e[Fetch<FMT, D, GS>::v_wave(tb + b2, kg)];
                 whole = whole && valid[b2] == ~0u;
             }
             // An LDS read takes about as long as ten products: operands are
@@ -388,18 +395,23 @@ __global__ __launch_bounds__(kBlock, (NT < most_nt<D>() ? 4 : 2)) void kv_prompt
             float reach[NT];
             bool move = false;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
+            for (int b2 = 0; b2 < TB; ++b2) {
+                const f32x4 e[2] = {*(const f32x4 *)&S.e[32 * (tb + b2) + 4 * kg],
+                                    *(const f32x4 *)&S.e[32 * (tb + b2) + 16 + 4 * kg]};
 #pragma unroll
-                for (int b2 = 0; b2 < TB; ++b2) {
-                    float top = x[b2][n][0];
+                for (int n = 0; n < NT; ++n) {
+                    float top = b2 ? reach[n] : -__builtin_inff();
 #pragma unroll
-                    for (int k = 1; k < 8; ++k)
+                    for (int k = 0; k < 8; ++k) {
+                        x[b2][n][k] = __builtin_fmaf(x[b2][n][k], q[n].factor, e[k >> 2][k & 3]);
                         top = fmaxf(top, x[b2][n][k]);
-                    const float to = __builtin_fmaf(top, q[n].factor, e[b2]);
-                    reach[n] = b2 ? fmaxf(reach[n], to) : to;
+                    }
+                    reach[n] = top;
                 }
-                move = move || reach[n] > m[n] + 15.5f;
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                move = move || reach[n] > m[n] + 15.5f;
             if (__builtin_expect(__any(move), 0)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -414,18 +426,18 @@ __global__ __launch_bounds__(kBlock, (NT < most_nt<D>() ? 4 : 2)) void kv_prompt
             }
 #pragma unroll
             for (int b2 = 0; b2 < TB; ++b2) {
-                const float inv_e = __builtin_amdgcn_ldexpf(1.0f, -(int)e[b2]);
+                const f32x4 down[2] = {*(const f32x4 *)&S.down[32 * (tb + b2) + 4 * kg],
+                                       *(const f32x4 *)&S.down[32 * (tb + b2) + 16 + 4 * kg]};
                 u32x4 w[NT];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float off = e[b2] - m[n];
                     float sum = 0.0f, p[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        p[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[b2][n][k], q[n].factor, off));
-                        sum += p[k];
+                        p[k] = __builtin_amdgcn_exp2f(x[b2][n][k] - m[n]);
+                        sum = __builtin_fmaf(p[k], down[k >> 2][k & 3], sum);
                     }
-                    l[n] = __builtin_fmaf(sum, inv_e, l[n]);
+                    l[n] += sum;
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         w[n][k] = pair_h2(p[2 * k], p[2 * k + 1]);
