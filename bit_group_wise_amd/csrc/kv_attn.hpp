@@ -19,6 +19,11 @@ __device__ __forceinline__ int branch_only(int v)
     asm volatile("" : "+s"(v));
     return v;
 }
+__device__ __forceinline__ uint32_t branch_only_lane(uint32_t v)  // the same, a value a lane
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
 
 // Where a launch puts a row's result.
 struct Rows {
@@ -280,6 +285,19 @@ struct Scales4 {
             else
                 w[r >> 1] = r < n ? w[r >> 1] : w[r >> 1] & (r & 1 ? 0x0000ffffu : 0xffff0000u);
         }
+    }
+    // The same, converted to binary32 in the branch that asks for them.
+    __device__ __forceinline__ Scales4 branch_only() const
+    {
+        Scales4 s;
+#pragma unroll
+        for (int i = 0; i < (f32_absmax(FMT) ? 4 : 2); ++i)
+            s.w[i] = branch_only_lane(w[i]);
+        return s;
+    }
+    __device__ __forceinline__ float smallest() const
+    {
+        return fminf(fminf((*this)[0], (*this)[1]), fminf((*this)[2], (*this)[3]));
     }
     __device__ __forceinline__ float largest() const  // (no scale is negative)
     {

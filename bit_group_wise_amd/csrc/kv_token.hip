@@ -27,7 +27,11 @@
 //    and is then set to put the largest at 2^13.5, so that a weight has fp16's
 //    full 11 bits down to 2^-27 of the largest (in long caches most of the sum
 //    is in weights far below it; with the largest at 2^6 the 131071-token case
-//    was 2.5 times as far from binary64).
+//    was 2.5 times as far from binary64).  That it may have to move is seen from
+//    a bound (the largest score and the largest scale of eight tokens); where
+//    their scales differ by more than 2^4, it moves to the largest sum of a
+//    token's own two, so large values of tokens that the row does not see, or
+//    hardly weighs, take no more bits than that of the others'.
 //
 // Bound: HBM traffic of the packed rows in the limit; in practice the rate at
 // which lanes receive their words (the texture path takes some 16 cycles an
@@ -255,6 +259,25 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
             move = move || reach[n] > m[n] + 15.5f;
         }
         if (__builtin_expect(__any(move), 0)) {
+            // (the bound does where the eight tokens' scales are within 2^4)
+            const Scales4<FMT> s0 = vs[0].branch_only(), s1 = vs[1].branch_only();
+            const float least = group_max<NG>(fminf(s0.smallest(), s1.smallest()));
+            if (__any(!(__builtin_amdgcn_logf(least) >= big - 4.0f))) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    reach[n] = -__builtin_inff();
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const Scales4<FMT> here = (u ? s1 : s0).branch_only();
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float size = __builtin_amdgcn_logf(fmaxf(group_max<NG>(here[r]), 0x1p-40f));
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            reach[n] = fmaxf(reach[n], __builtin_fmaf(x[u][n][r], q.factor[n], size));
+                    }
+                }
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float to = fmaxf(m[n], quad_max(reach[n]) - 13.5f);

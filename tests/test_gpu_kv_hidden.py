@@ -5,7 +5,7 @@ Every row is held to what that row sees.  Tolerances, from the arithmetic:
 scores and softmax weights as in test_gpu_kv_attention (relative error 2 delta
 + 2^-18 of a weight, delta of the row's own scores); a weight and a value are
 each rounded once to fp16 (2^-11 each), the result once to the output's type.
-A row's largest product of weight and scale is held at 2^11 or more, values at
+A row's largest product of weight and scale is held at 2^9 or more, values at
 2^11 or more for the largest scale of their token, so what fp16's subnormals
 lose (2^-25 each) is less than 2^-31 of the row's largest product of weight
 and scale a token, at 16 levels 2^-27 times that; groups down to 2^-14 of
@@ -20,7 +20,7 @@ from _kv import DEV, FMTS, TORCH, UNIT, Pool, row_values
 
 pytestmark = pytest.mark.gpu
 TABLES = [q4.NF4, q4.FP4]
-KINDS = ["prompt"]
+KINDS = ["prompt", "few"]
 
 
 def set_scales(pool, half, b, scales):
