@@ -9,7 +9,8 @@
 // the first ones, as many as are missing.  A workgroup's threads hold runs of
 // consecutive tokens, so two running counts over the threads give every kept
 // token's place.  Counting needs no atomics: a wave counts by ballot, and the
-// waves' counts meet in LDS.
+// waves' counts meet in LDS.  Tokens whose page does not exist are not there:
+// they are no candidates, and the recent ones are the last that are.
 //
 // Bound: latency.  A pass over the candidates is some 500 cycles of ballots, a
 // barrier and the exchange in LDS, whatever the length: 12 us for 1088 tokens
@@ -77,34 +78,84 @@ __global__ __launch_bounds__(SEL) void kv_select_kernel(KvCache c, KvBatch b, co
                                                          int64_t new_width, int32_t *__restrict__ kept, int per)
 {
     constexpr int WAVES = SEL / 64;
-    __shared__ int counts[2][3][16], wsum[2][WAVES];
+    __shared__ int counts[2][3][16], wsum[3][WAVES], gone[WAVES], first_recent;
     const int h = blockIdx.x, seq = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int len = min(max(b.lens[seq], 0), b.max_len);
     const int64_t rowid = (int64_t)seq * c.heads + h;
     const float *m = mass + rowid * width;
     float *mo = new_mass + rowid * new_width;
     int32_t *ko = kept + rowid * budget;
-    const int n = min(len, budget);
+    int n = min(len, budget), old = len - recent;  // tokens from `old` on are recent
+    const int t0 = per * tid;
+    // keys of the thread's tokens; 0, which no candidate value is, where there
+    // is no old token.  Bit i of `here`: token i of the thread is there.
+    uint32_t key[HELD ? HELD : 1], here = 0;
+    if constexpr (HELD) {
+#pragma unroll
+        for (int i = 0; i < HELD; ++i)
+            key[i] = i < per && t0 + i < old ? mass_key(m[t0 + i]) : 0u;
+        const int mine = min(max(len - t0, 0), per);
+        here = mine >= 32 ? ~0u : (1u << mine) - 1;
+    }
+    // whether any page of the sequence is missing
+    const int32_t *table = b.table + (int64_t)seq * b.table_width;
+    bool miss = false;
+    for (int p = tid; p < (len + (1 << c.page_shift) - 1) >> c.page_shift; p += SEL)
+        miss = miss || (unsigned)table[p] >= (unsigned)c.pages;
+    miss = __any(miss);
+    if (lane == 0)
+        gone[wave] = miss;
+    __syncthreads();
+    const bool holes = __any(gone[min(lane, WAVES - 1)] != 0);
+    auto there = [&](int t) { return t < len && (!holes || (unsigned)table[t >> c.page_shift] < (unsigned)c.pages); };
+    if (holes) {
+        int mine = 0;
+        for (int i = 0; i < per; ++i)
+            mine += there(t0 + i);
+        int rank = block_before<WAVES>(mine, wsum[2]), all = 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w)
+            all += wsum[2][w];
+        n = min(all, budget);
+        if (tid == 0)
+            first_recent = len;
+        __syncthreads();
+        // (all that are there stay where they do not exceed the budget)
+        const int first = all <= budget ? 0 : all - recent;
+        for (int i = 0; i < per; ++i)
+            if (there(t0 + i) && rank++ == first)
+                first_recent = t0 + i;
+        __syncthreads();
+        old = all <= budget ? 0 : first_recent;
+        for (int i = n + tid; i < budget; i += SEL)
+            ko[i] = -1;
+        if constexpr (HELD) {
+            for (int i = 0; i < per; ++i)
+                if (!there(t0 + i))
+                    here &= ~(1u << i);
+#pragma unroll
+            for (int i = 0; i < HELD; ++i)
+                key[i] = (here >> i & 1) && t0 + i < old ? mass_key(m[t0 + i]) : 0u;
+        }
+    }
     if (h == 0 && tid == 0)
         new_lens[seq] = n;
     for (int64_t i = n + tid; i < new_width; i += SEL)
         mo[i] = 0.0f;
-    if (len <= budget) {
+    if (len <= budget && !holes) {
         for (int i = tid; i < n; i += SEL)
             mo[i] = m[i];
         for (int i = tid; i < budget; i += SEL)
             ko[i] = i < n ? i : -1;
         return;
     }
-    const int old = len - recent, want = budget - recent;  // want < old
-    const int t0 = per * tid;
-    // keys of the thread's tokens; 0, which no candidate is, past the old ones
-    uint32_t key[HELD ? HELD : 1];
-    if constexpr (HELD) {
-#pragma unroll
-        for (int i = 0; i < HELD; ++i)
-            key[i] = i < per && t0 + i < old ? mass_key(m[t0 + i]) : 0u;
-    }
+    const int want = old == 0 ? 0 : budget - recent;  // of the tokens before `old`, fewer than they are
+    auto stands = [&](int i) -> bool {
+        if constexpr (HELD)
+            return here >> i & 1;
+        else
+            return there(t0 + i);
+    };
     uint32_t T = 0;
     int above = 0;  // keys above T
     for (int shift = 30; shift >= 0; shift -= 2) {
@@ -121,7 +172,7 @@ __global__ __launch_bounds__(SEL) void kv_select_kernel(KvCache c, KvBatch b, co
         } else {
             // (in strides here: no order is needed to count)
             for (int t = tid; t < per * SEL; t += SEL)
-                count(t < old ? mass_key(m[t]) : 0u);
+                count(t < old && there(t) ? mass_key(m[t]) : 0u);
         }
         int(&to)[3][16] = counts[(shift >> 1) & 1];
         if (lane < 3)
@@ -170,11 +221,11 @@ __global__ __launch_bounds__(SEL) void kv_select_kernel(KvCache c, KvBatch b, co
                 fn(i);
         }
     };
-    each([&](int i) { ties += t0 + i < old && key_at(i) == T; });
+    each([&](int i) { ties += t0 + i < old && stands(i) && key_at(i) == T; });
     int tie = block_before<WAVES>(ties, wsum[0]);
     auto stays = [&](int i) -> bool {  // in order of i, once
         const int t = t0 + i;
-        if (t >= len)
+        if (!stands(i))
             return false;
         if (t >= old)
             return true;

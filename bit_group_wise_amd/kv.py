@@ -260,9 +260,10 @@ def attention(cache, batch, q, *, scale=None, window=0, mass=None, lse=None, out
 
 def evict(cache, batch, mass, new_table, budget, recent, *, width=None):
     """Keep `budget` tokens of every sequence and head that has more: the last
-    `recent` and the heaviest others by mass (q4_kv_evict).  They move to the
-    pages that new_table [seqs, new_width] names, free pages of this pool.
-    Returns (new_lens [seqs], new_mass [seqs, heads, width], kept [seqs, heads,
+    `recent` and the heaviest others by mass (q4_kv_evict; tokens on pages that
+    do not exist neither stay nor count).  They move to the pages that
+    new_table [seqs, new_width] names, free pages of this pool.  Returns
+    (new_lens [seqs], new_mass [seqs, heads, width], kept [seqs, heads,
     budget]); width defaults to what new_table can hold."""
     torch = _torch()
     ref = batch._ref(cache)

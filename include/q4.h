@@ -362,15 +362,18 @@ q4_status q4_kv_attention(const q4_kv_cache *cache, const q4_kv_batch *batch, q4
                           size_t workspace_bytes, void *stream);
 
 /* Eviction by accumulated attention weight.  Per sequence and head, the tokens
- * that stay are: all of them if lens[b] <= budget; otherwise the last
+ * that stay are: all of them if they are at most `budget`; otherwise the last
  * `recent` tokens and the budget - recent others of largest mass (equal
- * masses: the earlier token; NaN counts below every number).  They move, in
+ * masses: the earlier token; NaN counts below every number).  Tokens whose
+ * page number is outside the pool are not there: they never stay, and none of
+ * these counts takes them in.  The tokens that stay move, in
  * token order, to slots 0, 1, ... of the pages new_table names, with their
  * mass; codes, scales and zero-points are copied as they are.
  * batch: table, lens, seqs and max_len are used; starts, tokens and max_new
  * are not.  new_table [seqs, new_table_width] names pages of the same pool,
  * none of them in use by the sequences that are read.  0 <= recent <= budget.
- *   new_lens int32 [seqs]: min(lens[b], budget)
+ *   new_lens int32 [seqs]: the number of tokens that stay (in every head the
+ *            same): min(lens[b], budget), where all pages exist
  *   new_mass float32 [seqs, heads, new_width], new_width >= budget: the kept
  *            tokens' masses, then zeros; not overlapping mass
  *   kept     int32 [seqs, heads, budget]: the kept tokens' positions, then -1 */
