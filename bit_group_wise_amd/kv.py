@@ -2,7 +2,9 @@
 
 A `KVCache` is the pool of pages, a `Batch` says which sequences a call works
 on and where their new tokens are.  Both are thin handles over device tensors
-that the caller owns and may update in place (lens, table) between calls:
+that the caller owns and may update in place (lens, table) between calls; a
+Batch's fields may also be assigned, and one Batch serves the caches of all
+layers:
 
     cache = kv.alloc_cache(q4.INT4_SYM, 64, pages=512, page=64, heads=8, dim=128, device="cuda:0")
     step = kv.Batch(table, lens)                    # one new token a sequence
@@ -88,6 +90,13 @@ class KVCache:
                                   (k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros)),
                                 pages, page, heads, dim, g, fmt, 0)
         self._ref = ctypes.addressof(self._args)
+        self._key = (dev.index, fmt, g, page, heads, dim)  # what a batch's record and workspaces go by
+
+    def __setattr__(self, name, value):
+        # (_args holds their addresses for good)
+        if name in self.__dict__:
+            raise AttributeError(f"a KVCache's {name} cannot be replaced")
+        super().__setattr__(name, value)
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in
@@ -112,54 +121,90 @@ def alloc_cache(fmt, g, pages, page, heads, dim, device) -> KVCache:
     return KVCache(fmt, g, *half(), *half())
 
 
+class _Record:
+    """What a call hands to C of a batch.  Whoever holds a record may use its
+    address: it keeps the tensors that it points to, and nothing changes it."""
+
+    __slots__ = ("args", "addr", "tensors", "sizes", "seqs", "tokens", "lens")
+
+    def __init__(self, batch, page):
+        table, lens, starts = batch.table, batch.lens, batch.starts
+        self.seqs, width = table.shape
+        self.tokens, self.lens, self.tensors = batch.tokens, lens, (table, starts)
+        self.args = _BatchArgs(table.data_ptr(), lens.data_ptr(), None if starts is None else starts.data_ptr(),
+                               batch.tokens, width, self.seqs, batch.max_new,
+                               width * page if batch.max_len is None else batch.max_len)
+        self.addr = ctypes.addressof(self.args)
+        self.sizes = {}
+
+    def workspace(self, cache, q_heads, window, mass):
+        """q4_kv_workspace_bytes, asked once for each kind of call."""
+        key = (q_heads, window, mass)
+        n = self.sizes.get(key)
+        if n is None:
+            n = self.sizes[key] = lib().q4_kv_workspace_bytes(cache._ref, self.addr, q_heads, window, int(mass))
+        return n
+
+
 class Batch:
     """Sequences of a call: table int32 [seqs, width] of page numbers, lens
     int32 [seqs] (new tokens counted), and for more or fewer than one new token
     a sequence starts int32 [seqs + 1], the total `tokens` and the largest
     number `max_new`.  max_len bounds lens (default: what the table can hold);
-    a tight bound spares work."""
+    a tight bound spares work.  The fields may be assigned between calls; the
+    next call checks them anew."""
 
     def __init__(self, table, lens, starts=None, *, tokens=None, max_new=None, max_len=None):
-        torch = _torch()
         if table.dim() != 2:
             raise ValueError("table must be [seqs, width]")
-        seqs, width = table.shape
-        dev = table.device
-        _tensor(table, "table", torch.int32)
-        _tensor(lens, "lens", torch.int32, (seqs,), dev)
         if starts is None:
-            if tokens not in (None, seqs) or max_new not in (None, 1):
-                raise ValueError("without starts, every sequence has one new token")
-            tokens, max_new = seqs, 1
-        else:
-            _tensor(starts, "starts", torch.int32, (seqs + 1,), dev)
-            if tokens is None or max_new is None:
-                raise ValueError("starts needs tokens and max_new")
+            tokens, max_new = table.shape[0] if tokens is None else tokens, 1 if max_new is None else max_new
+        elif tokens is None or max_new is None:
+            raise ValueError("starts needs tokens and max_new")
         self.table, self.lens, self.starts = table, lens, starts
-        self.seqs, self.width, self.tokens, self.max_new = seqs, width, tokens, max_new
-        self.max_len, self.device = max_len, dev
-        self._cache, self._sizes = None, {}
+        self.tokens, self.max_new, self.max_len = tokens, max_new, max_len
+        self._check()
 
-    def _ref(self, cache):
-        """The C record for a cache (its page size bounds the lengths)."""
-        if self._cache is not cache:
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        # records by KVCache._key, made of the fields as they are now; a call
+        # that is under way keeps the one it has
+        super().__setattr__("_records", {})
+
+    @property
+    def seqs(self):
+        return self.table.shape[0]
+
+    @property
+    def width(self):
+        return self.table.shape[1]
+
+    @property
+    def device(self):
+        return self.table.device
+
+    def _check(self):
+        torch = _torch()
+        if self.table.dim() != 2:
+            raise ValueError("table must be [seqs, width]")
+        _tensor(self.table, "table", torch.int32)
+        _tensor(self.lens, "lens", torch.int32, (self.seqs,), self.device)
+        if self.starts is not None:
+            _tensor(self.starts, "starts", torch.int32, (self.seqs + 1,), self.device)
+        elif self.tokens != self.seqs or self.max_new != 1:
+            raise ValueError("without starts, every sequence has one new token")
+
+    def _record(self, cache):
+        """The C record for caches of this one's shape (its page size bounds the
+        lengths).  To be held while a call uses its address."""
+        records = self._records
+        rec = records.get(cache._key)
+        if rec is None:
+            self._check()
             if self.device != cache.device:
                 raise ValueError(f"the batch is on {self.device}, the cache on {cache.device}")
-            self._args = _BatchArgs(self.table.data_ptr(), self.lens.data_ptr(),
-                                    None if self.starts is None else self.starts.data_ptr(),
-                                    self.tokens, self.width, self.seqs, self.max_new,
-                                    self.width * cache.page if self.max_len is None else self.max_len)
-            self._addr = ctypes.addressof(self._args)
-            self._cache, self._sizes = cache, {}
-        return self._addr
-
-    def _workspace(self, cache, q_heads, window, mass):
-        """q4_kv_workspace_bytes, asked once for each kind of call."""
-        ref, key = self._ref(cache), (q_heads, window, mass)
-        n = self._sizes.get(key)
-        if n is None:
-            n = self._sizes[key] = lib().q4_kv_workspace_bytes(cache._ref, ref, q_heads, window, int(mass))
-        return n
+            rec = records[cache._key] = _Record(self, cache.page)
+        return rec
 
 
 def _rows(t, name, tokens, heads, cache):
@@ -179,12 +224,12 @@ def append(cache, batch, k, v):
     """Code the new tokens' keys and values [tokens, heads, dim] (fp16 or bf16,
     rows contiguous, any multiple of 8 between them) into their pages
     (q4_kv_append)."""
-    ref = batch._ref(cache)
-    ks = _rows(k, "k", batch.tokens, cache.heads, cache)
-    vs = _rows(v, "v", batch.tokens, cache.heads, cache)
+    rec = batch._record(cache)
+    ks = _rows(k, "k", rec.tokens, cache.heads, cache)
+    vs = _rows(v, "v", rec.tokens, cache.heads, cache)
     if v.dtype != k.dtype:
         raise TypeError("k and v must have one dtype")
-    st = lib().q4_kv_append(cache._ref, ref, _act_code(k.dtype), k.data_ptr(), *ks, v.data_ptr(), *vs,
+    st = lib().q4_kv_append(cache._ref, rec.addr, _act_code(k.dtype), k.data_ptr(), *ks, v.data_ptr(), *vs,
                             cache._stream())
     _check(st, "q4_kv_append")
 
@@ -193,9 +238,9 @@ def read(cache, batch, dtype, out=None):
     """The new tokens' keys and values as the cache holds them, dequantized to
     [tokens, heads, dim] (q4_kv_read).  Returns (k, v)."""
     torch = _torch()
-    ref = batch._ref(cache)
+    rec = batch._record(cache)
     code = _act_code(dtype)
-    shape = (batch.tokens, cache.heads, cache.dim)
+    shape = (rec.tokens, cache.heads, cache.dim)
     if out is None:
         k = torch.empty(shape, dtype=dtype, device=cache.device)
         v = torch.empty_like(k)
@@ -203,14 +248,14 @@ def read(cache, batch, dtype, out=None):
         for t in out:
             _tensor(t, "out", dtype, shape, cache.device)
         k, v = out
-    st = lib().q4_kv_read(cache._ref, ref, code, k.data_ptr(), v.data_ptr(), cache._stream())
+    st = lib().q4_kv_read(cache._ref, rec.addr, code, k.data_ptr(), v.data_ptr(), cache._stream())
     _check(st, "q4_kv_read")
     return k, v
 
 
 def workspace_bytes(cache, batch, q_heads, mass=False, window=0) -> int:
     """Bytes of device workspace that attention needs (q4_kv_workspace_bytes)."""
-    return batch._workspace(cache, q_heads, window, bool(mass))
+    return batch._record(cache).workspace(cache, q_heads, window, bool(mass))
 
 
 def attention(cache, batch, q, *, scale=None, window=0, mass=None, lse=None, out=None, workspace=None):
@@ -223,27 +268,27 @@ def attention(cache, batch, q, *, scale=None, window=0, mass=None, lse=None, out
     float32 [tokens, q_heads], receives the log-sum-exp.  workspace: a uint8
     tensor of at least workspace_bytes, else one is allocated."""
     torch = _torch()
-    ref = batch._ref(cache)
+    rec = batch._record(cache)
     if q.dim() != 3:
         raise ValueError("q must be [tokens, q_heads, dim]")
     heads = q.shape[1]
-    qs = _rows(q, "q", batch.tokens, heads, cache)
+    qs = _rows(q, "q", rec.tokens, heads, cache)
     code = _act_code(q.dtype)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
-        _tensor(out, "out", q.dtype, (batch.tokens, heads, cache.dim), cache.device)
+        _tensor(out, "out", q.dtype, (rec.tokens, heads, cache.dim), cache.device)
     mass_p, width = None, 0
     if mass is not None:
         if mass.dim() != 3:
             raise ValueError("mass must be [seqs, heads, width]")
         width = mass.shape[2]
-        _tensor(mass, "mass", torch.float32, (batch.seqs, cache.heads, width), cache.device)
+        _tensor(mass, "mass", torch.float32, (rec.seqs, cache.heads, width), cache.device)
         mass_p = mass.data_ptr()
     lse_p = None
     if lse is not None:
-        lse_p = _tensor(lse, "lse", torch.float32, (batch.tokens, heads), cache.device).data_ptr()
-    need = batch._workspace(cache, heads, window, mass is not None)
+        lse_p = _tensor(lse, "lse", torch.float32, (rec.tokens, heads), cache.device).data_ptr()
+    need = rec.workspace(cache, heads, window, mass is not None)
     work_p, have = None, 0
     if workspace is not None:
         _tensor(workspace, "workspace", torch.uint8, None, cache.device)
@@ -251,7 +296,7 @@ def attention(cache, batch, q, *, scale=None, window=0, mass=None, lse=None, out
     elif need:
         workspace = torch.empty((need,), dtype=torch.uint8, device=cache.device)
         work_p, have = workspace.data_ptr(), need
-    st = lib().q4_kv_attention(cache._ref, ref, code, q.data_ptr(), *qs, heads,
+    st = lib().q4_kv_attention(cache._ref, rec.addr, code, q.data_ptr(), *qs, heads,
                                cache.dim ** -0.5 if scale is None else scale, window, out.data_ptr(), lse_p,
                                mass_p, width, work_p, have, cache._stream())
     _check(st, "q4_kv_attention")
@@ -266,21 +311,21 @@ def evict(cache, batch, mass, new_table, budget, recent, *, width=None):
     (new_lens [seqs], new_mass [seqs, heads, width], kept [seqs, heads,
     budget]); width defaults to what new_table can hold."""
     torch = _torch()
-    ref = batch._ref(cache)
+    rec = batch._record(cache)
     if mass.dim() != 3:
         raise ValueError("mass must be [seqs, heads, width]")
-    _tensor(mass, "mass", torch.float32, (batch.seqs, cache.heads, mass.shape[2]), cache.device)
+    _tensor(mass, "mass", torch.float32, (rec.seqs, cache.heads, mass.shape[2]), cache.device)
     if new_table.dim() != 2:
         raise ValueError("new_table must be [seqs, width]")
-    _tensor(new_table, "new_table", torch.int32, (batch.seqs, new_table.shape[1]), cache.device)
+    _tensor(new_table, "new_table", torch.int32, (rec.seqs, new_table.shape[1]), cache.device)
     if budget <= 0:
         raise q4.Q4Error(q4.EINVAL, "q4_kv_evict")
     if width is None:
         width = new_table.shape[1] * cache.page
-    new_lens = torch.empty_like(batch.lens)
-    new_mass = mass.new_empty((batch.seqs, cache.heads, width))
-    kept = new_lens.new_empty((batch.seqs, cache.heads, budget))
-    st = lib().q4_kv_evict(cache._ref, ref, mass.data_ptr(), mass.shape[2], new_table.data_ptr(),
+    new_lens = torch.empty_like(rec.lens)
+    new_mass = mass.new_empty((rec.seqs, cache.heads, width))
+    kept = new_lens.new_empty((rec.seqs, cache.heads, budget))
+    st = lib().q4_kv_evict(cache._ref, rec.addr, mass.data_ptr(), mass.shape[2], new_table.data_ptr(),
                            new_table.shape[1], budget, recent, new_lens.data_ptr(), new_mass.data_ptr(),
                            width, kept.data_ptr(), cache._stream())
     _check(st, "q4_kv_evict")
