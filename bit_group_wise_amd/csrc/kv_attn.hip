@@ -87,6 +87,10 @@ void join(const KvBatch &b, const Rows &rows, const Split &sp, const float *part
                                                                                                      part_ml);
 }
 
+// A window that no sequence outgrows is none: positions less a window then stay
+// far inside 32 bits, also where a sequence has more new tokens than cached ones.
+int window_of(const KvBatch &b, int window) { return window < b.max_len ? window : 0; }
+
 size_t round256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // A head's rows by scale groups fill the columns of the token kernel's tiles;
@@ -102,6 +106,7 @@ Split split_for(const KvCache &c, const KvBatch &b, int group, int window)
 
 size_t kv_attention_workspace(const KvCache &c, const KvBatch &b, int q_heads, int window, bool mass)
 {
+    window = window_of(b, window);
     const Split sp = split_for(c, b, q_heads / c.heads, window);
     const size_t rows = (size_t)b.tokens * q_heads;
     size_t n = 0;
@@ -120,6 +125,7 @@ hipError_t launch_kv_attention(int f, const KvCache &c, const KvBatch &b, int ac
                                void *workspace, hipStream_t s)
 {
     const int group = q_heads / c.heads;
+    window = window_of(b, window);
     const Split sp = split_for(c, b, group, window);
     const size_t n = (size_t)b.tokens * q_heads;
     char *w = (char *)workspace;

@@ -253,9 +253,14 @@ def read(cache, batch, dtype, out=None):
     return k, v
 
 
+def _window(window):
+    """A window as a C int: one past its range is no limit, as any that no sequence outgrows."""
+    return window if -1 <= window <= 0x7fffffff else 0x7fffffff if window > 0 else -1
+
+
 def workspace_bytes(cache, batch, q_heads, mass=False, window=0) -> int:
     """Bytes of device workspace that attention needs (q4_kv_workspace_bytes)."""
-    return batch._record(cache).workspace(cache, q_heads, window, bool(mass))
+    return batch._record(cache).workspace(cache, q_heads, _window(window), bool(mass))
 
 
 def attention(cache, batch, q, *, scale=None, window=0, mass=None, lse=None, out=None, workspace=None):
@@ -288,6 +293,7 @@ def attention(cache, batch, q, *, scale=None, window=0, mass=None, lse=None, out
     lse_p = None
     if lse is not None:
         lse_p = _tensor(lse, "lse", torch.float32, (rec.tokens, heads), cache.device).data_ptr()
+    window = _window(window)
     need = rec.workspace(cache, heads, window, mass is not None)
     work_p, have = None, 0
     if workspace is not None:
