@@ -193,6 +193,11 @@ class Batch:
             _tensor(self.starts, "starts", torch.int32, (self.seqs + 1,), self.device)
         elif self.tokens != self.seqs or self.max_new != 1:
             raise ValueError("without starts, every sequence has one new token")
+        # (the record's fields are C ints, which would take the low 32 bits)
+        for name in ("max_new", "max_len"):
+            n = getattr(self, name)
+            if n is not None and not -2 ** 31 <= n < 2 ** 31:
+                raise ValueError(f"{name} must fit 32 bits, got {n}")
 
     def _record(self, cache):
         """The C record for caches of this one's shape (its page size bounds the
@@ -324,7 +329,7 @@ def evict(cache, batch, mass, new_table, budget, recent, *, width=None):
     if new_table.dim() != 2:
         raise ValueError("new_table must be [seqs, width]")
     _tensor(new_table, "new_table", torch.int32, (rec.seqs, new_table.shape[1]), cache.device)
-    if budget <= 0:
+    if not 0 < budget < 2 ** 31 or not 0 <= recent <= budget:
         raise q4.Q4Error(q4.EINVAL, "q4_kv_evict")
     if width is None:
         width = new_table.shape[1] * cache.page

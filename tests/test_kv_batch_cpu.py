@@ -71,8 +71,6 @@ class Library:
         self.asked += 1
         return 64
 
-    def q4_status_str(self, s):
-        return b"status"
 
 
 @pytest.fixture
@@ -190,3 +188,27 @@ def test_a_cache_keeps_its_tensors():
     for name in ("k_codes", "v_scales", "page", "fmt"):
         with pytest.raises(AttributeError):
             setattr(c, name, getattr(c, name))
+
+
+@pytest.mark.parametrize("field", ["max_len", "max_new"])
+@pytest.mark.parametrize("n", [2 ** 31, 2 ** 32 + 5, -2 ** 32 + 5])
+def test_bounds_past_32_bits_are_refused(field, n):
+    """Not taken for their low 32 bits."""
+    kw = dict(tokens=3, max_new=3)
+    kw[field] = n
+    with pytest.raises(ValueError):
+        kv.Batch(ints(3, 4), ints(3), ints(4), **kw)
+
+
+@pytest.mark.parametrize("budget,recent", [(8, 2 ** 32 + 3), (8, -2 ** 32 + 3), (2 ** 31, 0)])
+def test_eviction_counts_past_32_bits_are_refused(library, monkeypatch, budget, recent):
+    cache = make_cache(16)
+    monkeypatch.setattr(torch, "empty_like", lambda t: t)
+    mass, table = Fake((3, 2, 64), torch.float32, 0x10000), ints(3, 4)
+    mass.new_empty = lambda shape: mass
+    lens = ints(3)
+    lens.new_empty = lambda shape: lens
+    library.q4_kv_evict = lambda *a: pytest.fail("called")
+    with pytest.raises(q4.Q4Error) as e:
+        kv.evict(cache, kv.Batch(ints(3, 4), lens), mass, table, budget, recent)
+    assert e.value.status == q4.EINVAL
