@@ -143,8 +143,8 @@ hipError_t launch_kv_attention(int f, const KvCache &c, const KvBatch &b, int ac
     }
     float2 *part_ml = (float2 *)w;
     float *part = (float *)(w + round256(n * sp.parts * sizeof(float2)));
-    hipError_t e = is_prompt(c, b, group) ? launch_kv_prompt(f, c, b, rows, sp, part, part_ml, s)
-                                       : launch_kv_token(f, c, b, rows, sp, part, part_ml, s);
+    const auto launch = is_prompt(c, b, group) ? launch_kv_prompt : act_t == Q4_F16 ? launch_kv_token_f16 : launch_kv_token;
+    hipError_t e = launch(f, c, b, rows, sp, part, part_ml, s);
     if (e != hipSuccess)
         return e;
     if (sp.parts > 1) {

@@ -446,6 +446,8 @@ Split token_split(const KvCache &c, const KvBatch &b, int group, int window);
 Split prompt_split(const KvCache &c, const KvBatch &b, int group, int window);
 hipError_t launch_kv_token(int f, const KvCache &c, const KvBatch &b, const Rows &rows, const Split &sp,
                            float *part, float2 *part_ml, hipStream_t s);
+hipError_t launch_kv_token_f16(int f, const KvCache &c, const KvBatch &b, const Rows &rows, const Split &sp,
+                               float *part, float2 *part_ml, hipStream_t s);
 hipError_t launch_kv_prompt(int f, const KvCache &c, const KvBatch &b, const Rows &rows, const Split &sp,
                             float *part, float2 *part_ml, hipStream_t s);
 size_t kv_mass_workspace(const KvCache &c, const KvBatch &b, int group);

@@ -15,11 +15,12 @@
 //    each lane with eight tokens of one row; contracting the tokens in that
 //    order makes them the second product's column operand without moving.  A
 //    V scale belongs to a token and a group, so it goes into the weight of the
-//    group's column, w_t s_tj, rounded to fp16 (11 bits against the output's 8
-//    or 11: each weight is off by at most 2^-11 of itself, independently, which
-//    leaves an fp16 output 2.8e-4 to 3.5e-4 from binary64, 2.1e-4 of it the
-//    output's own rounding; a second product with what the rounding leaves
-//    would give 2.1e-4, for 67.5 instead of 62 us at 131071 tokens).  Of a
+//    group's column, w_t s_tj, rounded to fp16: 11 bits.  That is 2^-11 of each
+//    weight, independently: a bf16 output, of 8 bits, is as far from binary64
+//    as without it (1.7e-3).  An fp16 output would be 2.8e-4 to 3.5e-4 off
+//    instead of the 2.1e-4 of its own rounding, so for those a second product
+//    adds what the rounding left of the weights (TWO; kv_token_f16.hip): 66.9
+//    instead of 60.8 us at 131071 tokens, 29.3 for 26.2 in 8 drafts of 4.  Of a
 //    column's result only its group's values are used.
 //  * Reference.  w_t s_tj must stay below 65504 and the largest should be well
 //    inside fp16's normal range whatever the values' size, so m tracks
@@ -50,12 +51,17 @@
 // workgroups and a second launch joins the parts.
 #include "kv_attn.hpp"
 
+#ifndef Q4_KV_TOKEN_TWO
+#define Q4_KV_TOKEN_TWO 0  // weights in two parts: kv_token_f16.hip
+#endif
+
 namespace q4 {
 namespace {
 
 constexpr int kWaves = 4;
 constexpr int kBlock = 64 * kWaves;
 constexpr int kStep = 32;  // tokens per wave and step
+constexpr bool kTwo = Q4_KV_TOKEN_TWO;
 
 // The values of a step's 32 tokens: as they are in memory, 16 bytes a lane in a
 // row, and from LDS a lane's share of rows 4 kg .. + 3, the values (D/16) i ..
@@ -114,7 +120,7 @@ __device__ __forceinline__ uint32_t zero_pair(const uint32_t *z, int r, int h, i
     return (a & 15u) | (b & 15u) << 16;
 }
 
-template <int FMT, int D, int GS, int NT, bool KEEP>
+template <int FMT, int D, int GS, int NT, bool KEEP, bool TWO>
 __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_token_kernel(
     KvCache c, KvBatch b, Rows rows, Split sp, float *__restrict__ part, float2 *__restrict__ part_ml)
 {
@@ -291,7 +297,7 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
                         o[n][v][p] *= f;
             }
         }
-        u32x4 wp[NT];
+        u32x4 wp[NT], wr[TWO ? NT : 1];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -301,7 +307,10 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
                 const float w1 = __builtin_amdgcn_exp2f(__builtin_fmaf(x[u][n][r + 1], q.factor[n], -m[n]));
                 l[n] += w0 + w1;
                 // (fma with 0: the scale's conversion is part of v_fma_mix)
-                wp[n][e] = pair_h2(__builtin_fmaf(w0, vs[u][r], 0.0f), __builtin_fmaf(w1, vs[u][r + 1], 0.0f));
+                const float s0 = __builtin_fmaf(w0, vs[u][r], 0.0f), s1 = __builtin_fmaf(w1, vs[u][r + 1], 0.0f);
+                wp[n][e] = pair_h2(s0, s1);
+                if constexpr (TWO)
+                    wr[n][e] = pair_h2(s0 - h2f(wp[n][e] & 0xffffu), s1 - h2f(wp[n][e] >> 16));
             }
 #pragma unroll
         for (int v = 0; v < HV; ++v) {
@@ -325,8 +334,11 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
 #pragma unroll
             for (int k = 0; k < NP; ++k)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                for (int n = 0; n < NT; ++n) {
+                    if constexpr (TWO)
+                        o[n][v][k] = mfma<Q4_F16>(va[k], wr[n], o[n][v][k]);
                     o[n][v][k] = mfma<Q4_F16>(va[k], wp[n], o[n][v][k]);
+                }
         }
         t0 = tn;
         row0 = next0;
@@ -402,6 +414,7 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
     }
 }
 
+#if !Q4_KV_TOKEN_TWO
 // Most parts that a length is split into: as many as leave every workgroup
 // resident at once (three to each of the 256 compute units, two where rows
 // fill more than one column tile; dim 256 takes the registers of one), none
@@ -419,8 +432,11 @@ int most_parts(const KvCache &c, const KvBatch &b, int group)
     return (int)std::max<int64_t>(1, std::min<int64_t>(room / wgs, (b.max_len + 255) / 256));
 }
 
+#endif
+
 }  // namespace
 
+#if !Q4_KV_TOKEN_TWO
 Split token_split(const KvCache &c, const KvBatch &b, int group, int window)
 {
     Split sp;
@@ -434,6 +450,8 @@ Split token_split(const KvCache &c, const KvBatch &b, int group, int window)
     return sp;
 }
 
+#endif
+
 hipError_t launch_kv_token(int f, const KvCache &c, const KvBatch &b, const Rows &rows, const Split &sp,
                            float *part, float2 *part_ml, hipStream_t s)
 {
@@ -444,9 +462,9 @@ hipError_t launch_kv_token(int f, const KvCache &c, const KvBatch &b, const Rows
         auto go = [&](auto nt) {
             constexpr int NT = decltype(nt)::value;
             if (rows.kept)
-                kv_token_kernel<F, D, GS, NT, true><<<grid, kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+                kv_token_kernel<F, D, GS, NT, true, kTwo><<<grid, kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
             else
-                kv_token_kernel<F, D, GS, NT, false><<<grid, kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+                kv_token_kernel<F, D, GS, NT, false, kTwo><<<grid, kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
         };
         if (cols <= 16)
             go(KvInt<1>{});

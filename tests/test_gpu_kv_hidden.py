@@ -42,7 +42,8 @@ def sized_pool(fmt, g, dim, heads, page, lens, seed, size):
     return pool
 
 
-def check(pool, new, act, q, window=0):
+def check(pool, new, act, q, window=0, roundings=2):
+    """roundings: to fp16 that a weight times a value goes through."""
     qd = q.double().cpu().numpy()
     T, hq, dim = qd.shape
     G, scale = hq // pool.heads, dim ** -0.5
@@ -64,7 +65,7 @@ def check(pool, new, act, q, window=0):
             p = np.exp(x - x.max(-1, keepdims=True))
             p /= p.sum(-1, keepdims=True)
             ref, mag, top = p @ V, p @ np.abs(V), (p * s[:, h]).max(-1)
-            rel = 2 * (2.0 ** -24 * (dim + 16) * worst + 2.0 ** -20) + 2.0 ** -18 + 2 * 2.0 ** -11
+            rel = 2 * (2.0 ** -24 * (dim + 16) * worst + 2.0 ** -20) + 2.0 ** -18 + roundings * 2.0 ** -11
             tol = rel[:, None] * mag + UNIT[act] * np.abs(ref) + n * 2.0 ** -27 * top[:, None]
             tol += 2.0 ** -25 if act == q4.F16 else 0.0
             over = np.abs(got[first:first + m, j] - ref) - tol
