@@ -8,16 +8,23 @@
 //
 //  * Keys lie there as exact fp16 levels less zero-points, their scales beside
 //    them in binary32; a score is sum_j s_j acc_j as before.
-//  * Values lie there as fp16(level * s_tj 2^-E_t), one rounding of the cached
-//    value.  E_t puts a token's largest scale just below 2^12: it is added to
-//    the token's score, which puts it into the weight, and taken off the row
-//    sum again.  So a row meets a token's size only in what it sees of it (a
+//  * Values lie there as fp16(level * s_tj 2^-E_t), at most one rounding of the
+//    cached value.  2^E_t is the token's size: E_t is added to its score, which
+//    puts it into the weight, and taken off the row sum again.  Table formats
+//    and single groups take the largest scale itself, so that its group's levels
+//    are exact (of an NF4 cache in groups of 64, half of them); several groups of
+//    INT4 the power of two that puts it just below 2^12, by which fp16 scales
+//    stay exact and small levels round to themselves.  So a row meets a token's size only in what it sees of it (a
 //    size shared by several tokens would let one that a row does not see take
 //    the others' bits), and neither weights (at most 2^15.5) nor values (at
 //    most 61440) leave fp16: groups down to 2^-21 of their token's largest
 //    keep all their bits.  (The reference puts the largest weight at 2^11: it
 //    moves rarely, and weights down to 2^-25 of the largest are exact to fp16's
 //    11 bits.)
+//  * For fp16 outputs a second product adds what rounding the weights left
+//    (TWO): 2.1e-4 to 2.8e-4 from binary64, 2.1e-4 of it the output's own
+//    rounding, where 3.0e-4 to 3.4e-4 were; it costs a fifth (140 us for 116
+//    below).  A bf16 output is 1.7e-3 off either way.
 //  * LDS holds operands as the lanes read them, 16 bytes a lane in a row, in
 //    two buffers: the next tile is fetched while one is worked on, one barrier
 //    a tile.  Rows of V operands are values d = 8 i + j of the dword i that a
@@ -31,7 +38,7 @@
 // rows a wave, eight waves, so that a row pays little of the unpacking.  The
 // vector ALUs are busy 60 % of the time, the matrix cores 33 %; the rest is the
 // barrier a tile and the staging waves' wait for their loads.  dim 128, g 64:
-//   2 x 2048 new tokens, 32 heads, causal, INT4-sym       115 us, 588 TFLOP/s
+//   2 x 2048 new tokens, 32 heads, causal, INT4-sym       116 us, 583 TFLOP/s
 //   1024 after 31744, 8 heads of 4 rows, INT4-asym        675 us, 800 TFLOP/s
 #include "kv_attn.hpp"
 
@@ -153,6 +160,10 @@ struct Fetch {
     }
 };
 
+// Whether a token's size is its largest scale itself, or the power of two above.
+template <int FMT, int D, int GS>
+constexpr bool whole_scale() { return !kv_int<FMT>() || D == GS; }
+
 template <int FMT, int D, int GS>
 struct Stage {
     static constexpr int NG = D / GS, TT = prompt_tile<D>();
@@ -194,10 +205,18 @@ __device__ __forceinline__ void stage(Stage<FMT, D, GS> &st, const Fetch<FMT, D,
         s[t] = f.ok >> t & 1 ? scale_of<FMT>(f.s[t]) : 0.0f;
         // (2^-40: a token of zeros has a weight in the row sum all the same,
         // which must not vanish beside large ones)
-        const int e2 = min(max(__builtin_amdgcn_frexp_expf(fmaxf(token_max<D, GS>(s[t]), 0x1p-40f)), -40), 100) - 12;
-        e[t] = (float)e2;
-        down[t] = __builtin_amdgcn_ldexpf(1.0f, -e2);
-        s[t] *= down[t];
+        const float top = fmaxf(token_max<D, GS>(s[t]), 0x1p-40f);
+        if constexpr (whole_scale<FMT, D, GS>()) {
+            constexpr float up = FMT == Q4_NF4 ? 4.0f : FMT == Q4_FP4 ? 1024.0f : 4096.0f;
+            e[t] = __builtin_amdgcn_logf(top * (key_unit<FMT>() / up));
+            down[t] = __builtin_amdgcn_exp2f(-e[t]);
+            s[t] *= __builtin_amdgcn_rcpf(top) * up;
+        } else {
+            const int e2 = min(__builtin_amdgcn_frexp_expf(top), 100) - 12;
+            e[t] = (float)e2;
+            down[t] = __builtin_amdgcn_ldexpf(1.0f, -e2);
+            s[t] *= down[t];
+        }
     }
     if (i == 0) {
         *(f32x4 *)&st.e[4 * qd] = e;
@@ -214,10 +233,9 @@ __device__ __forceinline__ void stage(Stage<FMT, D, GS> &st, const Fetch<FMT, D,
             for (int p = 0; p < 4; ++p)
                 x[t][p] = std::bit_cast<uint32_t>(std::bit_cast<f16x2>(a[p]) * std::bit_cast<f16x2>(p & 1 ? q : h));
         } else {
-            const float un = s[t] * key_unit<FMT>();
 #pragma unroll
             for (int p = 0; p < 4; ++p)
-                x[t][p] = pair_h2(h2f(a[p] & 0xffffu) * un, h2f(a[p] >> 16) * un);
+                x[t][p] = pair_h2(h2f(a[p] & 0xffffu) * s[t], h2f(a[p] >> 16) * s[t]);
         }
     }
     // quad qd = 8 tb + 4 tt + kg: half tt of lane (kg, row)
@@ -234,7 +252,7 @@ __device__ __forceinline__ void stage(Stage<FMT, D, GS> &st, const Fetch<FMT, D,
     }
 }
 
-template <int FMT, int D, int GS, int NT>
+template <int FMT, int D, int GS, int NT, bool TWO>
 __global__ __launch_bounds__(kBlock, (NT < most_nt<D>() ? 4 : 2)) void kv_prompt_kernel(KvCache c, KvBatch b, Rows rows, Split sp,
                                                               float *__restrict__ part,
                                                               float2 *__restrict__ part_ml)
@@ -428,7 +446,7 @@ __global__ __launch_bounds__(kBlock, (NT < most_nt<D>() ? 4 : 2)) void kv_prompt
             for (int b2 = 0; b2 < TB; ++b2) {
                 const f32x4 down[2] = {*(const f32x4 *)&S.down[32 * (tb + b2) + 4 * kg],
                                        *(const f32x4 *)&S.down[32 * (tb + b2) + 16 + 4 * kg]};
-                u32x4 w[NT];
+                u32x4 w[NT], left[TWO ? NT : 1];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float sum = 0.0f, p[8];
@@ -439,8 +457,11 @@ __global__ __launch_bounds__(kBlock, (NT < most_nt<D>() ? 4 : 2)) void kv_prompt
                     }
                     l[n] += sum;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < 4; ++k) {
                         w[n][k] = pair_h2(p[2 * k], p[2 * k + 1]);
+                        if constexpr (TWO)
+                            left[n][k] = pair_h2(p[2 * k] - h2f(w[n][k] & 0xffffu), p[2 * k + 1] - h2f(w[n][k] >> 16));
+                    }
                 }
 #pragma unroll
                 for (int v0 = 0; v0 < NV; v0 += VF) {
@@ -449,8 +470,11 @@ __global__ __launch_bounds__(kBlock, (NT < most_nt<D>() ? 4 : 2)) void kv_prompt
 #pragma unroll
                     for (int v = 0; v < VF; ++v)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
+                        for (int n = 0; n < NT; ++n) {
+                            if constexpr (TWO)
+                                o[v0 + v][n] = mfma<Q4_F16>(va[v], left[n], o[v0 + v][n]);
                             o[v0 + v][n] = mfma<Q4_F16>(va[v], w[n], o[v0 + v][n]);
+                        }
                 }
                 if (b2 + 1 < TB)
 #pragma unroll
@@ -546,10 +570,17 @@ hipError_t launch_kv_prompt(int f, const KvCache &c, const KvBatch &b, const Row
     return kv_by_shape(f, c.dim, c.g, [&](auto fmt, auto dim, auto gs) {
         const int64_t grid = (int64_t)sp.parts * sp.tiles * b.seqs * c.heads;
         constexpr int F = decltype(fmt)::value, D = decltype(dim)::value, GS = decltype(gs)::value;
+        auto go = [&](auto nt) {
+            constexpr int NT = decltype(nt)::value;
+            if (rows.act == Q4_F16)
+                kv_prompt_kernel<F, D, GS, NT, true><<<dim3((unsigned)grid), kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+            else
+                kv_prompt_kernel<F, D, GS, NT, false><<<dim3((unsigned)grid), kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+        };
         if (sp.rows == block_rows(most_nt<D>()))
-            kv_prompt_kernel<F, D, GS, most_nt<D>()><<<dim3((unsigned)grid), kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+            go(KvInt<most_nt<D>()>{});
         else
-            kv_prompt_kernel<F, D, GS, 1><<<dim3((unsigned)grid), kBlock, 0, s>>>(c, b, rows, sp, part, part_ml);
+            go(KvInt<1>{});
         return hipGetLastError();
     });
 }

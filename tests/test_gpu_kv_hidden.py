@@ -52,7 +52,7 @@ def check(pool, new, act, q, window=0, roundings=2):
     batch = pool.batch(None if all(m == 1 for m in new) else new)
     got = kv.attention(pool.cache, batch, q, window=window).double().cpu().numpy()
     assert np.isfinite(got).all()
-    first = 0
+    first, wants = 0, np.empty(qd.shape)
     for b, (n, m) in enumerate(zip(pool.lens, new)):
         t, pos = np.arange(n), np.arange(n - m, n)[:, None]
         see = (t <= pos) & ((t > pos - window) if window else True)
@@ -68,10 +68,12 @@ def check(pool, new, act, q, window=0, roundings=2):
             rel = 2 * (2.0 ** -24 * (dim + 16) * worst + 2.0 ** -20) + 2.0 ** -18 + roundings * 2.0 ** -11
             tol = rel[:, None] * mag + UNIT[act] * np.abs(ref) + n * 2.0 ** -27 * top[:, None]
             tol += 2.0 ** -25 if act == q4.F16 else 0.0
+            wants[first:first + m, j] = ref
             over = np.abs(got[first:first + m, j] - ref) - tol
             assert (over <= 0).all(), f"sequence {b}, head {j}, row {np.unravel_index(over.argmax(), over.shape)}: " \
                                       f"{over.max()} past the tolerance"
         first += m
+    return got, wants
 
 
 def queries(tokens, heads, dim, act, seed):
