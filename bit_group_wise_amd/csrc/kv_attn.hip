@@ -68,7 +68,7 @@ __global__ __launch_bounds__(kJoin) void kv_join_kernel(KvBatch b, Rows rows, Sp
     pk[1] = rows.act == Q4_F16 ? pair_h2(sum[2], sum[3]) : pack_bf2(sum[2], sum[3]);
     *(u32x2 *)(rows.out + to * D + 4 * d) = pk;
     if (d == 0) {
-        const float e = l > 0.0f ? m + __builtin_amdgcn_logf(l) : -__builtin_inff();
+        const float e = l > 0.0f ? row_stat(m, l) : -__builtin_inff();
         if (rows.lse)
             rows.lse[to] = e * kLn2;
         if (rows.stat)

@@ -83,6 +83,14 @@ __device__ __forceinline__ float quad_sum(float v)
     return v + __shfl_xor(v, 32);
 }
 
+// m + log2(l), the base-2 log of a row's denominator, l > 0.  The hardware's
+// logarithm is up to a last place low, so it is asked for a number in [-1, 0): of
+// l itself, some 2^25 here, it left all of a row's weights 5e-7 to 1e-6 too large.
+__device__ __forceinline__ float row_stat(float m, float l)
+{
+    return (m + (float)__builtin_amdgcn_frexp_expf(l)) + __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(l));
+}
+
 // The range of cached tokens that a sequence's rows can see.
 __device__ __forceinline__ int range_begin(const KvSeq &s, int window)
 {

@@ -529,7 +529,7 @@ __global__ __launch_bounds__(kBlock, (NT < most_nt<D>() ? 4 : 2)) void kv_prompt
             if (sp.parts > 1) {
                 part_ml[to * sp.parts + pt] = float2{m[n], ll};
             } else {
-                const float v = ll > 0.0f ? m[n] + __builtin_amdgcn_logf(ll) : -__builtin_inff();
+                const float v = ll > 0.0f ? row_stat(m[n], ll) : -__builtin_inff();
                 if (rows.lse)
                     rows.lse[to] = v * kLn2;
                 if (rows.stat)

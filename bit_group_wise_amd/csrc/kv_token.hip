@@ -399,7 +399,7 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
             pk[1] = rows.act == Q4_F16 ? pair_h2(sum[2], sum[3]) : pack_bf2(sum[2], sum[3]);
             *(u32x2 *)(rows.out + to * D + d) = pk;
             if (d == 0) {
-                const float v = ll > 0.0f ? mm + __builtin_amdgcn_logf(ll) : -__builtin_inff();
+                const float v = ll > 0.0f ? row_stat(mm, ll) : -__builtin_inff();
                 if (rows.lse)
                     rows.lse[to] = v * kLn2;
                 if (rows.stat)
