@@ -421,7 +421,12 @@ __device__ __forceinline__ void col_scores(const KeyCodes<FMT, D, GS> &t, uint32
             x[n][r] = group_sum<D / GS>(__builtin_fmaf(a[n][r], s[r], 0.0f));
 }
 
-// Rows that the few-row kernels take: four column tiles (dim 64) or two.
+// Rows that the few-row kernels take: four column tiles (dim 64) or two; the
+// sums of more do not fit the registers.  At as many rows (INT4-sym, 8 heads, 1
+// and 32 sequences of 4096 tokens; a call's time) against the prompt kernel:
+// 16 rows of dim 128, g 64 12.9 and 42.5 us (14.9 and 70.2 there); 8 of dim 256,
+// g 64 17.6 and 75 (18.8 and 158); 64 of dim 64, g 64 15.0 and 47.4 (13.5 and
+// 54.8); at half as many no form is slower here.
 inline int few_rows(const KvCache &c) { return (c.dim == 64 ? 64 : 32) / (c.dim / c.g); }
 
 template <class F>

@@ -18,7 +18,9 @@
 // Bound: reading, HBM traffic: 16 x 4096 tokens of 8 heads of 128, INT4-asym
 // g32, 57 us for 354 MB (6.2 TB/s, where a large copy reaches 5.2 and a read
 // 6.2).  Appending, vector-ALU issue (the division and the code of every
-// value): 8191 NF4 g64 tokens of 32 heads of 128 43 us, 4.0 TB/s.
+// value): 8191 NF4 g64 tokens of 32 heads of 128 43 us, 4.0 TB/s, 80 % of the
+// slots; 4 prompts of up to 2048 INT4-asym g32 tokens of 8 heads 13.3 us, 2.8
+// TB/s, 62 % (short enough that a tenth of it is the launch's ramp).
 #include "kv_common.hpp"
 #include "q4_code.hpp"
 
@@ -29,7 +31,9 @@ constexpr int kBlock = 256;
 // Rows a lane works on, and from how many pieces of 8 values on (16 x 4096
 // INT4-asym tokens of 8 heads read in 1, 2, 4, 8 rows a lane: 84, 68, 58, 56 us;
 // 8191 NF4 tokens of 32 heads appended: 61, 50, 43, 43 and read: 39, 31, 28, 36;
-// 1024 tokens of 8 heads read in 1 and 4: 3.9 and 4.0).
+// 1024 tokens of 8 heads read in 1 and 4: 3.9 and 4.0.  Calls in 1 and 4, INT4-asym
+// tokens of 8 heads of 128: 2^19 pieces alike, 2^20 appended 7.5 and 7.5, read 6.2
+// and 5.9; 2^21 12.2 and 11.5, 9.1 and 8.2).
 constexpr int kRowsMany = 4;
 constexpr int64_t kManyItems = 1 << 20;
 
@@ -272,7 +276,9 @@ Launch launch_of(const KvCache &c, const KvBatch &b)
     Launch l;
     l.shift = __builtin_ctz(c.dim / 8);
     const int64_t items = (int64_t)b.max_new << l.shift;
-    l.block = items <= 64 ? 64 : kBlock;  // (single tokens leave most of a large workgroup idle)
+    // (single tokens leave most of a large workgroup idle: 64 sequences of 8
+    // heads appended in 2.4 us, in workgroups of 256 2.6)
+    l.block = items <= 64 ? 64 : kBlock;
     l.many = items * 2 * c.heads * b.seqs >= kManyItems;
     const int64_t per = (int64_t)l.block * (l.many ? kRowsMany : 1);
     l.grid = dim3((unsigned)((items + per - 1) / per), (unsigned)(2 * c.heads), (unsigned)b.seqs);

@@ -14,14 +14,14 @@
 //
 // Bound: latency.  A pass over the candidates is some 500 cycles of ballots, a
 // barrier and the exchange in LDS, whatever the length: 12 us for 1088 tokens
-// in four waves, 23 us for 16 x 8 rows of 8192 in sixteen.
+// in four waves, 24 us for 16 x 8 rows of 8192 in sixteen.
 //
 // Move: rows go to other pages, so no order is needed: a lane copies 16 bytes
 // of a row's codes, and a row's lanes share its scales and zero-points.  Bound:
 // HBM traffic.  Kept tokens lie among dropped ones and a row of codes is half a
-// 128-byte line (dim 128), so nearly every line is read: 16 x 4096 of 8192
-// tokens, 8 heads of 128, INT4-asym g32 36.6 us, 86 MB written and up to twice
-// that read, 7 TB/s.
+// 128-byte line (dim 128), so more is read than written: 16 x 4096 of 8192
+// tokens, 8 heads of 128, INT4-asym g32 36.8 us, 113 MB read and 78 MB written
+// (counted), 5.2 TB/s, what a large copy reaches.
 #include <algorithm>
 
 #include "kv_common.hpp"
@@ -33,8 +33,8 @@ constexpr int kSel = 1024;
 constexpr int kSelFew = 256;
 constexpr int kMove = 256;
 // Rows a lane moves, and from how many 16-byte pieces on (16 x 4096 kept tokens
-// of 8 heads of 128: 1, 2, 4 rows 39.5, 36.6, 38.1 us; fewer pieces leave units
-// without work).
+// of 8 heads of 128: 1, 2, 4 rows 39.5, 36.6, 38.1 us.  Whole calls in 1 and 2
+// rows: 2^18 pieces 26.8 and 27.7, 2^20 40.9 and 39.9, 2^21 56.9 and 55.5).
 constexpr int kRowsMany = 2;
 constexpr int64_t kManyPieces = 1 << 19;
 
@@ -378,7 +378,8 @@ hipError_t launch_kv_evict(int f, const KvCache &c, const KvBatch &b, const floa
     const dim3 grid(c.heads, b.seqs);
     // up to 4096 tokens in four waves (one to a SIMD: a pass over the candidates
     // is a few hundred cycles of latency, which more waves only lengthen), else
-    // in sixteen
+    // in sixteen (calls: 1088 tokens 13.2 and 16.7 us, 2048 13.3 and 16.8, 4096
+    // 20.0 and 19.1)
     const int threads = b.max_len <= 16 * kSelFew ? kSelFew : kSel;
     const int per = std::max(1, (b.max_len + threads - 1) / threads);
     auto select = [&](auto sel, auto held) {

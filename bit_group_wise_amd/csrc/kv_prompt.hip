@@ -35,8 +35,9 @@
 // scales, the exponent's fma, maximum, reference, exp2 at a quarter rate, sum,
 // rounding; one size a wave's tokens would save one: 110 us where this takes 115)
 // against 4 D / 1024 of matrix time; tiles are 64 tokens (dim 128) by 16 NT
-// rows a wave, eight waves, so that a row pays little of the unpacking.  The
-// vector ALUs are busy 60 % of the time, the matrix cores 33 %; the rest is the
+// rows a wave, eight waves, so that a row pays little of the unpacking.  Of the
+// chunk below the vector ALUs are busy 60 % of the time, the matrix cores 31 %
+// (of the prompts, whose workgroups end unevenly, 50 and 22 %); the rest is the
 // barrier a tile and the staging waves' wait for their loads.  dim 128, g 64:
 //   2 x 2048 new tokens, 32 heads, causal, INT4-sym       116 us, 583 TFLOP/s
 //   1024 after 31744, 8 heads of 4 rows, INT4-asym        675 us, 800 TFLOP/s
@@ -544,7 +545,14 @@ __global__ __launch_bounds__(kBlock, (NT < most_nt<D>() ? 4 : 2)) void kv_prompt
 // Row tiles of 256 (dim 256: 128) rows fill the 256 compute units, one
 // workgroup each, or are split into as many parts as do, none shorter than 256
 // tokens.  Where even that leaves units idle or rows empty, tiles of 128 rows,
-// two workgroups a unit.
+// two workgroups a unit.  Calls in large and in small tiles (8 heads of dim 128,
+// INT4-sym g 64): rows that a large tile would half fill, 4 x 100 on 2048 28.3 and
+// 27.6 us; units idle, 1024 on 1024 31.2 and 25.5, 6 x 1024 on 2048 91.7 and 85.1;
+// units filled, 1024 x 4 rows on 32768 680 and 797, 3 x 4096 x 4 on 4096 639 and
+// 852, 8 x 1024 on 2048 93 and 91.  (Whole prompts that just fill the units are
+// faster in small tiles all the same, their last rows having twice the mean to
+// see: 32 heads of 2048 on 2048 92 and 77; not told apart.)  Parts of at least
+// 128, 256 and 512 tokens: 64 on 4096 21.7, 18.2 and 23.0, on 1024 14.1, 15.9, 22.2.
 Split prompt_split(const KvCache &c, const KvBatch &b, int group, int window)
 {
     const int64_t range = longest_range(b, window), rows = (int64_t)b.max_new * group;

@@ -39,7 +39,8 @@
 // instruction, whatever its width, hence 16-byte loads of whole rows handed on
 // through LDS) and vector-ALU issue, each busy for half to two thirds of the
 // time.  Nothing is read twice.  One new token a sequence, dim 128:
-//   2 x 131071 tokens, 8 heads, 4 rows, INT4-asym g32   60 us + 5 to join, 4.3 TB/s
+//   2 x 131071 tokens, 8 heads, 4 rows, INT4-asym g32   61 us + 5 to join, 4.2 TB/s
+//     (fp16, weights in two parts: 67 + 5)
 //   32 x 4096, 8 heads, 4 rows, INT4-sym g64, scores kept   35 us + 4 to 6
 //   16 x 2048, 32 heads, 1 row, NF4 g64                 35 us, 3.4 TB/s (level
 //     lookups: LDS busy half the time, with conflicts; levels by v_perm 39 us)
@@ -422,7 +423,10 @@ __global__ __launch_bounds__(kBlock, (D == 256 ? 1 : NT == 1 ? 3 : 2)) void kv_t
 // single launch of at most four steps a wave).  A second round of workgroups
 // costs more than it balances: 32 x 4096 tokens in 3, 4, 8 parts 27.3, 31.0,
 // 34.8 us; 512 sequences and heads of 2048 tokens in 1, 2, 4 parts 36.8, 40.1
-// (+ 4.6 to join), 44.3 (+ 4.4) us.
+// (+ 4.6 to join), 44.3 (+ 4.4) us; 8 heads of 4096 tokens in parts of 256 and
+// 128 tokens 12.3 and 13.5; 333 and 500 tokens in one part 7.6 and 8.7 a call, in
+// two 12.0 and 11.9.  (The parts are cut by max_len: a batch of ragged lengths
+// leaves those past a sequence's end empty.)
 int most_parts(const KvCache &c, const KvBatch &b, int group)
 {
     if (b.max_len <= 512)

@@ -345,9 +345,16 @@ q4_status q4_kv_read(const q4_kv_cache *cache, const q4_kv_batch *batch, q4_dtyp
  * A token at position p sees the tokens t with t <= p and, for window > 0,
  * t > p - window.  With x_t = scale * <q, K_t>: out = sum_t softmax(x)_t V_t.
  * A row that sees nothing gives out = 0 and lse = -infinity.  0 < scale <= 2^60.
- * Scores, softmax statistics and sums are binary32; the result does not
- * depend on timing (no floating-point atomics).  |value| < 2^60 is assumed
- * of what a table format's cache holds.
+ * Scores, softmax statistics, sums and masses are binary32; the result does not
+ * depend on timing (no floating-point atomics).  In the product with the values
+ * the weights are fp16 (act_t fp16: in two parts, of 22 bits together), and
+ * where a head has many rows (more than 32 times g / dim, dim 64: 64 times) so
+ * are the values, relative to their token's largest scale: groups down to
+ * 2^-21 of it keep 11 bits, and so do weights that, times their token's scale,
+ * are 2^-23 of the row's largest.  What a row does not see changes nothing of
+ * that.  (An fp16 output is 2.1e-4 to 2.8e-4 off in relative 2-norm, where
+ * rounding it alone leaves 2.1e-4; a bf16 output 1.7e-3, its rounding.)  Of what
+ * a cache holds it is assumed that scales are not negative and |value| < 2^60.
  * workspace: device memory of q4_kv_workspace_bytes (for the same window and
  * with_mass = (mass != NULL)), 256-byte aligned, needed
  * until the call's work has run; its contents before and after do not matter
