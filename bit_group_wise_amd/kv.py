@@ -90,7 +90,11 @@ class KVCache:
                                   (k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros)),
                                 pages, page, heads, dim, g, fmt, 0)
         self._ref = ctypes.addressof(self._args)
-        self._key = (dev.index, fmt, g, page, heads, dim)  # what a batch's record and workspaces go by
+        # What a batch's record and workspace sizes go by: all that the library
+        # checks of a cache (it answers 0 for one that it refuses).
+        self._key = (dev.index, fmt, g, pages, page, heads, dim,
+                     all(t is None or t.data_ptr() % 16 == 0 for t in
+                         (k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros)))
 
     def __setattr__(self, name, value):
         # (_args holds their addresses for good)

@@ -41,9 +41,9 @@ def ints(*shape, ptr=0x1000, device=DEVICE):
     return Fake(shape, torch.int32, ptr, device)
 
 
-def make_cache(page=16, heads=2, dim=64, at=0x100000, device=DEVICE):
-    half = lambda p: (Fake((8, heads, page, dim // 2), torch.uint8, p, device),  # noqa: E731
-                      Fake((8, heads, page, dim // 64), torch.float16, p + 0x1000, device), None)
+def make_cache(page=16, heads=2, dim=64, at=0x100000, device=DEVICE, pages=8):
+    half = lambda p: (Fake((pages, heads, page, dim // 2), torch.uint8, p, device),  # noqa: E731
+                      Fake((pages, heads, page, dim // 64), torch.float16, p + 0x1000, device), None)
     return kv.KVCache(q4.INT4_SYM, 64, *half(at), *half(at + 0x8000))
 
 
@@ -212,3 +212,12 @@ def test_eviction_counts_past_32_bits_are_refused(library, monkeypatch, budget, 
     with pytest.raises(q4.Q4Error) as e:
         kv.evict(cache, kv.Batch(ints(3, 4), lens), mass, table, budget, recent)
     assert e.value.status == q4.EINVAL
+
+
+@pytest.mark.parametrize("bad", ["address", "pages"])
+def test_a_bad_cache_leaves_others_their_sizes(bad):
+    """The library's answer of 0 for a cache that it refuses is not taken for another cache of the shape."""
+    b = kv.Batch(ints(3, 1024), ints(3))
+    good, other = make_cache(16), make_cache(16, at=0x100008 if bad == "address" else 0x100000, pages=0 if bad == "pages" else 8)
+    assert kv.workspace_bytes(other, b, 4) == 0
+    assert kv.workspace_bytes(good, b, 4) > 0
