@@ -23,7 +23,7 @@
 //    11 bits.)
 //  * For fp16 outputs a second product adds what rounding the weights left
 //    (TWO): 2.1e-4 to 2.8e-4 from binary64, 2.1e-4 of it the output's own
-//    rounding, where 3.0e-4 to 3.4e-4 were; it costs a fifth (140 us for 116
+//    rounding, where 3.0e-4 to 3.4e-4 were; it costs a fifth (137 us for 113
 //    below).  A bf16 output is 1.7e-3 off either way.
 //  * LDS holds operands as the lanes read them, 16 bytes a lane in a row, in
 //    two buffers: the next tile is fetched while one is worked on, one barrier
@@ -33,14 +33,14 @@
 //
 // Bound: vector-ALU issue.  A score costs about eleven issue slots (its groups'
 // scales, the exponent's fma, maximum, reference, exp2 at a quarter rate, sum,
-// rounding; one size a wave's tokens would save one: 110 us where this takes 115)
+// rounding; one size a wave's tokens would save one: 110 us where this takes 113)
 // against 4 D / 1024 of matrix time; tiles are 64 tokens (dim 128) by 16 NT
 // rows a wave, eight waves, so that a row pays little of the unpacking.  Of the
 // chunk below the vector ALUs are busy 60 % of the time, the matrix cores 31 %
 // (of the prompts, whose workgroups end unevenly, 50 and 22 %); the rest is the
 // barrier a tile and the staging waves' wait for their loads.  dim 128, g 64:
-//   2 x 2048 new tokens, 32 heads, causal, INT4-sym       116 us, 583 TFLOP/s
-//   1024 after 31744, 8 heads of 4 rows, INT4-asym        675 us, 800 TFLOP/s
+//   2 x 2048 new tokens, 32 heads, causal, INT4-sym       113 us, 595 TFLOP/s
+//   1024 after 31744, 8 heads of 4 rows, INT4-asym        662 us, 817 TFLOP/s
 #include "kv_attn.hpp"
 
 namespace q4 {
@@ -170,9 +170,9 @@ struct Stage {
     static constexpr int NG = D / GS, TT = prompt_tile<D>();
     u32x4 k[TT * D / 8];        // [16 tokens][D / 32] operands of 64 lanes
     u32x2 v[TT * D / 4];        // [32 tokens][D / 16] operands, halves of lanes
-    float ks[NG][TT];
-    uint32_t valid[TT / 32];
+    float ks[NG][TT];           // (four at a time, as the next two: 16 bytes aligned)
     float e[TT], down[TT];      // E_t, and 2^-E_t
+    uint32_t valid[TT / 32];
 };
 
 template <int FMT, int D, int GS>
