@@ -36,8 +36,8 @@
 // rounding; one size a wave's tokens would save one: 110 us where this takes 113)
 // against 4 D / 1024 of matrix time; tiles are 64 tokens (dim 128) by 16 NT
 // rows a wave, eight waves, so that a row pays little of the unpacking.  Of the
-// chunk below the vector ALUs are busy 60 % of the time, the matrix cores 31 %
-// (of the prompts, whose workgroups end unevenly, 50 and 22 %); the rest is the
+// chunk below the vector ALUs are busy 60 % of the time, the matrix cores 32 %
+// (of the prompts, whose workgroups end unevenly, 50 and 23 %); the rest is the
 // barrier a tile and the staging waves' wait for their loads.  dim 128, g 64:
 //   2 x 2048 new tokens, 32 heads, causal, INT4-sym       113 us, 595 TFLOP/s
 //   1024 after 31744, 8 heads of 4 rows, INT4-asym        662 us, 817 TFLOP/s
