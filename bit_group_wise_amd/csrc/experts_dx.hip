@@ -1,0 +1,62 @@
+// experts_dx.hip -- the gradient through experts' weights, dX[r] = dY[r] .
+// What_e for the rows r of each expert e: gemm_dx_tile.hpp's tiles over pieces
+// of up to TM rows of one expert.
+#include "gemm_dx_tile.hpp"
+#include "rows.hpp"
+
+namespace q4 {
+namespace {
+
+template <int FMT, int ACT>
+__global__ __launch_bounds__(kBlock) void experts_dx_kernel(
+    const uint16_t *__restrict__ dy, const int32_t *__restrict__ offsets, int rows, int experts,
+    const uint8_t *__restrict__ codes, const void *__restrict__ scales, const uint8_t *__restrict__ zeros, int N,
+    int K, int gshift, int ktiles, uint16_t *__restrict__ dx)
+{
+    int kt;
+    const Piece p = find_piece<TM>(offsets, experts, rows, blockIdx.x, ktiles, kt);
+    if (p.group < 0)
+        return;
+    const DxTile tile{p.lo, p.hi, kt * TK, (int64_t)p.group * N, (int64_t)experts * N};
+    dx_tile<FMT, ACT, kDxGroup>(tile, dy, codes, scales, zeros, N, K, gshift, dx);
+}
+
+template <int FMT>
+hipError_t launch_edx(q4_dtype act_t, const ExpertsArgs &a, int gshift, hipStream_t s)
+{
+    const int64_t ktiles = (a.K + TK - 1) / TK;
+    const int64_t blocks = ktiles * most_pieces(a.rows, a.experts, TM);
+    if (blocks > 0x7fffffffll)
+        return hipErrorInvalidValue;
+    const dim3 grid((unsigned)blocks), block(kBlock);
+    if (act_t == Q4_BF16)
+        hipLaunchKernelGGL((experts_dx_kernel<FMT, Q4_BF16>), grid, block, 0, s, (const uint16_t *)a.x, a.offsets,
+                           (int)a.rows, a.experts, a.codes, a.scales, a.zeros, (int)a.N, (int)a.K, gshift,
+                           (int)ktiles, (uint16_t *)a.y);
+    else
+        hipLaunchKernelGGL((experts_dx_kernel<FMT, Q4_F16>), grid, block, 0, s, (const uint16_t *)a.x, a.offsets,
+                           (int)a.rows, a.experts, a.codes, a.scales, a.zeros, (int)a.N, (int)a.K, gshift,
+                           (int)ktiles, (uint16_t *)a.y);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_experts_dx(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s)
+{
+    const int gshift = g == 32 ? 5 : (g == 64 ? 6 : 7);
+    switch (f) {
+    case Q4_NF4:
+        return launch_edx<Q4_NF4>(act_t, a, gshift, s);
+    case Q4_FP4:
+        return launch_edx<Q4_FP4>(act_t, a, gshift, s);
+    case Q4_NF4_DQ:
+        return launch_edx<Q4_NF4_DQ>(act_t, a, gshift, s);
+    case Q4_INT4_SYM:
+        return launch_edx<Q4_INT4_SYM>(act_t, a, gshift, s);
+    default:
+        return launch_edx<Q4_INT4_ASYM>(act_t, a, gshift, s);
+    }
+}
+
+}  // namespace q4

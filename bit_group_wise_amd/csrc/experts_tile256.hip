@@ -1,0 +1,4 @@
+// experts_tile256.hip -- experts' products in tiles of 256 rows by 256 weight
+// rows, as the prefill GEMM's.
+#define Q4_EXPERTS_LAUNCH launch_experts_tile256
+#include "experts_tile.hpp"

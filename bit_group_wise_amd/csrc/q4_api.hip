@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <mutex>
 
+#include "api_check.hpp"
 #include "q4.h"
 #include "q4_common.hpp"
 #include "q4_internal.hpp"
@@ -24,6 +25,8 @@
 // In host code this name is not a device address; the address of each
 // device's copy comes from hipGetSymbolAddress.
 static __device__ __align__(256) uint32_t scratch[Q4_GEMV_CHAIN_SYNC_BYTES / 4];
+
+using namespace q4;
 
 namespace {
 
@@ -53,34 +56,6 @@ hipError_t scratch_for_current_device(uint32_t **out)
     *out = g_scratch_ptr[dev];
     return hipSuccess;
 }
-
-bool format_ok(q4_format f)
-{
-    return f == Q4_NF4 || f == Q4_INT4_SYM || f == Q4_INT4_ASYM || f == Q4_NF4_DQ || f == Q4_FP4;
-}
-bool dtype_ok(q4_dtype t) { return t == Q4_F16 || t == Q4_BF16; }
-bool group_ok(int g) { return g == 32 || g == 64 || g == 128; }
-bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-// Checks shared by every entry point that takes a quantized weight.
-q4_status check_weight(q4_format f, int g, const void *codes, const void *scales,
-                       const void *zeros, int64_t N, int64_t K)
-{
-    if (!format_ok(f) || !group_ok(g))
-        return Q4_EUNSUPPORTED;
-    if (!codes || !scales)
-        return Q4_EINVAL;
-    if (N <= 0 || K <= 0 || K % g != 0)
-        return Q4_EINVAL;
-    if ((f == Q4_INT4_ASYM) != (zeros != nullptr))
-        return Q4_EINVAL;
-    const uintptr_t sa = f == Q4_NF4_DQ ? 16 : (q4::f32_absmax(f) ? 4 : 2);
-    if (!aligned(codes, 16) || !aligned(scales, sa))
-        return Q4_EALIGN;
-    return Q4_OK;
-}
-
-q4_status from_hip(hipError_t e) { return e == hipSuccess ? Q4_OK : Q4_EHIP; }
 
 }  // namespace
 

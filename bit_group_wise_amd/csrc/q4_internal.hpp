@@ -62,4 +62,28 @@ hipError_t launch_gemm_bn128(q4_format f, int g, q4_dtype act_t, const void *x, 
                        const uint8_t *codes, const void *scales, const uint8_t *zeros,
                        int64_t N, int64_t K, void *y, hipStream_t s);
 
+// A product through experts' weights, one array of experts * N rows: row r of
+// group e (rows offsets[e] .. offsets[e + 1] - 1 of `rows`) is x's row index[r]
+// (r without an index), of xrows, against the N rows of expert e.
+struct ExpertsArgs {
+    const void *x;
+    int64_t xrows;
+    const int32_t *index, *offsets;
+    int64_t rows;
+    int experts;
+    const uint8_t *codes;
+    const void *scales;
+    const uint8_t *zeros;
+    int64_t N, K;
+    void *y;
+};
+hipError_t launch_experts(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
+// Pieces of up to 16 mt (1, 2 or 4) rows of an expert a workgroup.
+hipError_t launch_experts_skinny(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, int mt, hipStream_t s);
+// Tiles of up to 128 or 256 rows of an expert.
+hipError_t launch_experts_tile128(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
+hipError_t launch_experts_tile256(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
+// The gradient dX[r] = dY[r] . What_e: x is dY, y is dX.
+hipError_t launch_experts_dx(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
+
 }  // namespace q4

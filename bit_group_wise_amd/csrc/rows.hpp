@@ -1,0 +1,99 @@
+// rows.hpp -- which rows of a grouped product a workgroup works on.
+//
+// A grouped product's rows lie in groups (the rows of one expert), given by
+// their offsets on the device, so the host knows their number and no more
+// when it launches.  The grid therefore counts pieces of up to CH rows of one
+// group at their largest possible number, and every wave finds its piece
+// itself: 64 groups at a time, one per lane, with prefix sums over the lanes.
+// Offsets are taken as they can be: inside 0 .. rows, and one that falls
+// below an earlier one as that one (its group is empty), so that no piece
+// leaves the arrays, no row is in two of them, and their number stays within
+// the grid whatever the offsets hold.
+#pragma once
+
+#include "q4_common.hpp"
+
+namespace q4 {
+
+// The lanes' values of lower or equal number combined: rows of 16 lanes
+// first, then the rows' last lanes handed on (0 is neutral in both uses).
+template <class Op>
+__device__ __forceinline__ int wave_scan(int v, Op op)
+{
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));  // one lane up in its row
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));  // two
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));  // four
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));  // eight
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));  // lane 15 of rows 0 and 2 to rows 1 and 3
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));  // lane 31 to rows 2 and 3
+    return v;
+}
+
+// Rows lo .. hi - 1 of group `group` (-1: no such piece).
+struct Piece {
+    int group, lo, hi;
+};
+
+// Groups base + lane of a launch: their first rows and numbers of rows.
+struct GroupLane {
+    int start, n;
+};
+__device__ __forceinline__ GroupLane group_lane(const int32_t *__restrict__ offsets, int groups, int rows, int base,
+                                                int lane, int &highest)
+{
+    const int e = base + lane;
+    const bool in = e < groups;
+    const int a = in ? min(max(offsets[e], 0), rows) : 0;
+    const int b = in ? min(max(offsets[e + 1], 0), rows) : 0;
+    const int start = max(wave_scan(a, [](int p, int q) { return max(p, q); }), highest);
+    highest = __builtin_amdgcn_readlane(start, 63);
+    return GroupLane{start, in ? max(b - start, 0) : 0};
+}
+
+// Piece `block % pieces` of the launch and `block / pieces` in other, or
+// group -1 for a block past all pieces: block counts pieces fastest, so the
+// blocks that have work are the grid's first ones.
+template <int CH>
+__device__ __forceinline__ Piece find_piece(const int32_t *__restrict__ offsets, int groups, int rows, unsigned block,
+                                            int others, int &other)
+{
+    const int lane = threadIdx.x & 63;
+    const auto add = [](int p, int q) { return p + q; };
+    int highest = 0, total = 0;
+    GroupLane g{};
+    int upto = 0;
+    for (int base = 0; base < groups; base += 64) {
+        g = group_lane(offsets, groups, rows, base, lane, highest);
+        upto = wave_scan((g.n + CH - 1) / CH, add);
+        total += __builtin_amdgcn_readlane(upto, 63);
+    }
+    if (total == 0 || block / (unsigned)total >= (unsigned)others)
+        return Piece{-1, 0, 0};
+    other = (int)(block / (unsigned)total);
+    int want = (int)(block % (unsigned)total), base = 0;
+    if (groups > 64) {  // (else the lanes still hold all groups)
+        highest = 0;
+        for (;; base += 64) {
+            g = group_lane(offsets, groups, rows, base, lane, highest);
+            upto = wave_scan((g.n + CH - 1) / CH, add);
+            const int here = __builtin_amdgcn_readlane(upto, 63);
+            if (want < here || base + 64 >= groups)
+                break;
+            want -= here;
+        }
+    }
+    const int l = (int)__builtin_ctzll(__ballot(upto > want) | 1ull << 63);
+    const int before = l ? __builtin_amdgcn_readlane(upto, l > 0 ? l - 1 : 0) : 0;
+    const int start = __builtin_amdgcn_readlane(g.start, l), n = __builtin_amdgcn_readlane(g.n, l);
+    const int lo = start + (want - before) * CH;
+    return Piece{base + l, lo, min(lo + CH, start + n)};
+}
+
+// The most pieces that `rows` rows in `groups` groups make: every group but
+// for whole pieces adds at most one.
+inline int64_t most_pieces(int64_t rows, int64_t groups, int ch)
+{
+    return rows / ch + (groups < rows ? groups : rows);
+}
+
+}  // namespace q4

@@ -35,6 +35,10 @@ SIGNATURES = {
     "q4_gemv_chain": (_int, [_int, _int, _int, ctypes.c_void_p, _int, _vp, _vp]),
     "q4_gemv_chain_static": (_int, [_int, _int, _int, ctypes.c_void_p, _int, _vp]),
     "q4_status_str": (ctypes.c_char_p, [_int]),
+    # products through experts' weights (bit_group_wise_amd.experts)
+    "q4_experts_gemm": (_int, [_int, _int, _int, _vp, _i64, _vp, _vp, _i64, _int, _vp, _vp, _vp, _i64, _i64,
+                               _vp, _vp]),
+    "q4_experts_gemm_dx": (_int, [_int, _int, _int, _vp, _vp, _i64, _int, _vp, _vp, _vp, _i64, _i64, _vp, _vp]),
     # the key/value cache (bit_group_wise_amd.kv)
     "q4_kv_append": (_int, [_vp, _vp, _int, _vp, _i64, _i64, _vp, _i64, _i64, _vp]),
     "q4_kv_read": (_int, [_vp, _vp, _int, _vp, _vp, _vp]),
@@ -105,6 +109,15 @@ def _torch():
 def _stream_ptr(t) -> int | None:
     torch = _torch()
     return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _launch(device, fn, *args) -> int:
+    """fn(*args, stream) with the device's current stream, the device current."""
+    torch = _torch()
+    if torch._C._cuda_getDevice() == device.index:
+        return fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    with torch.cuda.device(device):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
 
 
 def _ptr(t) -> int | None:

@@ -256,6 +256,41 @@ q4_status q4_gemv_chain(q4_format f, int g, q4_dtype act_t, const q4_gemv_task *
 q4_status q4_gemv_chain_static(q4_format f, int g, q4_dtype act_t, const q4_gemv_task *tasks,
                                int ntasks, void *stream);
 
+/* ------------------------------------------- products through experts' weights
+ * A mixture's experts hold one weight each, of one shape, and every row of
+ * the activations goes through one of them.  The experts' weights are one
+ * quantized array [experts * N, K], expert e's rows being e*N .. e*N + N - 1
+ * (q4_quantize of the stacked weights); any format.  The rows are sorted by
+ * expert: those of expert e are rows offsets[e] .. offsets[e+1] - 1 of the
+ * `rows` rows of y (offsets: int32 [experts + 1] on the device, read by the
+ * kernels, so groups may change between replays of a captured call).  Groups
+ * may have any size, none among them.  Offsets are held to 0 .. rows, and one
+ * below an earlier one counts as that; rows of y before the first group and
+ * behind the last are left as they were.
+ *
+ * y[r] = x[index[r]] . What_e^T for the rows r of each expert e, with the
+ * values and the rounding of q4_gemm.  index int32 [rows] on the device, or
+ * NULL for x[r] (then x_rows must be rows): a token's rows for its experts
+ * read the token's one row of x [x_rows, K].  A row whose index is outside
+ * 0 .. x_rows - 1 gets zeros.  With an index x_rows * K * 2 must stay below
+ * 2^31 bytes, else Q4_EUNSUPPORTED.  rows = 0 is no work.  The mean number of
+ * rows an expert chooses the kernel; every choice takes any groups. */
+#define Q4_EXPERTS_MAX 65536
+#define Q4_EXPERTS_MAX_ROWS 1073741824
+q4_status q4_experts_gemm(q4_format f, int g, q4_dtype act_t, const void *x, int64_t x_rows,
+                          const int32_t *index, const int32_t *offsets, int64_t rows, int experts,
+                          const uint8_t *codes, const void *scales, const uint8_t *zeros,
+                          int64_t N, int64_t K, void *y, void *stream);
+
+/* The gradient through the frozen experts: dx[r] = dy[r] . What_e for the
+ * rows r of each expert e, as q4_gemm_dx (and with its limits and alignment
+ * for N and K); dy [rows, N], dx [rows, K].  Rows of dx outside every group
+ * are left as they were. */
+q4_status q4_experts_gemm_dx(q4_format f, int g, q4_dtype act_t, const void *dy,
+                             const int32_t *offsets, int64_t rows, int experts,
+                             const uint8_t *codes, const void *scales, const uint8_t *zeros,
+                             int64_t N, int64_t K, void *dx, void *stream);
+
 /* ------------------------------------------------- the 4-bit key/value cache
  * Attention layers keep the keys and values of earlier tokens; here they are
  * held in the same 4 bits per value as the weights, and read by attention
