@@ -42,6 +42,7 @@
 #include "q4_common.hpp"
 #include "q4_internal.hpp"
 #include "q4_mfma.hpp"
+#include "lora.hpp"
 
 namespace q4 {
 namespace {
@@ -79,7 +80,8 @@ __device__ __forceinline__ int yswz(int r, int c) { return c ^ ((r >> 1) & 7); }
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 
 // A tile of a grouped product (kDxGroup) lies among rows that may hold anything.
-enum { kDxDense = 0, kDxGroup = 1 };
+// kDxLora: low-rank adapters beside the weight.
+enum { kDxDense = 0, kDxGroup = 1, kDxLora = 2 };
 
 // One thread's loads of a step: 16-byte pieces of dY (chunk t % 8 of rows
 // t / 8 + 64 i), and for weight rows 2p, 2p + 1 of the step (p = t % 32)
@@ -122,9 +124,9 @@ __device__ __forceinline__ void dx_load(DxLoads &ld, const DxCtx &c, int n0_, in
     for (int i = 0; i < kYLoads; ++i) {
         const int yrow = (t >> 3) + 64 * i;
         int off = 2 * (yrow * c.N + 8 * (t & 7));
-        // (in a group the next row may be another's and hold anything: such
-        // elements are not loaded)
-        if constexpr (KIND == kDxGroup)
+        // (the next row may be another's and hold anything: such elements are
+        // not loaded)
+        if constexpr (KIND != kDxDense)
             off = n0 + 8 * (t & 7) < c.N ? off : -16;
         ld.y[i] = __builtin_amdgcn_raw_buffer_load_b128(yr, off, 0, 0);
     }
@@ -173,7 +175,7 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
                                         const uint8_t *__restrict__ codes,
                                         const void *__restrict__ scales,
                                         const uint8_t *__restrict__ zeros, int N, int K, int gshift,
-                                        uint16_t *__restrict__ dx)
+                                        uint16_t *__restrict__ dx, const LowRank *low = nullptr)
 {
     __shared__ __attribute__((aligned(16))) char ys[2][TM * kYRow];
     __shared__ __attribute__((aligned(16))) char wt[2][TN * kWPitch];
@@ -222,6 +224,91 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
 #pragma unroll
         for (int f = 0; f < kWMF; ++f)
             acc[j][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // The adapters' part, u A, as steps of the same form: 64 values r of u as
+    // the step's dY (its two parts in the two dY buffers) and the adapter's 64
+    // rows of A as its weight rows (for fp16 its two parts in the two weight
+    // buffers).
+    if constexpr (KIND == kDxLora) {
+        constexpr int C = TM / 64;
+        const int rows = M - m0 < TM ? M - m0 : TM;
+        for (int rc = 0; rc < low->rank; rc += 64) {
+            for (int p = t; p < TM * 8; p += kBlock) {
+                const int row = p >> 3, ch = p & 7;
+                float v[8] = {};
+                if (row < rows && rc + 8 * ch < low->rank)
+                    sum_parts(*low, m0 + row, rc + 8 * ch, v);
+                const Parts8 q = two_parts(v);
+                const int at = row * kYRow + 16 * yswz(row, ch);
+                *(u32x4 *)(ys[0] + at) = q.hi;
+                *(u32x4 *)(ys[1] + at) = q.lo;
+            }
+            AdapterSet<C> set;
+            set.init(low->ids, low->adapters, m0, rows);
+            int ad;
+            uint64_t mask[C];
+            while (set.next(ad, mask)) {
+                const int r = rc + (t >> 3), k = k0 + 16 * (t & 7);
+                u32x4 v[2] = {};
+                if (r < low->rank && k < K) {
+                    const u32x4 *w = (const u32x4 *)(low->w + ((int64_t)ad * low->rank + r) * K + k);
+                    v[0] = w[0];
+                    v[1] = w[1];
+                }
+                __syncthreads();  // (the last adapter's rows have been read)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const Parts8 w = two_parts16<ACT>(v[e]);
+                    *(u32x4 *)(wt[0] + wofs(t >> 3, 16 * (t & 7) + 8 * e)) = w.hi;
+                    if constexpr (ACT == Q4_F16)
+                        *(u32x4 *)(wt[1] + wofs(t >> 3, 16 * (t & 7) + 8 * e)) = w.lo;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kKF; ++j) {
+                    Parts8 fa[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int nl = 32 * h + 8 * fq + 4 * u + (fi >> 2);
+                            const int kl = 64 * wk + 16 * j + 4 * (fi & 3);
+                            const v4i16 p = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                (__attribute__((address_space(3))) v4i16 *)(wt[0] + wofs(nl, kl)));
+                            fa[h].hi[2 * u] = (uint32_t)(uint16_t)p[0] | ((uint32_t)(uint16_t)p[1] << 16);
+                            fa[h].hi[2 * u + 1] = (uint32_t)(uint16_t)p[2] | ((uint32_t)(uint16_t)p[3] << 16);
+                            if constexpr (ACT == Q4_F16) {
+                                const v4i16 o = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                    (__attribute__((address_space(3))) v4i16 *)(wt[1] + wofs(nl, kl)));
+                                fa[h].lo[2 * u] = (uint32_t)(uint16_t)o[0] | ((uint32_t)(uint16_t)o[1] << 16);
+                                fa[h].lo[2 * u + 1] = (uint32_t)(uint16_t)o[2] | ((uint32_t)(uint16_t)o[3] << 16);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int f = 0; f < kWMF; ++f) {
+                        const int row = 16 * kWMF * wm + 16 * f + fi;  // (a wave's rows lie in one mask of 64)
+                        f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = row * kYRow + 16 * yswz(row, 4 * h + fq);
+                            const Parts8 u{*(const u32x4 *)(ys[0] + at), *(const u32x4 *)(ys[1] + at)};
+                            p = mfma_parts_a<ACT>(fa[h], u, p);
+                        }
+                        uint64_t of = mask[0];
+#pragma unroll
+                        for (int c2 = 1; c2 < C; ++c2)
+                            of = (16 * kWMF * wm) / 64 == c2 ? mask[c2] : of;
+                        const bool mine = (of >> (row & 63)) & 1;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[j][f][e] = mine ? acc[j][f][e] + p[e] : acc[j][f][e];
+                    }
+                }
+            }
+            __syncthreads();
+        }
+    }
 
     // One round: the products of the step in LDS buffer (ysc, wtc), with the
     // staging of the next step (register set ld -> buffer (ysn, wtn)) worked

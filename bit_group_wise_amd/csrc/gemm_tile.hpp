@@ -49,6 +49,7 @@
 #include "q4_common.hpp"
 #include "q4_internal.hpp"
 #include "q4_mfma.hpp"
+#include "lora.hpp"
 
 namespace q4 {
 namespace {
@@ -156,13 +157,13 @@ struct TileCtx {
                  // the run holding the tile's first group
     int zo;      // ... and that nibble's position in it (0 or 1)
     int fq;      // lane quad
-    uint32_t xg[kXBlocks];  // gathered rows: voffset of the lane's row and chunk, per block
+    uint32_t xg[kXBlocks];  // not dense: voffset of the lane's row and chunk, per block
     int xk[2];              // ... and that chunk's first k, for even / odd blocks
 };
 
 // What is particular to a tile of a grouped product.  GATHER: its x rows are
-// those that an index names, anywhere in x.
-enum { kDense = 0, kGather = 1 };
+// those that an index names, anywhere in x.  LORA: low-rank adapters beside it.
+enum { kDense = 0, kGather = 1, kLora = 2 };
 // A chunk of x that is not there: past every view.
 constexpr uint32_t kNowhere = 0xfffffff0u;
 
@@ -173,7 +174,7 @@ template <int KIND>
 __device__ __forceinline__ void load_x1(const TileCtx &c, char *xn, int wave, int i, int k0)
 {
     const int B = kXBlocks * wave + i;
-    if constexpr (KIND == kGather) {
+    if constexpr (KIND != kDense) {
         // (chunks past a row's end are not loaded: they would be another row's
         // values, which may be anything, against zero weights)
         const uint32_t v = k0 + c.xk[i & 1] < c.K ? c.xg[i] : kNowhere;
@@ -374,12 +375,81 @@ struct Tile {
     int xrows;
 };
 
+// The tile's accumulators as the adapters' part makes them, h B^T, with the
+// same operand roles, fragment positions and staging as a K step: 64 values r
+// of all x rows of h as the step's x, its two parts in the two x buffers, and
+// B [n][r] straight from memory as the weights.  (One step of 2 or 3 products
+// against the K / 64 of the product itself.)
+template <int ACT>
+__device__ __forceinline__ void lora_start(f32x4 (&acc)[kNF][kMF], const LowRank &l, const TileCtx &c, char *xs0,
+                                           char *xs1, int m0, int mend, int wave, int fr, int nrow, int N)
+{
+    const int rows = min(mend - m0, BM);
+    constexpr int C = (BM + 63) / 64;
+    for (int rc = 0; rc < l.rank; rc += 64) {
+        // (uniform loop: the workgroup's threads all stage and meet here)
+        for (int p = threadIdx.x; p < BM * 8; p += kBlock) {
+            const int row = p >> 3, ch = p & 7;
+            float v[8] = {};
+            if (row < rows && rc + 8 * ch < l.rank)
+                sum_parts(l, m0 + row, rc + 8 * ch, v);
+            const Parts8 q = two_parts(v);
+            const int at = row * ROW_BYTES + 16 * swz(row, ch);
+            *(u32x4 *)(xs0 + at) = q.hi;
+            *(u32x4 *)(xs1 + at) = q.lo;
+        }
+        __syncthreads();
+        AdapterSet<C> set;
+        set.init(l.ids, l.adapters, m0, rows);
+        int ad;
+        uint64_t mask[C];
+        while (set.next(ad, mask)) {
+            Parts8 b[kNF][2];
+            const uint16_t *w = l.w + (int64_t)ad * N * l.rank;
+#pragma unroll
+            for (int j = 0; j < kNF; ++j) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int n = nrow + 4 * j, r = rc + 16 * c.fq + 8 * h;
+                    u32x4 v{0, 0, 0, 0};
+                    if (n < N && r < l.rank)
+                        v = *(const u32x4 *)(w + (int64_t)n * l.rank + r);
+                    b[j][h] = two_parts16<ACT>(v);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kMF; ++i) {
+                if (((mask[i / 4] >> (16 * (i % 4))) & 0xffff) == 0)
+                    continue;
+                const bool mine = (mask[i / 4] >> (16 * (i % 4) + fr)) & 1;
+                f32x4 t[kNF];
+#pragma unroll
+                for (int j = 0; j < kNF; ++j)
+                    t[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const Parts8 x{*(const u32x4 *)(xs0 + c.rd[h] + 2048 * i), *(const u32x4 *)(xs1 + c.rd[h] + 2048 * i)};
+#pragma unroll
+                    for (int j = 0; j < kNF; ++j)
+                        t[j] = mfma_parts_a<ACT>(b[j][h], x, t[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < kNF; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        acc[j][i][v] = mine ? acc[j][i][v] + t[j][v] : acc[j][i][v];
+            }
+        }
+        __syncthreads();
+    }
+}
+
 template <int FMT, int ACT, int G, int KIND>
 __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__restrict__ x,
                                           const uint8_t *__restrict__ codes,
                                           const void *__restrict__ scales,
                                           const uint8_t *__restrict__ zeros, int K, int vec_y,
-                                          uint16_t *__restrict__ y)
+                                          uint16_t *__restrict__ y, const LowRank *low = nullptr)
 {
     using S = Span<FMT, G>;
     // two x buffers as separate objects, so the compiler can tell that the
@@ -463,7 +533,7 @@ __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__re
 #pragma unroll
         for (int e = 0; e < 2; ++e)
             c.xv[e] = rl * 2 * K + 16 * swz(8 * e + rl, p);
-        if constexpr (KIND == kGather) {
+        if constexpr (KIND != kDense) {
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 c.xk[e] = 8 * swz(8 * e + rl, p);
@@ -472,7 +542,7 @@ __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__re
                 const int m = m0 + 8 * (kXBlocks * wave + i) + rl;
                 uint32_t row = (uint32_t)(m - m0);
                 bool there = m < M;
-                if (tile.index) {
+                if (KIND == kGather && tile.index) {
                     row = (uint32_t)tile.index[there ? m : m0];
                     there = there && row < (uint32_t)tile.xrows;
                 }
@@ -491,6 +561,9 @@ __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__re
 #pragma unroll
         for (int i = 0; i < kMF; ++i)
             acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    if constexpr (KIND == kLora)
+        lora_start<ACT>(acc, *low, c, xs0, xs1, m0, M, wave, fr, n0 + wrow, N);
 
     // prologue: x of step 0 into LDS buffer 0, codes of steps 0 and 1, the
     // scales of span 0, the first half of step 0 dequantized

@@ -1,0 +1,279 @@
+// lora_grad.hip -- the adapters' gradients, dA[a] = sum_m u[m]^T x[m] and
+// dB[a] = sum_m dy[m]^T h[m] over the rows m of adapter a.
+//
+// Both are G[c][r] = sum_m X[m][c] P[m][r] with a short side r (P = u or h)
+// and a long one c (X = x or dy), so they are bound by reading X once.  A
+// workgroup of 4 waves takes 128 columns c, up to 64 values r and one part of
+// the rows, 64 rows a step:
+//  * the contraction runs over the rows, so both operands need 8 consecutive
+//    rows of one column: X's 64 x 128 tile and P's (its two bfloat16 parts side
+//    by side) lie in LDS row by row and come back transposed
+//    (ds_read_b64_tr_b16; layout and bank spread as in gemm_dx_tile.hpp);
+//  * rows of other adapters enter both tiles as zeros, and steps without a row
+//    of this adapter are left out: the rows' adapters are looked through first,
+//    1024 steps at a time;
+//  * the next step's rows are loaded while this one's products run;
+//  * dA's accumulators hold columns in a lane and dB's values r, so each is
+//    stored along its own rows;
+//  * with few columns and adapters the rows are split over workgroups, whose
+//    binary32 sums a second kernel adds in order and rounds.
+#include "lora.hpp"
+#include "q4_internal.hpp"
+
+namespace q4 {
+namespace {
+
+constexpr int kGrWaves = 4;
+constexpr int kGrBlock = 64 * kGrWaves;
+constexpr int kGrRows = 64;     // rows per step
+constexpr int kGrCols = 128;    // columns c per workgroup (32 per wave)
+constexpr int kGrPitch = 288;   // bytes of a staged row of 128 values
+constexpr int kGrList = 1024;   // steps listed at a time
+
+typedef short v4i16 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ int gofs(int row, int col) { return row * kGrPitch + ((2 * col) ^ (((row >> 3) & 1) << 7)); }
+
+// 8 rows of one column as an operand: rows 32 h + 8 fq .. + 7, column c0 + fi.
+__device__ __forceinline__ u32x4 column8(const char *tile, int h, int c0)
+{
+    const int lane = threadIdx.x & 63, fi = lane & 15, fq = lane >> 4;
+    u32x4 v;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const v4i16 q = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) v4i16 *)(tile + gofs(32 * h + 8 * fq + 4 * u + (fi >> 2),
+                                                                    c0 + 4 * (fi & 3))));
+        v[2 * u] = (uint32_t)(uint16_t)q[0] | ((uint32_t)(uint16_t)q[1] << 16);
+        v[2 * u + 1] = (uint32_t)(uint16_t)q[2] | ((uint32_t)(uint16_t)q[3] << 16);
+    }
+    return v;
+}
+
+// One kind of gradient: X [rows, cols], P's partial sums, and the output [ad,
+// rank, cols] (dA) or [ad, cols, rank] (dB).
+struct Side {
+    const uint16_t *x;
+    const float *p;
+    int cols;
+    int64_t out;  // where the side's sums begin in a part of `sums`
+    uint16_t *g;
+};
+
+template <int ACT, int RF, bool IS_B>
+__device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cblock, int slice, int ad, int split,
+                                     char *xt, char *xl, char *pt, uint16_t *list, int *count)
+{
+    const int t = threadIdx.x, lane = t & 63;
+    const int wave = (int)__builtin_amdgcn_readfirstlane(t >> 6);
+    const int fi = lane & 15, fq = lane >> 4;
+    const int c0 = cblock * kGrCols, r0 = slice * 16 * RF;
+    const int64_t steps = (a.rows + kGrRows - 1) / kGrRows;
+    const int64_t per = (steps + a.splits - 1) / a.splits;
+    const int64_t first = split * per, last = first + per < steps ? first + per : steps;
+
+    f32x4 acc[RF][2];
+#pragma unroll
+    for (int f = 0; f < RF; ++f)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            acc[f][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    for (int64_t base = first; base < last; base += kGrList) {
+        // the steps with rows of this adapter, in order
+        const int n = (int)(last - base < kGrList ? last - base : kGrList);
+        __syncthreads();  // (the last list and tiles have been read)
+        for (int s = wave; s < n; s += kGrWaves) {
+            const int64_t m = (base + s) * kGrRows + lane;
+            const uint64_t any = __ballot(m < a.rows && adapter_of(a.ids, a.adapters, m) == ad);
+            if (lane == 0)
+                list[s] = any != 0;
+        }
+        __syncthreads();
+        if (wave == 0) {
+            int found = 0;
+            for (int s = 0; s < n; s += 64) {
+                const bool on = s + lane < n && list[s + lane];
+                const uint64_t m = __ballot(on);
+                if (on)  // (behind this place nothing is still to be read: found <= s)
+                    list[found + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)(s + lane);
+                found += __popcll(m);
+            }
+            if (lane == 0)
+                *count = found;
+        }
+        __syncthreads();
+        const int found = *count;
+
+        u32x4 xv[4];
+        Parts8 pv[2 * RF > 2 ? RF / 2 : 1];
+        constexpr int kPPieces = kGrRows * 2 * RF;  // 8-value pieces of P's tile
+        constexpr int kPLoads = (kPPieces + kGrBlock - 1) / kGrBlock;
+        static_assert(sizeof(pv) / sizeof(pv[0]) >= kPLoads, "pieces of P");
+        auto load = [&](int i) {
+            const int64_t m0 = (base + list[i]) * kGrRows;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int64_t m = m0 + (t >> 4) + 16 * q;
+                const int c = c0 + 8 * (t & 15);
+                xv[q] = u32x4{0, 0, 0, 0};
+                if (m < a.rows && c < side.cols && adapter_of(a.ids, a.adapters, m) == ad)
+                    xv[q] = *(const u32x4 *)(side.x + m * side.cols + c);
+            }
+#pragma unroll
+            for (int q = 0; q < kPLoads; ++q) {
+                const int p = t + kGrBlock * q;
+                const int64_t m = m0 + p / (2 * RF);
+                const int r = r0 + 8 * (p % (2 * RF));
+                float v[8] = {};
+                if (p < kPPieces && m < a.rows && r < a.rank && adapter_of(a.ids, a.adapters, m) == ad) {
+                    const LowRank l{side.p, a.parts, a.rank, a.adapters, a.rows, nullptr, nullptr};
+                    sum_parts(l, m, r, v);
+                }
+                pv[q] = two_parts(v);
+            }
+        };
+        if (found)
+            load(0);
+        for (int i = 0; i < found; ++i) {
+            __syncthreads();  // (the last step's tiles have been read)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const Parts8 w = two_parts16<ACT>(xv[q]);
+                const int at = gofs((t >> 4) + 16 * q, 8 * (t & 15));
+                *(u32x4 *)(xt + at) = w.hi;
+                if constexpr (ACT == Q4_F16)
+                    *(u32x4 *)(xl + at) = w.lo;
+            }
+#pragma unroll
+            for (int q = 0; q < kPLoads; ++q) {
+                const int p = t + kGrBlock * q;
+                if (p < kPPieces) {
+                    const int row = p / (2 * RF), r = 8 * (p % (2 * RF));
+                    *(u32x4 *)(pt + gofs(row, r)) = pv[q].hi;
+                    *(u32x4 *)(pt + gofs(row, 64 + r)) = pv[q].lo;
+                }
+            }
+            __syncthreads();
+            if (i + 1 < found)
+                load(i + 1);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                Parts8 x[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    x[j].hi = column8(xt, h, 32 * wave + 16 * j);
+                    if constexpr (ACT == Q4_F16)
+                        x[j].lo = column8(xl, h, 32 * wave + 16 * j);
+                }
+#pragma unroll
+                for (int f = 0; f < RF; ++f) {
+                    const Parts8 p{column8(pt, h, 16 * f), column8(pt, h, 64 + 16 * f)};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        acc[f][j] = IS_B ? mfma_parts_b<ACT>(p, x[j], acc[f][j]) : mfma_parts_a<ACT>(x[j], p, acc[f][j]);
+                }
+            }
+        }
+    }
+
+    // dA: a lane has value r = fi of columns 4 fq ..; dB: column fi, values 4 fq ..
+#pragma unroll
+    for (int f = 0; f < RF; ++f) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int cb = c0 + 32 * wave + 16 * j;
+            const int r = r0 + 16 * f + (IS_B ? 4 * fq : fi), c = cb + (IS_B ? fi : 4 * fq);
+            if (r >= a.rank || c >= side.cols)
+                continue;
+            const int64_t at = IS_B ? ((int64_t)ad * side.cols + c) * a.rank + r : ((int64_t)ad * a.rank + r) * side.cols + c;
+            const f32x4 v = acc[f][j];
+            if (a.splits > 1)
+                *(f32x4 *)(a.sums + (int64_t)split * a.adapters * a.rank * ((int64_t)a.N + a.K) + side.out + at) = v;
+            else
+                *(u32x2 *)(side.g + at) = u32x2{pack2<ACT>(v[0], v[1]), pack2<ACT>(v[2], v[3])};
+        }
+    }
+}
+
+// blockIdx: x columns of x, then of dy; y adapters and slices of r; z parts of the rows.
+template <int ACT, int RF>
+__global__ __launch_bounds__(kGrBlock) void grad_kernel(GradArgs a, int slices)
+{
+    __shared__ __attribute__((aligned(16))) char xt[kGrRows * kGrPitch];
+    __shared__ __attribute__((aligned(16))) char xl[ACT == Q4_F16 ? kGrRows * kGrPitch : 16];
+    __shared__ __attribute__((aligned(16))) char pt[kGrRows * kGrPitch];
+    __shared__ uint16_t list[kGrList];
+    __shared__ int count;
+    const int kblocks = (a.K + kGrCols - 1) / kGrCols;
+    const int slice = blockIdx.y % slices, ad = blockIdx.y / slices;
+    const int64_t asize = (int64_t)a.adapters * a.rank * a.K;
+    if ((int)blockIdx.x < kblocks) {
+        const Side side{(const uint16_t *)a.x, a.u, a.K, 0, (uint16_t *)a.da};
+        grad<ACT, RF, false>(a, side, blockIdx.x, slice, ad, blockIdx.z, xt, xl, pt, list, &count);
+    } else {
+        const Side side{(const uint16_t *)a.dy, a.h, a.N, asize, (uint16_t *)a.db};
+        grad<ACT, RF, true>(a, side, blockIdx.x - kblocks, slice, ad, blockIdx.z, xt, xl, pt, list, &count);
+    }
+}
+
+// The parts' sums added in order and rounded: 4 values a thread (both outputs
+// are a multiple of 8 long).
+template <int ACT>
+__global__ __launch_bounds__(256) void grad_join_kernel(GradArgs a)
+{
+    const int64_t asize = (int64_t)a.adapters * a.rank * a.K, size = asize + (int64_t)a.adapters * a.rank * a.N;
+    const int64_t at = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    if (at >= size)
+        return;
+    f32x4 v = *(const f32x4 *)(a.sums + at);
+    for (int i = 1; i < a.splits; ++i) {
+        const f32x4 u = *(const f32x4 *)(a.sums + i * size + at);
+        v = f32x4{v[0] + u[0], v[1] + u[1], v[2] + u[2], v[3] + u[3]};
+    }
+    uint16_t *to = at < asize ? (uint16_t *)a.da + at : (uint16_t *)a.db + (at - asize);
+    *(u32x2 *)to = u32x2{pack2<ACT>(v[0], v[1]), pack2<ACT>(v[2], v[3])};
+}
+
+int grad_rf(int rank) { return rank <= 16 ? 1 : (rank <= 32 ? 2 : 4); }
+
+template <int ACT>
+hipError_t launch_grad_act(const GradArgs &a, hipStream_t s)
+{
+    const int rf = grad_rf(a.rank), slices = (a.rank + 16 * rf - 1) / (16 * rf);
+    const dim3 grid((unsigned)((a.K + kGrCols - 1) / kGrCols + (a.N + kGrCols - 1) / kGrCols),
+                    (unsigned)(a.adapters * slices), (unsigned)a.splits);
+    if (rf == 1)
+        hipLaunchKernelGGL((grad_kernel<ACT, 1>), grid, dim3(kGrBlock), 0, s, a, slices);
+    else if (rf == 2)
+        hipLaunchKernelGGL((grad_kernel<ACT, 2>), grid, dim3(kGrBlock), 0, s, a, slices);
+    else
+        hipLaunchKernelGGL((grad_kernel<ACT, 4>), grid, dim3(kGrBlock), 0, s, a, slices);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1)
+        return e;
+    const int64_t size = (int64_t)a.adapters * a.rank * ((int64_t)a.K + a.N);
+    hipLaunchKernelGGL((grad_join_kernel<ACT>), dim3((unsigned)((size / 4 + 255) / 256)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// Parts of the rows: as many as give every compute unit two workgroups, at
+// least four steps each, at most 8 (their sums are written and read).
+int grad_splits(int64_t rows, int64_t N, int64_t K, int adapters, int rank)
+{
+    const int rf = grad_rf(rank), slices = (rank + 16 * rf - 1) / (16 * rf);
+    const int64_t blocks = ((K + kGrCols - 1) / kGrCols + (N + kGrCols - 1) / kGrCols) * adapters * slices;
+    const int64_t steps = (rows + kGrRows - 1) / kGrRows;
+    int64_t n = 512 / blocks;
+    n = n < steps / 4 ? n : steps / 4;
+    return (int)(n < 1 ? 1 : (n > 8 ? 8 : n));
+}
+
+hipError_t launch_lora_grad(q4_dtype act_t, const GradArgs &a, hipStream_t s)
+{
+    return act_t == Q4_BF16 ? launch_grad_act<Q4_BF16>(a, s) : launch_grad_act<Q4_F16>(a, s);
+}
+
+}  // namespace q4

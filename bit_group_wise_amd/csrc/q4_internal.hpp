@@ -86,4 +86,61 @@ hipError_t launch_experts_tile256(q4_format f, int g, q4_dtype act_t, const Expe
 // The gradient dX[r] = dY[r] . What_e: x is dY, y is dX.
 hipError_t launch_experts_dx(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
 
+// Low-rank adapters beside a weight: h[m] = scale x[m] A^T and u[m] = scale
+// dy[m] B of each row's adapter, as `parts` partial sums [parts, rows, rank]
+// (x or dy NULL: h or u is not formed).
+struct DownArgs {
+    const void *x, *dy, *a, *b;
+    const float *scale;
+    const int32_t *ids;
+    float *h, *u;
+    int64_t rows;
+    int N, K, adapters, rank;
+    int slices, slots, parts;  // of the plan
+};
+// How they are cut: 16 mt rows, 16 rf values r and one of `parts` parts of the
+// long axis a workgroup, the adapters of a tile over `slots` workgroups.
+struct DownPlan {
+    int rf, mt, slices, slots, parts;
+    int64_t tiles;
+};
+DownPlan down_plan(int64_t rows, int64_t longest, int adapters, int rank, int both);
+hipError_t launch_down(q4_dtype act_t, DownArgs a, const DownPlan &p, hipStream_t s);
+
+// The products with the adapters' part added: y = x What^T + h B^T and dX = dY
+// What + u A.
+struct LoraArgs {
+    const void *x;  // or dY
+    int64_t M;
+    const uint8_t *codes;
+    const void *scales;
+    const uint8_t *zeros;
+    int64_t N, K;
+    const void *w;  // B [adapters, N, rank], or A [adapters, rank, K]
+    const int32_t *ids;
+    int adapters, rank;
+    const float *part;  // h or u as launch_down leaves it
+    int parts;
+    void *y;  // or dX
+};
+hipError_t launch_lora_skinny(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
+hipError_t launch_lora_tile128(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
+hipError_t launch_lora_tile256(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
+hipError_t launch_lora_dx(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
+
+// The adapters' gradients, dA[a] = sum u[m]^T x[m] and dB[a] = sum dy[m]^T
+// h[m] over the rows m of adapter a, in `splits` parts of the rows (more than
+// one: sums in `sums`, which launch_lora_grad joins).
+struct GradArgs {
+    const void *x, *dy;
+    const int32_t *ids;
+    const float *h, *u;
+    float *sums;
+    int64_t rows;
+    int N, K, adapters, rank, parts, splits;
+    void *da, *db;
+};
+int grad_splits(int64_t rows, int64_t N, int64_t K, int adapters, int rank);
+hipError_t launch_lora_grad(q4_dtype act_t, const GradArgs &a, hipStream_t s);
+
 }  // namespace q4

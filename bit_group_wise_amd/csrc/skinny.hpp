@@ -39,6 +39,7 @@
 #include "q4_common.hpp"
 #include "q4_internal.hpp"
 #include "q4_mfma.hpp"
+#include "lora.hpp"
 
 namespace q4 {
 namespace {
@@ -50,7 +51,7 @@ constexpr int kSkStep = 128;  // k per step
 #define Q4_SK_RING 2
 #endif
 constexpr int kSkRing = Q4_SK_RING;
-enum { kSkDense = 0, kSkGather = 1 };
+enum { kSkDense = 0, kSkGather = 1, kSkLora = 2 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t sk_rsrc(const void *base, int64_t bytes)
 {
@@ -87,7 +88,7 @@ __device__ __forceinline__ void skinny_product(const SkTask &task, const uint16_
                                                const uint8_t *__restrict__ codes,
                                                const void *__restrict__ scales,
                                                const uint8_t *__restrict__ zeros, int K, int gshift,
-                                               uint16_t *__restrict__ y)
+                                               uint16_t *__restrict__ y, const LowRank *low = nullptr)
 {
     constexpr int LF = level_fmt(FMT);
     __shared__ float2 ptbl[LF == Q4_NF4 ? 256 : 1];
@@ -194,6 +195,44 @@ __device__ __forceinline__ void skinny_product(const SkTask &task, const uint16_
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
             acc[b][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // the adapters' part, h B^T, 32 values r of one adapter a wave at a time
+    if constexpr (KIND == kSkLora) {
+        AdapterSet<1> set;
+        set.init(low->ids, low->adapters, 0, M);
+        int ad, turn = 0;
+        uint64_t mask[1];
+        while (set.next(ad, mask)) {
+            for (int rs = 0; rs < low->rank; rs += 32) {
+                if (turn++ % kSkWaves != wave)
+                    continue;
+                const int r0 = rs + 8 * q;
+                Parts8 h[MT];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    float v[8] = {};
+                    if (((mask[0] >> (16 * mt + r)) & 1) && r0 < low->rank)
+                        sum_parts(*low, 16 * mt + r, r0, v);
+                    h[mt] = two_parts(v);
+                }
+#pragma unroll
+                for (int b = 0; b < RB; ++b) {
+                    const int n = n0 + 16 * b + r;
+                    u32x4 v{0, 0, 0, 0};
+                    if (n < N && r0 < low->rank)
+                        v = *(const u32x4 *)(low->w + ((int64_t)ad * N + n) * low->rank + r0);
+                    const Parts8 w = two_parts16<ACT>(v);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const f32x4 t = mfma_parts_a<ACT>(w, h[mt], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+                        const bool mine = (mask[0] >> (16 * mt + r)) & 1;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[b][mt][e] = mine ? acc[b][mt][e] + t[e] : acc[b][mt][e];
+                    }
+                }
+            }
+        }
+    }
     for (int step = wave; step < nsteps; step += kSkWaves * kSkRing) {
 #pragma unroll
         for (int i = 0; i < kSkRing; ++i) {

@@ -39,6 +39,11 @@ SIGNATURES = {
     "q4_experts_gemm": (_int, [_int, _int, _int, _vp, _i64, _vp, _vp, _i64, _int, _vp, _vp, _vp, _i64, _i64,
                                _vp, _vp]),
     "q4_experts_gemm_dx": (_int, [_int, _int, _int, _vp, _vp, _i64, _int, _vp, _vp, _vp, _i64, _i64, _vp, _vp]),
+    # low-rank adapters beside a weight (bit_group_wise_amd.lora)
+    "q4_lora_workspace_bytes": (_sz, [_i64, _i64, _i64, _int, _int, _int]),
+    "q4_lora_gemm": (_int, [_int, _int, _int, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "q4_lora_backward": (_int, [_int, _int, _int, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp,
+                                _vp, _sz, _vp]),
     # the key/value cache (bit_group_wise_amd.kv)
     "q4_kv_append": (_int, [_vp, _vp, _int, _vp, _i64, _i64, _vp, _i64, _i64, _vp]),
     "q4_kv_read": (_int, [_vp, _vp, _int, _vp, _vp, _vp]),

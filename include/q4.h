@@ -291,6 +291,57 @@ q4_status q4_experts_gemm_dx(q4_format f, int g, q4_dtype act_t, const void *dy,
                              const uint8_t *codes, const void *scales, const uint8_t *zeros,
                              int64_t N, int64_t K, void *dx, void *stream);
 
+/* --------------------------------------- low-rank adapters beside a weight
+ * Fine-tuning leaves the 4-bit weight as it is and trains a pair of small
+ * matrices beside it; serving holds many such pairs and every row of the
+ * activations has its own, or none ("What is 4-bit quantization and why does
+ * it matter?", "QLoRA fine-tunes in 4-bit").
+ *   a      [adapters, rank, K] of act_t       (row-major, 16-byte aligned)
+ *   b      [adapters, N, rank] of act_t
+ *   scale  float32 [adapters] on the device, or NULL: 1
+ *   ids    int32 [M] on the device: each row's adapter; a number outside
+ *          0 .. adapters - 1 is none.  NULL: every row has adapter 0.
+ * Rows may come in any order; an adapter's weights meet its own rows alone.
+ * With a row's adapter (a, b, scale):
+ *   h = scale x a^T,   y = x What^T + h b^T
+ *   u = scale dy b,    dx = dy What + u a,
+ *   da = sum of u^T x and db = sum of dy^T h over the adapter's rows
+ * What as in q4_gemm.  Sums are binary32, h and u enter their second products
+ * with 16 bits (a relative 2^-17), and each output is rounded once to act_t.
+ * Results do not depend on timing (no floating-point atomics).
+ * rank is a multiple of 8 up to Q4_LORA_MAX_RANK; N rank and K rank below
+ * 2^30.  M = 0 is no work (gradients of the adapters: zeros).
+ * workspace: device memory of q4_lora_workspace_bytes for the same sizes,
+ * 256-byte aligned, needed until the call's work has run; its contents before
+ * and after do not matter (calls that may overlap need their own). */
+#define Q4_LORA_MAX_RANK 256
+#define Q4_LORA_MAX_ADAPTERS 16384
+#define Q4_LORA_MAX_ROWS 16777216
+typedef struct {
+    const void *a;
+    const void *b;
+    const float *scale;
+    const int32_t *ids;
+    int32_t adapters;
+    int32_t rank;
+} q4_lora;
+size_t q4_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int adapters, int rank,
+                               int backward);
+q4_status q4_lora_gemm(q4_format f, int g, q4_dtype act_t, const void *x, int64_t M,
+                       const uint8_t *codes, const void *scales, const uint8_t *zeros,
+                       int64_t N, int64_t K, const q4_lora *lora, void *y, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/* The backward pass: dx [M, K] (NULL: not wanted), and da [adapters, rank, K]
+ * and db [adapters, N, rank] (both NULL: not wanted, x is then not read), all
+ * of act_t and overwritten; adapters without rows get zeros.  N and K are
+ * limited and dy, dx aligned as in q4_gemm_dx. */
+q4_status q4_lora_backward(q4_format f, int g, q4_dtype act_t, const void *dy, const void *x,
+                           int64_t M, const uint8_t *codes, const void *scales,
+                           const uint8_t *zeros, int64_t N, int64_t K, const q4_lora *lora,
+                           void *dx, void *da, void *db, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
 /* ------------------------------------------------- the 4-bit key/value cache
  * Attention layers keep the keys and values of earlier tokens; here they are
  * held in the same 4 bits per value as the weights, and read by attention

@@ -1,0 +1,408 @@
+"""Low-rank adapters beside a 4-bit weight (q4_lora_*) against the formulas in
+binary64: every kernel, rank and mixture of adapters, gradients also against
+differences, and what an adapter or a row that is not finite may reach."""
+
+import ctypes
+
+import pytest
+import torch
+
+from bit_group_wise_amd import lora, q4
+from _groups import ACTS, DEV, FORMATS, generator, half_step, normal, tiny, values, weight
+
+pytestmark = pytest.mark.gpu
+
+
+def pairs_of(gen, act, adapters, rank, N, K, scale=True, size=1.0):
+    s = (torch.rand((adapters,), generator=gen, device=DEV) + 0.5) if scale else None
+    return lora.Adapters(normal(gen, act, adapters, rank, K, size=size * K ** -0.5),
+                         normal(gen, act, adapters, N, rank, size=rank ** -0.5), s)
+
+
+def ids_of(gen, M, adapters, kind):
+    if kind == "none":
+        return None
+    if kind == "runs":  # sorted, some rows with none
+        return (torch.arange(M, device=DEV) * (adapters + 1) // max(M, 1) - 1).int()
+    ids = torch.randint(-1, adapters + 1, (M,), generator=gen, device=DEV).int()  # -1 and `adapters`: none
+    if M > 3:
+        ids[M // 3], ids[M // 2] = 2 ** 31 - 1, -2 ** 31
+    return ids
+
+
+def of_rows(pairs, ids, M):
+    """[(adapter, its rows, its scale)] and matrices in binary64."""
+    ids = torch.zeros((M,), device=DEV) if ids is None else ids
+    scale = torch.ones((pairs.adapters,), device=DEV) if pairs.scale is None else pairs.scale
+    return [(i, (ids == i).nonzero()[:, 0], float(scale[i].double())) for i in range(pairs.adapters)]
+
+
+def assert_within(got, want, sums, act, tag):
+    """The sum's error, and the rounding of what it makes."""
+    assert bool(torch.isfinite(got).all()), f"{tag} not finite"
+    worst = ((got.double() - want).abs() - (sums + half_step(act) * (want.abs() + sums) + tiny(act))).max()
+    assert bool(worst <= 0), f"{tag} past the tolerance by {float(worst)}"
+
+
+# Errors relative to the sums of magnitudes: an addition in binary32 at most
+# 2^-23 (the matrix cores may cut where they do not round); h and u as two
+# bfloat16 numbers 2^-18 (2^-9 of 2^-9), fp16's product of second parts 2^-18:
+# 2^-17 together.
+def short(terms):
+    return terms * 2.0 ** -23
+
+
+TWO_PARTS = 2.0 ** -17
+
+
+def check(x, q, pairs, ids, tag="", **kw):
+    act = q4.F16 if x.dtype == torch.float16 else q4.BF16
+    M, K, R = x.shape[0], pairs.K, pairs.rank
+    y = lora.gemm(x, q, pairs, ids, **kw)
+    w, xd = values(q, act), x.double()
+    want, sums = xd @ w.T, short(K + 1) * (xd.abs() @ w.abs().T)
+    for i, rows, s in of_rows(pairs, ids, M):
+        a, b = pairs.a[i].double(), pairs.b[i].double()
+        want[rows] += s * (xd[rows] @ a.T) @ b.T
+        low = s * (xd[rows].abs() @ a.abs().T) @ b.abs().T
+        sums[rows] += low * (short(K + 16 + 3 * R) + TWO_PARTS)
+    assert_within(y, want, sums, act, tag)
+    return y
+
+
+def check_backward(dy, x, q, pairs, ids, tag="", **kw):
+    act = q4.F16 if x.dtype == torch.float16 else q4.BF16
+    M, N, K, R = x.shape[0], pairs.N, pairs.K, pairs.rank
+    dx, da, db = lora.backward(dy, x, q, pairs, ids, **kw)
+    w, xd, d = values(q, act), x.double(), dy.double()
+    want, sums = d @ w, short(N + 1) * (d.abs() @ w.abs())
+    for i, rows, s in of_rows(pairs, ids, M):
+        a, b, xr, dr = pairs.a[i].double(), pairs.b[i].double(), xd[rows], d[rows]
+        u, ub = s * dr @ b, s * dr.abs() @ b.abs()
+        h, hb = s * xr @ a.T, s * xr.abs() @ a.abs().T
+        want[rows] += u @ a
+        sums[rows] += (ub @ a.abs()) * (short(N + 16 + 3 * R) + TWO_PARTS)
+        many = 3 * len(rows) + 16
+        assert_within(da[i], u.T @ xr, (ub.T @ xr.abs()) * (short(N + many) + TWO_PARTS), act, f"{tag} da {i}")
+        assert_within(db[i], dr.T @ h, (dr.abs().T @ hb) * (short(K + many) + TWO_PARTS), act, f"{tag} db {i}")
+    assert_within(dx, want, sums, act, f"{tag} dx")
+    return dx, da, db
+
+
+@pytest.mark.parametrize("M", [1, 2, 16, 17, 33, 64, 65, 97, 256, 513])
+@pytest.mark.parametrize("kind,adapters,rank", [("none", 1, 16), ("runs", 3, 8), ("mixed", 5, 40), ("mixed", 70, 64)])
+def test_rows(M, kind, adapters, rank):
+    gen = generator(M + rank)
+    fmt, act = FORMATS[(M + rank) % 5], (M + rank) // 8 % 2
+    q = weight(144, 320, fmt, 32, gen)
+    pairs = pairs_of(gen, act, adapters, rank, 144, 320)
+    ids = ids_of(gen, M, adapters, kind)
+    x, dy = normal(gen, act, M, 320), normal(gen, act, M, 144)
+    check(x, q, pairs, ids)
+    check_backward(dy, x, q, pairs, ids)
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 48, 64, 72, 128, 200, 256])
+@pytest.mark.parametrize("M", [5, 70, 150])
+@pytest.mark.parametrize("act", [q4.F16, q4.BF16])
+def test_ranks(rank, M, act):
+    gen = generator(rank + M)
+    q = weight(80, 256, q4.NF4, 64, gen)
+    pairs = pairs_of(gen, act, 3, rank, 80, 256)
+    ids = ids_of(gen, M, 3, "mixed")
+    x, dy = normal(gen, act, M, 256), normal(gen, act, M, 80)
+    check(x, q, pairs, ids)
+    check_backward(dy, x, q, pairs, ids)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("g", [32, 64, 128])
+@pytest.mark.parametrize("act", [q4.F16, q4.BF16])
+def test_formats(fmt, g, act):
+    gen = generator(fmt * 7 + g)
+    N, K = 264, 640
+    q = weight(N, K, fmt, g, gen)
+    pairs = pairs_of(gen, act, 2, 16, N, K)
+    for M in (3, 30, 60, 200, 600):
+        ids = ids_of(gen, M, 2, "runs")
+        x, dy = normal(gen, act, M, K), normal(gen, act, M, N)
+        check(x, q, pairs, ids, f"M {M}")
+        if M in (3, 600):
+            check_backward(dy, x, q, pairs, ids, f"M {M}")
+
+
+@pytest.mark.parametrize("N,K", [(1, 32), (79, 96), (130, 1120), (257, 4096), (1000, 64)])
+@pytest.mark.parametrize("M", [1, 40, 130, 520])
+def test_odd_sizes(M, N, K):
+    gen = generator(M + N + K)
+    q = weight(N, K, q4.INT4_ASYM, 32, gen)
+    pairs = pairs_of(gen, q4.BF16, 4, 24, N, K)
+    ids = ids_of(gen, M, 4, "mixed")
+    check(normal(gen, q4.BF16, M, K), q, pairs, ids)
+
+
+@pytest.mark.parametrize("N,K", [(8, 32), (72, 96), (136, 1120), (264, 4096), (4096, 64)])
+@pytest.mark.parametrize("M", [1, 40, 130, 1100])
+def test_odd_gradients(M, N, K):
+    gen = generator(M + N + K)
+    q = weight(N, K, q4.INT4_ASYM, 32, gen)
+    pairs = pairs_of(gen, q4.F16, 4, 24, N, K)
+    ids = ids_of(gen, M, 4, "mixed")
+    check_backward(normal(gen, q4.F16, M, N), normal(gen, q4.F16, M, K), q, pairs, ids)
+
+
+def test_many_rows_of_one_adapter():
+    """Rows split over workgroups, their sums joined; no ids, no scale."""
+    gen = generator(6)
+    q = weight(256, 512, q4.NF4_DQ, 64, gen)
+    for act in (q4.F16, q4.BF16):
+        pairs = pairs_of(gen, act, 1, 64, 256, 512, scale=False)
+        x, dy = normal(gen, act, 5000, 512), normal(gen, act, 5000, 256)
+        check(x, q, pairs, None)
+        check_backward(dy, x, q, pairs, None)
+
+
+def test_every_row_its_own_adapter():
+    gen = generator(8)
+    M = 300
+    q = weight(64, 128, q4.NF4, 64, gen)
+    pairs = pairs_of(gen, q4.BF16, M, 8, 64, 128)
+    ids = torch.randperm(M, generator=gen, device=DEV).int()
+    x, dy = normal(gen, q4.BF16, M, 128), normal(gen, q4.BF16, M, 64)
+    check(x, q, pairs, ids)
+    check_backward(dy, x, q, pairs, ids)
+    check(x[:64], q, pairs, ids[:64])
+
+
+@pytest.mark.parametrize("M", [3, 64, 200, 600])
+def test_rows_without_an_adapter_are_the_products_own(M):
+    """The same bits as q4.gemm and q4.gemm_dx, and gradients of zero."""
+    gen = generator(M)
+    q = weight(128, 256, q4.INT4_SYM, 64, gen)
+    pairs = pairs_of(gen, q4.BF16, 2, 16, 128, 256)
+    ids = torch.full((M,), -1, dtype=torch.int32, device=DEV)
+    x, dy = normal(gen, q4.BF16, M, 256), normal(gen, q4.BF16, M, 128)
+    assert torch.equal(lora.gemm(x, q, pairs, ids), q4.gemm(x, q))
+    dx, da, db = lora.backward(dy, x, q, pairs, ids)
+    assert torch.equal(dx, q4.gemm_dx(dy, q))
+    assert not da.any() and not db.any()
+
+
+@pytest.mark.parametrize("M", [20, 90, 300, 700])
+@pytest.mark.parametrize("act", [q4.F16, q4.BF16])
+def test_an_adapter_that_is_not_finite_reaches_its_own_rows_alone(M, act):
+    gen = generator(M)
+    q = weight(72, 96, q4.NF4, 32, gen)
+    pairs = pairs_of(gen, act, 4, 24, 72, 96)
+    ids = ids_of(gen, M, 4, "mixed")
+    x, dy = normal(gen, act, M, 96), normal(gen, act, M, 72)
+    clean, grads = lora.gemm(x, q, pairs, ids), lora.backward(dy, x, q, pairs, ids)
+    for part, bad in (("a", float("nan")), ("b", float("inf")), ("scale", float("nan"))):
+        new = lora.Adapters(pairs.a.clone(), pairs.b.clone(), pairs.scale.clone())
+        getattr(new, part)[2] = bad
+        others = ids != 2
+        y, (dx, da, db) = lora.gemm(x, q, new, ids), lora.backward(dy, x, q, new, ids)
+        assert torch.equal(y[others], clean[others]) and not torch.isfinite(y[~others]).all()
+        assert torch.equal(dx[others], grads[0][others])
+        for got, want in ((da, grads[1]), (db, grads[2])):
+            assert torch.equal(got[[0, 1, 3]], want[[0, 1, 3]])
+
+
+@pytest.mark.parametrize("M", [20, 90, 300, 700])
+@pytest.mark.parametrize("N,K", [(72, 96), (128, 512)])
+def test_a_row_that_is_not_finite_reaches_its_own_alone(M, N, K):
+    gen = generator(M + K)
+    q = weight(N, K, q4.INT4_ASYM, 32, gen)
+    pairs = pairs_of(gen, q4.BF16, 3, 16, N, K)
+    ids = ids_of(gen, M, 3, "mixed")
+    bad = M // 2 + 1
+    ids[bad] = 1
+    x, dy = normal(gen, q4.BF16, M, K), normal(gen, q4.BF16, M, N)
+    clean, grads = lora.gemm(x, q, pairs, ids), lora.backward(dy, x, q, pairs, ids)
+    x[bad], dy[bad] = float("nan"), float("inf")
+    keep = torch.arange(M, device=DEV) != bad
+    y, (dx, da, db) = lora.gemm(x, q, pairs, ids), lora.backward(dy, x, q, pairs, ids)
+    assert torch.equal(y[keep], clean[keep]) and bool(torch.isnan(y[bad]).all())
+    assert torch.equal(dx[keep], grads[0][keep]) and not torch.isfinite(dx[bad]).any()
+    for got, want in ((da, grads[1]), (db, grads[2])):
+        assert torch.equal(got[[0, 2]], want[[0, 2]])
+
+
+@pytest.mark.parametrize("M", [4, 100, 600])
+def test_fp16_far_from_one(M):
+    """h past fp16's range, and gradients below it, in fp16."""
+    gen = generator(M)
+    N, K = 96, 512
+    q = weight(N, K, q4.NF4, 64, gen)
+    a = normal(gen, q4.F16, 1, 16, K, size=40.0)
+    x = normal(gen, q4.F16, M, K, size=100.0)
+    b = normal(gen, q4.F16, 1, N, 16, size=1e-3)
+    pairs = lora.Adapters(a, b)
+    assert float((x.double() @ a[0].double().T).abs().max()) > 65504
+    check(x, q, pairs, None)
+    # u is about 2^-24 and smaller; its products are numbers again
+    dy = normal(gen, q4.F16, M, N, size=1e-4)
+    pairs = lora.Adapters(normal(gen, q4.F16, 1, 16, K, size=1000.0), normal(gen, q4.F16, 1, N, 16, size=1e-4))
+    assert float((dy.double() @ pairs.b[0].double()).abs().max()) < 2.0 ** -17
+    check_backward(dy, x, q, pairs, None)
+
+
+def test_gradients_against_differences():
+    """Along a direction, with y in binary64: what the gradients say up to their rounding."""
+    gen = generator(11)
+    M, N, K, R = 150, 64, 96, 16
+    act = q4.BF16
+    q = weight(N, K, q4.NF4, 32, gen)
+    pairs = pairs_of(gen, act, 2, R, N, K)
+    ids = ids_of(gen, M, 2, "mixed")
+    x, dy = normal(gen, act, M, K), normal(gen, act, M, N)
+    grads = lora.backward(dy, x, q, pairs, ids)
+    w = values(q, act)
+
+    def loss(x, a, b):
+        y = x @ w.T
+        for i, rows, s in of_rows(pairs, ids, M):
+            y[rows] = y[rows] + s * (x[rows] @ a[i].T) @ b[i].T
+        return float((y * dy.double()).sum())
+
+    at = [x.double(), pairs.a.double(), pairs.b.double()]
+    for k, g in enumerate(grads):
+        way = torch.randn(at[k].shape, generator=gen, device=DEV, dtype=torch.float64)
+        step = 1e-3
+        ahead, behind = list(at), list(at)
+        ahead[k], behind[k] = at[k] + step * way, at[k] - step * way
+        rate = (loss(*ahead) - loss(*behind)) / (2 * step)  # (exact: the loss is linear in each)
+        said, rough = float((g.double() * way).sum()), float((g.double() * way).abs().sum())
+        assert abs(rate - said) <= rough * (half_step(act) + TWO_PARTS + short(M * 4)) + 1e-6 * rough
+
+
+def test_parts_alone_and_again():
+    """Each output alone, twice, into given tensors and from a workspace full of NaN: the same bits."""
+    gen = generator(12)
+    M, N, K = 700, 128, 256
+    q = weight(N, K, q4.INT4_SYM, 64, gen)
+    pairs = pairs_of(gen, q4.F16, 3, 40, N, K)
+    ids = ids_of(gen, M, 3, "mixed")
+    x, dy = normal(gen, q4.F16, M, K), normal(gen, q4.F16, M, N)
+    y, (dx, da, db) = lora.gemm(x, q, pairs, ids), lora.backward(dy, x, q, pairs, ids)
+    work = torch.full((lora.workspace_bytes(M, pairs, True),), 255, dtype=torch.uint8, device=DEV)
+    assert torch.equal(lora.gemm(x, q, pairs, ids, workspace=work), y)
+    work.fill_(255)
+    out = [torch.full_like(t, float("nan")) for t in (dx, da, db)]
+    got = lora.backward(dy, x, q, pairs, ids, out=out, workspace=work)
+    for a, b, c in zip(got, out, (dx, da, db)):
+        assert a is b and torch.equal(a, c)
+    got = lora.backward(dy, None, q, pairs, ids, need_pairs=False)
+    assert torch.equal(got[0], dx) and got[1] is None and got[2] is None
+    got = lora.backward(dy, x, q, pairs, ids, need_dx=False)
+    assert got[0] is None and torch.equal(got[1], da) and torch.equal(got[2], db)
+
+
+def test_no_rows():
+    gen = generator(1)
+    q = weight(64, 64, q4.NF4, 64, gen)
+    pairs = pairs_of(gen, q4.BF16, 2, 8, 64, 64)
+    x = normal(gen, q4.BF16, 0, 64)
+    assert lora.gemm(x, q, pairs).shape == (0, 64)
+    dx, da, db = lora.backward(x, x, q, pairs)
+    assert dx.shape == (0, 64) and not da.any() and not db.any()
+
+
+def test_captured_and_replayed():
+    """With other adapters, ids and activations between replays, eager work beside it."""
+    gen = generator(13)
+    M, N, K = 130, 96, 128
+    q = weight(N, K, q4.NF4, 64, gen)
+    pairs = pairs_of(gen, q4.BF16, 3, 16, N, K)
+    ids = ids_of(gen, M, 3, "mixed")
+    x, dy = normal(gen, q4.BF16, M, K), normal(gen, q4.BF16, M, N)
+    few, work, more = x[:5], [torch.empty((lora.workspace_bytes(M, pairs, True),), dtype=torch.uint8, device=DEV)
+                              for _ in range(2)], lora.workspace_bytes(5, pairs)
+    few_ids = ids[:5]
+
+    def calls():
+        return (lora.gemm(x, q, pairs, ids, workspace=work[0]), *lora.backward(dy, x, q, pairs, ids, workspace=work[0]),
+                lora.gemm(few, q, pairs, few_ids, workspace=work[1][:more]))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        outs = calls()
+    for seed in range(4):
+        gen = generator(100 + seed)
+        pairs.a.copy_(normal(gen, q4.BF16, 3, 16, K, size=K ** -0.5))
+        pairs.b.copy_(normal(gen, q4.BF16, 3, N, 16))
+        ids.copy_(ids_of(gen, M, 3, "mixed"))
+        x.copy_(normal(gen, q4.BF16, M, K))
+        graph.replay()
+        got = [t.clone() for t in outs]
+        torch.cuda.synchronize()
+        want = (lora.gemm(x, q, pairs, ids), *lora.backward(dy, x, q, pairs, ids), lora.gemm(few, q, pairs, few_ids))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_on_another_stream():
+    gen = generator(14)
+    M, N, K = 40, 96, 128
+    q = weight(N, K, q4.NF4, 64, gen)
+    pairs = pairs_of(gen, q4.BF16, 3, 16, N, K)
+    ids = ids_of(gen, M, 3, "mixed")
+    x, dy = normal(gen, q4.BF16, M, K), normal(gen, q4.BF16, M, N)
+    want = (lora.gemm(x, q, pairs, ids), *lora.backward(dy, x, q, pairs, ids))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = (lora.gemm(x, q, pairs, ids), *lora.backward(dy, x, q, pairs, ids))
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_outputs_at_any_two_bytes():
+    gen = generator(15)
+    N, K = 72, 64
+    q = weight(N, K, q4.INT4_SYM, 32, gen)
+    pairs = pairs_of(gen, q4.BF16, 2, 8, N, K)
+    for M in (5, 90, 200, 600):
+        x = normal(gen, q4.BF16, M, K)
+        flat = torch.full((M * N + 8,), 3.0, dtype=x.dtype, device=DEV)
+        check(x, q, pairs, None, out=flat[3:3 + M * N].view(M, N))
+        assert bool((flat[:3] == 3).all()) and bool((flat[3 + M * N:] == 3).all())
+
+
+def test_arguments():
+    gen = generator(2)
+    q = weight(64, 64, q4.NF4, 64, gen)
+    pairs = pairs_of(gen, q4.BF16, 2, 8, 64, 64)
+    x = normal(gen, q4.BF16, 6, 64)
+    ids = torch.zeros((6,), dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError):
+        lora.Adapters(pairs.a, pairs.b[:, :, :4].contiguous())
+    with pytest.raises(TypeError):
+        lora.Adapters(pairs.a.float(), pairs.b.float())
+    with pytest.raises(TypeError):
+        lora.Adapters(pairs.a, pairs.b.half())
+    with pytest.raises(ValueError):
+        lora.Adapters(pairs.a, pairs.b, torch.ones((3,), device=DEV))
+    with pytest.raises(TypeError):
+        lora.gemm(x.half(), q, pairs, ids)
+    with pytest.raises(ValueError):
+        lora.gemm(x, q, pairs, ids[:5])
+    with pytest.raises(TypeError):
+        lora.gemm(x, q, pairs, ids.long())
+    with pytest.raises(ValueError):
+        lora.gemm(x.cpu(), q, pairs)
+    with pytest.raises(ValueError):
+        lora.gemm(x, weight(128, 64, q4.NF4, 64, gen), pairs)
+    with pytest.raises(ValueError):
+        lora.backward(x, x[:5], q, pairs)
+    small = torch.empty((lora.workspace_bytes(6, pairs) - 1,), dtype=torch.uint8, device=DEV)
+    with pytest.raises(q4.Q4Error) as e:
+        lora.gemm(x, q, pairs, workspace=small)
+    assert e.value.status == q4.EINVAL
+    assert ctypes.sizeof(lora._LoraArgs) == 40
