@@ -232,29 +232,41 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
     if constexpr (KIND == kDxLora) {
         constexpr int C = TM / 64;
         const int rows = M - m0 < TM ? M - m0 : TM;
+        AdapterSet<C> all;
+        all.init(low->ids, low->adapters, m0, rows);
         for (int rc = 0; rc < low->rank; rc += 64) {
             for (int p = t; p < TM * 8; p += kBlock) {
                 const int row = p >> 3, ch = p & 7;
-                float v[8] = {};
-                if (row < rows && rc + 8 * ch < low->rank)
-                    sum_parts(*low, m0 + row, rc + 8 * ch, v);
-                const Parts8 q = two_parts(v);
+                u32x4 q[2] = {};
+                if (row < rows && rc + 8 * ch < low->rank) {
+                    const uint16_t *from = low->two + (m0 + row) * (int64_t)low->rank + rc + 8 * ch;
+                    q[0] = *(const u32x4 *)from;
+                    q[1] = *(const u32x4 *)(from + low->rows * low->rank);
+                }
                 const int at = row * kYRow + 16 * yswz(row, ch);
-                *(u32x4 *)(ys[0] + at) = q.hi;
-                *(u32x4 *)(ys[1] + at) = q.lo;
+                *(u32x4 *)(ys[0] + at) = q[0];
+                *(u32x4 *)(ys[1] + at) = q[1];
             }
-            AdapterSet<C> set;
-            set.init(low->ids, low->adapters, m0, rows);
+            AdapterSet<C> set = all;
             int ad;
-            uint64_t mask[C];
-            while (set.next(ad, mask)) {
+            uint64_t mask[C], next[C] = {};
+            u32x4 v[2];
+            auto load = [&]() {  // the adapter's rows, the next one's while one is worked on
                 const int r = rc + (t >> 3), k = k0 + 16 * (t & 7);
-                u32x4 v[2] = {};
+                v[0] = v[1] = u32x4{0, 0, 0, 0};
                 if (r < low->rank && k < K) {
                     const u32x4 *w = (const u32x4 *)(low->w + ((int64_t)ad * low->rank + r) * K + k);
                     v[0] = w[0];
                     v[1] = w[1];
                 }
+            };
+            bool on = set.next(ad, next);
+            if (on)
+                load();
+            while (on) {
+#pragma unroll
+                for (int q = 0; q < C; ++q)
+                    mask[q] = next[q];
                 __syncthreads();  // (the last adapter's rows have been read)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -263,6 +275,9 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
                     if constexpr (ACT == Q4_F16)
                         *(u32x4 *)(wt[1] + wofs(t >> 3, 16 * (t & 7) + 8 * e)) = w.lo;
                 }
+                on = set.next(ad, next);
+                if (on)
+                    load();
                 __syncthreads();
 #pragma unroll
                 for (int j = 0; j < kKF; ++j) {

@@ -378,45 +378,66 @@ struct Tile {
 // The tile's accumulators as the adapters' part makes them, h B^T, with the
 // same operand roles, fragment positions and staging as a K step: 64 values r
 // of all x rows of h as the step's x, its two parts in the two x buffers, and
-// B [n][r] straight from memory as the weights.  (One step of 2 or 3 products
-// against the K / 64 of the product itself.)
+// B [n][r] straight from memory as the weights, the next adapter's while one
+// is worked on.  (One step of 2 or 3 products against the K / 64 of the
+// product itself.)
 template <int ACT>
 __device__ __forceinline__ void lora_start(f32x4 (&acc)[kNF][kMF], const LowRank &l, const TileCtx &c, char *xs0,
                                            char *xs1, int m0, int mend, int wave, int fr, int nrow, int N)
 {
+    const int lane = threadIdx.x & 63;
     const int rows = min(mend - m0, BM);
     constexpr int C = (BM + 63) / 64;
+    AdapterSet<C> all;
+    all.init(l.ids, l.adapters, m0, rows);
+    const View hv = make_view(l.two + (int64_t)m0 * l.rank, (int64_t)rows * l.rank * 2);
+    const View lv = make_view(l.two + (l.rows + m0) * l.rank, (int64_t)rows * l.rank * 2);
+    // (uniform loops: the workgroup's waves all stage, meet and work together)
     for (int rc = 0; rc < l.rank; rc += 64) {
-        // (uniform loop: the workgroup's threads all stage and meet here)
-        for (int p = threadIdx.x; p < BM * 8; p += kBlock) {
-            const int row = p >> 3, ch = p & 7;
-            float v[8] = {};
-            if (row < rows && rc + 8 * ch < l.rank)
-                sum_parts(l, m0 + row, rc + 8 * ch, v);
-            const Parts8 q = two_parts(v);
-            const int at = row * ROW_BYTES + 16 * swz(row, ch);
-            *(u32x4 *)(xs0 + at) = q.hi;
-            *(u32x4 *)(xs1 + at) = q.lo;
+#pragma unroll
+        for (int i = 0; i < kXBlocks; ++i) {
+            const int B = kXBlocks * wave + i, row = 8 * B + (lane >> 3), r = rc + c.xk[i & 1];
+            const uint32_t v = r < l.rank ? 2u * (uint32_t)(row * l.rank + r) : kNowhere;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                at(hv, 0), (__attribute__((address_space(3))) void *)(xs0 + 1024 * B), 16, (int)v, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                at(lv, 0), (__attribute__((address_space(3))) void *)(xs1 + 1024 * B), 16, (int)v, 0, 0, 0);
         }
-        __syncthreads();
-        AdapterSet<C> set;
-        set.init(l.ids, l.adapters, m0, rows);
+        AdapterSet<C> set = all;
         int ad;
-        uint64_t mask[C];
-        while (set.next(ad, mask)) {
-            Parts8 b[kNF][2];
+        uint64_t mask[C], next[C] = {};
+        u32x4 raw[kNF][2];
+        auto load = [&]() {
             const uint16_t *w = l.w + (int64_t)ad * N * l.rank;
 #pragma unroll
             for (int j = 0; j < kNF; ++j) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int n = nrow + 4 * j, r = rc + 16 * c.fq + 8 * h;
-                    u32x4 v{0, 0, 0, 0};
+                    raw[j][h] = u32x4{0, 0, 0, 0};
                     if (n < N && r < l.rank)
-                        v = *(const u32x4 *)(w + (int64_t)n * l.rank + r);
-                    b[j][h] = two_parts16<ACT>(v);
+                        raw[j][h] = *(const u32x4 *)(w + (int64_t)n * l.rank + r);
                 }
             }
+        };
+        bool on = set.next(ad, next);
+        if (on)
+            load();
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // h is in LDS
+        __syncthreads();
+        while (on) {
+            Parts8 b[kNF][2];
+#pragma unroll
+            for (int j = 0; j < kNF; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    b[j][h] = two_parts16<ACT>(raw[j][h]);
+#pragma unroll
+            for (int q = 0; q < C; ++q)
+                mask[q] = next[q];
+            on = set.next(ad, next);
+            if (on)
+                load();
 #pragma unroll
             for (int i = 0; i < kMF; ++i) {
                 if (((mask[i / 4] >> (16 * (i % 4))) & 0xffff) == 0)

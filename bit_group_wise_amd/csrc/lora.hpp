@@ -2,10 +2,9 @@
 // weight (q4_lora_*).
 //
 // An adapter adds s (x A^T) B^T to a row's product.  The rows' h = s x A^T
-// (and for gradients u = s dy B) are formed first, in binary32, as a few
-// partial sums over the long axis in the workspace; the product's own kernel
-// then adds h B^T (or u A) to its binary32 accumulators, so the sum is rounded
-// once and y is written once.
+// (and for gradients u = s dy B) are formed first, summed in binary32, and left
+// in the workspace; the product's own kernel then adds h B^T (or u A) to its
+// binary32 accumulators, so the sum is rounded once and y is written once.
 //
 // Operands: the matrix cores take 16 bits, so h and u enter as two bfloat16
 // numbers, the value's rounding and the rounding of what that left: 16 bits
@@ -21,11 +20,14 @@
 
 namespace q4 {
 
-// h[m][r] (or u) as partial sums: part[i * rows * rank + m * rank + r], i <
-// parts, and what they go through.
+// h[m][r] (or u) and what they go through.  For few rows h is left as binary32
+// partial sums, part[i * rows * rank + m * rank + r] for i < parts; else as its
+// operands' two parts, two[m * rank + r] and two[(rows + m) * rank + r].
 struct LowRank {
     const float *part;
-    int parts, rank, adapters;
+    int parts;
+    const uint16_t *two;
+    int rank, adapters;
     int64_t rows;
     const int32_t *ids;  // adapter of each row, or NULL: all 0
     const uint16_t *w;   // B [adapters, N, rank] or A [adapters, rank, K]

@@ -48,7 +48,8 @@ q4_status check_lora(q4_format f, int g, q4_dtype act_t, int64_t M, const void *
 
 int64_t padded(int64_t floats) { return (4 * floats + 255) / 256 * 256; }
 
-// The workspace: h, then (backward) u and the gradients' sums.
+// The workspace: h, then (backward) u, then sums that are joined: of the parts
+// of h and u, later of the gradients.
 struct Layout {
     DownPlan plan;
     int splits;
@@ -58,11 +59,15 @@ Layout layout(int64_t M, int64_t N, int64_t K, int adapters, int rank, int backw
 {
     Layout w{};
     w.plan = down_plan(M, backward && N > K ? N : K, adapters, rank, backward);
-    const int64_t part = padded((int64_t)w.plan.parts * M * rank);
+    // (two 16-bit parts are as long as one of 32)
+    const int64_t one = padded((int64_t)(w.plan.two ? 1 : w.plan.parts) * M * rank);
+    const int kinds = backward ? 2 : 1;
     w.splits = backward ? grad_splits(M, N, K, adapters, rank) : 1;
-    w.u = part;
-    w.sums = 2 * part;
-    w.bytes = !backward ? part : 2 * part + (w.splits > 1 ? padded((int64_t)w.splits * adapters * rank * (N + K)) : 0);
+    w.u = one;
+    w.sums = kinds * one;
+    const int64_t joined = w.plan.two && w.plan.parts > 1 ? padded((int64_t)kinds * w.plan.parts * M * rank) : 0;
+    const int64_t grads = w.splits > 1 ? padded((int64_t)w.splits * adapters * rank * (N + K)) : 0;
+    w.bytes = w.sums + (joined > grads ? joined : grads);
     return w;
 }
 
@@ -97,7 +102,8 @@ q4_status q4_lora_gemm(q4_format f, int g, q4_dtype act_t, const void *x, int64_
     d.a = lora->a;
     d.scale = lora->scale;
     d.ids = lora->ids;
-    d.h = (float *)workspace;
+    d.h = workspace;
+    d.sums = (float *)((char *)workspace + w.sums);
     d.rows = M;
     d.N = (int)N;
     d.K = (int)K;
@@ -147,8 +153,9 @@ q4_status q4_lora_backward(q4_format f, int g, q4_dtype act_t, const void *dy, c
     d.b = lora->b;
     d.scale = lora->scale;
     d.ids = lora->ids;
-    d.h = (float *)workspace;
-    d.u = (float *)((char *)workspace + w.u);
+    d.h = workspace;
+    d.u = (char *)workspace + w.u;
+    d.sums = (float *)((char *)workspace + w.sums);
     d.rows = M;
     d.N = (int)N;
     d.K = (int)K;
@@ -161,8 +168,9 @@ q4_status q4_lora_backward(q4_format f, int g, q4_dtype act_t, const void *dy, c
         e = launch_lora_dx(f, g, act_t, a, s);
     }
     if (e == hipSuccess && da) {
-        const GradArgs a{x, dy, lora->ids, d.h, d.u, (float *)((char *)workspace + w.sums), M, (int)N, (int)K,
-                         lora->adapters, lora->rank, w.plan.parts, w.splits, da, db};
+        const GradArgs a{x, dy, lora->ids, (const uint16_t *)d.h, (const uint16_t *)d.u,
+                         d.sums, M, (int)N, (int)K, lora->adapters, lora->rank,
+                         w.splits, da, db};
         e = launch_lora_grad(act_t, a, s);
     }
     return from_hip(e);

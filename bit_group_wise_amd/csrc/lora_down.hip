@@ -1,27 +1,31 @@
 // lora_down.hip -- the rows' products with the adapters' long sides, h[m] =
-// s x[m] A^T and u[m] = s dy[m] B, as binary32 partial sums.
+// s x[m] A^T and u[m] = s dy[m] B.
 //
 // Both contract a long axis (K or N, thousands) to at most 256 values a row,
 // so they are bound by reading x (or dy), and with a few rows by reading the
-// adapters.  A workgroup of 4 waves takes 16 MT rows, up to 16 RF values r and
-// one part of the long axis, over whose steps its waves alternate; their sums
-// meet in LDS, and the parts in the kernel that reads them (which adds them in
-// order: no atomics).
-//  * The matrix cores' first operand is the adapter (16 values r), the second
-//    16 rows, so a result lane holds 4 consecutive r of one row.
-//  * A [rank, K] is read as it lies, 8 consecutive k a lane.  B [N, rank] has
-//    the contraction in its rows: a wave stages 32 rows in its own LDS and
-//    takes them back transposed (ds_read_b64_tr_b16, see gemm_dx_tile.hpp).
-//  * Rows of several adapters are done adapter by adapter; where rows are few
-//    the adapters of a tile are spread over workgroups.
+// adapters.  A [rank, K] is read as it lies, 8 consecutive k a lane; B [N,
+// rank] has the contraction in its rows and comes from LDS transposed
+// (ds_read_b64_tr_b16, see gemm_dx_tile.hpp).  The matrix cores' first operand
+// is the adapter (16 values r), the second 16 rows, so a result lane holds 4
+// consecutive r of one row.  Rows of several adapters are done adapter by
+// adapter; where rows are few the adapters are spread over workgroups.
+//  * Few rows (q4_lora_gemm up to 96): 16 rows a workgroup of 4 waves, whose
+//    waves alternate over the long axis' steps of 32 with the operands straight
+//    in registers.  The axis is cut into parts on different workgroups, whose
+//    binary32 sums the kernel that reads them adds in order (no atomics).
+//  * More: 64 rows a workgroup, both operands staged in LDS 64 of the axis at a
+//    time, so that a row's lines are read whole and the adapter's matrix once
+//    for 64 rows: what a compute unit can load (20 to 40 bytes a cycle) is the
+//    limit, and with 16 rows a workgroup half of it was the adapter's matrix
+//    (25 and 40 us on 2048 rows of 4096 with rank 32 and of 11008 with rank 16).
+//    The axis' parts are joined by a second launch, which also splits the sums
+//    into the two bfloat16 operands that their readers need.  (Readers that add
+//    up 8 parts spent 20 to 130 us on it, one latency after another.)
 #include "lora.hpp"
 #include "q4_internal.hpp"
 
 namespace q4 {
 namespace {
-
-constexpr int kDnWaves = 4;
-constexpr int kDnBlock = 64 * kDnWaves;
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 
@@ -32,36 +36,147 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t dn_rsrc(const void *base, int6
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n, 0x00020000);
 }
 
-// One step's operands: 32 of the long axis for the adapter (as read: of A 8
-// consecutive values of a row r a lane; of B 16-byte pieces of its rows) and
-// for the rows.
-template <int RF, int MT>
-struct DnStep {
+constexpr int kMostParts = 8;
+
+// Four values as their two bfloat16 parts, at two[to] and two[size + to].
+__device__ __forceinline__ void store_two(uint16_t *two, int64_t size, int64_t to, const f32x4 &v)
+{
+    const u32x2 hi{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3])};
+    const u32x2 lo{pack_bf2(v[0] - std::bit_cast<float>(hi[0] << 16), v[1] - std::bit_cast<float>(hi[0] & 0xffff0000u)),
+                   pack_bf2(v[2] - std::bit_cast<float>(hi[1] << 16), v[3] - std::bit_cast<float>(hi[1] & 0xffff0000u))};
+    *(u32x2 *)(two + to) = hi;
+    *(u32x2 *)(two + size + to) = lo;
+}
+
+// ---------------------------------------------------------------- few rows
+constexpr int kFewWaves = 4, kFewBlock = 64 * kFewWaves;
+
+// One step's operands: 32 of the long axis for the adapter (8 consecutive
+// values of a row r a lane) and for the rows.
+template <int RF>
+struct FewStep {
     u32x4 w[RF];
-    u32x4 x[MT];
+    u32x4 x;
 };
 
-// Bytes of a staged row of B (not a multiple of 64: rows spread over the banks).
-constexpr int dn_pitch(int rf) { return 32 * rf + 16; }
-
-template <int ACT, int RF, int MT, bool TRANS>
-__device__ __forceinline__ void down(const uint16_t *__restrict__ x, const DownArgs &a, const uint16_t *__restrict__ w,
-                                     float *__restrict__ part, int len, int slice, int slot, int split,
-                                     f32x4 (&red)[kDnWaves][RF][MT][64], char *stages)
+// blockIdx: x the rows, y the part of the long axis, z slices of r and
+// adapters' slots.
+template <int ACT, int RF>
+__global__ __launch_bounds__(kFewBlock) void down_few_kernel(DownArgs a)
 {
-    constexpr int kPitch = dn_pitch(RF);
+    __shared__ f32x4 red[kFewWaves][RF][64];
     const int lane = threadIdx.x & 63;
     const int wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int fi = lane & 15, fq = lane >> 4;
-    char *stage = stages + wave * 32 * kPitch;
-    const int64_t m0 = (int64_t)blockIdx.x * (16 * MT);
-    const int rows = (int)(a.rows - m0 < 16 * MT ? a.rows - m0 : 16 * MT);
-    const int r0 = slice * 16 * RF;
-    const __amdgpu_buffer_rsrc_t xr = dn_rsrc(x + m0 * len, (int64_t)rows * len * 2);
+    const int slice = blockIdx.z % a.slices, slot = blockIdx.z / a.slices;
+    const int len = a.K, r0 = slice * 16 * RF;
+    const int64_t m0 = (int64_t)blockIdx.x * 16;
+    const int rows = (int)(a.rows - m0 < 16 ? a.rows - m0 : 16);
+    const __amdgpu_buffer_rsrc_t xr = dn_rsrc((const uint16_t *)a.x + m0 * len, (int64_t)rows * len * 2);
     // this part's steps of 32
-    const int steps = (len + 31) / 32;
-    const int per = (steps + a.parts - 1) / a.parts;
-    const int first = split * per, last = min(first + per, steps);
+    const int steps = (len + 31) / 32, per = (steps + a.parts - 1) / a.parts;
+    const int first = blockIdx.y * per, last = min(first + per, steps);
+
+    AdapterSet<1> set;
+    set.init(a.ids, a.adapters, m0, rows);
+    int ad, at = 0;
+    uint64_t mask[1];
+    while (set.next(ad, mask)) {
+        if (at++ % a.slots != slot)
+            continue;
+        const __amdgpu_buffer_rsrc_t wr =
+            dn_rsrc((const uint16_t *)a.a + (int64_t)ad * a.rank * len, (int64_t)a.rank * len * 2);
+        auto load = [&](FewStep<RF> &st, int step) {
+            const int k = 32 * step + 8 * fq;
+            const bool on = step < last && k < len;
+#pragma unroll
+            for (int f = 0; f < RF; ++f) {
+                const int r = r0 + 16 * f + fi;
+                st.w[f] = __builtin_amdgcn_raw_buffer_load_b128(wr, on && r < a.rank ? 2 * (r * len + k) : -16, 0, 0);
+            }
+            st.x = __builtin_amdgcn_raw_buffer_load_b128(xr, on && fi < rows ? 2 * (fi * len + k) : -16, 0, 0);
+        };
+        f32x4 acc[RF];
+#pragma unroll
+        for (int f = 0; f < RF; ++f)
+            acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        constexpr int kRing = 4;
+        FewStep<RF> ring[kRing];
+#pragma unroll
+        for (int i = 0; i < kRing; ++i)
+            load(ring[i], first + wave + kFewWaves * i);
+        for (int step = first + wave; step < last; step += kFewWaves * kRing) {
+#pragma unroll
+            for (int i = 0; i < kRing; ++i) {
+#pragma unroll
+                for (int f = 0; f < RF; ++f)
+                    acc[f] = mfma<ACT>(ring[i].w[f], ring[i].x, acc[f]);
+                load(ring[i], step + kFewWaves * (i + kRing));
+            }
+        }
+        __syncthreads();  // (the last adapter's sums have been read)
+#pragma unroll
+        for (int f = 0; f < RF; ++f)
+            red[wave][f][lane] = acc[f];
+        __syncthreads();
+        const float s = a.scale ? a.scale[ad] : 1.0f;
+        for (int f = wave; f < RF; f += kFewWaves) {
+            f32x4 v = red[0][f][lane];
+#pragma unroll
+            for (int i = 1; i < kFewWaves; ++i) {
+                const f32x4 u = red[i][f][lane];
+                v = f32x4{v[0] + u[0], v[1] + u[1], v[2] + u[2], v[3] + u[3]};
+            }
+            const int r = r0 + 16 * f + 4 * fq;
+            if (((mask[0] >> fi) & 1) && r < a.rank)
+                *(f32x4 *)((float *)a.h + (blockIdx.y * a.rows + m0 + fi) * a.rank + r) =
+                    f32x4{v[0] * s, v[1] * s, v[2] * s, v[3] * s};
+        }
+    }
+}
+
+// --------------------------------------------------------------- more rows
+constexpr int kBlock = 256;  // 4 waves of 16 rows
+constexpr int kRows = 64;
+constexpr int kStep = 64;    // of the long axis
+constexpr int kAhead = 3;    // steps whose loads are in flight in registers
+
+// Position of 16-byte chunk c of a staged row of 128 bytes.
+__device__ __forceinline__ int dswz(int r, int c) { return c ^ ((r >> 1) & 7); }
+// Byte offset of chunk c (8 values r) of staged row n of B (32 RF bytes a row):
+// pairs of chunks, which a transposed read takes together, are exchanged so
+// that its 4 rows and the next lanes' 4, 8 rows on, lie in other banks.
+template <int RF>
+__device__ __forceinline__ int bofs(int n, int c)
+{
+    constexpr int pairs = RF;
+    const int key = pairs == 4 ? (n & 3) ^ ((n >> 3) & 1) : (pairs == 2 ? (n >> 3) & 1 : 0);
+    return n * 32 * RF + 16 * (c ^ (2 * key));
+}
+
+// A thread's loads of a step: x's 16-byte chunks t % 8 of rows t / 8 + 32 i,
+// and the adapter's: of A as x's, of B chunks of its 64 rows one after another.
+template <int RF>
+struct ManyStep {
+    u32x4 x[2];
+    u32x4 w[RF > 2 ? 2 : 1];
+};
+
+template <int ACT, int RF, bool TRANS>
+__device__ __forceinline__ void down_many(const DownArgs &a, const uint16_t *__restrict__ x,
+                                          const uint16_t *__restrict__ w, uint16_t *two, float *part, int len,
+                                          int slice, int slot, char (&xs)[2][kRows * 128], char (&ws)[2][RF * 2048])
+{
+    constexpr int kW = RF > 2 ? 2 : 1;  // loads of the adapter a thread
+    const int t = threadIdx.x, lane = t & 63;
+    const int wave = (int)__builtin_amdgcn_readfirstlane(t >> 6);
+    const int fi = lane & 15, fq = lane >> 4;
+    const int r0 = slice * 16 * RF;
+    const int64_t m0 = (int64_t)blockIdx.x * kRows;
+    const int rows = (int)(a.rows - m0 < kRows ? a.rows - m0 : kRows);
+    const __amdgpu_buffer_rsrc_t xr = dn_rsrc(x + m0 * len, (int64_t)rows * len * 2);
+    const int steps = (len + kStep - 1) / kStep, per = (steps + a.parts - 1) / a.parts;
+    const int first = blockIdx.y * per, last = min(first + per, steps);
 
     AdapterSet<1> set;
     set.init(a.ids, a.adapters, m0, rows);
@@ -71,164 +186,207 @@ __device__ __forceinline__ void down(const uint16_t *__restrict__ x, const DownA
         if (at++ % a.slots != slot)
             continue;
         const __amdgpu_buffer_rsrc_t wr = dn_rsrc(w + (int64_t)ad * a.rank * len, (int64_t)a.rank * len * 2);
-        auto load = [&](DnStep<RF, MT> &st, int step) {
+        auto load = [&](ManyStep<RF> &st, int step) {
+            const int k = kStep * step + 8 * (t & 7);
             const bool on = step < last;
-            const int k = 32 * step + 8 * fq;
 #pragma unroll
-            for (int f = 0; f < RF; ++f) {
-                if constexpr (TRANS) {
-                    const int p = 64 * f + lane, n = 32 * step + p / (2 * RF), r = r0 + 8 * (p % (2 * RF));
-                    st.w[f] = __builtin_amdgcn_raw_buffer_load_b128(
-                        wr, on && n < len && r < a.rank ? 2 * (n * a.rank + r) : -16, 0, 0);
-                } else {
-                    const int r = r0 + 16 * f + fi;
-                    st.w[f] = __builtin_amdgcn_raw_buffer_load_b128(
-                        wr, on && k < len && r < a.rank ? 2 * (r * len + k) : -16, 0, 0);
-                }
-            }
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const int m = 16 * mt + fi;
-                st.x[mt] = __builtin_amdgcn_raw_buffer_load_b128(
+            for (int i = 0; i < 2; ++i) {
+                const int m = (t >> 3) + 32 * i;
+                st.x[i] = __builtin_amdgcn_raw_buffer_load_b128(
                     xr, on && k < len && m < rows ? 2 * (m * len + k) : -16, 0, 0);
             }
+#pragma unroll
+            for (int i = 0; i < kW; ++i) {
+                int off = -16;
+                if constexpr (TRANS) {
+                    const int p = t + kBlock * i, n = kStep * step + p / (2 * RF), r = r0 + 8 * (p % (2 * RF));
+                    if (on && p < 128 * RF && n < len && r < a.rank)
+                        off = 2 * (n * a.rank + r);
+                } else {
+                    const int r = r0 + (t >> 3) + 32 * i;
+                    if (on && k < len && (t >> 3) + 32 * i < 16 * RF && r < a.rank)
+                        off = 2 * (r * len + k);
+                }
+                st.w[i] = __builtin_amdgcn_raw_buffer_load_b128(wr, off, 0, 0);
+            }
         };
-        f32x4 acc[RF][MT];
+        auto store = [&](const ManyStep<RF> &st, char *xb, char *wb) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int m = (t >> 3) + 32 * i;
+                *(u32x4 *)(xb + m * 128 + 16 * dswz(m, t & 7)) = st.x[i];
+            }
+#pragma unroll
+            for (int i = 0; i < kW; ++i) {
+                if constexpr (TRANS) {
+                    const int p = t + kBlock * i;
+                    if (p < 128 * RF)
+                        *(u32x4 *)(wb + bofs<RF>(p / (2 * RF), p % (2 * RF))) = st.w[i];
+                } else {
+                    const int r = (t >> 3) + 32 * i;
+                    if (r < 16 * RF)
+                        *(u32x4 *)(wb + r * 128 + 16 * dswz(r, t & 7)) = st.w[i];
+                }
+            }
+        };
+        f32x4 acc[RF];
 #pragma unroll
         for (int f = 0; f < RF; ++f)
+            acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        auto work = [&](const char *xb, const char *wb) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                acc[f][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        constexpr int kRing = 4;
-        DnStep<RF, MT> ring[kRing];
+            for (int h = 0; h < 2; ++h) {
+                const int m = 16 * wave + fi;
+                const u32x4 xf = *(const u32x4 *)(xb + m * 128 + 16 * dswz(m, 4 * h + fq));
 #pragma unroll
-        for (int i = 0; i < kRing; ++i)
-            load(ring[i], first + wave + kDnWaves * i);
-        for (int step = first + wave; step < last; step += kDnWaves * kRing) {
-#pragma unroll
-            for (int i = 0; i < kRing; ++i) {
-                DnStep<RF, MT> &st = ring[i];
-                u32x4 wf[RF];
-                if constexpr (TRANS) {
-                    // (one wave's LDS accesses run in order)
-#pragma unroll
-                    for (int f = 0; f < RF; ++f) {
-                        const int p = 64 * f + lane;
-                        *(u32x4 *)(stage + (p / (2 * RF)) * kPitch + 16 * (p % (2 * RF))) = st.w[f];
-                    }
-                    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-                    for (int f = 0; f < RF; ++f) {
+                for (int f = 0; f < RF; ++f) {
+                    u32x4 wf;
+                    if constexpr (TRANS) {
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            const int n = 8 * fq + 4 * u + (fi >> 2);
+                            const int n = 32 * h + 8 * fq + 4 * u + (fi >> 2);
                             const v4i16 q = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                (__attribute__((address_space(3))) v4i16 *)(stage + n * kPitch + 32 * f +
-                                                                            8 * (fi & 3)));
-                            wf[f][2 * u] = (uint32_t)(uint16_t)q[0] | ((uint32_t)(uint16_t)q[1] << 16);
-                            wf[f][2 * u + 1] = (uint32_t)(uint16_t)q[2] | ((uint32_t)(uint16_t)q[3] << 16);
+                                (__attribute__((address_space(3))) v4i16 *)(wb + bofs<RF>(n, 2 * f + ((fi >> 1) & 1)) +
+                                                                            8 * (fi & 1)));
+                            wf[2 * u] = (uint32_t)(uint16_t)q[0] | ((uint32_t)(uint16_t)q[1] << 16);
+                            wf[2 * u + 1] = (uint32_t)(uint16_t)q[2] | ((uint32_t)(uint16_t)q[3] << 16);
                         }
+                    } else {
+                        const int r = 16 * f + fi;
+                        wf = *(const u32x4 *)(wb + r * 128 + 16 * dswz(r, 4 * h + fq));
                     }
-                    __builtin_amdgcn_wave_barrier();
-                } else {
-#pragma unroll
-                    for (int f = 0; f < RF; ++f)
-                        wf[f] = st.w[f];
+                    acc[f] = mfma<ACT>(wf, xf, acc[f]);
                 }
+            }
+        };
+        // steps in flight in registers, the current one in one of two LDS
+        // buffers: one barrier a step (whoever writes a buffer has passed the
+        // barrier behind the reads of its last contents)
+        ManyStep<RF> ring[kAhead];
 #pragma unroll
-                for (int f = 0; f < RF; ++f)
+        for (int i = 0; i < kAhead; ++i)
+            load(ring[i], first + i);
+        __syncthreads();  // (the last adapter's tiles have been read)
+        for (int step = first; step < last; step += 2 * kAhead) {
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-                        acc[f][mt] = mfma<ACT>(wf[f], st.x[mt], acc[f][mt]);
-                load(st, step + kDnWaves * (i + kRing));
+            for (int i = 0; i < 2 * kAhead; ++i) {
+                if (step + i >= last)
+                    break;
+                store(ring[i % kAhead], xs[i & 1], ws[i & 1]);
+                load(ring[i % kAhead], step + i + kAhead);
+                __syncthreads();
+                work(xs[i & 1], ws[i & 1]);
             }
         }
-        __syncthreads();  // (the last adapter's sums have been read)
-#pragma unroll
-        for (int f = 0; f < RF; ++f)
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                red[wave][f][mt][lane] = acc[f][mt];
-        __syncthreads();
         const float s = a.scale ? a.scale[ad] : 1.0f;
-        for (int t = wave; t < RF * MT; t += kDnWaves) {
-            const int f = t / MT, mt = t % MT;
-            f32x4 v = red[0][f][mt][lane];
+        const bool mine = (mask[0] >> (16 * wave + fi)) & 1;
 #pragma unroll
-            for (int i = 1; i < kDnWaves; ++i) {
-                const f32x4 u = red[i][f][mt][lane];
-                v = f32x4{v[0] + u[0], v[1] + u[1], v[2] + u[2], v[3] + u[3]};
-            }
+        for (int f = 0; f < RF; ++f) {
             const int r = r0 + 16 * f + 4 * fq;
-            if (((mask[0] >> (16 * mt + fi)) & 1) && r < a.rank)
-                *(f32x4 *)(part + ((int64_t)split * a.rows + m0 + 16 * mt + fi) * a.rank + r) =
-                    f32x4{v[0] * s, v[1] * s, v[2] * s, v[3] * s};
+            if (!mine || r >= a.rank)
+                continue;
+            const f32x4 v{acc[f][0] * s, acc[f][1] * s, acc[f][2] * s, acc[f][3] * s};
+            const int64_t to = (m0 + 16 * wave + fi) * a.rank + r;
+            if (a.parts > 1)
+                *(f32x4 *)(part + blockIdx.y * a.rows * a.rank + to) = v;
+            else
+                store_two(two, a.rows * a.rank, to, v);
         }
     }
 }
 
 // blockIdx: x the rows, y the part of the long axis, z slices of r, adapters'
 // slots and (h, u) where both are wanted.
-template <int ACT, int RF, int MT>
-__global__ __launch_bounds__(kDnBlock) void down_kernel(DownArgs a)
+template <int ACT, int RF>
+__global__ __launch_bounds__(kBlock) void down_many_kernel(DownArgs a)
 {
-    __shared__ f32x4 red[kDnWaves][RF][MT][64];
-    __shared__ __attribute__((aligned(16))) char stages[kDnWaves * 32 * dn_pitch(RF)];
+    __shared__ __attribute__((aligned(16))) char xs[2][kRows * 128];
+    __shared__ __attribute__((aligned(16))) char ws[2][RF * 2048];
     int z = blockIdx.z;
     const int slice = z % a.slices;
     z /= a.slices;
     const int slot = z % a.slots;
     z /= a.slots;
-    const bool trans = a.x ? z != 0 : true;
-    if (trans)
-        down<ACT, RF, MT, true>((const uint16_t *)a.dy, a, (const uint16_t *)a.b, a.u, a.N, slice, slot, blockIdx.y, red,
-                                   stages);
+    if (a.x && z == 0)
+        down_many<ACT, RF, false>(a, (const uint16_t *)a.x, (const uint16_t *)a.a, (uint16_t *)a.h, a.sums, a.K, slice,
+                                  slot, xs, ws);
     else
-        down<ACT, RF, MT, false>((const uint16_t *)a.x, a, (const uint16_t *)a.a, a.h, a.K, slice, slot, blockIdx.y, red,
-                                    stages);
+        down_many<ACT, RF, true>(a, (const uint16_t *)a.dy, (const uint16_t *)a.b, (uint16_t *)a.u,
+                                 a.sums + (a.x ? a.parts * a.rows * a.rank : 0), a.N, slice, slot, xs, ws);
 }
 
-template <int ACT, int RF>
-hipError_t launch_dn(const DownArgs &a, const DownPlan &p, hipStream_t s)
+// The parts' sums added in order and split into operands, 4 values a thread
+// (rank is a multiple of 8); blockIdx.y: h, u.
+__global__ __launch_bounds__(256) void down_join_kernel(DownArgs a)
 {
-    const dim3 grid((unsigned)p.tiles, (unsigned)a.parts,
-                    (unsigned)(a.slices * a.slots * ((a.x ? 1 : 0) + (a.dy ? 1 : 0))));
-    if (p.mt == 1)
-        hipLaunchKernelGGL((down_kernel<ACT, RF, 1>), grid, dim3(kDnBlock), 0, s, a);
-    else
-        hipLaunchKernelGGL((down_kernel<ACT, RF, 2>), grid, dim3(kDnBlock), 0, s, a);
-    return hipGetLastError();
+    const int64_t size = a.rows * a.rank, at = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    if (at >= size)
+        return;
+    const bool h = a.x && blockIdx.y == 0;
+    const float *p = a.sums + (blockIdx.y ? a.parts * size : 0) + at;
+    f32x4 v = *(const f32x4 *)p;
+#pragma unroll
+    for (int i = 1; i < kMostParts; ++i) {
+        if (i < a.parts) {
+            const f32x4 u = *(const f32x4 *)(p + i * size);
+            v = f32x4{v[0] + u[0], v[1] + u[1], v[2] + u[2], v[3] + u[3]};
+        }
+    }
+    store_two((uint16_t *)(h ? a.h : a.u), size, at, v);
 }
 
 template <int ACT>
-hipError_t launch_dn_act(const DownArgs &a, const DownPlan &p, hipStream_t s)
+hipError_t launch_dn(const DownArgs &a, const DownPlan &p, hipStream_t s)
 {
+    const int kinds = (a.x ? 1 : 0) + (a.dy ? 1 : 0);
+    const dim3 grid((unsigned)p.tiles, (unsigned)a.parts, (unsigned)(a.slices * a.slots * kinds));
+    if (!p.two) {
+        if (p.rf == 1)
+            hipLaunchKernelGGL((down_few_kernel<ACT, 1>), grid, dim3(kFewBlock), 0, s, a);
+        else if (p.rf == 2)
+            hipLaunchKernelGGL((down_few_kernel<ACT, 2>), grid, dim3(kFewBlock), 0, s, a);
+        else
+            hipLaunchKernelGGL((down_few_kernel<ACT, 4>), grid, dim3(kFewBlock), 0, s, a);
+        return hipGetLastError();
+    }
     if (p.rf == 1)
-        return launch_dn<ACT, 1>(a, p, s);
-    if (p.rf == 2)
-        return launch_dn<ACT, 2>(a, p, s);
-    return launch_dn<ACT, 4>(a, p, s);
+        hipLaunchKernelGGL((down_many_kernel<ACT, 1>), grid, dim3(kBlock), 0, s, a);
+    else if (p.rf == 2)
+        hipLaunchKernelGGL((down_many_kernel<ACT, 2>), grid, dim3(kBlock), 0, s, a);
+    else
+        hipLaunchKernelGGL((down_many_kernel<ACT, 4>), grid, dim3(kBlock), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.parts == 1)
+        return e;
+    const dim3 joins((unsigned)((a.rows * a.rank / 4 + 255) / 256), (unsigned)kinds);
+    hipLaunchKernelGGL(down_join_kernel, joins, dim3(256), 0, s, a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-DownPlan down_plan(int64_t rows, int64_t longest, int adapters, int rank, int both)
+DownPlan down_plan(int64_t rows, int64_t longest, int adapters, int rank, int backward)
 {
     DownPlan p;
+    p.two = backward || rows > 96;  // (96: as far as the skinny product goes)
     p.rf = rank <= 16 ? 1 : (rank <= 32 ? 2 : 4);
     p.slices = (rank + 16 * p.rf - 1) / (16 * p.rf);
-    p.mt = rows <= 16 ? 1 : 2;
-    p.tiles = (rows + 16 * p.mt - 1) / (16 * p.mt);
+    const int tile = p.two ? kRows : 16;
+    p.tiles = (rows + tile - 1) / tile;
     // few rows: their adapters side by side
     const int64_t most = adapters < rows ? adapters : rows;
-    p.slots = rows <= 64 ? (int)(most < 16 * p.mt ? most : 16 * p.mt) : 1;
-    // parts: as many as give every compute unit two workgroups, at least 16
-    // steps of 32 each, and no more than the kernels that add them up can take
-    // in passing
-    const int64_t blocks = p.tiles * p.slices * p.slots * (both ? 2 : 1);
-    int64_t parts = 512 / (blocks ? blocks : 1), steps = (longest + 31) / 32;
-    parts = parts < steps / 16 ? parts : steps / 16;
-    p.parts = (int)(parts < 1 ? 1 : (parts > 8 ? 8 : parts));
+    p.slots = rows <= 512 ? (int)(most < 16 ? most : 16) : 1;
+    if (p.slots < 1)
+        p.slots = 1;
+    // parts of the long axis: as many as give every compute unit two
+    // workgroups, of at least 16 (few rows) or 8 steps each; with up to 16
+    // steps of 64 the join's launch would cost more than it saves
+    const int64_t blocks = p.tiles * p.slices * p.slots * (backward ? 2 : 1);
+    const int64_t steps = p.two ? (longest + kStep - 1) / kStep : (longest + 31) / 32;
+    const int64_t most_parts = p.two ? (steps <= 16 ? 1 : steps / 8) : steps / 16;
+    int64_t parts = 512 / (blocks ? blocks : 1);
+    parts = parts < most_parts ? parts : most_parts;
+    p.parts = (int)(parts < 1 ? 1 : (parts > kMostParts ? kMostParts : parts));
     return p;
 }
 
@@ -237,7 +395,7 @@ hipError_t launch_down(q4_dtype act_t, DownArgs a, const DownPlan &p, hipStream_
     a.slices = p.slices;
     a.slots = p.slots;
     a.parts = p.parts;
-    return act_t == Q4_BF16 ? launch_dn_act<Q4_BF16>(a, p, s) : launch_dn_act<Q4_F16>(a, p, s);
+    return act_t == Q4_BF16 ? launch_dn<Q4_BF16>(a, p, s) : launch_dn<Q4_F16>(a, p, s);
 }
 
 }  // namespace q4

@@ -23,7 +23,7 @@ hipError_t launch_ldx(q4_dtype act_t, const LoraArgs &a, int gshift, hipStream_t
     const int64_t mtiles = (a.M + TM - 1) / TM, ktiles = (a.K + TK - 1) / TK;
     if (mtiles * ktiles > 0x7fffffffll)
         return hipErrorInvalidValue;
-    const LowRank low{a.part, a.parts, a.rank, a.adapters, a.M, a.ids, (const uint16_t *)a.w};
+    const LowRank low{nullptr, 0, (const uint16_t *)a.low, a.rank, a.adapters, a.M, a.ids, (const uint16_t *)a.w};
     const dim3 grid((unsigned)(mtiles * ktiles)), block(kBlock);
     if (act_t == Q4_BF16)
         hipLaunchKernelGGL((lora_dx_kernel<FMT, Q4_BF16>), grid, block, 0, s, (const uint16_t *)a.x, (int)a.M, a.codes,

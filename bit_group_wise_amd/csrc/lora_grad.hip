@@ -54,7 +54,7 @@ __device__ __forceinline__ u32x4 column8(const char *tile, int h, int c0)
 // rank, cols] (dA) or [ad, cols, rank] (dB).
 struct Side {
     const uint16_t *x;
-    const float *p;
+    const uint16_t *p;
     int cols;
     int64_t out;  // where the side's sums begin in a part of `sums`
     uint16_t *g;
@@ -125,12 +125,12 @@ __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cb
                 const int p = t + kGrBlock * q;
                 const int64_t m = m0 + p / (2 * RF);
                 const int r = r0 + 8 * (p % (2 * RF));
-                float v[8] = {};
+                pv[q] = Parts8{u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
                 if (p < kPPieces && m < a.rows && r < a.rank && adapter_of(a.ids, a.adapters, m) == ad) {
-                    const LowRank l{side.p, a.parts, a.rank, a.adapters, a.rows, nullptr, nullptr};
-                    sum_parts(l, m, r, v);
+                    const uint16_t *from = side.p + m * a.rank + r;
+                    pv[q].hi = *(const u32x4 *)from;
+                    pv[q].lo = *(const u32x4 *)(from + a.rows * a.rank);
                 }
-                pv[q] = two_parts(v);
             }
         };
         if (found)

@@ -67,8 +67,8 @@ hipError_t launch_lora_skinny(q4_format f, int g, q4_dtype act_t, const LoraArgs
         b.M = a.M - m0 < kSkMaxRows ? a.M - m0 : kSkMaxRows;
         b.x = (const uint16_t *)a.x + m0 * a.K;
         b.y = (uint16_t *)a.y + m0 * a.N;
-        const LowRank low{a.part + m0 * a.rank, a.parts,  a.rank, a.adapters, a.M, a.ids ? a.ids + m0 : nullptr,
-                          (const uint16_t *)a.w};
+        const LowRank low{(const float *)a.low + m0 * a.rank, a.parts, nullptr, a.rank, a.adapters, a.M,
+                          a.ids ? a.ids + m0 : nullptr, (const uint16_t *)a.w};
         hipError_t e;
         switch (f) {
         case Q4_NF4:

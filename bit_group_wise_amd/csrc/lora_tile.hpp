@@ -27,7 +27,7 @@ hipError_t launch_g(q4_dtype act_t, const LoraArgs &a, hipStream_t s)
         return hipErrorInvalidValue;
     // 16-byte output stores need 16-byte rows
     const int vec_y = (a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0) ? 1 : 0;
-    const LowRank low{a.part, a.parts, a.rank, a.adapters, a.M, a.ids, (const uint16_t *)a.w};
+    const LowRank low{nullptr, 0, (const uint16_t *)a.low, a.rank, a.adapters, a.M, a.ids, (const uint16_t *)a.w};
     const dim3 grid((unsigned)(mt * nt)), block(kBlock);
     if (act_t == Q4_BF16)
         hipLaunchKernelGGL((lora_tile_kernel<FMT, Q4_BF16, G>), grid, block, 0, s, (const uint16_t *)a.x, (int)a.M,

@@ -87,24 +87,28 @@ hipError_t launch_experts_tile256(q4_format f, int g, q4_dtype act_t, const Expe
 hipError_t launch_experts_dx(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
 
 // Low-rank adapters beside a weight: h[m] = scale x[m] A^T and u[m] = scale
-// dy[m] B of each row's adapter, as `parts` partial sums [parts, rows, rank]
-// (x or dy NULL: h or u is not formed).
+// dy[m] B of each row's adapter (x or dy NULL: h or u is not formed), as the
+// plan says in binary32 partial sums [parts, rows, rank] or as two bfloat16
+// parts [2, rows, rank] (LowRank in lora.hpp).
 struct DownArgs {
     const void *x, *dy, *a, *b;
     const float *scale;
     const int32_t *ids;
-    float *h, *u;
+    void *h, *u;
+    float *sums;  // [h, u][parts, rows, rank]: of the parts where they are joined
     int64_t rows;
     int N, K, adapters, rank;
     int slices, slots, parts;  // of the plan
 };
-// How they are cut: 16 mt rows, 16 rf values r and one of `parts` parts of the
-// long axis a workgroup, the adapters of a tile over `slots` workgroups.
+// How they are cut: a tile of rows, 16 rf values r and one of `parts` parts of
+// the long axis a workgroup, the adapters of a tile over `slots` workgroups.
+// two: left as two 16-bit parts, the parts of the axis joined.
 struct DownPlan {
-    int rf, mt, slices, slots, parts;
+    bool two;
+    int rf, slices, slots, parts;
     int64_t tiles;
 };
-DownPlan down_plan(int64_t rows, int64_t longest, int adapters, int rank, int both);
+DownPlan down_plan(int64_t rows, int64_t longest, int adapters, int rank, int backward);
 hipError_t launch_down(q4_dtype act_t, DownArgs a, const DownPlan &p, hipStream_t s);
 
 // The products with the adapters' part added: y = x What^T + h B^T and dX = dY
@@ -119,7 +123,7 @@ struct LoraArgs {
     const void *w;  // B [adapters, N, rank], or A [adapters, rank, K]
     const int32_t *ids;
     int adapters, rank;
-    const float *part;  // h or u as launch_down leaves it
+    const void *low;  // h or u as launch_down leaves it
     int parts;
     void *y;  // or dX
 };
@@ -134,10 +138,10 @@ hipError_t launch_lora_dx(q4_format f, int g, q4_dtype act_t, const LoraArgs &a,
 struct GradArgs {
     const void *x, *dy;
     const int32_t *ids;
-    const float *h, *u;
+    const uint16_t *h, *u;  // two parts each
     float *sums;
     int64_t rows;
-    int N, K, adapters, rank, parts, splits;
+    int N, K, adapters, rank, splits;
     void *da, *db;
 };
 int grad_splits(int64_t rows, int64_t N, int64_t K, int adapters, int rank);
