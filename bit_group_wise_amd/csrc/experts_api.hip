@@ -84,6 +84,8 @@ q4_status q4_experts_gemm_dx(q4_format f, int g, q4_dtype act_t, const void *dy,
 hipError_t q4::launch_experts(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s)
 {
     const int64_t mean = a.rows / (a.experts < a.rows ? a.experts : a.rows);
+    if (mean <= 32 && a.K <= kStreamMaxK)
+        return launch_experts_stream(f, g, act_t, a, mean <= 12 ? 1 : 2, s);
     if (mean <= 16)
         return launch_experts_skinny(f, g, act_t, a, 1, s);
     if (mean <= 24)

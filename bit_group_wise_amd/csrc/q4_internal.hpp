@@ -80,6 +80,9 @@ struct ExpertsArgs {
 hipError_t launch_experts(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
 // Pieces of up to 16 mt (1, 2 or 4) rows of an expert a workgroup.
 hipError_t launch_experts_skinny(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, int mt, hipStream_t s);
+// The same for K up to kStreamMaxK and mt 1 or 2, by resident workgroups.
+constexpr int64_t kStreamMaxK = 4096;
+hipError_t launch_experts_stream(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, int mt, hipStream_t s);
 // Tiles of up to 128 or 256 rows of an expert.
 hipError_t launch_experts_tile128(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
 hipError_t launch_experts_tile256(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);

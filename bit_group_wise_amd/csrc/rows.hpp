@@ -50,6 +50,48 @@ __device__ __forceinline__ GroupLane group_lane(const int32_t *__restrict__ offs
     return GroupLane{start, in ? max(b - start, 0) : 0};
 }
 
+// The number of pieces of the launch; of up to 64 groups also what the lanes
+// hold of them, for piece_in.
+template <int CH>
+__device__ __forceinline__ int count_pieces(const int32_t *__restrict__ offsets, int groups, int rows, GroupLane &g,
+                                            int &upto)
+{
+    const int lane = threadIdx.x & 63;
+    int highest = 0, total = 0;
+    for (int base = 0; base < groups; base += 64) {
+        g = group_lane(offsets, groups, rows, base, lane, highest);
+        upto = wave_scan((g.n + CH - 1) / CH, [](int p, int q) { return p + q; });
+        total += __builtin_amdgcn_readlane(upto, 63);
+    }
+    return total;
+}
+// Piece `want` of those of the 64 groups from `base` (upto: the lanes' pieces
+// up to theirs).
+template <int CH>
+__device__ __forceinline__ Piece piece_in(const GroupLane &g, int upto, int base, int want)
+{
+    const int l = (int)__builtin_ctzll(__ballot(upto > want) | 1ull << 63);
+    const int before = l ? __builtin_amdgcn_readlane(upto, l > 0 ? l - 1 : 0) : 0;
+    const int start = __builtin_amdgcn_readlane(g.start, l), n = __builtin_amdgcn_readlane(g.n, l);
+    const int lo = start + (want - before) * CH;
+    return Piece{base + l, lo, min(lo + CH, start + n)};
+}
+// Piece `want`, below their number, of the launch.
+template <int CH>
+__device__ __forceinline__ Piece piece_at(const int32_t *__restrict__ offsets, int groups, int rows, int want)
+{
+    const int lane = threadIdx.x & 63;
+    int highest = 0;
+    for (int base = 0;; base += 64) {
+        const GroupLane g = group_lane(offsets, groups, rows, base, lane, highest);
+        const int upto = wave_scan((g.n + CH - 1) / CH, [](int p, int q) { return p + q; });
+        const int here = __builtin_amdgcn_readlane(upto, 63);
+        if (want < here || base + 64 >= groups)
+            return piece_in<CH>(g, upto, base, want);
+        want -= here;
+    }
+}
+
 // Piece `block % pieces` of the launch and `block / pieces` in other, or
 // group -1 for a block past all pieces: block counts pieces fastest, so the
 // blocks that have work are the grid's first ones.
@@ -57,36 +99,14 @@ template <int CH>
 __device__ __forceinline__ Piece find_piece(const int32_t *__restrict__ offsets, int groups, int rows, unsigned block,
                                             int others, int &other)
 {
-    const int lane = threadIdx.x & 63;
-    const auto add = [](int p, int q) { return p + q; };
-    int highest = 0, total = 0;
     GroupLane g{};
     int upto = 0;
-    for (int base = 0; base < groups; base += 64) {
-        g = group_lane(offsets, groups, rows, base, lane, highest);
-        upto = wave_scan((g.n + CH - 1) / CH, add);
-        total += __builtin_amdgcn_readlane(upto, 63);
-    }
+    const int total = count_pieces<CH>(offsets, groups, rows, g, upto);
     if (total == 0 || block / (unsigned)total >= (unsigned)others)
         return Piece{-1, 0, 0};
     other = (int)(block / (unsigned)total);
-    int want = (int)(block % (unsigned)total), base = 0;
-    if (groups > 64) {  // (else the lanes still hold all groups)
-        highest = 0;
-        for (;; base += 64) {
-            g = group_lane(offsets, groups, rows, base, lane, highest);
-            upto = wave_scan((g.n + CH - 1) / CH, add);
-            const int here = __builtin_amdgcn_readlane(upto, 63);
-            if (want < here || base + 64 >= groups)
-                break;
-            want -= here;
-        }
-    }
-    const int l = (int)__builtin_ctzll(__ballot(upto > want) | 1ull << 63);
-    const int before = l ? __builtin_amdgcn_readlane(upto, l > 0 ? l - 1 : 0) : 0;
-    const int start = __builtin_amdgcn_readlane(g.start, l), n = __builtin_amdgcn_readlane(g.n, l);
-    const int lo = start + (want - before) * CH;
-    return Piece{base + l, lo, min(lo + CH, start + n)};
+    const int want = (int)(block % (unsigned)total);
+    return groups > 64 ? piece_at<CH>(offsets, groups, rows, want) : piece_in<CH>(g, upto, 0, want);
 }
 
 // The most pieces that `rows` rows in `groups` groups make: every group but
