@@ -85,7 +85,7 @@ hipError_t q4::launch_experts(q4_format f, int g, q4_dtype act_t, const ExpertsA
 {
     const int64_t mean = a.rows / (a.experts < a.rows ? a.experts : a.rows);
     if (mean <= 32 && a.K <= kStreamMaxK)
-        return launch_experts_stream(f, g, act_t, a, mean <= 12 ? 1 : 2, s);
+        return launch_experts_stream(f, g, act_t, a, mean <= 4 ? 1 : 2, s);
     if (mean <= 16)
         return launch_experts_skinny(f, g, act_t, a, 1, s);
     if (mean <= 24)

@@ -19,8 +19,8 @@
 //  * A block's codes and scales are 16 S contiguous bytes and S * 32 / g scales
 //    a lane; the loads of the next two or three blocks are in flight while one
 //    is dequantized and multiplied.
-//  * The 8 partial 16 x 16 MT tiles of a block meet in LDS (two buffers, one
-//    barrier a block); the waves take turns in summing them, in wave order.
+//  * The 8 partial 16 x 16 tiles of 8 / MT blocks meet in LDS at once (two
+//    buffers, one barrier), and each wave sums one, in wave order.
 #include "q4_common.hpp"
 #include "q4_internal.hpp"
 #include "q4_mfma.hpp"
@@ -66,7 +66,8 @@ __global__ __launch_bounds__(kBlock, 1) void experts_stream_kernel(
     constexpr int kRing = 3;
     constexpr int ng = Share<FMT, G, S>::ng;
     __shared__ float2 ptbl[LF == Q4_NF4 ? 256 : 1];
-    __shared__ f32x4 part[2][kWaves][MT][64];
+    constexpr int kBatch = kWaves / MT;  // blocks whose sums meet at once: a tile a wave
+    __shared__ f32x4 part[2][kWaves][kWaves][64];
 
     const int lane = threadIdx.x & 63;
     const int wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(kBlock, 1) void experts_stream_kernel(
     for (int s = 0; s < S; ++s)
         past[s] = k0 + 32 * s < K ? 0u : kPast;
 
-    int turn = 0;  // blocks done: their LDS buffer, and whose turn it is to sum
+    int turn = 0, slot = 0;  // batches done (the LDS buffer), and blocks of this one
     for (int64_t at = begin; at < end;) {
         // the piece, and its blocks nb .. nend - 1
         const int pi = (int)(at / nblocks), nb = (int)(at % nblocks);
@@ -238,33 +239,34 @@ __global__ __launch_bounds__(kBlock, 1) void experts_stream_kernel(
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
-                    part[turn & 1][wave][mt][lane] = acc[mt];
+                    part[turn & 1][wave][slot * MT + mt][lane] = acc[mt];
+                if (++slot < kBatch && b + 1 < nend)
+                    continue;
                 __syncthreads();
-                if (turn % kWaves == wave) {
-                    // (buffer turn & 1 is written again only behind the next barrier)
+                // tile `wave` of the batch: block b + 1 - slot + wave / MT (buffer
+                // turn & 1 is written again only behind the next barrier)
+                if (wave < slot * MT) {
+                    f32x4 v = part[turn & 1][0][wave][lane];
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        f32x4 v = part[turn & 1][0][mt][lane];
+                    for (int w = 1; w < kWaves; ++w) {
+                        const f32x4 u = part[turn & 1][w][wave][lane];
+                        v = f32x4{v[0] + u[0], v[1] + u[1], v[2] + u[2], v[3] + u[3]};
+                    }
+                    const int m = 16 * (wave % MT) + r, n = 16 * (b + 1 - slot + wave / MT) + 4 * q;
+                    uint16_t *to = y + (int64_t)(p.lo + m) * N + n;
+                    const uint32_t a0 = pack2<ACT>(v[0], v[1]), a1 = pack2<ACT>(v[2], v[3]);
+                    if (m < M) {
+                        if (vec_y && n < N) {
+                            *(u32x2 *)to = u32x2{a0, a1};
+                        } else {
 #pragma unroll
-                        for (int w = 1; w < kWaves; ++w) {
-                            const f32x4 u = part[turn & 1][w][mt][lane];
-                            v = f32x4{v[0] + u[0], v[1] + u[1], v[2] + u[2], v[3] + u[3]};
-                        }
-                        const int m = 16 * mt + r, n = 16 * b + 4 * q;
-                        uint16_t *to = y + (int64_t)(p.lo + m) * N + n;
-                        const uint32_t a0 = pack2<ACT>(v[0], v[1]), a1 = pack2<ACT>(v[2], v[3]);
-                        if (m < M) {
-                            if (vec_y && n < N) {
-                                *(u32x2 *)to = u32x2{a0, a1};
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (n + e < N)
-                                        to[e] = (uint16_t)((e < 2 ? a0 : a1) >> (16 * (e & 1)));
-                            }
+                            for (int e = 0; e < 4; ++e)
+                                if (n + e < N)
+                                    to[e] = (uint16_t)((e < 2 ? a0 : a1) >> (16 * (e & 1)));
                         }
                     }
                 }
+                slot = 0;
                 ++turn;
             }
         }
