@@ -13,14 +13,14 @@
 //    16 MT rows of one expert), one after another; workgroup i of G takes an
 //    equal share of consecutive ones, so most of its blocks belong to one
 //    piece.
-//  * 8 waves split K: lane quad q of wave w has the 32 S values from 32 S (4 w +
-//    q), in S steps of 32 (S = 1, 2 or 4).  Its part of x stays in registers
+//  * The waves (16 or 8) split K: lane quad q of wave w has the 32 S values from
+//    32 S (4 w + q), in S steps of 32 (S = 1, 2 or 4).  Its part of x stays in registers
 //    for all blocks of a piece.
 //  * A block's codes and scales are 16 S contiguous bytes and S * 32 / g scales
 //    a lane; the loads of the next two or three blocks are in flight while one
 //    is dequantized and multiplied.
-//  * The 8 partial 16 x 16 tiles of 8 / MT blocks meet in LDS at once (two
-//    buffers, one barrier), and each wave sums one, in wave order.
+//  * The waves' partial 16 x 16 tiles of a few blocks meet in LDS at once (two
+//    buffers, one barrier), and a wave each sums one, in wave order.
 #include "q4_common.hpp"
 #include "q4_internal.hpp"
 #include "q4_mfma.hpp"
@@ -28,9 +28,6 @@
 
 namespace q4 {
 namespace {
-
-constexpr int kWaves = 8;
-constexpr int kBlock = 64 * kWaves;
 
 constexpr uint32_t kPast = 0x80000000u;
 
@@ -54,8 +51,8 @@ struct Share {
     int first;  // place of the first group: asym its nibble in z, NF4_DQ its number in its run
 };
 
-template <int FMT, int ACT, int G, int S, int MT>
-__global__ __launch_bounds__(kBlock, 1) void experts_stream_kernel(
+template <int FMT, int ACT, int G, int WAVES, int S, int MT>
+__global__ __launch_bounds__(64 * WAVES) void experts_stream_kernel(
     const uint16_t *__restrict__ x, int xrows, const int32_t *__restrict__ index,
     const int32_t *__restrict__ offsets, int rows, int experts, const uint8_t *__restrict__ codes,
     const void *__restrict__ scales, const uint8_t *__restrict__ zeros, int N, int K, int vec_y,
@@ -63,11 +60,12 @@ __global__ __launch_bounds__(kBlock, 1) void experts_stream_kernel(
 {
     constexpr int LF = level_fmt(FMT);
     constexpr int ss = f32_absmax(FMT) ? 4 : (FMT == Q4_NF4_DQ ? 1 : 2);
-    constexpr int kRing = 3;
+    constexpr int kRing = WAVES == 16 ? 2 : 3;  // blocks in flight: as the registers hold
     constexpr int ng = Share<FMT, G, S>::ng;
     __shared__ float2 ptbl[LF == Q4_NF4 ? 256 : 1];
-    constexpr int kBatch = kWaves / MT;  // blocks whose sums meet at once: a tile a wave
-    __shared__ f32x4 part[2][kWaves][kWaves][64];
+    constexpr int kTiles = WAVES == 16 ? 4 : 8;  // whose sums meet at once
+    constexpr int kBatch = kTiles / MT;          // ... and blocks
+    __shared__ f32x4 part[2][WAVES][kTiles][64];
 
     const int lane = threadIdx.x & 63;
     const int wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -248,7 +246,7 @@ __global__ __launch_bounds__(kBlock, 1) void experts_stream_kernel(
                 if (wave < slot * MT) {
                     f32x4 v = part[turn & 1][0][wave][lane];
 #pragma unroll
-                    for (int w = 1; w < kWaves; ++w) {
+                    for (int w = 1; w < WAVES; ++w) {
                         const f32x4 u = part[turn & 1][w][wave][lane];
                         v = f32x4{v[0] + u[0], v[1] + u[1], v[2] + u[2], v[3] + u[3]};
                     }
@@ -273,29 +271,35 @@ __global__ __launch_bounds__(kBlock, 1) void experts_stream_kernel(
     }
 }
 
-template <int FMT, int G, int S, int MT>
-hipError_t launch_est_mt(q4_dtype act_t, const ExpertsArgs &a, hipStream_t s)
+template <int FMT, int G, int WAVES, int S, int MT>
+hipError_t launch_est_s(q4_dtype act_t, const ExpertsArgs &a, hipStream_t s)
 {
     // one workgroup a compute unit, and no more than there are blocks
     const int64_t blocks = most_pieces(a.rows, a.experts, 16 * MT) * ((a.N + 15) / 16);
     const int64_t cus = device_cu_count();
-    const dim3 grid((unsigned)(blocks < cus ? blocks : cus)), block(kBlock);
+    const dim3 grid((unsigned)(blocks < cus ? blocks : cus)), block(64 * WAVES);
     const int vec_y = (a.N % 4 == 0 && ((uintptr_t)a.y & 7) == 0) ? 1 : 0;
     if (act_t == Q4_BF16)
-        hipLaunchKernelGGL((experts_stream_kernel<FMT, Q4_BF16, G, S, MT>), grid, block, 0, s,
+        hipLaunchKernelGGL((experts_stream_kernel<FMT, Q4_BF16, G, WAVES, S, MT>), grid, block, 0, s,
                            (const uint16_t *)a.x, (int)a.xrows, a.index, a.offsets, (int)a.rows, a.experts, a.codes,
                            a.scales, a.zeros, (int)a.N, (int)a.K, vec_y, (uint16_t *)a.y);
     else
-        hipLaunchKernelGGL((experts_stream_kernel<FMT, Q4_F16, G, S, MT>), grid, block, 0, s,
+        hipLaunchKernelGGL((experts_stream_kernel<FMT, Q4_F16, G, WAVES, S, MT>), grid, block, 0, s,
                            (const uint16_t *)a.x, (int)a.xrows, a.index, a.offsets, (int)a.rows, a.experts, a.codes,
                            a.scales, a.zeros, (int)a.N, (int)a.K, vec_y, (uint16_t *)a.y);
     return hipGetLastError();
 }
 
+// Waves and steps so that the lanes' parts of K reach 2048 or 4096: 16 waves
+// where their registers hold x's part (one block of 16 rows: 62 -> 58 us for
+// 16 rows through 7 experts of 14336 x 4096), 8 for two blocks (with 16 the
+// registers spill: 89 -> 100 us).
 template <int FMT, int G>
 hipError_t launch_est_g(q4_dtype act_t, const ExpertsArgs &a, int mt, hipStream_t s)
 {
-    return mt == 1 ? launch_est_mt<FMT, G, 4, 1>(act_t, a, s) : launch_est_mt<FMT, G, 4, 2>(act_t, a, s);
+    if (mt == 1)
+        return a.K <= 2048 ? launch_est_s<FMT, G, 16, 1, 1>(act_t, a, s) : launch_est_s<FMT, G, 16, 2, 1>(act_t, a, s);
+    return a.K <= 2048 ? launch_est_s<FMT, G, 8, 2, 2>(act_t, a, s) : launch_est_s<FMT, G, 8, 4, 2>(act_t, a, s);
 }
 
 template <int FMT>
