@@ -1,6 +1,8 @@
 // experts_tile.hpp -- the product of many rows an expert, y[r] = x[index[r]] .
 // What_e^T for the rows r of each expert e: gemm_tile.hpp's tiles over pieces
-// of up to BM rows of one expert.
+// of up to Q4_EXPERTS_MF blocks of 16 rows of one expert.  A piece that fills
+// half of that or less, an expert's last or only one, runs as a tile of half
+// the rows, and of a quarter: its products take that much less.
 #pragma once
 
 #include "gemm_tile.hpp"
@@ -9,26 +11,42 @@
 namespace q4 {
 namespace {
 
+constexpr int kPieceMF = Q4_EXPERTS_MF;
+
 template <int FMT, int ACT, int G>
-__global__ __launch_bounds__(kBlock) void experts_tile_kernel(
+__global__ __launch_bounds__(kBlock, Q4_EXPERTS_WAVES_PER_SIMD) void experts_tile_kernel(
     const uint16_t *__restrict__ x, int xrows, const int32_t *__restrict__ index,
     const int32_t *__restrict__ offsets, int rows, int experts, const uint8_t *__restrict__ codes,
     const void *__restrict__ scales, const uint8_t *__restrict__ zeros, int N, int K, int ntiles, int vec_y,
     uint16_t *__restrict__ y)
 {
+    Q4_GEMM_TILE_LDS(FMT, kPieceMF);
     int nt;
-    const Piece p = find_piece<BM>(offsets, experts, rows, blockIdx.x, ntiles, nt);
+    const Piece p = find_piece<16 * kPieceMF>(offsets, experts, rows, blockIdx.x, ntiles, nt);
     if (p.group < 0)
         return;
     const Tile tile{p.lo, p.hi, nt * BN, N, (int64_t)p.group * N, (int64_t)experts * N, index, xrows};
-    gemm_tile<FMT, ACT, G, kGather>(tile, x, codes, scales, zeros, K, vec_y, y);
+    const int n = p.hi - p.lo;
+    if (n > 8 * kPieceMF) {
+        gemm_tile<FMT, ACT, G, kGather, kPieceMF>(tile, x, codes, scales, zeros, K, vec_y, y, xs0, xs1, ptbl);
+        return;
+    }
+    if constexpr (kPieceMF > 8) {
+        if (n > 4 * kPieceMF) {
+            gemm_tile<FMT, ACT, G, kGather, kPieceMF / 2>(tile, x, codes, scales, zeros, K, vec_y, y, xs0, xs1, ptbl);
+            return;
+        }
+        gemm_tile<FMT, ACT, G, kGather, kPieceMF / 4>(tile, x, codes, scales, zeros, K, vec_y, y, xs0, xs1, ptbl);
+    } else {
+        gemm_tile<FMT, ACT, G, kGather, kPieceMF / 2>(tile, x, codes, scales, zeros, K, vec_y, y, xs0, xs1, ptbl);
+    }
 }
 
 template <int FMT, int G>
 hipError_t launch_g(q4_dtype act_t, const ExpertsArgs &a, hipStream_t s)
 {
     const int64_t ntiles = (a.N + BN - 1) / BN;
-    const int64_t blocks = ntiles * most_pieces(a.rows, a.experts, BM);
+    const int64_t blocks = ntiles * most_pieces(a.rows, a.experts, 16 * kPieceMF);
     if (blocks > 0x7fffffffll)
         return hipErrorInvalidValue;
     // 16-byte output stores need 16-byte rows

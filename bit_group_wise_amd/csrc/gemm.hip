@@ -13,9 +13,10 @@ __global__ __launch_bounds__(kBlock) void gemm_kernel(const uint16_t *__restrict
                                                       int K, int mtiles, int vec_y,
                                                       uint16_t *__restrict__ y)
 {
+    Q4_GEMM_TILE_LDS(FMT, kMF);
     const Tile tile{(int)(blockIdx.x % (unsigned)mtiles) * BM, M, (int)(blockIdx.x / (unsigned)mtiles) * BN,
                     N, 0, N, nullptr, 0};
-    gemm_tile<FMT, ACT, G, kDense>(tile, x, codes, scales, zeros, K, vec_y, y);
+    gemm_tile<FMT, ACT, G, kDense, kMF>(tile, x, codes, scales, zeros, K, vec_y, y, xs0, xs1, ptbl);
 }
 
 template <int FMT, int G>

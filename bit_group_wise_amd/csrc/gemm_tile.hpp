@@ -1,7 +1,7 @@
 // gemm_tile.hpp -- prefill-shape fused dequant-GEMM on the matrix cores,
 // y[M, N] = x[M, K] . What^T for any M: one tile of y by a workgroup.  The
-// files that include it say the tile's size (Q4_GEMM_BM x rows, Q4_GEMM_BN W
-// rows, Q4_GEMM_WAVES) and launch it.
+// files that include it say the tile's W rows (Q4_GEMM_BN, Q4_GEMM_WAVES), its
+// x rows are a parameter (16 MF), and launch it.
 //
 // Method ("Loading a model in 4-bit", "Where the accuracy goes"; "INT4
 // Quantization > Practical Implementation with bitsandbytes"): the weights
@@ -54,10 +54,7 @@
 namespace q4 {
 namespace {
 
-#ifndef Q4_GEMM_BM
-#define Q4_GEMM_BM 256
-#endif
-constexpr int BM = Q4_GEMM_BM;                // x rows per tile
+constexpr int BM = 256;                       // x rows per whole tile
 #ifndef Q4_GEMM_BN
 #define Q4_GEMM_BN 256
 #endif
@@ -69,9 +66,9 @@ constexpr int BK = 64;                        // k per step
 constexpr int kWaves = Q4_GEMM_WAVES;         // waves per workgroup (BN / 32)
 constexpr int kBlock = 64 * kWaves;
 constexpr int ROW_BYTES = BK * 2;             // one staged x row
-constexpr int X_BYTES = BM * ROW_BYTES;
-constexpr int kXBlocks = X_BYTES / 1024 / kWaves;  // 1 KB x DMA blocks per wave per step (4)
 constexpr int kMF = BM / 16;                  // x fragments per wave (16)
+constexpr int x_bytes(int mf) { return 16 * mf * ROW_BYTES; }  // of a step's x
+constexpr int x_blocks(int mf) { return x_bytes(mf) / 1024 / kWaves; }  // 1 KB DMA blocks per wave (4)
 constexpr int kNF = BN / 16 / kWaves;         // W fragments per wave (2)
 constexpr int kWRows = 16 * kNF;              // W rows per wave (32)
 constexpr int kSpan = 4;                      // steps per scale / zero-point span
@@ -145,10 +142,12 @@ struct MSpan {
 // Per-thread constants of the tile.  Every load address is a lane constant
 // (voffset) plus a wave-uniform part that moves the view (scalar
 // arithmetic), so the loads cost no vector arithmetic.
+template <int MF>
 struct TileCtx {
+    static constexpr int kXBlocks = x_blocks(MF);
     View xr, cr, sr, zr;
     int K, Gn;   // K and groups per row
-    int xv[2];   // x DMA: voffset for even / odd blocks
+    int xv[2];   // x DMA: voffset for the wave's even / odd blocks
     int rd[2];   // fragment reads: LDS byte offset of half step h (+2048 per fragment)
     int cv;      // codes: voffset of fragment 0 at k = 0
     int sv;      // scales: voffset of fragment 0's row
@@ -158,7 +157,7 @@ struct TileCtx {
     int zo;      // ... and that nibble's position in it (0 or 1)
     int fq;      // lane quad
     uint32_t xg[kXBlocks];  // not dense: voffset of the lane's row and chunk, per block
-    int xk[2];              // ... and that chunk's first k, for even / odd blocks
+    int xk[2];              // ... and that chunk's first k, for the wave's even / odd blocks
 };
 
 // What is particular to a tile of a grouped product.  GATHER: its x rows are
@@ -167,38 +166,41 @@ enum { kDense = 0, kGather = 1, kLora = 2 };
 // A chunk of x that is not there: past every view.
 constexpr uint32_t kNowhere = 0xfffffff0u;
 
+// 16 bytes a lane from the view moved by `off` into 1 KB of LDS.
+__device__ __forceinline__ void load_lds16(const View &v, uint32_t off, char *to, uint32_t voffset)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(at(v, off), (__attribute__((address_space(3))) void *)to, 16,
+                                             (int)voffset, 0, 0, 0);
+}
+
 // x of the step at k0 into LDS buffer xn: 32 blocks of 1 KB (8 rows each),
 // kXBlocks per wave, written by the buffer unit straight into LDS (lane l
 // of a block lands at 16 l).  Rows past M read zeros.
-template <int KIND>
-__device__ __forceinline__ void load_x1(const TileCtx &c, char *xn, int wave, int i, int k0)
+template <int KIND, int MF>
+__device__ __forceinline__ void load_x1(const TileCtx<MF> &c, char *xn, int wave, int i, int k0)
 {
-    const int B = kXBlocks * wave + i;
+    const int B = x_blocks(MF) * wave + i;
     if constexpr (KIND != kDense) {
         // (chunks past a row's end are not loaded: they would be another row's
         // values, which may be anything, against zero weights)
-        const uint32_t v = k0 + c.xk[i & 1] < c.K ? c.xg[i] : kNowhere;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            at(c.xr, (uint32_t)(2 * k0)),
-            (__attribute__((address_space(3))) void *)(xn + 1024 * B), 16, (int)v, 0, 0, 0);
+        load_lds16(c.xr, (uint32_t)(2 * k0), xn + 1024 * B, k0 + c.xk[i & 1] < c.K ? c.xg[i] : kNowhere);
         return;
     }
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-        at(c.xr, (uint32_t)(B * 16 * c.K + 2 * k0)),
-        (__attribute__((address_space(3))) void *)(xn + 1024 * B), 16, c.xv[i & 1], 0, 0, 0);
+    load_lds16(c.xr, (uint32_t)(B * 16 * c.K + 2 * k0), xn + 1024 * B, (uint32_t)c.xv[i & 1]);
 }
 
 // Codes of fragment j at step k0 (fragment j's rows are 4 j below
 // fragment 0's).
-__device__ __forceinline__ void load_codes(WStep &ws, int j, const TileCtx &c, int k0)
+template <int MF>
+__device__ __forceinline__ void load_codes(WStep &ws, int j, const TileCtx<MF> &c, int k0)
 {
     ws.cw[j] = __builtin_amdgcn_raw_buffer_load_b64(at(c.cr, (uint32_t)(4 * j * (c.K >> 1) + (k0 >> 1))),
                                                     c.cv, 0, 0);
 }
 
 // Scales and zero-points of fragment j for the span starting at k0.
-template <int FMT, int G>
-__device__ __forceinline__ void load_span(MSpan<FMT, G> &ms, int j, const TileCtx &c, int k0)
+template <int FMT, int G, int MF>
+__device__ __forceinline__ void load_span(MSpan<FMT, G> &ms, int j, const TileCtx<MF> &c, int k0)
 {
     using S = Span<FMT, G>;
     const int ug = 4 * j * c.Gn + k0 / G;  // uniform part of the group index (even)
@@ -238,8 +240,8 @@ __device__ __forceinline__ void load_span(MSpan<FMT, G> &ms, int j, const TileCt
 // at k0; the lane's 16 weights are group (64 sp + 16 fq) / G of the span.
 // Weights at k >= K (the tail of a step past the end of the row) get
 // s = b = 0, so they contribute exact zeros whatever x holds there.
-template <int FMT, int G>
-__device__ __forceinline__ void wscale(const MSpan<FMT, G> &ms, int j, int sp, const TileCtx &c,
+template <int FMT, int G, int MF>
+__device__ __forceinline__ void wscale(const MSpan<FMT, G> &ms, int j, int sp, const TileCtx<MF> &c,
                                        int k0, float &s, float &b)
 {
     if constexpr (f32_absmax(FMT)) {
@@ -298,11 +300,11 @@ __device__ __forceinline__ void wscale(const MSpan<FMT, G> &ms, int j, int sp, c
 // reads stay two groups ahead of their use and no load is waited for
 // early.  The step ends once this wave's x DMA has landed (later loads may
 // still be in flight) at a workgroup barrier.
-template <int FMT, int ACT, int G, int SP, bool LOADSPAN, int KIND>
+template <int FMT, int ACT, int G, int SP, bool LOADSPAN, int KIND, int kMF>
 __device__ __forceinline__ void kstep(f32x4 (&acc)[kNF][kMF], u32x4 (&wf)[2][kNF], WStep &own,
                                       const WStep &nxt, const MSpan<FMT, G> &mo,
                                       const MSpan<FMT, G> &mn, MSpan<FMT, G> &mload,
-                                      const char *xb, char *xn, const TileCtx &c,
+                                      const char *xb, char *xn, const TileCtx<kMF> &c,
                                       const float2 *ptbl, int wave, int k0)
 {
     constexpr int SPN = (SP + 1) % kSpan;             // next step's index in its span
@@ -319,7 +321,7 @@ __device__ __forceinline__ void kstep(f32x4 (&acc)[kNF][kMF], u32x4 (&wf)[2][kNF
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int g = 0; g < 2 * kMF; ++g) {
-        if (g < kXBlocks)
+        if (g < x_blocks(kMF))
             load_x1<KIND>(c, xn, wave, g, ks + BK);
         if (g >= kMF && g < kMF + kNF)
             load_codes(own, g - kMF, c, ks + 2 * BK);
@@ -364,7 +366,7 @@ __device__ __forceinline__ void kstep(f32x4 (&acc)[kNF][kMF], u32x4 (&wf)[2][kNF
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// Where a tile lies: rows m0 .. mend - 1 of y (at most BM) against W rows n0
+// Where a tile lies: rows m0 .. mend - 1 of y (at most 16 kMF) against W rows n0
 // .. N - 1 (at most BN) of the weight that starts at row wrow0 of an array of
 // wrows rows.  Dense: x's rows are y's.  Gathered: y's row m has x's row
 // index[m] (m itself without an index), of xrows; one outside them is zeros.
@@ -382,7 +384,7 @@ struct Tile {
 // is worked on.  (One step of 2 or 3 products against the K / 64 of the
 // product itself.)
 template <int ACT>
-__device__ __forceinline__ void lora_start(f32x4 (&acc)[kNF][kMF], const LowRank &l, const TileCtx &c, char *xs0,
+__device__ __forceinline__ void lora_start(f32x4 (&acc)[kNF][kMF], const LowRank &l, const TileCtx<kMF> &c, char *xs0,
                                            char *xs1, int m0, int mend, int wave, int fr, int nrow, int N)
 {
     const int lane = threadIdx.x & 63;
@@ -395,13 +397,11 @@ __device__ __forceinline__ void lora_start(f32x4 (&acc)[kNF][kMF], const LowRank
     // (uniform loops: the workgroup's waves all stage, meet and work together)
     for (int rc = 0; rc < l.rank; rc += 64) {
 #pragma unroll
-        for (int i = 0; i < kXBlocks; ++i) {
-            const int B = kXBlocks * wave + i, row = 8 * B + (lane >> 3), r = rc + c.xk[i & 1];
+        for (int i = 0; i < x_blocks(kMF); ++i) {
+            const int B = x_blocks(kMF) * wave + i, row = 8 * B + (lane >> 3), r = rc + c.xk[i & 1];
             const uint32_t v = r < l.rank ? 2u * (uint32_t)(row * l.rank + r) : kNowhere;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                at(hv, 0), (__attribute__((address_space(3))) void *)(xs0 + 1024 * B), 16, (int)v, 0, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                at(lv, 0), (__attribute__((address_space(3))) void *)(xs1 + 1024 * B), 16, (int)v, 0, 0, 0);
+            load_lds16(hv, 0, xs0 + 1024 * B, v);
+            load_lds16(lv, 0, xs1 + 1024 * B, v);
         }
         AdapterSet<C> set = all;
         int ad;
@@ -465,20 +465,22 @@ __device__ __forceinline__ void lora_start(f32x4 (&acc)[kNF][kMF], const LowRank
     }
 }
 
-template <int FMT, int ACT, int G, int KIND>
+// The tile's LDS: two x buffers as separate objects, so the compiler can tell
+// that the reads of one never alias the DMA into the other, and the level pairs.
+#define Q4_GEMM_TILE_LDS(FMT, MF)                                     \
+    __shared__ __attribute__((aligned(1024))) char xs0[x_bytes(MF)];  \
+    __shared__ __attribute__((aligned(1024))) char xs1[x_bytes(MF)];  \
+    __shared__ float2 ptbl[level_fmt(FMT) == Q4_NF4 ? 256 : 1]
+
+template <int FMT, int ACT, int G, int KIND, int kMF>
 __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__restrict__ x,
                                           const uint8_t *__restrict__ codes,
                                           const void *__restrict__ scales,
                                           const uint8_t *__restrict__ zeros, int K, int vec_y,
-                                          uint16_t *__restrict__ y, const LowRank *low = nullptr)
+                                          uint16_t *__restrict__ y, char *xs0, char *xs1, float2 *ptbl,
+                                          const LowRank *low = nullptr)
 {
     using S = Span<FMT, G>;
-    // two x buffers as separate objects, so the compiler can tell that the
-    // reads of one never alias the DMA into the other
-    __shared__ __attribute__((aligned(1024))) char xs0[X_BYTES];
-    __shared__ __attribute__((aligned(1024))) char xs1[X_BYTES];
-    __shared__ float2 ptbl[level_fmt(FMT) == Q4_NF4 ? 256 : 1];
-
     const int t = threadIdx.x;
     const int lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -493,7 +495,7 @@ __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__re
             ptbl[t] = float2{level_entry<FMT>(t & 15), level_entry<FMT>(t >> 4)};
     }
 
-    TileCtx c;
+    TileCtx<kMF> c;
     c.K = K;
     c.Gn = Gn;
     c.fq = fq;
@@ -504,7 +506,7 @@ __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__re
     // tile's first group to the end of the padded arrays, so a wide span
     // load that starts at a meaningful byte never meets a dword straddling
     // the end (such a dword would read as zero).
-    const int64_t mrows = M - m0 < BM ? M - m0 : BM;
+    const int64_t mrows = M - m0 < 16 * kMF ? M - m0 : 16 * kMF;
     const int64_t nrows = N - n0 < BN ? N - n0 : BN;
     if (KIND == kGather && tile.index)
         c.xr = make_view(x, (int64_t)tile.xrows * K * 2);
@@ -552,15 +554,19 @@ __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__re
     {
         const int rl = lane >> 3, p = lane & 7;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            c.xv[e] = rl * 2 * K + 16 * swz(8 * e + rl, p);
+        for (int e = 0; e < 2; ++e) {
+            const int odd = x_blocks(kMF) % 2 ? (wave + e) & 1 : e;  // the block's number is
+            c.xv[e] = rl * 2 * K + 16 * swz(8 * odd + rl, p);
+        }
         if constexpr (KIND != kDense) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                c.xk[e] = 8 * swz(8 * e + rl, p);
+            for (int e = 0; e < 2; ++e) {
+                const int odd = x_blocks(kMF) % 2 ? (wave + e) & 1 : e;
+                c.xk[e] = 8 * swz(8 * odd + rl, p);
+            }
 #pragma unroll
-            for (int i = 0; i < kXBlocks; ++i) {
-                const int m = m0 + 8 * (kXBlocks * wave + i) + rl;
+            for (int i = 0; i < x_blocks(kMF); ++i) {
+                const int m = m0 + 8 * (x_blocks(kMF) * wave + i) + rl;
                 uint32_t row = (uint32_t)(m - m0);
                 bool there = m < M;
                 if (KIND == kGather && tile.index) {
@@ -583,7 +589,7 @@ __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__re
         for (int i = 0; i < kMF; ++i)
             acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    if constexpr (KIND == kLora)
+    if constexpr (KIND == kLora)  // (whole tiles alone)
         lora_start<ACT>(acc, *low, c, xs0, xs1, m0, M, wave, fr, n0 + wrow, N);
 
     // prologue: x of step 0 into LDS buffer 0, codes of steps 0 and 1, the
@@ -592,7 +598,7 @@ __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__re
     WStep wa, wb;
     MSpan<FMT, G> mc, mn;
 #pragma unroll
-    for (int i = 0; i < kXBlocks; ++i)
+    for (int i = 0; i < x_blocks(kMF); ++i)
         load_x1<KIND>(c, xs0, wave, i, 0);
 #pragma unroll
     for (int j = 0; j < kNF; ++j) {
@@ -622,10 +628,10 @@ __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__re
     // (A loop exit inside the span would keep two copies of the
     // accumulators live.)
     for (int k0 = 0; k0 < K; k0 += kSpanK) {
-        kstep<FMT, ACT, G, 0, false, KIND>(acc, wf, wa, wb, mc, mc, mn, xs0, xs1, c, ptbl, wave, k0);
-        kstep<FMT, ACT, G, 1, true, KIND>(acc, wf, wb, wa, mc, mc, mn, xs1, xs0, c, ptbl, wave, k0);
-        kstep<FMT, ACT, G, 2, false, KIND>(acc, wf, wa, wb, mc, mc, mn, xs0, xs1, c, ptbl, wave, k0);
-        kstep<FMT, ACT, G, 3, false, KIND>(acc, wf, wb, wa, mc, mn, mn, xs1, xs0, c, ptbl, wave, k0);
+        kstep<FMT, ACT, G, 0, false, KIND, kMF>(acc, wf, wa, wb, mc, mc, mn, xs0, xs1, c, ptbl, wave, k0);
+        kstep<FMT, ACT, G, 1, true, KIND, kMF>(acc, wf, wb, wa, mc, mc, mn, xs1, xs0, c, ptbl, wave, k0);
+        kstep<FMT, ACT, G, 2, false, KIND, kMF>(acc, wf, wa, wb, mc, mc, mn, xs0, xs1, c, ptbl, wave, k0);
+        kstep<FMT, ACT, G, 3, false, KIND, kMF>(acc, wf, wb, wa, mc, mn, mn, xs1, xs0, c, ptbl, wave, k0);
         mc = mn;
     }
 

@@ -14,9 +14,10 @@ __global__ __launch_bounds__(kBlock) void lora_tile_kernel(const uint16_t *__res
                                                            const uint8_t *__restrict__ zeros, int N, int K, int mtiles,
                                                            int vec_y, LowRank low, uint16_t *__restrict__ y)
 {
+    Q4_GEMM_TILE_LDS(FMT, kMF);
     const Tile tile{(int)(blockIdx.x % (unsigned)mtiles) * BM, M, (int)(blockIdx.x / (unsigned)mtiles) * BN,
                     N, 0, N, nullptr, 0};
-    gemm_tile<FMT, ACT, G, kLora>(tile, x, codes, scales, zeros, K, vec_y, y, &low);
+    gemm_tile<FMT, ACT, G, kLora, kMF>(tile, x, codes, scales, zeros, K, vec_y, y, xs0, xs1, ptbl, &low);
 }
 
 template <int FMT, int G>

@@ -78,10 +78,11 @@ struct ExpertsArgs {
     void *y;
 };
 hipError_t launch_experts(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
-// Pieces of up to 16 mt (1, 2 or 4) rows of an expert a workgroup.
-hipError_t launch_experts_skinny(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, int mt, hipStream_t s);
-// The same for K up to kStreamMaxK and mt 1 or 2, by resident workgroups.
-constexpr int64_t kStreamMaxK = 4096;
+// Pieces of up to 16 rows of an expert a workgroup.
+hipError_t launch_experts_skinny(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
+// Pieces of up to 16 mt (1 or 2) rows by resident workgroups, for K up to
+// kStreamMaxK and up to kStreamMaxCodes bytes of codes an expert.
+constexpr int64_t kStreamMaxK = 4096, kStreamMaxCodes = 0x7fff0000;
 hipError_t launch_experts_stream(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, int mt, hipStream_t s);
 // Tiles of up to 128 or 256 rows of an expert.
 hipError_t launch_experts_tile128(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
