@@ -1,6 +1,6 @@
 // experts_dx.hip -- the gradient through experts' weights, dX[r] = dY[r] .
 // What_e for the rows r of each expert e: gemm_dx_tile.hpp's tiles over pieces
-// of up to TM rows of one expert.
+// of up to 256 rows of one expert, shorter pieces as tiles of fewer rows.
 #include "gemm_dx_tile.hpp"
 #include "rows.hpp"
 
@@ -13,12 +13,24 @@ __global__ __launch_bounds__(kBlock) void experts_dx_kernel(
     const uint8_t *__restrict__ codes, const void *__restrict__ scales, const uint8_t *__restrict__ zeros, int N,
     int K, int gshift, int ktiles, uint16_t *__restrict__ dx)
 {
+    Q4_DX_TILE_LDS(FMT);
     int kt;
-    const Piece p = find_piece<TM>(offsets, experts, rows, blockIdx.x, ktiles, kt);
+    const Piece p = find_piece_long_first<TM>(offsets, experts, rows, blockIdx.x, ktiles, kt);
     if (p.group < 0)
         return;
     const DxTile tile{p.lo, p.hi, kt * TK, (int64_t)p.group * N, (int64_t)experts * N};
-    dx_tile<FMT, ACT, kDxGroup>(tile, dy, codes, scales, zeros, N, K, gshift, dx);
+    // the tile of as many quarters of its rows as the piece needs
+    const int n = p.hi - p.lo;
+#define Q4_TILE(WMF) dx_tile<FMT, ACT, kDxGroup, WMF>(tile, dy, codes, scales, zeros, N, K, gshift, dx, ys, wt, ptbl)
+    if (n > 192)
+        Q4_TILE(4);
+    else if (n > 128)
+        Q4_TILE(3);
+    else if (n > 64)
+        Q4_TILE(2);
+    else
+        Q4_TILE(1);
+#undef Q4_TILE
 }
 
 template <int FMT>

@@ -1,8 +1,8 @@
 // experts_tile.hpp -- the product of many rows an expert, y[r] = x[index[r]] .
 // What_e^T for the rows r of each expert e: gemm_tile.hpp's tiles over pieces
-// of up to Q4_EXPERTS_MF blocks of 16 rows of one expert.  A piece that fills
-// half of that or less, an expert's last or only one, runs as a tile of half
-// the rows, and of a quarter: its products take that much less.
+// of up to Q4_EXPERTS_MF blocks of 16 rows of one expert.  A shorter piece, an
+// expert's last or only one, runs as a tile of three quarters, half or a
+// quarter of the rows: its products take that much less.
 #pragma once
 
 #include "gemm_tile.hpp"
@@ -22,24 +22,23 @@ __global__ __launch_bounds__(kBlock, Q4_EXPERTS_WAVES_PER_SIMD) void experts_til
 {
     Q4_GEMM_TILE_LDS(FMT, kPieceMF);
     int nt;
-    const Piece p = find_piece<16 * kPieceMF>(offsets, experts, rows, blockIdx.x, ntiles, nt);
+    const Piece p = find_piece_long_first<16 * kPieceMF>(offsets, experts, rows, blockIdx.x, ntiles, nt);
     if (p.group < 0)
         return;
     const Tile tile{p.lo, p.hi, nt * BN, N, (int64_t)p.group * N, (int64_t)experts * N, index, xrows};
+    // the tile of as many quarters of its rows as the piece needs
     const int n = p.hi - p.lo;
-    if (n > 8 * kPieceMF) {
-        gemm_tile<FMT, ACT, G, kGather, kPieceMF>(tile, x, codes, scales, zeros, K, vec_y, y, xs0, xs1, ptbl);
-        return;
+#define Q4_TILE(MF) gemm_tile<FMT, ACT, G, kGather, MF>(tile, x, codes, scales, zeros, K, vec_y, y, xs0, xs1, ptbl)
+    if (n > 12 * kPieceMF) {
+        Q4_TILE(kPieceMF);
+    } else if (n > 8 * kPieceMF) {
+        Q4_TILE(kPieceMF * 3 / 4);
+    } else if (kPieceMF == 8 || n > 4 * kPieceMF) {
+        Q4_TILE(kPieceMF / 2);
+    } else if constexpr (kPieceMF > 8) {
+        Q4_TILE(kPieceMF / 4);
     }
-    if constexpr (kPieceMF > 8) {
-        if (n > 4 * kPieceMF) {
-            gemm_tile<FMT, ACT, G, kGather, kPieceMF / 2>(tile, x, codes, scales, zeros, K, vec_y, y, xs0, xs1, ptbl);
-            return;
-        }
-        gemm_tile<FMT, ACT, G, kGather, kPieceMF / 4>(tile, x, codes, scales, zeros, K, vec_y, y, xs0, xs1, ptbl);
-    } else {
-        gemm_tile<FMT, ACT, G, kGather, kPieceMF / 2>(tile, x, codes, scales, zeros, K, vec_y, y, xs0, xs1, ptbl);
-    }
+#undef Q4_TILE
 }
 
 template <int FMT, int G>

@@ -13,8 +13,9 @@ __global__ __launch_bounds__(kBlock) void gemm_dx_kernel(const uint16_t *__restr
                                                          int K, int gshift, int mtiles,
                                                          uint16_t *__restrict__ dx)
 {
+    Q4_DX_TILE_LDS(FMT);
     const DxTile tile{(int)(blockIdx.x % (unsigned)mtiles) * TM, M, (int)(blockIdx.x / (unsigned)mtiles) * TK, 0, N};
-    dx_tile<FMT, ACT, kDxDense>(tile, dy, codes, scales, zeros, N, K, gshift, dx);
+    dx_tile<FMT, ACT, kDxDense, kWMF>(tile, dy, codes, scales, zeros, N, K, gshift, dx, ys, wt, ptbl);
 }
 
 template <int FMT>

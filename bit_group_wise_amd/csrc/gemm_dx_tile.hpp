@@ -1,6 +1,7 @@
 // gemm_dx_tile.hpp -- the backward product through a 4-bit weight,
 // dX[M, K] = dY[M, N] . What[N, K], on the matrix cores: one tile of dX by a
-// workgroup.  The files that include it say its rows (Q4_DX_TM) and launch it.
+// workgroup.  Its rows are a parameter (64 WMF); the files that include it
+// launch it.
 //
 // Method ("What is 4-bit quantization and why does it matter?", "QLoRA
 // fine-tunes in 4-bit": the 4-bit base weights stay frozen and the gradient
@@ -47,21 +48,19 @@
 namespace q4 {
 namespace {
 
-#ifndef Q4_DX_TM
-#define Q4_DX_TM 256
-#endif
-constexpr int TM = Q4_DX_TM;           // dY / dX rows per tile
+constexpr int TM = 256;                // dY / dX rows per whole tile
 constexpr int TK = 128;                // dX columns per tile (16 per wave)
+constexpr int kWholeRows = TM;
 constexpr int TN = 64;                 // contraction (weight rows) per step
 constexpr int kWaves = 8;
 constexpr int kBlock = 64 * kWaves;
 constexpr int kYRow = TN * 2;          // bytes of one staged dY row
 constexpr int kWPitch = TK * 2 + 32;   // bytes of one staged weight row (128 columns)
 constexpr int kKF = 4;                 // k fragments per wave (64 columns)
-constexpr int kWMF = TM / 64;          // m fragments per wave (4: 64 rows)
-constexpr int kYLoads = TM / 64;       // 16-byte pieces of dY per thread and step
+constexpr int kWMF = TM / 64;          // m fragments per wave (4: 64 rows), and 16-byte
+                                       // pieces of dY per thread and step
 
-static_assert(TK == 2 * 16 * kKF && TM == 4 * 16 * kWMF && kWaves == 8 && kYLoads <= kKF, "2 x 4 waves");
+static_assert(TK == 2 * 16 * kKF && TM == 4 * 16 * kWMF && kWaves == 8 && kWMF <= kKF, "2 x 4 waves");
 static_assert(TN * TK / 16 == kBlock, "16 columns of one row per thread");
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t dx_rsrc(const void *base, int64_t bytes)
@@ -88,8 +87,9 @@ enum { kDxDense = 0, kDxGroup = 1, kDxLora = 2 };
 // the code dword of columns 8 cq .. 8 cq + 7 (cq = t / 32) with its group's
 // scale (NF4: fp32 bits, INT4: fp16 bits, NF4_DQ: the 8-bit code) and
 // zero-point byte (asym) or run constant (NF4_DQ).
+template <int WMF>
 struct DxLoads {
-    u32x4 y[kYLoads];
+    u32x4 y[WMF];
     u32x2 c;
     uint32_t s, z;
     int zsh;
@@ -107,8 +107,8 @@ struct DxCtx {
     int64_t first;  // flat number of the weight's first group in its array
 };
 
-template <int FMT, int KIND>
-__device__ __forceinline__ void dx_load(DxLoads &ld, const DxCtx &c, int n0_, int k0)
+template <int FMT, int KIND, int WMF>
+__device__ __forceinline__ void dx_load(DxLoads<WMF> &ld, const DxCtx &c, int n0_, int k0)
 {
     // (the step is wave-uniform; said so, or the compiler may wrap the loads
     // in a loop over the lanes' values of their scalar offset)
@@ -121,7 +121,7 @@ __device__ __forceinline__ void dx_load(DxLoads &ld, const DxCtx &c, int n0_, in
     const uint32_t yoff = 2u * (uint32_t)n0;
     const __amdgpu_buffer_rsrc_t yr = dx_rsrc(c.yb + yoff, yoff < c.ybytes ? c.ybytes - yoff : 0);
 #pragma unroll
-    for (int i = 0; i < kYLoads; ++i) {
+    for (int i = 0; i < WMF; ++i) {
         const int yrow = (t >> 3) + 64 * i;
         int off = 2 * (yrow * c.N + 8 * (t & 7));
         // (the next row may be another's and hold anything: such elements are
@@ -162,7 +162,7 @@ __device__ __forceinline__ void dx_load(DxLoads &ld, const DxCtx &c, int n0_, in
 // (so that the next group of 8 rows uses the other banks).
 __device__ __forceinline__ int wofs(int nl, int kl) { return nl * kWPitch + ((2 * kl) ^ (((nl >> 3) & 1) << 7)); }
 
-// Where a tile lies: rows m0 .. mend - 1 of dX (at most TM), columns from k0,
+// Where a tile lies: rows m0 .. mend - 1 of dX (at most 64 kWMF), columns from k0,
 // through the N rows of a weight that starts at row wrow0 of an array of
 // wrows rows.
 struct DxTile {
@@ -170,17 +170,21 @@ struct DxTile {
     int64_t wrow0, wrows;
 };
 
-template <int FMT, int ACT, int KIND>
+// The tile's LDS.
+#define Q4_DX_TILE_LDS(FMT)                                             \
+    __shared__ __attribute__((aligned(16))) char ys[2][TM * kYRow];     \
+    __shared__ __attribute__((aligned(16))) char wt[2][TN * kWPitch];   \
+    __shared__ float2 ptbl[level_fmt(FMT) == Q4_NF4 ? 256 : 1]
+
+template <int FMT, int ACT, int KIND, int kWMF>
 __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__restrict__ dy,
                                         const uint8_t *__restrict__ codes,
                                         const void *__restrict__ scales,
                                         const uint8_t *__restrict__ zeros, int N, int K, int gshift,
-                                        uint16_t *__restrict__ dx, const LowRank *low = nullptr)
+                                        uint16_t *__restrict__ dx, char (&ys)[2][kWholeRows * kYRow],
+                                        char (&wt)[2][TN * kWPitch], float2 *ptbl, const LowRank *low = nullptr)
 {
-    __shared__ __attribute__((aligned(16))) char ys[2][TM * kYRow];
-    __shared__ __attribute__((aligned(16))) char wt[2][TN * kWPitch];
-    __shared__ float2 ptbl[level_fmt(FMT) == Q4_NF4 ? 256 : 1];
-
+    constexpr int TM = 64 * kWMF;  // this tile's rows
     const int t = threadIdx.x;
     const int lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -216,7 +220,7 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
     else
         c.zr = FMT == Q4_INT4_ASYM ? dx_rsrc(zeros + (first >> 1), ((first & 1) + ngroups + 1) / 2) : c.cr;
 
-    // waves: 2 along k (64 columns each) x 4 along m (TM / 4 rows each)
+    // waves: 2 along k (64 columns each) x 4 along m (16 kWMF rows each)
     const int wk = wave & 1, wm = wave >> 1;
     f32x4 acc[kKF][kWMF];
 #pragma unroll
@@ -331,7 +335,7 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
     // step into ld.  Scheduling fences keep that order: the two waves of a
     // SIMD run in step (one barrier per round), so staging that is not
     // interleaved leaves the matrix cores idle.
-    auto round = [&](const char *ysc, const char *wtc, char *ysn, char *wtn, DxLoads &ld,
+    auto round = [&](const char *ysc, const char *wtc, char *ysn, char *wtn, DxLoads<kWMF> &ld,
                      int next_n0) {
         u32x4 fa[kKF], fb[kWMF];
         auto reads = [&](int h) {
@@ -396,7 +400,7 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
         for (int j = 0; j < kKF; ++j) {
             mfmas(j);
             // dY of the next step, one 16-byte piece per group of MFMAs
-            if (j < kYLoads) {
+            if (j < kWMF) {
                 const int yr = (t >> 3) + 64 * j;
                 *(u32x4 *)(ysn + yr * kYRow + 16 * yswz(yr, t & 7)) = ld.y[j];
             }
@@ -426,14 +430,14 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
     // other step s + 2.  Loads of steps past the end read zeros (rows
     // clamped) or unused data; the buffers they fill are never computed.
     const int nsteps = (N + TN - 1) / TN;
-    DxLoads la, lb;
+    DxLoads<kWMF> la, lb;
     dx_load<FMT, KIND>(la, c, 0, k0);
     dx_load<FMT, KIND>(lb, c, TN, k0);
     __syncthreads();  // the level-pair table
     {
         // step 0 into buffer 0 (no products yet)
 #pragma unroll
-        for (int i = 0; i < kYLoads; ++i) {
+        for (int i = 0; i < kWMF; ++i) {
             const int yr = (t >> 3) + 64 * i;
             *(u32x4 *)(ys[0] + yr * kYRow + 16 * yswz(yr, t & 7)) = la.y[i];
         }

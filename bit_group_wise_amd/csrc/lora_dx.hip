@@ -13,8 +13,9 @@ __global__ __launch_bounds__(kBlock) void lora_dx_kernel(const uint16_t *__restr
                                                          const uint8_t *__restrict__ zeros, int N, int K, int gshift,
                                                          int mtiles, LowRank low, uint16_t *__restrict__ dx)
 {
+    Q4_DX_TILE_LDS(FMT);
     const DxTile tile{(int)(blockIdx.x % (unsigned)mtiles) * TM, M, (int)(blockIdx.x / (unsigned)mtiles) * TK, 0, N};
-    dx_tile<FMT, ACT, kDxLora>(tile, dy, codes, scales, zeros, N, K, gshift, dx, &low);
+    dx_tile<FMT, ACT, kDxLora, kWMF>(tile, dy, codes, scales, zeros, N, K, gshift, dx, ys, wt, ptbl, &low);
 }
 
 template <int FMT>

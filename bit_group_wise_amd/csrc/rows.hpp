@@ -109,6 +109,56 @@ __device__ __forceinline__ Piece find_piece(const int32_t *__restrict__ offsets,
     return groups > 64 ? piece_at<CH>(offsets, groups, rows, want) : piece_in<CH>(g, upto, 0, want);
 }
 
+// The same with the pieces in order of their size in quarters of CH rows,
+// whole ones first: where a workgroup's time goes by that, the short ones fill
+// up what the last whole round of workgroups leaves.
+template <int CH>
+__device__ __forceinline__ Piece find_piece_long_first(const int32_t *__restrict__ offsets, int groups, int rows,
+                                                       unsigned block, int others, int &other)
+{
+    const int lane = threadIdx.x & 63;
+    const auto add = [](int p, int q) { return p + q; };
+    // pieces of q quarters in a group of n rows: all whole ones and the last
+    const auto pieces = [](int n, int q) { return (q == 4 ? n / CH : 0) + ((n % CH * 4 + CH - 1) / CH == q ? 1 : 0); };
+    int highest = 0, count[5] = {};
+    for (int base = 0; base < groups; base += 64) {
+        const GroupLane g = group_lane(offsets, groups, rows, base, lane, highest);
+        count[4] += __builtin_amdgcn_readlane(wave_scan(pieces(g.n, 4), add), 63);
+#pragma unroll
+        for (int q = 1; q < 4; ++q)
+            count[q] += (int)__popcll(__ballot(pieces(g.n, q) != 0));
+    }
+    int q = 4, of = count[4];
+#pragma unroll
+    for (int c = 4; c > 1; --c) {
+        if (q == c && block >= (unsigned)count[c] * (unsigned)others) {
+            block -= (unsigned)count[c] * (unsigned)others;
+            q = c - 1;
+            of = count[c - 1];
+        }
+    }
+    if (of == 0 || block / (unsigned)of >= (unsigned)others)
+        return Piece{-1, 0, 0};
+    other = (int)(block / (unsigned)of);
+    int want = (int)(block % (unsigned)of);
+    highest = 0;
+    for (int base = 0;; base += 64) {
+        const GroupLane g = group_lane(offsets, groups, rows, base, lane, highest);
+        const int upto = wave_scan(pieces(g.n, q), add);
+        const int here = __builtin_amdgcn_readlane(upto, 63);
+        if (want >= here && base + 64 < groups) {
+            want -= here;
+            continue;
+        }
+        const int l = (int)__builtin_ctzll(__ballot(upto > want) | 1ull << 63);
+        const int before = l ? __builtin_amdgcn_readlane(upto, l > 0 ? l - 1 : 0) : 0;
+        const int start = __builtin_amdgcn_readlane(g.start, l), n = __builtin_amdgcn_readlane(g.n, l);
+        // (a group's last piece comes behind its whole ones)
+        const int lo = start + (q == 4 ? want - before : n / CH) * CH;
+        return Piece{base + l, lo, min(lo + CH, start + n)};
+    }
+}
+
 // The most pieces that `rows` rows in `groups` groups make: every group but
 // for whole pieces adds at most one.
 inline int64_t most_pieces(int64_t rows, int64_t groups, int ch)
