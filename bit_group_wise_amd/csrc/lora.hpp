@@ -104,21 +104,37 @@ __device__ __forceinline__ f32x4 mfma_parts_b(const Parts8 &a, const Parts8 &exa
     return mfma<Q4_BF16>(a.hi, exact.hi, c);
 }
 
-// The sum of h's partial sums at row m, r0 .. r0 + 7 (in order of the parts).
-__device__ __forceinline__ void sum_parts(const LowRank &l, int64_t m, int r0, float (&v)[8])
+// Most parts that h is left in (the readers hold so many loads in flight).
+constexpr int kMostParts = 8;
+
+// The sum of h's partial sums at row m, r0 .. r0 + 7 (in order of the parts),
+// or zeros where not `there`; the parts by a view of them all.  All loads are
+// issued before the first sum.
+__device__ __forceinline__ void sum_parts(__amdgpu_buffer_rsrc_t view, const LowRank &l, int m, int r0, bool there,
+                                          float (&v)[8])
 {
-    const float *p = l.part + m * l.rank + r0;
-    f32x4 a = *(const f32x4 *)p, b = *(const f32x4 *)(p + 4);
-    for (int i = 1; i < l.parts; ++i) {
-        p += l.rows * l.rank;
-        const f32x4 c = *(const f32x4 *)p, d = *(const f32x4 *)(p + 4);
-        a = f32x4{a[0] + c[0], a[1] + c[1], a[2] + c[2], a[3] + c[3]};
-        b = f32x4{b[0] + d[0], b[1] + d[1], b[2] + d[2], b[3] + d[3]};
+    u32x4 a[kMostParts], b[kMostParts];
+    const uint32_t at = 4u * (uint32_t)(m * l.rank + r0), none = there ? 0u : 0x80000000u;
+#pragma unroll
+    for (int i = 0; i < kMostParts; ++i) {
+        const uint32_t off = (at + 4u * (uint32_t)i * (uint32_t)(l.rows * l.rank)) | none | (i < l.parts ? 0u : 0x80000000u);
+        a[i] = __builtin_amdgcn_raw_buffer_load_b128(view, (int)off, 0, 0);
+        b[i] = __builtin_amdgcn_raw_buffer_load_b128(view, (int)off, 16, 0);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = a[i];
-        v[4 + i] = b[i];
+    for (int e = 0; e < 4; ++e) {
+        v[e] = std::bit_cast<float>(a[0][e]);
+        v[4 + e] = std::bit_cast<float>(b[0][e]);
+    }
+#pragma unroll
+    for (int i = 1; i < kMostParts; ++i) {
+        if (i < l.parts) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] += std::bit_cast<float>(a[i][e]);
+                v[4 + e] += std::bit_cast<float>(b[i][e]);
+            }
+        }
     }
 }
 

@@ -36,8 +36,6 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t dn_rsrc(const void *base, int6
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n, 0x00020000);
 }
 
-constexpr int kMostParts = 8;
-
 // Four values as their two bfloat16 parts, at two[to] and two[size + to].
 __device__ __forceinline__ void store_two(uint16_t *two, int64_t size, int64_t to, const f32x4 &v)
 {

@@ -201,6 +201,7 @@ __device__ __forceinline__ void skinny_product(const SkTask &task, const uint16_
         set.init(low->ids, low->adapters, 0, M);
         int ad, turn = 0;
         uint64_t mask[1];
+        const __amdgpu_buffer_rsrc_t parts = sk_rsrc(low->part, 4 * low->parts * low->rows * low->rank);
         while (set.next(ad, mask)) {
             for (int rs = 0; rs < low->rank; rs += 32) {
                 if (turn++ % kSkWaves != wave)
@@ -210,8 +211,8 @@ __device__ __forceinline__ void skinny_product(const SkTask &task, const uint16_
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     float v[8] = {};
-                    if (((mask[0] >> (16 * mt + r)) & 1) && r0 < low->rank)
-                        sum_parts(*low, 16 * mt + r, r0, v);
+                    if (((mask[0] >> (16 * mt)) & 0xffff) != 0)
+                        sum_parts(parts, *low, 16 * mt + r, r0, ((mask[0] >> (16 * mt + r)) & 1) && r0 < low->rank, v);
                     h[mt] = two_parts(v);
                 }
 #pragma unroll

@@ -14,35 +14,35 @@ begin (int32 [experts + 1] on the device, as a cumulative count gives them):
 
 from __future__ import annotations
 
-from . import q4
 from .q4 import _act_code, _check, _launch, _torch, lib
 
 
-def _tensor(t, name, device):
+def _refuse(t, name, device):
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the weight on {device}")
-    return t
+    raise ValueError(f"{name} is on {t.device}, the weight on {device}")
 
 
 def _rows(t, name, width, device):
-    _tensor(t, name, device)
-    if t.dim() != 2 or t.shape[1] != width:
-        raise ValueError(f"{name} must be [rows, {width}], got {list(t.shape)}")
-    return t.shape[0]
+    if t.get_device() != device.index or not t.is_contiguous():
+        _refuse(t, name, device)
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width:
+        raise ValueError(f"{name} must be [rows, {width}], got {list(shape)}")
+    return shape[0]
 
 
 def _index(t, name, device):
-    _tensor(t, name, device)
+    if t.get_device() != device.index or not t.is_contiguous():
+        _refuse(t, name, device)
     if t.dtype != _torch().int32 or t.dim() != 1:
         raise TypeError(f"{name} must be a 1-D int32 tensor")
     return t.data_ptr()
 
 
-def _groups(q, offsets):
+def _groups(q, offsets, device):
     """Pointer of the offsets, experts and rows of each expert's weight."""
-    p = _index(offsets, "offsets", q.codes.device)
+    p = _index(offsets, "offsets", device)
     experts = offsets.shape[0] - 1
     if experts < 1 or q.N % experts:
         raise ValueError(f"offsets must be [experts + 1], experts a divisor of the weight's {q.N} rows")
@@ -65,13 +65,15 @@ def gemm(x, q, offsets, *, index=None, out=None):
     dev = q.codes.device
     n = _rows(x, "x", q.K, dev)
     act = _act_code(x.dtype)
-    off, experts, N = _groups(q, offsets)
+    off, experts, N = _groups(q, offsets, dev)
     rows, idx = n, None
     if index is not None:
         idx, rows = _index(index, "index", dev), index.shape[0]
     y = _out(out, rows, N, x)
+    zeros = q.zeros
     st = _launch(dev, lib().q4_experts_gemm, q.fmt, q.g, act, x.data_ptr(), n, idx, off, rows, experts,
-                 q.codes.data_ptr(), q.scales.data_ptr(), q4._ptr(q.zeros), N, q.K, y.data_ptr())
+                 q.codes.data_ptr(), q.scales.data_ptr(), None if zeros is None else zeros.data_ptr(), N, q.K,
+                 y.data_ptr())
     _check(st, "q4_experts_gemm")
     return y
 
@@ -81,11 +83,13 @@ def gemm_dx(dy, q, offsets, *, out=None):
     (q4_experts_gemm_dx); dy [rows, N].  The gradient of gathered rows is the
     sum of a token's rows of dx."""
     dev = q.codes.device
-    off, experts, N = _groups(q, offsets)
+    off, experts, N = _groups(q, offsets, dev)
     rows = _rows(dy, "dy", N, dev)
     act = _act_code(dy.dtype)
     dx = _out(out, rows, q.K, dy)
+    zeros = q.zeros
     st = _launch(dev, lib().q4_experts_gemm_dx, q.fmt, q.g, act, dy.data_ptr(), off, rows, experts,
-                 q.codes.data_ptr(), q.scales.data_ptr(), q4._ptr(q.zeros), N, q.K, dx.data_ptr())
+                 q.codes.data_ptr(), q.scales.data_ptr(), None if zeros is None else zeros.data_ptr(), N, q.K,
+                 dx.data_ptr())
     _check(st, "q4_experts_gemm_dx")
     return dx

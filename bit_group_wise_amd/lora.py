@@ -23,15 +23,21 @@ class _LoraArgs(ctypes.Structure):
     _fields_ = [("a", _vp), ("b", _vp), ("scale", _vp), ("ids", _vp), ("adapters", _i32), ("rank", _i32)]
 
 
-def _tensor(t, name, dtype, shape, device):
+def _refuse(t, name, dtype, shape, index):
+    """The error of a tensor that is not a contiguous CUDA one of this dtype and shape on this device."""
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{index}")
+
+
+def _tensor(t, name, dtype, shape, index):
+    """t's address, if it is a contiguous CUDA tensor of this dtype and shape on this device."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _refuse(t, name, dtype, shape, index)
     return t.data_ptr()
 
 
@@ -43,24 +49,42 @@ class Adapters:
         torch = _torch()
         if a.dim() != 3 or b.dim() != 3 or b.shape[0] != a.shape[0] or b.shape[2] != a.shape[1]:
             raise ValueError("a must be [adapters, rank, K] and b [adapters, N, rank]")
-        _act_code(a.dtype)
+        self._act = _act_code(a.dtype)
         self.adapters, self.rank, self.K = a.shape
         self.N = b.shape[1]
-        _tensor(a, "a", a.dtype, a.shape, a.device)
-        _tensor(b, "b", a.dtype, b.shape, a.device)
+        self.dtype, self.device, self._index = a.dtype, a.device, a.get_device()
+        args = [_tensor(a, "a", a.dtype, a.shape, self._index), _tensor(b, "b", a.dtype, b.shape, self._index), None]
         if scale is not None:
-            _tensor(scale, "scale", torch.float32, (self.adapters,), a.device)
+            args[2] = _tensor(scale, "scale", torch.float32, (self.adapters,), self._index)
         self.a, self.b, self.scale = a, b, scale
-        self.dtype, self.device = a.dtype, a.device
+        self._int32 = torch.int32
+        # what every call's record begins as (it holds the tensors' addresses)
+        self._args = _LoraArgs(*args, None, self.adapters, self.rank)
+        self._sizes = {}
 
-    def _record(self, x, q, ids, M, name):
-        """The C record of a call on M rows, checked against the weight and the activations."""
-        if (q.N, q.K) != (self.N, self.K) or q.codes.device != self.device:
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError(f"an Adapters' {name} cannot be replaced")
+        super().__setattr__(name, value)
+
+    def _record(self, q, ids, M):
+        """The C record of a call on M rows, to be held while it runs."""
+        if q.N != self.N or q.K != self.K or q.codes.get_device() != self._index:
             raise ValueError(f"the adapters are of a [{self.N}, {self.K}] weight on {self.device}")
-        if x.dtype != self.dtype:
-            raise TypeError(f"{name} must be {self.dtype}, as the adapters are, got {x.dtype}")
-        ids_p = None if ids is None else _tensor(ids, "ids", _torch().int32, (M,), self.device)
-        return _LoraArgs(self.a.data_ptr(), self.b.data_ptr(), q4._ptr(self.scale), ids_p, self.adapters, self.rank)
+        if ids is None:
+            return self._args
+        rec = _LoraArgs.from_buffer_copy(self._args)
+        rec.ids = _tensor(ids, "ids", self._int32, (M,), self._index)
+        return rec
+
+    def _bytes(self, M, backward):
+        """q4_lora_workspace_bytes, asked once for each number of rows."""
+        n = self._sizes.get((M, backward))
+        if n is None:
+            n = lib().q4_lora_workspace_bytes(M, self.N, self.K, self.adapters, self.rank, int(backward))
+            if len(self._sizes) < 4096:
+                self._sizes[M, backward] = n
+        return n
 
 
 def _rows(t, name, width):
@@ -71,15 +95,14 @@ def _rows(t, name, width):
 
 def workspace_bytes(M, pairs, backward=False) -> int:
     """Bytes of device workspace that a call on M rows needs (q4_lora_workspace_bytes)."""
-    return lib().q4_lora_workspace_bytes(M, pairs.N, pairs.K, pairs.adapters, pairs.rank, int(backward))
+    return pairs._bytes(M, bool(backward))
 
 
-def _workspace(workspace, M, pairs, backward):
-    torch = _torch()
+def _workspace(workspace, like, M, pairs, backward):
+    """The workspace of a call, as the tensor given or a new one."""
     if workspace is None:
-        workspace = torch.empty((workspace_bytes(M, pairs, backward),), dtype=torch.uint8, device=pairs.device)
-    else:
-        _tensor(workspace, "workspace", torch.uint8, (workspace.numel(),), pairs.device)
+        return like.new_empty((pairs._bytes(M, backward),), dtype=_torch().uint8)
+    _tensor(workspace, "workspace", _torch().uint8, (workspace.numel(),), pairs._index)
     return workspace
 
 
@@ -88,16 +111,17 @@ def gemm(x, q, pairs, ids=None, *, out=None, workspace=None):
     workspace: a uint8 tensor of at least workspace_bytes, else one is
     allocated."""
     M = _rows(x, "x", pairs.K)
-    rec = pairs._record(x, q, ids, M, "x")
-    xp = _tensor(x, "x", x.dtype, x.shape, pairs.device)
+    rec = pairs._record(q, ids, M)
+    xp = _tensor(x, "x", pairs.dtype, x.shape, pairs._index)
     if out is None:
         out = x.new_empty((M, pairs.N))
     else:
-        _tensor(out, "out", x.dtype, (M, pairs.N), pairs.device)
-    work = _workspace(workspace, M, pairs, False)
-    st = _launch(pairs.device, lib().q4_lora_gemm, q.fmt, q.g, _act_code(x.dtype), xp, M, q.codes.data_ptr(),
-                 q.scales.data_ptr(), q4._ptr(q.zeros), q.N, q.K, ctypes.addressof(rec), out.data_ptr(),
-                 work.data_ptr(), work.numel())
+        _tensor(out, "out", pairs.dtype, (M, pairs.N), pairs._index)
+    work = _workspace(workspace, x, M, pairs, False)
+    zeros = q.zeros
+    st = _launch(pairs.device, lib().q4_lora_gemm, q.fmt, q.g, pairs._act, xp, M, q.codes.data_ptr(),
+                 q.scales.data_ptr(), None if zeros is None else zeros.data_ptr(), q.N, q.K, ctypes.addressof(rec),
+                 out.data_ptr(), work.data_ptr(), work.numel())
     _check(st, "q4_lora_gemm")
     return out
 
@@ -107,13 +131,12 @@ def backward(dy, x, q, pairs, ids=None, *, need_dx=True, need_pairs=True, out=No
     needed None (x may be None where the adapters' are not).  out: a tuple of
     three tensors to write, None where one is to be allocated."""
     M = _rows(dy, "dy", pairs.N)
-    rec = pairs._record(dy, q, ids, M, "dy")
-    dev = pairs.device
-    dyp = _tensor(dy, "dy", dy.dtype, dy.shape, dev)
+    rec = pairs._record(q, ids, M)
+    index, dtype = pairs._index, pairs.dtype
+    dyp = _tensor(dy, "dy", dtype, dy.shape, index)
+    xp = None
     if need_pairs or x is not None:
-        xp = _tensor(x, "x", dy.dtype, (M, pairs.K), dev)
-    else:
-        xp = None
+        xp = _tensor(x, "x", dtype, (M, pairs.K), index)
     got = []
     for t, name, shape, need in zip(out or (None,) * 3, ("dx", "da", "db"),
                                     ((M, pairs.K), pairs.a.shape, pairs.b.shape),
@@ -123,10 +146,10 @@ def backward(dy, x, q, pairs, ids=None, *, need_dx=True, need_pairs=True, out=No
         elif t is None:
             t = dy.new_empty(shape)
         else:
-            _tensor(t, name, dy.dtype, shape, dev)
+            _tensor(t, name, dtype, shape, index)
         got.append(t)
-    work = _workspace(workspace, M, pairs, True)
-    st = _launch(dev, lib().q4_lora_backward, q.fmt, q.g, _act_code(dy.dtype), dyp, xp, M, q.codes.data_ptr(),
+    work = _workspace(workspace, dy, M, pairs, True)
+    st = _launch(pairs.device, lib().q4_lora_backward, q.fmt, q.g, pairs._act, dyp, xp, M, q.codes.data_ptr(),
                  q.scales.data_ptr(), q4._ptr(q.zeros), q.N, q.K, ctypes.addressof(rec),
                  *(None if t is None else t.data_ptr() for t in got), work.data_ptr(), work.numel())
     _check(st, "q4_lora_backward")
