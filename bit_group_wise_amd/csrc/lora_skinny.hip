@@ -7,21 +7,26 @@ namespace {
 
 constexpr int kSkMaxRows = 64;  // activation rows per launch (4 blocks of 16)
 
+// Waves for the adapters' part, as the registers allow: 8 with one block of
+// activation rows (16 rows of 16 adapters of rank 16 beside 11008 x 4096 NF4:
+// 22 -> XX us), 4 with two, none with four.
+constexpr int extra_waves(int mt) { return mt == 1 ? 8 : (mt == 2 ? 4 : 0); }
+
 template <int FMT, int ACT, int RB, int MT>
-__global__ __launch_bounds__(kSkBlock) void lora_skinny_kernel(const uint16_t *__restrict__ x, int M,
+__global__ __launch_bounds__(kSkBlock + 64 * extra_waves(MT)) void lora_skinny_kernel(const uint16_t *__restrict__ x, int M,
                                                                const uint8_t *__restrict__ codes,
                                                                const void *__restrict__ scales,
                                                                const uint8_t *__restrict__ zeros, int N, int K,
                                                                int gshift, LowRank low, uint16_t *__restrict__ y)
 {
     const SkTask task{M, (int)(blockIdx.x * 16 * RB), N, 0, N, nullptr, 0};
-    skinny_product<FMT, ACT, RB, MT, kSkLora>(task, x, codes, scales, zeros, K, gshift, y, &low);
+    skinny_product<FMT, ACT, RB, MT, kSkLora, extra_waves(MT)>(task, x, codes, scales, zeros, K, gshift, y, &low);
 }
 
 template <int FMT, int RB, int MT>
 hipError_t launch_ls_mt(q4_dtype act_t, const LoraArgs &a, const LowRank &low, int gshift, hipStream_t s)
 {
-    const dim3 grid((unsigned)((a.N + 16 * RB - 1) / (16 * RB))), block(kSkBlock);
+    const dim3 grid((unsigned)((a.N + 16 * RB - 1) / (16 * RB))), block(kSkBlock + 64 * extra_waves(MT));
     if (act_t == Q4_BF16)
         hipLaunchKernelGGL((lora_skinny_kernel<FMT, Q4_BF16, RB, MT>), grid, block, 0, s, (const uint16_t *)a.x,
                            (int)a.M, a.codes, a.scales, a.zeros, (int)a.N, (int)a.K, gshift, low, (uint16_t *)a.y);

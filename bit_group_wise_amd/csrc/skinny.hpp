@@ -83,7 +83,10 @@ struct SkTask {
     int xrows;
 };
 
-template <int FMT, int ACT, int RB, int MT, int KIND>
+// EXTRA: waves beside the 8 that multiply, for the adapters' part (kSkLora),
+// whose chain of latencies (ids, then h and B) then passes beside the stream of
+// the weights; 0: the 8 waves do it themselves before that.
+template <int FMT, int ACT, int RB, int MT, int KIND, int EXTRA = 0>
 __device__ __forceinline__ void skinny_product(const SkTask &task, const uint16_t *__restrict__ x,
                                                const uint8_t *__restrict__ codes,
                                                const void *__restrict__ scales,
@@ -92,7 +95,8 @@ __device__ __forceinline__ void skinny_product(const SkTask &task, const uint16_
 {
     constexpr int LF = level_fmt(FMT);
     __shared__ float2 ptbl[LF == Q4_NF4 ? 256 : 1];
-    __shared__ f32x4 part[kSkWaves][RB][MT][64];
+    constexpr int kAll = kSkWaves + EXTRA;
+    __shared__ f32x4 part[kAll][RB][MT][64];
 
     const int lane = threadIdx.x & 63;
     const int wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -182,112 +186,140 @@ __device__ __forceinline__ void skinny_product(const SkTask &task, const uint16_
         }
     };
 
-    // the wave's steps: wave, wave + 8, ...
-    SkStep<FMT, RB, MT> ring[kSkRing];
+    // the adapters' part, h B^T, left in the wave's tiles
+    const auto adapters = [&]() {
+        if constexpr (KIND == kSkLora) {
+            f32x4 acc[RB][MT];
 #pragma unroll
-    for (int i = 0; i < kSkRing; ++i)
-        load(ring[i], wave + kSkWaves * i);
-    __syncthreads();  // the level-pair table
-
-    f32x4 acc[RB][MT];
+            for (int b = 0; b < RB; ++b)
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-            acc[b][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // the adapters' part, h B^T, 32 values r of one adapter a wave at a time
-    if constexpr (KIND == kSkLora) {
-        AdapterSet<1> set;
-        set.init(low->ids, low->adapters, 0, M);
-        int ad, turn = 0;
-        uint64_t mask[1];
-        const __amdgpu_buffer_rsrc_t parts = sk_rsrc(low->part, 4 * low->parts * low->rows * low->rank);
-        while (set.next(ad, mask)) {
-            for (int rs = 0; rs < low->rank; rs += 32) {
-                if (turn++ % kSkWaves != wave)
-                    continue;
-                const int r0 = rs + 8 * q;
-                Parts8 h[MT];
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    float v[8] = {};
-                    if (((mask[0] >> (16 * mt)) & 0xffff) != 0)
-                        sum_parts(parts, *low, 16 * mt + r, r0, ((mask[0] >> (16 * mt + r)) & 1) && r0 < low->rank, v);
-                    h[mt] = two_parts(v);
-                }
-#pragma unroll
-                for (int b = 0; b < RB; ++b) {
-                    const int n = n0 + 16 * b + r;
-                    u32x4 v{0, 0, 0, 0};
-                    if (n < N && r0 < low->rank)
-                        v = *(const u32x4 *)(low->w + ((int64_t)ad * N + n) * low->rank + r0);
-                    const Parts8 w = two_parts16<ACT>(v);
+                for (int mt = 0; mt < MT; ++mt)
+                    acc[b][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            AdapterSet<1> set;
+            set.init(low->ids, low->adapters, 0, M);
+            int ad, turn = 0;
+            uint64_t mask[1];
+            const __amdgpu_buffer_rsrc_t parts = sk_rsrc(low->part, 4 * low->parts * low->rows * low->rank);
+            while (set.next(ad, mask)) {
+                for (int rs = 0; rs < low->rank; rs += 32) {
+                    if (turn++ % (EXTRA ? EXTRA : kSkWaves) != wave - (EXTRA ? kSkWaves : 0))
+                        continue;
+                    const int r0 = rs + 8 * q;
+                    Parts8 h[MT];
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
-                        const f32x4 t = mfma_parts_a<ACT>(w, h[mt], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-                        const bool mine = (mask[0] >> (16 * mt + r)) & 1;
+                        float v[8] = {};
+                        if (((mask[0] >> (16 * mt)) & 0xffff) != 0)
+                            sum_parts(parts, *low, 16 * mt + r, r0, ((mask[0] >> (16 * mt + r)) & 1) && r0 < low->rank, v);
+                        h[mt] = two_parts(v);
+                    }
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[b][mt][e] = mine ? acc[b][mt][e] + t[e] : acc[b][mt][e];
+                    for (int b = 0; b < RB; ++b) {
+                        const int n = n0 + 16 * b + r;
+                        u32x4 v{0, 0, 0, 0};
+                        if (n < N && r0 < low->rank)
+                            v = *(const u32x4 *)(low->w + ((int64_t)ad * N + n) * low->rank + r0);
+                        const Parts8 w = two_parts16<ACT>(v);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            const f32x4 t = mfma_parts_a<ACT>(w, h[mt], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+                            const bool mine = (mask[0] >> (16 * mt + r)) & 1;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                acc[b][mt][e] = mine ? acc[b][mt][e] + t[e] : acc[b][mt][e];
+                        }
                     }
                 }
             }
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    part[wave][b][mt][lane] = acc[b][mt];
         }
-    }
-    for (int step = wave; step < nsteps; step += kSkWaves * kSkRing) {
-#pragma unroll
-        for (int i = 0; i < kSkRing; ++i) {
-            SkStep<FMT, RB, MT> &st = ring[i];
-            // a step past the end is not computed (its slot is still
-            // refilled below, so the load waits stay partial)
-#pragma unroll
-            for (int b = 0; b < RB; ++b) {
-                if (step + kSkWaves * i >= nsteps)
-                    break;
-                float s, bias;
-                if constexpr (f32_absmax(FMT)) {
-                    s = std::bit_cast<float>(st.sraw[b]);
-                    bias = 0.0f;
-                } else if constexpr (FMT == Q4_NF4_DQ) {  // c' = qc * s2, one product
-                    s = keep_f32((float)st.sraw[b] * std::bit_cast<float>(st.zraw[b]));
-                    bias = 0.0f;
-                } else {
-                    s = h2f(st.sraw[b] & 0xffffu);
-                    bias = FMT == Q4_INT4_SYM ? -8.0f * s
-                                              : -(float)((st.zraw[b] >> st.zsh[b]) & 0xfu) * s;
-                }
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    float2 lp[4];
-                    if constexpr (LF == Q4_NF4) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            lp[e] = ptbl[(st.cw[b][d] >> (8 * e)) & 0xffu];
-                    }
-                    const u32x4 wf = dequant8<FMT, ACT>(st.cw[b][d], s, bias, lp);
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-                        acc[b][mt] = mfma<ACT>(wf, st.xv[mt][d], acc[b][mt]);
-                }
-            }
-            load(st, step + kSkWaves * (i + kSkRing));
-        }
-    }
+    };
 
-    // sum the 8 partial tiles of each (row block, activation block) in wave
-    // order; lane l holds rows 4 q + v of the row block against activation
-    // row 16 mt + r
+    if (EXTRA > 0 && wave >= kSkWaves) {
+        __syncthreads();  // (with the others, at their level-pair table)
+        adapters();
+    } else {
+        if constexpr (EXTRA == 0)
+            adapters();
+        // the wave's steps: wave, wave + 8, ...
+        SkStep<FMT, RB, MT> ring[kSkRing];
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
+        for (int i = 0; i < kSkRing; ++i)
+            load(ring[i], wave + kSkWaves * i);
+        __syncthreads();  // the level-pair table
+
+        f32x4 acc[RB][MT];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-            part[wave][b][mt][lane] = acc[b][mt];
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                acc[b][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int step = wave; step < nsteps; step += kSkWaves * kSkRing) {
+#pragma unroll
+            for (int i = 0; i < kSkRing; ++i) {
+                SkStep<FMT, RB, MT> &st = ring[i];
+                // a step past the end is not computed (its slot is still
+                // refilled below, so the load waits stay partial)
+#pragma unroll
+                for (int b = 0; b < RB; ++b) {
+                    if (step + kSkWaves * i >= nsteps)
+                        break;
+                    float s, bias;
+                    if constexpr (f32_absmax(FMT)) {
+                        s = std::bit_cast<float>(st.sraw[b]);
+                        bias = 0.0f;
+                    } else if constexpr (FMT == Q4_NF4_DQ) {  // c' = qc * s2, one product
+                        s = keep_f32((float)st.sraw[b] * std::bit_cast<float>(st.zraw[b]));
+                        bias = 0.0f;
+                    } else {
+                        s = h2f(st.sraw[b] & 0xffffu);
+                        bias = FMT == Q4_INT4_SYM ? -8.0f * s
+                                                  : -(float)((st.zraw[b] >> st.zsh[b]) & 0xfu) * s;
+                    }
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        float2 lp[4];
+                        if constexpr (LF == Q4_NF4) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                lp[e] = ptbl[(st.cw[b][d] >> (8 * e)) & 0xffu];
+                        }
+                        const u32x4 wf = dequant8<FMT, ACT>(st.cw[b][d], s, bias, lp);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt)
+                            acc[b][mt] = mfma<ACT>(wf, st.xv[mt][d], acc[b][mt]);
+                    }
+                }
+                load(st, step + kSkWaves * (i + kSkRing));
+            }
+        }
+
+        // sum the waves' partial tiles of each (row block, activation block) in
+        // wave order; lane l holds rows 4 q + v of the row block against
+        // activation row 16 mt + r
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                if constexpr (KIND == kSkLora && EXTRA == 0) {  // (beside the adapters' part)
+                    const f32x4 u = part[wave][b][mt][lane];
+                    acc[b][mt] = f32x4{acc[b][mt][0] + u[0], acc[b][mt][1] + u[1], acc[b][mt][2] + u[2],
+                                       acc[b][mt][3] + u[3]};
+                }
+                part[wave][b][mt][lane] = acc[b][mt];
+            }
+        }
+    }
     __syncthreads();
-    for (int t = wave; t < RB * MT; t += kSkWaves) {
+    for (int t = wave; t < RB * MT; t += kAll) {
         const int b = t / MT, mt = t % MT;
         f32x4 u0 = part[0][b][mt][lane];
 #pragma unroll
-        for (int w = 1; w < kSkWaves; ++w) {
+        for (int w = 1; w < kAll; ++w) {
             const f32x4 u = part[w][b][mt][lane];
             u0 = f32x4{u0[0] + u[0], u0[1] + u[1], u0[2] + u[2], u0[3] + u[3]};
         }
