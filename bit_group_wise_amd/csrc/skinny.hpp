@@ -195,39 +195,73 @@ __device__ __forceinline__ void skinny_product(const SkTask &task, const uint16_
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
                     acc[b][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            AdapterSet<1> set;
-            set.init(low->ids, low->adapters, 0, M);
-            int ad, turn = 0;
-            uint64_t mask[1];
+            AdapterSet<1> all;
+            all.init(low->ids, low->adapters, 0, M);
             const __amdgpu_buffer_rsrc_t parts = sk_rsrc(low->part, 4 * low->parts * low->rows * low->rank);
-            while (set.next(ad, mask)) {
-                for (int rs = 0; rs < low->rank; rs += 32) {
-                    if (turn++ % (EXTRA ? EXTRA : kSkWaves) != wave - (EXTRA ? kSkWaves : 0))
-                        continue;
-                    const int r0 = rs + 8 * q;
-                    Parts8 h[MT];
+            constexpr int kTurns = EXTRA ? EXTRA : kSkWaves;  // waves that share the adapters
+            constexpr int kAhead = 3;                         // adapters whose B is in flight
+            constexpr uint32_t kPast = 0x80000000u;           // past every view
+            const int first = wave - (EXTRA ? kSkWaves : 0);
+            for (int rs = 0; rs < low->rank; rs += 32) {
+                const int r0 = rs + 8 * q;
+                // this wave's adapters: every kTurns-th, another wave's turn with
+                // the next 32 values
+                AdapterSet<1> set = all;
+                int turn = kTurns - first + (rs >> 5);
+                struct Slot {
+                    bool on;
+                    uint64_t mask;
+                    u32x4 b[RB];
+                };
+                const auto next = [&](Slot &sl) {
+                    int ad;
+                    uint64_t mask[1] = {};
+                    do
+                        sl.on = set.next(ad, mask);
+                    while (sl.on && turn++ % kTurns != 0);
+                    sl.mask = mask[0];
+                    const __amdgpu_buffer_rsrc_t br =
+                        sk_rsrc(low->w + (int64_t)(sl.on ? ad : 0) * N * low->rank, (int64_t)N * low->rank * 2);
+                    const uint32_t none = sl.on && r0 < low->rank ? 0u : kPast;  // (rows past N lie past the view)
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        float v[8] = {};
-                        if (((mask[0] >> (16 * mt)) & 0xffff) != 0)
-                            sum_parts(parts, *low, 16 * mt + r, r0, ((mask[0] >> (16 * mt + r)) & 1) && r0 < low->rank, v);
-                        h[mt] = two_parts(v);
-                    }
+                    for (int b = 0; b < RB; ++b)
+                        sl.b[b] = __builtin_amdgcn_raw_buffer_load_b128(
+                            br, (int)((2u * (uint32_t)((n0 + 16 * b + r) * low->rank + r0)) | none), 0, 0);
+                };
+                Slot slots[kAhead];
+                next(slots[0]);
+                if (!slots[0].on)
+                    continue;
 #pragma unroll
-                    for (int b = 0; b < RB; ++b) {
-                        const int n = n0 + 16 * b + r;
-                        u32x4 v{0, 0, 0, 0};
-                        if (n < N && r0 < low->rank)
-                            v = *(const u32x4 *)(low->w + ((int64_t)ad * N + n) * low->rank + r0);
-                        const Parts8 w = two_parts16<ACT>(v);
+                for (int i = 1; i < kAhead; ++i)
+                    next(slots[i]);
+                Parts8 h[MT];  // of all rows, whatever their adapters
 #pragma unroll
-                        for (int mt = 0; mt < MT; ++mt) {
-                            const f32x4 t = mfma_parts_a<ACT>(w, h[mt], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-                            const bool mine = (mask[0] >> (16 * mt + r)) & 1;
+                for (int mt = 0; mt < MT; ++mt) {
+                    float v[8];
+                    sum_parts(parts, *low, 16 * mt + r, r0, 16 * mt + r < M && r0 < low->rank, v);
+                    h[mt] = two_parts(v);
+                }
+                while (slots[0].on) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                acc[b][mt][e] = mine ? acc[b][mt][e] + t[e] : acc[b][mt][e];
+                    for (int i = 0; i < kAhead; ++i) {
+                        if (slots[i].on) {
+#pragma unroll
+                            for (int b = 0; b < RB; ++b) {
+                                const Parts8 w = two_parts16<ACT>(slots[i].b[b]);
+#pragma unroll
+                                for (int mt = 0; mt < MT; ++mt) {
+                                    if (((slots[i].mask >> (16 * mt)) & 0xffff) == 0)
+                                        continue;
+                                    const f32x4 t = mfma_parts_a<ACT>(w, h[mt], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+                                    const bool mine = (slots[i].mask >> (16 * mt + r)) & 1;
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        acc[b][mt][e] = mine ? acc[b][mt][e] + t[e] : acc[b][mt][e];
+                                }
+                            }
                         }
+                        next(slots[i]);
                     }
                 }
             }
