@@ -229,106 +229,6 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
         for (int f = 0; f < kWMF; ++f)
             acc[j][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    // The adapters' part, u A, as steps of the same form: 64 values r of u as
-    // the step's dY (its two parts in the two dY buffers) and the adapter's 64
-    // rows of A as its weight rows (for fp16 its two parts in the two weight
-    // buffers).
-    if constexpr (KIND == kDxLora) {
-        constexpr int C = TM / 64;
-        const int rows = M - m0 < TM ? M - m0 : TM;
-        AdapterSet<C> all;
-        all.init(low->ids, low->adapters, m0, rows);
-        for (int rc = 0; rc < low->rank; rc += 64) {
-            for (int p = t; p < TM * 8; p += kBlock) {
-                const int row = p >> 3, ch = p & 7;
-                u32x4 q[2] = {};
-                if (row < rows && rc + 8 * ch < low->rank) {
-                    const uint16_t *from = low->two + (m0 + row) * (int64_t)low->rank + rc + 8 * ch;
-                    q[0] = *(const u32x4 *)from;
-                    q[1] = *(const u32x4 *)(from + low->rows * low->rank);
-                }
-                const int at = row * kYRow + 16 * yswz(row, ch);
-                *(u32x4 *)(ys[0] + at) = q[0];
-                *(u32x4 *)(ys[1] + at) = q[1];
-            }
-            AdapterSet<C> set = all;
-            int ad;
-            uint64_t mask[C], next[C] = {};
-            u32x4 v[2];
-            auto load = [&]() {  // the adapter's rows, the next one's while one is worked on
-                const int r = rc + (t >> 3), k = k0 + 16 * (t & 7);
-                v[0] = v[1] = u32x4{0, 0, 0, 0};
-                if (r < low->rank && k < K) {
-                    const u32x4 *w = (const u32x4 *)(low->w + ((int64_t)ad * low->rank + r) * K + k);
-                    v[0] = w[0];
-                    v[1] = w[1];
-                }
-            };
-            bool on = set.next(ad, next);
-            if (on)
-                load();
-            while (on) {
-#pragma unroll
-                for (int q = 0; q < C; ++q)
-                    mask[q] = next[q];
-                __syncthreads();  // (the last adapter's rows have been read)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const Parts8 w = two_parts16<ACT>(v[e]);
-                    *(u32x4 *)(wt[0] + wofs(t >> 3, 16 * (t & 7) + 8 * e)) = w.hi;
-                    if constexpr (ACT == Q4_F16)
-                        *(u32x4 *)(wt[1] + wofs(t >> 3, 16 * (t & 7) + 8 * e)) = w.lo;
-                }
-                on = set.next(ad, next);
-                if (on)
-                    load();
-                __syncthreads();
-#pragma unroll
-                for (int j = 0; j < kKF; ++j) {
-                    Parts8 fa[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int nl = 32 * h + 8 * fq + 4 * u + (fi >> 2);
-                            const int kl = 64 * wk + 16 * j + 4 * (fi & 3);
-                            const v4i16 p = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                (__attribute__((address_space(3))) v4i16 *)(wt[0] + wofs(nl, kl)));
-                            fa[h].hi[2 * u] = (uint32_t)(uint16_t)p[0] | ((uint32_t)(uint16_t)p[1] << 16);
-                            fa[h].hi[2 * u + 1] = (uint32_t)(uint16_t)p[2] | ((uint32_t)(uint16_t)p[3] << 16);
-                            if constexpr (ACT == Q4_F16) {
-                                const v4i16 o = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                    (__attribute__((address_space(3))) v4i16 *)(wt[1] + wofs(nl, kl)));
-                                fa[h].lo[2 * u] = (uint32_t)(uint16_t)o[0] | ((uint32_t)(uint16_t)o[1] << 16);
-                                fa[h].lo[2 * u + 1] = (uint32_t)(uint16_t)o[2] | ((uint32_t)(uint16_t)o[3] << 16);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int f = 0; f < kWMF; ++f) {
-                        const int row = 16 * kWMF * wm + 16 * f + fi;  // (a wave's rows lie in one mask of 64)
-                        f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int at = row * kYRow + 16 * yswz(row, 4 * h + fq);
-                            const Parts8 u{*(const u32x4 *)(ys[0] + at), *(const u32x4 *)(ys[1] + at)};
-                            p = mfma_parts_a<ACT>(fa[h], u, p);
-                        }
-                        uint64_t of = mask[0];
-#pragma unroll
-                        for (int c2 = 1; c2 < C; ++c2)
-                            of = (16 * kWMF * wm) / 64 == c2 ? mask[c2] : of;
-                        const bool mine = (of >> (row & 63)) & 1;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[j][f][e] = mine ? acc[j][f][e] + p[e] : acc[j][f][e];
-                    }
-                }
-            }
-            __syncthreads();
-        }
-    }
-
     // One round: the products of the step in LDS buffer (ysc, wtc), with the
     // staging of the next step (register set ld -> buffer (ysn, wtn)) worked
     // in between the matrix-core instructions, then the loads of a later
@@ -433,6 +333,113 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
     DxLoads<kWMF> la, lb;
     dx_load<FMT, KIND>(la, c, 0, k0);
     dx_load<FMT, KIND>(lb, c, TN, k0);
+    // The adapters' part, u A, as steps of the same form: 64 values r of u as
+    // the step's dY (its two parts in the two dY buffers) and the adapter's 64
+    // rows of A as its weight rows (for fp16 its two parts in the two weight
+    // buffers).
+    if constexpr (KIND == kDxLora) {
+        constexpr int C = TM / 64;
+        const int rows = M - m0 < TM ? M - m0 : TM;
+        AdapterSet<C> all;
+        all.init(low->ids, low->adapters, m0, rows);
+        // (rows past the tile's end lie past the views)
+        const __amdgpu_buffer_rsrc_t uhr = dx_rsrc(low->two + (int64_t)m0 * low->rank, (int64_t)rows * low->rank * 2);
+        const __amdgpu_buffer_rsrc_t ulr =
+            dx_rsrc(low->two + (low->rows + m0) * low->rank, (int64_t)rows * low->rank * 2);
+        for (int rc = 0; rc < low->rank; rc += 64) {
+            // u's chunk t % 8 of rows t / 8 + 64 i, all loads before the first store
+            u32x4 uh[kWMF], ul[kWMF];
+#pragma unroll
+            for (int i = 0; i < kWMF; ++i) {
+                const uint32_t off = 2u * (uint32_t)(((t >> 3) + 64 * i) * low->rank + rc + 8 * (t & 7)) |
+                                     (rc + 8 * (t & 7) < low->rank ? 0u : 0x80000000u);
+                uh[i] = __builtin_amdgcn_raw_buffer_load_b128(uhr, (int)off, 0, 0);
+                ul[i] = __builtin_amdgcn_raw_buffer_load_b128(ulr, (int)off, 0, 0);
+            }
+            AdapterSet<C> set = all;
+            int ad;
+            uint64_t mask[C], next[C] = {};
+            u32x4 v[2];
+            auto load = [&]() {  // the adapter's rows, the next one's while one is worked on
+                const int r = rc + (t >> 3), k = k0 + 16 * (t & 7);
+                v[0] = v[1] = u32x4{0, 0, 0, 0};
+                if (r < low->rank && k < K) {
+                    const u32x4 *w = (const u32x4 *)(low->w + ((int64_t)ad * low->rank + r) * K + k);
+                    v[0] = w[0];
+                    v[1] = w[1];
+                }
+            };
+            bool on = set.next(ad, next);
+            if (on)
+                load();
+#pragma unroll
+            for (int i = 0; i < kWMF; ++i) {
+                const int row = (t >> 3) + 64 * i, at = row * kYRow + 16 * yswz(row, t & 7);
+                *(u32x4 *)(ys[0] + at) = uh[i];
+                *(u32x4 *)(ys[1] + at) = ul[i];
+            }
+            while (on) {
+#pragma unroll
+                for (int q = 0; q < C; ++q)
+                    mask[q] = next[q];
+                __syncthreads();  // (the last adapter's rows have been read)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const Parts8 w = two_parts16<ACT>(v[e]);
+                    *(u32x4 *)(wt[0] + wofs(t >> 3, 16 * (t & 7) + 8 * e)) = w.hi;
+                    if constexpr (ACT == Q4_F16)
+                        *(u32x4 *)(wt[1] + wofs(t >> 3, 16 * (t & 7) + 8 * e)) = w.lo;
+                }
+                on = set.next(ad, next);
+                if (on)
+                    load();
+                __syncthreads();
+#pragma unroll
+                for (int j = 0; j < kKF; ++j) {
+                    Parts8 fa[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int nl = 32 * h + 8 * fq + 4 * u + (fi >> 2);
+                            const int kl = 64 * wk + 16 * j + 4 * (fi & 3);
+                            const v4i16 p = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                (__attribute__((address_space(3))) v4i16 *)(wt[0] + wofs(nl, kl)));
+                            fa[h].hi[2 * u] = (uint32_t)(uint16_t)p[0] | ((uint32_t)(uint16_t)p[1] << 16);
+                            fa[h].hi[2 * u + 1] = (uint32_t)(uint16_t)p[2] | ((uint32_t)(uint16_t)p[3] << 16);
+                            if constexpr (ACT == Q4_F16) {
+                                const v4i16 o = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                    (__attribute__((address_space(3))) v4i16 *)(wt[1] + wofs(nl, kl)));
+                                fa[h].lo[2 * u] = (uint32_t)(uint16_t)o[0] | ((uint32_t)(uint16_t)o[1] << 16);
+                                fa[h].lo[2 * u + 1] = (uint32_t)(uint16_t)o[2] | ((uint32_t)(uint16_t)o[3] << 16);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int f = 0; f < kWMF; ++f) {
+                        const int row = 16 * kWMF * wm + 16 * f + fi;  // (a wave's rows lie in one mask of 64)
+                        f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int at = row * kYRow + 16 * yswz(row, 4 * h + fq);
+                            const Parts8 u{*(const u32x4 *)(ys[0] + at), *(const u32x4 *)(ys[1] + at)};
+                            p = mfma_parts_a<ACT>(fa[h], u, p);
+                        }
+                        uint64_t of = mask[0];
+#pragma unroll
+                        for (int c2 = 1; c2 < C; ++c2)
+                            of = (16 * kWMF * wm) / 64 == c2 ? mask[c2] : of;
+                        const bool mine = (of >> (row & 63)) & 1;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[j][f][e] = mine ? acc[j][f][e] + p[e] : acc[j][f][e];
+                    }
+                }
+            }
+            __syncthreads();
+        }
+    }
+
     __syncthreads();  // the level-pair table
     {
         // step 0 into buffer 0 (no products yet)

@@ -589,22 +589,27 @@ __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__re
         for (int i = 0; i < kMF; ++i)
             acc[j][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    if constexpr (KIND == kLora)  // (whole tiles alone)
-        lora_start<ACT>(acc, *low, c, xs0, xs1, m0, M, wave, fr, n0 + wrow, N);
-
     // prologue: x of step 0 into LDS buffer 0, codes of steps 0 and 1, the
     // scales of span 0, the first half of step 0 dequantized
     u32x4 wf[2][kNF];
     WStep wa, wb;
     MSpan<FMT, G> mc, mn;
+    if constexpr (KIND != kLora) {
 #pragma unroll
-    for (int i = 0; i < x_blocks(kMF); ++i)
-        load_x1<KIND>(c, xs0, wave, i, 0);
+        for (int i = 0; i < x_blocks(kMF); ++i)
+            load_x1<KIND>(c, xs0, wave, i, 0);
+    }
 #pragma unroll
     for (int j = 0; j < kNF; ++j) {
         load_codes(wa, j, c, 0);
         load_codes(wb, j, c, BK);
         load_span<FMT, G>(mc, j, c, 0);
+    }
+    if constexpr (KIND == kLora) {  // (whole tiles alone; x's buffers hold h first)
+        lora_start<ACT>(acc, *low, c, xs0, xs1, m0, M, wave, fr, n0 + wrow, N);
+#pragma unroll
+        for (int i = 0; i < x_blocks(kMF); ++i)
+            load_x1<KIND>(c, xs0, wave, i, 0);
     }
     __builtin_amdgcn_s_waitcnt(0x0f70);  // everything issued so far
     __syncthreads();                     // x step 0 and the NF4 level-pair table

@@ -11,8 +11,9 @@
 //    (ds_read_b64_tr_b16; layout and bank spread as in gemm_dx_tile.hpp);
 //  * rows of other adapters enter both tiles as zeros, and steps without a row
 //    of this adapter are left out: the rows' adapters are looked through first,
-//    1024 steps at a time;
-//  * the next step's rows are loaded while this one's products run;
+//    256 steps at a time;
+//  * the loads of the next three steps are in flight while one's products run
+//    (with one, 8 steps a workgroup took 29 us where the rows' bytes take 13);
 //  * dA's accumulators hold columns in a lane and dB's values r, so each is
 //    stored along its own rows;
 //  * with few columns and adapters the rows are split over workgroups, whose
@@ -28,7 +29,14 @@ constexpr int kGrBlock = 64 * kGrWaves;
 constexpr int kGrRows = 64;     // rows per step
 constexpr int kGrCols = 128;    // columns c per workgroup (32 per wave)
 constexpr int kGrPitch = 288;   // bytes of a staged row of 128 values
-constexpr int kGrList = 1024;   // steps listed at a time
+constexpr int kGrList = 256;    // steps listed at a time
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t gr_rsrc(const void *base, int64_t bytes)
+{
+    const uint32_t n = __builtin_amdgcn_readfirstlane(
+        bytes <= 0 ? 0u : (bytes >= 0x7fffffffll ? 0x7fffffffu : (uint32_t)bytes));
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n, 0x00020000);
+}
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 
@@ -60,10 +68,35 @@ struct Side {
     uint16_t *g;
 };
 
+// A thread's loads of a step: X's 16-byte chunks t % 16 of rows t / 16 + 16 i,
+// and of P's two parts 16-byte chunks one after another.
+template <int RF>
+struct GradStep {
+    u32x4 x[4];
+    u32x4 hi[RF > 2 ? 2 : 1], lo[RF > 2 ? 2 : 1];
+};
+
+// The LDS of a workgroup: two steps' tiles, and the steps listed.
+template <int ACT>
+struct GradLds {
+    char x[2][kGrRows * kGrPitch];
+    char xlo[ACT == Q4_F16 ? 2 : 1][ACT == Q4_F16 ? kGrRows * kGrPitch : 16];
+    char p[2][kGrRows * kGrPitch];
+    uint64_t mask[kGrList];  // rows of the adapter in the step
+    uint16_t list[kGrList];
+    int count;
+};
+
 template <int ACT, int RF, bool IS_B>
 __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cblock, int slice, int ad, int split,
-                                     char *xt, char *xl, char *pt, uint16_t *list, int *count)
+                                     GradLds<ACT> &lds)
 {
+    constexpr int kPPieces = kGrRows * 2 * RF;  // 8-value pieces of P's tile
+    constexpr int kPLoads = RF > 2 ? 2 : 1;     // ... a thread
+    static_assert(kPPieces <= kPLoads * kGrBlock, "pieces of P");
+    constexpr int kAhead = 3;                   // steps whose loads are in flight
+    constexpr uint32_t kPast = 0x80000000u;     // past every view
+
     const int t = threadIdx.x, lane = t & 63;
     const int wave = (int)__builtin_amdgcn_readfirstlane(t >> 6);
     const int fi = lane & 15, fq = lane >> 4;
@@ -85,94 +118,109 @@ __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cb
         __syncthreads();  // (the last list and tiles have been read)
         for (int s = wave; s < n; s += kGrWaves) {
             const int64_t m = (base + s) * kGrRows + lane;
-            const uint64_t any = __ballot(m < a.rows && adapter_of(a.ids, a.adapters, m) == ad);
+            const uint64_t mine = __ballot(m < a.rows && adapter_of(a.ids, a.adapters, m < a.rows ? m : 0) == ad);
             if (lane == 0)
-                list[s] = any != 0;
+                lds.mask[s] = mine;
         }
         __syncthreads();
         if (wave == 0) {
             int found = 0;
             for (int s = 0; s < n; s += 64) {
-                const bool on = s + lane < n && list[s + lane];
+                const bool on = s + lane < n && lds.mask[s + lane] != 0;
                 const uint64_t m = __ballot(on);
-                if (on)  // (behind this place nothing is still to be read: found <= s)
-                    list[found + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)(s + lane);
+                if (on)
+                    lds.list[found + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)(s + lane);
                 found += __popcll(m);
             }
             if (lane == 0)
-                *count = found;
+                lds.count = found;
         }
         __syncthreads();
-        const int found = *count;
+        const int found = __builtin_amdgcn_readfirstlane(lds.count);
 
-        u32x4 xv[4];
-        Parts8 pv[2 * RF > 2 ? RF / 2 : 1];
-        constexpr int kPPieces = kGrRows * 2 * RF;  // 8-value pieces of P's tile
-        constexpr int kPLoads = (kPPieces + kGrBlock - 1) / kGrBlock;
-        static_assert(sizeof(pv) / sizeof(pv[0]) >= kPLoads, "pieces of P");
-        auto load = [&](int i) {
-            const int64_t m0 = (base + list[i]) * kGrRows;
+        // (rows of other adapters, past the end, and columns and values past
+        // theirs are sent past the views and read as zeros; so are steps past
+        // the last listed one)
+        auto load = [&](GradStep<RF> &st, int i) {
+            const bool on = i < found;
+            const int s = __builtin_amdgcn_readfirstlane(on ? lds.list[i] : 0);
+            const uint64_t mask = on ? lds.mask[s] : 0;
+            const int64_t m0 = (base + s) * kGrRows;
+            const int rows = (int)(a.rows - m0 < kGrRows ? a.rows - m0 : kGrRows);
+            const __amdgpu_buffer_rsrc_t xr = gr_rsrc(side.x + m0 * side.cols, (int64_t)rows * side.cols * 2);
+            const __amdgpu_buffer_rsrc_t hr = gr_rsrc(side.p + m0 * a.rank, (int64_t)rows * a.rank * 2);
+            const __amdgpu_buffer_rsrc_t lr = gr_rsrc(side.p + (a.rows + m0) * a.rank, (int64_t)rows * a.rank * 2);
+            const int c = c0 + 8 * (t & 15);
+            const uint32_t cpast = c < side.cols ? 0u : kPast;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const int64_t m = m0 + (t >> 4) + 16 * q;
-                const int c = c0 + 8 * (t & 15);
-                xv[q] = u32x4{0, 0, 0, 0};
-                if (m < a.rows && c < side.cols && adapter_of(a.ids, a.adapters, m) == ad)
-                    xv[q] = *(const u32x4 *)(side.x + m * side.cols + c);
+                const int row = (t >> 4) + 16 * q;
+                const uint32_t none = (mask >> row) & 1 ? 0u : kPast;
+                st.x[q] = __builtin_amdgcn_raw_buffer_load_b128(
+                    xr, (int)(2u * (uint32_t)(row * side.cols + c) | none | cpast), 0, 0);
             }
 #pragma unroll
             for (int q = 0; q < kPLoads; ++q) {
-                const int p = t + kGrBlock * q;
-                const int64_t m = m0 + p / (2 * RF);
-                const int r = r0 + 8 * (p % (2 * RF));
-                pv[q] = Parts8{u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}};
-                if (p < kPPieces && m < a.rows && r < a.rank && adapter_of(a.ids, a.adapters, m) == ad) {
-                    const uint16_t *from = side.p + m * a.rank + r;
-                    pv[q].hi = *(const u32x4 *)from;
-                    pv[q].lo = *(const u32x4 *)(from + a.rows * a.rank);
-                }
+                const int p = t + kGrBlock * q, row = (p / (2 * RF)) & 63, r = r0 + 8 * (p % (2 * RF));
+                const uint32_t none = ((mask >> row) & 1) && p < kPPieces && r < a.rank ? 0u : kPast;
+                const int off = (int)(2u * (uint32_t)(row * a.rank + r) | none);
+                st.hi[q] = __builtin_amdgcn_raw_buffer_load_b128(hr, off, 0, 0);
+                st.lo[q] = __builtin_amdgcn_raw_buffer_load_b128(lr, off, 0, 0);
             }
         };
-        if (found)
-            load(0);
-        for (int i = 0; i < found; ++i) {
-            __syncthreads();  // (the last step's tiles have been read)
+        auto store = [&](const GradStep<RF> &st, int buf) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const Parts8 w = two_parts16<ACT>(xv[q]);
+                const Parts8 w = two_parts16<ACT>(st.x[q]);
                 const int at = gofs((t >> 4) + 16 * q, 8 * (t & 15));
-                *(u32x4 *)(xt + at) = w.hi;
+                *(u32x4 *)(lds.x[buf] + at) = w.hi;
                 if constexpr (ACT == Q4_F16)
-                    *(u32x4 *)(xl + at) = w.lo;
+                    *(u32x4 *)(lds.xlo[buf] + at) = w.lo;
             }
 #pragma unroll
             for (int q = 0; q < kPLoads; ++q) {
                 const int p = t + kGrBlock * q;
                 if (p < kPPieces) {
                     const int row = p / (2 * RF), r = 8 * (p % (2 * RF));
-                    *(u32x4 *)(pt + gofs(row, r)) = pv[q].hi;
-                    *(u32x4 *)(pt + gofs(row, 64 + r)) = pv[q].lo;
+                    *(u32x4 *)(lds.p[buf] + gofs(row, r)) = st.hi[q];
+                    *(u32x4 *)(lds.p[buf] + gofs(row, 64 + r)) = st.lo[q];
                 }
             }
-            __syncthreads();
-            if (i + 1 < found)
-                load(i + 1);
+        };
+        auto work = [&](int buf) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 Parts8 x[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    x[j].hi = column8(xt, h, 32 * wave + 16 * j);
+                    x[j].hi = column8(lds.x[buf], h, 32 * wave + 16 * j);
                     if constexpr (ACT == Q4_F16)
-                        x[j].lo = column8(xl, h, 32 * wave + 16 * j);
+                        x[j].lo = column8(lds.xlo[buf], h, 32 * wave + 16 * j);
                 }
 #pragma unroll
                 for (int f = 0; f < RF; ++f) {
-                    const Parts8 p{column8(pt, h, 16 * f), column8(pt, h, 64 + 16 * f)};
+                    const Parts8 p{column8(lds.p[buf], h, 16 * f), column8(lds.p[buf], h, 64 + 16 * f)};
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
                         acc[f][j] = IS_B ? mfma_parts_b<ACT>(p, x[j], acc[f][j]) : mfma_parts_a<ACT>(x[j], p, acc[f][j]);
                 }
+            }
+        };
+        // steps in flight in registers, the current one in one of two LDS
+        // buffers: one barrier a step
+        GradStep<RF> ring[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            load(ring[i], i);
+        for (int i0 = 0; i0 < found; i0 += 2 * kAhead) {
+#pragma unroll
+            for (int i = 0; i < 2 * kAhead; ++i) {
+                if (i0 + i >= found)
+                    break;
+                store(ring[i % kAhead], i & 1);
+                load(ring[i % kAhead], i0 + i + kAhead);
+                __syncthreads();
+                work(i & 1);
             }
         }
     }
@@ -198,22 +246,18 @@ __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cb
 
 // blockIdx: x columns of x, then of dy; y adapters and slices of r; z parts of the rows.
 template <int ACT, int RF>
-__global__ __launch_bounds__(kGrBlock) void grad_kernel(GradArgs a, int slices)
+__global__ __launch_bounds__(kGrBlock, 2) void grad_kernel(GradArgs a, int slices)
 {
-    __shared__ __attribute__((aligned(16))) char xt[kGrRows * kGrPitch];
-    __shared__ __attribute__((aligned(16))) char xl[ACT == Q4_F16 ? kGrRows * kGrPitch : 16];
-    __shared__ __attribute__((aligned(16))) char pt[kGrRows * kGrPitch];
-    __shared__ uint16_t list[kGrList];
-    __shared__ int count;
+    __shared__ __attribute__((aligned(16))) GradLds<ACT> lds;
     const int kblocks = (a.K + kGrCols - 1) / kGrCols;
     const int slice = blockIdx.y % slices, ad = blockIdx.y / slices;
     const int64_t asize = (int64_t)a.adapters * a.rank * a.K;
     if ((int)blockIdx.x < kblocks) {
         const Side side{(const uint16_t *)a.x, a.u, a.K, 0, (uint16_t *)a.da};
-        grad<ACT, RF, false>(a, side, blockIdx.x, slice, ad, blockIdx.z, xt, xl, pt, list, &count);
+        grad<ACT, RF, false>(a, side, blockIdx.x, slice, ad, blockIdx.z, lds);
     } else {
         const Side side{(const uint16_t *)a.dy, a.h, a.N, asize, (uint16_t *)a.db};
-        grad<ACT, RF, true>(a, side, blockIdx.x - kblocks, slice, ad, blockIdx.z, xt, xl, pt, list, &count);
+        grad<ACT, RF, true>(a, side, blockIdx.x - kblocks, slice, ad, blockIdx.z, lds);
     }
 }
 
