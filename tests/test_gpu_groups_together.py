@@ -15,6 +15,8 @@ pytestmark = pytest.mark.gpu
 
 def near(got, want, sums, act, tag):
     """`sums` bounds the error of the binary32 sums and of 16-bit second operands; the output is rounded once."""
+    if got.numel() == 0:
+        return
     worst = ((got.double() - want).abs() - (sums + half_step(act) * (want.abs() + sums) + 2.0 ** -25)).max()
     assert float(worst) <= 0, f"{tag}: {float(worst)}"
 
