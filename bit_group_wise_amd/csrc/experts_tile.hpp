@@ -29,14 +29,16 @@ __global__ __launch_bounds__(kBlock, Q4_EXPERTS_WAVES_PER_SIMD) void experts_til
     // the tile of as many quarters of its rows as the piece needs
     const int n = p.hi - p.lo;
 #define Q4_TILE(MF) gemm_tile<FMT, ACT, G, kGather, MF>(tile, x, codes, scales, zeros, K, vec_y, y, xs0, xs1, ptbl)
-    if (n > 12 * kPieceMF) {
+    if (kPieceMF == 4 || n > 12 * kPieceMF) {
         Q4_TILE(kPieceMF);
-    } else if (n > 8 * kPieceMF) {
-        Q4_TILE(kPieceMF * 3 / 4);
-    } else if (kPieceMF == 8 || n > 4 * kPieceMF) {
-        Q4_TILE(kPieceMF / 2);
-    } else if constexpr (kPieceMF > 8) {
-        Q4_TILE(kPieceMF / 4);
+    } else if constexpr (kPieceMF > 4) {
+        if (n > 8 * kPieceMF) {
+            Q4_TILE(kPieceMF * 3 / 4);
+        } else if (kPieceMF == 8 || n > 4 * kPieceMF) {
+            Q4_TILE(kPieceMF / 2);
+        } else if constexpr (kPieceMF > 8) {
+            Q4_TILE(kPieceMF / 4);
+        }
     }
 #undef Q4_TILE
 }

@@ -383,13 +383,13 @@ struct Tile {
 // B [n][r] straight from memory as the weights, the next adapter's while one
 // is worked on.  (One step of 2 or 3 products against the K / 64 of the
 // product itself.)
-template <int ACT>
+template <int ACT, int kMF>
 __device__ __forceinline__ void lora_start(f32x4 (&acc)[kNF][kMF], const LowRank &l, const TileCtx<kMF> &c, char *xs0,
                                            char *xs1, int m0, int mend, int wave, int fr, int nrow, int N)
 {
     const int lane = threadIdx.x & 63;
-    const int rows = min(mend - m0, BM);
-    constexpr int C = (BM + 63) / 64;
+    const int rows = min(mend - m0, 16 * kMF);
+    constexpr int C = (kMF + 3) / 4;
     AdapterSet<C> all;
     all.init(l.ids, l.adapters, m0, rows);
     const View hv = make_view(l.two + (int64_t)m0 * l.rank, (int64_t)rows * l.rank * 2);
@@ -605,7 +605,7 @@ __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__re
         load_codes(wb, j, c, BK);
         load_span<FMT, G>(mc, j, c, 0);
     }
-    if constexpr (KIND == kLora) {  // (whole tiles alone; x's buffers hold h first)
+    if constexpr (KIND == kLora) {  // (x's buffers hold h first)
         lora_start<ACT>(acc, *low, c, xs0, xs1, m0, M, wave, fr, n0 + wrow, N);
 #pragma unroll
         for (int i = 0; i < x_blocks(kMF); ++i)

@@ -114,10 +114,14 @@ q4_status q4_lora_gemm(q4_format f, int g, q4_dtype act_t, const void *x, int64_
         return Q4_EHIP;
     const LoraArgs a{x,          M,         codes,          scales,     zeros, N, K, lora->b,
                      lora->ids, lora->adapters, lora->rank, d.h, w.plan.parts, y};
-    // the kernel by the number of rows, as q4_gemm
+    // the kernel by the number of rows, as q4_gemm, but for tiles that would
+    // leave half of the compute units idle (835 rows of 553 x 8064, rank 80: 199
+    // -> 80 us in tiles of 64 rows; 619 of 682 x 1920, rank 24: 83 -> 35)
     if (M <= 96)
         return from_hip(launch_lora_skinny(f, g, act_t, a, s));
-    if (M <= 512)
+    if ((M + 255) / 256 * ((N + 127) / 128) < 128)
+        return from_hip(launch_lora_tile64(f, g, act_t, a, s));
+    if (M <= 512 || (M + 255) / 256 * ((N + 255) / 256) < 128)
         return from_hip(launch_lora_tile128(f, g, act_t, a, s));
     return from_hip(launch_lora_tile256(f, g, act_t, a, s));
 }

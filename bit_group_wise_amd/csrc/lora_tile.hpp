@@ -1,11 +1,18 @@
 // lora_tile.hpp -- y = x . What^T + h . B^T for many rows: gemm_tile.hpp's
-// tiles, begun with the adapters' part.
+// tiles of 16 Q4_LORA_MF rows, begun with the adapters' part.
 #pragma once
+
+#ifndef Q4_LORA_MF
+#define Q4_LORA_MF 16
+#endif
 
 #include "gemm_tile.hpp"
 
 namespace q4 {
 namespace {
+
+constexpr int kTileMF = Q4_LORA_MF;
+constexpr int kTileRows = 16 * kTileMF;
 
 template <int FMT, int ACT, int G>
 __global__ __launch_bounds__(kBlock) void lora_tile_kernel(const uint16_t *__restrict__ x, int M,
@@ -14,16 +21,16 @@ __global__ __launch_bounds__(kBlock) void lora_tile_kernel(const uint16_t *__res
                                                            const uint8_t *__restrict__ zeros, int N, int K, int mtiles,
                                                            int vec_y, LowRank low, uint16_t *__restrict__ y)
 {
-    Q4_GEMM_TILE_LDS(FMT, kMF);
-    const Tile tile{(int)(blockIdx.x % (unsigned)mtiles) * BM, M, (int)(blockIdx.x / (unsigned)mtiles) * BN,
+    Q4_GEMM_TILE_LDS(FMT, kTileMF);
+    const Tile tile{(int)(blockIdx.x % (unsigned)mtiles) * kTileRows, M, (int)(blockIdx.x / (unsigned)mtiles) * BN,
                     N, 0, N, nullptr, 0};
-    gemm_tile<FMT, ACT, G, kLora, kMF>(tile, x, codes, scales, zeros, K, vec_y, y, xs0, xs1, ptbl, &low);
+    gemm_tile<FMT, ACT, G, kLora, kTileMF>(tile, x, codes, scales, zeros, K, vec_y, y, xs0, xs1, ptbl, &low);
 }
 
 template <int FMT, int G>
 hipError_t launch_g(q4_dtype act_t, const LoraArgs &a, hipStream_t s)
 {
-    const int64_t mt = (a.M + BM - 1) / BM, nt = (a.N + BN - 1) / BN;
+    const int64_t mt = (a.M + kTileRows - 1) / kTileRows, nt = (a.N + BN - 1) / BN;
     if (mt * nt > 0x7fffffffll)
         return hipErrorInvalidValue;
     // 16-byte output stores need 16-byte rows

@@ -84,7 +84,8 @@ hipError_t launch_experts_skinny(q4_format f, int g, q4_dtype act_t, const Exper
 // kStreamMaxK and up to kStreamMaxCodes bytes of codes an expert.
 constexpr int64_t kStreamMaxK = 4096, kStreamMaxCodes = 0x7fff0000;
 hipError_t launch_experts_stream(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, int mt, hipStream_t s);
-// Tiles of up to 128 or 256 rows of an expert.
+// Tiles of up to 64, 128 or 256 rows of an expert.
+hipError_t launch_experts_tile64(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
 hipError_t launch_experts_tile128(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
 hipError_t launch_experts_tile256(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
 // The gradient dX[r] = dY[r] . What_e: x is dY, y is dX.
@@ -132,6 +133,7 @@ struct LoraArgs {
     void *y;  // or dX
 };
 hipError_t launch_lora_skinny(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
+hipError_t launch_lora_tile64(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
 hipError_t launch_lora_tile128(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
 hipError_t launch_lora_tile256(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
 hipError_t launch_lora_dx(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
