@@ -68,7 +68,8 @@ q4_status q4_experts_gemm_dx(q4_format f, int g, q4_dtype act_t, const void *dy,
     const q4_status st = check_experts(f, g, act_t, a);
     if (st != Q4_OK)
         return st;
-    if (N % 8 != 0 || N > Q4_GEMM_DX_MAX_N || N * (K / 2) > Q4_GEMV_CHAIN_MAX_CODES)
+    if (N % 8 != 0 || N > Q4_GEMM_DX_MAX_N || N * (K / 2) > Q4_GEMV_CHAIN_MAX_CODES ||
+        (K + 127) / 128 * most_pieces(rows, experts, 64) > INT32_MAX)
         return Q4_EUNSUPPORTED;
     if (rows == 0)
         return Q4_OK;

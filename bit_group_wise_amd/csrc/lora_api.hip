@@ -22,6 +22,10 @@ q4_status check_sizes(int64_t M, int64_t N, int64_t K, int adapters, int rank)
         return Q4_EUNSUPPORTED;
     if (rank % 8 != 0 || rank > Q4_LORA_MAX_RANK)
         return Q4_EUNSUPPORTED;
+    // the grids count tiles of at least 64 rows by 128 columns (M and the sides
+    // below 2^44 / 2^13 tiles)
+    if (M * N >= (int64_t)1 << 44 || M * K >= (int64_t)1 << 44)
+        return Q4_EUNSUPPORTED;
     // an adapter's matrices are addressed with 32 bits
     if (N > INT32_MAX / (2 * rank) || K > INT32_MAX / (2 * rank))
         return Q4_EUNSUPPORTED;

@@ -58,8 +58,9 @@ class Adapters:
             args[2] = _tensor(scale, "scale", torch.float32, (self.adapters,), self._index)
         self.a, self.b, self.scale = a, b, scale
         self._int32 = torch.int32
-        # what every call's record begins as (it holds the tensors' addresses)
+        # what every call's record begins as, with the addresses that were checked
         self._args = _LoraArgs(*args, None, self.adapters, self.rank)
+        self._addrs = tuple(args[:2])
         self._sizes = {}
 
     def __setattr__(self, name, value):
@@ -71,6 +72,9 @@ class Adapters:
         """The C record of a call on M rows, to be held while it runs."""
         if q.N != self.N or q.K != self.K or q.codes.get_device() != self._index:
             raise ValueError(f"the adapters are of a [{self.N}, {self.K}] weight on {self.device}")
+        if (self.a.data_ptr(), self.b.data_ptr()) != self._addrs:
+            # (storage replaced in place, as by `.data =` or set_())
+            raise ValueError("the adapters' storage was replaced: make a new Adapters")
         if ids is None:
             return self._args
         rec = _LoraArgs.from_buffer_copy(self._args)

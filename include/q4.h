@@ -5,9 +5,11 @@
  * Four operations: quantize fp16 weights to packed 4-bit codes plus per-group
  * metadata, dequantize them back to fp16/bf16, and multiply activations by
  * the quantized weights without materialising them (y = x . W^T), as a decode
- * GEMV (1 <= M <= 16) and a prefill GEMM (any M).  Beside them, the key/value
- * cache of a decoder in the same 4 bits: append, read back, attention over it
- * and eviction from it (q4_kv_*).
+ * GEMV (1 <= M <= 16) and a prefill GEMM (any M).  Beside them, products whose
+ * rows fall into groups, through the weights of a mixture's experts
+ * (q4_experts_*) and with each row's own low-rank adapter (q4_lora_*), both
+ * with their gradients; and the key/value cache of a decoder in the same 4
+ * bits: append, read back, attention over it and eviction from it (q4_kv_*).
  *
  * Definitions this library implements (web pages on 4-bit group-wise
  * quantization, cited by title and section):
@@ -310,12 +312,13 @@ q4_status q4_experts_gemm_dx(q4_format f, int g, q4_dtype act_t, const void *dy,
  * with 16 bits (a relative 2^-17), and each output is rounded once to act_t.
  * Results do not depend on timing (no floating-point atomics).
  * rank is a multiple of 8 up to Q4_LORA_MAX_RANK; N rank and K rank below
- * 2^30.  M = 0 is no work (gradients of the adapters: zeros).
+ * 2^30, and M N and M K below 2^44 (else Q4_EUNSUPPORTED).  M = 0 is no work
+ * (gradients of the adapters: zeros).
  * workspace: device memory of q4_lora_workspace_bytes for the same sizes,
  * 256-byte aligned, needed until the call's work has run; its contents before
  * and after do not matter (calls that may overlap need their own). */
 #define Q4_LORA_MAX_RANK 256
-#define Q4_LORA_MAX_ADAPTERS 16384
+#define Q4_LORA_MAX_ADAPTERS 16383
 #define Q4_LORA_MAX_ROWS 16777216
 typedef struct {
     const void *a;

@@ -56,6 +56,7 @@ def test_gemm_refuses(kw, status):
     (dict(dy=None), q4.EINVAL), (dict(dx=None), q4.EINVAL), (dict(N=60), q4.EUNSUPPORTED),
     (dict(dy=A + 8), q4.EALIGN), (dict(dx=A + 8), q4.EALIGN),
     (dict(N=8 * 524288, experts=1), q4.EUNSUPPORTED), (dict(N=262144, K=16384), q4.EUNSUPPORTED),
+    (dict(N=8, K=64 * 16384, rows=2 ** 30, experts=1), q4.EUNSUPPORTED),  # more workgroups than a grid has
 ])
 def test_dx_refuses(kw, status):
     assert dx(**kw) == status

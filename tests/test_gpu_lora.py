@@ -174,6 +174,17 @@ def test_every_row_its_own_adapter():
     check(x[:64], q, pairs, ids[:64])
 
 
+def test_many_rows_of_many_adapters():
+    """More steps of rows than a workgroup lists at a time, most without a row of its adapter."""
+    gen = generator(16)
+    M, A = 20000, 300
+    q = weight(64, 64, q4.NF4, 64, gen)
+    pairs = pairs_of(gen, q4.BF16, A, 8, 64, 64)
+    ids = torch.randint(-1, A, (M,), generator=gen, device=DEV).int()
+    ids[:16500] = torch.where(ids[:16500] == 7, 8, ids[:16500])  # adapter 7: in the last steps alone
+    check_backward(normal(gen, q4.BF16, M, 64), normal(gen, q4.BF16, M, 64), q, pairs, ids)
+
+
 @pytest.mark.parametrize("M", [3, 64, 200, 600])
 def test_rows_without_an_adapter_are_the_products_own(M):
     """The same bits as q4.gemm and q4.gemm_dx, and gradients of zero."""
@@ -401,6 +412,12 @@ def test_arguments():
         lora.gemm(x, weight(128, 64, q4.NF4, 64, gen), pairs)
     with pytest.raises(ValueError):
         lora.backward(x, x[:5], q, pairs)
+    moved = lora.Adapters(pairs.a.clone(), pairs.b)
+    moved.a.data = pairs.a.clone()
+    with pytest.raises(ValueError):
+        lora.gemm(x, q, moved)
+    with pytest.raises(AttributeError):
+        moved.a = pairs.a
     small = torch.empty((lora.workspace_bytes(6, pairs) - 1,), dtype=torch.uint8, device=DEV)
     with pytest.raises(q4.Q4Error) as e:
         lora.gemm(x, q, pairs, workspace=small)

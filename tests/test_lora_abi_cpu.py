@@ -47,7 +47,7 @@ def test_both_refuse(kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(a=None), q4.EINVAL), (dict(b=None), q4.EINVAL), (dict(adapters=0), q4.EINVAL), (dict(adapters=-1), q4.EINVAL),
     (dict(rank=0), q4.EINVAL), (dict(rank=-8), q4.EINVAL), (dict(rank=12), q4.EUNSUPPORTED),
-    (dict(rank=264), q4.EUNSUPPORTED), (dict(adapters=16385), q4.EUNSUPPORTED),
+    (dict(rank=264), q4.EUNSUPPORTED), (dict(adapters=16384), q4.EUNSUPPORTED),
     (dict(a=A + 8), q4.EALIGN), (dict(b=A + 8), q4.EALIGN), (dict(scale=A + 2), q4.EALIGN), (dict(ids=A + 2), q4.EALIGN),
 ])
 def test_adapters_refused(kw, status):
@@ -73,6 +73,11 @@ def test_backward_refuses(kw, status):
 def test_an_adapter_past_32_bits():
     assert gemm(pairs(rank=256), N=2 ** 22 + 8) == q4.EUNSUPPORTED
     assert gemm(pairs(rank=256), K=4194304, N=8) == q4.EUNSUPPORTED
+
+
+def test_more_tiles_than_a_grid_has():
+    assert gemm(M=2 ** 24, N=2 ** 20, K=64) == q4.EUNSUPPORTED
+    assert backward(M=2 ** 24, N=8, K=2 ** 20) == q4.EUNSUPPORTED
 
 
 def test_workspace_bytes():
