@@ -79,8 +79,9 @@ __device__ __forceinline__ int yswz(int r, int c) { return c ^ ((r >> 1) & 7); }
 typedef short v4i16 __attribute__((ext_vector_type(4)));
 
 // A tile of a grouped product (kDxGroup) lies among rows that may hold anything.
-// kDxLora: low-rank adapters beside the weight.
-enum { kDxDense = 0, kDxGroup = 1, kDxLora = 2 };
+// kDxLora: low-rank adapters beside the weight.  kDxLoraPart: the same for one
+// part of the weight's rows, in binary32.
+enum { kDxDense = 0, kDxGroup = 1, kDxLora = 2, kDxLoraPart = 3 };
 
 // One thread's loads of a step: 16-byte pieces of dY (chunk t % 8 of rows
 // t / 8 + 64 i), and for weight rows 2p, 2p + 1 of the step (p = t % 32)
@@ -168,6 +169,9 @@ __device__ __forceinline__ int wofs(int nl, int kl) { return nl * kWPitch + ((2 
 struct DxTile {
     int m0, mend, k0;
     int64_t wrow0, wrows;
+    int step0 = 0, steps = 0;  // kDxLoraPart: its steps of TN weight rows (0: the
+                               // adapters' too), and
+    float *part = nullptr;     // where its sums go, [rows, K]
 };
 
 // The tile's LDS.
@@ -329,15 +333,16 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
     // s, buffer s & 1 holds step s, one register set step s + 1 and the
     // other step s + 2.  Loads of steps past the end read zeros (rows
     // clamped) or unused data; the buffers they fill are never computed.
-    const int nsteps = (N + TN - 1) / TN;
+    const int nsteps = KIND == kDxLoraPart ? tile.steps : (N + TN - 1) / TN;
+    const int n0 = KIND == kDxLoraPart ? tile.step0 * TN : 0;
     DxLoads<kWMF> la, lb;
-    dx_load<FMT, KIND>(la, c, 0, k0);
-    dx_load<FMT, KIND>(lb, c, TN, k0);
+    dx_load<FMT, KIND>(la, c, n0, k0);
+    dx_load<FMT, KIND>(lb, c, n0 + TN, k0);
     // The adapters' part, u A, as steps of the same form: 64 values r of u as
     // the step's dY (its two parts in the two dY buffers) and the adapter's 64
     // rows of A as its weight rows (for fp16 its two parts in the two weight
     // buffers).
-    if constexpr (KIND == kDxLora) {
+    if (KIND == kDxLora || (KIND == kDxLoraPart && tile.step0 == 0)) {
         constexpr int C = TM / 64;
         const int rows = M - m0 < TM ? M - m0 : TM;
         AdapterSet<C> all;
@@ -468,13 +473,13 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
             *(u32x4 *)(wt[0] + wofs(t >> 3, 16 * (t & 7) + 8 * e)) = dequant8<FMT, ACT>(la.c[e], sc, bias, lp);
         }
     }
-    dx_load<FMT, KIND>(la, c, 2 * TN, k0);
+    dx_load<FMT, KIND>(la, c, n0 + 2 * TN, k0);
     __syncthreads();
     for (int st = 0; st < nsteps; st += 2) {
-        round(ys[0], wt[0], ys[1], wt[1], lb, (st + 3) * TN);  // step st; stages st + 1
+        round(ys[0], wt[0], ys[1], wt[1], lb, n0 + (st + 3) * TN);  // step st; stages st + 1
         if (st + 1 >= nsteps)
             break;
-        round(ys[1], wt[1], ys[0], wt[0], la, (st + 4) * TN);  // step st + 1; stages st + 2
+        round(ys[1], wt[1], ys[0], wt[0], la, n0 + (st + 4) * TN);  // step st + 1; stages st + 2
     }
 
     // lane (fi, fq) of fragment (j, f) holds
@@ -486,9 +491,13 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
 #pragma unroll
             for (int f = 0; f < kWMF; ++f) {
                 const int m = m0 + 16 * kWMF * wm + 16 * f + fi;
-                if (m < M)
+                if constexpr (KIND == kDxLoraPart) {
+                    if (m < M)
+                        *(f32x4 *)(tile.part + (int64_t)m * K + k) = acc[j][f];
+                } else if (m < M) {
                     *(u32x2 *)(dx + (int64_t)m * K + k) = u32x2{
                         pack2<ACT>(acc[j][f][0], acc[j][f][1]), pack2<ACT>(acc[j][f][2], acc[j][f][3])};
+                }
             }
         }
     }

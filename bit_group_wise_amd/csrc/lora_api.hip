@@ -53,10 +53,10 @@ q4_status check_lora(q4_format f, int g, q4_dtype act_t, int64_t M, const void *
 int64_t padded(int64_t floats) { return (4 * floats + 255) / 256 * 256; }
 
 // The workspace: h, then (backward) u, then sums that are joined: of the parts
-// of h and u, later of the gradients.
+// of h and u, later of dX and of the adapters' gradients.
 struct Layout {
     DownPlan plan;
-    int splits;
+    int splits, dx_parts;
     int64_t u, sums, bytes;
 };
 Layout layout(int64_t M, int64_t N, int64_t K, int adapters, int rank, int backward)
@@ -71,7 +71,10 @@ Layout layout(int64_t M, int64_t N, int64_t K, int adapters, int rank, int backw
     w.sums = kinds * one;
     const int64_t joined = w.plan.two && w.plan.parts > 1 ? padded((int64_t)kinds * w.plan.parts * M * rank) : 0;
     const int64_t grads = w.splits > 1 ? padded((int64_t)w.splits * adapters * rank * (N + K)) : 0;
-    w.bytes = w.sums + (joined > grads ? joined : grads);
+    w.dx_parts = backward ? lora_dx_parts(M, N, K) : 1;
+    const int64_t dx = w.dx_parts > 1 ? padded(w.dx_parts * M * K) : 0;
+    const int64_t most = joined > grads ? joined : grads;
+    w.bytes = w.sums + (most > dx ? most : dx);
     return w;
 }
 
@@ -117,7 +120,7 @@ q4_status q4_lora_gemm(q4_format f, int g, q4_dtype act_t, const void *x, int64_
     if (e != hipSuccess)
         return Q4_EHIP;
     const LoraArgs a{x,          M,         codes,          scales,     zeros, N, K, lora->b,
-                     lora->ids, lora->adapters, lora->rank, d.h, w.plan.parts, y};
+                     lora->ids, lora->adapters, lora->rank, d.h, w.plan.parts, y, 1, nullptr};
     // the kernel by the number of rows, as q4_gemm, but for tiles that would
     // leave half of the compute units idle (835 rows of 553 x 8064, rank 80: 199
     // -> 80 us in tiles of 64 rows; 619 of 682 x 1920, rank 24: 83 -> 35)
@@ -172,7 +175,7 @@ q4_status q4_lora_backward(q4_format f, int g, q4_dtype act_t, const void *dy, c
     hipError_t e = M > 0 ? launch_down(act_t, d, w.plan, s) : hipSuccess;
     if (e == hipSuccess && dx && M > 0) {
         const LoraArgs a{dy,        M,         codes,          scales,     zeros, N, K, lora->a,
-                         lora->ids, lora->adapters, lora->rank, d.u, w.plan.parts, dx};
+                         lora->ids, lora->adapters, lora->rank, d.u, w.plan.parts, dx, w.dx_parts, d.sums};
         e = launch_lora_dx(f, g, act_t, a, s);
     }
     if (e == hipSuccess && da) {

@@ -131,11 +131,15 @@ struct LoraArgs {
     const void *low;  // h or u as launch_down leaves it
     int parts;
     void *y;  // or dX
+    // dX: the weight's rows in so many parts, whose sums [dx_parts, M, K] go here
+    int dx_parts;
+    float *sums;
 };
 hipError_t launch_lora_skinny(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
 hipError_t launch_lora_tile64(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
 hipError_t launch_lora_tile128(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
 hipError_t launch_lora_tile256(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
+int lora_dx_parts(int64_t M, int64_t N, int64_t K);
 hipError_t launch_lora_dx(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
 
 // The adapters' gradients, dA[a] = sum u[m]^T x[m] and dB[a] = sum dy[m]^T

@@ -151,6 +151,18 @@ def test_odd_gradients(M, N, K):
     check_backward(normal(gen, q4.F16, M, N), normal(gen, q4.F16, M, K), q, pairs, ids)
 
 
+@pytest.mark.parametrize("N,K", [(2048, 128), (4104, 96), (7640, 640)])
+@pytest.mark.parametrize("M", [1, 70, 333])
+@pytest.mark.parametrize("act", [q4.F16, q4.BF16])
+def test_gradients_of_long_outputs(M, N, K, act):
+    """N in parts on different workgroups, their sums joined; rows of no adapter among them."""
+    gen = generator(M + N + K)
+    q = weight(N, K, q4.NF4_DQ if K % 64 == 0 else q4.INT4_ASYM, 64 if K % 64 == 0 else 32, gen)
+    pairs = pairs_of(gen, act, 3, 72, N, K)
+    ids = ids_of(gen, M, 3, "mixed")
+    check_backward(normal(gen, act, M, N), normal(gen, act, M, K), q, pairs, ids)
+
+
 def test_many_rows_of_one_adapter():
     """Rows split over workgroups, their sums joined; no ids, no scale."""
     gen = generator(6)
