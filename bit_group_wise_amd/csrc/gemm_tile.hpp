@@ -161,8 +161,9 @@ struct TileCtx {
 };
 
 // What is particular to a tile of a grouped product.  GATHER: its x rows are
-// those that an index names, anywhere in x.  LORA: low-rank adapters beside it.
-enum { kDense = 0, kGather = 1, kLora = 2 };
+// those that an index names, anywhere in x.  LORA: low-rank adapters beside it
+// (LORAPART: one part of K, in binary32).
+enum { kDense = 0, kGather = 1, kLora = 2, kLoraPart = 3 };
 // A chunk of x that is not there: past every view.
 constexpr uint32_t kNowhere = 0xfffffff0u;
 
@@ -375,6 +376,9 @@ struct Tile {
     int64_t wrow0, wrows;
     const int32_t *index;
     int xrows;
+    int k0 = 0, k1 = 0;     // kLoraPart: from k0 to k1, whole spans (0: with the
+    float *part = nullptr;  // adapters' part), the sums to here, rows of
+    int pitch = 0;          // `pitch` values (N up to a multiple of 4)
 };
 
 // The tile's accumulators as the adapters' part makes them, h B^T, with the
@@ -594,22 +598,25 @@ __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__re
     u32x4 wf[2][kNF];
     WStep wa, wb;
     MSpan<FMT, G> mc, mn;
-    if constexpr (KIND != kLora) {
+    constexpr bool kAdapters = KIND == kLora || KIND == kLoraPart;
+    const int kfirst = KIND == kLoraPart ? tile.k0 : 0, klast = KIND == kLoraPart ? tile.k1 : K;
+    if constexpr (!kAdapters) {
 #pragma unroll
         for (int i = 0; i < x_blocks(kMF); ++i)
             load_x1<KIND>(c, xs0, wave, i, 0);
     }
 #pragma unroll
     for (int j = 0; j < kNF; ++j) {
-        load_codes(wa, j, c, 0);
-        load_codes(wb, j, c, BK);
-        load_span<FMT, G>(mc, j, c, 0);
+        load_codes(wa, j, c, kfirst);
+        load_codes(wb, j, c, kfirst + BK);
+        load_span<FMT, G>(mc, j, c, kfirst);
     }
-    if constexpr (KIND == kLora) {  // (x's buffers hold h first)
-        lora_start<ACT>(acc, *low, c, xs0, xs1, m0, M, wave, fr, n0 + wrow, N);
+    if constexpr (kAdapters) {  // (x's buffers hold h first)
+        if (kfirst == 0)
+            lora_start<ACT>(acc, *low, c, xs0, xs1, m0, M, wave, fr, n0 + wrow, N);
 #pragma unroll
         for (int i = 0; i < x_blocks(kMF); ++i)
-            load_x1<KIND>(c, xs0, wave, i, 0);
+            load_x1<KIND>(c, xs0, wave, i, kfirst);
     }
     __builtin_amdgcn_s_waitcnt(0x0f70);  // everything issued so far
     __syncthreads();                     // x step 0 and the NF4 level-pair table
@@ -617,7 +624,7 @@ __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__re
     for (int j = 0; j < kNF; ++j) {
         float s, b;
         float2 lp[4];
-        wscale<FMT, G>(mc, j, 0, c, 0, s, b);
+        wscale<FMT, G>(mc, j, 0, c, kfirst, s, b);
         if constexpr (level_fmt(FMT) == Q4_NF4) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -632,7 +639,7 @@ __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__re
     // past K, where every weight has zero scale, so it adds exact zeros.
     // (A loop exit inside the span would keep two copies of the
     // accumulators live.)
-    for (int k0 = 0; k0 < K; k0 += kSpanK) {
+    for (int k0 = kfirst; k0 < klast; k0 += kSpanK) {
         kstep<FMT, ACT, G, 0, false, KIND, kMF>(acc, wf, wa, wb, mc, mc, mn, xs0, xs1, c, ptbl, wave, k0);
         kstep<FMT, ACT, G, 1, true, KIND, kMF>(acc, wf, wb, wa, mc, mc, mn, xs1, xs0, c, ptbl, wave, k0);
         kstep<FMT, ACT, G, 2, false, KIND, kMF>(acc, wf, wa, wb, mc, mc, mn, xs0, xs1, c, ptbl, wave, k0);
@@ -647,6 +654,13 @@ __device__ __forceinline__ void gemm_tile(const Tile &tile, const uint16_t *__re
         const int m = m0 + 16 * i + fr;
         if (m >= M)
             continue;
+        if constexpr (KIND == kLoraPart) {
+#pragma unroll
+            for (int j = 0; j < kNF; ++j)
+                if (nb + 4 * j < tile.pitch)
+                    *(f32x4 *)(tile.part + (int64_t)m * tile.pitch + nb + 4 * j) = acc[j][i];
+            continue;
+        }
         uint32_t p[2 * kNF];
 #pragma unroll
         for (int j = 0; j < kNF; ++j) {

@@ -52,11 +52,28 @@ q4_status check_lora(q4_format f, int g, q4_dtype act_t, int64_t M, const void *
 
 int64_t padded(int64_t floats) { return (4 * floats + 255) / 256 * 256; }
 
+// Whether a product of more than 96 rows runs in tiles of 64 (q4_lora_gemm).
+bool short_tiles(int64_t M, int64_t N) { return M > 96 && (M + 255) / 256 * ((N + 127) / 128) < 128; }
+
+// Parts of K for them: as many as give every compute unit a workgroup, of at
+// least 8 steps of 64.  Whole calls in us, whole / in parts: 237 rows of 147 x
+// 5888, rank 88, 60 / 26; 835 of 553 x 8064, rank 80, 85 / 45; 128 of 512 x 14336,
+// rank 16, 117 / 33; 128 of 4096 x 4096 42 / 28; 697 of 394 x 1472, rank 112, 29 /
+// 24; 512 of 4096 x 4096 46 / 44.
+int lora_parts(int64_t M, int64_t N, int64_t K)
+{
+    const int64_t tiles = (M + 63) / 64 * ((N + 127) / 128);
+    if (!short_tiles(M, N) || tiles >= 256)
+        return 1;
+    const int64_t parts = 256 / tiles, most = (K + 255) / 256 / 2;
+    return (int)(parts < most ? parts : (most > 1 ? most : 1));
+}
+
 // The workspace: h, then (backward) u, then sums that are joined: of the parts
-// of h and u, later of dX and of the adapters' gradients.
+// of h and u, later of y or of dX and of the adapters' gradients.
 struct Layout {
     DownPlan plan;
-    int splits, dx_parts;
+    int splits, out_parts;
     int64_t u, sums, bytes;
 };
 Layout layout(int64_t M, int64_t N, int64_t K, int adapters, int rank, int backward)
@@ -71,10 +88,10 @@ Layout layout(int64_t M, int64_t N, int64_t K, int adapters, int rank, int backw
     w.sums = kinds * one;
     const int64_t joined = w.plan.two && w.plan.parts > 1 ? padded((int64_t)kinds * w.plan.parts * M * rank) : 0;
     const int64_t grads = w.splits > 1 ? padded((int64_t)w.splits * adapters * rank * (N + K)) : 0;
-    w.dx_parts = backward ? lora_dx_parts(M, N, K) : 1;
-    const int64_t dx = w.dx_parts > 1 ? padded(w.dx_parts * M * K) : 0;
+    w.out_parts = backward ? lora_dx_parts(M, N, K) : lora_parts(M, N, K);
+    const int64_t out = w.out_parts > 1 ? padded(w.out_parts * M * (backward ? K : (N + 3) / 4 * 4)) : 0;
     const int64_t most = joined > grads ? joined : grads;
-    w.bytes = w.sums + (most > dx ? most : dx);
+    w.bytes = w.sums + (most > out ? most : out);
     return w;
 }
 
@@ -120,13 +137,13 @@ q4_status q4_lora_gemm(q4_format f, int g, q4_dtype act_t, const void *x, int64_
     if (e != hipSuccess)
         return Q4_EHIP;
     const LoraArgs a{x,          M,         codes,          scales,     zeros, N, K, lora->b,
-                     lora->ids, lora->adapters, lora->rank, d.h, w.plan.parts, y, 1, nullptr};
+                     lora->ids, lora->adapters, lora->rank, d.h, w.plan.parts, y, w.out_parts, d.sums};
     // the kernel by the number of rows, as q4_gemm, but for tiles that would
     // leave half of the compute units idle (835 rows of 553 x 8064, rank 80: 199
-    // -> 80 us in tiles of 64 rows; 619 of 682 x 1920, rank 24: 83 -> 35)
+    // -> 80 us in tiles of 64 rows, without parts; 619 of 682 x 1920, rank 24: 83 -> 35)
     if (M <= 96)
         return from_hip(launch_lora_skinny(f, g, act_t, a, s));
-    if ((M + 255) / 256 * ((N + 127) / 128) < 128)
+    if (short_tiles(M, N))
         return from_hip(launch_lora_tile64(f, g, act_t, a, s));
     if (M <= 512 || (M + 255) / 256 * ((N + 255) / 256) < 128)
         return from_hip(launch_lora_tile128(f, g, act_t, a, s));
@@ -175,7 +192,7 @@ q4_status q4_lora_backward(q4_format f, int g, q4_dtype act_t, const void *dy, c
     hipError_t e = M > 0 ? launch_down(act_t, d, w.plan, s) : hipSuccess;
     if (e == hipSuccess && dx && M > 0) {
         const LoraArgs a{dy,        M,         codes,          scales,     zeros, N, K, lora->a,
-                         lora->ids, lora->adapters, lora->rank, d.u, w.plan.parts, dx, w.dx_parts, d.sums};
+                         lora->ids, lora->adapters, lora->rank, d.u, w.plan.parts, dx, w.out_parts, d.sums};
         e = launch_lora_dx(f, g, act_t, a, s);
     }
     if (e == hipSuccess && da) {

@@ -58,7 +58,7 @@ hipError_t launch_ldx_parts(const LoraArgs &a, int gshift, hipStream_t s)
 {
     const int64_t mtiles = (a.M + 63) / 64, ktiles = (a.K + TK - 1) / TK;
     const LowRank low{nullptr, 0, (const uint16_t *)a.low, a.rank, a.adapters, a.M, a.ids, (const uint16_t *)a.w};
-    hipLaunchKernelGGL((lora_dx_part_kernel<FMT, ACT>), dim3((unsigned)(mtiles * ktiles), (unsigned)a.dx_parts),
+    hipLaunchKernelGGL((lora_dx_part_kernel<FMT, ACT>), dim3((unsigned)(mtiles * ktiles), (unsigned)a.out_parts),
                        dim3(kBlock), 0, s, (const uint16_t *)a.x, (int)a.M, a.codes, a.scales, a.zeros, (int)a.N,
                        (int)a.K, gshift, (int)mtiles, low, a.sums);
     const hipError_t e = hipGetLastError();
@@ -66,7 +66,7 @@ hipError_t launch_ldx_parts(const LoraArgs &a, int gshift, hipStream_t s)
         return e;
     const int64_t size = a.M * a.K;
     hipLaunchKernelGGL((lora_dx_join_kernel<ACT>), dim3((unsigned)((size / 4 + 255) / 256)), dim3(256), 0, s, a.sums,
-                       size, a.dx_parts, (uint16_t *)a.y);
+                       size, a.out_parts, (uint16_t *)a.y);
     return hipGetLastError();
 }
 
@@ -97,7 +97,7 @@ template <int FMT>
 hipError_t launch_ldx(q4_dtype act_t, const LoraArgs &a, int gshift, hipStream_t s)
 {
     const int64_t tiles = (a.M + 255) / 256 * ((a.K + TK - 1) / TK);
-    if (a.dx_parts > 1)
+    if (a.out_parts > 1)
         return act_t == Q4_BF16 ? launch_ldx_parts<FMT, Q4_BF16>(a, gshift, s)
                                 : launch_ldx_parts<FMT, Q4_F16>(a, gshift, s);
     if (tiles <= 64)

@@ -131,8 +131,9 @@ struct LoraArgs {
     const void *low;  // h or u as launch_down leaves it
     int parts;
     void *y;  // or dX
-    // dX: the weight's rows in so many parts, whose sums [dx_parts, M, K] go here
-    int dx_parts;
+    // the contraction (dX; y in tiles of 64 rows) in so many parts, whose sums go
+    // here, [out_parts, M, K] or [out_parts, M, N up to a multiple of 4]
+    int out_parts;
     float *sums;
 };
 hipError_t launch_lora_skinny(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);

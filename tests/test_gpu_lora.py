@@ -151,6 +151,19 @@ def test_odd_gradients(M, N, K):
     check_backward(normal(gen, q4.F16, M, N), normal(gen, q4.F16, M, K), q, pairs, ids)
 
 
+@pytest.mark.parametrize("N,K", [(1, 1024), (130, 2272), (147, 5888), (256, 3328)])
+@pytest.mark.parametrize("M", [97, 200, 450])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_long_rows(M, N, K, fmt):
+    """K in parts on different workgroups, their sums joined; rows of no adapter among them."""
+    gen = generator(M + N + K)
+    q = weight(N, K, fmt, 32, gen)
+    for act in (q4.F16, q4.BF16):
+        pairs = pairs_of(gen, act, 3, 72, N, K)
+        ids = ids_of(gen, M, 3, "mixed")
+        check(normal(gen, act, M, K), q, pairs, ids)
+
+
 @pytest.mark.parametrize("N,K", [(2048, 128), (4104, 96), (7640, 640)])
 @pytest.mark.parametrize("M", [1, 70, 333])
 @pytest.mark.parametrize("act", [q4.F16, q4.BF16])
