@@ -98,7 +98,8 @@ def _rows(t, name, width):
 
 
 def workspace_bytes(M, pairs, backward=False) -> int:
-    """Bytes of device workspace that a call on M rows needs (q4_lora_workspace_bytes)."""
+    """Bytes of device workspace that a call on M rows needs (q4_lora_workspace_bytes);
+    fewer rows may need more."""
     return pairs._bytes(M, bool(backward))
 
 

@@ -314,8 +314,9 @@ q4_status q4_experts_gemm_dx(q4_format f, int g, q4_dtype act_t, const void *dy,
  * rank is a multiple of 8 up to Q4_LORA_MAX_RANK; N rank and K rank below
  * 2^30, and M N and M K below 2^44 (else Q4_EUNSUPPORTED).  M = 0 is no work
  * (gradients of the adapters: zeros).
- * workspace: device memory of q4_lora_workspace_bytes for the same sizes,
- * 256-byte aligned, needed until the call's work has run; its contents before
+ * workspace: device memory of q4_lora_workspace_bytes for the same sizes
+ * (fewer rows may need more: few are shared out more finely), 256-byte
+ * aligned, needed until the call's work has run; its contents before
  * and after do not matter (calls that may overlap need their own). */
 #define Q4_LORA_MAX_RANK 256
 #define Q4_LORA_MAX_ADAPTERS 16383
