@@ -58,9 +58,12 @@ class Adapters:
             args[2] = _tensor(scale, "scale", torch.float32, (self.adapters,), self._index)
         self.a, self.b, self.scale = a, b, scale
         self._int32 = torch.int32
-        # what every call's record begins as, with the addresses that were checked
+        # what every call's record begins as, and the tensors as they were checked;
+        # their storages are held, so that nothing else can come to lie at the
+        # record's addresses
         self._args = _LoraArgs(*args, None, self.adapters, self.rank)
-        self._addrs = tuple(args[:2])
+        self._checked = self._seen()
+        self._held = tuple(t.untyped_storage() for t in (a, b, scale) if t is not None)
         self._sizes = {}
 
     def __setattr__(self, name, value):
@@ -68,12 +71,19 @@ class Adapters:
             raise AttributeError(f"an Adapters' {name} cannot be replaced")
         super().__setattr__(name, value)
 
+    def _seen(self):
+        """Where the tensors lie and what they are now."""
+        a, b, scale = self.a, self.b, self.scale
+        if scale is None:
+            return a.data_ptr(), b.data_ptr(), a.shape, b.shape, a.dtype, b.dtype
+        return a.data_ptr(), b.data_ptr(), scale.data_ptr(), a.shape, b.shape, scale.shape, a.dtype, b.dtype, scale.dtype
+
     def _record(self, q, ids, M):
         """The C record of a call on M rows, to be held while it runs."""
         if q.N != self.N or q.K != self.K or q.codes.get_device() != self._index:
             raise ValueError(f"the adapters are of a [{self.N}, {self.K}] weight on {self.device}")
-        if (self.a.data_ptr(), self.b.data_ptr()) != self._addrs:
-            # (storage replaced in place, as by `.data =` or set_())
+        if self._seen() != self._checked:
+            # (storage or shape replaced in place, as by `.data =`, set_() or resize_())
             raise ValueError("the adapters' storage was replaced: make a new Adapters")
         if ids is None:
             return self._args

@@ -448,3 +448,41 @@ def test_arguments():
         lora.gemm(x, q, pairs, workspace=small)
     assert e.value.status == q4.EINVAL
     assert ctypes.sizeof(lora._LoraArgs) == 40
+
+
+@pytest.mark.parametrize("part", ["a", "b", "scale"])
+def test_tensors_replaced_under_the_adapters(part):
+    """Another storage, shape or type behind a tensor's name is refused, and the first one's memory is not given away."""
+    gen = generator(17)
+    q = weight(64, 64, q4.NF4, 64, gen)
+    x = normal(gen, q4.BF16, 6, 64)
+
+    def made():
+        pairs = pairs_of(gen, q4.BF16, 2, 8, 64, 64)
+        lora.gemm(x, q, pairs)
+        return pairs, getattr(pairs, part)
+
+    def refused(pairs):
+        with pytest.raises(ValueError):
+            lora.gemm(x, q, pairs)
+        with pytest.raises(ValueError):
+            lora.backward(x, x, q, pairs)
+
+    pairs, t = made()
+    kept = t.clone()
+    t.mul_(0.5)  # (values may change)
+    lora.gemm(x, q, pairs)
+    old = t.data_ptr()
+    t.data = kept
+    refused(pairs)
+    others = [torch.empty_like(kept) for _ in range(64)]
+    assert old not in [o.data_ptr() for o in others]
+    pairs, t = made()
+    t.set_(torch.empty_like(t))
+    refused(pairs)
+    pairs, t = made()
+    t.data = t.data.reshape(-1)[:t.numel() // 2]
+    refused(pairs)
+    pairs, t = made()
+    t.data = t.data.view(torch.int32 if part == "scale" else torch.float16)
+    refused(pairs)
