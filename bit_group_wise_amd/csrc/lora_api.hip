@@ -160,7 +160,7 @@ q4_status q4_lora_backward(q4_format f, int g, q4_dtype act_t, const void *dy, c
         return st;
     if (N % 8 != 0 || N > Q4_GEMM_DX_MAX_N || N * (K / 2) > Q4_GEMV_CHAIN_MAX_CODES)
         return Q4_EUNSUPPORTED;
-    if ((!da) != (!db) || (!dx && !da))
+    if ((!da) != (!db) || (!dx && !da && M > 0))
         return Q4_EINVAL;
     if (!aligned(dx, 16) || !aligned(da, 16) || !aligned(db, 16))
         return Q4_EALIGN;
@@ -170,6 +170,8 @@ q4_status q4_lora_backward(q4_format f, int g, q4_dtype act_t, const void *dy, c
         if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(workspace, 256))
             return Q4_EALIGN;
     }
+    if (M == 0 && !da)  // (dX of no rows, which may be NULL)
+        return Q4_OK;
     const Layout w = layout(M, N, K, lora->adapters, lora->rank, 1);
     if (M > 0 && workspace_bytes < (size_t)w.bytes)
         return Q4_EINVAL;

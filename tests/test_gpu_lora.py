@@ -486,3 +486,15 @@ def test_tensors_replaced_under_the_adapters(part):
     pairs, t = made()
     t.data = t.data.view(torch.int32 if part == "scale" else torch.float16)
     refused(pairs)
+
+
+def test_each_gradient_of_no_rows_alone():
+    gen = generator(1)
+    q = weight(64, 128, q4.NF4, 64, gen)
+    pairs = pairs_of(gen, q4.BF16, 2, 8, 64, 128)
+    x, dy = normal(gen, q4.BF16, 0, 128), normal(gen, q4.BF16, 0, 64)
+    dx, da, db = lora.backward(dy, None, q, pairs, need_pairs=False)
+    assert dx.shape == (0, 128) and da is None and db is None
+    out = (None, torch.ones_like(pairs.a), torch.ones_like(pairs.b))
+    dx, da, db = lora.backward(dy, x, q, pairs, need_dx=False, out=out)
+    assert dx is None and not da.any() and not db.any()

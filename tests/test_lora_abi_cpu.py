@@ -96,3 +96,11 @@ def test_workspace_bytes():
 
 def test_no_rows_is_no_work():
     assert gemm(M=0, x=None, y=None, work=None, bytes=0) == q4.OK
+
+
+def test_the_gradient_of_no_rows():
+    """An empty tensor's address may be NULL, whichever gradients are wanted."""
+    none = dict(M=0, dy=None, x=None, da=None, db=None, work=None, bytes=0)
+    assert backward(**none) == q4.OK and backward(dx=None, **none) == q4.OK
+    assert backward(**dict(none, da=A)) == q4.EINVAL and backward(**dict(none, db=A)) == q4.EINVAL
+    assert backward(pairs(rank=12), **none) == q4.EUNSUPPORTED and backward(**dict(none, dx=A + 8)) == q4.EALIGN
