@@ -80,33 +80,21 @@ q4_status q4_experts_gemm_dx(q4_format f, int g, q4_dtype act_t, const void *dy,
 
 }  // extern "C"
 
-// The kernel by the mean number of rows an expert has (of the experts that can
-// have any).  Times in us, one card; a: 64 experts of 2048 x 4096 INT4-asym g
-// 32, b: 16 of 4096 x 4096 NF4 g 64, c: 64 of 1024 x 2048 INT4-sym g 64, d: 8
-// of 4096 x 14336 NF4 g 64; bf16 rows, uneven groups:
-//   mean                 4             8            12            16            24
-//   one block   a 80  b 39   a 96  b 42   a 105  b 53   a 118  b 60   a 151  b 77
-//   two blocks  a 83  b 46   a 89  b 53   a 103  b 55   a 109  b 64   a 121  b 77
-//   128 rows                 a 123 b 53   a 126  b 56   a 128  b 58   a 147  b 67
-//   two, 128    c 24         c 24  c 26   c 30   c 26   c 32   c 27   c 35   c 32
-//   skinny, 128 d 112        d 108 d 141  d 128  d 148  d 157  d 148  d 206  d 156
-//   mean                96           128           192           256
-//   128 rows    a 207  b 101  a 250  b 124  a 434  b 206  a 563  b 277
-//   256 rows    a 229  b 141  a 238  b 145  a 296  b 187  a 340  b 195
+
 hipError_t q4::launch_experts(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s)
 {
-    const int64_t mean = a.rows / (a.experts < a.rows ? a.experts : a.rows);
-    if (mean <= 12) {
-        if (a.K <= kStreamMaxK && a.N * (a.K / 2) <= kStreamMaxCodes)
-            return launch_experts_stream(f, g, act_t, a, mean < 8 ? 1 : 2, s);
+    switch (experts_kernel(a.rows, a.experts, a.N, a.K)) {
+    case ExpertsKernel::stream1:
+        return launch_experts_stream(f, g, act_t, a, 1, s);
+    case ExpertsKernel::stream2:
+        return launch_experts_stream(f, g, act_t, a, 2, s);
+    case ExpertsKernel::skinny:
         return launch_experts_skinny(f, g, act_t, a, s);
-    }
-    // tiles that would leave half of the compute units idle are cut: 2 experts of
-    // 298 x 6496 INT4-asym, 333 rows: 164 -> 63 us
-    const int64_t tiles = (a.rows + 127) / 128 * ((a.N + 127) / 128);
-    if (tiles < 128)
+    case ExpertsKernel::tile64:
         return launch_experts_tile64(f, g, act_t, a, s);
-    if (mean < 160 || tiles < 512)
+    case ExpertsKernel::tile128:
         return launch_experts_tile128(f, g, act_t, a, s);
-    return launch_experts_tile256(f, g, act_t, a, s);
+    default:
+        return launch_experts_tile256(f, g, act_t, a, s);
+    }
 }

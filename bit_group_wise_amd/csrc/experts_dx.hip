@@ -53,14 +53,11 @@ hipError_t launch_edx_rows(q4_dtype act_t, const ExpertsArgs &a, int gshift, hip
     return hipGetLastError();
 }
 
-// Pieces of 256 rows, or of 64 where those are too few to fill the card (1694
-// rows of 5 experts of 5864 x 256 INT4-sym g 32: 91 -> 55 us).
 template <int FMT>
 hipError_t launch_edx(q4_dtype act_t, const ExpertsArgs &a, int gshift, hipStream_t s)
 {
-    if ((a.rows + 255) / 256 * ((a.K + TK - 1) / TK) <= 64)
-        return launch_edx_rows<FMT, 1>(act_t, a, gshift, s);
-    return launch_edx_rows<FMT, 4>(act_t, a, gshift, s);
+    return experts_dx_rows(a.rows, a.K) == 64 ? launch_edx_rows<FMT, 1>(act_t, a, gshift, s)
+                                              : launch_edx_rows<FMT, 4>(act_t, a, gshift, s);
 }
 
 }  // namespace

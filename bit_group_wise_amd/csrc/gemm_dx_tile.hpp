@@ -60,6 +60,7 @@ constexpr int kKF = 4;                 // k fragments per wave (64 columns)
 constexpr int kWMF = TM / 64;          // m fragments per wave (4: 64 rows), and 16-byte
                                        // pieces of dY per thread and step
 
+static_assert(TK == kDxCols && TN == kDxStep, "the plan's tiles");
 static_assert(TK == 2 * 16 * kKF && TM == 4 * 16 * kWMF && kWaves == 8 && kWMF <= kKF, "2 x 4 waves");
 static_assert(TN * TK / 16 == kBlock, "16 columns of one row per thread");
 

@@ -15,6 +15,7 @@
 // is left out.
 #pragma once
 
+#include "plan.hpp"
 #include "q4_common.hpp"
 #include "q4_mfma.hpp"
 
@@ -104,8 +105,6 @@ __device__ __forceinline__ f32x4 mfma_parts_b(const Parts8 &a, const Parts8 &exa
     return mfma<Q4_BF16>(a.hi, exact.hi, c);
 }
 
-// Most parts that h is left in (the readers hold so many loads in flight).
-constexpr int kMostParts = 8;
 
 // The sum of h's partial sums at row m, r0 .. r0 + 7 (in order of the parts),
 // or zeros where not `there`; the parts by a view of them all.  All loads are

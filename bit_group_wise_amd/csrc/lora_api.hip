@@ -1,5 +1,5 @@
 // lora_api.hip -- the C ABI of low-rank adapters beside a weight (declared in
-// include/q4.h): host-side argument validation, workspace and dispatch.  As in
+// include/q4.h): host-side argument validation and dispatch.  As in
 // q4_api.hip, every check runs before the first HIP call.
 #include <hip/hip_runtime.h>
 
@@ -103,7 +103,7 @@ size_t q4_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int adapters, in
 {
     if (check_sizes(M, N, K, adapters, rank) != Q4_OK || M == 0)
         return 0;
-    return (size_t)layout(M, N, K, adapters, rank, backward != 0).bytes;
+    return (size_t)lora_layout(M, N, K, adapters, rank, backward != 0).bytes;
 }
 
 q4_status q4_lora_gemm(q4_format f, int g, q4_dtype act_t, const void *x, int64_t M, const uint8_t *codes,
@@ -117,7 +117,7 @@ q4_status q4_lora_gemm(q4_format f, int g, q4_dtype act_t, const void *x, int64_
         return Q4_EINVAL;
     if (!aligned(x, 16) || !aligned(y, 2) || !aligned(workspace, 256))
         return Q4_EALIGN;
-    const Layout w = layout(M, N, K, lora->adapters, lora->rank, 0);
+    const LoraLayout w = lora_layout(M, N, K, lora->adapters, lora->rank, 0);
     if (workspace_bytes < (size_t)w.bytes)
         return Q4_EINVAL;
     const hipStream_t s = (hipStream_t)stream;
@@ -138,16 +138,16 @@ q4_status q4_lora_gemm(q4_format f, int g, q4_dtype act_t, const void *x, int64_
         return Q4_EHIP;
     const LoraArgs a{x,          M,         codes,          scales,     zeros, N, K, lora->b,
                      lora->ids, lora->adapters, lora->rank, d.h, w.plan.parts, y, w.out_parts, d.sums};
-    // the kernel by the number of rows, as q4_gemm, but for tiles that would
-    // leave half of the compute units idle (835 rows of 553 x 8064, rank 80: 199
-    // -> 80 us in tiles of 64 rows, without parts; 619 of 682 x 1920, rank 24: 83 -> 35)
-    if (M <= 96)
+    switch (lora_kernel(M, N)) {
+    case LoraKernel::skinny:
         return from_hip(launch_lora_skinny(f, g, act_t, a, s));
-    if (short_tiles(M, N))
+    case LoraKernel::tile64:
         return from_hip(launch_lora_tile64(f, g, act_t, a, s));
-    if (M <= 512 || (M + 255) / 256 * ((N + 255) / 256) < 128)
+    case LoraKernel::tile128:
         return from_hip(launch_lora_tile128(f, g, act_t, a, s));
-    return from_hip(launch_lora_tile256(f, g, act_t, a, s));
+    default:
+        return from_hip(launch_lora_tile256(f, g, act_t, a, s));
+    }
 }
 
 q4_status q4_lora_backward(q4_format f, int g, q4_dtype act_t, const void *dy, const void *x, int64_t M,
@@ -172,7 +172,7 @@ q4_status q4_lora_backward(q4_format f, int g, q4_dtype act_t, const void *dy, c
     }
     if (M == 0 && !da)  // (dX of no rows, which may be NULL)
         return Q4_OK;
-    const Layout w = layout(M, N, K, lora->adapters, lora->rank, 1);
+    const LoraLayout w = lora_layout(M, N, K, lora->adapters, lora->rank, 1);
     if (M > 0 && workspace_bytes < (size_t)w.bytes)
         return Q4_EINVAL;
     const hipStream_t s = (hipStream_t)stream;

@@ -135,8 +135,8 @@ __global__ __launch_bounds__(kFewBlock) void down_few_kernel(DownArgs a)
 
 // --------------------------------------------------------------- more rows
 constexpr int kBlock = 256;  // 4 waves of 16 rows
-constexpr int kRows = 64;
-constexpr int kStep = 64;    // of the long axis
+constexpr int kRows = kDownRows;
+constexpr int kStep = kDownStep;  // of the long axis
 constexpr int kAhead = 3;    // steps whose loads are in flight in registers
 
 // Position of 16-byte chunk c of a staged row of 128 bytes.
@@ -362,31 +362,6 @@ hipError_t launch_dn(const DownArgs &a, const DownPlan &p, hipStream_t s)
 }
 
 }  // namespace
-
-DownPlan down_plan(int64_t rows, int64_t longest, int adapters, int rank, int backward)
-{
-    DownPlan p;
-    p.two = backward || rows > 96;  // (96: as far as the skinny product goes)
-    p.rf = rank <= 16 ? 1 : (rank <= 32 ? 2 : 4);
-    p.slices = (rank + 16 * p.rf - 1) / (16 * p.rf);
-    const int tile = p.two ? kRows : 16;
-    p.tiles = (rows + tile - 1) / tile;
-    // few rows: their adapters side by side
-    const int64_t most = adapters < rows ? adapters : rows;
-    p.slots = rows <= 512 ? (int)(most < 16 ? most : 16) : 1;
-    if (p.slots < 1)
-        p.slots = 1;
-    // parts of the long axis: as many as give every compute unit two
-    // workgroups, of at least 16 (few rows) or 8 steps each; with up to 16
-    // steps of 64 the join's launch would cost more than it saves
-    const int64_t blocks = p.tiles * p.slices * p.slots * (backward ? 2 : 1);
-    const int64_t steps = p.two ? (longest + kStep - 1) / kStep : (longest + 31) / 32;
-    const int64_t most_parts = p.two ? (steps <= 16 ? 1 : steps / 8) : steps / 16;
-    int64_t parts = 512 / (blocks ? blocks : 1);
-    parts = parts < most_parts ? parts : most_parts;
-    p.parts = (int)(parts < 1 ? 1 : (parts > kMostParts ? kMostParts : parts));
-    return p;
-}
 
 hipError_t launch_down(q4_dtype act_t, DownArgs a, const DownPlan &p, hipStream_t s)
 {

@@ -20,8 +20,6 @@ __global__ __launch_bounds__(kBlock) void lora_dx_kernel(const uint16_t *__restr
     dx_tile<FMT, ACT, kDxLora, WMF>(tile, dy, codes, scales, zeros, N, K, gshift, dx, ys, wt, ptbl, &low);
 }
 
-constexpr int kPartSteps = 8;  // least steps of TN rows of a part
-
 template <int FMT, int ACT>
 __global__ __launch_bounds__(kBlock) void lora_dx_part_kernel(const uint16_t *__restrict__ dy, int M,
                                                               const uint8_t *__restrict__ codes,
@@ -87,39 +85,23 @@ hipError_t launch_ldx_rows(q4_dtype act_t, const LoraArgs &a, int gshift, hipStr
     return hipGetLastError();
 }
 
-// Tiles of 256 rows, or of 128 or 64 where those too are one round of
-// workgroups or less (256 compute units): a short tile takes less time, but a
-// weight's column is dequantized once a tile.  dX alone, rank 16, in us, with
-// tiles of 256 / 128 / 64 rows: 512 rows of 4096 x 4096 NF4 g 64 (64 tiles of
-// 256) 80 / 64 / 57, 768 rows (96) 81 / 64 / 100, 1024 rows (128) 81 / 65 / 100;
-// 333 rows of 1024 x 1024 (16) 30 / 23 / 20.
 template <int FMT>
 hipError_t launch_ldx(q4_dtype act_t, const LoraArgs &a, int gshift, hipStream_t s)
 {
-    const int64_t tiles = (a.M + 255) / 256 * ((a.K + TK - 1) / TK);
     if (a.out_parts > 1)
         return act_t == Q4_BF16 ? launch_ldx_parts<FMT, Q4_BF16>(a, gshift, s)
                                 : launch_ldx_parts<FMT, Q4_F16>(a, gshift, s);
-    if (tiles <= 64)
+    switch (lora_dx_rows(a.M, a.K)) {
+    case 64:
         return launch_ldx_rows<FMT, 1>(act_t, a, gshift, s);
-    if (tiles <= 128)
+    case 128:
         return launch_ldx_rows<FMT, 2>(act_t, a, gshift, s);
-    return launch_ldx_rows<FMT, 4>(act_t, a, gshift, s);
+    default:
+        return launch_ldx_rows<FMT, 4>(act_t, a, gshift, s);
+    }
 }
 
 }  // namespace
-
-// Parts of N: as many as give every compute unit a workgroup, of at least
-// kPartSteps steps.  dX alone in us, NF4 g 64, rank 16, whole / in parts of at
-// least 16 / of 8 steps: 1 row, N 7640, K 1024 89 / 27 / 24; 16 rows of 4096 x
-// 4096 53 / 26 / 23; 64 of 14336 x 4096 162 / 43 / 42; 16 of 2048 x 4096 32 / 25 /
-// 21; 333 of 4096 x 2048 55 / 39 / 39; 333 of 1024 x 1024 (16 steps) 19.6 / 19.6 / 18.8.
-int lora_dx_parts(int64_t M, int64_t N, int64_t K)
-{
-    const int64_t tiles = (M + 63) / 64 * ((K + TK - 1) / TK), steps = (N + TN - 1) / TN;
-    const int64_t parts = tiles > 0 && tiles < 256 ? 256 / tiles : 1, most = steps / kPartSteps;
-    return (int)(parts < most ? parts : (most > 1 ? most : 1));
-}
 
 hipError_t launch_lora_dx(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s)
 {

@@ -26,8 +26,6 @@ namespace {
 
 constexpr int kGrWaves = 4;
 constexpr int kGrBlock = 64 * kGrWaves;
-constexpr int kGrRows = 64;     // rows per step
-constexpr int kGrCols = 128;    // columns c per workgroup (32 per wave)
 constexpr int kGrPitch = 288;   // bytes of a staged row of 128 values
 constexpr int kGrList = 256;    // steps listed at a time
 
@@ -279,8 +277,6 @@ __global__ __launch_bounds__(256) void grad_join_kernel(GradArgs a)
     *(u32x2 *)to = u32x2{pack2<ACT>(v[0], v[1]), pack2<ACT>(v[2], v[3])};
 }
 
-int grad_rf(int rank) { return rank <= 16 ? 1 : (rank <= 32 ? 2 : 4); }
-
 template <int ACT>
 hipError_t launch_grad_act(const GradArgs &a, hipStream_t s)
 {
@@ -302,18 +298,6 @@ hipError_t launch_grad_act(const GradArgs &a, hipStream_t s)
 }
 
 }  // namespace
-
-// Parts of the rows: as many as give every compute unit two workgroups, at
-// least four steps each, at most 8 (their sums are written and read).
-int grad_splits(int64_t rows, int64_t N, int64_t K, int adapters, int rank)
-{
-    const int rf = grad_rf(rank), slices = (rank + 16 * rf - 1) / (16 * rf);
-    const int64_t blocks = ((K + kGrCols - 1) / kGrCols + (N + kGrCols - 1) / kGrCols) * adapters * slices;
-    const int64_t steps = (rows + kGrRows - 1) / kGrRows;
-    int64_t n = 512 / blocks;
-    n = n < steps / 4 ? n : steps / 4;
-    return (int)(n < 1 ? 1 : (n > 8 ? 8 : n));
-}
 
 hipError_t launch_lora_grad(q4_dtype act_t, const GradArgs &a, hipStream_t s)
 {

@@ -6,6 +6,7 @@
 
 #include <cstdint>
 
+#include "plan.hpp"
 #include "q4.h"
 
 namespace q4 {
@@ -82,7 +83,6 @@ hipError_t launch_experts(q4_format f, int g, q4_dtype act_t, const ExpertsArgs 
 hipError_t launch_experts_skinny(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
 // Pieces of up to 16 mt (1 or 2) rows by resident workgroups, for K up to
 // kStreamMaxK and up to kStreamMaxCodes bytes of codes an expert.
-constexpr int64_t kStreamMaxK = 4096, kStreamMaxCodes = 0x7fff0000;
 hipError_t launch_experts_stream(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, int mt, hipStream_t s);
 // Tiles of up to 64, 128 or 256 rows of an expert.
 hipError_t launch_experts_tile64(q4_format f, int g, q4_dtype act_t, const ExpertsArgs &a, hipStream_t s);
@@ -105,15 +105,6 @@ struct DownArgs {
     int N, K, adapters, rank;
     int slices, slots, parts;  // of the plan
 };
-// How they are cut: a tile of rows, 16 rf values r and one of `parts` parts of
-// the long axis a workgroup, the adapters of a tile over `slots` workgroups.
-// two: left as two 16-bit parts, the parts of the axis joined.
-struct DownPlan {
-    bool two;
-    int rf, slices, slots, parts;
-    int64_t tiles;
-};
-DownPlan down_plan(int64_t rows, int64_t longest, int adapters, int rank, int backward);
 hipError_t launch_down(q4_dtype act_t, DownArgs a, const DownPlan &p, hipStream_t s);
 
 // The products with the adapters' part added: y = x What^T + h B^T and dX = dY
@@ -140,7 +131,6 @@ hipError_t launch_lora_skinny(q4_format f, int g, q4_dtype act_t, const LoraArgs
 hipError_t launch_lora_tile64(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
 hipError_t launch_lora_tile128(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
 hipError_t launch_lora_tile256(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
-int lora_dx_parts(int64_t M, int64_t N, int64_t K);
 hipError_t launch_lora_dx(q4_format f, int g, q4_dtype act_t, const LoraArgs &a, hipStream_t s);
 
 // The adapters' gradients, dA[a] = sum u[m]^T x[m] and dB[a] = sum dy[m]^T
@@ -155,7 +145,6 @@ struct GradArgs {
     int N, K, adapters, rank, splits;
     void *da, *db;
 };
-int grad_splits(int64_t rows, int64_t N, int64_t K, int adapters, int rank);
 hipError_t launch_lora_grad(q4_dtype act_t, const GradArgs &a, hipStream_t s);
 
 }  // namespace q4

@@ -8,6 +8,7 @@ import torch
 
 from bit_group_wise_amd import experts, q4
 from _groups import ACTS, DEV, FORMATS, assert_product, generator, normal, values, weight
+from _sizes import EXPERTS, EXPERTS_DX
 
 pytestmark = pytest.mark.gpu
 
@@ -52,7 +53,7 @@ def check_dx(dy, q, offsets, out=None, tag=""):
     return dx
 
 
-# counts whose means choose each kernel: 1, 2 and 4 blocks of 16 rows, tiles of 128 and of 256
+# small groups: streamed, and in tiles of 64 rows (sizes that reach each kernel: EXPERTS below)
 COUNTS = {
     "one": [0, 1, 0, 0],
     "few": [3, 0, 17, 5, 1],
@@ -267,3 +268,102 @@ def test_arguments():
         experts.gemm_dx(x[:, :32].contiguous(), q, off)
     with pytest.raises(TypeError):
         experts.gemm(x, q, off, index=off[:3].float())
+
+
+def framed(act, rows, width, before, behind, value):
+    """[before + rows + behind, width] of `value`, beginning at an odd element, and its flat storage."""
+    n = (before + rows + behind) * width
+    flat = torch.full((n + 16,), value, dtype=ACTS[act], device=DEV)
+    return flat[1:1 + n].view(-1, width), flat
+
+
+def kept(y, flat, before, rows, value):
+    """Whether all but the groups' rows still holds `value`."""
+    y = y.clone()
+    inside = y[before:before + rows].numel()
+    return (int((flat == value).sum()) - int((y[before:before + rows] == value).sum())) == flat.numel() - inside
+
+
+@pytest.mark.parametrize("name", list(EXPERTS))
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_each_kernel(fmt, name):
+    """Rows as they lie, gathered ones, bad indexes, rows outside the groups, a row of NaN, outputs at any element."""
+    _, counts, before, behind, N, K, g = EXPERTS[name]
+    gen = generator(fmt + N + K)
+    n, act = sum(counts), (fmt + len(name)) % 2
+    q = weight(len(counts) * N, K, fmt, g, gen)
+    off = offsets_of(counts, before)
+    x = normal(gen, act, before + n + behind, K)
+    x[:before], x[before + n:] = float("nan"), float("inf")
+    y = torch.full((before + n + behind, N), 3.0, dtype=x.dtype, device=DEV)
+    check(x, q, off, out=y, tag=name)
+    assert bool((y[:before] == 3).all()) and bool((y[before + n:] == 3).all())
+
+    bad = before + n // 2
+    x[bad] = float("nan")
+    again = experts.gemm(x, q, off)
+    assert bool(torch.isnan(again[bad]).all())
+    inside = torch.arange(x.shape[0], device=DEV)
+    inside = (inside >= before) & (inside < before + n) & (inside != bad)
+    assert torch.equal(again[inside], y[inside])
+
+    tokens = 3 + n // 2
+    t = normal(gen, act, tokens, K)
+    index = torch.randint(0, tokens, (x.shape[0],), generator=gen, device=DEV).int()
+    index[:before], index[before + n:] = tokens, -7
+    index[before:before + n][::5], index[before:before + n][3::7] = -1, tokens
+    got, flat = framed(act, n, N, before, behind, 3.0)
+    got = check(t, q, off, index, out=got, tag=f"{name} gathered")
+    none = (index < 0) | (index >= tokens)
+    none[:before], none[before + n:] = False, False
+    assert bool((got[none] == 0).all()) and kept(got, flat, before, n, 3.0)
+
+
+@pytest.mark.parametrize("name", list(EXPERTS_DX))
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_each_gradient_kernel(fmt, name):
+    _, counts, before, behind, N, K, g = EXPERTS_DX[name]
+    gen = generator(fmt + N + K)
+    n, act = sum(counts), (fmt + len(name)) % 2
+    q = weight(len(counts) * N, K, fmt, g, gen)
+    off = offsets_of(counts, before)
+    dy = normal(gen, act, before + n + behind, N)
+    dy[:before], dy[before + n:] = float("nan"), float("inf")
+    dx = torch.full((before + n + behind, K), 3.0, dtype=dy.dtype, device=DEV)
+    check_dx(dy, q, off, out=dx, tag=name)
+    assert bool((dx[:before] == 3).all()) and bool((dx[before + n:] == 3).all())
+    bad = before + n // 2
+    dy[bad] = float("nan")
+    again = experts.gemm_dx(dy, q, off)
+    assert bool(torch.isnan(again[bad]).all())
+    inside = torch.arange(dy.shape[0], device=DEV)
+    inside = (inside >= before) & (inside < before + n) & (inside != bad)
+    assert torch.equal(again[inside], dx[inside])
+
+
+@pytest.mark.parametrize("name", ["stream1", "stream2", "skinny", "tile128", "tile256"])
+def test_each_kernel_captured_and_replayed_with_other_groups(name):
+    _, counts, before, behind, N, K, g = EXPERTS[name]
+    gen = generator(N)
+    rows = before + sum(counts) + behind
+    q = weight(len(counts) * N, K, q4.NF4_DQ, g, gen)
+    x, off = normal(gen, q4.BF16, rows, K), offsets_of(counts, before)
+    y = torch.zeros((rows, N), dtype=x.dtype, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        experts.gemm(x, q, off, out=y)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        experts.gemm(x, q, off, out=y)
+    for k in range(4):
+        cuts = torch.randint(0, rows + 1, (len(counts) + 1,), generator=gen, device=DEV).sort().values.int()
+        off.copy_(cuts if k < 3 else torch.full_like(cuts, rows).index_fill_(0, torch.tensor([0], device=DEV), 0))
+        y.zero_()
+        x.copy_(normal(gen, q4.BF16, rows, K))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = torch.zeros_like(y)
+        check(x, q, off, out=want, tag=f"{name} {k}")
+        assert torch.equal(y, want)
