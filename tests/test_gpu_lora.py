@@ -9,6 +9,7 @@ import torch
 
 from bit_group_wise_amd import lora, q4
 from _groups import ACTS, DEV, FORMATS, generator, half_step, normal, tiny, values, weight
+from _sizes import LORA, LORA_DX
 
 pytestmark = pytest.mark.gpu
 
@@ -498,3 +499,69 @@ def test_each_gradient_of_no_rows_alone():
     out = (None, torch.ones_like(pairs.a), torch.ones_like(pairs.b))
     dx, da, db = lora.backward(dy, x, q, pairs, need_dx=False, out=out)
     assert dx is None and not da.any() and not db.any()
+
+
+@pytest.mark.parametrize("rank", [8, 72, 256])
+@pytest.mark.parametrize("name", list(LORA))
+def test_each_kernel(name, rank):
+    """Mixed adapters and none, an adapter that is not finite, a row of NaN, outputs at any element."""
+    _, M, N, K, g = LORA[name]
+    gen = generator(M + N + rank)
+    for act in (q4.F16, q4.BF16):
+        q = weight(N, K, FORMATS[(len(name) + rank // 8 + act) % 5], g, gen)
+        pairs = pairs_of(gen, act, 5, rank, N, K)
+        ids = ids_of(gen, M, 5, "mixed")
+        bad = M // 2
+        ids[0], ids[bad] = 1, 4
+        x = normal(gen, act, M, K)
+        y = check(x, q, pairs, ids, name)
+        flat = torch.full((M * N + 16,), 3.0, dtype=x.dtype, device=DEV)
+        got = lora.gemm(x, q, pairs, ids, out=flat[1:1 + M * N].view(M, N))
+        assert torch.equal(got, y) and bool((flat[:1] == 3).all()) and bool((flat[1 + M * N:] == 3).all())
+        x[bad] = float("nan")
+        pairs.a[3], pairs.b[3] = float("nan"), float("inf")
+        keep = (ids != 3) & (torch.arange(M, device=DEV) != bad)
+        got = lora.gemm(x, q, pairs, ids)
+        assert torch.equal(got[keep], y[keep]) and bool(torch.isnan(got[bad]).all())
+        assert not bool((ids == 3).any()) or not bool(torch.isfinite(got[ids == 3]).any())
+
+
+@pytest.mark.parametrize("rank", [16, 136])
+@pytest.mark.parametrize("name", list(LORA_DX))
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_each_gradient_kernel(fmt, name, rank):
+    _, _, M, N, K, g = LORA_DX[name]
+    gen = generator(M + N + rank)
+    act = (fmt + rank // 8) % 2
+    q = weight(N, K, fmt, g, gen)
+    pairs = pairs_of(gen, act, 3, rank, N, K)
+    ids = ids_of(gen, M, 3, "mixed")
+    check_backward(normal(gen, act, M, N), normal(gen, act, M, K), q, pairs, ids, name)
+
+
+def test_kernels_captured_and_replayed():
+    """The wide tiles, with other ids and adapters between replays."""
+    for name in ("tile128", "tile256", "skinny-blocks3"):
+        _, M, N, K, g = LORA[name]
+        gen = generator(N)
+        q = weight(N, K, q4.INT4_ASYM, g, gen)
+        pairs = pairs_of(gen, q4.BF16, 3, 24, N, K)
+        ids, x = ids_of(gen, M, 3, "mixed"), normal(gen, q4.BF16, M, K)
+        work = torch.empty((lora.workspace_bytes(M, pairs),), dtype=torch.uint8, device=DEV)
+        out = x.new_empty((M, N))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            lora.gemm(x, q, pairs, ids, out=out, workspace=work)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            lora.gemm(x, q, pairs, ids, out=out, workspace=work)
+        for seed in range(3):
+            gen = generator(200 + seed)
+            pairs.b.copy_(normal(gen, q4.BF16, 3, N, 24))
+            ids.copy_(ids_of(gen, M, 3, "mixed"))
+            x.copy_(normal(gen, q4.BF16, M, K))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, check(x, q, pairs, ids, name))
