@@ -101,10 +101,14 @@ class Adapters:
         return n
 
 
-def _rows(t, name, width):
-    if t.dim() != 2 or t.shape[1] != width:
-        raise ValueError(f"{name} must be [rows, {width}], got {list(t.shape)}")
-    return t.shape[0]
+def _rows(t, name, width, pairs):
+    """Address and rows of a contiguous tensor [rows, width] of the adapters' type, on their device."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width:
+        raise ValueError(f"{name} must be [rows, {width}], got {list(shape)}")
+    if t.dtype != pairs.dtype or t.get_device() != pairs._index or not t.is_contiguous():
+        _refuse(t, name, pairs.dtype, shape, pairs._index)
+    return t.data_ptr(), shape[0]
 
 
 def workspace_bytes(M, pairs, backward=False) -> int:
@@ -125,9 +129,8 @@ def gemm(x, q, pairs, ids=None, *, out=None, workspace=None):
     """y = x . What^T + scale (x a^T) b^T with each row's adapter (q4_lora_gemm).
     workspace: a uint8 tensor of at least workspace_bytes, else one is
     allocated."""
-    M = _rows(x, "x", pairs.K)
+    xp, M = _rows(x, "x", pairs.K, pairs)
     rec = pairs._record(q, ids, M)
-    xp = _tensor(x, "x", pairs.dtype, x.shape, pairs._index)
     if out is None:
         out = x.new_empty((M, pairs.N))
     else:
@@ -145,10 +148,9 @@ def backward(dy, x, q, pairs, ids=None, *, need_dx=True, need_pairs=True, out=No
     """Gradients of gemm (q4_lora_backward): (dx [M, K], da, db), those not
     needed None (x may be None where the adapters' are not).  out: a tuple of
     three tensors to write, None where one is to be allocated."""
-    M = _rows(dy, "dy", pairs.N)
+    dyp, M = _rows(dy, "dy", pairs.N, pairs)
     rec = pairs._record(q, ids, M)
     index, dtype = pairs._index, pairs.dtype
-    dyp = _tensor(dy, "dy", dtype, dy.shape, index)
     xp = None
     if need_pairs or x is not None:
         xp = _tensor(x, "x", dtype, (M, pairs.K), index)
