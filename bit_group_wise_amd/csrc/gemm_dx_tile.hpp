@@ -175,7 +175,11 @@ struct DxTile {
     float *part = nullptr;     // where its sums go, [rows, K]
 };
 
-// The tile's LDS.
+// The tile's LDS, and with adapters the third part of u: a workgroup has a
+// compute unit to itself either way.
+#define Q4_DX_LORA_LDS(FMT)                                             \
+    Q4_DX_TILE_LDS(FMT);                                                \
+    __shared__ __attribute__((aligned(16))) char us[TM * kYRow]
 #define Q4_DX_TILE_LDS(FMT)                                             \
     __shared__ __attribute__((aligned(16))) char ys[2][TM * kYRow];     \
     __shared__ __attribute__((aligned(16))) char wt[2][TN * kWPitch];   \
@@ -187,7 +191,8 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
                                         const void *__restrict__ scales,
                                         const uint8_t *__restrict__ zeros, int N, int K, int gshift,
                                         uint16_t *__restrict__ dx, char (&ys)[2][kWholeRows * kYRow],
-                                        char (&wt)[2][TN * kWPitch], float2 *ptbl, const LowRank *low = nullptr)
+                                        char (&wt)[2][TN * kWPitch], float2 *ptbl, char *us = nullptr,
+                                        const LowRank *low = nullptr)
 {
     constexpr int TM = 64 * kWMF;  // this tile's rows
     const int t = threadIdx.x;
@@ -337,30 +342,34 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
     const int nsteps = KIND == kDxLoraPart ? tile.steps : (N + TN - 1) / TN;
     const int n0 = KIND == kDxLoraPart ? tile.step0 * TN : 0;
     DxLoads<kWMF> la, lb;
+    constexpr bool kAdapters = KIND == kDxLora || KIND == kDxLoraPart;
     dx_load<FMT, KIND>(la, c, n0, k0);
-    dx_load<FMT, KIND>(lb, c, n0 + TN, k0);
-    // The adapters' part, u A, as steps of the same form: 64 values r of u as
-    // the step's dY (its two parts in the two dY buffers) and the adapter's 64
-    // rows of A as its weight rows (for fp16 its two parts in the two weight
-    // buffers).
-    if (KIND == kDxLora || (KIND == kDxLoraPart && tile.step0 == 0)) {
+    if constexpr (!kAdapters)  // (beside them the registers hold one step's loads)
+        dx_load<FMT, KIND>(lb, c, n0 + TN, k0);
+    // The adapters' part, u A, as steps of the same form: 64 values r of u as the
+    // step's dY (its three parts in the two dY buffers and one of their own) and
+    // the adapter's 64 rows of A as its weight rows (for fp16 its two parts in the
+    // two weight buffers).
+    if constexpr (kAdapters) {
         constexpr int C = TM / 64;
         const int rows = M - m0 < TM ? M - m0 : TM;
         AdapterSet<C> all;
         all.init(low->ids, low->adapters, m0, rows);
-        // (rows past the tile's end lie past the views)
-        const __amdgpu_buffer_rsrc_t uhr = dx_rsrc(low->two + (int64_t)m0 * low->rank, (int64_t)rows * low->rank * 2);
-        const __amdgpu_buffer_rsrc_t ulr =
-            dx_rsrc(low->two + (low->rows + m0) * low->rank, (int64_t)rows * low->rank * 2);
-        for (int rc = 0; rc < low->rank; rc += 64) {
+        char *const parts[3] = {ys[0], ys[1], us};
+        // (rows past the tile's end lie past the view)
+        const __amdgpu_buffer_rsrc_t ur =
+            dx_rsrc(low->split + (int64_t)m0 * 3 * low->rank, (int64_t)rows * 3 * low->rank * 2);
+        const int rank = KIND == kDxLora || tile.step0 == 0 ? low->rank : 0;  // (of a later part: none)
+        for (int rc = 0; rc < rank; rc += 64) {
             // u's chunk t % 8 of rows t / 8 + 64 i, all loads before the first store
-            u32x4 uh[kWMF], ul[kWMF];
+            u32x4 u[3][kWMF];
 #pragma unroll
             for (int i = 0; i < kWMF; ++i) {
-                const uint32_t off = 2u * (uint32_t)(((t >> 3) + 64 * i) * low->rank + rc + 8 * (t & 7)) |
-                                     (rc + 8 * (t & 7) < low->rank ? 0u : 0x80000000u);
-                uh[i] = __builtin_amdgcn_raw_buffer_load_b128(uhr, (int)off, 0, 0);
-                ul[i] = __builtin_amdgcn_raw_buffer_load_b128(ulr, (int)off, 0, 0);
+                const uint32_t none = rc + 8 * (t & 7) < rank ? 0u : 0x80000000u;
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+                    u[p][i] = __builtin_amdgcn_raw_buffer_load_b128(
+                        ur, (int)(2u * (uint32_t)((3 * ((t >> 3) + 64 * i) + p) * rank + rc + 8 * (t & 7)) | none), 0, 0);
             }
             AdapterSet<C> set = all;
             int ad;
@@ -369,8 +378,8 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
             auto load = [&]() {  // the adapter's rows, the next one's while one is worked on
                 const int r = rc + (t >> 3), k = k0 + 16 * (t & 7);
                 v[0] = v[1] = u32x4{0, 0, 0, 0};
-                if (r < low->rank && k < K) {
-                    const u32x4 *w = (const u32x4 *)(low->w + ((int64_t)ad * low->rank + r) * K + k);
+                if (r < rank && k < K) {
+                    const u32x4 *w = (const u32x4 *)(low->w + ((int64_t)ad * rank + r) * K + k);
                     v[0] = w[0];
                     v[1] = w[1];
                 }
@@ -381,8 +390,9 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
 #pragma unroll
             for (int i = 0; i < kWMF; ++i) {
                 const int row = (t >> 3) + 64 * i, at = row * kYRow + 16 * yswz(row, t & 7);
-                *(u32x4 *)(ys[0] + at) = uh[i];
-                *(u32x4 *)(ys[1] + at) = ul[i];
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+                    *(u32x4 *)(parts[p] + at) = u[p][i];
             }
             while (on) {
 #pragma unroll
@@ -391,7 +401,7 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
                 __syncthreads();  // (the last adapter's rows have been read)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const Parts8 w = two_parts16<ACT>(v[e]);
+                    const Exact8 w = exact_parts<ACT>(v[e]);
                     *(u32x4 *)(wt[0] + wofs(t >> 3, 16 * (t & 7) + 8 * e)) = w.hi;
                     if constexpr (ACT == Q4_F16)
                         *(u32x4 *)(wt[1] + wofs(t >> 3, 16 * (t & 7) + 8 * e)) = w.lo;
@@ -402,20 +412,21 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
                 __syncthreads();
 #pragma unroll
                 for (int j = 0; j < kKF; ++j) {
-                    Parts8 fa[2];
+                    Exact8 fa[2] = {};
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
+                        if (rc + 32 * h >= rank)
+                            break;
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            const int nl = 32 * h + 8 * fq + 4 * u + (fi >> 2);
-                            const int kl = 64 * wk + 16 * j + 4 * (fi & 3);
+                            const int at = wofs(32 * h + 8 * fq + 4 * u + (fi >> 2), 64 * wk + 16 * j + 4 * (fi & 3));
                             const v4i16 p = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                (__attribute__((address_space(3))) v4i16 *)(wt[0] + wofs(nl, kl)));
+                                (__attribute__((address_space(3))) v4i16 *)(wt[0] + at));
                             fa[h].hi[2 * u] = (uint32_t)(uint16_t)p[0] | ((uint32_t)(uint16_t)p[1] << 16);
                             fa[h].hi[2 * u + 1] = (uint32_t)(uint16_t)p[2] | ((uint32_t)(uint16_t)p[3] << 16);
                             if constexpr (ACT == Q4_F16) {
                                 const v4i16 o = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                    (__attribute__((address_space(3))) v4i16 *)(wt[1] + wofs(nl, kl)));
+                                    (__attribute__((address_space(3))) v4i16 *)(wt[1] + at));
                                 fa[h].lo[2 * u] = (uint32_t)(uint16_t)o[0] | ((uint32_t)(uint16_t)o[1] << 16);
                                 fa[h].lo[2 * u + 1] = (uint32_t)(uint16_t)o[2] | ((uint32_t)(uint16_t)o[3] << 16);
                             }
@@ -427,9 +438,12 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
                         f32x4 p{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
+                            if (rc + 32 * h >= rank)
+                                break;
                             const int at = row * kYRow + 16 * yswz(row, 4 * h + fq);
-                            const Parts8 u{*(const u32x4 *)(ys[0] + at), *(const u32x4 *)(ys[1] + at)};
-                            p = mfma_parts_a<ACT>(fa[h], u, p);
+                            const Low8 l{{*(const u32x4 *)(parts[0] + at), *(const u32x4 *)(parts[1] + at),
+                                          *(const u32x4 *)(parts[2] + at)}};
+                            p = mfma_exact_low<ACT>(fa[h], l, p);
                         }
                         uint64_t of = mask[0];
 #pragma unroll
@@ -444,6 +458,7 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
             }
             __syncthreads();
         }
+        dx_load<FMT, KIND>(lb, c, n0 + TN, k0);
     }
 
     __syncthreads();  // the level-pair table

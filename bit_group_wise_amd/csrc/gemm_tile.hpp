@@ -382,11 +382,11 @@ struct Tile {
 };
 
 // The tile's accumulators as the adapters' part makes them, h B^T, with the
-// same operand roles, fragment positions and staging as a K step: 64 values r
-// of all x rows of h as the step's x, its two parts in the two x buffers, and
-// B [n][r] straight from memory as the weights, the next adapter's while one
-// is worked on.  (One step of 2 or 3 products against the K / 64 of the
-// product itself.)
+// same operand roles, fragment positions and staging as a K step: 32 values r
+// of all x rows of h as the step's x, the first two of its three parts side by
+// side in one x buffer and the third in the other, and B [n][r] straight from
+// memory as the weights, the next adapter's while one is worked on.  (3 or 5
+// products for 32 values r against the K / 32 of the product itself.)
 template <int ACT, int kMF>
 __device__ __forceinline__ void lora_start(f32x4 (&acc)[kNF][kMF], const LowRank &l, const TileCtx<kMF> &c, char *xs0,
                                            char *xs1, int m0, int mend, int wave, int fr, int nrow, int N)
@@ -396,32 +396,34 @@ __device__ __forceinline__ void lora_start(f32x4 (&acc)[kNF][kMF], const LowRank
     constexpr int C = (kMF + 3) / 4;
     AdapterSet<C> all;
     all.init(l.ids, l.adapters, m0, rows);
-    const View hv = make_view(l.two + (int64_t)m0 * l.rank, (int64_t)rows * l.rank * 2);
-    const View lv = make_view(l.two + (l.rows + m0) * l.rank, (int64_t)rows * l.rank * 2);
+    const View hv = make_view(l.split + (int64_t)m0 * 3 * l.rank, (int64_t)rows * 3 * l.rank * 2);
+    // the lane's reads of row fr: chunk fq of each part
+    int rd[3];
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+        rd[p] = fr * ROW_BYTES + 16 * swz(fr, c.fq + (p == 1 ? 4 : 0));
     // (uniform loops: the workgroup's waves all stage, meet and work together)
-    for (int rc = 0; rc < l.rank; rc += 64) {
+    for (int rc = 0; rc < l.rank; rc += 32) {
 #pragma unroll
         for (int i = 0; i < x_blocks(kMF); ++i) {
-            const int B = x_blocks(kMF) * wave + i, row = 8 * B + (lane >> 3), r = rc + c.xk[i & 1];
-            const uint32_t v = r < l.rank ? 2u * (uint32_t)(row * l.rank + r) : kNowhere;
-            load_lds16(hv, 0, xs0 + 1024 * B, v);
-            load_lds16(lv, 0, xs1 + 1024 * B, v);
+            const int B = x_blocks(kMF) * wave + i, row = 8 * B + (lane >> 3);
+            const int chunk = c.xk[i & 1] >> 3, r = rc + 8 * (chunk & 3);
+            const uint32_t v = 2u * (uint32_t)((3 * row + (chunk >> 2)) * l.rank + r);
+            load_lds16(hv, 0, xs0 + 1024 * B, r < l.rank ? v : kNowhere);
+            load_lds16(hv, (uint32_t)(4 * l.rank), xs1 + 1024 * B, r < l.rank && chunk < 4 ? v : kNowhere);
         }
         AdapterSet<C> set = all;
         int ad;
         uint64_t mask[C], next[C] = {};
-        u32x4 raw[kNF][2];
+        u32x4 raw[kNF];
         auto load = [&]() {
             const uint16_t *w = l.w + (int64_t)ad * N * l.rank;
 #pragma unroll
             for (int j = 0; j < kNF; ++j) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int n = nrow + 4 * j, r = rc + 16 * c.fq + 8 * h;
-                    raw[j][h] = u32x4{0, 0, 0, 0};
-                    if (n < N && r < l.rank)
-                        raw[j][h] = *(const u32x4 *)(w + (int64_t)n * l.rank + r);
-                }
+                const int n = nrow + 4 * j, r = rc + 8 * c.fq;
+                raw[j] = u32x4{0, 0, 0, 0};
+                if (n < N && r < l.rank)
+                    raw[j] = *(const u32x4 *)(w + (int64_t)n * l.rank + r);
             }
         };
         bool on = set.next(ad, next);
@@ -430,12 +432,10 @@ __device__ __forceinline__ void lora_start(f32x4 (&acc)[kNF][kMF], const LowRank
         __builtin_amdgcn_s_waitcnt(0x0f70);  // h is in LDS
         __syncthreads();
         while (on) {
-            Parts8 b[kNF][2];
+            Exact8 b[kNF];
 #pragma unroll
             for (int j = 0; j < kNF; ++j)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    b[j][h] = two_parts16<ACT>(raw[j][h]);
+                b[j] = exact_parts<ACT>(raw[j]);
 #pragma unroll
             for (int q = 0; q < C; ++q)
                 mask[q] = next[q];
@@ -447,22 +447,15 @@ __device__ __forceinline__ void lora_start(f32x4 (&acc)[kNF][kMF], const LowRank
                 if (((mask[i / 4] >> (16 * (i % 4))) & 0xffff) == 0)
                     continue;
                 const bool mine = (mask[i / 4] >> (16 * (i % 4) + fr)) & 1;
-                f32x4 t[kNF];
+                const Low8 h{{*(const u32x4 *)(xs0 + rd[0] + 2048 * i), *(const u32x4 *)(xs0 + rd[1] + 2048 * i),
+                              *(const u32x4 *)(xs1 + rd[2] + 2048 * i)}};
 #pragma unroll
-                for (int j = 0; j < kNF; ++j)
-                    t[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const Parts8 x{*(const u32x4 *)(xs0 + c.rd[h] + 2048 * i), *(const u32x4 *)(xs1 + c.rd[h] + 2048 * i)};
-#pragma unroll
-                    for (int j = 0; j < kNF; ++j)
-                        t[j] = mfma_parts_a<ACT>(b[j][h], x, t[j]);
-                }
-#pragma unroll
-                for (int j = 0; j < kNF; ++j)
+                for (int j = 0; j < kNF; ++j) {
+                    const f32x4 t = mfma_exact_low<ACT>(b[j], h, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        acc[j][i][v] = mine ? acc[j][i][v] + t[j][v] : acc[j][i][v];
+                        acc[j][i][v] = mine ? acc[j][i][v] + t[v] : acc[j][i][v];
+                }
             }
         }
         __syncthreads();

@@ -6,13 +6,13 @@
 // in the workspace; the product's own kernel then adds h B^T (or u A) to its
 // binary32 accumulators, so the sum is rounded once and y is written once.
 //
-// Operands: the matrix cores take 16 bits, so h and u enter as two bfloat16
-// numbers, the value's rounding and the rounding of what that left: 16 bits
-// and binary32's range (a relative 2^-17, 1/64 of the half step of an fp16
-// output, and nothing lost of a gradient below fp16's range).  What they meet
-// is bfloat16 as it is, or for fp16 activations also two bfloat16 numbers (11
-// bits = 8 + 3: exact); the product of the two second parts, a relative 2^-18,
-// is left out.
+// Operands: the matrix cores take 16 bits, so h and u enter as three bfloat16
+// numbers, each the first 8 bits of what the ones before it left: all 24 bits of
+// binary32 (and its range: nothing is lost of a gradient below fp16's).  What
+// they meet is bfloat16 as it is, or for fp16 activations two such numbers (11
+// bits = 8 + 3), of which the second and the third of h are not multiplied: below
+// 2^-21 of the product, 2^-24 in the mean.  (With two numbers, 16 bits, gradients
+// of long batches rounded the other way in one of 2000 bfloat16 values.)
 #pragma once
 
 #include "plan.hpp"
@@ -23,11 +23,11 @@ namespace q4 {
 
 // h[m][r] (or u) and what they go through.  For few rows h is left as binary32
 // partial sums, part[i * rows * rank + m * rank + r] for i < parts; else as its
-// operands' two parts, two[m * rank + r] and two[(rows + m) * rank + r].
+// operands, split[(3 m + i) * rank + r] for i < 3.
 struct LowRank {
     const float *part;
     int parts;
-    const uint16_t *two;
+    const uint16_t *split;
     int rank, adapters;
     int64_t rows;
     const int32_t *ids;  // adapter of each row, or NULL: all 0
@@ -54,57 +54,91 @@ __device__ __forceinline__ void unpack2(uint32_t w, float &a, float &b)
     }
 }
 
-// 8 binary32 values as bfloat16 operands: their roundings, and the roundings
-// of the rest.
-struct Parts8 {
-    u32x4 hi, lo;
-};
-__device__ __forceinline__ Parts8 two_parts(const float (&v)[8])
+// The first 8 bits of a binary32 value (a bfloat16 number).
+__device__ __forceinline__ float first8(float v)
 {
-    Parts8 p;
+    return std::bit_cast<float>(std::bit_cast<uint32_t>(v) & 0xffff0000u);
+}
+// Two values' first 8 bits as a pair of bfloat16 numbers.
+__device__ __forceinline__ uint32_t pack_first8(float a, float b)
+{
+    return __builtin_amdgcn_perm(std::bit_cast<uint32_t>(b), std::bit_cast<uint32_t>(a), 0x07060302u);
+}
+// A pair of binary32 values as three pairs of bfloat16 numbers.
+struct Split3 {
+    uint32_t p[3];
+};
+__device__ __forceinline__ Split3 split3(float a, float b)
+{
+    Split3 s;
+    s.p[0] = pack_first8(a, b);
+    a = a - first8(a);
+    b = b - first8(b);
+    s.p[1] = pack_first8(a, b);
+    s.p[2] = pack_first8(a - first8(a), b - first8(b));
+    return s;
+}
+
+// 8 values of h (or u) as operands.
+struct Low8 {
+    u32x4 p[3];
+};
+__device__ __forceinline__ Low8 three_parts(const float (&v)[8])
+{
+    Low8 l;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t h = pack_bf2(v[2 * i], v[2 * i + 1]);
-        p.hi[i] = h;
-        p.lo[i] = pack_bf2(v[2 * i] - std::bit_cast<float>(h << 16),
-                           v[2 * i + 1] - std::bit_cast<float>(h & 0xffff0000u));
+        const Split3 s = split3(v[2 * i], v[2 * i + 1]);
+        l.p[0][i] = s.p[0];
+        l.p[1][i] = s.p[1];
+        l.p[2][i] = s.p[2];
     }
-    return p;
+    return l;
 }
-// 8 activations (or adapter weights) as such operands: bfloat16 ones are their
-// own first part and have no second.
+// 8 activations (or adapter weights) as operands: bfloat16 ones are their own
+// first part and have no second.
+struct Exact8 {
+    u32x4 hi, lo;
+};
 template <int ACT>
-__device__ __forceinline__ Parts8 two_parts16(const u32x4 &w)
+__device__ __forceinline__ Exact8 exact_parts(const u32x4 &w)
 {
-    if constexpr (ACT == Q4_BF16) {
-        return Parts8{w, u32x4{0, 0, 0, 0}};
-    } else {
-        float v[8];
+    Exact8 e{w, u32x4{0, 0, 0, 0}};
+    if constexpr (ACT == Q4_F16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            unpack2<ACT>(w[i], v[2 * i], v[2 * i + 1]);
-        return two_parts(v);
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            unpack2<ACT>(w[i], a, b);
+            e.hi[i] = pack_first8(a, b);
+            e.lo[i] = pack_first8(a - first8(a), b - first8(b));
+        }
     }
+    return e;
 }
 
-// Products of such operands: `exact` has a second part for fp16 alone.
+// Products of such operands, small ones first.
 template <int ACT>
-__device__ __forceinline__ f32x4 mfma_parts_a(const Parts8 &exact, const Parts8 &b, f32x4 c)
+__device__ __forceinline__ f32x4 mfma_exact_low(const Exact8 &x, const Low8 &l, f32x4 c)
 {
-    c = mfma<Q4_BF16>(exact.hi, b.lo, c);
+    c = mfma<Q4_BF16>(x.hi, l.p[2], c);
     if constexpr (ACT == Q4_F16)
-        c = mfma<Q4_BF16>(exact.lo, b.hi, c);
-    return mfma<Q4_BF16>(exact.hi, b.hi, c);
+        c = mfma<Q4_BF16>(x.lo, l.p[1], c);
+    c = mfma<Q4_BF16>(x.hi, l.p[1], c);
+    if constexpr (ACT == Q4_F16)
+        c = mfma<Q4_BF16>(x.lo, l.p[0], c);
+    return mfma<Q4_BF16>(x.hi, l.p[0], c);
 }
 template <int ACT>
-__device__ __forceinline__ f32x4 mfma_parts_b(const Parts8 &a, const Parts8 &exact, f32x4 c)
+__device__ __forceinline__ f32x4 mfma_low_exact(const Low8 &l, const Exact8 &x, f32x4 c)
 {
-    c = mfma<Q4_BF16>(a.lo, exact.hi, c);
+    c = mfma<Q4_BF16>(l.p[2], x.hi, c);
     if constexpr (ACT == Q4_F16)
-        c = mfma<Q4_BF16>(a.hi, exact.lo, c);
-    return mfma<Q4_BF16>(a.hi, exact.hi, c);
+        c = mfma<Q4_BF16>(l.p[1], x.lo, c);
+    c = mfma<Q4_BF16>(l.p[1], x.hi, c);
+    if constexpr (ACT == Q4_F16)
+        c = mfma<Q4_BF16>(l.p[0], x.lo, c);
+    return mfma<Q4_BF16>(l.p[0], x.hi, c);
 }
-
 
 // The sum of h's partial sums at row m, r0 .. r0 + 7 (in order of the parts),
 // or zeros where not `there`; the parts by a view of them all.  All loads are

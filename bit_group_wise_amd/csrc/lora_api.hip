@@ -50,51 +50,6 @@ q4_status check_lora(q4_format f, int g, q4_dtype act_t, int64_t M, const void *
     return Q4_OK;
 }
 
-int64_t padded(int64_t floats) { return (4 * floats + 255) / 256 * 256; }
-
-// Whether a product of more than 96 rows runs in tiles of 64 (q4_lora_gemm).
-bool short_tiles(int64_t M, int64_t N) { return M > 96 && (M + 255) / 256 * ((N + 127) / 128) < 128; }
-
-// Parts of K for them: as many as give every compute unit a workgroup, of at
-// least 8 steps of 64.  Whole calls in us, whole / in parts: 237 rows of 147 x
-// 5888, rank 88, 60 / 26; 835 of 553 x 8064, rank 80, 85 / 45; 128 of 512 x 14336,
-// rank 16, 117 / 33; 128 of 4096 x 4096 42 / 28; 697 of 394 x 1472, rank 112, 29 /
-// 24; 512 of 4096 x 4096 46 / 44.
-int lora_parts(int64_t M, int64_t N, int64_t K)
-{
-    const int64_t tiles = (M + 63) / 64 * ((N + 127) / 128);
-    if (!short_tiles(M, N) || tiles >= 256)
-        return 1;
-    const int64_t parts = 256 / tiles, most = (K + 255) / 256 / 2;
-    return (int)(parts < most ? parts : (most > 1 ? most : 1));
-}
-
-// The workspace: h, then (backward) u, then sums that are joined: of the parts
-// of h and u, later of y or of dX and of the adapters' gradients.
-struct Layout {
-    DownPlan plan;
-    int splits, out_parts;
-    int64_t u, sums, bytes;
-};
-Layout layout(int64_t M, int64_t N, int64_t K, int adapters, int rank, int backward)
-{
-    Layout w{};
-    w.plan = down_plan(M, backward && N > K ? N : K, adapters, rank, backward);
-    // (two 16-bit parts are as long as one of 32)
-    const int64_t one = padded((int64_t)(w.plan.two ? 1 : w.plan.parts) * M * rank);
-    const int kinds = backward ? 2 : 1;
-    w.splits = backward ? grad_splits(M, N, K, adapters, rank) : 1;
-    w.u = one;
-    w.sums = kinds * one;
-    const int64_t joined = w.plan.two && w.plan.parts > 1 ? padded((int64_t)kinds * w.plan.parts * M * rank) : 0;
-    const int64_t grads = w.splits > 1 ? padded((int64_t)w.splits * adapters * rank * (N + K)) : 0;
-    w.out_parts = backward ? lora_dx_parts(M, N, K) : lora_parts(M, N, K);
-    const int64_t out = w.out_parts > 1 ? padded(w.out_parts * M * (backward ? K : (N + 3) / 4 * 4)) : 0;
-    const int64_t most = joined > grads ? joined : grads;
-    w.bytes = w.sums + (most > out ? most : out);
-    return w;
-}
-
 }  // namespace
 
 extern "C" {

@@ -19,7 +19,7 @@
 //    limit, and with 16 rows a workgroup half of it was the adapter's matrix
 //    (25 and 40 us on 2048 rows of 4096 with rank 32 and of 11008 with rank 16).
 //    The axis' parts are joined by a second launch, which also splits the sums
-//    into the two bfloat16 operands that their readers need.  (Readers that add
+//    into the three bfloat16 operands that their readers need.  (Readers that add
 //    up 8 parts spent 20 to 130 us on it, one latency after another.)
 #include "lora.hpp"
 #include "q4_internal.hpp"
@@ -36,14 +36,14 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t dn_rsrc(const void *base, int6
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n, 0x00020000);
 }
 
-// Four values as their two bfloat16 parts, at two[to] and two[size + to].
-__device__ __forceinline__ void store_two(uint16_t *two, int64_t size, int64_t to, const f32x4 &v)
+// Four values r of row m as their operands, at split[(3 m + i) * rank + r].
+__device__ __forceinline__ void store_split(uint16_t *split, int rank, int64_t m, int r, const f32x4 &v)
 {
-    const u32x2 hi{pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3])};
-    const u32x2 lo{pack_bf2(v[0] - std::bit_cast<float>(hi[0] << 16), v[1] - std::bit_cast<float>(hi[0] & 0xffff0000u)),
-                   pack_bf2(v[2] - std::bit_cast<float>(hi[1] << 16), v[3] - std::bit_cast<float>(hi[1] & 0xffff0000u))};
-    *(u32x2 *)(two + to) = hi;
-    *(u32x2 *)(two + size + to) = lo;
+    const Split3 a = split3(v[0], v[1]), b = split3(v[2], v[3]);
+    uint16_t *to = split + 3 * m * rank + r;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        *(u32x2 *)(to + i * rank) = u32x2{a.p[i], b.p[i]};
 }
 
 // ---------------------------------------------------------------- few rows
@@ -162,7 +162,7 @@ struct ManyStep {
 
 template <int ACT, int RF, bool TRANS>
 __device__ __forceinline__ void down_many(const DownArgs &a, const uint16_t *__restrict__ x,
-                                          const uint16_t *__restrict__ w, uint16_t *two, float *part, int len,
+                                          const uint16_t *__restrict__ w, uint16_t *split, float *part, int len,
                                           int slice, int slot, char (&xs)[2][kRows * 128], char (&ws)[2][RF * 2048])
 {
     constexpr int kW = RF > 2 ? 2 : 1;  // loads of the adapter a thread
@@ -284,11 +284,11 @@ __device__ __forceinline__ void down_many(const DownArgs &a, const uint16_t *__r
             if (!mine || r >= a.rank)
                 continue;
             const f32x4 v{acc[f][0] * s, acc[f][1] * s, acc[f][2] * s, acc[f][3] * s};
-            const int64_t to = (m0 + 16 * wave + fi) * a.rank + r;
+            const int64_t m = m0 + 16 * wave + fi;
             if (a.parts > 1)
-                *(f32x4 *)(part + blockIdx.y * a.rows * a.rank + to) = v;
+                *(f32x4 *)(part + (blockIdx.y * a.rows + m) * a.rank + r) = v;
             else
-                store_two(two, a.rows * a.rank, to, v);
+                store_split(split, a.rank, m, r, v);
         }
     }
 }
@@ -330,7 +330,8 @@ __global__ __launch_bounds__(256) void down_join_kernel(DownArgs a)
             v = f32x4{v[0] + u[0], v[1] + u[1], v[2] + u[2], v[3] + u[3]};
         }
     }
-    store_two((uint16_t *)(h ? a.h : a.u), size, at, v);
+    const int64_t m = at / a.rank;
+    store_split((uint16_t *)(h ? a.h : a.u), a.rank, m, (int)(at - m * a.rank), v);
 }
 
 template <int ACT>
@@ -338,7 +339,7 @@ hipError_t launch_dn(const DownArgs &a, const DownPlan &p, hipStream_t s)
 {
     const int kinds = (a.x ? 1 : 0) + (a.dy ? 1 : 0);
     const dim3 grid((unsigned)p.tiles, (unsigned)a.parts, (unsigned)(a.slices * a.slots * kinds));
-    if (!p.two) {
+    if (!p.split) {
         if (p.rf == 1)
             hipLaunchKernelGGL((down_few_kernel<ACT, 1>), grid, dim3(kFewBlock), 0, s, a);
         else if (p.rf == 2)

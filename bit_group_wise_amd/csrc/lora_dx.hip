@@ -15,9 +15,9 @@ __global__ __launch_bounds__(kBlock) void lora_dx_kernel(const uint16_t *__restr
                                                          const uint8_t *__restrict__ zeros, int N, int K, int gshift,
                                                          int mtiles, LowRank low, uint16_t *__restrict__ dx)
 {
-    Q4_DX_TILE_LDS(FMT);
+    Q4_DX_LORA_LDS(FMT);
     const DxTile tile{(int)(blockIdx.x % (unsigned)mtiles) * (64 * WMF), M, (int)(blockIdx.x / (unsigned)mtiles) * TK, 0, N};
-    dx_tile<FMT, ACT, kDxLora, WMF>(tile, dy, codes, scales, zeros, N, K, gshift, dx, ys, wt, ptbl, &low);
+    dx_tile<FMT, ACT, kDxLora, WMF>(tile, dy, codes, scales, zeros, N, K, gshift, dx, ys, wt, ptbl, us, &low);
 }
 
 template <int FMT, int ACT>
@@ -28,12 +28,12 @@ __global__ __launch_bounds__(kBlock) void lora_dx_part_kernel(const uint16_t *__
                                                               int gshift, int mtiles, LowRank low,
                                                               float *__restrict__ sums)
 {
-    Q4_DX_TILE_LDS(FMT);
+    Q4_DX_LORA_LDS(FMT);
     const int steps = (N + TN - 1) / TN, part = blockIdx.y, parts = gridDim.y;
     const int first = steps * part / parts, last = steps * (part + 1) / parts;
     const DxTile tile{(int)(blockIdx.x % (unsigned)mtiles) * 64, M, (int)(blockIdx.x / (unsigned)mtiles) * TK, 0, N,
                       first, last - first, sums + (int64_t)part * M * K};
-    dx_tile<FMT, ACT, kDxLoraPart, 1>(tile, dy, codes, scales, zeros, N, K, gshift, nullptr, ys, wt, ptbl, &low);
+    dx_tile<FMT, ACT, kDxLoraPart, 1>(tile, dy, codes, scales, zeros, N, K, gshift, nullptr, ys, wt, ptbl, us, &low);
 }
 
 template <int ACT>

@@ -6,9 +6,10 @@
 // workgroup of 4 waves takes 128 columns c, up to 64 values r and one part of
 // the rows, 64 rows a step:
 //  * the contraction runs over the rows, so both operands need 8 consecutive
-//    rows of one column: X's 64 x 128 tile and P's (its two bfloat16 parts side
-//    by side) lie in LDS row by row and come back transposed
-//    (ds_read_b64_tr_b16; layout and bank spread as in gemm_dx_tile.hpp);
+//    rows of one column: X's 64 x 128 tile and P's (its three bfloat16 parts side
+//    by side; of 64 values r the third in a tile of its own) lie in LDS row by
+//    row and come back transposed (ds_read_b64_tr_b16; layout and bank spread as
+//    in gemm_dx_tile.hpp);
 //  * rows of other adapters enter both tiles as zeros, and steps without a row
 //    of this adapter are left out: the rows' adapters are looked through first,
 //    256 steps at a time;
@@ -56,8 +57,8 @@ __device__ __forceinline__ u32x4 column8(const char *tile, int h, int c0)
     return v;
 }
 
-// One kind of gradient: X [rows, cols], P's partial sums, and the output [ad,
-// rank, cols] (dA) or [ad, cols, rank] (dB).
+// One kind of gradient: X [rows, cols], P's parts [rows, 3, rank], and the
+// output [ad, rank, cols] (dA) or [ad, cols, rank] (dB).
 struct Side {
     const uint16_t *x;
     const uint16_t *p;
@@ -67,19 +68,29 @@ struct Side {
 };
 
 // A thread's loads of a step: X's 16-byte chunks t % 16 of rows t / 16 + 16 i,
-// and of P's two parts 16-byte chunks one after another.
+// and of each of P's parts 16-byte chunks one after another.
 template <int RF>
 struct GradStep {
     u32x4 x[4];
-    u32x4 hi[RF > 2 ? 2 : 1], lo[RF > 2 ? 2 : 1];
+    u32x4 p[3][RF > 2 ? 2 : 1];
 };
 
-// The LDS of a workgroup: two steps' tiles, and the steps listed.
-template <int ACT>
+// Buffers of P: two, but one of 64 values r beside bfloat16, so that two
+// workgroups still share a compute unit's LDS (67 KB each; the backward pass of
+// 4096 rows through 4096 x 4096, rank 64: 206 us, with two and one workgroup a
+// unit 212; rank 128: 234 and 241).
+template <int ACT, int RF>
+constexpr int kPBufs = RF > 2 && ACT == Q4_BF16 ? 1 : 2;
+
+// The LDS of a workgroup: two steps' tiles, and the steps listed.  P's part i of
+// value r lies in column PW i + r of its row; of 64 values the third, which has
+// no room there, in column 64 (row / 32) + r of row % 32 of a tile of its own.
+template <int ACT, int RF>
 struct GradLds {
     char x[2][kGrRows * kGrPitch];
     char xlo[ACT == Q4_F16 ? 2 : 1][ACT == Q4_F16 ? kGrRows * kGrPitch : 16];
-    char p[2][kGrRows * kGrPitch];
+    char p[kPBufs<ACT, RF>][kGrRows * kGrPitch];
+    char p2[RF > 2 ? kPBufs<ACT, RF> : 1][RF > 2 ? kGrRows / 2 * kGrPitch : 16];
     uint64_t mask[kGrList];  // rows of the adapter in the step
     uint16_t list[kGrList];
     int count;
@@ -87,8 +98,10 @@ struct GradLds {
 
 template <int ACT, int RF, bool IS_B>
 __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cblock, int slice, int ad, int split,
-                                     GradLds<ACT> &lds)
+                                     GradLds<ACT, RF> &lds)
 {
+    constexpr int PW = RF > 2 ? 64 : 32;        // columns a part
+    constexpr bool kOneP = kPBufs<ACT, RF> == 1;
     constexpr int kPPieces = kGrRows * 2 * RF;  // 8-value pieces of P's tile
     constexpr int kPLoads = RF > 2 ? 2 : 1;     // ... a thread
     static_assert(kPPieces <= kPLoads * kGrBlock, "pieces of P");
@@ -146,8 +159,7 @@ __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cb
             const int64_t m0 = (base + s) * kGrRows;
             const int rows = (int)(a.rows - m0 < kGrRows ? a.rows - m0 : kGrRows);
             const __amdgpu_buffer_rsrc_t xr = gr_rsrc(side.x + m0 * side.cols, (int64_t)rows * side.cols * 2);
-            const __amdgpu_buffer_rsrc_t hr = gr_rsrc(side.p + m0 * a.rank, (int64_t)rows * a.rank * 2);
-            const __amdgpu_buffer_rsrc_t lr = gr_rsrc(side.p + (a.rows + m0) * a.rank, (int64_t)rows * a.rank * 2);
+            const __amdgpu_buffer_rsrc_t pr = gr_rsrc(side.p + 3 * m0 * a.rank, (int64_t)rows * 3 * a.rank * 2);
             const int c = c0 + 8 * (t & 15);
             const uint32_t cpast = c < side.cols ? 0u : kPast;
 #pragma unroll
@@ -161,34 +173,41 @@ __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cb
             for (int q = 0; q < kPLoads; ++q) {
                 const int p = t + kGrBlock * q, row = (p / (2 * RF)) & 63, r = r0 + 8 * (p % (2 * RF));
                 const uint32_t none = ((mask >> row) & 1) && p < kPPieces && r < a.rank ? 0u : kPast;
-                const int off = (int)(2u * (uint32_t)(row * a.rank + r) | none);
-                st.hi[q] = __builtin_amdgcn_raw_buffer_load_b128(hr, off, 0, 0);
-                st.lo[q] = __builtin_amdgcn_raw_buffer_load_b128(lr, off, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    st.p[i][q] = __builtin_amdgcn_raw_buffer_load_b128(
+                        pr, (int)(2u * (uint32_t)((3 * row + i) * a.rank + r) | none), 0, 0);
             }
         };
-        auto store = [&](const GradStep<RF> &st, int buf) {
+        auto store_x = [&](const GradStep<RF> &st, int buf) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const Parts8 w = two_parts16<ACT>(st.x[q]);
+                const Exact8 w = exact_parts<ACT>(st.x[q]);
                 const int at = gofs((t >> 4) + 16 * q, 8 * (t & 15));
                 *(u32x4 *)(lds.x[buf] + at) = w.hi;
                 if constexpr (ACT == Q4_F16)
                     *(u32x4 *)(lds.xlo[buf] + at) = w.lo;
             }
+        };
+        auto store_p = [&](const GradStep<RF> &st, int buf) {
 #pragma unroll
             for (int q = 0; q < kPLoads; ++q) {
                 const int p = t + kGrBlock * q;
                 if (p < kPPieces) {
                     const int row = p / (2 * RF), r = 8 * (p % (2 * RF));
-                    *(u32x4 *)(lds.p[buf] + gofs(row, r)) = st.hi[q];
-                    *(u32x4 *)(lds.p[buf] + gofs(row, 64 + r)) = st.lo[q];
+                    *(u32x4 *)(lds.p[buf] + gofs(row, r)) = st.p[0][q];
+                    *(u32x4 *)(lds.p[buf] + gofs(row, PW + r)) = st.p[1][q];
+                    if constexpr (RF > 2)
+                        *(u32x4 *)(lds.p2[buf] + gofs(row & 31, 64 * (row >> 5) + r)) = st.p[2][q];
+                    else
+                        *(u32x4 *)(lds.p[buf] + gofs(row, 2 * PW + r)) = st.p[2][q];
                 }
             }
         };
-        auto work = [&](int buf) {
+        auto work = [&](int buf, int pbuf) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                Parts8 x[2];
+                Exact8 x[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     x[j].hi = column8(lds.x[buf], h, 32 * wave + 16 * j);
@@ -197,15 +216,17 @@ __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cb
                 }
 #pragma unroll
                 for (int f = 0; f < RF; ++f) {
-                    const Parts8 p{column8(lds.p[buf], h, 16 * f), column8(lds.p[buf], h, 64 + 16 * f)};
+                    const Low8 p{{column8(lds.p[pbuf], h, 16 * f), column8(lds.p[pbuf], h, PW + 16 * f),
+                                  RF > 2 ? column8(lds.p2[pbuf], 0, 64 * h + 16 * f)
+                                         : column8(lds.p[pbuf], h, 2 * PW + 16 * f)}};
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        acc[f][j] = IS_B ? mfma_parts_b<ACT>(p, x[j], acc[f][j]) : mfma_parts_a<ACT>(x[j], p, acc[f][j]);
+                        acc[f][j] = IS_B ? mfma_low_exact<ACT>(p, x[j], acc[f][j]) : mfma_exact_low<ACT>(x[j], p, acc[f][j]);
                 }
             }
         };
         // steps in flight in registers, the current one in one of two LDS
-        // buffers: one barrier a step
+        // buffers: one barrier a step, a second where P has one buffer
         GradStep<RF> ring[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
@@ -215,10 +236,13 @@ __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cb
             for (int i = 0; i < 2 * kAhead; ++i) {
                 if (i0 + i >= found)
                     break;
-                store(ring[i % kAhead], i & 1);
+                store_x(ring[i % kAhead], i & 1);
+                if constexpr (kOneP)
+                    __syncthreads();  // (the last step's P has been read)
+                store_p(ring[i % kAhead], kOneP ? 0 : i & 1);
                 load(ring[i % kAhead], i0 + i + kAhead);
                 __syncthreads();
-                work(i & 1);
+                work(i & 1, kOneP ? 0 : i & 1);
             }
         }
     }
@@ -246,7 +270,7 @@ __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cb
 template <int ACT, int RF>
 __global__ __launch_bounds__(kGrBlock, 2) void grad_kernel(GradArgs a, int slices)
 {
-    __shared__ __attribute__((aligned(16))) GradLds<ACT> lds;
+    __shared__ __attribute__((aligned(16))) GradLds<ACT, RF> lds;
     const int kblocks = (a.K + kGrCols - 1) / kGrCols;
     const int slice = blockIdx.y % slices, ad = blockIdx.y / slices;
     const int64_t asize = (int64_t)a.adapters * a.rank * a.K;

@@ -58,9 +58,9 @@ constexpr int kMostParts = 8;
 
 // How h and u are formed: a tile of rows, 16 rf values r and one of `parts`
 // parts of the long axis a workgroup, the adapters of a tile over `slots`
-// workgroups.  two: left as two 16-bit parts, the parts of the axis joined.
+// workgroups.  split: left as three 16-bit parts, the parts of the axis joined.
 struct DownPlan {
-    bool two;
+    bool split;
     int rf, slices, slots, parts;
     int64_t tiles;
 };
@@ -69,10 +69,10 @@ constexpr int kDownRows = 64, kDownStep = 64;
 inline DownPlan down_plan(int64_t rows, int64_t longest, int adapters, int rank, int backward)
 {
     DownPlan p;
-    p.two = backward || rows > 96;  // (96: as far as the skinny product goes)
+    p.split = backward || rows > 96;  // (96: as far as the skinny product goes)
     p.rf = rank <= 16 ? 1 : (rank <= 32 ? 2 : 4);
     p.slices = (rank + 16 * p.rf - 1) / (16 * p.rf);
-    const int tile = p.two ? kDownRows : 16;
+    const int tile = p.split ? kDownRows : 16;
     p.tiles = (rows + tile - 1) / tile;
     // few rows: their adapters side by side
     const int64_t most = adapters < rows ? adapters : rows;
@@ -83,8 +83,8 @@ inline DownPlan down_plan(int64_t rows, int64_t longest, int adapters, int rank,
     // workgroups, of at least 16 (few rows) or 8 steps each; with up to 16
     // steps of 64 the join's launch would cost more than it saves
     const int64_t blocks = p.tiles * p.slices * p.slots * (backward ? 2 : 1);
-    const int64_t steps = p.two ? (longest + kDownStep - 1) / kDownStep : (longest + 31) / 32;
-    const int64_t most_parts = p.two ? (steps <= 16 ? 1 : steps / 8) : steps / 16;
+    const int64_t steps = p.split ? (longest + kDownStep - 1) / kDownStep : (longest + 31) / 32;
+    const int64_t most_parts = p.split ? (steps <= 16 ? 1 : steps / 8) : steps / 16;
     int64_t parts = 512 / (blocks ? blocks : 1);
     parts = parts < most_parts ? parts : most_parts;
     p.parts = (int)(parts < 1 ? 1 : (parts > kMostParts ? kMostParts : parts));
@@ -176,13 +176,13 @@ inline LoraLayout lora_layout(int64_t M, int64_t N, int64_t K, int adapters, int
 {
     LoraLayout w{};
     w.plan = down_plan(M, backward && N > K ? N : K, adapters, rank, backward);
-    // (two 16-bit parts are as long as one of 32)
-    const int64_t one = padded((int64_t)(w.plan.two ? 1 : w.plan.parts) * M * rank);
+    // (three 16-bit parts are as long as one and a half of 32; rank is even)
+    const int64_t one = padded(w.plan.split ? M * rank / 2 * 3 : w.plan.parts * M * rank);
     const int kinds = backward ? 2 : 1;
     w.splits = backward ? grad_splits(M, N, K, adapters, rank) : 1;
     w.u = one;
     w.sums = kinds * one;
-    const int64_t joined = w.plan.two && w.plan.parts > 1 ? padded((int64_t)kinds * w.plan.parts * M * rank) : 0;
+    const int64_t joined = w.plan.split && w.plan.parts > 1 ? padded((int64_t)kinds * w.plan.parts * M * rank) : 0;
     const int64_t grads = w.splits > 1 ? padded((int64_t)w.splits * adapters * rank * (N + K)) : 0;
     w.out_parts = backward ? lora_dx_parts(M, N, K) : lora_parts(M, N, K);
     const int64_t out = w.out_parts > 1 ? padded(w.out_parts * M * (backward ? K : (N + 3) / 4 * 4)) : 0;

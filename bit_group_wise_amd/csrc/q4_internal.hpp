@@ -93,8 +93,8 @@ hipError_t launch_experts_dx(q4_format f, int g, q4_dtype act_t, const ExpertsAr
 
 // Low-rank adapters beside a weight: h[m] = scale x[m] A^T and u[m] = scale
 // dy[m] B of each row's adapter (x or dy NULL: h or u is not formed), as the
-// plan says in binary32 partial sums [parts, rows, rank] or as two bfloat16
-// parts [2, rows, rank] (LowRank in lora.hpp).
+// plan says in binary32 partial sums [parts, rows, rank] or as three bfloat16
+// parts [rows, 3, rank] (LowRank in lora.hpp).
 struct DownArgs {
     const void *x, *dy, *a, *b;
     const float *scale;
@@ -139,7 +139,7 @@ hipError_t launch_lora_dx(q4_format f, int g, q4_dtype act_t, const LoraArgs &a,
 struct GradArgs {
     const void *x, *dy;
     const int32_t *ids;
-    const uint16_t *h, *u;  // two parts each
+    const uint16_t *h, *u;  // three parts each
     float *sums;
     int64_t rows;
     int N, K, adapters, rank, splits;

@@ -235,12 +235,12 @@ __device__ __forceinline__ void skinny_product(const SkTask &task, const uint16_
 #pragma unroll
                 for (int i = 1; i < kAhead; ++i)
                     next(slots[i]);
-                Parts8 h[MT];  // of all rows, whatever their adapters
+                Low8 h[MT];  // of all rows, whatever their adapters
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     float v[8];
                     sum_parts(parts, *low, 16 * mt + r, r0, 16 * mt + r < M && r0 < low->rank, v);
-                    h[mt] = two_parts(v);
+                    h[mt] = three_parts(v);
                 }
                 while (slots[0].on) {
 #pragma unroll
@@ -248,12 +248,12 @@ __device__ __forceinline__ void skinny_product(const SkTask &task, const uint16_
                         if (slots[i].on) {
 #pragma unroll
                             for (int b = 0; b < RB; ++b) {
-                                const Parts8 w = two_parts16<ACT>(slots[i].b[b]);
+                                const Exact8 w = exact_parts<ACT>(slots[i].b[b]);
 #pragma unroll
                                 for (int mt = 0; mt < MT; ++mt) {
                                     if (((slots[i].mask >> (16 * mt)) & 0xffff) == 0)
                                         continue;
-                                    const f32x4 t = mfma_parts_a<ACT>(w, h[mt], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+                                    const f32x4 t = mfma_exact_low<ACT>(w, h[mt], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
                                     const bool mine = (slots[i].mask >> (16 * mt + r)) & 1;
 #pragma unroll
                                     for (int e = 0; e < 4; ++e)

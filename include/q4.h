@@ -309,7 +309,8 @@ q4_status q4_experts_gemm_dx(q4_format f, int g, q4_dtype act_t, const void *dy,
  *   u = scale dy b,    dx = dy What + u a,
  *   da = sum of u^T x and db = sum of dy^T h over the adapter's rows
  * What as in q4_gemm.  Sums are binary32, h and u enter their second products
- * with 16 bits (a relative 2^-17), and each output is rounded once to act_t.
+ * with all their 24 bits (of fp16 operands a relative 2^-21 of a product is
+ * left out), and each output is rounded once to act_t.
  * Results do not depend on timing (no floating-point atomics).
  * rank is a multiple of 8 up to Q4_LORA_MAX_RANK; N rank and K rank below
  * 2^30, and M N and M K below 2^44 (else Q4_EUNSUPPORTED).  M = 0 is no work

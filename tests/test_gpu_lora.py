@@ -565,3 +565,81 @@ def test_kernels_captured_and_replayed():
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(out, check(x, q, pairs, ids, name))
+
+
+def whole(gen, act, lo, hi, *shape):
+    return torch.randint(lo, hi + 1, shape, generator=gen, device=DEV).to(ACTS[act])
+
+
+def nearly_twice(t, dim):
+    """Every second slice of t along dim made the one before it, but for two of its values that are one larger."""
+    t = t.movedim(dim, 0).clone()
+    for odd in range(1, t.shape[0], 2):
+        t[odd] = t[odd - 1]
+        flat = t[odd].reshape(-1, t.shape[-1])
+        flat[:, (5 * odd) % t.shape[-1]] += 1
+        flat[:, (7 * odd + 3) % t.shape[-1]] += 1
+    return t.movedim(0, dim).contiguous()
+
+
+def differences(act, rows, columns):
+    """[rows, columns] (rows even) with 1 in an even row and -1 in the next, a pair of rows for each column."""
+    t = torch.zeros((rows, columns), dtype=ACTS[act], device=DEV)
+    c = torch.arange(columns, device=DEV)
+    even = 2 * (c % (rows // 2))
+    t[even, c], t[even + 1, c] = 1, -1
+    return t
+
+
+def largest(n):
+    """Of the whole numbers in a sum of n: its terms' mean makes sums of 2^18 to 2^20."""
+    return max(4, min(62, 6000 // n))
+
+
+@pytest.mark.parametrize("rank", [8, 24, 40, 136])
+@pytest.mark.parametrize("name", ["skinny", "skinny-two", "skinny-four", "tile64", "tile64-parts", "tile128", "tile256"])
+def test_every_bit_of_the_low_product(name, rank):
+    """Whole numbers, exact in binary32: h of 2^18 and more, whose small differences y has to hold exactly."""
+    _, M, N, K, g = LORA[name]
+    gen = generator(M + rank)
+    for act in (q4.F16, q4.BF16):
+        q = q4.quantize(torch.zeros((N, K), dtype=torch.float16, device=DEV), q4.INT4_SYM, g)
+        x = whole(gen, act, 1, largest(K), M, K)
+        a = nearly_twice(whole(gen, act, 64, 126, 1, rank, K), 1)
+        b = differences(act, rank, N).t().contiguous()[None]
+        h = x.double() @ a[0].double().T
+        assert float(h.abs().max()) > 2 ** 18 and float(h.abs().max()) < 2 ** 24
+        y = lora.gemm(x, q, lora.Adapters(a, b))
+        assert torch.equal(y.double(), h @ b[0].double().T) and bool((y != 0).any())
+
+
+@pytest.mark.parametrize("rank", [8, 24, 40, 136])
+@pytest.mark.parametrize("name", list(LORA_DX))
+def test_every_bit_of_the_low_products_gradients(name, rank):
+    """The same for u in dx (whose A takes differences of values r), and for h and u in db and da (whose dy and x take
+    differences of rows)."""
+    _, _, M, N, K, g = LORA_DX[name]
+    M -= M % 2
+    gen = generator(M + rank)
+    for act in (q4.F16, q4.BF16):
+        q = q4.quantize(torch.zeros((N, K), dtype=torch.float16, device=DEV), q4.INT4_SYM, g)
+        b = nearly_twice(whole(gen, act, 64, 126, 1, N, rank), 2)
+        pairs = lora.Adapters(differences(act, rank, K)[None].contiguous(), b)
+        dy = whole(gen, act, 1, largest(N), M, N)
+        u = dy.double() @ b[0].double()
+        assert float(u.abs().max()) > 2 ** 17 and float(u.abs().max()) < 2 ** 24
+        dx, _, _ = lora.backward(dy, None, q, pairs, need_pairs=False)
+        assert torch.equal(dx.double(), u @ pairs.a[0].double()) and bool((dx != 0).any())
+
+        dy, x = nearly_twice(dy, 0), differences(act, M, K)
+        u = dy.double() @ b[0].double()
+        _, da, _ = lora.backward(dy, x, q, pairs, need_dx=False)
+        want = u.T @ x.double()
+        assert float(want.abs().max()) <= 256 and torch.equal(da[0].double(), want) and bool((da != 0).any())
+
+        x, dy = nearly_twice(whole(gen, act, 1, largest(K), M, K), 0), differences(act, M, N)
+        a = whole(gen, act, 64, 126, 1, rank, K)
+        h = x.double() @ a[0].double().T
+        _, _, db = lora.backward(dy, x, q, lora.Adapters(a, b), need_dx=False)
+        want = dy.double().T @ h
+        assert float(want.abs().max()) <= 256 and torch.equal(db[0].double(), want) and bool((db != 0).any())
