@@ -11,8 +11,9 @@
 // binary32 (and its range: nothing is lost of a gradient below fp16's).  What
 // they meet is bfloat16 as it is, or for fp16 activations two such numbers (11
 // bits = 8 + 3), of which the second and the third of h are not multiplied: below
-// 2^-21 of the product, 2^-24 in the mean.  (With two numbers, 16 bits, gradients
-// of long batches rounded the other way in one of 2000 bfloat16 values.)
+// 2^-21 of the product, 2^-24 in the mean.  (With two numbers, 16 bits, one in 400
+// bfloat16 gradients of a long batch rounded otherwise than its exact value; now
+// one in 2700, of the plain binary32 form one in 1200.)
 #pragma once
 
 #include "plan.hpp"
@@ -59,6 +60,11 @@ __device__ __forceinline__ float first8(float v)
 {
     return std::bit_cast<float>(std::bit_cast<uint32_t>(v) & 0xffff0000u);
 }
+// What they leave of a number (nothing of an infinite one).
+__device__ __forceinline__ float rest8(float v)
+{
+    return __builtin_fabsf(v) < __builtin_inff() ? v - first8(v) : 0.0f;
+}
 // Two values' first 8 bits as a pair of bfloat16 numbers.
 __device__ __forceinline__ uint32_t pack_first8(float a, float b)
 {
@@ -68,14 +74,30 @@ __device__ __forceinline__ uint32_t pack_first8(float a, float b)
 struct Split3 {
     uint32_t p[3];
 };
+// One value's parts, in their upper halves.  Their sum is the value exactly, and
+// each has its sign and is zero only if it is (a part that would leave nothing
+// is the number below, by 8 bits): beside an infinite operand every product is
+// infinite of one sign.  An infinite (or NaN) value is in the last part, which
+// alone meets nothing but operands' first parts, beside ones.
+__device__ __forceinline__ void split3(float v, uint32_t (&p)[3])
+{
+    const bool number = __builtin_fabsf(v) < __builtin_inff();
+    const float n = number ? v : __builtin_copysignf(1.0f, v);
+    const uint32_t below = n != 0.0f ? 1u : 0u;
+    p[0] = (std::bit_cast<uint32_t>(n) - below) & 0xffff0000u;
+    const float r = n - std::bit_cast<float>(p[0]);
+    p[1] = (std::bit_cast<uint32_t>(r) - below) & 0xffff0000u;
+    p[2] = std::bit_cast<uint32_t>(number ? r - std::bit_cast<float>(p[1]) : v);
+}
 __device__ __forceinline__ Split3 split3(float a, float b)
 {
+    uint32_t pa[3], pb[3];
+    split3(a, pa);
+    split3(b, pb);
     Split3 s;
-    s.p[0] = pack_first8(a, b);
-    a = a - first8(a);
-    b = b - first8(b);
-    s.p[1] = pack_first8(a, b);
-    s.p[2] = pack_first8(a - first8(a), b - first8(b));
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        s.p[i] = __builtin_amdgcn_perm(pb[i], pa[i], 0x07060302u);
     return s;
 }
 
@@ -110,7 +132,7 @@ __device__ __forceinline__ Exact8 exact_parts(const u32x4 &w)
             float a, b;
             unpack2<ACT>(w[i], a, b);
             e.hi[i] = pack_first8(a, b);
-            e.lo[i] = pack_first8(a - first8(a), b - first8(b));
+            e.lo[i] = pack_first8(rest8(a), rest8(b));
         }
     }
     return e;

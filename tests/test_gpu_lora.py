@@ -643,3 +643,62 @@ def test_every_bit_of_the_low_products_gradients(name, rank):
         _, _, db = lora.backward(dy, x, q, lora.Adapters(a, b), need_dx=False)
         want = dy.double().T @ h
         assert float(want.abs().max()) <= 256 and torch.equal(db[0].double(), want) and bool((db != 0).any())
+
+
+def assert_same_kind(got, want, tag):
+    """NaN where the formula is, infinities of its sign, numbers elsewhere."""
+    got = got.double()
+    for kind in (torch.isnan, torch.isposinf, torch.isneginf):
+        assert torch.equal(kind(got), kind(want)), f"{tag} {kind.__name__}"
+
+
+@pytest.mark.parametrize("rank", [8, 72])
+@pytest.mark.parametrize("name", ["skinny", "skinny-two", "skinny-four", "tile64", "tile64-parts", "tile128", "tile256"])
+def test_infinities_of_adapters(name, rank):
+    """An infinite value of A or B: infinities and NaN as the formula has them, beside values that 8 bits hold and others."""
+    _, M, N, K, g = LORA[name]
+    gen = generator(M + rank)
+    for act in (q4.F16, q4.BF16):
+        q = weight(N, K, q4.NF4, g, gen)
+        x = normal(gen, act, M, K)
+        x[::2] = whole(gen, act, -3, 3, (M + 1) // 2, K)
+        a, b = whole(gen, act, -2, 2, 3, rank, K), normal(gen, act, 3, N, rank)
+        a[2], b[1] = normal(gen, act, rank, K), whole(gen, act, -2, 2, N, rank)
+        a[0, 5, 7], a[1, rank - 1, 3] = float("inf"), -float("inf")
+        b[1, N // 2, 2], b[2, N - 1, 6], b[2, 0, 1] = float("inf"), -float("inf"), float("inf")
+        ids = ids_of(gen, M, 3, "mixed")
+        ids[:4] = torch.tensor([0, 1, 2, 0], device=DEV)
+        y = lora.gemm(x, q, lora.Adapters(a, b), ids)
+        want = x.double() @ values(q, act).T
+        for i in range(3):
+            at = (ids == i).nonzero()[:, 0]
+            want[at] += (x[at].double() @ a[i].double().T) @ b[i].double().T
+        assert bool(torch.isinf(want).any())
+        assert_same_kind(y, want, name)
+
+
+@pytest.mark.parametrize("rank", [8, 24, 72])
+@pytest.mark.parametrize("name", list(LORA_DX))
+def test_infinities_of_adapters_in_gradients(name, rank):
+    _, _, M, N, K, g = LORA_DX[name]
+    gen = generator(M + rank)
+    inf = float("inf")
+    for act in (q4.F16, q4.BF16):
+        q = weight(N, K, q4.NF4, g, gen)
+        x, dy = normal(gen, act, M, K), normal(gen, act, M, N)
+        x[::2], dy[::3] = whole(gen, act, -3, 3, (M + 1) // 2, K), whole(gen, act, -3, 3, (M + 2) // 3, N)
+        a, b = whole(gen, act, -2, 2, 3, rank, K), normal(gen, act, 3, N, rank)
+        a[2], b[1] = normal(gen, act, rank, K), whole(gen, act, -2, 2, N, rank)
+        a[0, 5, 7], b[1, N // 2, 2], b[2, 3, 6] = inf, -inf, inf
+        ids = torch.full((M,), -1, dtype=torch.int32, device=DEV)
+        ids[M // 2], ids[M // 3], ids[M - 1], ids[1] = 0, 1, 2, 2
+        dx, da, db = lora.backward(dy, x, q, lora.Adapters(a, b), ids)
+        want = dy.double() @ values(q, act)
+        for i in range(3):
+            at = (ids == i).nonzero()[:, 0]
+            u, h = dy[at].double() @ b[i].double(), x[at].double() @ a[i].double().T
+            want[at] += u @ a[i].double()
+            assert_same_kind(da[i], u.T @ x[at].double(), f"{name} da {i}")
+            assert_same_kind(db[i], dy[at].double().T @ h, f"{name} db {i}")
+        assert bool(torch.isinf(want).any()) and not bool(torch.isfinite(db[0]).all() or torch.isfinite(da[2]).all())
+        assert_same_kind(dx, want, f"{name} dx")
