@@ -75,22 +75,28 @@ struct GradStep {
     u32x4 p[3][RF > 2 ? 2 : 1];
 };
 
-// Buffers of P: two, but one of 64 values r beside bfloat16, so that two
-// workgroups still share a compute unit's LDS (67 KB each; the backward pass of
-// 4096 rows through 4096 x 4096, rank 64: 206 us, with two and one workgroup a
-// unit 212; rank 128: 234 and 241).
+// Buffers of P, and of X with its parts: two, but of 64 values r one of P, and
+// beside fp16 one of X, so that two workgroups still share a compute unit's LDS
+// (67 KB each).  The backward pass of 4096 rows through 4096 x 4096 in us, two
+// buffers and a workgroup a unit / this: rank 64 bfloat16 212 / 206, fp16 236 /
+// 224; rank 128 241 / 234, 284 / 261.  (One of each for 16 or 32 values r of fp16:
+// 283.6 / 284.5 on 2048 rows of 4096 x 11008, rank 16; 67.7 / 68.2 on 300 of 4096 x
+// 4096, rank 32.)
+template <int RF>
+constexpr int kPBufs = RF > 2 ? 1 : 2;
 template <int ACT, int RF>
-constexpr int kPBufs = RF > 2 && ACT == Q4_BF16 ? 1 : 2;
+constexpr int kXBufs = RF > 2 && ACT == Q4_F16 ? 1 : 2;
 
-// The LDS of a workgroup: two steps' tiles, and the steps listed.  P's part i of
-// value r lies in column PW i + r of its row; of 64 values the third, which has
-// no room there, in column 64 (row / 32) + r of row % 32 of a tile of its own.
+// The LDS of a workgroup: one or two steps' tiles, and the steps listed.  P's
+// part i of value r lies in column PW i + r of its row; of 64 values the third,
+// which has no room there, in column 64 (row / 32) + r of row % 32 of a tile of
+// its own.
 template <int ACT, int RF>
 struct GradLds {
-    char x[2][kGrRows * kGrPitch];
-    char xlo[ACT == Q4_F16 ? 2 : 1][ACT == Q4_F16 ? kGrRows * kGrPitch : 16];
-    char p[kPBufs<ACT, RF>][kGrRows * kGrPitch];
-    char p2[RF > 2 ? kPBufs<ACT, RF> : 1][RF > 2 ? kGrRows / 2 * kGrPitch : 16];
+    char x[kXBufs<ACT, RF>][kGrRows * kGrPitch];
+    char xlo[kXBufs<ACT, RF>][ACT == Q4_F16 ? kGrRows * kGrPitch : 16];
+    char p[kPBufs<RF>][kGrRows * kGrPitch];
+    char p2[RF > 2 ? kPBufs<RF> : 1][RF > 2 ? kGrRows / 2 * kGrPitch : 16];
     uint64_t mask[kGrList];  // rows of the adapter in the step
     uint16_t list[kGrList];
     int count;
@@ -101,7 +107,7 @@ __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cb
                                      GradLds<ACT, RF> &lds)
 {
     constexpr int PW = RF > 2 ? 64 : 32;        // columns a part
-    constexpr bool kOneP = kPBufs<ACT, RF> == 1;
+    constexpr bool kOneP = kPBufs<RF> == 1, kOneX = kXBufs<ACT, RF> == 1;
     constexpr int kPPieces = kGrRows * 2 * RF;  // 8-value pieces of P's tile
     constexpr int kPLoads = RF > 2 ? 2 : 1;     // ... a thread
     static_assert(kPPieces <= kPLoads * kGrBlock, "pieces of P");
@@ -226,7 +232,7 @@ __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cb
             }
         };
         // steps in flight in registers, the current one in one of two LDS
-        // buffers: one barrier a step, a second where P has one buffer
+        // buffers: one barrier a step, a second where there is one buffer
         GradStep<RF> ring[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i)
@@ -236,13 +242,15 @@ __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cb
             for (int i = 0; i < 2 * kAhead; ++i) {
                 if (i0 + i >= found)
                     break;
-                store_x(ring[i % kAhead], i & 1);
-                if constexpr (kOneP)
+                if constexpr (kOneX)
+                    __syncthreads();  // (the last step's tiles have been read)
+                store_x(ring[i % kAhead], kOneX ? 0 : i & 1);
+                if constexpr (kOneP && !kOneX)
                     __syncthreads();  // (the last step's P has been read)
                 store_p(ring[i % kAhead], kOneP ? 0 : i & 1);
                 load(ring[i % kAhead], i0 + i + kAhead);
                 __syncthreads();
-                work(i & 1, kOneP ? 0 : i & 1);
+                work(kOneX ? 0 : i & 1, kOneP ? 0 : i & 1);
             }
         }
     }
