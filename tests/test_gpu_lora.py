@@ -702,3 +702,29 @@ def test_infinities_of_adapters_in_gradients(name, rank):
             assert_same_kind(db[i], dy[at].double().T @ h, f"{name} db {i}")
         assert bool(torch.isinf(want).any()) and not bool(torch.isfinite(db[0]).all() or torch.isfinite(da[2]).all())
         assert_same_kind(dx, want, f"{name} dx")
+
+
+@pytest.mark.parametrize("M,N,K,adapters,rank", [
+    (5, 520, 4096, 3, 16), (95, 1000, 2048, 8, 72),                 # h in parts
+    (200, 2056, 5888, 3, 72), (130, 1032, 1024, 2, 8),              # and K, N in parts
+    (2048, 264, 2048, 8, 32), (4100, 136, 1280, 1, 64), (5000, 256, 512, 1, 64),  # and the rows
+    (300, 72, 96, 5, 256)])
+def test_a_workspace_of_exactly_the_bytes(M, N, K, adapters, rank):
+    """Nothing behind it is written or matters, and nothing in it before."""
+    gen = generator(M + N)
+    for act in (q4.F16, q4.BF16):
+        q = weight(N, K, q4.NF4, 32, gen)
+        pairs = pairs_of(gen, act, adapters, rank, N, K)
+        ids = ids_of(gen, M, adapters, "mixed")
+        x, dy = normal(gen, act, M, K), normal(gen, act, M, N)
+        for bwd in (False, True):
+            n = lora.workspace_bytes(M, pairs, bwd)
+            room = torch.full((n + 65536,), 255, dtype=torch.uint8, device=DEV)
+            call = check_backward if bwd else check
+            given = (dy, x) if bwd else (x,)
+            first = call(*given, q, pairs, ids, workspace=room[:n])
+            assert bool((room[n:] == 255).all())
+            room[n:] = 0
+            again = call(*given, q, pairs, ids, workspace=room[:n])
+            for a, b in zip(first, again) if bwd else ((first, again),):
+                assert torch.equal(a, b)

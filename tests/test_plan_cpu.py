@@ -68,3 +68,34 @@ def test_lora_sizes(ask):
 def test_lora_gradient_sizes(ask):
     got = ask(*(("lora", M, N, K, 3, 16) for _, _, M, N, K, _ in LORA_DX.values()))
     assert [(int(g[1]), int(g[5])) for g in got] == [v[:2] for v in LORA_DX.values()]
+
+
+# name: (the largest of the sums that the product's and the gradient's workspaces hold, M, N, K, adapters, rank)
+WORKSPACES = {
+    "few rows": (None, "out", 5, 4096, 4096, 3, 16),
+    "few rows, many adapters": (None, "out", 16, 11008, 4096, 32, 72),
+    "parts of K": ("out", "joined", 200, 2056, 5888, 3, 72),
+    "parts of K and N": ("out", "out", 130, 1032, 1024, 2, 8),
+    "parts of h": ("joined", "joined", 2048, 4096, 2048, 8, 32),
+    "parts of h and the rows": ("joined", "grads", 4096, 4096, 4096, 1, 64),
+    "parts of the rows": (None, "grads", 5000, 256, 512, 1, 64),
+    "no parts": (None, None, 20000, 64, 64, 300, 8),
+}
+
+
+@pytest.mark.parametrize("name", list(WORKSPACES))
+def test_workspace_bytes_are_those_of_the_parts(ask, name):
+    """h (and u): their parts in binary32 for few rows, else three 16-bit numbers a value; behind them the sums that are
+    joined, of which one kind at a time is needed."""
+    forward, backward, M, N, K, adapters, rank = WORKSPACES[name]
+    got = ask(("lora", M, N, K, adapters, rank))[0]
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    for bwd, largest, (down, out, splits) in ((0, forward, (int(got[2]), int(got[3]), 1)),
+                                            (1, backward, tuple(int(v) for v in got[4:]))):
+        kinds, split = 1 + bwd, bwd or M > 96
+        low = kinds * up(6 * M * rank if split else 4 * down * M * rank)
+        sums = {"joined": up(4 * kinds * down * M * rank) if split and down > 1 else 0,
+                "grads": up(4 * splits * adapters * rank * (N + K)) if splits > 1 else 0,
+                "out": up(4 * out * M * (K if bwd else (N + 3) // 4 * 4)) if out > 1 else 0}
+        assert (max(sums, key=sums.get) if any(sums.values()) else None) == largest
+        assert q4.lib().q4_lora_workspace_bytes(M, N, K, adapters, rank, bwd) == low + max(sums.values())
