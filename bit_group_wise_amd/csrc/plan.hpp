@@ -17,18 +17,44 @@ constexpr int64_t kStreamMaxK = 4096, kStreamMaxCodes = 0x7fff0000;
 enum class ExpertsKernel { stream1, stream2, skinny, tile64, tile128, tile256 };
 
 // The kernel by the mean number of rows an expert has (of the experts that can
-// have any).  Times in us, one card; a: 64 experts of 2048 x 4096 INT4-asym g
-// 32, b: 16 of 4096 x 4096 NF4 g 64, c: 64 of 1024 x 2048 INT4-sym g 64, d: 8
-// of 4096 x 14336 NF4 g 64; bf16 rows, uneven groups:
-//   mean                 4             8            12            16            24
-//   one block   a 80  b 39   a 96  b 42   a 105  b 53   a 118  b 60   a 151  b 77
-//   two blocks  a 83  b 46   a 89  b 53   a 103  b 55   a 109  b 64   a 121  b 77
-//   128 rows                 a 123 b 53   a 126  b 56   a 128  b 58   a 147  b 67
-//   two, 128    c 24         c 24  c 26   c 30   c 26   c 32   c 27   c 35   c 32
-//   skinny, 128 d 112        d 108 d 141  d 128  d 148  d 157  d 148  d 206  d 156
-//   mean                96           128           192           256
-//   128 rows    a 207  b 101  a 250  b 124  a 434  b 206  a 563  b 277
-//   256 rows    a 229  b 141  a 238  b 145  a 296  b 187  a 340  b 195
+// have any).  Times in us, one card, bf16 rows, uneven groups; a: 64 experts of
+// 2048 x 4096 INT4-asym g 32, b: 16 of 4096 x 4096 NF4 g 64, c: 64 of 1024 x 2048
+// INT4-sym g 64, d: 8 of 4096 x 14336 NF4 g 64, e: 64 of 1024 x 4096 NF4 g 64, f: 8
+// of 1024 x 4096 INT4-sym g 64:
+//   mean               4     8    12    16    24    32    48    64    96   128
+//   a one block       75    90   103   117   147   185   245
+//     two blocks      77    93   100   106   123   137   171
+//     64 rows        114   120   125   129   147   157   171   228   310   367
+//     128 rows       115   121   124   127   130   151   152   175   196   258
+//     256 rows                                           142   181   204   231
+//   b one block       36    43    51    59    66    86   112
+//     two blocks      42    46    59    61    68    76    96
+//     64 rows         50    50    51    52    52    55    76    88   122   168
+//     128 rows        50    50    51    51    52    53    80    83    91   107
+//     256 rows                                            78    80    84   104
+//   c one block       23    25    29    32    40    46    62
+//     two blocks      24    25    30    32    37    40    48
+//     64 rows         25    26    26    26    37    38    41    45    59    79
+//     128 rows        25    26    26    27    28    41    42    45    48    52
+//     256 rows                                            47    48    51    55
+//   d skinny          81   112   125   166   207   269   373
+//     64 rows        107   132   133   142   139   146   180   182   201   295
+//     128 rows       107   138   138   141   139   145   209   171   201   218
+//     256 rows                                           247   212   292   293
+//   e one block       39    48    53    61    74    87   118
+//     two blocks      47    56    62    64    75    82   102
+//     64 rows         49    50    52    52    74    75    79    94   140   161
+//     128 rows        49    51    51    52    79    59    82    89   109   136
+//     256 rows                                            78    81   103   114
+//   f two blocks      14    12    14    15    24    29    33
+//     64 rows         30    30    30    30    32    33    33    33    33    33
+//     128 rows        30    30    30    30    32    36    39    39    39    40
+//   mean             192   256   (128 / 256 rows)
+//   a            434/296   563/340
+//   b            206/187   277/195
+// The few rows' kernels win or tie up to 12 rows on all but c (29 against 26); from
+// 16 on tiles do on b to e, two blocks on a up to 24 and on f, whose blocks are
+// few, up to 32.
 inline ExpertsKernel experts_kernel(int64_t rows, int64_t experts, int64_t N, int64_t K)
 {
     const int64_t mean = rows / (experts < rows ? experts : rows);
@@ -37,8 +63,11 @@ inline ExpertsKernel experts_kernel(int64_t rows, int64_t experts, int64_t N, in
             return mean < 8 ? ExpertsKernel::stream1 : ExpertsKernel::stream2;
         return ExpertsKernel::skinny;
     }
-    // tiles that would leave half of the compute units idle are cut: 2 experts of
-    // 298 x 6496 INT4-asym, 333 rows: 164 -> 63 us
+    // 64-row tiles where those of 128, the rows counted as one group, would be
+    // fewer than 128: with few experts they leave half of the compute units idle
+    // (f; d at 48 rows; 2 of 298 x 6496 INT4-asym, 256 rows: 76 / 60 us).  Many
+    // small groups make more tiles than that, but then both kernels run most of
+    // their pieces as the same 64-row tiles: b and e within 7 %, c at 24 rows 37 / 28.
     const int64_t tiles = (rows + 127) / 128 * ((N + 127) / 128);
     if (tiles < 128)
         return ExpertsKernel::tile64;
@@ -74,7 +103,13 @@ inline DownPlan down_plan(int64_t rows, int64_t longest, int adapters, int rank,
     p.slices = (rank + 16 * p.rf - 1) / (16 * p.rf);
     const int tile = p.split ? kDownRows : 16;
     p.tiles = (rows + tile - 1) / tile;
-    // few rows: their adapters side by side
+    // few rows: their adapters side by side.  Whole calls on 4096 x 4096 in us, a
+    // tile's adapters one after another / on up to 16 workgroups; product, then
+    // backward.  100 rows of 32 adapters of rank 16 in any order 95 / 40, 124 / 68;
+    // of 4 34 / 28, 43 / 36; 512 rows of 32 in any order 121 / 66, 177 / 126, in runs
+    // 51.5 / 45.4, 82 / 81.  Beyond 512 workgroups without rows of theirs cost runs
+    // (1024 rows of 32 adapters 77.9 / 79.4, 90 / 99; 2048 104 / 112, 121 / 130) what
+    // rows in any order would gain (1024 171 / 125, 218 / 184; 2048 205 / 169, 383 / 295).
     const int64_t most = adapters < rows ? adapters : rows;
     p.slots = rows <= 512 ? (int)(most < 16 ? most : 16) : 1;
     if (p.slots < 1)
