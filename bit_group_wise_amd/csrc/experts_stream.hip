@@ -31,13 +31,6 @@ namespace {
 
 constexpr uint32_t kPast = 0x80000000u;
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t es_rsrc(const void *base, int64_t bytes)
-{
-    const uint32_t n = __builtin_amdgcn_readfirstlane(
-        bytes <= 0 ? 0u : (bytes >= 0x7fffffffll ? 0x7fffffffu : (uint32_t)bytes));
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n, 0x00020000);
-}
-
 // A lane's share of a block of 16 weight rows: S times 32 codes of one row and
 // their groups' scales as stored (and zero-points, from the byte of the first;
 // NF4_DQ: the constants of the first group's run and the next).
@@ -106,8 +99,8 @@ __global__ __launch_bounds__(64 * WAVES) void experts_stream_kernel(
         // the lane's part of x: row r of each 16, k0 .. k0 + 32 S - 1
         u32x4 xf[MT][S][4];
         {
-            const __amdgpu_buffer_rsrc_t xr = index ? es_rsrc(x, (int64_t)xrows * K * 2)
-                                                    : es_rsrc(x + (int64_t)p.lo * K, (int64_t)M * K * 2);
+            const __amdgpu_buffer_rsrc_t xr = index ? buffer_view(x, (int64_t)xrows * K * 2)
+                                                    : buffer_view(x + (int64_t)p.lo * K, (int64_t)M * K * 2);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 int m = 16 * mt + r;
@@ -125,17 +118,17 @@ __global__ __launch_bounds__(64 * WAVES) void experts_stream_kernel(
                             0);
             }
         }
-        const __amdgpu_buffer_rsrc_t cr = es_rsrc(codes + w0 * row_bytes, (int64_t)N * row_bytes);
+        const __amdgpu_buffer_rsrc_t cr = buffer_view(codes + w0 * row_bytes, (int64_t)N * row_bytes);
         // scales and zero-points: to the end of the padded arrays, so that no word
         // of a meaningful entry is cut by a view's end (which would make it zero)
         const int64_t g0 = w0 * Gn, groups = (int64_t)experts * N * Gn;  // flat number of the expert's first group, and of all
         const int64_t s_total = padded_meta_bytes(FMT == Q4_NF4_DQ ? dq_scales_bytes(groups) : groups * ss);
-        const __amdgpu_buffer_rsrc_t sr = es_rsrc((const char *)scales + g0 * ss, s_total - g0 * ss);
+        const __amdgpu_buffer_rsrc_t sr = buffer_view((const char *)scales + g0 * ss, s_total - g0 * ss);
         __amdgpu_buffer_rsrc_t zr = sr;
         if constexpr (FMT == Q4_INT4_ASYM)
-            zr = es_rsrc(zeros + (g0 >> 1), padded_meta_bytes((groups + 1) / 2) - (g0 >> 1));
+            zr = buffer_view(zeros + (g0 >> 1), padded_meta_bytes((groups + 1) / 2) - (g0 >> 1));
         if constexpr (FMT == Q4_NF4_DQ)
-            zr = es_rsrc((const char *)scales + dq_s2_offset(groups) + 4 * (g0 / kDqRun),
+            zr = buffer_view((const char *)scales + dq_s2_offset(groups) + 4 * (g0 / kDqRun),
                          s_total - dq_s2_offset(groups) - 4 * (g0 / kDqRun));
 
         auto load = [&](Share<FMT, G, S> &sh, int b) {

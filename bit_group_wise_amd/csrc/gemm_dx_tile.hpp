@@ -64,20 +64,8 @@ static_assert(TK == kDxCols && TN == kDxStep, "the plan's tiles");
 static_assert(TK == 2 * 16 * kKF && TM == 4 * 16 * kWMF && kWaves == 8 && kWMF <= kKF, "2 x 4 waves");
 static_assert(TN * TK / 16 == kBlock, "16 columns of one row per thread");
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t dx_rsrc(const void *base, int64_t bytes)
-{
-    // (read back as a wave-uniform value: a resource the compiler cannot
-    // prove uniform turns every load through it into a loop over lanes)
-    const uint32_t n = __builtin_amdgcn_readfirstlane(
-        bytes <= 0 ? 0u : (bytes >= 0x7fffffffll ? 0x7fffffffu : (uint32_t)bytes));
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n,
-                                             0x00020000);
-}
-
 // Position of 16-byte chunk c of staged dY row r.
 __device__ __forceinline__ int yswz(int r, int c) { return c ^ ((r >> 1) & 7); }
-
-typedef short v4i16 __attribute__((ext_vector_type(4)));
 
 // A tile of a grouped product (kDxGroup) lies among rows that may hold anything.
 // kDxLora: low-rank adapters beside the weight.  kDxLoraPart: the same for one
@@ -121,7 +109,7 @@ __device__ __forceinline__ void dx_load(DxLoads<WMF> &ld, const DxCtx &c, int n0
     // whole rows (rows past M and elements past the buffer read zeros;
     // elements past N of a row read the next row, which meets zero weights)
     const uint32_t yoff = 2u * (uint32_t)n0;
-    const __amdgpu_buffer_rsrc_t yr = dx_rsrc(c.yb + yoff, yoff < c.ybytes ? c.ybytes - yoff : 0);
+    const __amdgpu_buffer_rsrc_t yr = buffer_view(c.yb + yoff, yoff < c.ybytes ? c.ybytes - yoff : 0);
 #pragma unroll
     for (int i = 0; i < WMF; ++i) {
         const int yrow = (t >> 3) + 64 * i;
@@ -220,15 +208,15 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
     c.ybytes = (uint32_t)((int64_t)mrows * N * 2 > 0x7fffffffll ? 0x7fffffffll : (int64_t)mrows * N * 2);
     const int64_t first = tile.wrow0 * c.G;
     c.first = first;
-    c.cr = dx_rsrc(codes + tile.wrow0 * (K >> 1), (int64_t)N * (K >> 1));
+    c.cr = buffer_view(codes + tile.wrow0 * (K >> 1), (int64_t)N * (K >> 1));
     // scales: exactly the meaningful entries (an index at or past the end
     // reads zero); NF4_DQ: the 8-bit codes, and zr the run constants
-    c.sr = dx_rsrc((const char *)scales + first * ss, ngroups * ss);
+    c.sr = buffer_view((const char *)scales + first * ss, ngroups * ss);
     if constexpr (FMT == Q4_NF4_DQ)
-        c.zr = dx_rsrc((const char *)scales + dq_s2_offset(tile.wrows * c.G) + 4 * (first / kDqRun),
+        c.zr = buffer_view((const char *)scales + dq_s2_offset(tile.wrows * c.G) + 4 * (first / kDqRun),
                        4 * ((first % kDqRun + ngroups + kDqRun - 1) / kDqRun));
     else
-        c.zr = FMT == Q4_INT4_ASYM ? dx_rsrc(zeros + (first >> 1), ((first & 1) + ngroups + 1) / 2) : c.cr;
+        c.zr = FMT == Q4_INT4_ASYM ? buffer_view(zeros + (first >> 1), ((first & 1) + ngroups + 1) / 2) : c.cr;
 
     // waves: 2 along k (64 columns each) x 4 along m (16 kWMF rows each)
     const int wk = wave & 1, wm = wave >> 1;
@@ -238,6 +226,15 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
 #pragma unroll
         for (int f = 0; f < kWMF; ++f)
             acc[j][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // 8 rows 32 h + 8 fq .. + 7 of a staged weight tile at column fi of the wave's
+    // fragment j: a lane addresses row 8 fq + 4 u + fi / 4, columns 4 (fi % 4) .. + 3.
+    const auto column8 = [&](const char *tile, int h, int j) {
+        const auto at = [&](int u) {
+            return tile + wofs(32 * h + 8 * fq + 4 * u + (fi >> 2), 64 * wk + 16 * j + 4 * (fi & 3));
+        };
+        return read_column8(at(0), at(1));
+    };
 
     // One round: the products of the step in LDS buffer (ysc, wtc), with the
     // staging of the next step (register set ld -> buffer (ysn, wtn)) worked
@@ -249,24 +246,11 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
                      int next_n0) {
         u32x4 fa[kKF], fb[kWMF];
         auto reads = [&](int h) {
-            // A operand (8 rows n = 32 h + 8 fq + 0..7 at column k of the
-            // fragment, for lane (k = fi, fq)) by two transposed reads: in
-            // each 16-lane group, result lane i takes element i % 4 of the
-            // 4-element row piece addressed by lane 4 e + i / 4 (e the
-            // result element); so lane s addresses row 8 fq + 4 u + s / 4,
-            // columns 4 (s % 4) .. + 3 of the fragment.
+            // A operand: 8 rows n = 32 h + 8 fq + 0..7 at column k of the fragment,
+            // for lane (k = fi, fq)
 #pragma unroll
-            for (int j = 0; j < kKF; ++j) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int nl = 32 * h + 8 * fq + 4 * u + (fi >> 2);
-                    const int kl = 64 * wk + 16 * j + 4 * (fi & 3);
-                    const v4i16 r = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (__attribute__((address_space(3))) v4i16 *)(wtc + wofs(nl, kl)));
-                    fa[j][2 * u] = (uint32_t)(uint16_t)r[0] | ((uint32_t)(uint16_t)r[1] << 16);
-                    fa[j][2 * u + 1] = (uint32_t)(uint16_t)r[2] | ((uint32_t)(uint16_t)r[3] << 16);
-                }
-            }
+            for (int j = 0; j < kKF; ++j)
+                fa[j] = column8(wtc, h, j);
 #pragma unroll
             for (int f = 0; f < kWMF; ++f) {
                 const int r = 16 * kWMF * wm + 16 * f + fi;
@@ -358,7 +342,7 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
         char *const parts[3] = {ys[0], ys[1], us};
         // (rows past the tile's end lie past the view)
         const __amdgpu_buffer_rsrc_t ur =
-            dx_rsrc(low->split + (int64_t)m0 * 3 * low->rank, (int64_t)rows * 3 * low->rank * 2);
+            buffer_view(low->split + (int64_t)m0 * 3 * low->rank, (int64_t)rows * 3 * low->rank * 2);
         const int rank = KIND == kDxLora || tile.step0 == 0 ? low->rank : 0;  // (of a later part: none)
         for (int rc = 0; rc < rank; rc += 64) {
             // u's chunk t % 8 of rows t / 8 + 64 i, all loads before the first store
@@ -417,20 +401,9 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
                     for (int h = 0; h < 2; ++h) {
                         if (rc + 32 * h >= rank)
                             break;
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int at = wofs(32 * h + 8 * fq + 4 * u + (fi >> 2), 64 * wk + 16 * j + 4 * (fi & 3));
-                            const v4i16 p = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                (__attribute__((address_space(3))) v4i16 *)(wt[0] + at));
-                            fa[h].hi[2 * u] = (uint32_t)(uint16_t)p[0] | ((uint32_t)(uint16_t)p[1] << 16);
-                            fa[h].hi[2 * u + 1] = (uint32_t)(uint16_t)p[2] | ((uint32_t)(uint16_t)p[3] << 16);
-                            if constexpr (ACT == Q4_F16) {
-                                const v4i16 o = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                    (__attribute__((address_space(3))) v4i16 *)(wt[1] + at));
-                                fa[h].lo[2 * u] = (uint32_t)(uint16_t)o[0] | ((uint32_t)(uint16_t)o[1] << 16);
-                                fa[h].lo[2 * u + 1] = (uint32_t)(uint16_t)o[2] | ((uint32_t)(uint16_t)o[3] << 16);
-                            }
-                        }
+                        fa[h].hi = column8(wt[0], h, j);
+                        if constexpr (ACT == Q4_F16)
+                            fa[h].lo = column8(wt[1], h, j);
                     }
 #pragma unroll
                     for (int f = 0; f < kWMF; ++f) {

@@ -27,15 +27,6 @@
 namespace q4 {
 namespace {
 
-typedef short v4i16 __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t dn_rsrc(const void *base, int64_t bytes)
-{
-    const uint32_t n = __builtin_amdgcn_readfirstlane(
-        bytes <= 0 ? 0u : (bytes >= 0x7fffffffll ? 0x7fffffffu : (uint32_t)bytes));
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n, 0x00020000);
-}
-
 // Four values r of row m as their operands, at split[(3 m + i) * rank + r].
 __device__ __forceinline__ void store_split(uint16_t *split, int rank, int64_t m, int r, const f32x4 &v)
 {
@@ -70,7 +61,7 @@ __global__ __launch_bounds__(kFewBlock) void down_few_kernel(DownArgs a)
     const int len = a.K, r0 = slice * 16 * RF;
     const int64_t m0 = (int64_t)blockIdx.x * 16;
     const int rows = (int)(a.rows - m0 < 16 ? a.rows - m0 : 16);
-    const __amdgpu_buffer_rsrc_t xr = dn_rsrc((const uint16_t *)a.x + m0 * len, (int64_t)rows * len * 2);
+    const __amdgpu_buffer_rsrc_t xr = buffer_view((const uint16_t *)a.x + m0 * len, (int64_t)rows * len * 2);
     // this part's steps of 32
     const int steps = (len + 31) / 32, per = (steps + a.parts - 1) / a.parts;
     const int first = blockIdx.y * per, last = min(first + per, steps);
@@ -83,7 +74,7 @@ __global__ __launch_bounds__(kFewBlock) void down_few_kernel(DownArgs a)
         if (at++ % a.slots != slot)
             continue;
         const __amdgpu_buffer_rsrc_t wr =
-            dn_rsrc((const uint16_t *)a.a + (int64_t)ad * a.rank * len, (int64_t)a.rank * len * 2);
+            buffer_view((const uint16_t *)a.a + (int64_t)ad * a.rank * len, (int64_t)a.rank * len * 2);
         auto load = [&](FewStep<RF> &st, int step) {
             const int k = 32 * step + 8 * fq;
             const bool on = step < last && k < len;
@@ -172,7 +163,7 @@ __device__ __forceinline__ void down_many(const DownArgs &a, const uint16_t *__r
     const int r0 = slice * 16 * RF;
     const int64_t m0 = (int64_t)blockIdx.x * kRows;
     const int rows = (int)(a.rows - m0 < kRows ? a.rows - m0 : kRows);
-    const __amdgpu_buffer_rsrc_t xr = dn_rsrc(x + m0 * len, (int64_t)rows * len * 2);
+    const __amdgpu_buffer_rsrc_t xr = buffer_view(x + m0 * len, (int64_t)rows * len * 2);
     const int steps = (len + kStep - 1) / kStep, per = (steps + a.parts - 1) / a.parts;
     const int first = blockIdx.y * per, last = min(first + per, steps);
 
@@ -183,7 +174,7 @@ __device__ __forceinline__ void down_many(const DownArgs &a, const uint16_t *__r
     while (set.next(ad, mask)) {
         if (at++ % a.slots != slot)
             continue;
-        const __amdgpu_buffer_rsrc_t wr = dn_rsrc(w + (int64_t)ad * a.rank * len, (int64_t)a.rank * len * 2);
+        const __amdgpu_buffer_rsrc_t wr = buffer_view(w + (int64_t)ad * a.rank * len, (int64_t)a.rank * len * 2);
         auto load = [&](ManyStep<RF> &st, int step) {
             const int k = kStep * step + 8 * (t & 7);
             const bool on = step < last;
@@ -240,15 +231,10 @@ __device__ __forceinline__ void down_many(const DownArgs &a, const uint16_t *__r
                 for (int f = 0; f < RF; ++f) {
                     u32x4 wf;
                     if constexpr (TRANS) {
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int n = 32 * h + 8 * fq + 4 * u + (fi >> 2);
-                            const v4i16 q = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                (__attribute__((address_space(3))) v4i16 *)(wb + bofs<RF>(n, 2 * f + ((fi >> 1) & 1)) +
-                                                                            8 * (fi & 1)));
-                            wf[2 * u] = (uint32_t)(uint16_t)q[0] | ((uint32_t)(uint16_t)q[1] << 16);
-                            wf[2 * u + 1] = (uint32_t)(uint16_t)q[2] | ((uint32_t)(uint16_t)q[3] << 16);
-                        }
+                        const auto at = [&](int u) {
+                            return wb + bofs<RF>(32 * h + 8 * fq + 4 * u + (fi >> 2), 2 * f + ((fi >> 1) & 1)) + 8 * (fi & 1);
+                        };
+                        wf = read_column8(at(0), at(1));
                     } else {
                         const int r = 16 * f + fi;
                         wf = *(const u32x4 *)(wb + r * 128 + 16 * dswz(r, 4 * h + fq));

@@ -30,31 +30,14 @@ constexpr int kGrBlock = 64 * kGrWaves;
 constexpr int kGrPitch = 288;   // bytes of a staged row of 128 values
 constexpr int kGrList = 256;    // steps listed at a time
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t gr_rsrc(const void *base, int64_t bytes)
-{
-    const uint32_t n = __builtin_amdgcn_readfirstlane(
-        bytes <= 0 ? 0u : (bytes >= 0x7fffffffll ? 0x7fffffffu : (uint32_t)bytes));
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n, 0x00020000);
-}
-
-typedef short v4i16 __attribute__((ext_vector_type(4)));
-
 __device__ __forceinline__ int gofs(int row, int col) { return row * kGrPitch + ((2 * col) ^ (((row >> 3) & 1) << 7)); }
 
 // 8 rows of one column as an operand: rows 32 h + 8 fq .. + 7, column c0 + fi.
 __device__ __forceinline__ u32x4 column8(const char *tile, int h, int c0)
 {
     const int lane = threadIdx.x & 63, fi = lane & 15, fq = lane >> 4;
-    u32x4 v;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const v4i16 q = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) v4i16 *)(tile + gofs(32 * h + 8 * fq + 4 * u + (fi >> 2),
-                                                                    c0 + 4 * (fi & 3))));
-        v[2 * u] = (uint32_t)(uint16_t)q[0] | ((uint32_t)(uint16_t)q[1] << 16);
-        v[2 * u + 1] = (uint32_t)(uint16_t)q[2] | ((uint32_t)(uint16_t)q[3] << 16);
-    }
-    return v;
+    const auto at = [&](int u) { return tile + gofs(32 * h + 8 * fq + 4 * u + (fi >> 2), c0 + 4 * (fi & 3)); };
+    return read_column8(at(0), at(1));
 }
 
 // One kind of gradient: X [rows, cols], P's parts [rows, 3, rank], and the
@@ -164,8 +147,8 @@ __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cb
             const uint64_t mask = on ? lds.mask[s] : 0;
             const int64_t m0 = (base + s) * kGrRows;
             const int rows = (int)(a.rows - m0 < kGrRows ? a.rows - m0 : kGrRows);
-            const __amdgpu_buffer_rsrc_t xr = gr_rsrc(side.x + m0 * side.cols, (int64_t)rows * side.cols * 2);
-            const __amdgpu_buffer_rsrc_t pr = gr_rsrc(side.p + 3 * m0 * a.rank, (int64_t)rows * 3 * a.rank * 2);
+            const __amdgpu_buffer_rsrc_t xr = buffer_view(side.x + m0 * side.cols, (int64_t)rows * side.cols * 2);
+            const __amdgpu_buffer_rsrc_t pr = buffer_view(side.p + 3 * m0 * a.rank, (int64_t)rows * 3 * a.rank * 2);
             const int c = c0 + 8 * (t & 15);
             const uint32_t cpast = c < side.cols ? 0u : kPast;
 #pragma unroll

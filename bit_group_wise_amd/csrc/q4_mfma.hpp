@@ -11,6 +11,29 @@ namespace q4 {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
+// A view of `bytes` from base for buffer loads; a load that is not wholly inside
+// reads zeros.  (The length is read back as a wave-uniform value: a resource that
+// the compiler cannot prove uniform turns every load through it into a loop over
+// lanes.)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_view(const void *base, int64_t bytes)
+{
+    const uint32_t n = __builtin_amdgcn_readfirstlane(
+        bytes <= 0 ? 0u : (bytes >= 0x7fffffffll ? 0x7fffffffu : (uint32_t)bytes));
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n, 0x00020000);
+}
+
+// 8 16-bit values of one column of LDS as an operand, 4 rows by each of two
+// transposed reads: in each 16-lane group, result lane i takes element i % 4 of the
+// 4-element row pieces that lanes 4 e + i / 4 address (e the result element).
+__device__ __forceinline__ u32x4 read_column8(const char *first, const char *second)
+{
+    typedef short v4i16 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) v4i16 *lds;
+    const u32x2 a = std::bit_cast<u32x2>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)first));
+    const u32x2 b = std::bit_cast<u32x2>(__builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)second));
+    return u32x4{a[0], a[1], b[0], b[1]};
+}
+
 template <int ACT>
 __device__ __forceinline__ uint32_t pack2(float a, float b)
 {

@@ -53,13 +53,6 @@ constexpr int kSkStep = 128;  // k per step
 constexpr int kSkRing = Q4_SK_RING;
 enum { kSkDense = 0, kSkGather = 1, kSkLora = 2 };
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t sk_rsrc(const void *base, int64_t bytes)
-{
-    const uint32_t n = bytes <= 0 ? 0u : (bytes >= 0x7fffffffll ? 0x7fffffffu : (uint32_t)bytes);
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)n,
-                                             0x00020000);
-}
-
 // One step's operands for a lane: for each of the RB row blocks, 32 codes
 // and their group's scale (and asym zero-point, or NF4_DQ run constant);
 // and 32 activations of one x row, shared by the blocks.
@@ -115,22 +108,22 @@ __device__ __forceinline__ void skinny_product(const SkTask &task, const uint16_
     // views: this workgroup's 16 RB weight rows (rows past N read zeros) and
     // the M activation rows
     const int nrows = N - n0 < 16 * RB ? N - n0 : 16 * RB;
-    const __amdgpu_buffer_rsrc_t cr = sk_rsrc(codes + r0 * row_bytes, (int64_t)nrows * row_bytes);
+    const __amdgpu_buffer_rsrc_t cr = buffer_view(codes + r0 * row_bytes, (int64_t)nrows * row_bytes);
     const __amdgpu_buffer_rsrc_t sr =
-        sk_rsrc((const char *)scales + r0 * G * ss, (int64_t)nrows * G * ss);
+        buffer_view((const char *)scales + r0 * G * ss, (int64_t)nrows * G * ss);
     const int64_t zg0 = r0 * G;  // flat group index of the first row's first group
     __amdgpu_buffer_rsrc_t zr = sr;
     if constexpr (FMT == Q4_INT4_ASYM)
-        zr = sk_rsrc(zeros + (zg0 >> 1), (((int64_t)nrows * G + (zg0 & 1)) + 1) / 2);
+        zr = buffer_view(zeros + (zg0 >> 1), (((int64_t)nrows * G + (zg0 & 1)) + 1) / 2);
     // double-quantized absmax: the runs' binary32 constants for the rows'
     // groups (zr then starts at the run holding the first group)
     if constexpr (FMT == Q4_NF4_DQ) {
         const float *s2 = (const float *)((const char *)scales + dq_s2_offset(task.wrows * G));
         const int64_t r0 = zg0 / kDqRun, r1 = (zg0 + (int64_t)nrows * G - 1) / kDqRun;
-        zr = sk_rsrc(s2 + r0, 4 * (r1 - r0 + 1));
+        zr = buffer_view(s2 + r0, 4 * (r1 - r0 + 1));
     }
     const bool gather = KIND == kSkGather && task.index;
-    const __amdgpu_buffer_rsrc_t xr = sk_rsrc(x, (int64_t)(gather ? task.xrows : M) * K * 2);
+    const __amdgpu_buffer_rsrc_t xr = buffer_view(x, (int64_t)(gather ? task.xrows : M) * K * 2);
     int xm[MT];  // gathered: the x row of the lane's row of each activation block (-1: none)
     if constexpr (KIND == kSkGather) {
 #pragma unroll
@@ -197,7 +190,7 @@ __device__ __forceinline__ void skinny_product(const SkTask &task, const uint16_
                     acc[b][mt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             AdapterSet<1> all;
             all.init(low->ids, low->adapters, 0, M);
-            const __amdgpu_buffer_rsrc_t parts = sk_rsrc(low->part, 4 * low->parts * low->rows * low->rank);
+            const __amdgpu_buffer_rsrc_t parts = buffer_view(low->part, 4 * low->parts * low->rows * low->rank);
             constexpr int kTurns = EXTRA ? EXTRA : kSkWaves;  // waves that share the adapters
             constexpr int kAhead = 3;                         // adapters whose B is in flight
             constexpr uint32_t kPast = 0x80000000u;           // past every view
@@ -221,7 +214,7 @@ __device__ __forceinline__ void skinny_product(const SkTask &task, const uint16_
                     while (sl.on && turn++ % kTurns != 0);
                     sl.mask = mask[0];
                     const __amdgpu_buffer_rsrc_t br =
-                        sk_rsrc(low->w + (int64_t)(sl.on ? ad : 0) * N * low->rank, (int64_t)N * low->rank * 2);
+                        buffer_view(low->w + (int64_t)(sl.on ? ad : 0) * N * low->rank, (int64_t)N * low->rank * 2);
                     const uint32_t none = sl.on && r0 < low->rank ? 0u : kPast;  // (rows past N lie past the view)
 #pragma unroll
                     for (int b = 0; b < RB; ++b)
