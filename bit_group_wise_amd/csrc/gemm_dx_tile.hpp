@@ -422,7 +422,7 @@ __device__ __forceinline__ void dx_tile(const DxTile &tile, const uint16_t *__re
 #pragma unroll
                         for (int c2 = 1; c2 < C; ++c2)
                             of = (16 * kWMF * wm) / 64 == c2 ? mask[c2] : of;
-                        const bool mine = (of >> (row & 63)) & 1;
+                        const bool mine = (rows16(of, (16 * kWMF * wm + 16 * f) & 63) >> fi) & 1;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             acc[j][f][e] = mine ? acc[j][f][e] + p[e] : acc[j][f][e];

@@ -444,9 +444,10 @@ __device__ __forceinline__ void lora_start(f32x4 (&acc)[kNF][kMF], const LowRank
                 load();
 #pragma unroll
             for (int i = 0; i < kMF; ++i) {
-                if (((mask[i / 4] >> (16 * (i % 4))) & 0xffff) == 0)
+                const uint32_t its = rows16(mask[i / 4], 16 * (i % 4));
+                if (its == 0)
                     continue;
-                const bool mine = (mask[i / 4] >> (16 * (i % 4) + fr)) & 1;
+                const bool mine = (its >> fr) & 1;
                 const Low8 h{{*(const u32x4 *)(xs0 + rd[0] + 2048 * i), *(const u32x4 *)(xs0 + rd[1] + 2048 * i),
                               *(const u32x4 *)(xs1 + rd[2] + 2048 * i)}};
 #pragma unroll

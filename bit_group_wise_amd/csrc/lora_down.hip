@@ -117,7 +117,7 @@ __global__ __launch_bounds__(kFewBlock) void down_few_kernel(DownArgs a)
                 v = f32x4{v[0] + u[0], v[1] + u[1], v[2] + u[2], v[3] + u[3]};
             }
             const int r = r0 + 16 * f + 4 * fq;
-            if (((mask[0] >> fi) & 1) && r < a.rank)
+            if (((rows16(mask[0], 0) >> fi) & 1) && r < a.rank)
                 *(f32x4 *)((float *)a.h + (blockIdx.y * a.rows + m0 + fi) * a.rank + r) =
                     f32x4{v[0] * s, v[1] * s, v[2] * s, v[3] * s};
         }
@@ -263,7 +263,7 @@ __device__ __forceinline__ void down_many(const DownArgs &a, const uint16_t *__r
             }
         }
         const float s = a.scale ? a.scale[ad] : 1.0f;
-        const bool mine = (mask[0] >> (16 * wave + fi)) & 1;
+        const bool mine = (rows16(mask[0], 16 * wave) >> fi) & 1;
 #pragma unroll
         for (int f = 0; f < RF; ++f) {
             const int r = r0 + 16 * f + 4 * fq;

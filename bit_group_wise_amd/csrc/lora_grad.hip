@@ -129,7 +129,8 @@ __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cb
                 const bool on = s + lane < n && lds.mask[s + lane] != 0;
                 const uint64_t m = __ballot(on);
                 if (on)
-                    lds.list[found + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)(s + lane);
+                    lds.list[found + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0))] =
+                        (uint16_t)(s + lane);
                 found += __popcll(m);
             }
             if (lane == 0)
@@ -145,6 +146,8 @@ __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cb
             const bool on = i < found;
             const int s = __builtin_amdgcn_readfirstlane(on ? lds.list[i] : 0);
             const uint64_t mask = on ? lds.mask[s] : 0;
+            const uint32_t halves[2] = {(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)mask),
+                                        (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(mask >> 32))};
             const int64_t m0 = (base + s) * kGrRows;
             const int rows = (int)(a.rows - m0 < kGrRows ? a.rows - m0 : kGrRows);
             const __amdgpu_buffer_rsrc_t xr = buffer_view(side.x + m0 * side.cols, (int64_t)rows * side.cols * 2);
@@ -154,14 +157,15 @@ __device__ __forceinline__ void grad(const GradArgs &a, const Side &side, int cb
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int row = (t >> 4) + 16 * q;
-                const uint32_t none = (mask >> row) & 1 ? 0u : kPast;
+                const uint32_t none = (halves[q / 2] >> (row & 31)) & 1 ? 0u : kPast;
                 st.x[q] = __builtin_amdgcn_raw_buffer_load_b128(
                     xr, (int)(2u * (uint32_t)(row * side.cols + c) | none | cpast), 0, 0);
             }
 #pragma unroll
             for (int q = 0; q < kPLoads; ++q) {
                 const int p = t + kGrBlock * q, row = (p / (2 * RF)) & 63, r = r0 + 8 * (p % (2 * RF));
-                const uint32_t none = ((mask >> row) & 1) && p < kPPieces && r < a.rank ? 0u : kPast;
+                const uint32_t its = halves[((64 * wave + kGrBlock * q) / (2 * RF)) >> 5 & 1];  // (a wave's rows lie in one)
+                const uint32_t none = ((its >> (row & 31)) & 1) && p < kPPieces && r < a.rank ? 0u : kPast;
 #pragma unroll
                 for (int i = 0; i < 3; ++i)
                     st.p[i][q] = __builtin_amdgcn_raw_buffer_load_b128(

@@ -244,10 +244,11 @@ __device__ __forceinline__ void skinny_product(const SkTask &task, const uint16_
                                 const Exact8 w = exact_parts<ACT>(slots[i].b[b]);
 #pragma unroll
                                 for (int mt = 0; mt < MT; ++mt) {
-                                    if (((slots[i].mask >> (16 * mt)) & 0xffff) == 0)
+                                    const uint32_t its = rows16(slots[i].mask, 16 * mt);
+                                    if (its == 0)
                                         continue;
                                     const f32x4 t = mfma_exact_low<ACT>(w, h[mt], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-                                    const bool mine = (slots[i].mask >> (16 * mt + r)) & 1;
+                                    const bool mine = (its >> r) & 1;
 #pragma unroll
                                     for (int e = 0; e < 4; ++e)
                                         acc[b][mt][e] = mine ? acc[b][mt][e] + t[e] : acc[b][mt][e];

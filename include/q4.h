@@ -274,7 +274,7 @@ q4_status q4_gemv_chain_static(q4_format f, int g, q4_dtype act_t, const q4_gemv
  * values and the rounding of q4_gemm.  index int32 [rows] on the device, or
  * NULL for x[r] (then x_rows must be rows): a token's rows for its experts
  * read the token's one row of x [x_rows, K].  A row whose index is outside
- * 0 .. x_rows - 1 gets zeros.  With an index x_rows * K * 2 must stay below
+ * 0 .. x_rows - 1 counts as a row of zeros.  With an index x_rows * K * 2 must stay below
  * 2^31 bytes, else Q4_EUNSUPPORTED.  rows = 0 is no work.  The mean number of
  * rows an expert chooses the kernel; every choice takes any groups. */
 #define Q4_EXPERTS_MAX 65536
