@@ -46,9 +46,10 @@ def assert_within(got, want, sums, act, tag):
 
 
 # Errors relative to the sums of magnitudes: an addition in binary32 at most
-# 2^-23 (the matrix cores may cut where they do not round); h and u as two
-# bfloat16 numbers 2^-18 (2^-9 of 2^-9), fp16's product of second parts 2^-18:
-# 2^-17 together.
+# 2^-23 (the matrix cores may cut where they do not round).  TWO_PARTS is room
+# for h and u as two bfloat16 numbers, 2^-18 (2^-9 of 2^-9), and fp16's product
+# of second parts, 2^-18; that they enter with all their bits is tested by whole
+# numbers (test_every_bit_of_the_low_product and its gradients).
 def short(terms):
     return terms * 2.0 ** -23
 
